@@ -390,6 +390,118 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
                                     const int32_t* seq_lens, const uint8_t* abort_mask,
                                     float sm_scale, void* out);
 
+/*
+ * kv_append_quantize of keys that are still to be rotated: the queries and
+ * keys of the new rows are turned by their positions (rotary position
+ * embedding on one or several axes, for example a token's time, height and
+ * width), the queries are written out, and keys and values go into the cache
+ * as they come, in one pass over them.  The post gives no position encoding;
+ * models of the kind it serves rotate q and k before attention.
+ *
+ *   total_new      rows of q, k_new, v_new and positions; new_indptr[B] must
+ *                  not exceed it (a request whose rows do gets
+ *                  KV_ERR_INVALID_ARG and none of them is written).
+ *   q              bf16 rows of num_q_heads x head_dim_k values, row t at
+ *                  q + t * q_stride (device).  num_q_heads 0: no queries (q
+ *                  and q_out may be NULL).
+ *   k_new, v_new   bf16 rows of num_kv_heads x head_dim, row t at
+ *                  k_new + t * k_stride / v_new + t * v_stride (device).
+ *   q_stride, k_stride, v_stride  elements, multiples of 8, at least a row's
+ *                  width: q, k and v may be parts of one projection's output.
+ *   positions      int32 [num_axes][total_new] (device)
+ *   pair_axis      uint8 [rotary_dim / 2] (device): the axis whose position
+ *                  turns pair i (an entry >= num_axes: KV_ERR_INVALID_ARG in
+ *                  ctl, and the pair is not turned).
+ *   inv_freq       double [rotary_dim / 2] (device): radians per position.
+ *   rotary_dim     dims that turn, a multiple of 16, <= head_dim_k; the dims
+ *                  behind them pass through.
+ *   interleaved    0: pair i is dims (i, i + rotary_dim / 2); 1: (2i, 2i + 1).
+ *   q_out          bf16 [total_new][num_q_heads][head_dim_k] (device); may be
+ *                  q itself when q_stride is a row's width.
+ * Pair (x, y) becomes (x cos a - y sin a, y cos a + x sin a) with a =
+ * positions[axis][t] * inv_freq[i] (64-bit product).  Keys stay in fp32
+ * between the rotation and their one rounding: e4m3 pages take their scale
+ * from the rotated fp32 rows, bf16 pools round them to bf16.  Everything else
+ * (page pops, tags, stops, partly filled pages, both scale modes, new_indptr,
+ * max_new_per_req, page_table, exp_tags, seq_lens) is as for
+ * kv_append_quantize; a request that is not served gets no q_out rows.
+ * GQA pools with page_size * head_dim <= 2048 for K and V; others return
+ * KV_ERR_UNSUPPORTED.  Two kernel launches.
+ */
+kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                           int32_t total_new, const void* q, int64_t q_stride, const void* k_new,
+                           int64_t k_stride, const void* v_new, int64_t v_stride,
+                           const int32_t* new_indptr, int32_t max_new_per_req,
+                           const int32_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                           const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                           void* q_out, int32_t* page_table, uint32_t* exp_tags,
+                           int32_t max_pages_per_req, int32_t* seq_lens);
+
+/*
+ * Cached rows back as contiguous bf16 rows (SFS "Quantizing the KV cache":
+ * prefill works on a BF16 cache, decode on an FP8 one): a prefix that a bf16
+ * prefill reuses, a request that moves to another worker.
+ *
+ *   row_start   int32 [B] (device), or NULL (0): request r's first row.
+ *   out_indptr  int32 [B+1] (device): rows row_start[r] .. of request r go to
+ *               output rows out_indptr[r] .. out_indptr[r+1]-1.
+ *   total_rows  rows of the outputs; output rows that no request owns are
+ *               left untouched.
+ *   abort_mask  uint8 [B] or NULL: an aborted request's rows are not read and
+ *               its output rows are left untouched.
+ *   k_out       bf16 [total_rows][num_kv_heads][head_dim_k] (device; LATENT:
+ *               [total_rows][head_dim_k])
+ *   v_out       bf16 [total_rows][num_kv_heads][head_dim_v] (device; LATENT:
+ *               NULL)
+ * e4m3 pools: bf16(code * scale), the product in fp32; bf16 pools: the bits.
+ * A request whose rows are not all cached (row_start < 0, a negative count,
+ * row_start + rows > seq_lens[r] or beyond its page table) or do not fit the
+ * outputs gets KV_ERR_INVALID_ARG and no rows; a page id out of range sets
+ * KV_ERR_BAD_PAGE_ID and that page's rows are not written.  Any pool shape,
+ * both layouts.  One kernel launch.
+ */
+kv_status kv_read_rows(kv_pool* pool, void* stream, int32_t B, const int32_t* page_table,
+                       int32_t max_pages_per_req, const int32_t* seq_lens,
+                       const int32_t* row_start, const int32_t* out_indptr, int32_t total_rows,
+                       const uint8_t* abort_mask, void* k_out, void* v_out);
+
+/* Bytes of device workspace paged_prefill_attn needs on the current device (0
+ * for invalid arguments, unsupported shapes or when no device is visible). */
+size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_q_heads,
+                                    int32_t total_q);
+
+/*
+ * Causal attention of many new tokens over the paged cache: a chunk of a
+ * prompt behind what is cached of it, drafts of any length, and batches that
+ * mix chunks with requests that decode one token (paged_decode_attn takes
+ * the same few tokens of every request).
+ *
+ *   total_q     rows of q and out (device); rows that no request owns are left
+ *               untouched.
+ *   q           bf16 [total_q][num_q_heads][128]
+ *   q_indptr    int32 [B+1] (device), not decreasing: request r's queries are
+ *               rows q_indptr[r] .. q_indptr[r+1]-1, its last tokens, in order.
+ *   seq_lens    int32 [B] (device): cached tokens, the new ones included.
+ *   abort_mask  uint8 [B] from kv_verify_tags, or NULL: an aborted request's
+ *               pages are not read and its output rows are left untouched.
+ *   out         bf16 [total_q][num_q_heads][128] (device)
+ *   workspace   device scratch of at least paged_prefill_workspace_size bytes,
+ *               256-byte aligned; contents need not be initialised.
+ * Query i of the n of request r (L = seq_lens[r]) attends to positions
+ * 0 .. L - n + i; a query with no visible position gets zeros.  A request
+ * with a negative length or count, one beyond its page table, or rows beyond
+ * total_q sets KV_ERR_INVALID_ARG and is not written; one whose needed pages
+ * include an id outside [0, num_pages) sets KV_ERR_BAD_PAGE_ID, and the rows
+ * that would read it are not written.  GQA pools with head_dim 128 and
+ * page_size 16, e4m3 and bf16, any num_q_heads / num_kv_heads; others return
+ * KV_ERR_UNSUPPORTED.
+ */
+kv_status paged_prefill_attn(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                             int32_t total_q, const void* q, const int32_t* q_indptr,
+                             const int32_t* page_table, int32_t max_pages_per_req,
+                             const int32_t* seq_lens, const uint8_t* abort_mask, float sm_scale,
+                             void* out, void* workspace, size_t workspace_bytes);
+
 /* Human-readable name of a status code (static string). */
 const char* kv_status_string(kv_status status);
 

@@ -50,6 +50,7 @@ class kv_pool_desc(ctypes.Structure):
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _lib.kv_pool_create.argtypes = [ctypes.POINTER(kv_pool_desc), ctypes.POINTER(_vp)]
 _lib.kv_pool_create.restype = _i32
 _lib.kv_pool_destroy.argtypes = [_vp]
@@ -85,6 +86,16 @@ _lib.kv_decode_step_workspace_size.restype = _sz
 _lib.kv_decode_step.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
                                 _i32, _vp, _vp, _f32, _vp, _vp, _i32, _vp, _sz]
 _lib.kv_decode_step.restype = _i32
+_lib.kv_append_rotary.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                  _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp]
+_lib.kv_append_rotary.restype = _i32
+_lib.kv_read_rows.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+_lib.kv_read_rows.restype = _i32
+_lib.paged_prefill_workspace_size.argtypes = [_vp, _i32, _i32, _i32]
+_lib.paged_prefill_workspace_size.restype = _sz
+_lib.paged_prefill_attn.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _f32,
+                                    _vp, _vp, _sz]
+_lib.paged_prefill_attn.restype = _i32
 _lib.kv_status_string.argtypes = [_i32]
 _lib.kv_status_string.restype = ctypes.c_char_p
 _lib.kv_last_launch_count.argtypes = [_vp]
@@ -132,6 +143,22 @@ def _ptr(t, dtype=None, name="tensor"):
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t, heads, dim, name):
+    """Device pointer and row stride (elements) of a bf16 [rows][heads][dim]
+    tensor whose rows may lie apart (a part of a wider projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected [rows][{heads}][{dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or t.stride(1) != dim:
+        raise ValueError(f"{name}: a row's heads and dims must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
 
 
 def _stream(stream):
@@ -285,6 +312,72 @@ def kv_decode_step(handle, B, num_q_heads, q_tokens, leave_mask, k_new, v_new, n
     _check(st, "kv_decode_step")
 
 
+def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                     positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
+                     seq_lens, stream=None):
+    """kv_append_quantize of keys rotated on the way, with the queries rotated
+    into q_out (see kvfp8.h).  q, k_new and v_new are [rows][heads][dim] with
+    rows any multiple of 8 elements apart; positions int32 [axes][rows]."""
+    rows, Hk, Dk = k_new.shape
+    if v_new.shape[0] != rows or positions.dim() != 2 or positions.shape[1] != rows:
+        raise ValueError("q, k_new, v_new and positions must have the same rows")
+    qp = qo = None
+    qs = 0
+    if num_q_heads > 0:
+        qp, qs = _rows(q, num_q_heads, Dk, "q")
+        qo = _ptr(q_out, torch.bfloat16, "q_out")
+        if q.shape[0] != rows or q_out.shape != q.shape:
+            raise ValueError("q and q_out must have the rows of k_new")
+        if qo == qp and qs != num_q_heads * Dk:
+            raise ValueError("q_out may be q only when q is contiguous")
+    kp, ks = _rows(k_new, Hk, Dk, "k_new")
+    vp, vs = _rows(v_new, Hk, v_new.shape[2], "v_new")
+    if pair_axis.numel() != inv_freq.numel():
+        raise ValueError("pair_axis and inv_freq must have the same length")
+    st = _lib.kv_append_rotary(
+        handle, _stream(stream), int(B), int(num_q_heads), rows, qp, qs, kp, ks, vp, vs,
+        _ptr(new_indptr, torch.int32, "new_indptr"), int(max_new_per_req),
+        _ptr(positions, torch.int32, "positions"), positions.shape[0],
+        _ptr(pair_axis, torch.uint8, "pair_axis"), _ptr(inv_freq, torch.float64, "inv_freq"),
+        2 * inv_freq.numel(), int(interleaved), qo, _ptr(page_table, torch.int32, "page_table"),
+        _ptr(exp_tags, _U32, "exp_tags"), page_table.shape[-1],
+        _ptr(seq_lens, torch.int32, "seq_lens"))
+    _check(st, "kv_append_rotary")
+
+
+def kv_read_rows(handle, B, page_table, seq_lens, row_start, out_indptr, abort_mask, k_out, v_out,
+                 stream=None):
+    """Cached rows row_start[r] .. of each request as contiguous bf16 rows
+    out_indptr[r] .. of k_out / v_out (v_out None for latent pools)."""
+    st = _lib.kv_read_rows(
+        handle, _stream(stream), int(B), _ptr(page_table, torch.int32, "page_table"),
+        page_table.shape[-1], _ptr(seq_lens, torch.int32, "seq_lens"),
+        _ptr(row_start, torch.int32, "row_start"), _ptr(out_indptr, torch.int32, "out_indptr"),
+        k_out.shape[0], _ptr(abort_mask, torch.uint8, "abort_mask"),
+        _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v_out, torch.bfloat16, "v_out"))
+    _check(st, "kv_read_rows")
+
+
+def paged_prefill_workspace_size(handle, B, num_q_heads, total_q) -> int:
+    return int(_lib.paged_prefill_workspace_size(handle, int(B), int(num_q_heads), int(total_q)))
+
+
+def paged_prefill_attn(handle, B, num_q_heads, q, q_indptr, page_table, seq_lens, abort_mask,
+                       sm_scale, out, workspace, stream=None):
+    """Causal attention of a ragged batch's new tokens (q [total_q][heads][128],
+    request r's at q_indptr[r] ..) over the paged cache (see kvfp8.h)."""
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    st = _lib.paged_prefill_attn(
+        handle, _stream(stream), int(B), int(num_q_heads), q.shape[0],
+        _ptr(q, torch.bfloat16, "q"), _ptr(q_indptr, torch.int32, "q_indptr"),
+        _ptr(page_table, torch.int32, "page_table"), page_table.shape[-1],
+        _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(abort_mask, torch.uint8, "abort_mask"),
+        float(sm_scale), _ptr(out, torch.bfloat16, "out"),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    _check(st, "paged_prefill_attn")
+
+
 # ---------------------------------------------------------------- pool helper
 
 class KVPool:
@@ -293,12 +386,15 @@ class KVPool:
     Allocates the caller-owned buffers the C ABI documents (cache, scales,
     tags, free list, control block) and holds the library handle.  GQA:
     k_cache [pages][Hkv][P][Dk], v_cache [pages][Hkv][Dv][P]; LATENT:
-    k_cache [pages][P][Dk].  e4m3 caches are uint8 tensors.
+    k_cache [pages][P][Dk].  e4m3 caches are uint8 tensors.  Buffers that the
+    caller holds already (k_cache, k_scale, v_cache, v_scale, ctl, of those
+    shapes and types, contiguous) are taken as they are.
     """
 
     def __init__(self, num_pages, page_size, num_kv_heads, head_dim_k, head_dim_v,
                  dtype=KV_DTYPE_E4M3, layout=KV_LAYOUT_GQA, device="cuda", tags=None,
-                 free_list=None, scale_mode=KV_SCALE_FROZEN):
+                 free_list=None, scale_mode=KV_SCALE_FROZEN, k_cache=None, k_scale=None,
+                 v_cache=None, v_scale=None, ctl=None):
         dev = torch.device(device)
         self.scale_mode = int(scale_mode)
         self.num_pages, self.page_size = int(num_pages), int(page_size)
@@ -306,28 +402,36 @@ class KVPool:
             int(num_kv_heads), int(head_dim_k), int(head_dim_v))
         self.dtype, self.layout = int(dtype), int(layout)
         edt = torch.uint8 if dtype == KV_DTYPE_E4M3 else torch.bfloat16
+
+        def buf(given, shape, dt, name):
+            if given is None:
+                return torch.zeros(shape, dtype=dt, device=dev)
+            if tuple(given.shape) != shape or given.device.type != dev.type:
+                raise ValueError(f"{name}: expected {shape} on {dev}, got {tuple(given.shape)} "
+                                 f"on {given.device}")
+            _ptr(given, dt, name)
+            return given
+
+        fp8 = dtype == KV_DTYPE_E4M3
         if layout == KV_LAYOUT_GQA:
-            self.k_cache = torch.zeros((num_pages, num_kv_heads, page_size, head_dim_k), dtype=edt,
-                                       device=dev)
-            self.v_cache = torch.zeros((num_pages, num_kv_heads, head_dim_v, page_size), dtype=edt,
-                                       device=dev)
-            if dtype == KV_DTYPE_E4M3:
-                self.k_scale = torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=dev)
-                self.v_scale = torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=dev)
-            else:
-                self.k_scale = self.v_scale = None
+            self.k_cache = buf(k_cache, (num_pages, num_kv_heads, page_size, head_dim_k), edt,
+                               "k_cache")
+            self.v_cache = buf(v_cache, (num_pages, num_kv_heads, head_dim_v, page_size), edt,
+                               "v_cache")
+            heads = (num_pages, num_kv_heads)
+            self.k_scale = buf(k_scale, heads, torch.float32, "k_scale") if fp8 else None
+            self.v_scale = buf(v_scale, heads, torch.float32, "v_scale") if fp8 else None
         else:
-            self.k_cache = torch.zeros((num_pages, page_size, head_dim_k), dtype=edt, device=dev)
+            self.k_cache = buf(k_cache, (num_pages, page_size, head_dim_k), edt, "k_cache")
             self.v_cache = None
-            self.k_scale = (torch.zeros((num_pages,), dtype=torch.float32, device=dev)
-                            if dtype == KV_DTYPE_E4M3 else None)
+            self.k_scale = buf(k_scale, (num_pages,), torch.float32, "k_scale") if fp8 else None
             self.v_scale = None
         # uint32 tags held in an int32 tensor (same bits; torch has few uint32 ops)
         self.tags = (torch.zeros(num_pages, dtype=torch.int32, device=dev) if tags is None
                      else u32_as_i32(tags).to(dev))
         self.free_list = (torch.arange(num_pages, dtype=torch.int32, device=dev) if free_list is None
                           else torch.as_tensor(free_list, dtype=torch.int32).to(dev))
-        self.ctl = torch.zeros(KV_CTL_WORDS, dtype=torch.int32, device=dev)
+        self.ctl = buf(ctl, (KV_CTL_WORDS,), torch.int32, "ctl")
         d = kv_pool_desc()
         d.num_pages, d.page_size, d.num_kv_heads = self.num_pages, self.page_size, self.num_kv_heads
         d.head_dim_k, d.head_dim_v, d.dtype, d.layout = (
@@ -394,6 +498,33 @@ class KVPool:
         kv_decode_step(self.handle, B, num_q_heads, q_tokens, leave_mask, k_new, v_new,
                        new_indptr, max_new_per_req, page_table, exp_tags, seq_lens, q, sm_scale,
                        out, abort_mask, flags, workspace, stream)
+
+    def append_rotary(self, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                      positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
+                      seq_lens, stream=None):
+        if tuple(k_new.shape[1:]) != (self.num_kv_heads, self.head_dim_k):
+            raise ValueError("k_new: expected [rows][num_kv_heads][head_dim_k]")
+        if tuple(v_new.shape[1:]) != (self.num_kv_heads, self.head_dim_v):
+            raise ValueError("v_new: expected [rows][num_kv_heads][head_dim_v]")
+        kv_append_rotary(self.handle, B, num_q_heads, q, k_new, v_new, new_indptr,
+                         max_new_per_req, positions, pair_axis, inv_freq, interleaved, q_out,
+                         page_table, exp_tags, seq_lens, stream)
+
+    def read_rows(self, B, page_table, seq_lens, row_start, out_indptr, abort_mask, k_out,
+                  v_out=None, stream=None):
+        kv_read_rows(self.handle, B, page_table, seq_lens, row_start, out_indptr, abort_mask,
+                     k_out, v_out, stream)
+
+    def prefill_workspace_size(self, B, num_q_heads, total_q) -> int:
+        n = paged_prefill_workspace_size(self.handle, B, num_q_heads, total_q)
+        if n == 0:
+            raise KVError(KV_ERR_UNSUPPORTED, "paged_prefill_workspace_size")
+        return n
+
+    def prefill_attn(self, B, num_q_heads, q, q_indptr, page_table, seq_lens, abort_mask,
+                     sm_scale, out, workspace, stream=None):
+        paged_prefill_attn(self.handle, B, num_q_heads, q, q_indptr, page_table, seq_lens,
+                           abort_mask, sm_scale, out, workspace, stream)
 
     def error(self) -> int:
         """Device error word (synchronises)."""

@@ -1,7 +1,7 @@
 // api.cu -- the C ABI declared in include/kvfp8.h: argument validation,
 // launch configuration and workspace carve-up.  All compute is in the
-// kernels of append.cu, verify.cu, release.cu, decode_gqa.cu and
-// decode_latent.cu; kv_decode_step chains them on one stream.
+// kernels of append.cu, rotary.cu, read.cu, verify.cu, release.cu, prefill.cu,
+// decode_gqa.cu and decode_latent.cu; kv_decode_step chains them on one stream.
 #include <math.h>
 
 #include <new>
@@ -174,6 +174,17 @@ kv_status decode_prepare(kv_pool* pool, int32_t B, int32_t Hq, int32_t T, const 
   const size_t need = decode_ws_layout(d, B, Hkv, cfg, workspace, &x.ws);
   if (B > 0 && workspace_bytes < need) return KV_ERR_INVALID_ARG;
   *kind = cfg.kind;
+  return KV_OK;
+}
+
+// Shapes that paged_prefill_attn takes.
+kv_status prefill_check(const kv_pool_desc& d, int B, int Hq, int total_q) {
+  if (B < 0 || Hq <= 0 || total_q < 0 || Hq % d.num_kv_heads != 0) return KV_ERR_INVALID_ARG;
+  if (d.layout != KV_LAYOUT_GQA || d.head_dim_k != 128 || d.head_dim_v != 128 ||
+      d.page_size != 16)
+    return KV_ERR_UNSUPPORTED;
+  // query rows of one kv head are counted in an int
+  if ((long long)total_q * Hq > INT32_MAX) return KV_ERR_UNSUPPORTED;
   return KV_OK;
 }
 
@@ -541,6 +552,140 @@ kv_status kv_decode_step(kv_pool* pool, void* stream, int32_t B, int32_t num_q_h
     ra.mask_bits = KV_ABORT_TAG;
     e = launch_release(ra, s, &n);
   }
+  pool->last_launches = n;
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                           int32_t total_new, const void* q, int64_t q_stride, const void* k_new,
+                           int64_t k_stride, const void* v_new, int64_t v_stride,
+                           const int32_t* new_indptr, int32_t max_new_per_req,
+                           const int32_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                           const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                           void* q_out, int32_t* page_table, uint32_t* exp_tags,
+                           int32_t max_pages_per_req, int32_t* seq_lens) {
+  if (!pool) return KV_ERR_INVALID_ARG;
+  pool->last_launches = 0;
+  const kv_pool_desc& d = pool->d;
+  if (B < 0 || total_new < 0 || max_new_per_req < 0 || max_pages_per_req <= 0 || num_q_heads < 0)
+    return KV_ERR_INVALID_ARG;
+  if (d.layout != KV_LAYOUT_GQA || !append_tile_fits(d)) return KV_ERR_UNSUPPORTED;
+  if (num_axes < 1 || num_axes > 256 || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
+      rotary_dim > d.head_dim_k || (interleaved != 0 && interleaved != 1))
+    return KV_ERR_INVALID_ARG;
+  if (B == 0) return KV_OK;
+  if (!new_indptr || !page_table || !exp_tags || !seq_lens) return KV_ERR_INVALID_ARG;
+  if (total_new > 0) {
+    const int64_t kw = (int64_t)d.num_kv_heads * d.head_dim_k;
+    const int64_t vw = (int64_t)d.num_kv_heads * d.head_dim_v;
+    const int64_t qw = (int64_t)num_q_heads * d.head_dim_k;
+    if (!k_new || !v_new || !positions || !pair_axis || !inv_freq || !aligned16(k_new) ||
+        !aligned16(v_new) || k_stride < kw || v_stride < vw || k_stride % 8 != 0 ||
+        v_stride % 8 != 0)
+      return KV_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < qw ||
+                            q_stride % 8 != 0))
+      return KV_ERR_INVALID_ARG;
+  }
+  RotaryArgs a = {};
+  a.app.d = d;
+  a.app.B = B;
+  a.app.k_new = static_cast<const uint16_t*>(k_new);
+  a.app.v_new = static_cast<const uint16_t*>(v_new);
+  a.app.new_indptr = new_indptr;
+  a.app.max_new = max_new_per_req < total_new ? max_new_per_req : total_new;
+  a.app.page_table = page_table;
+  a.app.exp_tags = exp_tags;
+  a.app.max_pages = max_pages_per_req;
+  a.app.seq_lens = seq_lens;
+  a.q = num_q_heads > 0 ? static_cast<const uint16_t*>(q) : nullptr;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.Hq = num_q_heads;
+  a.total_new = total_new;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.inv_freq = inv_freq;
+  a.num_axes = num_axes;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  int n = 0;
+  const cudaError_t e = launch_append_rotary(a, static_cast<cudaStream_t>(stream), &n);
+  pool->last_launches = n;
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+kv_status kv_read_rows(kv_pool* pool, void* stream, int32_t B, const int32_t* page_table,
+                       int32_t max_pages_per_req, const int32_t* seq_lens,
+                       const int32_t* row_start, const int32_t* out_indptr, int32_t total_rows,
+                       const uint8_t* abort_mask, void* k_out, void* v_out) {
+  if (!pool) return KV_ERR_INVALID_ARG;
+  pool->last_launches = 0;
+  if (B < 0 || total_rows < 0 || max_pages_per_req <= 0) return KV_ERR_INVALID_ARG;
+  if (B == 0 || total_rows == 0) return KV_OK;
+  if (!page_table || !seq_lens || !out_indptr || !k_out || !aligned16(k_out))
+    return KV_ERR_INVALID_ARG;
+  if (pool->d.layout == KV_LAYOUT_GQA && (!v_out || !aligned16(v_out))) return KV_ERR_INVALID_ARG;
+  ReadArgs a;
+  a.d = pool->d;
+  a.B = B;
+  a.max_pages = max_pages_per_req;
+  a.total_rows = total_rows;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.row_start = row_start;
+  a.out_indptr = out_indptr;
+  a.abort_mask = abort_mask;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  int n = 0;
+  const cudaError_t e = launch_read_rows(a, static_cast<cudaStream_t>(stream), &n);
+  pool->last_launches = n;
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_q_heads,
+                                    int32_t total_q) {
+  if (!pool || prefill_check(pool->d, B, num_q_heads, total_q) != KV_OK) return 0;
+  return prefill_ws_bytes(pool->d, B, num_q_heads, total_q);
+}
+
+kv_status paged_prefill_attn(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                             int32_t total_q, const void* q, const int32_t* q_indptr,
+                             const int32_t* page_table, int32_t max_pages_per_req,
+                             const int32_t* seq_lens, const uint8_t* abort_mask, float sm_scale,
+                             void* out, void* workspace, size_t workspace_bytes) {
+  if (!pool) return KV_ERR_INVALID_ARG;
+  pool->last_launches = 0;
+  const kv_status st = prefill_check(pool->d, B, num_q_heads, total_q);
+  if (st != KV_OK) return st;
+  if (B == 0 || total_q == 0) return KV_OK;
+  if (!q || !q_indptr || !page_table || max_pages_per_req <= 0 || !seq_lens || !out ||
+      !aligned16(q) || !aligned16(out) || !isfinite(sm_scale) || !workspace ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return KV_ERR_INVALID_ARG;
+  const size_t need = prefill_ws_bytes(pool->d, B, num_q_heads, total_q);
+  if (need == 0) return KV_ERR_CUDA;
+  if (workspace_bytes < need) return KV_ERR_INVALID_ARG;
+  PrefillArgs a;
+  a.d = pool->d;
+  a.B = B;
+  a.Hq = num_q_heads;
+  a.G = num_q_heads / pool->d.num_kv_heads;
+  a.total_q = total_q;
+  a.max_pages = max_pages_per_req;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_indptr = q_indptr;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.abort_mask = abort_mask;
+  a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.workspace = workspace;
+  int n = 0;
+  const cudaError_t e = launch_prefill(a, static_cast<cudaStream_t>(stream), &n);
   pool->last_launches = n;
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }

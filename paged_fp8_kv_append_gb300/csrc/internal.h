@@ -112,9 +112,58 @@ struct AppendArgs {
   const int32_t* src_lens;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches);
+// the plan kernel alone (pages popped, tags stamped, lengths advanced), for
+// an append whose rows another kernel writes
+cudaError_t launch_append_plan(const AppendArgs& a, cudaStream_t s, int* launches);
+// whether a (page, kv head, K|V) tile fits one warp's registers
+bool append_tile_fits(const kv_pool_desc& d);
 // whether a pool-to-pool handoff of B requests into a pool of this shape fits
 // the bulk append kernels
 bool append_handoff_supported(const kv_pool_desc& d, int B, int src_max_pages);
+
+// ---- rotary append --------------------------------------------------------
+struct RotaryArgs {
+  AppendArgs app;          // pool, rows (k_new, v_new), request bookkeeping
+  const uint16_t* q;       // bf16 bits, row t at q + t * q_stride (NULL: no queries)
+  uint16_t* q_out;         // bf16 bits [total_new][Hq][Dk]
+  int64_t q_stride, k_stride, v_stride;  // elements between rows of q / k_new / v_new
+  int32_t Hq, total_new;
+  const int32_t* positions;   // [num_axes][total_new]
+  const uint8_t* pair_axis;   // [rotary_dim / 2]
+  const double* inv_freq;     // [rotary_dim / 2]
+  int32_t num_axes, rotary_dim, interleaved;
+};
+cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launches);
+
+// ---- reading rows back ------------------------------------------------------
+struct ReadArgs {
+  kv_pool_desc d;
+  int32_t B, max_pages, total_rows;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* row_start;   // NULL: 0
+  const int32_t* out_indptr;
+  const uint8_t* abort_mask;  // NULL: none
+  uint16_t* k_out;            // bf16 bits
+  uint16_t* v_out;
+};
+cudaError_t launch_read_rows(const ReadArgs& a, cudaStream_t s, int* launches);
+
+// ---- attention of many new tokens -------------------------------------------
+struct PrefillArgs {
+  kv_pool_desc d;
+  int32_t B, Hq, G, total_q, max_pages;
+  const uint16_t* q;        // bf16 bits [total_q][Hq][D]
+  const int32_t* q_indptr;  // [B+1]
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const uint8_t* abort_mask;
+  float sm_scale_log2;      // sm_scale * log2(e)
+  uint16_t* out;            // bf16 bits [total_q][Hq][D]
+  void* workspace;
+};
+size_t prefill_ws_bytes(const kv_pool_desc& d, int B, int Hq, int total_q);
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s, int* launches);
 
 // Kernel configuration chosen for a pool (shape checks + grid).
 struct DecodeConfig {

@@ -1,0 +1,41 @@
+// ragged.cuh -- work items of a ragged batch without a prefix pass.
+//
+// Request r of a batch has the flat rows indptr[r] .. indptr[r+1]-1, which lie
+// in consecutive pages of its own from any slot on.  n rows touch at most
+// floor((n - 2) / P) + 2 pages, and
+//   first(r) = floor(indptr[r] / P) + 2 r
+// leaves floor(indptr[r+1] / P) - floor(indptr[r] / P) + 2 >= floor(n / P) + 2
+// item numbers to request r: enough for every page it touches, at most two a
+// request left over.  An item finds its request by searching indptr alone, so
+// a kernel over a batch's pages needs neither a plan launch nor a scan.
+#pragma once
+
+#include "common.cuh"
+
+namespace kvfp8 {
+
+__host__ __device__ inline long long ragged_items(long long total_rows, int B, int P) {
+  return total_rows / P + 2LL * B;
+}
+
+__device__ __forceinline__ long long ragged_first(long long row, int P, int r) {
+  return row / P + 2LL * r;
+}
+
+// The request whose item numbers hold `item` (indptr not decreasing), found by
+// a whole warp: 32 entries a step.  Always in [0, B).
+__device__ __forceinline__ int ragged_owner(const int32_t* indptr, int B, int P, long long item) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = lane * step < n && (lane == 0 || ragged_first(indptr[at], P, at) <= item);
+    const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+}  // namespace kvfp8
