@@ -1,116 +1,1036 @@
 // prefill.cu -- paged_prefill_attn: causal attention of many new tokens of a
-// ragged batch over the paged cache.
+// ragged batch over the paged cache, on the tcgen05 tensor cores.
+//
+// "Smaller, faster, safer: running Kimi and GLM at scale", section
+// "Quantizing the KV cache": attention reads the e4m3 cache and converts
+// values as it reads them; bf16 is the baseline format.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j), j <= L - n + i,
+// in one pass over the keys with the running maximum and sum of each row.
+//
+// Work decomposition.  A request's query rows of one kv head are row = t * G + g
+// (token, head of the group); 256 of them are an item's two tiles of 128 rows
+// (A and B).  An item with at most 128 rows has one tile, and then A and B are
+// the same rows over alternate key blocks, merged when the item ends.  A block is
+// 128 tokens (8 pages).  Items are laid out request-major, a block costing 2 (two
+// tiles) or 1, and the whole batch is cut into equal ranges, one per persistent
+// CTA: every CTA works equally long whatever the lengths.  A CTA writes an item
+// that lies wholly in its range; an item cut by a range's end leaves fp32
+// partials (o, running max, sum) for the combine kernel, at most two a CTA.
+//
+// Per CTA (one per SM), 13 warps:
+//   softmax A (0-3), B (4-7)  a thread per row: S from tensor memory twice (max,
+//                   then exp2), P back to tensor memory as the A operand of PV;
+//                   the output accumulator is rescaled only when a row's maximum
+//                   grows by more than 2^8, by the same warp; at an item's end
+//                   the output
+//   converters (8-11)  global pages -> registers -> 128B-swizzled K-major tiles
+//                   in shared memory: Q once an item, K [token][dim] and V
+//                   [dim][token] (pages hold V dim-major: no transpose).  e4m3
+//                   codes become f16 exactly, bf16 is copied
+//   MMA (12)        S = Q K^T and O += P V (M = N = 128), one tile's products
+//                   running while the other tile's softmax does
+// Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 #include <climits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
+#include "tcgen05.cuh"
 
 namespace kvfp8 {
 namespace {
 
-constexpr int kThreads = 256, kD = 128, kP = 16;
+constexpr int kD = 128, kP = 16;
+constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
+constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMeta = 4;  // block records in flight, and query exponents of as many pieces
 
-__device__ __forceinline__ int row_owner(const int32_t* indptr, int B, long long t) {
-  int lo = 0, hi = B;  // the last r with indptr[r] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (indptr[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
+// shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
+constexpr int kHalf = 128 * 128, kTileBytes = 2 * kHalf;
+constexpr int OFF_Q = 0;                          // tiles A, B
+constexpr int OFF_K = OFF_Q + 2 * kTileBytes;     // 2 blocks
+constexpr int OFF_V = OFF_K + 2 * kTileBytes;     // 2 blocks
+constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
+constexpr int OFF_QEXP = OFF_META + kMeta * kBlkPages * 16;  // [kMeta][256] int
+constexpr int OFF_MLB = OFF_QEXP + kMeta * kItemRows * 4;    // [128] float2
+constexpr int OFF_BAR = OFF_MLB + kTile * 8;
+constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1;
+constexpr int OFF_MISC = OFF_BAR + kBars * 8;
+constexpr int kSmem = OFF_MISC + 64;
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+
+// tensor memory columns: S (and P, in its first 64 columns) and O of each tile
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t tmem_s(int x) { return 128u * x; }
+__device__ __forceinline__ uint32_t tmem_o(int x) { return 256u + 128u * x; }
+
+// kind::f16 instruction descriptor: f32 accumulate, both operands K-major
+constexpr uint32_t idesc(bool bf16) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((128u >> 3) << 17) |
+         ((128u >> 4) << 24);
 }
 
-// One warp per (query token, head); lane l holds dims 4l .. 4l+3.
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads) prefill_simple_kernel(const PrefillArgs a) {
+// ------------------------------------------------------------------ plan
+
+struct Ws {
+  long long* pfx;   // [V+1] cost of the items before, per kv head
+  int4* items;      // [V] {request, first row, rows, blocks}
+  int4* cut;        // [grid] {item (-1: none), kv head, last CTA, 0}: the cut item a CTA begins
+  float2* ml;       // [2 grid][256] (running max, sum; -1: a page that must not be read)
+  float4* o;        // [2 grid][32][256]: 4 dims of a row
+  size_t bytes;
+};
+
+__host__ __device__ inline long long item_first(long long q0, int G, int r) {
+  return q0 * G / kItemRows + r;
+}
+
+long long item_count(int B, int G, int total_q) {
+  return (long long)total_q * G / kItemRows + B;
+}
+
+Ws ws_layout(void* base, int B, int G, int total_q, int grid) {
+  const size_t V = (size_t)item_count(B, G, total_q);
+  size_t off = 0;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  auto take = [&](size_t n) {
+    uint8_t* p = b + off;
+    off = (off + n + 255) & ~size_t(255);
+    return p;
+  };
+  Ws w;
+  w.pfx = reinterpret_cast<long long*>(take(8 * (V + 1)));
+  w.items = reinterpret_cast<int4*>(take(16 * V));
+  w.cut = reinterpret_cast<int4*>(take(16 * (size_t)grid));
+  w.ml = reinterpret_cast<float2*>(take(8ull * 2 * grid * kItemRows));
+  w.o = reinterpret_cast<float4*>(take(4ull * 2 * grid * kItemRows * kD));
+  w.bytes = off;
+  return w;
+}
+
+struct Args {
+  PrefillArgs p;
+  Ws ws;
+  int V, grid;
+};
+
+constexpr int kPlanThreads = 1024;
+
+// One CTA: every item's request, rows and blocks, and the cost prefix.
+__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (item >= (long long)a.total_q * a.Hq) return;
-  const long long t = item / a.Hq;
-  const int h = (int)(item % a.Hq), H = a.d.num_kv_heads, kvh = h / a.G;
-  const int r = row_owner(a.q_indptr, a.B, t);
-  const long long q0 = a.q_indptr[r], q1 = a.q_indptr[r + 1], L = a.seq_lens[r];
-  if (t < q0 || t >= q1) return;
-  if (a.abort_mask != nullptr && a.abort_mask[r] != 0) return;
-  if (L < 0 || (L + kP - 1) / kP > a.max_pages || q0 < 0 || q1 > a.total_q) {
-    if (lane == 0) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
+  __shared__ long long sums[32];
+  const PrefillArgs& p = a.p;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  long long carry = 0;
+  for (int base = 0; base < a.V; base += kPlanThreads) {
+    const int v = base + threadIdx.x;
+    long long cost = 0;
+    if (v < a.V) {
+      int lo = 0, hi = p.B;  // the last r whose items begin at or before v
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (item_first(p.q_indptr[mid], p.G, mid) <= v) lo = mid; else hi = mid;
+      }
+      const int r = lo;
+      const long long q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1], n = q1 - q0;
+      const long long L = p.seq_lens[r], row0 = (v - item_first(q0, p.G, r)) * kItemRows;
+      int4 it = make_int4(r, 0, 0, 0);
+      const bool aborted = p.abort_mask != nullptr && p.abort_mask[r] != 0;
+      if (!aborted && n != 0) {
+        if (n < 0 || q0 < 0 || q1 > p.total_q || L < 0 || (L + kP - 1) / kP > p.max_pages ||
+            L > INT_MAX - 2 * kBlk) {  // (positions of a block are ints)
+          set_error(p.d.ctl, KV_ERR_INVALID_ARG);
+        } else if (row0 >= 0 && row0 < n * p.G) {
+          it.y = (int)row0;
+          it.z = (int)min((long long)kItemRows, n * p.G - row0);
+          const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
+          it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
+          cost = (long long)it.w * (it.z > kTile ? 2 : 1);
+        }
+      }
+      a.ws.items[v] = it;
+    }
+    long long s = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) sums[wid] = s;
+    __syncthreads();
+    if (wid == 0) {
+      long long t = sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += x;
+      }
+      sums[lane] = t;
+    }
+    __syncthreads();
+    if (v < a.V) a.ws.pfx[v] = carry + s - cost + (wid > 0 ? sums[wid - 1] : 0);
+    carry += sums[31];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.ws.pfx[a.V] = carry;
+}
+
+// -------------------------------------------------------- a CTA's pieces
+
+// The piece of an item (item v, kv head h) that lies in [x_begin, x_end) of
+// the cost axis: blocks b_lo .. b_hi-1 of its nb.
+struct Piece {
+  int v, h;
+  int r, row0, nrows, nb;
+  int b_lo, b_hi;
+  int L, n, q0;
+  long long x0;  // cost position of its block 0
+  __device__ __forceinline__ int w() const { return nrows > kTile ? 2 : 1; }
+  __device__ __forceinline__ bool both() const { return nrows > kTile; }
+  __device__ __forceinline__ int count() const { return b_hi - b_lo; }
+};
+
+__device__ __forceinline__ int block_at(long long x, const Piece& s) {  // first block at or behind x
+  const long long d = x - s.x0;
+  return d <= 0 ? 0 : (int)min((long long)s.nb, (d + s.w() - 1) / s.w());
+}
+
+__device__ void piece_load(Piece& s, const Args& a, long long x_begin, long long x_end) {
+  const int4 it = a.ws.items[s.v];
+  s.r = it.x;
+  s.row0 = it.y;
+  s.nrows = it.z;
+  s.nb = it.w;
+  s.x0 = a.ws.pfx[s.v] * a.p.d.num_kv_heads + (long long)s.h * s.nb * s.w();
+  s.b_lo = block_at(x_begin, s);
+  s.b_hi = block_at(x_end, s);
+  s.L = a.p.seq_lens[s.r];
+  s.q0 = a.p.q_indptr[s.r];
+  s.n = a.p.q_indptr[s.r + 1] - s.q0;
+}
+
+// The next piece with a block; false behind the range.
+__device__ bool piece_next(Piece& s, const Args& a, long long x_begin, long long x_end) {
+  for (;;) {
+    if (s.x0 + (long long)s.nb * s.w() >= x_end) return false;
+    if (++s.h == a.p.d.num_kv_heads) {
+      s.h = 0;
+      do {
+        if (++s.v >= a.V) return false;
+      } while (a.ws.pfx[s.v + 1] == a.ws.pfx[s.v]);
+    }
+    piece_load(s, a, x_begin, x_end);
+    if (s.b_lo < s.b_hi) return true;
+  }
+}
+
+// The first piece (v: the item that holds x_begin).
+__device__ bool piece_first(Piece& s, const Args& a, int v, long long x_begin, long long x_end) {
+  s.v = v;
+  s.h = 0;
+  piece_load(s, a, x_begin, x_end);
+  const long long per_head = (long long)s.nb * s.w();
+  s.h = (int)((x_begin - s.x0) / per_head);
+  piece_load(s, a, x_begin, x_end);
+  return s.b_lo < s.b_hi || piece_next(s, a, x_begin, x_end);
+}
+
+// --------------------------------------------------------------- helpers
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  if (FP8) return pack_f16(lo, hi);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+struct Bars {
+  uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
+  uint64_t* meta_ready;                                  // [kMeta]
+  uint64_t *q_ready, *q_free;
+  uint64_t *s_full, *p_ready, *o_full, *epi_done;        // [2] (tile)
+  uint64_t *b_ml, *drain;
+};
+
+// --------------------------------------------------------------- kernel
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float4* meta = reinterpret_cast<float4*>(smem + OFF_META);
+  int* qexp = reinterpret_cast<int*>(smem + OFF_QEXP);
+  float2* ml_b = reinterpret_cast<float2*>(smem + OFF_MLB);
+  uint64_t* bp = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  Bars bar;
+  bar.k_ready = bp, bar.k_free = bp + 2, bar.v_ready = bp + 4, bar.v_free = bp + 6;
+  bar.meta_ready = bp + 8;
+  bar.q_ready = bp + 8 + kMeta, bar.q_free = bar.q_ready + 1;
+  bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
+  bar.epi_done = bar.s_full + 6;
+  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  volatile int* first_item = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
+
+  const PrefillArgs& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = p.d.num_kv_heads;
+  const long long total = a.ws.pfx[a.V] * H;
+  // at least 2, so that every range holds a block's start
+  const long long per = max(2LL, (total + a.grid - 1) / a.grid);
+  const long long x_begin = (long long)blockIdx.x * per, x_end = min(total, x_begin + per);
+  if (x_begin >= x_end) {
+    if (threadIdx.x == 0) a.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const long long seen = L - (q1 - q0) + (t - q0) + 1;  // visible positions
-  const uint2 qw = *reinterpret_cast<const uint2*>(a.q + item * kD + 4 * lane);
-  const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-  float o[4] = {0, 0, 0, 0}, M = -INFINITY, l = 0.0f;
-  for (long long j = 0; j * kP < seen; ++j) {
-    const int p = a.page_table[(long long)r * a.max_pages + j];
-    if (p < 0 || p >= a.d.num_pages) {
-      if (lane == 0) set_error(a.d.ctl, KV_ERR_BAD_PAGE_ID);
-      return;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 1) {
+    // the last item that begins at or before x_begin, 32 entries a step
+    int lo = 0, n = a.V;
+    while (n > 1) {
+      const int step = (n + 31) / 32, at = lo + lane * step;
+      const bool le = lane * step < n && (lane == 0 || a.ws.pfx[at] * H <= x_begin);
+      const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
+      n = min(step, n - k * step);
+      lo += k * step;
     }
-    const long long ph = (long long)p * H + kvh;
-    const float ks = FP8 ? a.d.k_scale[ph] : 1.0f, vs = FP8 ? a.d.v_scale[ph] : 1.0f;
-    const int nv = (int)min((long long)kP, seen - j * kP);
-    float s[kP], mx = -INFINITY;
+    if (lane == 0) *first_item = lo;
+  } else if (threadIdx.x == 64) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_ready[i], kConvWarps);
+      mbar_init(&bar.k_free[i], 1);
+      mbar_init(&bar.v_ready[i], kConvWarps);
+      mbar_init(&bar.v_free[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_ready[i], 4);
+      mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.epi_done[i], 4);
+    }
+    for (int i = 0; i < kMeta; ++i) mbar_init(&bar.meta_ready[i], kConvWarps);
+    mbar_init(bar.q_ready, kConvWarps);
+    mbar_init(bar.q_free, 1);
+    mbar_init(bar.b_ml, 4);
+    mbar_init(bar.drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int32_t* ctl = p.d.ctl;
+  Piece s;
+  bool more = piece_first(s, a, *first_item, x_begin, x_end);
+
+  if (warp >= kSoftWarps && warp < kMmaWarp) {
+    // ============================ converters ============================
+    const int cw = warp - kSoftWarps, ct = threadIdx.x - kSoftWarps * 32;
+    const bool flip = p.sm_scale_log2 < 0.0f;  // a negative scale turns the queries' sign
+    constexpr int kEs = FP8 ? 1 : 2;
+    constexpr int kParts = FP8 ? 1 : 2;        // 16 KB source parts of a block's K or V
+    constexpr long long kPageBytes = (long long)kP * kD * kEs;
+    const uint8_t* kc = static_cast<const uint8_t*>(p.d.k_cache);
+    const uint8_t* vc = static_cast<const uint8_t*>(p.d.v_cache);
+    int piece = 0;
+    long long u = 0;
+    bool go = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
+      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
+                                                   wait_info(warp, 1, info)));
+      return go;
+    };
+    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
+      // ---- the item's query rows (16 lanes a row)
+      if (piece > 0 && !wait(bar.q_free, (uint32_t)(piece - 1), 60)) break;
+      const int tiles = s.both() ? 2 : 1;
+      for (int i0 = 0; i0 < 16 * tiles; i0 += 8) {
+        uint4 x[8];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      float k[4];
-      if (FP8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-            static_cast<const uint8_t*>(a.d.k_cache) + (ph * kP + i) * kD + 4 * lane);
-        const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(w & 0xFFFF, __NV_E4M3)));
-        const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(w >> 16, __NV_E4M3)));
-        k[0] = x.x, k[1] = x.y, k[2] = y.x, k[3] = y.y;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(
-            static_cast<const uint16_t*>(a.d.k_cache) + (ph * kP + i) * kD + 4 * lane);
-        k[0] = bf16_lo(w.x), k[1] = bf16_hi(w.x), k[2] = bf16_lo(w.y), k[3] = bf16_hi(w.y);
+        for (int i = 0; i < 8; ++i) {
+          const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row < s.nrows) {
+            const int tg = s.row0 + row, t = tg / p.G, g = tg - t * p.G;
+            x[i] = *reinterpret_cast<const uint4*>(
+                p.q + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD + 8 * (lane & 15));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4), c = lane & 15;
+          uint4 y = x[i];
+          if (flip) {
+            y.x ^= 0x80008000u;
+            y.y ^= 0x80008000u;
+            y.z ^= 0x80008000u;
+            y.w ^= 0x80008000u;
+          }
+          if (FP8) {
+            uint32_t mb = bf16_absbits_max8(x[i]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+            const int e = q_row_exp(mb);
+            const float pw = pow2f(e);
+            y.x = bf16x2_to_f16x2_scaled(y.x, pw);
+            y.y = bf16x2_to_f16x2_scaled(y.y, pw);
+            y.z = bf16x2_to_f16x2_scaled(y.z, pw);
+            y.w = bf16x2_to_f16x2_scaled(y.w, pw);
+            if (c == 0) qexp[(piece & (kMeta - 1)) * kItemRows + row] = e;
+          }
+          *reinterpret_cast<uint4*>(smem + OFF_Q + (row >> 7) * kTileBytes + (c >> 3) * kHalf +
+                                    swz(row & 127, c & 7)) = y;
+        }
       }
-      const float dot = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]);
-      s[i] = i < nv ? dot * ks * a.sm_scale_log2 : -INFINITY;
-      mx = fmaxf(mx, s[i]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.q_ready);
+
+      // ---- the key blocks
+      const int32_t* prow = p.page_table + (long long)s.r * p.max_pages;
+      const int npages = s.L / kP + (s.L % kP != 0);
+      // lane l holds page l % 8 of a block: its id, -1 behind the request's
+      // last page, -2 for an id out of range.  An id is looked at a block after
+      // its load (page_raw), so that no load is waited for here.
+      auto page_in = [&](int b) { return b < s.b_hi && b * kBlkPages + (lane & 7) < npages; };
+      auto page_raw = [&](int b) -> int {
+        return page_in(b) ? prow[b * kBlkPages + (lane & 7)] : 0;
+      };
+      auto page_of = [&](int raw, int b) -> int {
+        return !page_in(b) ? -1 : raw >= 0 && raw < p.d.num_pages ? raw : -2;
+      };
+      auto scales_of = [&](int pg) -> float2 {  // of K and V
+        if (!FP8 || cw != 0 || pg < 0) return make_float2(1.0f, 1.0f);
+        const long long ph = (long long)pg * H + s.h;
+        return make_float2(p.d.k_scale[ph], p.d.v_scale[ph]);
+      };
+      // piece i of this thread: K token 16 i + ct / 8 (page i), 16-byte chunk ct % 8
+      auto load_k = [&](int pgl, int part, uint4 (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int pg = __shfl_sync(0xffffffffu, pgl, FP8 ? i : 4 * part + (i >> 1));
+          const int off = FP8 ? ct * 16 : (i & 1) * 2048 + ct * 16;
+          x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                               kc + ((long long)pg * H + s.h) * kPageBytes + off))
+                         : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto store_k = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (FP8) {
+            const int t = 16 * i + (ct >> 3), j = ct & 7;
+            uint4 lo, hi;
+            e4m3x4_to_f16(x[i].x, lo.x, lo.y);
+            e4m3x4_to_f16(x[i].y, lo.z, lo.w);
+            e4m3x4_to_f16(x[i].z, hi.x, hi.y);
+            e4m3x4_to_f16(x[i].w, hi.z, hi.w);
+            // the two halves' lanes store their chunks in opposite order: no
+            // two of 8 lanes then share a bank group
+            uint8_t* h = dst + (j >> 2) * kHalf;
+            const int c = 2 * (j & 3), odd = j >> 2;
+            *reinterpret_cast<uint4*>(h + swz(t, c + odd)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(h + swz(t, c + 1 - odd)) = odd ? lo : hi;
+          } else {
+            const int t = 64 * part + 8 * i + (ct >> 4), c = ct & 15;
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + swz(t, c & 7)) = x[i];
+          }
+        }
+      };
+      // piece i: e4m3 V dim 32 (i / 2) + ct / 4 of page 4 (i % 2) + ct % 4; bf16 V dim
+      // 16 i + ct / 8, page 4 part + (ct % 8) / 2, tokens 8 (ct % 2) ..
+      auto load_v = [&](int pgl, int part, uint4 (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int pi = FP8 ? 4 * (i & 1) + (ct & 3) : 4 * part + ((ct & 7) >> 1);
+          const int pg = __shfl_sync(0xffffffffu, pgl, pi);
+          const int off = FP8 ? (32 * (i >> 1) + (ct >> 2)) * 16
+                              : (16 * i + (ct >> 3)) * 32 + (ct & 1) * 16;
+          x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                               vc + ((long long)pg * H + s.h) * kPageBytes + off))
+                         : make_uint4(0, 0, 0, 0);
+        }
+      };
+      // valid tokens behind the length are zeroed: their bytes may be NaN, and
+      // 0 * NaN would reach the output
+      auto store_v = [&](uint8_t* dst, int part, int b, uint4 (&x)[8]) {
+        const bool ragged = (b + 1) * kBlk > s.L;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (FP8) {
+            const int d = 32 * (i >> 1) + (ct >> 2), pi = 4 * (i & 1) + (ct & 3);
+            if (ragged) {
+              const int nv = s.L - (b * kBlk + pi * kP);  // valid tokens of the page
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int left = nv - 4 * k;
+                w[k] = left >= 4 ? w[k] : left <= 0 ? 0u : w[k] & ((1u << (8 * left)) - 1u);
+              }
+            }
+            uint4 lo, hi;
+            e4m3x4_to_f16(x[i].x, lo.x, lo.y);
+            e4m3x4_to_f16(x[i].y, lo.z, lo.w);
+            e4m3x4_to_f16(x[i].z, hi.x, hi.y);
+            e4m3x4_to_f16(x[i].w, hi.z, hi.w);
+            uint8_t* h = dst + (i & 1) * kHalf;
+            *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3))) = lo;
+            *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3) + 1)) = hi;
+          } else {
+            const int d = 16 * i + (ct >> 3);
+            if (ragged) {
+              const int nv = s.L - (b * kBlk + (4 * part + ((ct & 7) >> 1)) * kP + (ct & 1) * 8);
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int left = nv - 2 * k;
+                w[k] = left >= 2 ? w[k] : left <= 0 ? 0u : w[k] & 0xFFFFu;
+              }
+            }
+            *reinterpret_cast<uint4*>(dst + part * kHalf + swz(d, ct & 7)) = x[i];
+          }
+        }
+      };
+      // pages two blocks ahead are pulled into L2 (lanes 0-7 K, 8-15 V, of one warp)
+      auto prefetch = [&](int pgl) {
+        if (cw != 3) return;
+        const int pg = __shfl_sync(0xffffffffu, pgl, lane & 7);
+        if (lane < 16 && pg >= 0)
+          prefetch_l2((lane < 8 ? kc : vc) + ((long long)pg * H + s.h) * kPageBytes,
+                      (uint32_t)kPageBytes);
+      };
+      const int raw0 = page_raw(s.b_lo), raw1 = page_raw(s.b_lo + 1);
+      int raw2 = page_raw(s.b_lo + 2);
+      int pg0 = page_of(raw0, s.b_lo), pg1 = page_of(raw1, s.b_lo + 1);
+      prefetch(pg0);
+      prefetch(pg1);
+      float2 sc0 = scales_of(pg0);
+      uint4 x0[8], x1[8];
+      load_k(pg0, 0, x0);
+      for (int b = s.b_lo; b < s.b_hi; ++b, ++u) {
+        const int st = (int)(u & 1), ms = (int)(u & (kMeta - 1));
+        const uint32_t free_phase = (uint32_t)((u >> 1) - 1);
+        const int pg2 = page_of(raw2, b + 2);
+        prefetch(pg2);
+        raw2 = page_raw(b + 3);
+        const float2 sc1 = scales_of(pg1);
+        // K
+        if (u >= 2 && !wait(&bar.k_free[st], free_phase, 32 + st)) break;
+        uint8_t* kd = smem + OFF_K + st * kTileBytes;
+        if (kParts == 2) {
+          load_k(pg0, 1, x1);
+          store_k(kd, 0, x0);
+          load_v(pg0, 0, x0);
+          store_k(kd, 1, x1);
+        } else {
+          load_v(pg0, 0, x1);
+          store_k(kd, 0, x0);
+        }
+        if (cw == 0 && lane < kBlkPages) {
+          if (pg0 == -2) set_error(ctl, KV_ERR_BAD_PAGE_ID);
+          const float bias = __log2f(sc0.y);
+          meta[ms * kBlkPages + lane] =
+              make_float4(sc0.x, bias, ex2(-bias), pg0 == -2 ? 1.0f : 0.0f);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.k_ready[st]);
+          mbar_arrive(&bar.meta_ready[ms]);
+        }
+        // V
+        if (u >= 2 && !wait(&bar.v_free[st], free_phase, 34 + st)) break;
+        uint8_t* vd = smem + OFF_V + st * kTileBytes;
+        if (kParts == 2) {
+          load_v(pg0, 1, x1);
+          store_v(vd, 0, b, x0);
+          if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
+          store_v(vd, 1, b, x1);
+        } else {
+          if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
+          store_v(vd, 0, b, x1);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_ready[st]);
+        pg0 = pg1;
+        pg1 = pg2;
+        sc0 = sc1;
+      }
     }
-    const float Mn = fmaxf(M, mx), al = exp2f(M - Mn);
-    l *= al;
+  } else if (warp == kMmaWarp) {
+    // ============================ MMA issuer ============================
+    // Task (block u, tile X): S = Q_X K^T.  Just before it, the PV that X still
+    // owes (its task before) is issued, so that one tile's softmax always runs
+    // beside the other tile's products.  A PV is never more than one block late,
+    // so that the V ring moves on.
+    const uint32_t leader = elect_one();
+    constexpr uint32_t kId = idesc(!FP8);
+    const uint64_t dq = sw128_desc(smem_u32(smem + OFF_Q), 16, 1024);
+    const uint64_t dk = sw128_desc(smem_u32(smem + OFF_K), 16, 1024);
+    const uint64_t dv = sw128_desc(smem_u32(smem + OFF_V), 16, 1024);
+    struct Owed {
+      long long u;
+      bool any, first, last, frees;  // of its tile in the piece; the block's last PV
+    } owed[2];
+    owed[0].any = owed[1].any = false;
+    uint32_t n_task[2] = {0, 0}, n_first[2] = {0, 0};  // tasks / pieces of each tile
+    bool go = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
+      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
+                                                   wait_info(warp, 0, info)));
+      return go;
+    };
+    auto pv = [&](int x) {
+      Owed& o = owed[x];
+      if (!o.any) return;
+      o.any = false;
+      const int st = (int)(o.u & 1);
+      if (!wait(&bar.p_ready[x], n_task[x] - 1, 40 + x)) return;
+      if (!wait(&bar.v_ready[st], (uint32_t)(o.u >> 1), 42 + st)) return;
+      if (o.first && n_first[x] > 1 && !wait(&bar.epi_done[x], n_first[x] - 2, 44 + x)) return;
+      tc_fence_after();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= al;
-    M = Mn;
+      for (int k = 0; k < kBlk / 16; ++k)
+        mma_f16_ts_if(leader, tmem + tmem_o(x), tmem + tmem_s(x) + 8 * k,
+                      dv + ((uint32_t)(st * kTileBytes + (k >> 2) * kHalf + (k & 3) * 32) >> 4), kId,
+                      !(o.first && k == 0));
+      if (leader) {
+        if (o.frees) mma_commit(&bar.v_free[st]);
+        if (o.last) mma_commit(&bar.o_full[x]);
+      }
+      __syncwarp();
+    };
+    long long u = 0;
+    uint32_t piece = 0;
+    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
+      if (!wait(bar.q_ready, piece, 46)) break;
+      const bool both = s.both();
+      const int cnt = s.count();
+      for (int i = 0; i < cnt && go; ++i, ++u) {
+        const int st = (int)(u & 1);
+        // what is owed from two blocks back or more
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      if (i >= nv) continue;
-      const float pr = exp2f(s[i] - M);
-      l += pr;
+        for (int x = 0; x < 2; ++x)
+          if (owed[x].any && owed[x].u + 1 < u) pv(x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const long long at = (ph * kD + 4 * lane + e) * kP + i;
-        const float v = FP8 ? __half2float(__half(__nv_cvt_fp8_to_halfraw(
-                                  static_cast<const uint8_t*>(a.d.v_cache)[at], __NV_E4M3))) * vs
-                            : bf16_bits_to_f32(static_cast<const uint16_t*>(a.d.v_cache)[at]);
-        o[e] += pr * v;
+        for (int x = 0; x < 2; ++x) {
+          if (!both && x != (i & 1)) continue;
+          pv(x);
+          if (!go || !wait(&bar.k_ready[st], (uint32_t)(u >> 1), 48 + st)) break;
+          tc_fence_after();
+          const int qt = both ? x : 0;
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
+            mma_f16_if(leader, tmem + tmem_s(x), dq + ((qt * kTileBytes + off) >> 4),
+                       dk + ((st * kTileBytes + off) >> 4), kId, k > 0);
+          }
+          const bool block_done = !both || x == 1;
+          if (leader) {
+            mma_commit(&bar.s_full[x]);
+            if (block_done) mma_commit(&bar.k_free[st]);
+            if (block_done && i == cnt - 1) mma_commit(bar.q_free);
+          }
+          __syncwarp();
+          Owed& o = owed[x];
+          o.any = true;
+          o.u = u;
+          o.first = both ? i == 0 : i < 2;
+          o.last = both ? i == cnt - 1 : i + 2 >= cnt;
+          o.frees = block_done;
+          ++n_task[x];
+          if (o.first) ++n_first[x];
+        }
+      }
+    }
+    if (go) {
+      const int x = owed[0].any && (!owed[1].any || owed[0].u <= owed[1].u) ? 0 : 1;
+      pv(x);
+      pv(1 - x);
+    }
+    // every operation issued here finishes (bounded) before tensor memory is freed
+    if (leader) {
+      mma_commit(bar.drain);
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(bar.drain, 0) && global_ns() - t0 < 100000000ull) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ============================== softmax ==============================
+    // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
+    // exponent and the reference maximum M follows max(score + bias), so that P <= 2^8
+    // whatever the scales; the row sum takes the bias back out.
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + tmem_s(x) + lanes, to = tmem + tmem_o(x) + lanes;
+    const float ssl = fabsf(p.sm_scale_log2);
+    long long u = 0;
+    uint32_t n_task = 0, n_o = 0, n_two = 0, n_b = 0;  // waits so far; pieces with blocks of B
+    int piece = 0;
+    bool go = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
+      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
+                                                   wait_info(warp, 0, info)));
+      return go;
+    };
+    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
+      const bool both = s.both();
+      const int cnt = s.count();
+      const int rr = both ? x * kTile + row : row;  // row of the item
+      const bool live = rr < s.nrows;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int t = (s.row0 + min(rr, s.nrows - 1)) / p.G;
+      const int lim = s.L - s.n + t;  // last visible position
+      // every row of the tile sees a block that ends at or before this position
+      const int lim_all = s.L - s.n + (s.row0 + (both ? x * kTile : 0)) / p.G;
+      float qsc = ssl, M = -INFINITY, l = 0.0f, bad = 0.0f;
+      bool first = true;
+      for (int i = 0; i < cnt && go; ++i, ++u) {
+        if (!both && (i & 1) != x) continue;
+        const int ms = (int)(u & (kMeta - 1));
+        if (!wait(&bar.s_full[x], n_task, 52 + x)) break;
+        if (!wait(&bar.meta_ready[ms], (uint32_t)(u / kMeta), 54)) break;
+        ++n_task;
+        tc_fence_after();
+        if (FP8 && first) qsc = ssl * pow2f(-qexp[(piece & (kMeta - 1)) * kItemRows + rr]);
+        const float4* mt = meta + ms * kBlkPages;
+        if (warp_live) {
+          const int pos0 = (s.b_lo + i) * kBlk;
+          const bool masked = pos0 + kBlk - 1 > lim_all;
+          const int thr = lim - pos0;  // columns <= thr are visible
+          // pass 1: the maximum
+          float mx = -INFINITY;
+          bool wide = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(ts + 32 * c, v);
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = 32 * c + k <= thr ? v[k] : -INFINITY;
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float pm = v[16 * g];
+#pragma unroll
+              for (int k = 1; k < 15; k += 2) pm = fmaxf(fmaxf(pm, v[16 * g + k]), v[16 * g + k + 1]);
+              pm = fmaxf(pm, v[16 * g + 15]);
+              const float4 m = mt[2 * c + g];
+              if (FP8) {
+                bad += m.w;
+                wide = wide || fabsf(m.y) > 48.0f;
+                mx = fmaxf(mx, pm == -INFINITY ? pm : pm * (m.x * qsc) + m.y);
+              } else {
+                bad += m.w;
+                mx = fmaxf(mx, pm == -INFINITY ? pm : pm * qsc);
+              }
+            }
+          }
+          float alpha = 1.0f;
+          if (mx > M + 8.0f) {
+            alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
+            l *= alpha;
+            M = mx;
+          }
+          if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            // PV of the block before was issued ahead of this S: it is complete
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(to + 32 * c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+          const float ref = M == -INFINITY ? 0.0f : M;
+          // where V scales lie far apart, P of a page with a small one can fall
+          // below fp32's range while its weight counts: such a block's sum is
+          // taken of the weights themselves (wide is the same in every lane)
+          if (FP8 && wide) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tmem_ld32(ts + 32 * c, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (32 * c + k <= thr) l += ex2(__fmaf_rn(v[k], mt[2 * c + k / 16].x * qsc, -ref));
+            }
+          }
+          // pass 2: P and its sum
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(ts + 32 * c, v);
+            uint32_t pk[16];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float4 m = mt[2 * c + g];
+              const float ks = FP8 ? m.x * qsc : qsc, add = FP8 ? m.y - ref : -ref;
+              const uint64_t k2 = pack2(ks, ks), a2 = pack2(add, add);
+              uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                float e0, e1;
+                unpack2(fma2(pack2(v[16 * g + k], v[16 * g + k + 1]), k2, a2), e0, e1);
+                if (masked) {
+                  e0 = 32 * c + 16 * g + k <= thr ? e0 : -INFINITY;
+                  e1 = 32 * c + 16 * g + k + 1 <= thr ? e1 : -INFINITY;
+                }
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum = add2(sum, pack2(e0, e1));
+                pk[8 * g + k / 2] = pack_p<FP8>(e0, e1);
+              }
+              float s0, s1;
+              unpack2(sum, s0, s1);
+              l = !FP8 ? l + (s0 + s1) : wide ? l : __fmaf_rn(s0 + s1, m.z, l);
+            }
+            tmem_st16u(ts + 16 * c, pk);
+          }
+          tmem_wait_st();
+        }
+        first = false;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_ready[x]);
+      }
+      if (!go) break;
+      // ---- the piece's output
+      const bool used = both || cnt > x;     // this tile had a block
+      const bool two = !both && cnt > 1;     // A and B hold parts of the same rows
+      if (used && !wait(&bar.o_full[x], n_o++, 56 + x)) break;
+      tc_fence_after();
+      if (!both && x == 1) {  // B's part goes to A's warps
+        if (two) {
+          ml_b[row] = make_float2(M, bad != 0.0f ? -1.0f : l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.b_ml);
+        }
+        continue;
+      }
+      float wa = 1.0f, wb = 0.0f;
+      if (two) {
+        if (!wait(bar.b_ml, n_two++, 58)) break;
+        if (!wait(&bar.o_full[1], n_b, 59)) break;
+        tc_fence_after();
+        const float2 b = ml_b[row];
+        if (b.y < 0.0f) bad = 1.0f;
+        const float Mn = fmaxf(M, b.x);
+        wa = M == -INFINITY ? 0.0f : ex2(M - Mn);
+        wb = b.x == -INFINITY ? 0.0f : ex2(b.x - Mn);
+        l = l * wa + b.y * wb;
+        M = Mn;
+      }
+      if (both || two) ++n_b;
+      const bool whole = s.b_lo == 0 && s.b_hi == s.nb;
+      const float scale = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      const int slot = 2 * (int)blockIdx.x + (s.b_lo > 0 ? 0 : 1);
+      if (warp_live) {
+        const int g = s.row0 + rr - t * p.G;
+        uint16_t* out = p.out + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(to + 32 * c, o);
+          if (two) {
+            float ob[32];
+            tmem_ld32(tmem + tmem_o(1) + lanes + 32 * c, ob);
+#pragma unroll
+            // (a part that saw nothing holds zeros times whatever: leave it out)
+            for (int k = 0; k < 32; ++k)
+              o[k] = (wa != 0.0f ? o[k] * wa : 0.0f) + (wb != 0.0f ? ob[k] * wb : 0.0f);
+          }
+          if (live && whole && bad == 0.0f) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint4 y;
+              y.x = pack_p<false>(o[k] * scale, o[k + 1] * scale);
+              y.y = pack_p<false>(o[k + 2] * scale, o[k + 3] * scale);
+              y.z = pack_p<false>(o[k + 4] * scale, o[k + 5] * scale);
+              y.w = pack_p<false>(o[k + 6] * scale, o[k + 7] * scale);
+              *reinterpret_cast<uint4*>(out + 32 * c + k) = l > 0.0f ? y : make_uint4(0, 0, 0, 0);
+            }
+          } else if (live && !whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              a.ws.o[((long long)slot * 32 + 8 * c + k / 4) * kItemRows + rr] =
+                  make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+          __syncwarp();  // the next tensor-memory load is the whole warp's
+        }
+        if (live && !whole)
+          a.ws.ml[(long long)slot * kItemRows + rr] = make_float2(M, bad != 0.0f ? -1.0f : l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.epi_done[x]);
+        if (two) mbar_arrive(&bar.epi_done[1]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  if (threadIdx.x == 0) {
+    // the item that begins in this range and is cut by its end
+    int4 cut = make_int4(-1, 0, 0, 0);
+    Piece c;
+    for (bool m = piece_first(c, a, *first_item, x_begin, x_end); m;
+         m = piece_next(c, a, x_begin, x_end))
+      if (c.b_lo == 0 && c.b_hi < c.nb)
+        cut = make_int4(c.v, c.h, (int)((c.x0 + (long long)c.w() * (c.nb - 1)) / per), 0);
+    a.ws.cut[blockIdx.x] = cut;
+  }
+}
+
+// Cut items: the partials of the CTAs from the one that begins the item to the
+// one that ends it, merged for 32 rows.
+__global__ void __launch_bounds__(256) prefill_combine_kernel(const Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x;
+  const int4 cut = a.ws.cut[c0];
+  if (cut.x < 0) return;
+  const PrefillArgs& p = a.p;
+  const int4 it = a.ws.items[cut.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rr = blockIdx.y * 32 + lane;
+  if (blockIdx.y * 32 >= it.z) return;
+  __shared__ uint2 tile[32][33];
+  __shared__ int skip[32];
+  const bool live = rr < it.z;
+  float M = -INFINITY, l = 0.0f;
+  bool bad = false;
+  auto slot_of = [&](int c) { return 2LL * c + (c == c0 ? 1 : 0); };
+  if (live) {
+    for (int c = c0; c <= cut.z; ++c) {
+      const float2 ml = a.ws.ml[slot_of(c) * kItemRows + rr];
+      bad = bad || ml.y < 0.0f;
+      M = fmaxf(M, ml.x);
+    }
+  }
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0, 0, 0, 0);
+  if (live && M != -INFINITY) {
+    for (int c = c0; c <= cut.z; ++c) {
+      const float2 ml = a.ws.ml[slot_of(c) * kItemRows + rr];
+      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      if (w == 0.0f) continue;  // (saw nothing, or nothing that counts)
+      l = __fmaf_rn(ml.y, w, l);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 o = a.ws.o[(slot_of(c) * 32 + warp + 8 * k) * kItemRows + rr];
+        acc[k].x = __fmaf_rn(o.x, w, acc[k].x);
+        acc[k].y = __fmaf_rn(o.y, w, acc[k].y);
+        acc[k].z = __fmaf_rn(o.z, w, acc[k].z);
+        acc[k].w = __fmaf_rn(o.w, w, acc[k].w);
       }
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const __nv_bfloat162 b0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
-  const __nv_bfloat162 b1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-  *reinterpret_cast<uint2*>(a.out + item * kD + 4 * lane) = make_uint2(
-      *reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    tile[lane][warp + 8 * k] = make_uint2(pack_p<false>(acc[k].x * inv, acc[k].y * inv),
+                                          pack_p<false>(acc[k].z * inv, acc[k].w * inv));
+  if (warp == 0) skip[lane] = !live || bad;
+  __syncthreads();
+  const int q0 = p.q_indptr[it.x];
+  for (int i = warp; i < 32; i += 8) {
+    if (skip[i]) continue;
+    const int tg = it.y + blockIdx.y * 32 + i, t = tg / p.G, g = tg - t * p.G;
+    *reinterpret_cast<uint2*>(p.out + ((long long)(q0 + t) * p.Hq + cut.y * p.G + g) * kD +
+                              4 * lane) = tile[i][lane];
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
 }
 
 }  // namespace
 
 size_t prefill_ws_bytes(const kv_pool_desc& d, int B, int Hq, int total_q) {
-  (void)d, (void)B, (void)Hq, (void)total_q;
-  return 256;
+  const int sms = sm_count();
+  return sms > 0 ? ws_layout(nullptr, B, Hq / d.num_kv_heads, total_q, sms).bytes : 0;
 }
 
-cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s, int* launches) {
-  const long long items = (long long)a.total_q * a.Hq;
-  const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
-  const cudaError_t e =
-      a.d.dtype == KV_DTYPE_E4M3
-          ? launch_pdl(prefill_simple_kernel<true>, dim3(grid), dim3(kThreads), 0, s, a)
-          : launch_pdl(prefill_simple_kernel<false>, dim3(grid), dim3(kThreads), 0, s, a);
+cudaError_t launch_prefill(const PrefillArgs& p, cudaStream_t s, int* launches) {
+  Args a;
+  a.p = p;
+  a.grid = sm_count();
+  if (a.grid <= 0) return cudaErrorInvalidDevice;
+  a.ws = ws_layout(p.workspace, p.B, p.G, p.total_q, a.grid);
+  a.V = (int)item_count(p.B, p.G, p.total_q);
+  const bool fp8 = p.d.dtype == KV_DTYPE_E4M3;
+  cudaError_t e = fp8 ? cudaFuncSetAttribute(prefill_kernel<true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)
+                      : cudaFuncSetAttribute(prefill_kernel<false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = fp8 ? launch_pdl(prefill_kernel<true>, dim3(a.grid), dim3(kThreads), kSmem, s, a)
+          : launch_pdl(prefill_kernel<false>, dim3(a.grid), dim3(kThreads), kSmem, s, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = launch_pdl(prefill_combine_kernel, dim3(a.grid, kItemRows / 32), dim3(256), 0, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
