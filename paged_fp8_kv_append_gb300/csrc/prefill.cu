@@ -46,7 +46,13 @@ constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
 constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = (kMmaWarp + 4) * 32;
+// registers a thread of each warpgroup: together the 4 x 128 of the launch
+constexpr int kSoftRegs = 168, kConvRegs = 120, kMmaRegs = 56;
+static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs == 512, "register split");
+// what an item costs beside its blocks (staging the queries, writing the output),
+// in halves of a two-tile block
+constexpr int kItemCost = 4;
 constexpr int kMeta = 4;  // block records in flight, and query exponents of as many pieces
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
@@ -72,6 +78,16 @@ __device__ __forceinline__ uint32_t tmem_o(int x) { return 256u + 128u * x; }
 constexpr uint32_t idesc(bool bf16) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((128u >> 3) << 17) |
          ((128u >> 4) << 24);
+}
+
+// register split of the warpgroups
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ------------------------------------------------------------------ plan
@@ -151,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
           it.z = (int)min((long long)kItemRows, n * p.G - row0);
           const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
           it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = (long long)it.w * (it.z > kTile ? 2 : 1);
+          cost = kItemCost + (long long)it.w * (it.z > kTile ? 2 : 1);
         }
       }
       a.ws.items[v] = it;
@@ -190,14 +206,15 @@ struct Piece {
   int r, row0, nrows, nb;
   int b_lo, b_hi;
   int L, n, q0;
-  long long x0;  // cost position of its block 0
+  long long x0;  // cost position of the item; its blocks begin kItemCost behind
   __device__ __forceinline__ int w() const { return nrows > kTile ? 2 : 1; }
+  __device__ __forceinline__ long long cost() const { return kItemCost + (long long)nb * w(); }
   __device__ __forceinline__ bool both() const { return nrows > kTile; }
   __device__ __forceinline__ int count() const { return b_hi - b_lo; }
 };
 
 __device__ __forceinline__ int block_at(long long x, const Piece& s) {  // first block at or behind x
-  const long long d = x - s.x0;
+  const long long d = x - s.x0 - kItemCost;
   return d <= 0 ? 0 : (int)min((long long)s.nb, (d + s.w() - 1) / s.w());
 }
 
@@ -207,7 +224,7 @@ __device__ void piece_load(Piece& s, const Args& a, long long x_begin, long long
   s.row0 = it.y;
   s.nrows = it.z;
   s.nb = it.w;
-  s.x0 = a.ws.pfx[s.v] * a.p.d.num_kv_heads + (long long)s.h * s.nb * s.w();
+  s.x0 = a.ws.pfx[s.v] * a.p.d.num_kv_heads + (long long)s.h * s.cost();
   s.b_lo = block_at(x_begin, s);
   s.b_hi = block_at(x_end, s);
   s.L = a.p.seq_lens[s.r];
@@ -218,7 +235,7 @@ __device__ void piece_load(Piece& s, const Args& a, long long x_begin, long long
 // The next piece with a block; false behind the range.
 __device__ bool piece_next(Piece& s, const Args& a, long long x_begin, long long x_end) {
   for (;;) {
-    if (s.x0 + (long long)s.nb * s.w() >= x_end) return false;
+    if (s.x0 + s.cost() >= x_end) return false;
     if (++s.h == a.p.d.num_kv_heads) {
       s.h = 0;
       do {
@@ -235,8 +252,7 @@ __device__ bool piece_first(Piece& s, const Args& a, int v, long long x_begin, l
   s.v = v;
   s.h = 0;
   piece_load(s, a, x_begin, x_end);
-  const long long per_head = (long long)s.nb * s.w();
-  s.h = (int)((x_begin - s.x0) / per_head);
+  s.h = (int)((x_begin - s.x0) / s.cost());
   piece_load(s, a, x_begin, x_end);
   return s.b_lo < s.b_hi || piece_next(s, a, x_begin, x_end);
 }
@@ -276,6 +292,43 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+#define KVFP8_R32(op, r)                                                                        \
+  op(r[0]), op(r[1]), op(r[2]), op(r[3]), op(r[4]), op(r[5]), op(r[6]), op(r[7]), op(r[8]),     \
+      op(r[9]), op(r[10]), op(r[11]), op(r[12]), op(r[13]), op(r[14]), op(r[15]), op(r[16]),    \
+      op(r[17]), op(r[18]), op(r[19]), op(r[20]), op(r[21]), op(r[22]), op(r[23]), op(r[24]),   \
+      op(r[25]), op(r[26]), op(r[27]), op(r[28]), op(r[29]), op(r[30]), op(r[31])
+// 32 columns, not waited for
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KVFP8_R32("=f", r)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// (behind the wait: the values are not read before it)
+__device__ __forceinline__ void tmem_landed(float (&r)[32]) {
+  asm volatile("" : KVFP8_R32("+f", r));
+}
+#undef KVFP8_R32
+// 16 columns times f, in place
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
+  float r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+  uint32_t w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(r[k] * f);
+  tmem_st16u(taddr, w);
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -318,10 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   // at least 2, so that every range holds a block's start
   const long long per = max(2LL, (total + a.grid - 1) / a.grid);
   const long long x_begin = (long long)blockIdx.x * per, x_end = min(total, x_begin + per);
-  if (x_begin >= x_end) {
-    if (threadIdx.x == 0) a.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
+  if (threadIdx.x == 0) a.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (x_begin >= x_end) return;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -365,9 +416,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   int32_t* ctl = p.d.ctl;
   Piece s;
   bool more = piece_first(s, a, *first_item, x_begin, x_end);
+  // the item that begins here and is cut by the range's end: for the combine
+  auto note_cut = [&]() {
+    if (s.b_lo == 0 && s.b_hi < s.nb)
+      a.ws.cut[blockIdx.x] = make_int4(
+          s.v, s.h, (int)((s.x0 + kItemCost + (long long)s.w() * (s.nb - 1)) / per), 0);
+  };
 
   if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ============================ converters ============================
+    regs_dec<kConvRegs>();
     const int cw = warp - kSoftWarps, ct = threadIdx.x - kSoftWarps * 32;
     const bool flip = p.sm_scale_log2 < 0.0f;  // a negative scale turns the queries' sign
     constexpr int kEs = FP8 ? 1 : 2;
@@ -387,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // ---- the item's query rows (16 lanes a row)
       if (piece > 0 && !wait(bar.q_free, (uint32_t)(piece - 1), 60)) break;
       const int tiles = s.both() ? 2 : 1;
+#pragma unroll 1
       for (int i0 = 0; i0 < 16 * tiles; i0 += 8) {
         uint4 x[8];
 #pragma unroll
@@ -447,15 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         const long long ph = (long long)pg * H + s.h;
         return make_float2(p.d.k_scale[ph], p.d.v_scale[ph]);
       };
+      // A page that is not there (behind the length, or an id out of range) is read as
+      // page 0: its scores are masked or its item is not written, and its V is
+      // zeroed with what lies behind the length.
+      const uint8_t *kh = kc + s.h * kPageBytes, *vh = vc + s.h * kPageBytes;
+      const long long page_step = (long long)H * kPageBytes;
       // piece i of this thread: K token 16 i + ct / 8 (page i), 16-byte chunk ct % 8
       auto load_k = [&](int pgl, int part, uint4 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int pg = __shfl_sync(0xffffffffu, pgl, FP8 ? i : 4 * part + (i >> 1));
+          const long long pg = __shfl_sync(0xffffffffu, max(pgl, 0), FP8 ? i : 4 * part + (i >> 1));
           const int off = FP8 ? ct * 16 : (i & 1) * 2048 + ct * 16;
-          x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                               kc + ((long long)pg * H + s.h) * kPageBytes + off))
-                         : make_uint4(0, 0, 0, 0);
+          x[i] = __ldg(reinterpret_cast<const uint4*>(kh + pg * page_step + off));
         }
       };
       auto store_k = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
@@ -486,31 +548,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int pi = FP8 ? 4 * (i & 1) + (ct & 3) : 4 * part + ((ct & 7) >> 1);
-          const int pg = __shfl_sync(0xffffffffu, pgl, pi);
+          const long long pg = __shfl_sync(0xffffffffu, max(pgl, 0), pi);
           const int off = FP8 ? (32 * (i >> 1) + (ct >> 2)) * 16
                               : (16 * i + (ct >> 3)) * 32 + (ct & 1) * 16;
-          x[i] = pg >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                               vc + ((long long)pg * H + s.h) * kPageBytes + off))
-                         : make_uint4(0, 0, 0, 0);
+          x[i] = __ldg(reinterpret_cast<const uint4*>(vh + pg * page_step + off));
         }
       };
-      // valid tokens behind the length are zeroed: their bytes may be NaN, and
+      // tokens behind the length are zeroed: their bytes may be NaN, and
       // 0 * NaN would reach the output
-      auto store_v = [&](uint8_t* dst, int part, int b, uint4 (&x)[8]) {
-        const bool ragged = (b + 1) * kBlk > s.L;
+      auto clean_v = [&](int part, int b, uint4 (&x)[8]) {
+        if ((b + 1) * kBlk <= s.L) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = FP8 ? (4 * (i & 1) + (ct & 3)) * kP
+                             : (4 * part + ((ct & 7) >> 1)) * kP + (ct & 1) * 8;
+          const int nv = s.L - (b * kBlk + at);  // valid tokens from the piece's first on
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int bytes = FP8 ? nv - 4 * k : 2 * (nv - 2 * k);
+            w[k] = bytes >= 4 ? w[k] : bytes <= 0 ? 0u : w[k] & ((1u << (8 * bytes)) - 1u);
+          }
+        }
+      };
+      auto store_v = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
-            const int d = 32 * (i >> 1) + (ct >> 2), pi = 4 * (i & 1) + (ct & 3);
-            if (ragged) {
-              const int nv = s.L - (b * kBlk + pi * kP);  // valid tokens of the page
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int left = nv - 4 * k;
-                w[k] = left >= 4 ? w[k] : left <= 0 ? 0u : w[k] & ((1u << (8 * left)) - 1u);
-              }
-            }
+            const int d = 32 * (i >> 1) + (ct >> 2);
             uint4 lo, hi;
             e4m3x4_to_f16(x[i].x, lo.x, lo.y);
             e4m3x4_to_f16(x[i].y, lo.z, lo.w);
@@ -520,17 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3))) = lo;
             *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3) + 1)) = hi;
           } else {
-            const int d = 16 * i + (ct >> 3);
-            if (ragged) {
-              const int nv = s.L - (b * kBlk + (4 * part + ((ct & 7) >> 1)) * kP + (ct & 1) * 8);
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int left = nv - 2 * k;
-                w[k] = left >= 2 ? w[k] : left <= 0 ? 0u : w[k] & 0xFFFFu;
-              }
-            }
-            *reinterpret_cast<uint4*>(dst + part * kHalf + swz(d, ct & 7)) = x[i];
+            *reinterpret_cast<uint4*>(dst + part * kHalf + swz(16 * i + (ct >> 3), ct & 7)) = x[i];
           }
         }
       };
@@ -586,12 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         uint8_t* vd = smem + OFF_V + st * kTileBytes;
         if (kParts == 2) {
           load_v(pg0, 1, x1);
-          store_v(vd, 0, b, x0);
+          clean_v(0, b, x0);
+          store_v(vd, 0, x0);
           if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          store_v(vd, 1, b, x1);
+          clean_v(1, b, x1);
+          store_v(vd, 1, x1);
         } else {
           if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          store_v(vd, 0, b, x1);
+          clean_v(0, b, x1);
+          store_v(vd, 0, x1);
         }
         fence_async_smem();
         __syncwarp();
@@ -601,7 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         sc0 = sc1;
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
+   regs_dec<kMmaRegs>();
+   if (warp == kMmaWarp) {
     // ============================ MMA issuer ============================
     // Task (block u, tile X): S = Q_X K^T.  Just before it, the PV that X still
     // owes (its task before) is issued, so that one tile's softmax always runs
@@ -612,85 +672,94 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     const uint64_t dq = sw128_desc(smem_u32(smem + OFF_Q), 16, 1024);
     const uint64_t dk = sw128_desc(smem_u32(smem + OFF_K), 16, 1024);
     const uint64_t dv = sw128_desc(smem_u32(smem + OFF_V), 16, 1024);
-    struct Owed {
-      long long u;
-      bool any, first, last, frees;  // of its tile in the piece; the block's last PV
-    } owed[2];
-    owed[0].any = owed[1].any = false;
-    uint32_t n_task[2] = {0, 0}, n_first[2] = {0, 0};  // tasks / pieces of each tile
+    // what each tile owes: its block, and whether that is its first or last of the
+    // piece and whether its PV is the block's last
+    enum { kFirst = 1, kLast = 2, kFrees = 4 };
+    long long owed0 = -1, owed1 = -1;
+    int how0 = 0, how1 = 0;
+    uint32_t task0 = 0, task1 = 0, begun0 = 0, begun1 = 0;  // tasks / pieces of each tile
     bool go = true;
     auto wait = [&](uint64_t* b, uint32_t parity, int info) {
       go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
                                                    wait_info(warp, 0, info)));
       return go;
     };
-    auto pv = [&](int x) {
-      Owed& o = owed[x];
-      if (!o.any) return;
-      o.any = false;
-      const int st = (int)(o.u & 1);
-      if (!wait(&bar.p_ready[x], n_task[x] - 1, 40 + x)) return;
-      if (!wait(&bar.v_ready[st], (uint32_t)(o.u >> 1), 42 + st)) return;
-      if (o.first && n_first[x] > 1 && !wait(&bar.epi_done[x], n_first[x] - 2, 44 + x)) return;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < kBlk / 16; ++k)
-        mma_f16_ts_if(leader, tmem + tmem_o(x), tmem + tmem_s(x) + 8 * k,
-                      dv + ((uint32_t)(st * kTileBytes + (k >> 2) * kHalf + (k & 3) * 32) >> 4), kId,
-                      !(o.first && k == 0));
-      if (leader) {
-        if (o.frees) mma_commit(&bar.v_free[st]);
-        if (o.last) mma_commit(&bar.o_full[x]);
-      }
-      __syncwarp();
-    };
     long long u = 0;
     uint32_t piece = 0;
-    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
-      if (!wait(bar.q_ready, piece, 46)) break;
-      const bool both = s.both();
-      const int cnt = s.count();
-      for (int i = 0; i < cnt && go; ++i, ++u) {
-        const int st = (int)(u & 1);
-        // what is owed from two blocks back or more
+    int i = 0, x = 0;  // the next task: block i of the piece, tile x
+    while (go) {
+      // the next step: a PV from two blocks back, the task's PV and S, or, behind the
+      // last task, what is still owed (the older first, tile A before B)
+      const bool late0 = owed0 >= 0 && (!more || owed0 + 1 < u);
+      const bool late1 = owed1 >= 0 && (!more || owed1 + 1 < u);
+      if (!more && !late0 && !late1) break;
+      const bool late = late0 || late1;
+      const int xs = !late ? x : late0 && (!late1 || owed0 <= owed1) ? 0 : 1;
+      const long long uo = xs ? owed1 : owed0;
+      const int how = xs ? how1 : how0;
+      const uint32_t task = xs ? task1 : task0, begun = xs ? begun1 : begun0;
+      if (uo >= 0) {  // ---- O += P V
+        const int st = (int)(uo & 1);
+        if (!wait(&bar.p_ready[xs], task - 1, 40 + xs)) break;
+        if (!wait(&bar.v_ready[st], (uint32_t)(uo >> 1), 42 + st)) break;
+        if ((how & kFirst) && begun > 1 && !wait(&bar.epi_done[xs], begun - 2, 44 + xs)) break;
+        tc_fence_after();
+        const uint32_t o = tmem + tmem_o(xs), pa = tmem + tmem_s(xs);
+        const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (owed[x].any && owed[x].u + 1 < u) pv(x);
+        for (int k = 0; k < kBlk / 16; ++k)
+          mma_f16_ts_if(leader, o, pa + 8 * k, d + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kId,
+                        !((how & kFirst) && k == 0));
+        if (leader) {
+          if (how & kFrees) mma_commit(&bar.v_free[st]);
+          if (how & kLast) mma_commit(&bar.o_full[xs]);
+        }
+        __syncwarp();
+        if (xs) owed1 = -1; else owed0 = -1;
+      }
+      if (late) continue;
+      {  // ---- S = Q K^T
+        const bool both = s.both();
+        const int cnt = s.count(), st = (int)(u & 1);
+        if (i == 0 && x == 0 && !wait(bar.q_ready, piece, 46)) break;
+        if (!wait(&bar.k_ready[st], (uint32_t)(u >> 1), 48 + st)) break;
+        tc_fence_after();
+        const uint32_t so = tmem + tmem_s(x);
+        const uint64_t q = dq + ((uint32_t)(both ? x * kTileBytes : 0) >> 4);
+        const uint64_t kk = dk + ((uint32_t)(st * kTileBytes) >> 4);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!both && x != (i & 1)) continue;
-          pv(x);
-          if (!go || !wait(&bar.k_ready[st], (uint32_t)(u >> 1), 48 + st)) break;
-          tc_fence_after();
-          const int qt = both ? x : 0;
-#pragma unroll
-          for (int k = 0; k < kD / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
-            mma_f16_if(leader, tmem + tmem_s(x), dq + ((qt * kTileBytes + off) >> 4),
-                       dk + ((st * kTileBytes + off) >> 4), kId, k > 0);
+        for (int k = 0; k < kD / 16; ++k) {
+          const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          mma_f16_if(leader, so, q + off, kk + off, kId, k > 0);
+        }
+        const bool frees = !both || x == 1, ends = frees && i == cnt - 1;
+        if (leader) {
+          mma_commit(&bar.s_full[x]);
+          if (frees) mma_commit(&bar.k_free[st]);
+          if (ends) mma_commit(bar.q_free);
+        }
+        __syncwarp();
+        const bool first = both ? i == 0 : i < 2, last = both ? i == cnt - 1 : i + 2 >= cnt;
+        const int h = (first ? kFirst : 0) | (last ? kLast : 0) | (frees ? kFrees : 0);
+        if (x) {
+          owed1 = u, how1 = h, ++task1;
+          if (first) ++begun1;
+        } else {
+          owed0 = u, how0 = h, ++task0;
+          if (first) ++begun0;
+        }
+        if (frees) {
+          ++i, ++u;
+          x = both ? 0 : i & 1;
+          if (ends) {
+            more = piece_next(s, a, x_begin, x_end);
+            i = x = 0;
+            ++piece;
           }
-          const bool block_done = !both || x == 1;
-          if (leader) {
-            mma_commit(&bar.s_full[x]);
-            if (block_done) mma_commit(&bar.k_free[st]);
-            if (block_done && i == cnt - 1) mma_commit(bar.q_free);
-          }
-          __syncwarp();
-          Owed& o = owed[x];
-          o.any = true;
-          o.u = u;
-          o.first = both ? i == 0 : i < 2;
-          o.last = both ? i == cnt - 1 : i + 2 >= cnt;
-          o.frees = block_done;
-          ++n_task[x];
-          if (o.first) ++n_first[x];
+        } else {
+          x = 1;
         }
       }
-    }
-    if (go) {
-      const int x = owed[0].any && (!owed[1].any || owed[0].u <= owed[1].u) ? 0 : 1;
-      pv(x);
-      pv(1 - x);
     }
     // every operation issued here finishes (bounded) before tensor memory is freed
     if (leader) {
@@ -700,11 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
     }
     __syncwarp();
+   }
   } else {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
     // exponent and the reference maximum M follows max(score + bias), so that P <= 2^8
     // whatever the scales; the row sum takes the bias back out.
+    regs_inc<kSoftRegs>();
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tmem_s(x) + lanes, to = tmem + tmem_o(x) + lanes;
@@ -719,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       return go;
     };
     for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
+      if (threadIdx.x == 0) note_cut();
       const bool both = s.both();
       const int cnt = s.count();
       const int rr = both ? x * kTile + row : row;  // row of the item
@@ -743,34 +815,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           const int pos0 = (s.b_lo + i) * kBlk;
           const bool masked = pos0 + kBlk - 1 > lim_all;
           const int thr = lim - pos0;  // columns <= thr are visible
-          // pass 1: the maximum
+          float v[4][32];  // this row of S
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, v[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_landed(v[c]);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < kBlk; ++k) v[k / 32][k % 32] = k <= thr ? v[k / 32][k % 32] : -INFINITY;
+          }
+          // the maximum
           float mx = -INFINITY;
           bool wide = false;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tmem_ld32(ts + 32 * c, v);
-            if (masked) {
+          for (int g = 0; g < kBlkPages; ++g) {
+            const float* w = &v[g / 2][16 * (g % 2)];
+            float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = 32 * c + k <= thr ? v[k] : -INFINITY;
+            for (int k = 4; k < 16; k += 4) {
+              pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
+              pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
             }
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float pm = v[16 * g];
-#pragma unroll
-              for (int k = 1; k < 15; k += 2) pm = fmaxf(fmaxf(pm, v[16 * g + k]), v[16 * g + k + 1]);
-              pm = fmaxf(pm, v[16 * g + 15]);
-              const float4 m = mt[2 * c + g];
-              if (FP8) {
-                bad += m.w;
-                wide = wide || fabsf(m.y) > 48.0f;
-                mx = fmaxf(mx, pm == -INFINITY ? pm : pm * (m.x * qsc) + m.y);
-              } else {
-                bad += m.w;
-                mx = fmaxf(mx, pm == -INFINITY ? pm : pm * qsc);
-              }
+            pm = fmaxf(pm, pn);
+            const float4 m = mt[g];
+            bad += m.w;
+            if (FP8) {
+              wide = wide || fabsf(m.y) > 48.0f;
+              mx = fmaxf(mx, pm == -INFINITY ? pm : __fmaf_rn(pm, m.x * qsc, m.y));
+            } else {
+              mx = fmaxf(mx, pm);
             }
           }
+          if (!FP8 && mx != -INFINITY) mx *= qsc;
           float alpha = 1.0f;
           if (mx > M + 8.0f) {
             alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
@@ -779,52 +856,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           }
           if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // PV of the block before was issued ahead of this S: it is complete
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld32(to + 32 * c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= alpha;
-              tmem_st32(to + 32 * c, o);
-            }
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) tmem_scale16(to + c, alpha);
           }
           const float ref = M == -INFINITY ? 0.0f : M;
           // where V scales lie far apart, P of a page with a small one can fall
           // below fp32's range while its weight counts: such a block's sum is
           // taken of the weights themselves (wide is the same in every lane)
           if (FP8 && wide) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tmem_ld32(ts + 32 * c, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (32 * c + k <= thr) l += ex2(__fmaf_rn(v[k], mt[2 * c + k / 16].x * qsc, -ref));
-            }
+            for (int k = 0; k < kBlk; ++k)
+              l += k <= thr ? ex2(__fmaf_rn(v[k / 32][k % 32], mt[k / 16].x * qsc, -ref)) : 0.0f;
           }
-          // pass 2: P and its sum
+          // P and its sum
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tmem_ld32(ts + 32 * c, v);
             uint32_t pk[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               const float4 m = mt[2 * c + g];
-              const float ks = FP8 ? m.x * qsc : qsc, add = FP8 ? m.y - ref : -ref;
+              // (a scale of 0 would make a masked score NaN)
+              const float ks = FP8 ? fmaxf(m.x * qsc, 1e-37f) : fmaxf(qsc, 1e-37f);
+              const float add = FP8 ? m.y - ref : -ref;
               const uint64_t k2 = pack2(ks, ks), a2 = pack2(add, add);
-              uint64_t sum = pack2(0.0f, 0.0f);
+              uint64_t sum = 0;
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 float e0, e1;
-                unpack2(fma2(pack2(v[16 * g + k], v[16 * g + k + 1]), k2, a2), e0, e1);
-                if (masked) {
-                  e0 = 32 * c + 16 * g + k <= thr ? e0 : -INFINITY;
-                  e1 = 32 * c + 16 * g + k + 1 <= thr ? e1 : -INFINITY;
-                }
+                unpack2(fma2(pack2(v[c][16 * g + k], v[c][16 * g + k + 1]), k2, a2), e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
-                sum = add2(sum, pack2(e0, e1));
+                sum = k == 0 ? pack2(e0, e1) : add2(sum, pack2(e0, e1));
                 pk[8 * g + k / 2] = pack_p<FP8>(e0, e1);
               }
               float s0, s1;
@@ -874,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       if (warp_live) {
         const int g = s.row0 + rr - t * p.G;
         uint16_t* out = p.out + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           float o[32];
           tmem_ld32(to + 32 * c, o);
@@ -923,16 +985,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");
-  if (threadIdx.x == 0) {
-    // the item that begins in this range and is cut by its end
-    int4 cut = make_int4(-1, 0, 0, 0);
-    Piece c;
-    for (bool m = piece_first(c, a, *first_item, x_begin, x_end); m;
-         m = piece_next(c, a, x_begin, x_end))
-      if (c.b_lo == 0 && c.b_hi < c.nb)
-        cut = make_int4(c.v, c.h, (int)((c.x0 + (long long)c.w() * (c.nb - 1)) / per), 0);
-    a.ws.cut[blockIdx.x] = cut;
-  }
 }
 
 // Cut items: the partials of the CTAs from the one that begins the item to the
