@@ -18,7 +18,7 @@
 // that lies wholly in its range; an item cut by a range's end leaves fp32
 // partials (o, running max, sum) for the combine kernel, at most two a CTA.
 //
-// Per CTA (one per SM), 13 warps:
+// Per CTA (one per SM):
 //   softmax A (0-3), B (4-7)  a thread per row: S from tensor memory twice (max,
 //                   then exp2), P back to tensor memory as the A operand of PV;
 //                   the output accumulator is rescaled only when a row's maximum
@@ -30,6 +30,8 @@
 //                   codes become f16 exactly, bf16 is copied
 //   MMA (12)        S = Q K^T and O += P V (M = N = 128), one tile's products
 //                   running while the other tile's softmax does
+//   scheduler (13)  the CTA's pieces, one after the other into a ring that the other
+//                   warps read, their query rows pulled into L2
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 #include <climits>
 
@@ -45,7 +47,8 @@ constexpr int kD = 128, kP = 16;
 constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
 constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps;
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kSchedWarp = kMmaWarp + 1;
+constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 4) * 32;
 // registers a thread of each warpgroup: together the 4 x 128 of the launch
 constexpr int kSoftRegs = 168, kConvRegs = 120, kMmaRegs = 56;
@@ -63,8 +66,9 @@ constexpr int OFF_V = OFF_K + 2 * kTileBytes;     // 2 blocks
 constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
 constexpr int OFF_QEXP = OFF_META + kMeta * kBlkPages * 16;  // [kMeta][256] int
 constexpr int OFF_MLB = OFF_QEXP + kMeta * kItemRows * 4;    // [128] float2
-constexpr int OFF_BAR = OFF_MLB + kTile * 8;
-constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1;
+constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
+constexpr int OFF_BAR = OFF_RING + kRing * 48;
+constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -199,62 +203,49 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
 
 // -------------------------------------------------------- a CTA's pieces
 
-// The piece of an item (item v, kv head h) that lies in [x_begin, x_end) of
-// the cost axis: blocks b_lo .. b_hi-1 of its nb.
+// The piece of an item (request r, kv head h, query rows row0 ..) that lies in a
+// CTA's range of the cost axis: blocks b_lo .. b_hi-1 of the item's nb.
 struct Piece {
-  int v, h;
-  int r, row0, nrows, nb;
-  int b_lo, b_hi;
-  int L, n, q0;
-  long long x0;  // cost position of the item; its blocks begin kItemCost behind
-  __device__ __forceinline__ int w() const { return nrows > kTile ? 2 : 1; }
-  __device__ __forceinline__ long long cost() const { return kItemCost + (long long)nb * w(); }
+  int r, h, row0, nrows;
+  int b_lo, b_hi, nb, L;
+  int n, q0, valid, pad;
   __device__ __forceinline__ bool both() const { return nrows > kTile; }
+  __device__ __forceinline__ int w() const { return both() ? 2 : 1; }
   __device__ __forceinline__ int count() const { return b_hi - b_lo; }
 };
+static_assert(sizeof(Piece) == 48, "ring slots");
 
-__device__ __forceinline__ int block_at(long long x, const Piece& s) {  // first block at or behind x
-  const long long d = x - s.x0 - kItemCost;
-  return d <= 0 ? 0 : (int)min((long long)s.nb, (d + s.w() - 1) / s.w());
+// The scheduler's place on the cost axis.
+struct Walk {
+  int v, h;
+  long long x0;  // cost position of (item v, head h); its blocks begin kItemCost behind
+  Piece s;
+  __device__ __forceinline__ long long cost() const { return kItemCost + (long long)s.nb * s.w(); }
+};
+
+__device__ __forceinline__ int block_at(long long x, const Walk& c) {  // first block at or behind x
+  const long long d = x - c.x0 - kItemCost, w = c.s.w();
+  return d <= 0 ? 0 : (int)min((long long)c.s.nb, (d + w - 1) >> (w - 1));
 }
 
-__device__ void piece_load(Piece& s, const Args& a, long long x_begin, long long x_end) {
-  const int4 it = a.ws.items[s.v];
-  s.r = it.x;
-  s.row0 = it.y;
-  s.nrows = it.z;
-  s.nb = it.w;
-  s.x0 = a.ws.pfx[s.v] * a.p.d.num_kv_heads + (long long)s.h * s.cost();
-  s.b_lo = block_at(x_begin, s);
-  s.b_hi = block_at(x_end, s);
-  s.L = a.p.seq_lens[s.r];
-  s.q0 = a.p.q_indptr[s.r];
-  s.n = a.p.q_indptr[s.r + 1] - s.q0;
+__device__ __forceinline__ void walk_item(Walk& c, const Args& a) {
+  const int4 it = a.ws.items[c.v];
+  c.s.r = it.x;
+  c.s.row0 = it.y;
+  c.s.nrows = it.z;
+  c.s.nb = it.w;
+  c.s.L = a.p.seq_lens[it.x];
+  c.s.q0 = a.p.q_indptr[it.x];
+  c.s.n = a.p.q_indptr[it.x + 1] - c.s.q0;
 }
 
-// The next piece with a block; false behind the range.
-__device__ bool piece_next(Piece& s, const Args& a, long long x_begin, long long x_end) {
-  for (;;) {
-    if (s.x0 + s.cost() >= x_end) return false;
-    if (++s.h == a.p.d.num_kv_heads) {
-      s.h = 0;
-      do {
-        if (++s.v >= a.V) return false;
-      } while (a.ws.pfx[s.v + 1] == a.ws.pfx[s.v]);
-    }
-    piece_load(s, a, x_begin, x_end);
-    if (s.b_lo < s.b_hi) return true;
-  }
-}
-
-// The first piece (v: the item that holds x_begin).
-__device__ bool piece_first(Piece& s, const Args& a, int v, long long x_begin, long long x_end) {
-  s.v = v;
-  s.h = 0;
-  piece_load(s, a, x_begin, x_end);
-  s.h = (int)((x_begin - s.x0) / s.cost());
-  piece_load(s, a, x_begin, x_end);
-  return s.b_lo < s.b_hi || piece_next(s, a, x_begin, x_end);
+__device__ __forceinline__ void walk_head(Walk& c, const Args& a, long long x_begin,
+                                          long long x_end) {
+  c.x0 = a.ws.pfx[c.v] * a.p.d.num_kv_heads + (long long)c.h * c.cost();
+  c.s.h = c.h;
+  c.s.b_lo = block_at(x_begin, c);
+  c.s.b_hi = block_at(x_end, c);
+  c.s.valid = 1;
 }
 
 // --------------------------------------------------------------- helpers
@@ -314,9 +305,7 @@ __device__ __forceinline__ void tmem_landed(float (&r)[32]) {
   asm volatile("" : KVFP8_R32("+f", r));
 }
 #undef KVFP8_R32
-// 16 columns times f, in place
-__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
-  float r[16];
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
@@ -325,6 +314,11 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
         "=f"(r[14]), "=f"(r[15])
       : "r"(taddr)
       : "memory");
+}
+// 16 columns times f, in place
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
+  float r[16];
+  tmem_ld16(taddr, r);
   uint32_t w[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(r[k] * f);
@@ -334,12 +328,32 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Wait for phase `parity` of `bar`: false once a wait of the CTA has run out
+// (kWaitLimitNs), which *abort_flag tells the others and the kernel's end reports.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag, int info) {
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity & 1u); ++i) {
+    if ((i & 15u) != 15u) continue;
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag != 0 || now - t0 > kWaitLimitNs) {
+      if (*abort_flag == 0) *abort_flag = info + 1;
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
   uint64_t* meta_ready;                                  // [kMeta]
   uint64_t *q_ready, *q_free;
   uint64_t *s_full, *p_ready, *o_full, *epi_done;        // [2] (tile)
   uint64_t *b_ml, *drain;
+  uint64_t *ring_full, *ring_free;                       // [kRing]
 };
 
 // --------------------------------------------------------------- kernel
@@ -360,9 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
   bar.epi_done = bar.s_full + 6;
   bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1;
+  bar.ring_full = bar.drain + 1, bar.ring_free = bar.ring_full + kRing;
+  Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  volatile int* first_item = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);
 
   const PrefillArgs& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,17 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == 1) {
-    // the last item that begins at or before x_begin, 32 entries a step
-    int lo = 0, n = a.V;
-    while (n > 1) {
-      const int step = (n + 31) / 32, at = lo + lane * step;
-      const bool le = lane * step < n && (lane == 0 || a.ws.pfx[at] * H <= x_begin);
-      const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
-      n = min(step, n - k * step);
-      lo += k * step;
-    }
-    if (lane == 0) *first_item = lo;
   } else if (threadIdx.x == 64) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_ready[i], kConvWarps);
@@ -406,6 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     mbar_init(bar.q_free, 1);
     mbar_init(bar.b_ml, 4);
     mbar_init(bar.drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.ring_full[i], 1);
+      mbar_init(&bar.ring_free[i], kMmaWarp + 1);  // every other working warp
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -414,13 +422,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int32_t* ctl = p.d.ctl;
+  bool go = true;  // the same in every lane of a warp
+  auto wait = [&](uint64_t* b, uint32_t parity, int info) {
+    if (go) go = wait_phase(b, parity, abort_flag, info);
+    return go;
+  };
+  // the CTA's next piece (valid 0: none is left)
   Piece s;
-  bool more = piece_first(s, a, *first_item, x_begin, x_end);
-  // the item that begins here and is cut by the range's end: for the combine
-  auto note_cut = [&]() {
-    if (s.b_lo == 0 && s.b_hi < s.nb)
-      a.ws.cut[blockIdx.x] = make_int4(
-          s.v, s.h, (int)((s.x0 + kItemCost + (long long)s.w() * (s.nb - 1)) / per), 0);
+  auto next_piece = [&](uint32_t piece) {
+    const uint32_t k = piece % kRing;
+    if (!wait(&bar.ring_full[k], piece / kRing, 1)) return false;
+    const int4* w = reinterpret_cast<const int4*>(&ring[k]);
+    const int4 w0 = w[0], w1 = w[1], w2 = w[2];
+    s.r = w0.x, s.h = w0.y, s.row0 = w0.z, s.nrows = w0.w;
+    s.b_lo = w1.x, s.b_hi = w1.y, s.nb = w1.z, s.L = w1.w;
+    s.n = w2.x, s.q0 = w2.y, s.valid = w2.z;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.ring_free[k]);
+    return s.valid != 0;
   };
 
   if (warp >= kSoftWarps && warp < kMmaWarp) {
@@ -433,23 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     constexpr long long kPageBytes = (long long)kP * kD * kEs;
     const uint8_t* kc = static_cast<const uint8_t*>(p.d.k_cache);
     const uint8_t* vc = static_cast<const uint8_t*>(p.d.v_cache);
-    int piece = 0;
-    long long u = 0;
-    bool go = true;
-    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
-      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
-                                                   wait_info(warp, 1, info)));
-      return go;
-    };
-    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
+    uint32_t u = 0;
+    for (uint32_t piece = 0; next_piece(piece); ++piece) {
       // ---- the item's query rows (16 lanes a row)
-      if (piece > 0 && !wait(bar.q_free, (uint32_t)(piece - 1), 60)) break;
+      if (piece > 0 && !wait(bar.q_free, piece - 1, 2)) break;
       const int tiles = s.both() ? 2 : 1;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 16 * tiles; i0 += 8) {
-        uint4 x[8];
+      for (int i0 = 0; i0 < 16 * tiles; i0 += 4) {
+        uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4);
           x[i] = make_uint4(0, 0, 0, 0);
           if (row < s.nrows) {
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4), c = lane & 15;
           uint4 y = x[i];
           if (flip) {
@@ -606,14 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       uint4 x0[8], x1[8];
       load_k(pg0, 0, x0);
       for (int b = s.b_lo; b < s.b_hi; ++b, ++u) {
-        const int st = (int)(u & 1), ms = (int)(u & (kMeta - 1));
-        const uint32_t free_phase = (uint32_t)((u >> 1) - 1);
+        const uint32_t st = u & 1, ms = u & (kMeta - 1), free_phase = (u >> 1) - 1;
         const int pg2 = page_of(raw2, b + 2);
         prefetch(pg2);
         raw2 = page_raw(b + 3);
         const float2 sc1 = scales_of(pg1);
         // K
-        if (u >= 2 && !wait(&bar.k_free[st], free_phase, 32 + st)) break;
+        if (u >= 2 && !wait(&bar.k_free[st], free_phase, 3)) break;
         uint8_t* kd = smem + OFF_K + st * kTileBytes;
         if (kParts == 2) {
           load_k(pg0, 1, x1);
@@ -637,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           mbar_arrive(&bar.meta_ready[ms]);
         }
         // V
-        if (u >= 2 && !wait(&bar.v_free[st], free_phase, 34 + st)) break;
+        if (u >= 2 && !wait(&bar.v_free[st], free_phase, 4)) break;
         uint8_t* vd = smem + OFF_V + st * kTileBytes;
         if (kParts == 2) {
           load_v(pg0, 1, x1);
@@ -675,17 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // what each tile owes: its block, and whether that is its first or last of the
     // piece and whether its PV is the block's last
     enum { kFirst = 1, kLast = 2, kFrees = 4 };
-    long long owed0 = -1, owed1 = -1;
+    int owed0 = -1, owed1 = -1;
     int how0 = 0, how1 = 0;
     uint32_t task0 = 0, task1 = 0, begun0 = 0, begun1 = 0;  // tasks / pieces of each tile
-    bool go = true;
-    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
-      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
-                                                   wait_info(warp, 0, info)));
-      return go;
-    };
-    long long u = 0;
+    int u = 0;
     uint32_t piece = 0;
+    bool more = next_piece(0);
     int i = 0, x = 0;  // the next task: block i of the piece, tile x
     while (go) {
       // the next step: a PV from two blocks back, the task's PV and S, or, behind the
@@ -695,14 +701,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       if (!more && !late0 && !late1) break;
       const bool late = late0 || late1;
       const int xs = !late ? x : late0 && (!late1 || owed0 <= owed1) ? 0 : 1;
-      const long long uo = xs ? owed1 : owed0;
+      const int uo = xs ? owed1 : owed0;
       const int how = xs ? how1 : how0;
       const uint32_t task = xs ? task1 : task0, begun = xs ? begun1 : begun0;
       if (uo >= 0) {  // ---- O += P V
-        const int st = (int)(uo & 1);
-        if (!wait(&bar.p_ready[xs], task - 1, 40 + xs)) break;
-        if (!wait(&bar.v_ready[st], (uint32_t)(uo >> 1), 42 + st)) break;
-        if ((how & kFirst) && begun > 1 && !wait(&bar.epi_done[xs], begun - 2, 44 + xs)) break;
+        const int st = uo & 1;
+        if (!wait(&bar.p_ready[xs], task - 1, 5)) break;
+        if (!wait(&bar.v_ready[st], (uint32_t)(uo >> 1), 6)) break;
+        if ((how & kFirst) && begun > 1 && !wait(&bar.epi_done[xs], begun - 2, 7)) break;
         tc_fence_after();
         const uint32_t o = tmem + tmem_o(xs), pa = tmem + tmem_s(xs);
         const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
@@ -720,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       if (late) continue;
       {  // ---- S = Q K^T
         const bool both = s.both();
-        const int cnt = s.count(), st = (int)(u & 1);
-        if (i == 0 && x == 0 && !wait(bar.q_ready, piece, 46)) break;
-        if (!wait(&bar.k_ready[st], (uint32_t)(u >> 1), 48 + st)) break;
+        const int cnt = s.count(), st = u & 1;
+        if (i == 0 && x == 0 && !wait(bar.q_ready, piece, 8)) break;
+        if (!wait(&bar.k_ready[st], (uint32_t)(u >> 1), 9)) break;
         tc_fence_after();
         const uint32_t so = tmem + tmem_s(x);
         const uint64_t q = dq + ((uint32_t)(both ? x * kTileBytes : 0) >> 4);
@@ -752,9 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           ++i, ++u;
           x = both ? 0 : i & 1;
           if (ends) {
-            more = piece_next(s, a, x_begin, x_end);
+            more = next_piece(++piece);
             i = x = 0;
-            ++piece;
           }
         } else {
           x = 1;
@@ -769,6 +774,61 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
     }
     __syncwarp();
+   } else if (warp == kSchedWarp) {
+    // ============================= scheduler =============================
+    Walk c;
+    {  // the last item that begins at or before x_begin, 32 entries a step
+      int lo = 0, n = a.V;
+      while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool le = lane * step < n && (lane == 0 || a.ws.pfx[at] * H <= x_begin);
+        const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
+        n = min(step, n - k * step);
+        lo += k * step;
+      }
+      c.v = lo;
+    }
+    walk_item(c, a);
+    c.h = (int)((x_begin - a.ws.pfx[c.v] * H) / c.cost());
+    bool more = true;
+    for (uint32_t piece = 0; more;) {
+      walk_head(c, a, x_begin, x_end);
+      if (c.s.b_lo < c.s.b_hi) {
+        // the item that begins here and is cut by the range's end: for the combine
+        if (lane == 0 && c.s.b_lo == 0 && c.s.b_hi < c.s.nb)
+          a.ws.cut[blockIdx.x] = make_int4(
+              c.v, c.h, (int)((c.x0 + kItemCost + (long long)c.s.w() * (c.s.nb - 1)) / per), 0);
+        if (piece >= kRing && !wait(&bar.ring_free[piece % kRing], piece / kRing - 1, 10)) break;
+        if (lane == 0) {
+          ring[piece % kRing] = c.s;
+          mbar_arrive(&bar.ring_full[piece % kRing]);
+        }
+        ++piece;
+        // its query rows: the heads of a token lie together
+        const int t0 = c.s.row0 / p.G, t1 = (c.s.row0 + c.s.nrows - 1) / p.G;
+        for (int t = t0 + lane; t <= t1; t += 32)
+          prefetch_l2(p.q + ((long long)(c.s.q0 + t) * p.Hq + c.h * p.G) * kD,
+                      (uint32_t)(p.G * kD * 2));
+      }
+      if (c.x0 + c.cost() >= x_end) more = false;
+      if (more && ++c.h == H) {
+        c.h = 0;
+        do {
+          if (++c.v >= a.V) {
+            more = false;
+            break;
+          }
+        } while (a.ws.pfx[c.v + 1] == a.ws.pfx[c.v]);
+        if (more) walk_item(c, a);
+      }
+      if (!more) {  // the end
+        if (piece >= kRing && !wait(&bar.ring_free[piece % kRing], piece / kRing - 1, 10)) break;
+        if (lane == 0) {
+          ring[piece % kRing].valid = 0;
+          mbar_arrive(&bar.ring_full[piece % kRing]);
+        }
+      }
+    }
    }
   } else {
     // ============================== softmax ==============================
@@ -780,17 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tmem_s(x) + lanes, to = tmem + tmem_o(x) + lanes;
     const float ssl = fabsf(p.sm_scale_log2);
-    long long u = 0;
-    uint32_t n_task = 0, n_o = 0, n_two = 0, n_b = 0;  // waits so far; pieces with blocks of B
-    int piece = 0;
-    bool go = true;
-    auto wait = [&](uint64_t* b, uint32_t parity, int info) {
-      go = go && __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, abort_flag, ctl,
-                                                   wait_info(warp, 0, info)));
-      return go;
-    };
-    for (; more && go; more = piece_next(s, a, x_begin, x_end), ++piece) {
-      if (threadIdx.x == 0) note_cut();
+    uint32_t u = 0, n_task = 0, n_o = 0, n_two = 0, n_b = 0;  // waits so far; pieces with blocks of B
+    for (uint32_t piece = 0; next_piece(piece); ++piece) {
       const bool both = s.both();
       const int cnt = s.count();
       const int rr = both ? x * kTile + row : row;  // row of the item
@@ -804,9 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       bool first = true;
       for (int i = 0; i < cnt && go; ++i, ++u) {
         if (!both && (i & 1) != x) continue;
-        const int ms = (int)(u & (kMeta - 1));
-        if (!wait(&bar.s_full[x], n_task, 52 + x)) break;
-        if (!wait(&bar.meta_ready[ms], (uint32_t)(u / kMeta), 54)) break;
+        const uint32_t ms = u & (kMeta - 1);
+        if (!wait(&bar.s_full[x], n_task, 11)) break;
+        if (!wait(&bar.meta_ready[ms], u / kMeta, 12)) break;
         ++n_task;
         tc_fence_after();
         if (FP8 && first) qsc = ssl * pow2f(-qexp[(piece & (kMeta - 1)) * kItemRows + rr]);
@@ -864,9 +915,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           // below fp32's range while its weight counts: such a block's sum is
           // taken of the weights themselves (wide is the same in every lane)
           if (FP8 && wide) {
+#pragma unroll 1
+            for (int c = 0; c < kBlkPages; ++c) {
+              float y[16];
+              tmem_ld16(ts + 16 * c, y);
+              const float ks = mt[c].x * qsc;
 #pragma unroll
-            for (int k = 0; k < kBlk; ++k)
-              l += k <= thr ? ex2(__fmaf_rn(v[k / 32][k % 32], mt[k / 16].x * qsc, -ref)) : 0.0f;
+              for (int k = 0; k < 16; ++k)
+                l += 16 * c + k <= thr ? ex2(__fmaf_rn(y[k], ks, -ref)) : 0.0f;
+            }
           }
           // P and its sum
 #pragma unroll
@@ -906,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // ---- the piece's output
       const bool used = both || cnt > x;     // this tile had a block
       const bool two = !both && cnt > 1;     // A and B hold parts of the same rows
-      if (used && !wait(&bar.o_full[x], n_o++, 56 + x)) break;
+      if (used && !wait(&bar.o_full[x], n_o++, 13)) break;
       tc_fence_after();
       if (!both && x == 1) {  // B's part goes to A's warps
         if (two) {
@@ -918,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
       float wa = 1.0f, wb = 0.0f;
       if (two) {
-        if (!wait(bar.b_ml, n_two++, 58)) break;
-        if (!wait(&bar.o_full[1], n_b, 59)) break;
+        if (!wait(bar.b_ml, n_two++, 14)) break;
+        if (!wait(&bar.o_full[1], n_b, 15)) break;
         tc_fence_after();
         const float2 b = ml_b[row];
         if (b.y < 0.0f) bad = 1.0f;
@@ -985,6 +1042,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");
+  if (threadIdx.x == 0 && *abort_flag != 0 &&
+      atomicCAS(reinterpret_cast<int*>(ctl + KV_CTL_ERROR), 0, KV_ERR_TIMEOUT) == 0)
+    ctl[KV_CTL_WAIT_INFO] = wait_info(kMmaWarp, 0, *abort_flag - 1);
 }
 
 // Cut items: the partials of the CTAs from the one that begins the item to the
