@@ -183,6 +183,7 @@ kv_status prefill_check(const kv_pool_desc& d, int B, int Hq, int total_q) {
   if (d.layout != KV_LAYOUT_GQA || d.head_dim_k != 128 || d.head_dim_v != 128 ||
       d.page_size != 16)
     return KV_ERR_UNSUPPORTED;
+  if (d.num_kv_heads > 4096) return KV_ERR_UNSUPPORTED;  // a page of all heads: 32-bit bytes
   // query rows of one kv head are counted in an int
   if ((long long)total_q * Hq > INT32_MAX) return KV_ERR_UNSUPPORTED;
   return KV_OK;

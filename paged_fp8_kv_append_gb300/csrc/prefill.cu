@@ -25,13 +25,16 @@
 //                   grows by more than 2^8, by the same warp; at an item's end
 //                   the output
 //   converters (8-11)  global pages -> registers -> 128B-swizzled K-major tiles
-//                   in shared memory: Q once an item, K [token][dim] and V
-//                   [dim][token] (pages hold V dim-major: no transpose).  e4m3
-//                   codes become f16 exactly, bf16 is copied
+//                   in shared memory: K [token][dim] and V [dim][token] (pages
+//                   hold V dim-major: no transpose).  e4m3 codes become f16
+//                   exactly, bf16 is copied
 //   MMA (12)        S = Q K^T and O += P V (M = N = 128), one tile's products
 //                   running while the other tile's softmax does
 //   scheduler (13)  the CTA's pieces, one after the other into a ring that the other
 //                   warps read, their query rows pulled into L2
+//   stagers (14-15) the next item's queries (f16 by an exact power of two a row, or
+//                   bf16) as an image of their tiles in global scratch; one bulk
+//                   copy brings it in once the item before has read its own
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 #include <climits>
 
@@ -48,11 +51,9 @@ constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
 constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kSchedWarp = kMmaWarp + 1;
+constexpr int kStageWarps = 2;  // behind the scheduler
 constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 4) * 32;
-// registers a thread of each warpgroup: together the 4 x 128 of the launch
-constexpr int kSoftRegs = 168, kConvRegs = 120, kMmaRegs = 56;
-static_assert(2 * kSoftRegs + kConvRegs + kMmaRegs == 512, "register split");
 // what an item costs beside its blocks (staging the queries, writing the output),
 // in halves of a two-tile block
 constexpr int kItemCost = 4;
@@ -68,7 +69,7 @@ constexpr int OFF_QEXP = OFF_META + kMeta * kBlkPages * 16;  // [kMeta][256] int
 constexpr int OFF_MLB = OFF_QEXP + kMeta * kItemRows * 4;    // [128] float2
 constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
 constexpr int OFF_BAR = OFF_RING + kRing * 48;
-constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 2 * kRing;
+constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 1 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -84,15 +85,8 @@ constexpr uint32_t idesc(bool bf16) {
          ((128u >> 4) << 24);
 }
 
-// register split of the warpgroups
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
+// flags of a key block, kept beside its scales
+constexpr uint32_t kBadPage = 1, kWide = 2;  // an id out of range; V scales far from 1
 
 // ------------------------------------------------------------------ plan
 
@@ -102,6 +96,7 @@ struct Ws {
   int4* cut;        // [grid] {item (-1: none), kv head, last CTA, 0}: the cut item a CTA begins
   float2* ml;       // [2 grid][256] (running max, sum; -1: a page that must not be read)
   float4* o;        // [2 grid][32][256]: 4 dims of a row
+  uint8_t* q;       // [grid] images of an item's query tiles
   size_t bytes;
 };
 
@@ -128,6 +123,7 @@ Ws ws_layout(void* base, int B, int G, int total_q, int grid) {
   w.cut = reinterpret_cast<int4*>(take(16 * (size_t)grid));
   w.ml = reinterpret_cast<float2*>(take(8ull * 2 * grid * kItemRows));
   w.o = reinterpret_cast<float4*>(take(4ull * 2 * grid * kItemRows * kD));
+  w.q = take(1ull * grid * 2 * kTileBytes);
   w.bytes = off;
   return w;
 }
@@ -281,30 +277,29 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
       "%13,%14,%15,%16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
 }
-#define KVFP8_R32(op, r)                                                                        \
-  op(r[0]), op(r[1]), op(r[2]), op(r[3]), op(r[4]), op(r[5]), op(r[6]), op(r[7]), op(r[8]),     \
-      op(r[9]), op(r[10]), op(r[11]), op(r[12]), op(r[13]), op(r[14]), op(r[15]), op(r[16]),    \
-      op(r[17]), op(r[18]), op(r[19]), op(r[20]), op(r[21]), op(r[22]), op(r[23]), op(r[24]),   \
-      op(r[25]), op(r[26]), op(r[27]), op(r[28]), op(r[29]), op(r[30]), op(r[31])
-// 32 columns, not waited for
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&r)[32]) {
+// 32 columns of this warp's lanes, not waited for
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : KVFP8_R32("=f", r)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
+// ... landed: no use of v comes before this
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile(""
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+        "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+        "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+        "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
-// (behind the wait: the values are not read before it)
-__device__ __forceinline__ void tmem_landed(float (&r)[32]) {
-  asm volatile("" : KVFP8_R32("+f", r));
-}
-#undef KVFP8_R32
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -330,27 +325,33 @@ __device__ __forceinline__ void tmem_wait_st() {
 
 // Wait for phase `parity` of `bar`: false once a wait of the CTA has run out
 // (kWaitLimitNs), which *abort_flag tells the others and the kernel's end reports.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
-                                           volatile int* abort_flag, int info) {
+// What follows a first probe (which itself waits a while) is out of line: the
+// kernel's loops have to stay small in the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                     int info) {
   uint64_t t0 = 0;
-  bool ok = true;
-  for (uint32_t i = 0; !mbar_try_wait(bar, parity & 1u); ++i) {
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
     if ((i & 15u) != 15u) continue;
     const uint64_t now = global_ns();
     if (t0 == 0) t0 = now;
     if (*abort_flag != 0 || now - t0 > kWaitLimitNs) {
       if (*abort_flag == 0) *abort_flag = info + 1;
-      ok = false;
-      break;
+      return false;
     }
   }
+  return true;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag, int info) {
+  bool ok = mbar_try_wait(bar, parity & 1u);
+  if (!ok) ok = wait_on(bar, parity & 1u, abort_flag, info);
   return __all_sync(0xffffffffu, ok);
 }
 
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
   uint64_t* meta_ready;                                  // [kMeta]
-  uint64_t *q_ready, *q_free;
+  uint64_t *q_ready, *q_free, *q_image;
   uint64_t *s_full, *p_ready, *o_full, *epi_done;        // [2] (tile)
   uint64_t *b_ml, *drain;
   uint64_t *ring_full, *ring_free;                       // [kRing]
@@ -373,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   bar.q_ready = bp + 8 + kMeta, bar.q_free = bar.q_ready + 1;
   bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
   bar.epi_done = bar.s_full + 6;
-  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1;
-  bar.ring_full = bar.drain + 1, bar.ring_free = bar.ring_full + kRing;
+  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1, bar.q_image = bar.drain + 1;
+  bar.ring_full = bar.q_image + 1, bar.ring_free = bar.ring_full + kRing;
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -400,19 +401,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       mbar_init(&bar.k_free[i], 1);
       mbar_init(&bar.v_ready[i], kConvWarps);
       mbar_init(&bar.v_free[i], 1);
-      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.s_full[i], 2);  // the products' end, and the issuing warp itself
       mbar_init(&bar.p_ready[i], 4);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.epi_done[i], 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&bar.meta_ready[i], kConvWarps);
-    mbar_init(bar.q_ready, kConvWarps);
+    mbar_init(bar.q_ready, 1);
+    mbar_init(bar.q_image, kStageWarps);
     mbar_init(bar.q_free, 1);
     mbar_init(bar.b_ml, 4);
     mbar_init(bar.drain, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ring_full[i], 1);
-      mbar_init(&bar.ring_free[i], kMmaWarp + 1);  // every other working warp
+      mbar_init(&bar.ring_free[i], kMmaWarp + 1 + kStageWarps);  // every warp that reads it
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -444,62 +446,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
 
   if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ============================ converters ============================
-    regs_dec<kConvRegs>();
     const int cw = warp - kSoftWarps, ct = threadIdx.x - kSoftWarps * 32;
-    const bool flip = p.sm_scale_log2 < 0.0f;  // a negative scale turns the queries' sign
     constexpr int kEs = FP8 ? 1 : 2;
     constexpr int kParts = FP8 ? 1 : 2;        // 16 KB source parts of a block's K or V
     constexpr long long kPageBytes = (long long)kP * kD * kEs;
     const uint8_t* kc = static_cast<const uint8_t*>(p.d.k_cache);
     const uint8_t* vc = static_cast<const uint8_t*>(p.d.v_cache);
+    const uint32_t page_step = (uint32_t)(H * kPageBytes);
+    // this thread's places in a swizzled tile (the row's low bits are the same in every piece)
+    const int vr = FP8 ? ct >> 2 : ct >> 3;
+    const uint32_t off0 = swz(vr, FP8 ? 2 * (ct & 3) : ct & 7);
+    const uint32_t off1 = swz(vr, 2 * (ct & 3) + 1);  // e4m3
     uint32_t u = 0;
     for (uint32_t piece = 0; next_piece(piece); ++piece) {
-      // ---- the item's query rows (16 lanes a row)
-      if (piece > 0 && !wait(bar.q_free, piece - 1, 2)) break;
-      const int tiles = s.both() ? 2 : 1;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 16 * tiles; i0 += 4) {
-        uint4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (row < s.nrows) {
-            const int tg = s.row0 + row, t = tg / p.G, g = tg - t * p.G;
-            x[i] = *reinterpret_cast<const uint4*>(
-                p.q + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD + 8 * (lane & 15));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 2 * ((i0 + i) * kConvWarps + cw) + (lane >> 4), c = lane & 15;
-          uint4 y = x[i];
-          if (flip) {
-            y.x ^= 0x80008000u;
-            y.y ^= 0x80008000u;
-            y.z ^= 0x80008000u;
-            y.w ^= 0x80008000u;
-          }
-          if (FP8) {
-            uint32_t mb = bf16_absbits_max8(x[i]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-            const int e = q_row_exp(mb);
-            const float pw = pow2f(e);
-            y.x = bf16x2_to_f16x2_scaled(y.x, pw);
-            y.y = bf16x2_to_f16x2_scaled(y.y, pw);
-            y.z = bf16x2_to_f16x2_scaled(y.z, pw);
-            y.w = bf16x2_to_f16x2_scaled(y.w, pw);
-            if (c == 0) qexp[(piece & (kMeta - 1)) * kItemRows + row] = e;
-          }
-          *reinterpret_cast<uint4*>(smem + OFF_Q + (row >> 7) * kTileBytes + (c >> 3) * kHalf +
-                                    swz(row & 127, c & 7)) = y;
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.q_ready);
-
       // ---- the key blocks
       const int32_t* prow = p.page_table + (long long)s.r * p.max_pages;
       const int npages = s.L / kP + (s.L % kP != 0);
@@ -522,83 +481,69 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // page 0: its scores are masked or its item is not written, and its V is
       // zeroed with what lies behind the length.
       const uint8_t *kh = kc + s.h * kPageBytes, *vh = vc + s.h * kPageBytes;
-      const long long page_step = (long long)H * kPageBytes;
-      // piece i of this thread: K token 16 i + ct / 8 (page i), 16-byte chunk ct % 8
+      auto page_at = [&](const uint8_t* base, int pgl, int l) {  // lane l's page
+        const uint32_t pg = (uint32_t)__shfl_sync(0xffffffffu, pgl, l);
+        return base + (uint64_t)pg * page_step;
+      };
+      // Piece i (16 bytes) of this thread goes to tile row 32 (i / 2) + ct / 4 (a token of K, a
+      // dim of V), half i % 2, as two chunks (bf16: row 16 i + ct / 8 of half `part`, one
+      // chunk): 8 lanes store 2 rows of 4 chunk pairs, which no bank group meets twice.
+      // e4m3: K token 32 (i / 2) + ct / 4, dims 64 (i % 2) + 16 (ct % 4) ..
+      //       V dim 32 (i / 2) + ct / 4, tokens of page 4 (i % 2) + ct % 4
+      // bf16: K token 16 i + ct / 8 (page i), dims 64 part + 8 (ct % 8) ..
+      //       V dim 16 i + ct / 8, tokens 64 part + 8 (ct % 8) ..
       auto load_k = [&](int pgl, int part, uint4 (&x)[8]) {
+        pgl = max(pgl, 0);
+        const uint8_t* src = nullptr;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const long long pg = __shfl_sync(0xffffffffu, max(pgl, 0), FP8 ? i : 4 * part + (i >> 1));
-          const int off = FP8 ? ct * 16 : (i & 1) * 2048 + ct * 16;
-          x[i] = __ldg(reinterpret_cast<const uint4*>(kh + pg * page_step + off));
+          if (!FP8 || (i & 1) == 0)
+            src = page_at(kh, pgl, FP8 ? i + (ct >> 6) : i) +
+                  (FP8 ? ((ct >> 2) & 15) * 128 + (ct & 3) * 16 : (ct >> 3) * 256 + (ct & 7) * 16);
+          x[i] = __ldg(reinterpret_cast<const uint4*>(src + (FP8 ? (i & 1) * 64 : part * 128)));
         }
       };
-      auto store_k = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (FP8) {
-            const int t = 16 * i + (ct >> 3), j = ct & 7;
-            uint4 lo, hi;
-            e4m3x4_to_f16(x[i].x, lo.x, lo.y);
-            e4m3x4_to_f16(x[i].y, lo.z, lo.w);
-            e4m3x4_to_f16(x[i].z, hi.x, hi.y);
-            e4m3x4_to_f16(x[i].w, hi.z, hi.w);
-            // the two halves' lanes store their chunks in opposite order: no
-            // two of 8 lanes then share a bank group
-            uint8_t* h = dst + (j >> 2) * kHalf;
-            const int c = 2 * (j & 3), odd = j >> 2;
-            *reinterpret_cast<uint4*>(h + swz(t, c + odd)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(h + swz(t, c + 1 - odd)) = odd ? lo : hi;
-          } else {
-            const int t = 64 * part + 8 * i + (ct >> 4), c = ct & 15;
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + swz(t, c & 7)) = x[i];
-          }
-        }
-      };
-      // piece i: e4m3 V dim 32 (i / 2) + ct / 4 of page 4 (i % 2) + ct % 4; bf16 V dim
-      // 16 i + ct / 8, page 4 part + (ct % 8) / 2, tokens 8 (ct % 2) ..
       auto load_v = [&](int pgl, int part, uint4 (&x)[8]) {
+        pgl = max(pgl, 0);
+        const uint8_t* s0 = page_at(vh, pgl, FP8 ? ct & 3 : 4 * part + ((ct & 7) >> 1)) +
+                            (FP8 ? (ct >> 2) * 16 : (ct >> 3) * 32 + (ct & 1) * 16);
+        const uint8_t* s1 = FP8 ? page_at(vh, pgl, 4 + (ct & 3)) + (ct >> 2) * 16 : s0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int pi = FP8 ? 4 * (i & 1) + (ct & 3) : 4 * part + ((ct & 7) >> 1);
-          const long long pg = __shfl_sync(0xffffffffu, max(pgl, 0), pi);
-          const int off = FP8 ? (32 * (i >> 1) + (ct >> 2)) * 16
-                              : (16 * i + (ct >> 3)) * 32 + (ct & 1) * 16;
-          x[i] = __ldg(reinterpret_cast<const uint4*>(vh + pg * page_step + off));
-        }
+        for (int i = 0; i < 8; ++i)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(FP8 ? ((i & 1) ? s1 : s0) + 512 * (i >> 1)
+                                                          : s0 + 512 * i));
       };
-      // tokens behind the length are zeroed: their bytes may be NaN, and
-      // 0 * NaN would reach the output
-      auto clean_v = [&](int part, int b, uint4 (&x)[8]) {
-        if ((b + 1) * kBlk <= s.L) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = FP8 ? (4 * (i & 1) + (ct & 3)) * kP
-                             : (4 * part + ((ct & 7) >> 1)) * kP + (ct & 1) * 8;
-          const int nv = s.L - (b * kBlk + at);  // valid tokens from the piece's first on
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int bytes = FP8 ? nv - 4 * k : 2 * (nv - 2 * k);
-            w[k] = bytes >= 4 ? w[k] : bytes <= 0 ? 0u : w[k] & ((1u << (8 * bytes)) - 1u);
-          }
-        }
-      };
-      auto store_v = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
+      auto store = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
-            const int d = 32 * (i >> 1) + (ct >> 2);
             uint4 lo, hi;
             e4m3x4_to_f16(x[i].x, lo.x, lo.y);
             e4m3x4_to_f16(x[i].y, lo.z, lo.w);
             e4m3x4_to_f16(x[i].z, hi.x, hi.y);
             e4m3x4_to_f16(x[i].w, hi.z, hi.w);
-            uint8_t* h = dst + (i & 1) * kHalf;
-            *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3))) = lo;
-            *reinterpret_cast<uint4*>(h + swz(d, 2 * (ct & 3) + 1)) = hi;
+            uint8_t* h = dst + (i & 1) * kHalf + (i >> 1) * 4096;
+            *reinterpret_cast<uint4*>(h + off0) = lo;
+            *reinterpret_cast<uint4*>(h + off1) = hi;
           } else {
-            *reinterpret_cast<uint4*>(dst + part * kHalf + swz(16 * i + (ct >> 3), ct & 7)) = x[i];
+            *reinterpret_cast<uint4*>(dst + off0 + part * kHalf + 2048 * i) = x[i];
           }
+        }
+      };
+      // tokens behind the length are zeroed where this thread stored them: their
+      // bytes may be NaN, and 0 * NaN would reach the output
+      auto clean_v = [&](uint8_t* dst, int b) {
+        if ((b + 1) * kBlk <= s.L) return;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {  // the thread's 16-byte chunks of 8 tokens
+          const uint32_t at = FP8 ? ((i >> 1) & 1) * kHalf + (i >> 2) * 4096 + ((i & 1) ? off1 : off0)
+                                  : (i & 1) * kHalf + (i >> 1) * 2048 + off0;
+          const int tok = FP8 ? (4 * ((i >> 1) & 1) + (ct & 3)) * kP + 8 * (i & 1)
+                              : 64 * (i & 1) + 8 * (ct & 7);
+          const int nv = s.L - b * kBlk - tok;  // valid tokens of the chunk
+          if (nv >= 8) continue;
+          uint16_t* h = reinterpret_cast<uint16_t*>(dst + at);
+          for (int k = max(nv, 0); k < 8; ++k) h[k] = 0;
         }
       };
       // pages two blocks ahead are pulled into L2 (lanes 0-7 K, 8-15 V, of one warp)
@@ -628,18 +573,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         uint8_t* kd = smem + OFF_K + st * kTileBytes;
         if (kParts == 2) {
           load_k(pg0, 1, x1);
-          store_k(kd, 0, x0);
+          store(kd, 0, x0);
           load_v(pg0, 0, x0);
-          store_k(kd, 1, x1);
+          store(kd, 1, x1);
         } else {
           load_v(pg0, 0, x1);
-          store_k(kd, 0, x0);
+          store(kd, 0, x0);
         }
-        if (cw == 0 && lane < kBlkPages) {
-          if (pg0 == -2) set_error(ctl, KV_ERR_BAD_PAGE_ID);
+        if (cw == 0) {
           const float bias = __log2f(sc0.y);
-          meta[ms * kBlkPages + lane] =
-              make_float4(sc0.x, bias, ex2(-bias), pg0 == -2 ? 1.0f : 0.0f);
+          const uint32_t flags =
+              (__any_sync(0xffffffffu, pg0 == -2) ? kBadPage : 0u) |
+              (__any_sync(0xffffffffu, lane < kBlkPages && fabsf(bias) > 48.0f) ? kWide : 0u);
+          if (lane < kBlkPages)
+            meta[ms * kBlkPages + lane] =
+                make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias), __uint_as_float(flags));
+          if (lane == 0 && (flags & kBadPage)) set_error(ctl, KV_ERR_BAD_PAGE_ID);
         }
         fence_async_smem();
         __syncwarp();
@@ -652,16 +601,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         uint8_t* vd = smem + OFF_V + st * kTileBytes;
         if (kParts == 2) {
           load_v(pg0, 1, x1);
-          clean_v(0, b, x0);
-          store_v(vd, 0, x0);
+          store(vd, 0, x0);
           if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          clean_v(1, b, x1);
-          store_v(vd, 1, x1);
+          store(vd, 1, x1);
         } else {
           if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          clean_v(0, b, x1);
-          store_v(vd, 0, x1);
+          store(vd, 0, x1);
         }
+        clean_v(vd, b);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v_ready[st]);
@@ -671,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
     }
   } else if (warp >= kMmaWarp) {
-   regs_dec<kMmaRegs>();
    if (warp == kMmaWarp) {
     // ============================ MMA issuer ============================
     // Task (block u, tile X): S = Q_X K^T.  Just before it, the PV that X still
@@ -712,10 +658,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         tc_fence_after();
         const uint32_t o = tmem + tmem_o(xs), pa = tmem + tmem_s(xs);
         const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
+        bool add = !(how & kFirst);
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int k = 0; k < kBlk / 16; ++k)
-          mma_f16_ts_if(leader, o, pa + 8 * k, d + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kId,
-                        !((how & kFirst) && k == 0));
+          for (int k = 0; k < 4; ++k) {
+            mma_f16_ts_if(leader, o, pa + 32 * j + 8 * k, d + ((j * kHalf + k * 32) >> 4), kId, add);
+            add = true;
+          }
+        }
         if (leader) {
           if (how & kFrees) mma_commit(&bar.v_free[st]);
           if (how & kLast) mma_commit(&bar.o_full[xs]);
@@ -733,14 +684,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         const uint32_t so = tmem + tmem_s(x);
         const uint64_t q = dq + ((uint32_t)(both ? x * kTileBytes : 0) >> 4);
         const uint64_t kk = dk + ((uint32_t)(st * kTileBytes) >> 4);
+        bool add = false;
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          mma_f16_if(leader, so, q + off, kk + off, kId, k > 0);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t off = (uint32_t)(j * kHalf + k * 32) >> 4;
+            mma_f16_if(leader, so, q + off, kk + off, kId, add);
+            add = true;
+          }
         }
         const bool frees = !both || x == 1, ends = frees && i == cnt - 1;
         if (leader) {
           mma_commit(&bar.s_full[x]);
+          mbar_arrive(&bar.s_full[x]);  // what this warp has waited for is seen behind it
           if (frees) mma_commit(&bar.k_free[st]);
           if (ends) mma_commit(bar.q_free);
         }
@@ -829,76 +786,157 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         }
       }
     }
+   } else {
+    // ============================== stagers ==============================
+    const int sw = warp - kSchedWarp - 1, c = lane & 15;  // 16 lanes a row, 8 dims each
+    const bool flip = p.sm_scale_log2 < 0.0f;  // a negative scale turns the queries' sign
+    uint8_t* img = a.ws.q + 2ll * blockIdx.x * kTileBytes;
+    uint32_t copies = 0;
+    for (uint32_t piece = 0; next_piece(piece); ++piece) {
+      // the copy of the piece before has read the image
+      if (piece > 0 && !wait(bar.q_ready, piece - 1, 2)) break;
+      const int rows = s.both() ? kItemRows : kTile;
+      constexpr int kGo = 4;  // rows of a half-warp in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < rows; i0 += 2 * kStageWarps * kGo) {
+        uint4 y[kGo];
+#pragma unroll
+        for (int i = 0; i < kGo; ++i) {
+          const int row = i0 + 2 * (i * kStageWarps + sw) + (lane >> 4);
+          y[i] = make_uint4(0, 0, 0, 0);
+          if (row < s.nrows) {
+            const int tg = s.row0 + row, t = tg / p.G, g = tg - t * p.G;
+            y[i] = *reinterpret_cast<const uint4*>(
+                p.q + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD + 8 * c);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kGo; ++i) {
+          const int row = i0 + 2 * (i * kStageWarps + sw) + (lane >> 4);
+          if (flip) {
+            y[i].x ^= 0x80008000u;
+            y[i].y ^= 0x80008000u;
+            y[i].z ^= 0x80008000u;
+            y[i].w ^= 0x80008000u;
+          }
+          if (FP8) {
+            uint32_t mb = absbits_max8(0, y[i]);
+            mb = max(mb & 0xFFFFu, mb >> 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+            const int e = q_row_exp(mb);
+            const float pw = pow2f(e);
+            y[i].x = bf16x2_to_f16x2_scaled(y[i].x, pw);
+            y[i].y = bf16x2_to_f16x2_scaled(y[i].y, pw);
+            y[i].z = bf16x2_to_f16x2_scaled(y[i].z, pw);
+            y[i].w = bf16x2_to_f16x2_scaled(y[i].w, pw);
+            if (c == 0) qexp[(piece & (kMeta - 1)) * kItemRows + row] = e;
+          }
+          *reinterpret_cast<uint4*>(img + (row >> 7) * kTileBytes + (c >> 3) * kHalf +
+                                    swz(row & 127, c & 7)) = y[i];
+        }
+      }
+      // the image is read by a bulk copy: written through the generic proxy, so fenced
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.q_image);
+      if (sw == 0) {
+        if (!wait(bar.q_image, piece, 16)) break;
+        if (piece > 0 && !wait(bar.q_free, piece - 1, 2)) break;
+        if (lane == 0) {
+          asm volatile("fence.proxy.async;" ::: "memory");
+          const uint32_t bytes = (uint32_t)((rows / kTile) * kTileBytes);
+          mbar_arrive_expect_tx(bar.q_ready, bytes);
+          bulk_g2s(smem + OFF_Q, img, bytes, bar.q_ready, l2_evict_first_policy());
+        }
+        ++copies;
+      }
+    }
+    if (!go && copies > 0) {  // a copy in flight ends (bounded) before the CTA does
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(bar.q_ready, (copies - 1) & 1u) && global_ns() - t0 < 100000000ull) {
+      }
+    }
    }
   } else {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
     // exponent and the reference maximum M follows max(score + bias), so that P <= 2^8
     // whatever the scales; the row sum takes the bias back out.
-    regs_inc<kSoftRegs>();
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tmem_s(x) + lanes, to = tmem + tmem_o(x) + lanes;
-    const float ssl = fabsf(p.sm_scale_log2);
-    uint32_t u = 0, n_task = 0, n_o = 0, n_two = 0, n_b = 0;  // waits so far; pieces with blocks of B
-    for (uint32_t piece = 0; next_piece(piece); ++piece) {
-      const bool both = s.both();
-      const int cnt = s.count();
-      const int rr = both ? x * kTile + row : row;  // row of the item
-      const bool live = rr < s.nrows;
-      const bool warp_live = __any_sync(0xffffffffu, live);
-      const int t = (s.row0 + min(rr, s.nrows - 1)) / p.G;
-      const int lim = s.L - s.n + t;  // last visible position
-      // every row of the tile sees a block that ends at or before this position
-      const int lim_all = s.L - s.n + (s.row0 + (both ? x * kTile : 0)) / p.G;
-      float qsc = ssl, M = -INFINITY, l = 0.0f, bad = 0.0f;
+    // phases of the barriers that this warp waits for, a bit each
+    enum { kS = 1, kO = 2, kMl = 4, kOB = 8 };
+    uint32_t u = 0, ph = 0;
+    for (uint32_t piece = 0;; ++piece) {
+      if (!wait(&bar.ring_full[piece % kRing], piece / kRing, 1)) break;
+      const volatile Piece* pc = ring + piece % kRing;
+      if (!pc->valid) break;
+      const int rows = pc->nrows, cnt = pc->b_hi - pc->b_lo;
+      const bool both = rows > kTile;
+      const int tile0 = both ? x * kTile : 0;  // the tile's first row in the item
+      const bool warp_live = tile0 + (warp & 3) * 32 < rows;
+      // last positions that this row and the tile's first row see, from the piece's first
+      // key block on
+      const int seen0 = pc->L - pc->n - pc->b_lo * kBlk;
+      int lim = seen0 + (pc->row0 + min(tile0 + row, rows - 1)) / p.G;
+      int lim_all = seen0 + (pc->row0 + tile0) / p.G;
+      float qsc = fabsf(p.sm_scale_log2), M = -INFINITY, l = 0.0f;
+      uint32_t flags = 0;
       bool first = true;
-      for (int i = 0; i < cnt && go; ++i, ++u) {
+      for (int i = 0; i < cnt && go; ++i, ++u, lim -= kBlk, lim_all -= kBlk) {
         if (!both && (i & 1) != x) continue;
         const uint32_t ms = u & (kMeta - 1);
-        if (!wait(&bar.s_full[x], n_task, 11)) break;
+        if (!wait(&bar.s_full[x], ph & kS, 11)) break;
         if (!wait(&bar.meta_ready[ms], u / kMeta, 12)) break;
-        ++n_task;
+        ph ^= kS;
         tc_fence_after();
-        if (FP8 && first) qsc = ssl * pow2f(-qexp[(piece & (kMeta - 1)) * kItemRows + rr]);
+        if (FP8 && first) qsc *= pow2f(-qexp[(piece & (kMeta - 1)) * kItemRows + tile0 + row]);
         const float4* mt = meta + ms * kBlkPages;
         if (warp_live) {
-          const int pos0 = (s.b_lo + i) * kBlk;
-          const bool masked = pos0 + kBlk - 1 > lim_all;
-          const int thr = lim - pos0;  // columns <= thr are visible
-          float v[4][32];  // this row of S
+          const uint32_t fl = __float_as_uint(mt[0].w);
+          flags |= fl;
+          float va[32], vb[32];  // 32 columns of this row of S, by turns
+          if (lim_all < kBlk - 1) {  // columns <= lim are visible: the others to -inf
+#pragma unroll 1
+            for (int c = 0; c < kBlk; c += 32) {
+              tmem_ld32_async(ts + c, va);
+              tmem_wait_ld(va);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, v[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_landed(v[c]);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < kBlk; ++k) v[k / 32][k % 32] = k <= thr ? v[k / 32][k % 32] : -INFINITY;
+              for (int k = 0; k < 32; ++k) va[k] = c + k <= lim ? va[k] : -INFINITY;
+              tmem_st32(ts + c, va);
+            }
           }
-          // the maximum
+          // the maximum (a scale of 0 would make a masked score NaN)
           float mx = -INFINITY;
-          bool wide = false;
+          auto max32 = [&](const float (&v)[32], const float4* m2) {
 #pragma unroll
-          for (int g = 0; g < kBlkPages; ++g) {
-            const float* w = &v[g / 2][16 * (g % 2)];
-            float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
+            for (int g = 0; g < 2; ++g) {
+              const float* w = &v[16 * g];
+              float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
 #pragma unroll
-            for (int k = 4; k < 16; k += 4) {
-              pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
-              pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
+              for (int k = 4; k < 16; k += 4) {
+                pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
+                pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
+              }
+              pm = fmaxf(pm, pn);
+              mx = FP8 ? fmaxf(mx, __fmaf_rn(pm, fmaxf(m2[g].x * qsc, 1e-37f), m2[g].y))
+                       : fmaxf(mx, pm);
             }
-            pm = fmaxf(pm, pn);
-            const float4 m = mt[g];
-            bad += m.w;
-            if (FP8) {
-              wide = wide || fabsf(m.y) > 48.0f;
-              mx = fmaxf(mx, pm == -INFINITY ? pm : __fmaf_rn(pm, m.x * qsc, m.y));
-            } else {
-              mx = fmaxf(mx, pm);
-            }
+          };
+          tmem_ld32_async(ts, va);
+          tmem_wait_ld(va);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32_async(ts + 64 * c + 32, vb);
+            max32(va, mt + 4 * c);
+            tmem_wait_ld(vb);
+            tmem_ld32_async(ts + 64 * (1 - c), va);  // (at last the first ones again)
+            max32(vb, mt + 4 * c + 2);
+            tmem_wait_ld(va);
           }
-          if (!FP8 && mx != -INFINITY) mx *= qsc;
+          if (!FP8) mx *= fmaxf(qsc, 1e-37f);
           float alpha = 1.0f;
           if (mx > M + 8.0f) {
             alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
@@ -913,34 +951,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           const float ref = M == -INFINITY ? 0.0f : M;
           // where V scales lie far apart, P of a page with a small one can fall
           // below fp32's range while its weight counts: such a block's sum is
-          // taken of the weights themselves (wide is the same in every lane)
-          if (FP8 && wide) {
+          // taken of the weights themselves (and its pages' factors below are 0)
+          if (FP8 && (fl & kWide)) {
 #pragma unroll 1
             for (int c = 0; c < kBlkPages; ++c) {
               float y[16];
               tmem_ld16(ts + 16 * c, y);
-              const float ks = mt[c].x * qsc;
+              const float kq = fmaxf(mt[c].x * qsc, 1e-37f);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                l += 16 * c + k <= thr ? ex2(__fmaf_rn(y[k], ks, -ref)) : 0.0f;
+              for (int k = 0; k < 16; ++k) l += ex2(__fmaf_rn(y[k], kq, -ref));
             }
           }
           // P and its sum
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          auto exp32 = [&](const float (&v)[32], const float4* m2, uint32_t tp) {
             uint32_t pk[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float4 m = mt[2 * c + g];
-              // (a scale of 0 would make a masked score NaN)
-              const float ks = FP8 ? fmaxf(m.x * qsc, 1e-37f) : fmaxf(qsc, 1e-37f);
-              const float add = FP8 ? m.y - ref : -ref;
-              const uint64_t k2 = pack2(ks, ks), a2 = pack2(add, add);
+              const float4 m = FP8 ? m2[g] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+              const float kq = fmaxf(FP8 ? m.x * qsc : qsc, 1e-37f), add = FP8 ? m.y - ref : -ref;
+              const uint64_t k2 = pack2(kq, kq), a2 = pack2(add, add);
               uint64_t sum = 0;
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 float e0, e1;
-                unpack2(fma2(pack2(v[c][16 * g + k], v[c][16 * g + k + 1]), k2, a2), e0, e1);
+                unpack2(fma2(pack2(v[16 * g + k], v[16 * g + k + 1]), k2, a2), e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum = k == 0 ? pack2(e0, e1) : add2(sum, pack2(e0, e1));
@@ -948,9 +982,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               }
               float s0, s1;
               unpack2(sum, s0, s1);
-              l = !FP8 ? l + (s0 + s1) : wide ? l : __fmaf_rn(s0 + s1, m.z, l);
+              l = !FP8 ? l + (s0 + s1) : __fmaf_rn(s0 + s1, m.z, l);
             }
-            tmem_st16u(ts + 16 * c, pk);
+            tmem_st16u(tp, pk);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32_async(ts + 64 * c + 32, vb);
+            exp32(va, mt + 4 * c, ts + 32 * c);
+            tmem_wait_ld(vb);
+            tmem_ld32_async(ts + 64, va);
+            exp32(vb, mt + 4 * c + 2, ts + 32 * c + 16);
+            tmem_wait_ld(va);
           }
           tmem_wait_st();
         }
@@ -963,75 +1006,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // ---- the piece's output
       const bool used = both || cnt > x;     // this tile had a block
       const bool two = !both && cnt > 1;     // A and B hold parts of the same rows
-      if (used && !wait(&bar.o_full[x], n_o++, 13)) break;
+      if (used) {
+        if (!wait(&bar.o_full[x], (ph & kO) != 0, 13)) break;
+        ph ^= kO;
+      }
       tc_fence_after();
+      float wa = 1.0f, wb = 0.0f;
       if (!both && x == 1) {  // B's part goes to A's warps
         if (two) {
-          ml_b[row] = make_float2(M, bad != 0.0f ? -1.0f : l);
+          ml_b[row] = make_float2(M, (flags & kBadPage) ? -1.0f : l);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar.b_ml);
         }
-        continue;
-      }
-      float wa = 1.0f, wb = 0.0f;
-      if (two) {
-        if (!wait(bar.b_ml, n_two++, 14)) break;
-        if (!wait(&bar.o_full[1], n_b, 15)) break;
-        tc_fence_after();
-        const float2 b = ml_b[row];
-        if (b.y < 0.0f) bad = 1.0f;
-        const float Mn = fmaxf(M, b.x);
-        wa = M == -INFINITY ? 0.0f : ex2(M - Mn);
-        wb = b.x == -INFINITY ? 0.0f : ex2(b.x - Mn);
-        l = l * wa + b.y * wb;
-        M = Mn;
-      }
-      if (both || two) ++n_b;
-      const bool whole = s.b_lo == 0 && s.b_hi == s.nb;
-      const float scale = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-      const int slot = 2 * (int)blockIdx.x + (s.b_lo > 0 ? 0 : 1);
-      if (warp_live) {
-        const int g = s.row0 + rr - t * p.G;
-        uint16_t* out = p.out + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tmem_ld32(to + 32 * c, o);
-          if (two) {
-            float ob[32];
-            tmem_ld32(tmem + tmem_o(1) + lanes + 32 * c, ob);
-#pragma unroll
-            // (a part that saw nothing holds zeros times whatever: leave it out)
-            for (int k = 0; k < 32; ++k)
-              o[k] = (wa != 0.0f ? o[k] * wa : 0.0f) + (wb != 0.0f ? ob[k] * wb : 0.0f);
-          }
-          if (live && whole && bad == 0.0f) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint4 y;
-              y.x = pack_p<false>(o[k] * scale, o[k + 1] * scale);
-              y.y = pack_p<false>(o[k + 2] * scale, o[k + 3] * scale);
-              y.z = pack_p<false>(o[k + 4] * scale, o[k + 5] * scale);
-              y.w = pack_p<false>(o[k + 6] * scale, o[k + 7] * scale);
-              *reinterpret_cast<uint4*>(out + 32 * c + k) = l > 0.0f ? y : make_uint4(0, 0, 0, 0);
-            }
-          } else if (live && !whole) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              a.ws.o[((long long)slot * 32 + 8 * c + k / 4) * kItemRows + rr] =
-                  make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          }
-          __syncwarp();  // the next tensor-memory load is the whole warp's
+      } else {
+        if (two) {
+          if (!wait(bar.b_ml, (ph & kMl) != 0, 14)) break;
+          if (!wait(&bar.o_full[1], (ph & kOB) != 0, 15)) break;
+          ph ^= kMl;
+          tc_fence_after();
+          const float2 b = ml_b[row];
+          if (b.y < 0.0f) flags |= kBadPage;
+          const float Mn = fmaxf(M, b.x);
+          wa = M == -INFINITY ? 0.0f : ex2(M - Mn);
+          wb = b.x == -INFINITY ? 0.0f : ex2(b.x - Mn);
+          l = l * wa + b.y * wb;
+          M = Mn;
         }
-        if (live && !whole)
-          a.ws.ml[(long long)slot * kItemRows + rr] = make_float2(M, bad != 0.0f ? -1.0f : l);
+        if (both || two) ph ^= kOB;
+        if (warp_live) {
+          const bool bad = (flags & kBadPage) != 0, live = tile0 + row < rows;
+          const bool whole = pc->b_lo == 0 && pc->b_hi == pc->nb;
+          const float scale = l > 0.0f ? 1.0f / l : 0.0f;
+          const int slot = 2 * (int)blockIdx.x + (pc->b_lo > 0 ? 0 : 1), tg = pc->row0 + tile0 + row;
+          const int t = tg / p.G, g = tg - t * p.G;
+          uint16_t* out = p.out + ((long long)(pc->q0 + t) * p.Hq + pc->h * p.G + g) * kD;
+          float4* part = a.ws.o + (long long)slot * 32 * kItemRows + tile0 + row;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[16];
+            tmem_ld16(to + 16 * c, o);
+            if (two) {
+              float ob[16];
+              tmem_ld16(tmem + tmem_o(1) + lanes + 16 * c, ob);
+              // (a part that saw nothing holds zeros times whatever: leave it out)
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                o[k] = (wa != 0.0f ? o[k] * wa : 0.0f) + (wb != 0.0f ? ob[k] * wb : 0.0f);
+            }
+            if (live && whole && !bad) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 8) {
+                uint4 y;
+                y.x = pack_p<false>(o[k] * scale, o[k + 1] * scale);
+                y.y = pack_p<false>(o[k + 2] * scale, o[k + 3] * scale);
+                y.z = pack_p<false>(o[k + 4] * scale, o[k + 5] * scale);
+                y.w = pack_p<false>(o[k + 6] * scale, o[k + 7] * scale);
+                *reinterpret_cast<uint4*>(out + 16 * c + k) = l > 0.0f ? y : make_uint4(0, 0, 0, 0);
+              }
+            } else if (live && !whole) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4)
+                part[(4 * c + k / 4) * kItemRows] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+            __syncwarp();  // the next tensor-memory load is the whole warp's
+          }
+          if (live && !whole)
+            a.ws.ml[(long long)slot * kItemRows + tile0 + row] = make_float2(M, bad ? -1.0f : l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.epi_done[x]);
+          if (two) mbar_arrive(&bar.epi_done[1]);
+        }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar.epi_done[x]);
-        if (two) mbar_arrive(&bar.epi_done[1]);
-      }
+      if (lane == 0) mbar_arrive(&bar.ring_free[piece % kRing]);
     }
   }
 
