@@ -622,105 +622,87 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // ============================ MMA issuer ============================
     // Task (block u, tile X): S = Q_X K^T.  Just before it, the PV that X still
     // owes (its task before) is issued, so that one tile's softmax always runs
-    // beside the other tile's products.  A PV is never more than one block late,
-    // so that the V ring moves on.
+    // beside the other tile's products.  A tile that sits a block out still issues the
+    // PV that ends its piece (the other tile's output may wait for it) and one that is
+    // two blocks late (the V ring moves on).  This warp's own instructions bound the kernel
+    // where they stand between two tiles' products: per tile they are kept few.
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc(!FP8);
     const uint64_t dq = sw128_desc(smem_u32(smem + OFF_Q), 16, 1024);
     const uint64_t dk = sw128_desc(smem_u32(smem + OFF_K), 16, 1024);
     const uint64_t dv = sw128_desc(smem_u32(smem + OFF_V), 16, 1024);
-    // what each tile owes: its block, and whether that is its first or last of the
-    // piece and whether its PV is the block's last
-    enum { kFirst = 1, kLast = 2, kFrees = 4 };
-    int owed0 = -1, owed1 = -1;
-    int how0 = 0, how1 = 0;
-    uint32_t task0 = 0, task1 = 0, begun0 = 0, begun1 = 0;  // tasks / pieces of each tile
-    int u = 0;
+    // what a tile owes: its block (-1: nothing), and whether that is its first or last
+    // of the piece and whether its PV is the block's last
+    enum { kFirst = 1, kLast = 2, kFrees = 4, kSecond = 8 };
+    int owed[2] = {-1, -1}, how[2] = {0, 0};
+    uint32_t tasks[2] = {0, 0}, begun[2] = {0, 0};  // tasks / pieces of each tile
+    int u = 0, i = 0;                               // block of the CTA / of the piece
     uint32_t piece = 0;
     bool more = next_piece(0);
-    int i = 0, x = 0;  // the next task: block i of the piece, tile x
-    while (go) {
-      // the next step: a PV from two blocks back, the task's PV and S, or, behind the
-      // last task, what is still owed (the older first, tile A before B)
-      const bool late0 = owed0 >= 0 && (!more || owed0 + 1 < u);
-      const bool late1 = owed1 >= 0 && (!more || owed1 + 1 < u);
-      if (!more && !late0 && !late1) break;
-      const bool late = late0 || late1;
-      const int xs = !late ? x : late0 && (!late1 || owed0 <= owed1) ? 0 : 1;
-      const int uo = xs ? owed1 : owed0;
-      const int how = xs ? how1 : how0;
-      const uint32_t task = xs ? task1 : task0, begun = xs ? begun1 : begun0;
-      if (uo >= 0) {  // ---- O += P V
-        const int st = uo & 1;
-        if (!wait(&bar.p_ready[xs], task - 1, 5)) break;
-        if (!wait(&bar.v_ready[st], (uint32_t)(uo >> 1), 6)) break;
-        if ((how & kFirst) && begun > 1 && !wait(&bar.epi_done[xs], begun - 2, 7)) break;
-        tc_fence_after();
-        const uint32_t o = tmem + tmem_o(xs), pa = tmem + tmem_s(xs);
-        const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
-        bool add = !(how & kFirst);
-#pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
+    bool both = s.both();
+    int cnt = s.count();
+    for (;;) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mma_f16_ts_if(leader, o, pa + 32 * j + 8 * k, d + ((j * kHalf + k * 32) >> 4), kId, add);
-            add = true;
+      for (int x = 0; x < 2; ++x) {
+        const bool act = more && (both || x == (i & 1));
+        if (go && owed[x] >= 0 &&
+            (act || !more || (how[x] & kLast) || owed[x] + 1 < u)) {  // ---- O += P V
+          const int st = owed[x] & 1, h = how[x];
+          if (wait(&bar.p_ready[x], tasks[x] - 1, 5) &&
+              ((h & kSecond) || wait(&bar.v_ready[st], (uint32_t)(owed[x] >> 1), 6)) &&
+              (!(h & kFirst) || begun[x] < 2 || wait(&bar.epi_done[x], begun[x] - 2, 7))) {
+            tc_fence_after();
+            const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
+            const bool add = !(h & kFirst);
+#pragma unroll
+            for (int k = 0; k < kBlk / 16; ++k)
+              mma_f16_ts_if(leader, tmem + tmem_o(x), tmem + tmem_s(x) + 8 * k,
+                            d + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kId, add || k > 0);
+            if (leader) {
+              if (h & kFrees) mma_commit(&bar.v_free[st]);
+              if (h & kLast) mma_commit(&bar.o_full[x]);
+            }
+            __syncwarp();
+            owed[x] = -1;
           }
         }
-        if (leader) {
-          if (how & kFrees) mma_commit(&bar.v_free[st]);
-          if (how & kLast) mma_commit(&bar.o_full[xs]);
+        if (go && act) {  // ---- S = Q K^T
+          const int st = u & 1;
+          const bool second = both && x == 1, ends = i == cnt - 1 && (!both || x == 1);
+          if ((i > 0 || x > 0 || wait(bar.q_ready, piece, 8)) &&
+              (second || wait(&bar.k_ready[st], (uint32_t)(u >> 1), 9))) {
+            tc_fence_after();
+            const uint64_t q = dq + (second ? kTileBytes >> 4 : 0);
+            const uint64_t kk = dk + ((uint32_t)(st * kTileBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k) {
+              const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+              mma_f16_if(leader, tmem + tmem_s(x), q + off, kk + off, kId, k > 0);
+            }
+            const bool frees = !both || x == 1;
+            if (leader) {
+              mma_commit(&bar.s_full[x]);
+              mbar_arrive(&bar.s_full[x]);  // what this warp has waited for is seen behind it
+              if (frees) mma_commit(&bar.k_free[st]);
+              if (ends) mma_commit(bar.q_free);
+            }
+            __syncwarp();
+            const bool first = both ? i == 0 : i < 2, last = both ? i == cnt - 1 : i + 2 >= cnt;
+            owed[x] = u;
+            how[x] = (first ? kFirst : 0) | (last ? kLast : 0) | (frees ? kFrees : 0) |
+                     (second ? kSecond : 0);
+            ++tasks[x];
+            begun[x] += first ? 1 : 0;
+          }
         }
-        __syncwarp();
-        if (xs) owed1 = -1; else owed0 = -1;
       }
-      if (late) continue;
-      {  // ---- S = Q K^T
-        const bool both = s.both();
-        const int cnt = s.count(), st = u & 1;
-        if (i == 0 && x == 0 && !wait(bar.q_ready, piece, 8)) break;
-        if (!wait(&bar.k_ready[st], (uint32_t)(u >> 1), 9)) break;
-        tc_fence_after();
-        const uint32_t so = tmem + tmem_s(x);
-        const uint64_t q = dq + ((uint32_t)(both ? x * kTileBytes : 0) >> 4);
-        const uint64_t kk = dk + ((uint32_t)(st * kTileBytes) >> 4);
-        bool add = false;
-#pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t off = (uint32_t)(j * kHalf + k * 32) >> 4;
-            mma_f16_if(leader, so, q + off, kk + off, kId, add);
-            add = true;
-          }
-        }
-        const bool frees = !both || x == 1, ends = frees && i == cnt - 1;
-        if (leader) {
-          mma_commit(&bar.s_full[x]);
-          mbar_arrive(&bar.s_full[x]);  // what this warp has waited for is seen behind it
-          if (frees) mma_commit(&bar.k_free[st]);
-          if (ends) mma_commit(bar.q_free);
-        }
-        __syncwarp();
-        const bool first = both ? i == 0 : i < 2, last = both ? i == cnt - 1 : i + 2 >= cnt;
-        const int h = (first ? kFirst : 0) | (last ? kLast : 0) | (frees ? kFrees : 0);
-        if (x) {
-          owed1 = u, how1 = h, ++task1;
-          if (first) ++begun1;
-        } else {
-          owed0 = u, how0 = h, ++task0;
-          if (first) ++begun0;
-        }
-        if (frees) {
-          ++i, ++u;
-          x = both ? 0 : i & 1;
-          if (ends) {
-            more = next_piece(++piece);
-            i = x = 0;
-          }
-        } else {
-          x = 1;
-        }
+      if (!go || !more) break;
+      ++u;
+      if (++i == cnt) {
+        i = 0;
+        more = next_piece(++piece);
+        both = s.both();
+        cnt = s.count();
       }
     }
     // every operation issued here finishes (bounded) before tensor memory is freed
