@@ -19,11 +19,12 @@
 // partials (o, running max, sum) for the combine kernel, at most two a CTA.
 //
 // Per CTA (one per SM):
-//   softmax A (0-3), B (4-7)  a thread per row: S from tensor memory twice (max,
+//   softmax A (0-3), B (4-7)  a thread per row: S from tensor memory twice (maximum,
 //                   then exp2), P back to tensor memory as the A operand of PV;
 //                   the output accumulator is rescaled only when a row's maximum
-//                   grows by more than 2^8, by the same warp; at an item's end
-//                   the output
+//                   grows by more than 2^8, by the same warp; between two items
+//                   the next item's query rows (f16 by an exact power of two a row,
+//                   or bf16) into shared memory, then the output
 //   converters (8-11)  global pages -> registers -> 128B-swizzled K-major tiles
 //                   in shared memory: K [token][dim] and V [dim][token] (pages
 //                   hold V dim-major: no transpose).  e4m3 codes become f16
@@ -32,9 +33,6 @@
 //                   running while the other tile's softmax does
 //   scheduler (13)  the CTA's pieces, one after the other into a ring that the other
 //                   warps read, their query rows pulled into L2
-//   stagers (14-15) the next item's queries (f16 by an exact power of two a row, or
-//                   bf16) as an image of their tiles in global scratch; one bulk
-//                   copy brings it in once the item before has read its own
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 #include <climits>
 
@@ -50,14 +48,17 @@ constexpr int kD = 128, kP = 16;
 constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
 constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps, kSchedWarp = kMmaWarp + 1;
-constexpr int kStageWarps = 2;  // behind the scheduler
+constexpr int kMmaWarp = kSoftWarps + kConvWarps;  // the scheduler is behind it
 constexpr int kRing = 4;  // pieces in flight from the scheduler
-constexpr int kThreads = (kMmaWarp + 4) * 32;
-// what an item costs beside its blocks (staging the queries, writing the output),
-// in halves of a two-tile block
-constexpr int kItemCost = 4;
-constexpr int kMeta = 4;  // block records in flight, and query exponents of as many pieces
+constexpr int kThreads = (kMmaWarp + 2) * 32;
+// what an item costs beside its blocks (queries in, output out), in halves of a two-tile
+// block (about 1 us each)
+constexpr int kItemCost = 6;
+__host__ __device__ inline long long item_lead(int nrows, int nb) {  // before its first block
+  (void)nrows, (void)nb;
+  return kItemCost;
+}
+constexpr int kMeta = 4;  // block records in flight
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
 constexpr int kHalf = 128 * 128, kTileBytes = 2 * kHalf;
@@ -65,11 +66,10 @@ constexpr int OFF_Q = 0;                          // tiles A, B
 constexpr int OFF_K = OFF_Q + 2 * kTileBytes;     // 2 blocks
 constexpr int OFF_V = OFF_K + 2 * kTileBytes;     // 2 blocks
 constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
-constexpr int OFF_QEXP = OFF_META + kMeta * kBlkPages * 16;  // [kMeta][256] int
-constexpr int OFF_MLB = OFF_QEXP + kMeta * kItemRows * 4;    // [128] float2
+constexpr int OFF_MLB = OFF_META + kMeta * kBlkPages * 16;   // [128] float2
 constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
 constexpr int OFF_BAR = OFF_RING + kRing * 48;
-constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 1 + 2 * kRing;
+constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -96,7 +96,6 @@ struct Ws {
   int4* cut;        // [grid] {item (-1: none), kv head, last CTA, 0}: the cut item a CTA begins
   float2* ml;       // [2 grid][256] (running max, sum; -1: a page that must not be read)
   float4* o;        // [2 grid][32][256]: 4 dims of a row
-  uint8_t* q;       // [grid] images of an item's query tiles
   size_t bytes;
 };
 
@@ -123,7 +122,6 @@ Ws ws_layout(void* base, int B, int G, int total_q, int grid) {
   w.cut = reinterpret_cast<int4*>(take(16 * (size_t)grid));
   w.ml = reinterpret_cast<float2*>(take(8ull * 2 * grid * kItemRows));
   w.o = reinterpret_cast<float4*>(take(4ull * 2 * grid * kItemRows * kD));
-  w.q = take(1ull * grid * 2 * kTileBytes);
   w.bytes = off;
   return w;
 }
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
           it.z = (int)min((long long)kItemRows, n * p.G - row0);
           const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
           it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = kItemCost + (long long)it.w * (it.z > kTile ? 2 : 1);
+          cost = item_lead(it.z, it.w) + (long long)it.w * (it.z > kTile ? 2 : 1);
         }
       }
       a.ws.items[v] = it;
@@ -214,13 +212,17 @@ static_assert(sizeof(Piece) == 48, "ring slots");
 // The scheduler's place on the cost axis.
 struct Walk {
   int v, h;
-  long long x0;  // cost position of (item v, head h); its blocks begin kItemCost behind
+  long long x0;  // cost position of (item v, head h)
   Piece s;
-  __device__ __forceinline__ long long cost() const { return kItemCost + (long long)s.nb * s.w(); }
+  // of its first block, and behind its last
+  __device__ __forceinline__ long long blocks0() const { return x0 + item_lead(s.nrows, s.nb); }
+  __device__ __forceinline__ long long cost() const {
+    return item_lead(s.nrows, s.nb) + (long long)s.nb * s.w();
+  }
 };
 
 __device__ __forceinline__ int block_at(long long x, const Walk& c) {  // first block at or behind x
-  const long long d = x - c.x0 - kItemCost, w = c.s.w();
+  const long long d = x - c.blocks0(), w = c.s.w();
   return d <= 0 ? 0 : (int)min((long long)c.s.nb, (d + w - 1) >> (w - 1));
 }
 
@@ -351,7 +353,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
   uint64_t* meta_ready;                                  // [kMeta]
-  uint64_t *q_ready, *q_free, *q_image;
+  uint64_t *q_ready, *q_free;
   uint64_t *s_full, *p_ready, *o_full, *epi_done;        // [2] (tile)
   uint64_t *b_ml, *drain;
   uint64_t *ring_full, *ring_free;                       // [kRing]
@@ -365,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem[];
   float4* meta = reinterpret_cast<float4*>(smem + OFF_META);
-  int* qexp = reinterpret_cast<int*>(smem + OFF_QEXP);
   float2* ml_b = reinterpret_cast<float2*>(smem + OFF_MLB);
   uint64_t* bp = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   Bars bar;
@@ -374,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   bar.q_ready = bp + 8 + kMeta, bar.q_free = bar.q_ready + 1;
   bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
   bar.epi_done = bar.s_full + 6;
-  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1, bar.q_image = bar.drain + 1;
-  bar.ring_full = bar.q_image + 1, bar.ring_free = bar.ring_full + kRing;
+  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1;
+  bar.ring_full = bar.drain + 1, bar.ring_free = bar.ring_full + kRing;
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -407,14 +408,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       mbar_init(&bar.epi_done[i], 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&bar.meta_ready[i], kConvWarps);
-    mbar_init(bar.q_ready, 1);
-    mbar_init(bar.q_image, kStageWarps);
+    mbar_init(bar.q_ready, kSoftWarps);
     mbar_init(bar.q_free, 1);
     mbar_init(bar.b_ml, 4);
     mbar_init(bar.drain, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ring_full[i], 1);
-      mbar_init(&bar.ring_free[i], kMmaWarp + 1 + kStageWarps);  // every warp that reads it
+      mbar_init(&bar.ring_free[i], kMmaWarp + 1);  // every warp that reads it
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
     }
     __syncwarp();
-   } else if (warp == kSchedWarp) {
+   } else {
     // ============================= scheduler =============================
     Walk c;
     {  // the last item that begins at or before x_begin, 32 entries a step
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         // the item that begins here and is cut by the range's end: for the combine
         if (lane == 0 && c.s.b_lo == 0 && c.s.b_hi < c.s.nb)
           a.ws.cut[blockIdx.x] = make_int4(
-              c.v, c.h, (int)((c.x0 + kItemCost + (long long)c.s.w() * (c.s.nb - 1)) / per), 0);
+              c.v, c.h, (int)((c.blocks0() + (long long)c.s.w() * (c.s.nb - 1)) / per), 0);
         if (piece >= kRing && !wait(&bar.ring_free[piece % kRing], piece / kRing - 1, 10)) break;
         if (lane == 0) {
           ring[piece % kRing] = c.s;
@@ -768,77 +768,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         }
       }
     }
-   } else {
-    // ============================== stagers ==============================
-    const int sw = warp - kSchedWarp - 1, c = lane & 15;  // 16 lanes a row, 8 dims each
-    const bool flip = p.sm_scale_log2 < 0.0f;  // a negative scale turns the queries' sign
-    uint8_t* img = a.ws.q + 2ll * blockIdx.x * kTileBytes;
-    uint32_t copies = 0;
-    for (uint32_t piece = 0; next_piece(piece); ++piece) {
-      // the copy of the piece before has read the image
-      if (piece > 0 && !wait(bar.q_ready, piece - 1, 2)) break;
-      const int rows = s.both() ? kItemRows : kTile;
-      constexpr int kGo = 4;  // rows of a half-warp in flight
-#pragma unroll 1
-      for (int i0 = 0; i0 < rows; i0 += 2 * kStageWarps * kGo) {
-        uint4 y[kGo];
-#pragma unroll
-        for (int i = 0; i < kGo; ++i) {
-          const int row = i0 + 2 * (i * kStageWarps + sw) + (lane >> 4);
-          y[i] = make_uint4(0, 0, 0, 0);
-          if (row < s.nrows) {
-            const int tg = s.row0 + row, t = tg / p.G, g = tg - t * p.G;
-            y[i] = *reinterpret_cast<const uint4*>(
-                p.q + ((long long)(s.q0 + t) * p.Hq + s.h * p.G + g) * kD + 8 * c);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kGo; ++i) {
-          const int row = i0 + 2 * (i * kStageWarps + sw) + (lane >> 4);
-          if (flip) {
-            y[i].x ^= 0x80008000u;
-            y[i].y ^= 0x80008000u;
-            y[i].z ^= 0x80008000u;
-            y[i].w ^= 0x80008000u;
-          }
-          if (FP8) {
-            uint32_t mb = absbits_max8(0, y[i]);
-            mb = max(mb & 0xFFFFu, mb >> 16);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-            const int e = q_row_exp(mb);
-            const float pw = pow2f(e);
-            y[i].x = bf16x2_to_f16x2_scaled(y[i].x, pw);
-            y[i].y = bf16x2_to_f16x2_scaled(y[i].y, pw);
-            y[i].z = bf16x2_to_f16x2_scaled(y[i].z, pw);
-            y[i].w = bf16x2_to_f16x2_scaled(y[i].w, pw);
-            if (c == 0) qexp[(piece & (kMeta - 1)) * kItemRows + row] = e;
-          }
-          *reinterpret_cast<uint4*>(img + (row >> 7) * kTileBytes + (c >> 3) * kHalf +
-                                    swz(row & 127, c & 7)) = y[i];
-        }
-      }
-      // the image is read by a bulk copy: written through the generic proxy, so fenced
-      asm volatile("fence.proxy.async;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.q_image);
-      if (sw == 0) {
-        if (!wait(bar.q_image, piece, 16)) break;
-        if (piece > 0 && !wait(bar.q_free, piece - 1, 2)) break;
-        if (lane == 0) {
-          asm volatile("fence.proxy.async;" ::: "memory");
-          const uint32_t bytes = (uint32_t)((rows / kTile) * kTileBytes);
-          mbar_arrive_expect_tx(bar.q_ready, bytes);
-          bulk_g2s(smem + OFF_Q, img, bytes, bar.q_ready, l2_evict_first_policy());
-        }
-        ++copies;
-      }
-    }
-    if (!go && copies > 0) {  // a copy in flight ends (bounded) before the CTA does
-      const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(bar.q_ready, (copies - 1) & 1u) && global_ns() - t0 < 100000000ull) {
-      }
-    }
    }
   } else {
     // ============================== softmax ==============================
@@ -851,10 +780,75 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // phases of the barriers that this warp waits for, a bit each
     enum { kS = 1, kO = 2, kMl = 4, kOB = 8 };
     uint32_t u = 0, ph = 0;
+    float next_qsc = 0.0f;
+    // This thread's query row of piece k (-1: there is none) into the item's tile, and
+    // the factor of its scores.  The two tiles' threads of an item with one tile hold the
+    // same rows and store a half each.
+    auto stage = [&](uint32_t k) {
+      if (!wait(&bar.ring_full[k % kRing], k / kRing, 1)) return false;
+      const volatile Piece* pc = ring + k % kRing;
+      if (!pc->valid) return true;
+      const int rows = pc->nrows, at = (rows > kTile ? x * kTile : 0) + row;
+      const bool both = rows > kTile, live = at < rows;
+      const bool any = __any_sync(0xffffffffu, live);
+      const uint4* src = nullptr;
+      float pw = 1.0f;
+      if (any) {
+        const int tg = pc->row0 + min(at, rows - 1), t = tg / p.G, g = tg - t * p.G;
+        src = reinterpret_cast<const uint4*>(
+            p.q + ((long long)(pc->q0 + t) * p.Hq + pc->h * p.G + g) * kD);
+        next_qsc = fabsf(p.sm_scale_log2);
+        if (FP8) {
+          uint32_t mb = 0;
+#pragma unroll 1
+          for (int c = 0; c < 16; c += 8) {
+            uint4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __ldg(src + c + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mb = absbits_max8(mb, y[i]);
+          }
+          const int e = q_row_exp(max(mb & 0xFFFFu, mb >> 16));
+          pw = pow2f(e);
+          next_qsc *= pow2f(-e);
+        }
+      }
+      // every product of the piece before has read the tiles
+      if (k > 0 && !wait(bar.q_free, k - 1, 2)) return false;
+      if (any) {
+        const uint32_t flip = p.sm_scale_log2 < 0.0f ? 0x80008000u : 0u;  // the scale's sign
+        uint8_t* dst = smem + OFF_Q + (both ? x * kTileBytes : 0);
+#pragma unroll 1
+        for (int j = both ? 0 : x; j < (both ? 2 : x + 1); ++j) {
+          uint4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = __ldg(src + 8 * j + i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint4 w = y[i];
+            w.x ^= flip;
+            w.y ^= flip;
+            w.z ^= flip;
+            w.w ^= flip;
+            if (FP8) {
+              w.x = bf16x2_to_f16x2_scaled(w.x, pw);
+              w.y = bf16x2_to_f16x2_scaled(w.y, pw);
+              w.z = bf16x2_to_f16x2_scaled(w.z, pw);
+              w.w = bf16x2_to_f16x2_scaled(w.w, pw);
+            }
+            *reinterpret_cast<uint4*>(dst + j * kHalf + swz(row, i)) = w;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar.q_ready);
+      return true;
+    };
+    stage(0);
     for (uint32_t piece = 0;; ++piece) {
-      if (!wait(&bar.ring_full[piece % kRing], piece / kRing, 1)) break;
-      const volatile Piece* pc = ring + piece % kRing;
-      if (!pc->valid) break;
+      const volatile Piece* pc = ring + piece % kRing;  // (stage has waited for it)
+      if (!go || !pc->valid) break;
       const int rows = pc->nrows, cnt = pc->b_hi - pc->b_lo;
       const bool both = rows > kTile;
       const int tile0 = both ? x * kTile : 0;  // the tile's first row in the item
@@ -864,7 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       const int seen0 = pc->L - pc->n - pc->b_lo * kBlk;
       int lim = seen0 + (pc->row0 + min(tile0 + row, rows - 1)) / p.G;
       int lim_all = seen0 + (pc->row0 + tile0) / p.G;
-      float qsc = fabsf(p.sm_scale_log2), M = -INFINITY, l = 0.0f;
+      const float qsc = next_qsc;
+      float M = -INFINITY, l = 0.0f;
       uint32_t flags = 0;
       bool first = true;
       for (int i = 0; i < cnt && go; ++i, ++u, lim -= kBlk, lim_all -= kBlk) {
@@ -874,7 +869,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (!wait(&bar.meta_ready[ms], u / kMeta, 12)) break;
         ph ^= kS;
         tc_fence_after();
-        if (FP8 && first) qsc *= pow2f(-qexp[(piece & (kMeta - 1)) * kItemRows + tile0 + row]);
         const float4* mt = meta + ms * kBlkPages;
         if (warp_live) {
           const uint32_t fl = __float_as_uint(mt[0].w);
@@ -985,6 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (lane == 0) mbar_arrive(&bar.p_ready[x]);
       }
       if (!go) break;
+      if (!stage(piece + 1)) break;
       // ---- the piece's output
       const bool used = both || cnt > x;     // this tile had a block
       const bool two = !both && cnt > 1;     // A and B hold parts of the same rows
