@@ -69,7 +69,7 @@ constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
 constexpr int OFF_MLB = OFF_META + kMeta * kBlkPages * 16;   // [128] float2
 constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
 constexpr int OFF_BAR = OFF_RING + kRing * 48;
-constexpr int kBars = 2 * 4 + kMeta + 2 + 2 * 4 + 1 + 1 + 2 * kRing;
+constexpr int kBars = 2 * 4 + 2 + 2 * 5 + 1 + 1 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -295,7 +295,7 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) 
 }
 // ... landed: no use of v comes before this
 __device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;");
   asm volatile(""
       : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
         "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
@@ -352,9 +352,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
 
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
-  uint64_t* meta_ready;                                  // [kMeta]
   uint64_t *q_ready, *q_free;
-  uint64_t *s_full, *p_ready, *o_full, *epi_done;        // [2] (tile)
+  uint64_t *s_full, *p_half, *p_ready, *o_full, *epi_done;  // [2] (tile)
   uint64_t *b_ml, *drain;
   uint64_t *ring_full, *ring_free;                       // [kRing]
 };
@@ -371,11 +370,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   uint64_t* bp = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   Bars bar;
   bar.k_ready = bp, bar.k_free = bp + 2, bar.v_ready = bp + 4, bar.v_free = bp + 6;
-  bar.meta_ready = bp + 8;
-  bar.q_ready = bp + 8 + kMeta, bar.q_free = bar.q_ready + 1;
+  bar.q_ready = bp + 8, bar.q_free = bar.q_ready + 1;
   bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
   bar.epi_done = bar.s_full + 6;
-  bar.b_ml = bar.s_full + 8, bar.drain = bar.b_ml + 1;
+  bar.p_half = bar.s_full + 8;
+  bar.b_ml = bar.p_half + 2, bar.drain = bar.b_ml + 1;
   bar.ring_full = bar.drain + 1, bar.ring_free = bar.ring_full + kRing;
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -403,11 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       mbar_init(&bar.v_ready[i], kConvWarps);
       mbar_init(&bar.v_free[i], 1);
       mbar_init(&bar.s_full[i], 2);  // the products' end, and the issuing warp itself
+      mbar_init(&bar.p_half[i], 4);
       mbar_init(&bar.p_ready[i], 4);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.epi_done[i], 4);
     }
-    for (int i = 0; i < kMeta; ++i) mbar_init(&bar.meta_ready[i], kConvWarps);
     mbar_init(bar.q_ready, kSoftWarps);
     mbar_init(bar.q_free, 1);
     mbar_init(bar.b_ml, 4);
@@ -592,10 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.k_ready[st]);
-          mbar_arrive(&bar.meta_ready[ms]);
-        }
+        if (lane == 0) mbar_arrive(&bar.k_ready[st]);
         // V
         if (u >= 2 && !wait(&bar.v_free[st], free_phase, 4)) break;
         uint8_t* vd = smem + OFF_V + st * kTileBytes;
@@ -648,16 +644,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (go && owed[x] >= 0 &&
             (act || !more || (how[x] & kLast) || owed[x] + 1 < u)) {  // ---- O += P V
           const int st = owed[x] & 1, h = how[x];
-          if (wait(&bar.p_ready[x], tasks[x] - 1, 5) &&
+          if (wait(&bar.p_half[x], tasks[x] - 1, 5) &&
               ((h & kSecond) || wait(&bar.v_ready[st], (uint32_t)(owed[x] >> 1), 6)) &&
               (!(h & kFirst) || begun[x] < 2 || wait(&bar.epi_done[x], begun[x] - 2, 7))) {
             tc_fence_after();
             const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
             const bool add = !(h & kFirst);
 #pragma unroll
-            for (int k = 0; k < kBlk / 16; ++k)
+            for (int k = 0; k < kBlk / 16; ++k) {
+              if (k == kBlk / 32) {  // the second half of P
+                wait(&bar.p_ready[x], tasks[x] - 1, 12);
+                tc_fence_after();
+              }
               mma_f16_ts_if(leader, tmem + tmem_o(x), tmem + tmem_s(x) + 8 * k,
                             d + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kId, add || k > 0);
+            }
             if (leader) {
               if (h & kFrees) mma_commit(&bar.v_free[st]);
               if (h & kLast) mma_commit(&bar.o_full[x]);
@@ -866,7 +867,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (!both && (i & 1) != x) continue;
         const uint32_t ms = u & (kMeta - 1);
         if (!wait(&bar.s_full[x], ph & kS, 11)) break;
-        if (!wait(&bar.meta_ready[ms], u / kMeta, 12)) break;
         ph ^= kS;
         tc_fence_after();
         const float4* mt = meta + ms * kBlkPages;
@@ -970,8 +970,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             tmem_ld32_async(ts + 64, va);
             exp32(vb, mt + 4 * c + 2, ts + 32 * c + 16);
             tmem_wait_ld(va);
+            if (c == 0) {  // half of the keys: their products may start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar.p_half[x]);
+            }
           }
           tmem_wait_st();
+        } else {
+          if (lane == 0) mbar_arrive(&bar.p_half[x]);
         }
         first = false;
         tc_fence_before();
