@@ -10,28 +10,28 @@
 //
 // Work decomposition.  A request's query rows of one kv head are row = t * G + g
 // (token, head of the group); 256 of them are an item's two tiles of 128 rows
-// (A and B).  An item with at most 128 rows has one tile, and then A and B are
-// the same rows over alternate key blocks, merged when the item ends.  A block is
-// 128 tokens (8 pages).  Items are laid out request-major, a block costing 2 (two
+// (A and B).  A block is 128 tokens (8 pages), a unit half of one.  An item with at
+// most 128 rows has one tile, and then A and B are the same rows over the two halves of
+// each block, merged when the item ends.  Items are laid out request-major, a block costing 2 (two
 // tiles) or 1, and the whole batch is cut into equal ranges, one per persistent
 // CTA: every CTA works equally long whatever the lengths.  A CTA writes an item
 // that lies wholly in its range; an item cut by a range's end leaves fp32
 // partials (o, running max, sum) for the combine kernel, at most two a CTA.
 //
 // Per CTA (one per SM):
-//   softmax A (0-3), B (4-7)  a thread per row: S from tensor memory twice (maximum,
-//                   then exp2), P back to tensor memory as the A operand of PV;
-//                   the output accumulator is rescaled only when a row's maximum
-//                   grows by more than 2^8, by the same warp; between two items
+//   softmax A (0-3), B (4-7)  a thread per row: a unit's 64 scores from tensor memory
+//                   into registers, maximum, exp2, P back to tensor memory as the A
+//                   operand of PV; the output accumulator is rescaled only when a row's
+//                   maximum grows by more than 2^8, by the same warp; between two items
 //                   the next item's query rows (f16 by an exact power of two a row,
 //                   or bf16) into shared memory, then the output
 //   converters (8-11)  global pages -> registers -> 128B-swizzled K-major tiles
 //                   in shared memory: K [token][dim] and V [dim][token] (pages
 //                   hold V dim-major: no transpose).  e4m3 codes become f16
 //                   exactly, bf16 is copied
-//   MMA (12)        S = Q K^T and O += P V (M = N = 128), one tile's products
-//                   running while the other tile's softmax does
-//   scheduler (13)  the CTA's pieces, one after the other into a ring that the other
+//   MMA A (12), B (13)  S = Q K^T (M 128, N 64) a unit ahead of O += P V (M = N = 128),
+//                   so that a tile's softmax finds its next scores when it has stored P
+//   scheduler (14)  the CTA's pieces, one after the other into a ring that the other
 //                   warps read, their query rows pulled into L2
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 #include <climits>
@@ -47,10 +47,11 @@ namespace {
 constexpr int kD = 128, kP = 16;
 constexpr int kTile = 128, kItemRows = 2 * kTile;  // query rows
 constexpr int kBlk = 128, kBlkPages = kBlk / kP;   // tokens / pages of a key block
+constexpr int kUnit = kBlk / 2, kUnitPages = kUnit / kP;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;  // the scheduler is behind it
 constexpr int kRing = 4;  // pieces in flight from the scheduler
-constexpr int kThreads = (kMmaWarp + 2) * 32;
+constexpr int kThreads = (kMmaWarp + 3) * 32;
 // what an item costs beside its blocks (queries in, output out), in halves of a two-tile
 // block (about 1 us each)
 constexpr int kItemCost = 6;
@@ -69,20 +70,18 @@ constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
 constexpr int OFF_MLB = OFF_META + kMeta * kBlkPages * 16;   // [128] float2
 constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
 constexpr int OFF_BAR = OFF_RING + kRing * 48;
-constexpr int kBars = 2 * 4 + 2 + 2 * 5 + 1 + 1 + 2 * kRing;
+constexpr int kBars = 8 + 2 + 8 + 6 + 3 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
-// tensor memory columns: S (and P, in its first 64 columns) and O of each tile
+// tensor memory columns: two S of 64 (P in the first half of each) and O of each tile
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t tmem_s(int x) { return 128u * x; }
 __device__ __forceinline__ uint32_t tmem_o(int x) { return 256u + 128u * x; }
 
-// kind::f16 instruction descriptor: f32 accumulate, both operands K-major
-constexpr uint32_t idesc(bool bf16) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((128u >> 3) << 17) |
-         ((128u >> 4) << 24);
+// kind::f16 instruction descriptor: M 128, f32 accumulate, both operands K-major
+constexpr uint32_t idesc(bool bf16, uint32_t n) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // flags of a key block, kept beside its scales
@@ -281,26 +280,26 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
 }
-// 32 columns of this warp's lanes, not waited for
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
+// 64 columns of this warp's lanes
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
         "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-// ... landed: no use of v comes before this
-__device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;");
-  asm volatile(""
-      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-        "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-        "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-        "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr), "r"(taddr + 32)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
@@ -350,10 +349,46 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
+// The K steps of one product in one piece of code, so that the predicates are set once
+// and descriptors differ by constants (16-byte units; the second 64-wide half of a tile
+// begins kHalf bytes behind the first).  ss4 / ts4: four steps of a half, the first
+// accumulating iff `add`.
+__device__ __forceinline__ void mma_ss4(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                        uint32_t id, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts4(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
+                                        uint32_t id, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 a;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.ne.b32 p, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.s32 a, %1, 8;\n add.s64 b, %2, 2;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 16;\n add.s64 b, %2, 4;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.s32 a, %1, 24;\n add.s64 b, %2, 6;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(add), "r"(leader)
+      : "memory");
+}
+
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
   uint64_t *q_ready, *q_free;
-  uint64_t *s_full, *p_half, *p_ready, *o_full, *epi_done;  // [2] (tile)
+  uint64_t *s_full, *p_ready;                            // [tile][S buffer]
+  uint64_t *pv_done, *o_full, *epi_done;                 // [tile]
   uint64_t *b_ml, *drain;
   uint64_t *ring_full, *ring_free;                       // [kRing]
 };
@@ -371,11 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   Bars bar;
   bar.k_ready = bp, bar.k_free = bp + 2, bar.v_ready = bp + 4, bar.v_free = bp + 6;
   bar.q_ready = bp + 8, bar.q_free = bar.q_ready + 1;
-  bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 2, bar.o_full = bar.s_full + 4,
-  bar.epi_done = bar.s_full + 6;
-  bar.p_half = bar.s_full + 8;
-  bar.b_ml = bar.p_half + 2, bar.drain = bar.b_ml + 1;
-  bar.ring_full = bar.drain + 1, bar.ring_free = bar.ring_full + kRing;
+  bar.s_full = bar.q_free + 1, bar.p_ready = bar.s_full + 4, bar.pv_done = bar.s_full + 8;
+  bar.o_full = bar.pv_done + 2, bar.epi_done = bar.o_full + 2;
+  bar.b_ml = bar.epi_done + 2, bar.drain = bar.b_ml + 1;
+  bar.ring_full = bar.drain + 2, bar.ring_free = bar.ring_full + kRing;
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -398,22 +432,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   } else if (threadIdx.x == 64) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_ready[i], kConvWarps);
-      mbar_init(&bar.k_free[i], 1);
+      mbar_init(&bar.k_free[i], 2);  // (both tiles')
       mbar_init(&bar.v_ready[i], kConvWarps);
-      mbar_init(&bar.v_free[i], 1);
-      mbar_init(&bar.s_full[i], 2);  // the products' end, and the issuing warp itself
-      mbar_init(&bar.p_half[i], 4);
-      mbar_init(&bar.p_ready[i], 4);
+      mbar_init(&bar.v_free[i], 2);
+      mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.epi_done[i], 4);
     }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.s_full[i], 2);  // the products' end, and the issuing warp itself
+      mbar_init(&bar.p_ready[i], 4);
+    }
     mbar_init(bar.q_ready, kSoftWarps);
-    mbar_init(bar.q_free, 1);
+    mbar_init(bar.q_free, 2);
     mbar_init(bar.b_ml, 4);
-    mbar_init(bar.drain, 1);
+    mbar_init(&bar.drain[0], 1);
+    mbar_init(&bar.drain[1], 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ring_full[i], 1);
-      mbar_init(&bar.ring_free[i], kMmaWarp + 1);  // every warp that reads it
+      mbar_init(&bar.ring_free[i], kMmaWarp + 2);  // every warp that reads it
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -614,103 +651,73 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       }
     }
   } else if (warp >= kMmaWarp) {
-   if (warp == kMmaWarp) {
+   if (warp < kMmaWarp + 2) {
     // ============================ MMA issuer ============================
-    // Task (block u, tile X): S = Q_X K^T.  Just before it, the PV that X still
-    // owes (its task before) is issued, so that one tile's softmax always runs
-    // beside the other tile's products.  A tile that sits a block out still issues the
-    // PV that ends its piece (the other tile's output may wait for it) and one that is
-    // two blocks late (the V ring moves on).  This warp's own instructions bound the kernel
-    // where they stand between two tiles' products: per tile they are kept few.
+    // One warp a tile.  Its units of a piece: n = 0, 1, ..; in an item of two tiles every
+    // half block, in one of a single tile its own half of each block.  S of unit n + 1 is
+    // issued before PV of unit n, so the tensor cores have work while P is awaited.
+    const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     const uint32_t leader = elect_one();
-    constexpr uint32_t kId = idesc(!FP8);
+    // (a broadcast marks a value as the warp's own: the products take theirs from uniform
+    // registers)
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint32_t kIdS = idesc(!FP8, kUnit), kIdPv = idesc(!FP8, kD);
     const uint64_t dq = sw128_desc(smem_u32(smem + OFF_Q), 16, 1024);
     const uint64_t dk = sw128_desc(smem_u32(smem + OFF_K), 16, 1024);
     const uint64_t dv = sw128_desc(smem_u32(smem + OFF_V), 16, 1024);
-    // what a tile owes: its block (-1: nothing), and whether that is its first or last
-    // of the piece and whether its PV is the block's last
-    enum { kFirst = 1, kLast = 2, kFrees = 4, kSecond = 8 };
-    int owed[2] = {-1, -1}, how[2] = {0, 0};
-    uint32_t tasks[2] = {0, 0}, begun[2] = {0, 0};  // tasks / pieces of each tile
-    int u = 0, i = 0;                               // block of the CTA / of the piece
-    uint32_t piece = 0;
-    bool more = next_piece(0);
-    bool both = s.both();
-    int cnt = s.count();
-    for (;;) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool act = more && (both || x == (i & 1));
-        if (go && owed[x] >= 0 &&
-            (act || !more || (how[x] & kLast) || owed[x] + 1 < u)) {  // ---- O += P V
-          const int st = owed[x] & 1, h = how[x];
-          if (wait(&bar.p_half[x], tasks[x] - 1, 5) &&
-              ((h & kSecond) || wait(&bar.v_ready[st], (uint32_t)(owed[x] >> 1), 6)) &&
-              (!(h & kFirst) || begun[x] < 2 || wait(&bar.epi_done[x], begun[x] - 2, 7))) {
-            tc_fence_after();
-            const uint64_t d = dv + ((uint32_t)(st * kTileBytes) >> 4);
-            const bool add = !(h & kFirst);
-#pragma unroll
-            for (int k = 0; k < kBlk / 16; ++k) {
-              if (k == kBlk / 32) {  // the second half of P
-                wait(&bar.p_ready[x], tasks[x] - 1, 12);
-                tc_fence_after();
-              }
-              mma_f16_ts_if(leader, tmem + tmem_o(x), tmem + tmem_s(x) + 8 * k,
-                            d + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kId, add || k > 0);
-            }
-            if (leader) {
-              if (h & kFrees) mma_commit(&bar.v_free[st]);
-              if (h & kLast) mma_commit(&bar.o_full[x]);
-            }
-            __syncwarp();
-            owed[x] = -1;
+    int u0 = 0;               // the CTA's block at the piece's begin
+    uint32_t t0 = 0;          // the tile's units before the piece
+    for (uint32_t piece = 0; next_piece(piece); ++piece) {
+      const bool both = s.both();
+      const int cnt = s.count(), units = both ? 2 * cnt : cnt;
+      const uint64_t q = dq + (uint32_t)((both ? x * kTileBytes : 0) >> 4);
+      if (!wait(bar.q_ready, piece, 8)) break;
+#pragma unroll 1
+      for (int n = -1; n < units && go; ++n) {
+        if (n + 1 < units) {  // ---- S of unit n + 1
+          const int m = n + 1, u = u0 + (both ? m >> 1 : m), h = both ? m & 1 : x;
+          const int st = __shfl_sync(0xffffffffu, u & 1, 0);
+          const uint32_t b = __shfl_sync(0xffffffffu, 2 * x + ((t0 + m) & 1), 0);
+          if ((h == 0 || !both) && !wait(&bar.k_ready[st], (uint32_t)(u >> 1), 9)) break;
+          tc_fence_after();
+          const uint64_t kk = dk + (uint32_t)((st * kTileBytes + h * (kHalf / 2)) >> 4);
+          mma_ss4(leader, tm + 64 * b, q, kk, kIdS, 0);
+          mma_ss4(leader, tm + 64 * b, q + (kHalf >> 4), kk + (kHalf >> 4), kIdS, 1);
+          if (leader) {
+            mma_commit(&bar.s_full[b]);
+            mbar_arrive(&bar.s_full[b]);  // what this warp has waited for is seen behind it
+            if (h == 1 || !both) mma_commit(&bar.k_free[st]);
+            if (m == units - 1) mma_commit(bar.q_free);
           }
+          __syncwarp();
         }
-        if (go && act) {  // ---- S = Q K^T
-          const int st = u & 1;
-          const bool second = both && x == 1, ends = i == cnt - 1 && (!both || x == 1);
-          if ((i > 0 || x > 0 || wait(bar.q_ready, piece, 8)) &&
-              (second || wait(&bar.k_ready[st], (uint32_t)(u >> 1), 9))) {
-            tc_fence_after();
-            const uint64_t q = dq + (second ? kTileBytes >> 4 : 0);
-            const uint64_t kk = dk + ((uint32_t)(st * kTileBytes) >> 4);
-#pragma unroll
-            for (int k = 0; k < kD / 16; ++k) {
-              const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              mma_f16_if(leader, tmem + tmem_s(x), q + off, kk + off, kId, k > 0);
-            }
-            const bool frees = !both || x == 1;
-            if (leader) {
-              mma_commit(&bar.s_full[x]);
-              mbar_arrive(&bar.s_full[x]);  // what this warp has waited for is seen behind it
-              if (frees) mma_commit(&bar.k_free[st]);
-              if (ends) mma_commit(bar.q_free);
-            }
-            __syncwarp();
-            const bool first = both ? i == 0 : i < 2, last = both ? i == cnt - 1 : i + 2 >= cnt;
-            owed[x] = u;
-            how[x] = (first ? kFirst : 0) | (last ? kLast : 0) | (frees ? kFrees : 0) |
-                     (second ? kSecond : 0);
-            ++tasks[x];
-            begun[x] += first ? 1 : 0;
+        if (n >= 0) {  // ---- O += P V of unit n
+          const int u = u0 + (both ? n >> 1 : n), h = both ? n & 1 : x;
+          const int st = __shfl_sync(0xffffffffu, u & 1, 0);
+          const uint32_t b = __shfl_sync(0xffffffffu, 2 * x + ((t0 + n) & 1), 0);
+          if ((h == 0 || !both) && !wait(&bar.v_ready[st], (uint32_t)(u >> 1), 6)) break;
+          if (n == 0 && piece > 0 && !wait(&bar.epi_done[x], piece - 1, 7)) break;
+          if (!wait(&bar.p_ready[b], (t0 + n) >> 1, 5)) break;
+          tc_fence_after();
+          mma_ts4(leader, tm + tmem_o(x), tm + 64 * b,
+                  dv + (uint32_t)((st * kTileBytes + h * kHalf) >> 4), kIdPv, n > 0 ? 1 : 0);
+          if (leader) {
+            mma_commit(&bar.pv_done[x]);
+            if (h == 1 || !both) mma_commit(&bar.v_free[st]);
+            if (n == units - 1) mma_commit(&bar.o_full[x]);
           }
+          __syncwarp();
         }
       }
-      if (!go || !more) break;
-      ++u;
-      if (++i == cnt) {
-        i = 0;
-        more = next_piece(++piece);
-        both = s.both();
-        cnt = s.count();
-      }
+      if (!go) break;
+      u0 += cnt;
+      t0 += units;
     }
     // every operation issued here finishes (bounded) before tensor memory is freed
     if (leader) {
-      mma_commit(bar.drain);
+      mma_commit(&bar.drain[x]);
       const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(bar.drain, 0) && global_ns() - t0 < 100000000ull) {
+      while (!mbar_try_wait(&bar.drain[x], 0) && global_ns() - t0 < 100000000ull) {
       }
     }
     __syncwarp();
@@ -777,10 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // whatever the scales; the row sum takes the bias back out.
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + tmem_s(x) + lanes, to = tmem + tmem_o(x) + lanes;
+    const uint32_t to = tmem + tmem_o(x) + lanes;
     // phases of the barriers that this warp waits for, a bit each
-    enum { kS = 1, kO = 2, kMl = 4, kOB = 8 };
-    uint32_t u = 0, ph = 0;
+    enum { kO = 2, kMl = 4, kOB = 8 };
+    uint32_t u0 = 0, t = 0, ph = 0;  // the CTA's block at the piece's begin; units so far
     float next_qsc = 0.0f;
     // This thread's query row of piece k (-1: there is none) into the item's tile, and
     // the factor of its scores.  The two tiles' threads of an item with one tile hold the
@@ -857,60 +864,45 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // last positions that this row and the tile's first row see, from the piece's first
       // key block on
       const int seen0 = pc->L - pc->n - pc->b_lo * kBlk;
-      int lim = seen0 + (pc->row0 + min(tile0 + row, rows - 1)) / p.G;
-      int lim_all = seen0 + (pc->row0 + tile0) / p.G;
+      const int lim = seen0 + (pc->row0 + min(tile0 + row, rows - 1)) / p.G;
+      const int lim_all = seen0 + (pc->row0 + tile0) / p.G;
       const float qsc = next_qsc;
       float M = -INFINITY, l = 0.0f;
       uint32_t flags = 0;
-      bool first = true;
-      for (int i = 0; i < cnt && go; ++i, ++u, lim -= kBlk, lim_all -= kBlk) {
-        if (!both && (i & 1) != x) continue;
-        const uint32_t ms = u & (kMeta - 1);
-        if (!wait(&bar.s_full[x], ph & kS, 11)) break;
-        ph ^= kS;
+      const int units = both ? 2 * cnt : cnt;
+#pragma unroll 1
+      for (int n = 0; n < units; ++n, ++t) {
+        const int i = both ? n >> 1 : n, h = both ? n & 1 : x;  // block of the piece, its half
+        const int b = 2 * x + (t & 1);
+        if (!wait(&bar.s_full[b], t >> 1, 11)) break;
         tc_fence_after();
-        const float4* mt = meta + ms * kBlkPages;
+        const float4* mt = meta + ((u0 + i) & (kMeta - 1)) * kBlkPages + kUnitPages * h;
+        const uint32_t ts = tmem + 64 * b + lanes;
         if (warp_live) {
           const uint32_t fl = __float_as_uint(mt[0].w);
           flags |= fl;
-          float va[32], vb[32];  // 32 columns of this row of S, by turns
-          if (lim_all < kBlk - 1) {  // columns <= lim are visible: the others to -inf
-#pragma unroll 1
-            for (int c = 0; c < kBlk; c += 32) {
-              tmem_ld32_async(ts + c, va);
-              tmem_wait_ld(va);
+          const int col0 = i * kBlk + h * kUnit;
+          float v[64];  // this row of S
+          tmem_ld64(ts, v);
+          if (lim_all < col0 + kUnit - 1) {  // columns <= lim are visible: the others to -inf
+            const int c = lim - col0;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) va[k] = c + k <= lim ? va[k] : -INFINITY;
-              tmem_st32(ts + c, va);
-            }
+            for (int k = 0; k < kUnit; ++k) v[k] = k <= c ? v[k] : -INFINITY;
           }
           // the maximum (a scale of 0 would make a masked score NaN)
           float mx = -INFINITY;
-          auto max32 = [&](const float (&v)[32], const float4* m2) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float* w = &v[16 * g];
-              float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
+          for (int g = 0; g < kUnitPages; ++g) {
+            const float* w = &v[16 * g];
+            float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
 #pragma unroll
-              for (int k = 4; k < 16; k += 4) {
-                pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
-                pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
-              }
-              pm = fmaxf(pm, pn);
-              mx = FP8 ? fmaxf(mx, __fmaf_rn(pm, fmaxf(m2[g].x * qsc, 1e-37f), m2[g].y))
-                       : fmaxf(mx, pm);
+            for (int k = 4; k < 16; k += 4) {
+              pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
+              pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
             }
-          };
-          tmem_ld32_async(ts, va);
-          tmem_wait_ld(va);
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld32_async(ts + 64 * c + 32, vb);
-            max32(va, mt + 4 * c);
-            tmem_wait_ld(vb);
-            tmem_ld32_async(ts + 64 * (1 - c), va);  // (at last the first ones again)
-            max32(vb, mt + 4 * c + 2);
-            tmem_wait_ld(va);
+            pm = fmaxf(pm, pn);
+            mx = FP8 ? fmaxf(mx, __fmaf_rn(pm, fmaxf(mt[g].x * qsc, 1e-37f), mt[g].y))
+                     : fmaxf(mx, pm);
           }
           if (!FP8) mx *= fmaxf(qsc, 1e-37f);
           float alpha = 1.0f;
@@ -919,8 +911,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             l *= alpha;
             M = mx;
           }
-          if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            // PV of the block before was issued ahead of this S: it is complete
+          if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            if (!wait(&bar.pv_done[x], t - 1, 12)) break;  // PV of the unit before
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kD; c += 16) tmem_scale16(to + c, alpha);
           }
@@ -930,27 +923,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           // taken of the weights themselves (and its pages' factors below are 0)
           if (FP8 && (fl & kWide)) {
 #pragma unroll 1
-            for (int c = 0; c < kBlkPages; ++c) {
+            for (int c = 0; c < kUnitPages; ++c) {
               float y[16];
               tmem_ld16(ts + 16 * c, y);
               const float kq = fmaxf(mt[c].x * qsc, 1e-37f);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) l += ex2(__fmaf_rn(y[k], kq, -ref));
+              for (int k = 0; k < 16; ++k)
+                l += col0 + 16 * c + k <= lim ? ex2(__fmaf_rn(y[k], kq, -ref)) : 0.0f;
             }
           }
           // P and its sum
-          auto exp32 = [&](const float (&v)[32], const float4* m2, uint32_t tp) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float4 m = FP8 ? m2[g] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+              const float4 m = FP8 ? mt[2 * c + g] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
               const float kq = fmaxf(FP8 ? m.x * qsc : qsc, 1e-37f), add = FP8 ? m.y - ref : -ref;
               const uint64_t k2 = pack2(kq, kq), a2 = pack2(add, add);
               uint64_t sum = 0;
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 float e0, e1;
-                unpack2(fma2(pack2(v[16 * g + k], v[16 * g + k + 1]), k2, a2), e0, e1);
+                const float* w = &v[32 * c + 16 * g + k];
+                unpack2(fma2(pack2(w[0], w[1]), k2, a2), e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum = k == 0 ? pack2(e0, e1) : add2(sum, pack2(e0, e1));
@@ -960,49 +956,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               unpack2(sum, s0, s1);
               l = !FP8 ? l + (s0 + s1) : __fmaf_rn(s0 + s1, m.z, l);
             }
-            tmem_st16u(tp, pk);
-          };
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld32_async(ts + 64 * c + 32, vb);
-            exp32(va, mt + 4 * c, ts + 32 * c);
-            tmem_wait_ld(vb);
-            tmem_ld32_async(ts + 64, va);
-            exp32(vb, mt + 4 * c + 2, ts + 32 * c + 16);
-            tmem_wait_ld(va);
-            if (c == 0) {  // half of the keys: their products may start
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bar.p_half[x]);
-            }
+            tmem_st16u(ts + 16 * c, pk);
           }
           tmem_wait_st();
-        } else {
-          if (lane == 0) mbar_arrive(&bar.p_half[x]);
         }
-        first = false;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_ready[x]);
+        if (lane == 0) mbar_arrive(&bar.p_ready[b]);
       }
+      u0 += cnt;
       if (!go) break;
       if (!stage(piece + 1)) break;
       // ---- the piece's output
-      const bool used = both || cnt > x;     // this tile had a block
-      const bool two = !both && cnt > 1;     // A and B hold parts of the same rows
-      if (used) {
-        if (!wait(&bar.o_full[x], (ph & kO) != 0, 13)) break;
-        ph ^= kO;
-      }
+      const bool two = !both;  // A and B hold parts of the same rows
+      if (!wait(&bar.o_full[x], (ph & kO) != 0, 13)) break;
+      ph ^= kO;
       tc_fence_after();
       float wa = 1.0f, wb = 0.0f;
       if (!both && x == 1) {  // B's part goes to A's warps
-        if (two) {
-          ml_b[row] = make_float2(M, (flags & kBadPage) ? -1.0f : l);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.b_ml);
-        }
+        ml_b[row] = make_float2(M, (flags & kBadPage) ? -1.0f : l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.b_ml);
       } else {
         if (two) {
           if (!wait(bar.b_ml, (ph & kMl) != 0, 14)) break;
@@ -1017,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           l = l * wa + b.y * wb;
           M = Mn;
         }
-        if (both || two) ph ^= kOB;
+        ph ^= kOB;
         if (warp_live) {
           const bool bad = (flags & kBadPage) != 0, live = tile0 + row < rows;
           const bool whole = pc->b_lo == 0 && pc->b_hi == pc->nb;
