@@ -260,6 +260,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -882,82 +887,97 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           const uint32_t fl = __float_as_uint(mt[0].w);
           flags |= fl;
           const int col0 = i * kBlk + h * kUnit;
-          float v[64];  // this row of S
-          tmem_ld64(ts, v);
-          if (lim_all < col0 + kUnit - 1) {  // columns <= lim are visible: the others to -inf
-            const int c = lim - col0;
-#pragma unroll
-            for (int k = 0; k < kUnit; ++k) v[k] = k <= c ? v[k] : -INFINITY;
-          }
-          // the maximum (a scale of 0 would make a masked score NaN)
-          float mx = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < kUnitPages; ++g) {
-            const float* w = &v[16 * g];
-            float pm = fmaxf(w[0], w[1]), pn = fmaxf(w[2], w[3]);
-#pragma unroll
-            for (int k = 4; k < 16; k += 4) {
-              pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
-              pn = fmaxf(fmaxf(pn, w[k + 2]), w[k + 3]);
-            }
-            pm = fmaxf(pm, pn);
-            mx = FP8 ? fmaxf(mx, __fmaf_rn(pm, fmaxf(mt[g].x * qsc, 1e-37f), mt[g].y))
-                     : fmaxf(mx, pm);
-          }
-          if (!FP8) mx *= fmaxf(qsc, 1e-37f);
-          float alpha = 1.0f;
-          if (mx > M + 8.0f) {
-            alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
-            l *= alpha;
-            M = mx;
-          }
-          if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            if (!wait(&bar.pv_done[x], t - 1, 12)) break;  // PV of the unit before
-            tc_fence_after();
+          // P against the reference M as it is: as long as a row's P stay below 2^15 (their
+          // sum tells) nothing is lost by a maximum that has grown since.  Only a first
+          // unit, a row that has seen nothing yet, or a sum beyond that takes the unit's
+          // maximum, and P again.
+          bool take = n == 0 || __any_sync(0xffffffffu, M == -INFINITY);
+          uint32_t pk[32];
+          uint64_t add_l;
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 16) tmem_scale16(to + c, alpha);
-          }
-          const float ref = M == -INFINITY ? 0.0f : M;
-          // where V scales lie far apart, P of a page with a small one can fall
-          // below fp32's range while its weight counts: such a block's sum is
-          // taken of the weights themselves (and its pages' factors below are 0)
-          if (FP8 && (fl & kWide)) {
-#pragma unroll 1
-            for (int c = 0; c < kUnitPages; ++c) {
-              float y[16];
-              tmem_ld16(ts + 16 * c, y);
-              const float kq = fmaxf(mt[c].x * qsc, 1e-37f);
+          for (;;) {
+            float v[64];  // this row of S
+            tmem_ld64(ts, v);
+            if (lim_all < col0 + kUnit - 1) {  // columns <= lim are visible: the others to -inf
+              const int c = lim - col0;
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                l += col0 + 16 * c + k <= lim ? ex2(__fmaf_rn(y[k], kq, -ref)) : 0.0f;
+              for (int k = 0; k < kUnit; ++k) v[k] = k <= c ? v[k] : -INFINITY;
             }
-          }
-          // P and its sum
+            if (take) {
+              float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
+              for (int g = 0; g < kUnitPages; ++g) {
+                const float* w = &v[16 * g];
+                float pm = fmaxf(w[0], w[1]);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float4 m = FP8 ? mt[2 * c + g] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-              const float kq = fmaxf(FP8 ? m.x * qsc : qsc, 1e-37f), add = FP8 ? m.y - ref : -ref;
-              const uint64_t k2 = pack2(kq, kq), a2 = pack2(add, add);
+                for (int k = 2; k < 16; k += 2) pm = fmaxf(fmaxf(pm, w[k]), w[k + 1]);
+                // (a scale of 0 would make a masked score NaN)
+                mx = FP8 ? fmaxf(mx, __fmaf_rn(pm, fmaxf(mt[g].x * qsc, 1e-37f), mt[g].y))
+                         : fmaxf(mx, pm * fmaxf(qsc, 1e-37f));
+              }
+              float alpha = 1.0f;
+              if (mx > M + 8.0f) {
+                alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
+                l *= alpha;
+                M = mx;
+              }
+              if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                if (!wait(&bar.pv_done[x], t - 1, 12)) break;  // PV of the unit before
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 16) tmem_scale16(to + c, alpha);
+              }
+            }
+            const float ref = M == -INFINITY ? 0.0f : M;
+            uint64_t raw = 0;
+#pragma unroll
+            for (int g = 0; g < kUnitPages; ++g) {
+              const float4 m = FP8 ? mt[g] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+              const float ks = fmaxf(FP8 ? m.x * qsc : qsc, 1e-37f), add = FP8 ? m.y - ref : -ref;
+              const uint64_t k2 = pack2(ks, ks), a2 = pack2(add, add);
               uint64_t sum = 0;
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 float e0, e1;
-                const float* w = &v[32 * c + 16 * g + k];
+                const float* w = &v[16 * g + k];
                 unpack2(fma2(pack2(w[0], w[1]), k2, a2), e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum = k == 0 ? pack2(e0, e1) : add2(sum, pack2(e0, e1));
                 pk[8 * g + k / 2] = pack_p<FP8>(e0, e1);
               }
-              float s0, s1;
-              unpack2(sum, s0, s1);
-              l = !FP8 ? l + (s0 + s1) : __fmaf_rn(s0 + s1, m.z, l);
+              raw = g == 0 ? sum : add2(raw, sum);
+              if (FP8) {
+                const uint64_t z = pack2(m.z, m.z);
+                add_l = g == 0 ? mul2(sum, z) : fma2(sum, z, add_l);
+              }
             }
-            tmem_st16u(ts + 16 * c, pk);
+            float r0, r1;
+            unpack2(raw, r0, r1);
+            if (!FP8) add_l = raw;
+            if (take || !__any_sync(0xffffffffu, fmaxf(r0, r1) >= 32768.0f)) break;
+            take = true;
           }
+          if (!go) break;
+          float s0, s1;
+          unpack2(add_l, s0, s1);
+          l += s0 + s1;
+          // where V scales lie far apart, P of a page with a small one can fall
+          // below fp32's range while its weight counts: such a block's sum is
+          // taken of the weights themselves (and its pages' factors above are 0)
+          if (FP8 && (fl & kWide)) {
+            const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll 1
+            for (int c = 0; c < kUnitPages; ++c) {
+              float y[16];
+              tmem_ld16(ts + 16 * c, y);
+              const float ks = fmaxf(mt[c].x * qsc, 1e-37f);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                l += col0 + 16 * c + k <= lim ? ex2(__fmaf_rn(y[k], ks, -ref)) : 0.0f;
+            }
+          }
+          tmem_st32u(ts, pk);
           tmem_wait_st();
         }
         tc_fence_before();
