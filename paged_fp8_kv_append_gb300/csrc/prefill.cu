@@ -54,11 +54,7 @@ constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 3) * 32;
 // what an item costs beside its blocks (queries in, output out), in halves of a two-tile
 // block (about 1 us each)
-constexpr int kItemCost = 6;
-__host__ __device__ inline long long item_lead(int nrows, int nb) {  // before its first block
-  (void)nrows, (void)nb;
-  return kItemCost;
-}
+__host__ __device__ inline long long item_lead(int nrows) { return nrows > 128 ? 8 : 6; }
 constexpr int kMeta = 4;  // block records in flight
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
@@ -164,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
           it.z = (int)min((long long)kItemRows, n * p.G - row0);
           const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
           it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = item_lead(it.z, it.w) + (long long)it.w * (it.z > kTile ? 2 : 1);
+          cost = item_lead(it.z) + (long long)it.w * (it.z > kTile ? 2 : 1);
         }
       }
       a.ws.items[v] = it;
@@ -214,9 +210,9 @@ struct Walk {
   long long x0;  // cost position of (item v, head h)
   Piece s;
   // of its first block, and behind its last
-  __device__ __forceinline__ long long blocks0() const { return x0 + item_lead(s.nrows, s.nb); }
+  __device__ __forceinline__ long long blocks0() const { return x0 + item_lead(s.nrows); }
   __device__ __forceinline__ long long cost() const {
-    return item_lead(s.nrows, s.nb) + (long long)s.nb * s.w();
+    return item_lead(s.nrows) + (long long)s.nb * s.w();
   }
 };
 
