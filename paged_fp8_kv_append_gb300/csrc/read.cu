@@ -7,9 +7,10 @@
 // and one rounding; bf16 pools copy the bits.
 //
 // Bounded by HBM: per row width codes in, 2 * width bytes out.  One CTA per
-// touched page: a page's tiles are contiguous, so every load and store of a
-// warp is a run of whole sectors; V tiles (dim-major) are transposed in
-// registers, a lane holding 4 dims of all 16 tokens.
+// touched page: a page's tiles are contiguous, and a warp's loads and stores
+// are runs of whole sectors (8 values a lane for token-major rows; a dim-major
+// V tile is transposed in registers, a lane holding 4 dims of all 16 tokens).
+// A tile's loads are issued together, K and V of a head by the same warp.
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -27,74 +28,101 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, float s) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+__device__ __forceinline__ uint4 dequant8(uint2 w, float s) {
+  return make_uint4(dequant2(w.x, s), dequant2(w.x >> 16, s), dequant2(w.y, s),
+                    dequant2(w.y >> 16, s));
+}
+
+// 8 cached values, and their bf16 values
+template <bool FP8>
+struct Chunk {
+  uint2 lo, hi;  // (hi: bf16 only)
+  __device__ __forceinline__ void load(const void* src, int c) {
+    if (FP8) {
+      lo = __ldcs(static_cast<const uint2*>(src) + c);
+    } else {
+      const uint4 x = __ldcs(static_cast<const uint4*>(src) + c);
+      lo = make_uint2(x.x, x.y);
+      hi = make_uint2(x.z, x.w);
+    }
+  }
+  __device__ __forceinline__ uint4 value(float s) const {
+    return FP8 ? dequant8(lo, s) : make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+};
 
 // `nrows` rows of D values, contiguous at src, to rows `stride` elements
-// apart at dst; threads tid, tid + n, ...
-__device__ __forceinline__ void read_token_major(const void* src, bool fp8, float s, int nrows,
-                                                 int D, uint16_t* dst, long long stride, int tid,
-                                                 int n) {
-  const int cpr = D / 16, total = nrows * cpr;  // 16 values a chunk
-  for (int c = tid; c < total; c += n) {
-    uint4 lo, hi;
-    if (fp8) {
-      const uint4 x = reinterpret_cast<const uint4*>(src)[c];
-      lo = make_uint4(dequant2(x.x, s), dequant2(x.x >> 16, s), dequant2(x.y, s),
-                      dequant2(x.y >> 16, s));
-      hi = make_uint4(dequant2(x.z, s), dequant2(x.z >> 16, s), dequant2(x.w, s),
-                      dequant2(x.w >> 16, s));
-    } else {
-      lo = reinterpret_cast<const uint4*>(src)[2 * c];
-      hi = reinterpret_cast<const uint4*>(src)[2 * c + 1];
+// apart at dst; threads tid, tid + n, .., kU chunks' loads in flight (kD: D
+// when it is known)
+template <bool FP8, int kD, int kU>
+__device__ __forceinline__ void read_rows_of(const void* src, float s, int nrows, int D,
+                                             uint16_t* dst, long long stride, int tid, int n) {
+  const int cpr = (kD ? kD : D) / 8, total = nrows * cpr;
+  for (int c0 = tid; c0 < total; c0 += kU * n) {
+    Chunk<FP8> x[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (c0 + k * n < total) x[k].load(src, c0 + k * n);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int c = c0 + k * n, r = c / cpr;
+      if (c < total)
+        __stcs(reinterpret_cast<uint4*>(dst + r * stride + 8 * (c - r * cpr)), x[k].value(s));
     }
-    uint4* o = reinterpret_cast<uint4*>(dst + (long long)(c / cpr) * stride + 16 * (c % cpr));
-    o[0] = lo;
-    o[1] = hi;
   }
 }
 
-// A dim-major tile of 16 tokens x 128 dims (one warp): lane l holds dims
-// 4l .. 4l+3 of every token and stores 8 bytes of each token's row.
-__device__ __forceinline__ void read_v_16x128(const uint8_t* src, bool fp8, float s, int slot0,
-                                              int nrows, uint16_t* dst, long long stride) {
+// A head's 16 x 128 tiles of K and V by one warp: tokens slot0 .. slot0 + nrows - 1 to rows
+// `stride` elements apart.  (The whole tiles are loaded: they lie in the page.)
+template <bool FP8>
+__device__ __forceinline__ void read_head_16x128(const uint8_t* ksrc, const uint8_t* vsrc,
+                                                 float ks, float vs, int slot0, int nrows,
+                                                 uint16_t* kdst, uint16_t* vdst,
+                                                 long long stride) {
+  constexpr int kN = FP8 ? 4 : 8;  // 16-byte pieces of a lane's 4 dims
   const int lane = threadIdx.x & 31;
-  uint16_t* o = dst + 4 * lane;
-  if (fp8) {
-    uint4 x[4];
+  Chunk<FP8> k[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = reinterpret_cast<const uint4*>(src)[4 * lane + k];
-    const uint32_t(*w)[4] = reinterpret_cast<const uint32_t(*)[4]>(x);
+  for (int i = 0; i < 8; ++i) k[i].load(ksrc, lane + 32 * i);
+  uint32_t w[kN][4];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      if (t < slot0 || t >= slot0 + nrows) continue;
-      const int sel = 0x0040 + (t & 3) * 0x0011;  // byte t & 3 of both words
-      const uint32_t a = __byte_perm(w[0][t >> 2], w[1][t >> 2], sel);
-      const uint32_t b = __byte_perm(w[2][t >> 2], w[3][t >> 2], sel);
-      *reinterpret_cast<uint2*>(o + (t - slot0) * stride) =
-          make_uint2(dequant2(a, s), dequant2(b, s));
+  for (int i = 0; i < kN; ++i) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(vsrc) + kN * lane + i);
+    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = 2 * i + (lane >> 4) - slot0;
+    if (t >= 0 && t < nrows)
+      __stcs(reinterpret_cast<uint4*>(kdst + t * stride + 8 * (lane & 15)), k[i].value(ks));
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int t = i - slot0;
+    uint32_t a, b;  // dims 4 lane, +1 and +2, +3 of token i
+    if (FP8) {
+      const int sel = 0x0040 + (i & 3) * 0x0011;  // byte i & 3 of both words
+      a = dequant2(__byte_perm(w[0][i >> 2], w[1][i >> 2], sel), vs);
+      b = dequant2(__byte_perm(w[2][i >> 2], w[3][i >> 2], sel), vs);
+    } else {
+      // dim d of the lane: pieces 2 d (tokens 0-7) and 2 d + 1
+      const int sel = (i & 1) ? 0x7632 : 0x5410, h = i >> 3, q = (i & 7) >> 1;
+      a = __byte_perm(w[0 + h][q], w[(2 + h) % kN][q], sel);
+      b = __byte_perm(w[(4 + h) % kN][q], w[(6 + h) % kN][q], sel);
     }
-  } else {
-    uint4 x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const uint4*>(src)[8 * lane + k];
-    const uint32_t(*w)[8] = reinterpret_cast<const uint32_t(*)[8]>(x);
-#pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      if (t < slot0 || t >= slot0 + nrows) continue;
-      const int sel = (t & 1) ? 0x7632 : 0x5410;
-      *reinterpret_cast<uint2*>(o + (t - slot0) * stride) =
-          make_uint2(__byte_perm(w[0][t >> 1], w[1][t >> 1], sel),
-                     __byte_perm(w[2][t >> 1], w[3][t >> 1], sel));
-    }
+    if (t >= 0 && t < nrows)
+      __stcs(reinterpret_cast<uint2*>(vdst + t * stride + 4 * lane), make_uint2(a, b));
   }
 }
 
 // Any other dim-major tile, element by element (stores coalesced).
-__device__ __noinline__ void read_v_any(const void* src, bool fp8, float s, int slot0, int nrows,
-                                        int D, int P, uint16_t* dst, long long stride) {
+template <bool FP8>
+__device__ __forceinline__ void read_v_any(const void* src, float s, int slot0, int nrows, int D,
+                                        int P, uint16_t* dst, long long stride) {
   for (int e = threadIdx.x & 31; e < nrows * (D / 2); e += 32) {
     const int i = e / (D / 2), dd = 2 * (e % (D / 2)), at = dd * P + slot0 + i;
     uint32_t w;
-    if (fp8) {
+    if (FP8) {
       const uint8_t* c = static_cast<const uint8_t*>(src);
       w = dequant2((uint32_t)c[at] | ((uint32_t)c[at + P] << 8), s);
     } else {
@@ -105,18 +133,20 @@ __device__ __noinline__ void read_v_any(const void* src, bool fp8, float s, int 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadArgs a) {
+enum Shape { kTile16x128, kLatent, kAny };
+
+template <bool FP8, int SHAPE>
+__global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 4 : 3) read_rows_kernel(const ReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const kv_pool_desc& d = a.d;
-  const int P = d.page_size;
+  const int P = SHAPE == kTile16x128 ? 16 : d.page_size;
   const int r = ragged_owner(a.out_indptr, a.B, P, blockIdx.x);
-  const long long o0 = a.out_indptr[r], o1 = a.out_indptr[r + 1];
-  const int local = blockIdx.x - ragged_first(o0, P, r);  // the request's touched page number
-  if (a.abort_mask != nullptr && a.abort_mask[r] != 0) return;
+  const long long o0 = a.out_indptr[r], o1 = a.out_indptr[r + 1], L = a.seq_lens[r];
   const long long start = a.row_start != nullptr ? a.row_start[r] : 0, n = o1 - o0;
-  const long long L = a.seq_lens[r];
-  if (n == 0) return;
+  const bool aborted = a.abort_mask != nullptr && a.abort_mask[r] != 0;
+  const int local = blockIdx.x - ragged_first(o0, P, r);  // the request's touched page number
+  if (aborted || n == 0) return;
   if (o0 < 0 || n < 0 || o1 > a.total_rows || start < 0 || start + n > L ||
       start + n > (long long)a.max_pages * P) {
     if (threadIdx.x == 0 && local == 0) set_error(d.ctl, KV_ERR_INVALID_ARG);
@@ -130,41 +160,57 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const ReadArgs a) {
     if (threadIdx.x == 0) set_error(d.ctl, KV_ERR_BAD_PAGE_ID);
     return;
   }
-  const bool fp8 = d.dtype == KV_DTYPE_E4M3;
-  const int es = fp8 ? 1 : 2, Dk = d.head_dim_k, Dv = d.head_dim_v, H = d.num_kv_heads;
+  constexpr int es = FP8 ? 1 : 2;
+  const int Dk = d.head_dim_k, Dv = d.head_dim_v, H = d.num_kv_heads;
   const int nrows = (int)(hi - lo), slot0 = (int)(lo - j * P);
   const long long row = o0 + (lo - start);
   const uint8_t* kc = static_cast<const uint8_t*>(d.k_cache);
-  if (d.layout == KV_LAYOUT_LATENT) {
-    read_token_major(kc + ((long long)p * P + slot0) * Dk * es, fp8, fp8 ? d.k_scale[p] : 1.0f,
-                     nrows, Dk, a.k_out + row * Dk, Dk, threadIdx.x, kThreads);
-    return;
-  }
   const uint8_t* vc = static_cast<const uint8_t*>(d.v_cache);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int t = warp; t < 2 * H; t += kThreads / 32) {
-    const int h = t >> 1;
-    const long long ph = (long long)p * H + h;
-    if ((t & 1) == 0) {
-      read_token_major(kc + (ph * P + slot0) * Dk * es, fp8, fp8 ? d.k_scale[ph] : 1.0f, nrows,
-                       Dk, a.k_out + (row * H + h) * Dk, (long long)H * Dk, lane, 32);
-    } else {
-      const uint8_t* src = vc + ph * P * Dv * es;
-      const float s = fp8 ? d.v_scale[ph] : 1.0f;
-      uint16_t* dst = a.v_out + (row * H + h) * Dv;
-      if (P == 16 && Dv == 128)
-        read_v_16x128(src, fp8, s, slot0, nrows, dst, (long long)H * Dv);
+  if (SHAPE == kLatent) {
+    const uint8_t* src = kc + ((long long)p * P + slot0) * Dk * es;
+    const float s = FP8 ? d.k_scale[p] : 1.0f;
+    uint16_t* dst = a.k_out + row * Dk;
+    if (Dk == 576)
+      read_rows_of<FP8, 576, 6>(src, s, nrows, Dk, dst, Dk, threadIdx.x, kThreads);
+    else
+      read_rows_of<FP8, 0, 2>(src, s, nrows, Dk, dst, Dk, threadIdx.x, kThreads);
+  } else if (SHAPE == kTile16x128) {
+    for (int h = warp; h < H; h += kThreads / 32) {
+      const long long ph = (long long)p * H + h, at = (row * H + h) * 128;
+      read_head_16x128<FP8>(kc + ph * 2048 * es, vc + ph * 2048 * es, FP8 ? d.k_scale[ph] : 1.0f,
+                            FP8 ? d.v_scale[ph] : 1.0f, slot0, nrows, a.k_out + at, a.v_out + at,
+                            H * 128ll);
+    }
+  } else {
+    for (int t = warp; t < 2 * H; t += kThreads / 32) {
+      const int h = t >> 1;
+      const long long ph = (long long)p * H + h;
+      if ((t & 1) == 0)
+        read_rows_of<FP8, 0, 2>(kc + (ph * P + slot0) * Dk * es, FP8 ? d.k_scale[ph] : 1.0f, nrows,
+                                Dk, a.k_out + (row * H + h) * Dk, (long long)H * Dk, lane, 32);
       else
-        read_v_any(src, fp8, s, slot0, nrows, Dv, P, dst, (long long)H * Dv);
+        read_v_any<FP8>(vc + ph * P * Dv * es, FP8 ? d.v_scale[ph] : 1.0f, slot0, nrows, Dv, P,
+                        a.v_out + (row * H + h) * Dv, (long long)H * Dv);
     }
   }
+}
+
+template <bool FP8>
+cudaError_t launch(const ReadArgs& a, cudaStream_t s) {
+  const kv_pool_desc& d = a.d;
+  const dim3 grid((unsigned)ragged_items(a.total_rows, a.B, d.page_size)), block(kThreads);
+  if (d.layout == KV_LAYOUT_LATENT)
+    return launch_pdl(read_rows_kernel<FP8, kLatent>, grid, block, 0, s, a);
+  if (d.page_size == 16 && d.head_dim_k == 128 && d.head_dim_v == 128)
+    return launch_pdl(read_rows_kernel<FP8, kTile16x128>, grid, block, 0, s, a);
+  return launch_pdl(read_rows_kernel<FP8, kAny>, grid, block, 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_read_rows(const ReadArgs& a, cudaStream_t s, int* launches) {
-  const unsigned items = (unsigned)ragged_items(a.total_rows, a.B, a.d.page_size);
-  const cudaError_t e = launch_pdl(read_rows_kernel, dim3(items), dim3(kThreads), 0, s, a);
+  const cudaError_t e = a.d.dtype == KV_DTYPE_E4M3 ? launch<true>(a, s) : launch<false>(a, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
