@@ -145,20 +145,50 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
-def _rows(t, heads, dim, name):
+def _device():
+    """The current device's number, which a call's tensors must lie on."""
+    return torch._C._cuda_getDevice()
+
+
+def _arg(t, dtype, name, dev, least=0):
+    """Device pointer of a contiguous tensor on device `dev` of at least `least`
+    elements (None -> NULL): _ptr with its checks in their cheapest form, for
+    calls whose device time is a few microseconds."""
+    if t is None:
+        return None
+    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous() or t.numel() < least):
+        _ptr(t, dtype, name)  # the error by its name
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: must be on the current device")
+        if t.numel() < least:
+            raise ValueError(f"{name}: {t.numel()} elements, {least} needed")
+    return t.data_ptr()
+
+
+def _rows(t, rows, heads, dim, name, dev):
     """Device pointer and row stride (elements) of a bf16 [rows][heads][dim]
     tensor whose rows may lie apart (a part of a wider projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: expected [rows][{heads}][{dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or t.stride(1) != dim:
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device")
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name}: expected [{rows}][{heads}][{dim}], got {tuple(t.shape)}")
+    stride, apart, one = t.stride()
+    if one != 1 or apart != dim:
         raise ValueError(f"{name}: a row's heads and dims must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+    return t.data_ptr(), stride if rows > 1 else max(stride, heads * dim)
+
+
+def _stream_on(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError("stream: must be a stream of the current device")
+    return _stream(stream)
 
 
 def _stream(stream):
@@ -319,43 +349,53 @@ def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_ne
     into q_out (see kvfp8.h).  q, k_new and v_new are [rows][heads][dim] with
     rows any multiple of 8 elements apart; positions int32 [axes][rows]."""
     rows, Hk, Dk = k_new.shape
-    if v_new.shape[0] != rows or positions.dim() != 2 or positions.shape[1] != rows:
-        raise ValueError("q, k_new, v_new and positions must have the same rows")
+    B, num_q_heads, axes, pairs = int(B), int(num_q_heads), positions.shape[0], inv_freq.numel()
+    dev, i32 = _device(), torch.int32
+    if positions.shape != (axes, rows):
+        raise ValueError("positions: expected [axes][rows of k_new]")
     qp = qo = None
     qs = 0
     if num_q_heads > 0:
-        qp, qs = _rows(q, num_q_heads, Dk, "q")
-        qo = _ptr(q_out, torch.bfloat16, "q_out")
-        if q.shape[0] != rows or q_out.shape != q.shape:
-            raise ValueError("q and q_out must have the rows of k_new")
+        qp, qs = _rows(q, rows, num_q_heads, Dk, "q", dev)
+        qo = _arg(q_out, torch.bfloat16, "q_out", dev, rows * num_q_heads * Dk)
         if qo == qp and qs != num_q_heads * Dk:
             raise ValueError("q_out may be q only when q is contiguous")
-    kp, ks = _rows(k_new, Hk, Dk, "k_new")
-    vp, vs = _rows(v_new, Hk, v_new.shape[2], "v_new")
-    if pair_axis.numel() != inv_freq.numel():
+    kp, ks = _rows(k_new, rows, Hk, Dk, "k_new", dev)
+    vp, vs = _rows(v_new, rows, Hk, v_new.shape[-1], "v_new", dev)
+    if pair_axis.numel() != pairs:
         raise ValueError("pair_axis and inv_freq must have the same length")
+    max_pages = page_table.shape[-1]
+    tags = exp_tags.dtype if exp_tags.dtype in _U32 else _U32
     st = _lib.kv_append_rotary(
-        handle, _stream(stream), int(B), int(num_q_heads), rows, qp, qs, kp, ks, vp, vs,
-        _ptr(new_indptr, torch.int32, "new_indptr"), int(max_new_per_req),
-        _ptr(positions, torch.int32, "positions"), positions.shape[0],
-        _ptr(pair_axis, torch.uint8, "pair_axis"), _ptr(inv_freq, torch.float64, "inv_freq"),
-        2 * inv_freq.numel(), int(interleaved), qo, _ptr(page_table, torch.int32, "page_table"),
-        _ptr(exp_tags, _U32, "exp_tags"), page_table.shape[-1],
-        _ptr(seq_lens, torch.int32, "seq_lens"))
-    _check(st, "kv_append_rotary")
+        handle, _stream_on(stream, dev), B, num_q_heads, rows, qp, qs, kp, ks, vp, vs,
+        _arg(new_indptr, i32, "new_indptr", dev, B + 1), int(max_new_per_req),
+        _arg(positions, i32, "positions", dev), axes,
+        _arg(pair_axis, torch.uint8, "pair_axis", dev),
+        _arg(inv_freq, torch.float64, "inv_freq", dev), 2 * pairs, int(interleaved), qo,
+        _arg(page_table, i32, "page_table", dev, B * max_pages),
+        _arg(exp_tags, tags, "exp_tags", dev, B * max_pages), max_pages,
+        _arg(seq_lens, i32, "seq_lens", dev, B))
+    if st:
+        _check(st, "kv_append_rotary")
 
 
 def kv_read_rows(handle, B, page_table, seq_lens, row_start, out_indptr, abort_mask, k_out, v_out,
                  stream=None):
     """Cached rows row_start[r] .. of each request as contiguous bf16 rows
     out_indptr[r] .. of k_out / v_out (v_out None for latent pools)."""
+    B, max_pages, rows = int(B), page_table.shape[-1], k_out.shape[0]
+    dev, i32 = _device(), torch.int32
+    if v_out is not None and v_out.shape[0] != rows:
+        raise ValueError("k_out and v_out must have the same rows")
     st = _lib.kv_read_rows(
-        handle, _stream(stream), int(B), _ptr(page_table, torch.int32, "page_table"),
-        page_table.shape[-1], _ptr(seq_lens, torch.int32, "seq_lens"),
-        _ptr(row_start, torch.int32, "row_start"), _ptr(out_indptr, torch.int32, "out_indptr"),
-        k_out.shape[0], _ptr(abort_mask, torch.uint8, "abort_mask"),
-        _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v_out, torch.bfloat16, "v_out"))
-    _check(st, "kv_read_rows")
+        handle, _stream_on(stream, dev), B,
+        _arg(page_table, i32, "page_table", dev, B * max_pages), max_pages,
+        _arg(seq_lens, i32, "seq_lens", dev, B), _arg(row_start, i32, "row_start", dev, B),
+        _arg(out_indptr, i32, "out_indptr", dev, B + 1), rows,
+        _arg(abort_mask, torch.uint8, "abort_mask", dev, B),
+        _arg(k_out, torch.bfloat16, "k_out", dev), _arg(v_out, torch.bfloat16, "v_out", dev))
+    if st:
+        _check(st, "kv_read_rows")
 
 
 def paged_prefill_workspace_size(handle, B, num_q_heads, total_q) -> int:
@@ -366,16 +406,21 @@ def paged_prefill_attn(handle, B, num_q_heads, q, q_indptr, page_table, seq_lens
                        sm_scale, out, workspace, stream=None):
     """Causal attention of a ragged batch's new tokens (q [total_q][heads][128],
     request r's at q_indptr[r] ..) over the paged cache (see kvfp8.h)."""
+    B, max_pages, total_q = int(B), page_table.shape[-1], q.shape[0]
+    dev, i32 = _device(), torch.int32
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     st = _lib.paged_prefill_attn(
-        handle, _stream(stream), int(B), int(num_q_heads), q.shape[0],
-        _ptr(q, torch.bfloat16, "q"), _ptr(q_indptr, torch.int32, "q_indptr"),
-        _ptr(page_table, torch.int32, "page_table"), page_table.shape[-1],
-        _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(abort_mask, torch.uint8, "abort_mask"),
-        float(sm_scale), _ptr(out, torch.bfloat16, "out"),
-        _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
-    _check(st, "paged_prefill_attn")
+        handle, _stream_on(stream, dev), B, int(num_q_heads), total_q,
+        _arg(q, torch.bfloat16, "q", dev, total_q * int(num_q_heads) * 128),
+        _arg(q_indptr, i32, "q_indptr", dev, B + 1),
+        _arg(page_table, i32, "page_table", dev, B * max_pages), max_pages,
+        _arg(seq_lens, i32, "seq_lens", dev, B),
+        _arg(abort_mask, torch.uint8, "abort_mask", dev, B), float(sm_scale),
+        _arg(out, torch.bfloat16, "out", dev), _arg(workspace, torch.uint8, "workspace", dev),
+        workspace.numel())
+    if st:
+        _check(st, "paged_prefill_attn")
 
 
 # ---------------------------------------------------------------- pool helper
@@ -502,16 +547,27 @@ class KVPool:
     def append_rotary(self, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
                       positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
                       seq_lens, stream=None):
-        if tuple(k_new.shape[1:]) != (self.num_kv_heads, self.head_dim_k):
+        self._same_device()
+        if k_new.shape[1:] != (self.num_kv_heads, self.head_dim_k):
             raise ValueError("k_new: expected [rows][num_kv_heads][head_dim_k]")
-        if tuple(v_new.shape[1:]) != (self.num_kv_heads, self.head_dim_v):
+        if v_new.shape[1:] != (self.num_kv_heads, self.head_dim_v):
             raise ValueError("v_new: expected [rows][num_kv_heads][head_dim_v]")
         kv_append_rotary(self.handle, B, num_q_heads, q, k_new, v_new, new_indptr,
                          max_new_per_req, positions, pair_axis, inv_freq, interleaved, q_out,
                          page_table, exp_tags, seq_lens, stream)
 
+    def _same_device(self):
+        if self.k_cache.get_device() != _device():
+            raise ValueError("the pool's device must be the current one")
+
     def read_rows(self, B, page_table, seq_lens, row_start, out_indptr, abort_mask, k_out,
                   v_out=None, stream=None):
+        self._same_device()
+        heads = 1 if self.v_cache is None else self.num_kv_heads
+        if k_out.numel() != k_out.shape[0] * heads * self.head_dim_k:
+            raise ValueError("k_out: expected rows of every head's head_dim_k")
+        if v_out is not None and v_out.numel() != v_out.shape[0] * heads * self.head_dim_v:
+            raise ValueError("v_out: expected rows of every head's head_dim_v")
         kv_read_rows(self.handle, B, page_table, seq_lens, row_start, out_indptr, abort_mask,
                      k_out, v_out, stream)
 
@@ -523,6 +579,7 @@ class KVPool:
 
     def prefill_attn(self, B, num_q_heads, q, q_indptr, page_table, seq_lens, abort_mask,
                      sm_scale, out, workspace, stream=None):
+        self._same_device()
         paged_prefill_attn(self.handle, B, num_q_heads, q, q_indptr, page_table, seq_lens,
                            abort_mask, sm_scale, out, workspace, stream)
 

@@ -26,43 +26,65 @@ namespace kvfp8 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnits = 4;  // 16-value units of a key tile a lane holds (P * Dk <= 2048)
+constexpr int kUnits = 4;   // 16-value units of a key tile a lane holds (P * Dk <= 2048)
+constexpr int kAhead = 4;   // query units a thread has in flight
 
-// Two 8-value chunks of a row hold 8 pairs: chunks j and j + rot/16 when the
-// pairs lie rot/2 apart, chunks 2j and 2j + 1 when interleaved; units from
-// rot/16 on pass through.
+// A frequency as the table holds it: turns per position in units of 2^-64,
+// whole turns dropped.
+struct Freq {
+  long long turns;
+  int axis;    // -1: the tables name an axis that positions does not have
+  float skew;  // 0, or NaN for a frequency that is not finite
+};
+static_assert(sizeof(Freq) == 16, "one shared load");
+
+// A unit is two 8-value chunks of a row, 8 pairs: chunks j and j + rot/16 for
+// j < rot/16 (pair k of dims k and k + rot/2: value k of each; neighbouring
+// pairs: 4 in each chunk), and the rest of the row in the same way, so that
+// the lanes of a row load and store neighbouring chunks.
 struct UnitPlace {
   int c0, c1;  // chunk numbers
   bool turn;
 };
-__device__ __forceinline__ UnitPlace unit_place(int j, int rot16, bool interleaved) {
+__device__ __forceinline__ UnitPlace unit_place(int j, int rot16, int upr) {
   UnitPlace u;
   u.turn = j < rot16;
-  const bool apart = u.turn && !interleaved;
-  u.c0 = apart ? j : 2 * j;
-  u.c1 = apart ? j + rot16 : 2 * j + 1;
+  u.c0 = u.turn ? j : j + rot16;
+  u.c1 = u.c0 + (u.turn ? rot16 : upr - rot16);
   return u;
 }
 
-// The unit's 16 values rotated: x[0..7] from chunk c0, x[8..15] from c1; cs:
-// (cos, sin) of its 8 pairs.
-__device__ __forceinline__ void unit_turn(uint4 a, uint4 b, const UnitPlace& u, bool interleaved,
-                                          const float2* cs, float (&x)[16]) {
+// (cos, sin) of a unit's 8 pairs from its token's row of them
+template <bool IL>
+__device__ __forceinline__ void unit_angles(const float2* row, int j, int rot16, float2 (&c)[8]) {
+  const float4* a = reinterpret_cast<const float4*>(row + (IL ? 4 : 8) * j);
+  const float4* b = IL ? reinterpret_cast<const float4*>(row + 4 * (j + rot16)) : a + 2;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 t = k < 2 ? a[k] : b[k - 2];
+    c[2 * k] = make_float2(t.x, t.y);
+    c[2 * k + 1] = make_float2(t.z, t.w);
+  }
+}
+
+// The unit's values rotated: x[0..7] of chunk c0, x[8..15] of c1.
+template <bool IL>
+__device__ __forceinline__ void unit_turn(uint4 a, uint4 b, bool turn, const float2 (&c)[8],
+                                          float (&x)[16]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     x[2 * k] = bf16_lo(w[k]);
     x[2 * k + 1] = bf16_hi(w[k]);
   }
-  if (!u.turn) return;
+  if (!turn) return;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float2 t = cs[k];
-    float& p = interleaved ? x[2 * k] : x[k];
-    float& q = interleaved ? x[2 * k + 1] : x[8 + k];
+    float& p = IL ? x[2 * k] : x[k];
+    float& q = IL ? x[2 * k + 1] : x[8 + k];
     const float p0 = p, q0 = q;
-    p = p0 * t.x - q0 * t.y;
-    q = q0 * t.x + p0 * t.y;
+    p = p0 * c[k].x - q0 * c[k].y;
+    q = q0 * c[k].x + p0 * c[k].y;
   }
 }
 
@@ -85,36 +107,53 @@ __device__ __forceinline__ uint2 codes8(const float* x, float s, float rs) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// One (page, kv head) key tile by one warp: `nrows` rows from slot0 on.
-__device__ void key_tile(const uint16_t* src, long long stride, int nrows, int D, int rot16,
-                         bool interleaved, const float2* cs, bool fp8, bool fresh, bool requant,
-                         float* scale_slot, uint8_t* dst, int slot0) {
-  const int lane = threadIdx.x & 31, upr = D / 16, total = nrows * upr;
-  float x[kUnits][16];
-  float m = 0.0f;
+// One (page, kv head) key tile by one warp: `nrows` rows from slot0 on.  The
+// tile's loads are issued together; the rows are turned once for the scale and
+// again for the codes, so that a lane holds 32 registers of them, not 64.
+template <int kD, bool IL>
+__device__ __forceinline__ void key_tile(const uint16_t* src, long long stride, int nrows, int D,
+                                         int rot16, const float2* cs, bool fp8, bool fresh,
+                                         bool requant, float* scale_slot, uint8_t* dst,
+                                         int slot0) {
+  const int lane = threadIdx.x & 31, upr = kD ? kD / 16 : D / 16, total = nrows * upr;
+  uint4 raw[kUnits][2];
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    const int u = lane + 32 * k;
+    const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
+    raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
     if (u < total) {
-      const int i = u / upr, j = u - i * upr;
-      const UnitPlace p = unit_place(j, rot16, interleaved);
+      const UnitPlace p = unit_place(j, rot16, upr);
       const uint4* row = reinterpret_cast<const uint4*>(src + i * stride);
-      unit_turn(row[p.c0], row[p.c1], p, interleaved, cs + (i * rot16 + j) * 8, x[k]);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[k][e]));
+      raw[k][0] = __ldcs(row + p.c0);
+      raw[k][1] = __ldcs(row + p.c1);
     }
   }
   float s = 1.0f;
   if (fp8) {
-    m = warp_max(m);
-    if (fresh) {
-      s = scale_from_amax(m);
-      if (lane == 0) *scale_slot = s;
-    } else {
-      s = *scale_slot;
-      const float s_new = scale_from_amax(m);
-      if (requant && s_new > s) {  // a larger scale for the new rows: re-encode the old ones
-        requant_block(dst, slot0, D, false, 0, s, s_new, lane, 32);
+    s = fresh ? 0.0f : *scale_slot;
+    if (fresh || requant) {
+      float m = 0.0f;
+#pragma unroll 1
+      for (int k = 0; k < kUnits; ++k) {
+        const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
+        if (u >= total) break;
+        uint4 r0 = raw[0][0], r1 = raw[0][1];
+#pragma unroll
+        for (int e = 1; e < kUnits; ++e)
+          if (e == k) r0 = raw[e][0], r1 = raw[e][1];
+        float2 c[8];
+        float x[16];
+        if (j < rot16) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+        unit_turn<IL>(r0, r1, j < rot16, c, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+      }
+      const float s_new = scale_from_amax(warp_max(m));
+      if (fresh) {
+        s = s_new;
+        if (lane == 0) *scale_slot = s;
+      } else if (s_new > s) {  // a larger scale for the new rows: re-encode the old ones
+        requant_block(dst, slot0, kD ? kD : D, false, 0, s, s_new, lane, 32);
         __syncwarp();
         if (lane == 0) *scale_slot = s_new;
         s = s_new;
@@ -122,33 +161,89 @@ __device__ void key_tile(const uint16_t* src, long long stride, int nrows, int D
     }
   }
   const float rs = __frcp_rn(s);
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < kUnits; ++k) {
-    const int u = lane + 32 * k;
-    if (u < total) {
-      const int i = u / upr, j = u - i * upr;
-      const UnitPlace p = unit_place(j, rot16, interleaved);
-      const long long at = (long long)(slot0 + i) * D;
-      if (fp8) {
-        *reinterpret_cast<uint2*>(dst + at + 8 * p.c0) = codes8(x[k], s, rs);
-        *reinterpret_cast<uint2*>(dst + at + 8 * p.c1) = codes8(x[k] + 8, s, rs);
-      } else {
-        uint4* o = reinterpret_cast<uint4*>(dst + 2 * at);
-        o[p.c0] = pack8_bf16(x[k]);
-        o[p.c1] = pack8_bf16(x[k] + 8);
-      }
+    const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
+    if (u >= total) break;
+    uint4 r0 = raw[0][0], r1 = raw[0][1];
+#pragma unroll
+    for (int e = 1; e < kUnits; ++e)
+      if (e == k) r0 = raw[e][0], r1 = raw[e][1];
+    const UnitPlace p = unit_place(j, rot16, upr);
+    float2 c[8];
+    float x[16];
+    if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+    unit_turn<IL>(r0, r1, p.turn, c, x);
+    const long long at = (long long)(slot0 + i) * (kD ? kD : D);
+    if (fp8) {
+      *reinterpret_cast<uint2*>(dst + at + 8 * p.c0) = codes8(x, s, rs);
+      *reinterpret_cast<uint2*>(dst + at + 8 * p.c1) = codes8(x + 8, s, rs);
+    } else {
+      uint4* o = reinterpret_cast<uint4*>(dst + 2 * at);
+      o[p.c0] = pack8_bf16(x);
+      o[p.c1] = pack8_bf16(x + 8);
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryArgs a) {
+// Query heads [h0, h1) of the page's tokens.  A thread keeps one unit of one
+// token, so its sines and cosines stay in registers over the heads.
+template <int kD, bool IL>
+__device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, long long row0,
+                                        int nrows, int rot16, int h0, int h1) {
+  const int D = kD ? kD : a.app.d.head_dim_k, upr = D / 16, groups = kThreads / upr;
+  const int g = threadIdx.x / upr, j = threadIdx.x - g * upr;
+  // P * Dk <= 2048: at least two groups of threads a token
+  const int hs = groups / nrows, i = g / hs;
+  if (g >= groups || i >= nrows) return;
+  const UnitPlace p = unit_place(j, rot16, upr);
+  float2 c[8];
+  if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+  const uint16_t* q = a.q + (row0 + i) * a.q_stride;
+  uint16_t* out = a.q_out + (row0 + i) * a.Hq * D;
+  for (int h = h0 + g - i * hs; h < h1; h += kAhead * hs) {
+    uint4 r[kAhead][2];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (h + k * hs < h1) {
+        const uint4* src = reinterpret_cast<const uint4*>(q + (long long)(h + k * hs) * D);
+        r[k][0] = __ldcs(src + p.c0);
+        r[k][1] = __ldcs(src + p.c1);
+      }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (h + k * hs < h1) {
+        float x[16];
+        unit_turn<IL>(r[k][0], r[k][1], p.turn, c, x);
+        uint4* o = reinterpret_cast<uint4*>(out + (long long)(h + k * hs) * D);
+        o[p.c0] = pack8_bf16(x);
+        o[p.c1] = pack8_bf16(x + 8);
+      }
+  }
+}
+
+// kD: head_dim_k when it is known (0: any); IL: neighbouring pairs
+template <int kD, bool IL>
+__global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const RotaryArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  float2* cs = reinterpret_cast<float2*>(smem);  // [tokens of the page][rot / 2] (cos, sin)
-  pdl_wait();
-  pdl_trigger();
   const AppendArgs& ap = a.app;
   const kv_pool_desc& d = ap.d;
-  const int P = d.page_size;
+  const int P = d.page_size, half = a.rotary_dim / 2, rot16 = a.rotary_dim / 16;
+  Freq* freq = reinterpret_cast<Freq*>(smem);               // [rot / 2]
+  float2* cs = reinterpret_cast<float2*>(freq + half);      // [tokens of the page][rot / 2] (cos, sin)
+  // ---- the tables, while the plan kernel runs: it has waited for what ran
+  // before it, and does not write them
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double f = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+    const int ax = a.pair_axis[i];
+    Freq e;
+    e.turns = __double2ll_rn((f - rint(f)) * 0x1p64);
+    e.axis = ax < a.num_axes ? ax : -1;
+    e.skew = isfinite(f) ? 0.0f : __int_as_float(0x7FFFFFFF);
+    freq[i] = e;
+  }
+  pdl_wait();
+  pdl_trigger();
   const int r = ragged_owner(ap.new_indptr, ap.B, P, blockIdx.x);
   if (r >= d.ctl[KV_CTL_APPEND_STOP]) return;  // not served: nothing of it is written
   const long long i0 = ap.new_indptr[r], i1 = ap.new_indptr[r + 1], n = i1 - i0;
@@ -164,41 +259,30 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryArg
   if (local < 0 || lo >= hi) return;
   const int nrows = (int)(hi - lo), slot0 = (int)(lo - jp * P);
   const long long row0 = i0 + (lo - L0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
   // ---- the angles of the page's tokens
-  const int half = a.rotary_dim / 2, rot16 = a.rotary_dim / 16;
-  const bool il = a.interleaved != 0;
   bool bad_axis = false;
-  for (int e = threadIdx.x; e < nrows * half; e += kThreads) {
-    const int t = e / half, i = e - t * half, ax = a.pair_axis[i];
-    double turn = 0.0;
-    if (ax < a.num_axes) {
-      const double angle = (double)a.positions[(long long)ax * a.total_new + row0 + t] * a.inv_freq[i];
-      turn = angle * 0.15915494309189535;  // 1 / (2 pi)
-      turn -= rint(turn);
-    } else {
-      bad_axis = true;
+  for (int t = warp; t < nrows; t += kWarps)
+    for (int i = lane; i < half; i += 32) {
+      const Freq f = freq[i];
+      long long turns = 0;
+      if (f.axis >= 0)
+        turns = (long long)((unsigned long long)(long long)a.positions[(long long)f.axis * a.total_new + row0 + t] *
+                            (unsigned long long)f.turns);
+      else
+        bad_axis = true;
+      float2 v;
+      sincospif(__ll2float_rn(turns) * 0x1p-63f + f.skew, &v.y, &v.x);
+      cs[t * half + i] = v;
     }
-    float2 v;
-    sincospif((float)(2.0 * turn), &v.y, &v.x);
-    cs[e] = v;
-  }
   if (bad_axis) set_error(d.ctl, KV_ERR_INVALID_ARG);
   __syncthreads();
   // ---- queries
-  const int Dk = d.head_dim_k, Dv = d.head_dim_v, H = d.num_kv_heads, upr = Dk / 16;
-  if (a.q != nullptr) {
-    const int per_row = a.Hq * upr, total = nrows * per_row;
-    for (int u = threadIdx.x; u < total; u += kThreads) {
-      const int i = u / per_row, hu = u - i * per_row, h = hu / upr, j = hu - h * upr;
-      const UnitPlace p = unit_place(j, rot16, il);
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + i) * a.q_stride + (long long)h * Dk);
-      float x[16];
-      unit_turn(src[p.c0], src[p.c1], p, il, cs + (i * rot16 + j) * 8, x);
-      uint4* o = reinterpret_cast<uint4*>(a.q_out + ((row0 + i) * a.Hq + h) * Dk);
-      o[p.c0] = pack8_bf16(x);
-      o[p.c1] = pack8_bf16(x + 8);
-    }
-  }
+  const int S = gridDim.y, part = blockIdx.y, H = d.num_kv_heads;
+  if (a.q != nullptr)
+    queries<kD, IL>(a, cs, row0, nrows, rot16, (int)((long long)a.Hq * part / S),
+                    (int)((long long)a.Hq * (part + 1) / S));
   // ---- keys and values
   const int pg = ap.page_table[(long long)r * ap.max_pages + jp];
   if (pg < 0 || pg >= d.num_pages) {
@@ -211,16 +295,17 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryArg
   if (!fresh && d.tags[pg] != ap.exp_tags[(long long)r * ap.max_pages + jp]) return;
   const bool fp8 = d.dtype == KV_DTYPE_E4M3;
   const bool requant = fp8 && d.scale_mode == KV_SCALE_REQUANTIZE;
-  const int es = fp8 ? 1 : 2, warp = threadIdx.x >> 5;
+  const int es = fp8 ? 1 : 2, Dk = kD ? kD : d.head_dim_k, Dv = d.head_dim_v;
+  const int h0 = (int)((long long)H * part / S), nh = (int)((long long)H * (part + 1) / S) - h0;
   uint8_t* kc = static_cast<uint8_t*>(d.k_cache);
   uint8_t* vc = static_cast<uint8_t*>(d.v_cache);
-  for (int t = warp; t < 2 * H; t += kWarps) {
-    const int h = t < H ? t : t - H;
+  for (int t = warp; t < 2 * nh; t += kWarps) {
+    const int h = h0 + (t < nh ? t : t - nh);
     const long long ph = (long long)pg * H + h;
-    if (t < H) {
-      key_tile(ap.k_new + row0 * a.k_stride + (long long)h * Dk, a.k_stride, nrows, Dk, rot16, il,
-               cs, fp8, fresh, requant, fp8 ? d.k_scale + ph : nullptr, kc + ph * P * Dk * es,
-               slot0);
+    if (t < nh) {
+      key_tile<kD, IL>(ap.k_new + row0 * a.k_stride + (long long)h * Dk, a.k_stride, nrows, Dk,
+                       rot16, cs, fp8, fresh, requant, fp8 ? d.k_scale + ph : nullptr,
+                       kc + ph * P * Dk * es, slot0);
     } else {
       const uint16_t* src = ap.v_new + row0 * a.v_stride + (long long)h * Dv;
       float* scale = fp8 ? d.v_scale + ph : nullptr;
@@ -239,11 +324,20 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryArg
 cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launches) {
   cudaError_t e = launch_append_plan(a.app, s, launches);
   if (e != cudaSuccess || a.total_new == 0) return e;
+  static int sms = 0;
+  if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess)
+    sms = 0;
   const int P = a.app.d.page_size;
-  const unsigned items = (unsigned)ragged_items(a.total_new, a.app.B, P);
-  // at most 16 KB: P * Dk <= 2048
-  const size_t smem = sizeof(float2) * (size_t)P * (a.rotary_dim / 2);
-  e = launch_pdl(append_rotary_kernel, dim3(items), dim3(kThreads), smem, s, a);
+  const long long items = ragged_items(a.total_new, a.app.B, P);
+  // few pages: their heads are split, up to one wave of CTAs
+  int split = (int)min(8LL, max(1LL, 3LL * sms / items));
+  split = min(split, a.app.d.num_kv_heads);
+  // at most 32 KB: P * Dk <= 2048
+  const size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
+  const auto kernel = a.app.d.head_dim_k == 128
+                          ? (a.interleaved ? append_rotary_kernel<128, true> : append_rotary_kernel<128, false>)
+                          : (a.interleaved ? append_rotary_kernel<0, true> : append_rotary_kernel<0, false>);
+  e = launch_pdl(kernel, dim3((unsigned)items, split), dim3(kThreads), smem, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
