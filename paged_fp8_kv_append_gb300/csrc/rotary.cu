@@ -193,7 +193,7 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
                                         int nrows, int rot16, int h0, int h1) {
   const int D = kD ? kD : a.app.d.head_dim_k, upr = D / 16, groups = kThreads / upr;
   const int g = threadIdx.x / upr, j = threadIdx.x - g * upr;
-  // P * Dk <= 2048: at least two groups of threads a token
+  // P * Dk <= 2048: a group of threads a token at least
   const int hs = groups / nrows, i = g / hs;
   if (g >= groups || i >= nrows) return;
   const UnitPlace p = unit_place(j, rot16, upr);
@@ -330,7 +330,7 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
   const int P = a.app.d.page_size;
   const long long items = ragged_items(a.total_new, a.app.B, P);
   // few pages: their heads are split, up to one wave of CTAs
-  int split = (int)min(8LL, max(1LL, 3LL * sms / items));
+  int split = (int)min(8LL, max(1LL, 2LL * sms / items));
   split = min(split, a.app.d.num_kv_heads);
   // at most 32 KB: P * Dk <= 2048
   const size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
