@@ -5,17 +5,31 @@
 // Pair i of a head turns by a_i = position[axis(i)] * inv_freq[i]:
 //   (x, y) -> (x cos a - y sin a, y cos a + x sin a),
 // the pair being dims (i, i + rot/2), or (2i, 2i + 1) when interleaved; dims
-// from rot on pass through.  The product of a position and a frequency is
-// taken in 64 bits and reduced to a fraction of a turn there, since a far
-// position times a frequency near 1 keeps no fraction in fp32; sine and cosine
-// of the fraction are fp32.  A rotated key stays in fp32 until its one
-// rounding: to e4m3 by its page's scale (amax/448 of the page's rotated rows,
-// as kv_append_quantize takes it of the rows it is given), or to bf16.
+// from rot on pass through.  A position times a frequency is wanted as a
+// fraction of a turn, which fp32 does not keep for a far position: the tables
+// hold a frequency as turns * 2^64, and the 64-bit integer product drops the
+// whole turns by itself and leaves the fraction, off by no more than position
+// times the table's own rounding (fp64: 2^-55 turns for a frequency of 1), with
+// two integer multiply-adds where fp64 (scarce here) would take six operations.  Sine and cosine of the fraction are fp32.  A rotated key
+// stays in fp32 until its one rounding: to e4m3 by its page's scale (amax/448
+// of the page's rotated rows, as kv_append_quantize takes it of the rows it is
+// given), or to bf16.
 //
 // Two launches: the append's plan kernel (append.cu: pages popped, tags
-// stamped, lengths advanced), then this kernel, one CTA per (request, touched
-// page): the angles of the page's tokens are computed once into shared memory
-// and serve every query and key head of those tokens.
+// stamped, lengths advanced), then this kernel, one CTA of 8 warps per
+// (request, touched page): the angles of the page's tokens are computed once
+// into shared memory and serve every query and key head of those tokens.  With
+// few pages the heads are split over up to 8 CTAs, to about two an SM.
+//
+// Bounded by HBM for prompts (every value read and written once).  8 prompts
+// of 1k-4k tokens, 64 query and 8 kv heads: 160 us with the plan, 5.3 TB/s of
+// the 6.8 of a plain copy; queries alone run at 6.3 (their threads keep a
+// token's sines in registers and have 8 loads of 16 bytes in flight), the
+// rest is the quantising of keys and values, half of the instructions.  Two
+// CTAs an SM at 128 registers: three at 80 spill and take 192 us; 4 of half
+// the threads 179; prefetching a page's rows into L2 changes nothing; a split
+// of the heads into 8 for all sizes 217.  One row a request (a decode step of
+// 64) is bounded by latency: about 7 us for the two kernels.
 #include "append_tile.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -26,7 +40,6 @@ namespace kvfp8 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnits = 4;   // 16-value units of a key tile a lane holds (P * Dk <= 2048)
 constexpr int kAhead = 4;   // query units a thread has in flight
 
 // A frequency as the table holds it: turns per position in units of 2^-64,
@@ -97,8 +110,7 @@ __device__ __forceinline__ uint4 pack8_bf16(const float* x) {
                     pack_bf16(x[6], x[7]));
 }
 
-// 8 codes of x / s (the quotient to fp32 by one corrected product where the
-// scale allows it, as the append kernels divide)
+// 8 codes of x / s, as the append kernels divide
 __device__ __forceinline__ uint2 codes8(const float* x, float s, float rs) {
   uint32_t c[4];
 #pragma unroll
@@ -106,83 +118,117 @@ __device__ __forceinline__ uint2 codes8(const float* x, float s, float rs) {
     c[k] = e4m3x2(div_by_scale(x[2 * k], s, rs), div_by_scale(x[2 * k + 1], s, rs));
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
-
-// One (page, kv head) key tile by one warp: `nrows` rows from slot0 on.  The
-// tile's loads are issued together; the rows are turned once for the scale and
-// again for the codes, so that a lane holds 32 registers of them, not 64.
-template <int kD, bool IL>
-__device__ __forceinline__ void key_tile(const uint16_t* src, long long stride, int nrows, int D,
-                                         int rot16, const float2* cs, bool fp8, bool fresh,
-                                         bool requant, float* scale_slot, uint8_t* dst,
-                                         int slot0) {
-  const int lane = threadIdx.x & 31, upr = kD ? kD / 16 : D / 16, total = nrows * upr;
-  uint4 raw[kUnits][2];
+// where |x| <= 448 s and scale_fast_ok(s): the quotient by one corrected product
+__device__ __forceinline__ uint2 codes8_fresh(const float* x, float s, float rs) {
+  uint32_t c[4];
 #pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
-    raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
-    if (u < total) {
+  for (int k = 0; k < 4; ++k)
+    c[k] = e4m3x2(div_fresh(x[2 * k], s, rs), div_fresh(x[2 * k + 1], s, rs));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// One (page, kv head) key tile by one warp: `nrows` rows from slot0 on; any
+// shape, page and scale, a unit at a time (kept out of line: a fresh page's
+// code stays small, and nothing of it lives across this call).
+template <bool IL>
+__device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride, int nrows, int D,
+                                          int rot16, const float2* cs, bool fp8, bool fresh,
+                                          bool requant, float* scale_slot, uint8_t* dst,
+                                          int slot0) {
+  const int lane = threadIdx.x & 31, upr = D / 16, total = nrows * upr;
+  float s = 1.0f, m = 0.0f;
+  // pass 0 finds the scale, pass 1 writes
+#pragma unroll 1
+  for (int pass = fp8 && (fresh || requant) ? 0 : 1; pass < 2; ++pass) {
+    if (pass == 1 && fp8) {
+      if (fresh) {
+        s = scale_from_amax(warp_max(m));
+        if (lane == 0) *scale_slot = s;
+      } else {
+        s = *scale_slot;
+        const float s_new = requant ? scale_from_amax(warp_max(m)) : s;
+        if (s_new > s) {  // a larger scale for the new rows: re-encode the old ones
+          requant_block(dst, slot0, D, false, 0, s, s_new, lane, 32);
+          __syncwarp();
+          if (lane == 0) *scale_slot = s_new;
+          s = s_new;
+        }
+      }
+    }
+    const float rs = __frcp_rn(s);
+#pragma unroll 1
+    for (int u = lane; u < total; u += 32) {
+      const int i = u / upr, j = u - i * upr;
       const UnitPlace p = unit_place(j, rot16, upr);
       const uint4* row = reinterpret_cast<const uint4*>(src + i * stride);
-      raw[k][0] = __ldcs(row + p.c0);
-      raw[k][1] = __ldcs(row + p.c1);
-    }
-  }
-  float s = 1.0f;
-  if (fp8) {
-    s = fresh ? 0.0f : *scale_slot;
-    if (fresh || requant) {
-      float m = 0.0f;
-#pragma unroll 1
-      for (int k = 0; k < kUnits; ++k) {
-        const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
-        if (u >= total) break;
-        uint4 r0 = raw[0][0], r1 = raw[0][1];
-#pragma unroll
-        for (int e = 1; e < kUnits; ++e)
-          if (e == k) r0 = raw[e][0], r1 = raw[e][1];
-        float2 c[8];
-        float x[16];
-        if (j < rot16) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
-        unit_turn<IL>(r0, r1, j < rot16, c, x);
+      float2 c[8];
+      float x[16];
+      if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+      unit_turn<IL>(row[p.c0], row[p.c1], p.turn, c, x);
+      if (pass == 0) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+        continue;
       }
-      const float s_new = scale_from_amax(warp_max(m));
-      if (fresh) {
-        s = s_new;
-        if (lane == 0) *scale_slot = s;
-      } else if (s_new > s) {  // a larger scale for the new rows: re-encode the old ones
-        requant_block(dst, slot0, kD ? kD : D, false, 0, s, s_new, lane, 32);
-        __syncwarp();
-        if (lane == 0) *scale_slot = s_new;
-        s = s_new;
+      const long long at = (long long)(slot0 + i) * D;
+      if (fp8) {
+        uint2* o = reinterpret_cast<uint2*>(dst + at);
+        o[p.c0] = codes8(x, s, rs);
+        o[p.c1] = codes8(x + 8, s, rs);
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(dst + 2 * at);
+        o[p.c0] = pack8_bf16(x);
+        o[p.c1] = pack8_bf16(x + 8);
       }
     }
   }
-  const float rs = __frcp_rn(s);
-#pragma unroll 1
-  for (int k = 0; k < kUnits; ++k) {
-    const int u = lane + 32 * k, i = u / upr, j = u - i * upr;
-    if (u >= total) break;
-    uint4 r0 = raw[0][0], r1 = raw[0][1];
+}
+
+// The same for a whole fresh page of 16 x 128 keys: its loads are issued
+// together and its turned values stay in registers.
+template <bool IL>
+__device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long stride, int rot16,
+                                                const float2* cs, bool fp8, float* scale_slot,
+                                                uint8_t* dst) {
+  const int lane = threadIdx.x & 31, j = lane & 7, i0 = lane >> 3;  // rows i0 + 4 k
+  const UnitPlace p = unit_place(j, rot16, 8);
+  uint4 raw[4][2];
 #pragma unroll
-    for (int e = 1; e < kUnits; ++e)
-      if (e == k) r0 = raw[e][0], r1 = raw[e][1];
-    const UnitPlace p = unit_place(j, rot16, upr);
+  for (int k = 0; k < 4; ++k) {
+    const uint4* row = reinterpret_cast<const uint4*>(src + (i0 + 4 * k) * stride);
+    raw[k][0] = __ldcs(row + p.c0);
+    raw[k][1] = __ldcs(row + p.c1);
+  }
+  float x[4][16];
+  float m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     float2 c[8];
-    float x[16];
-    if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
-    unit_turn<IL>(r0, r1, p.turn, c, x);
-    const long long at = (long long)(slot0 + i) * (kD ? kD : D);
-    if (fp8) {
-      *reinterpret_cast<uint2*>(dst + at + 8 * p.c0) = codes8(x, s, rs);
-      *reinterpret_cast<uint2*>(dst + at + 8 * p.c1) = codes8(x + 8, s, rs);
-    } else {
-      uint4* o = reinterpret_cast<uint4*>(dst + 2 * at);
-      o[p.c0] = pack8_bf16(x);
-      o[p.c1] = pack8_bf16(x + 8);
+    if (p.turn) unit_angles<IL>(cs + (i0 + 4 * k) * rot16 * 8, j, rot16, c);
+    unit_turn<IL>(raw[k][0], raw[k][1], p.turn, c, x[k]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[k][e]));
+  }
+  if (!fp8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4* o = reinterpret_cast<uint4*>(dst + (i0 + 4 * k) * 256);
+      o[p.c0] = pack8_bf16(x[k]);
+      o[p.c1] = pack8_bf16(x[k] + 8);
     }
+    return;
+  }
+  const float s = scale_from_amax(warp_max(m)), rs = __frcp_rn(s);
+  if (!scale_fast_ok(s)) {
+    key_tile_any<IL>(src, stride, 16, 128, rot16, cs, true, true, false, scale_slot, dst, 0);
+    return;
+  }
+  if (lane == 0) *scale_slot = s;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint2* o = reinterpret_cast<uint2*>(dst + (i0 + 4 * k) * 128);
+    o[p.c0] = codes8_fresh(x[k], s, rs);
+    o[p.c1] = codes8_fresh(x[k] + 8, s, rs);
   }
 }
 
@@ -219,6 +265,55 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
         o[p.c0] = pack8_bf16(x);
         o[p.c1] = pack8_bf16(x + 8);
       }
+  }
+}
+
+// The part's kv heads of the page: a warp a tile.
+template <int kD, bool IL>
+__device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* cs, int r,
+                                            long long jp, long long L0, long long row0, int nrows,
+                                            int slot0, int rot16) {
+  const AppendArgs& ap = a.app;
+  const kv_pool_desc& d = ap.d;
+  const int P = d.page_size, H = d.num_kv_heads, S = gridDim.y, part = blockIdx.y;
+  const int warp = threadIdx.x >> 5;
+  const int pg = ap.page_table[(long long)r * ap.max_pages + jp];
+  if (pg < 0 || pg >= d.num_pages) {
+    if (threadIdx.x == 0) set_error(d.ctl, KV_ERR_BAD_PAGE_ID);
+    return;
+  }
+  const bool fresh = jp * P >= L0;  // popped by this call
+  // a partly filled page that this call's pops handed to a later request is
+  // not written through the stale mapping
+  if (!fresh && d.tags[pg] != ap.exp_tags[(long long)r * ap.max_pages + jp]) return;
+  const bool fp8 = d.dtype == KV_DTYPE_E4M3;
+  const bool requant = fp8 && d.scale_mode == KV_SCALE_REQUANTIZE;
+  const int es = fp8 ? 1 : 2, Dk = kD ? kD : d.head_dim_k, Dv = d.head_dim_v;
+  const int h0 = (int)((long long)H * part / S), nh = (int)((long long)H * (part + 1) / S) - h0;
+  uint8_t* kc = static_cast<uint8_t*>(d.k_cache);
+  uint8_t* vc = static_cast<uint8_t*>(d.v_cache);
+  for (int t = warp; t < 2 * nh; t += kWarps) {
+    const int h = h0 + (t < nh ? t : t - nh);
+    const long long ph = (long long)pg * H + h;
+    if (t < nh) {
+      const uint16_t* src = ap.k_new + row0 * a.k_stride + (long long)h * Dk;
+      float* scale = fp8 ? d.k_scale + ph : nullptr;
+      uint8_t* dst = kc + ph * P * Dk * es;
+      if (kD == 128 && nrows == 16 && P == 16)
+        key_page_16x128<IL>(src, a.k_stride, rot16, cs, fp8, scale, dst);
+      else
+        key_tile_any<IL>(src, a.k_stride, nrows, Dk, rot16, cs, fp8, fresh, requant, scale, dst,
+                         slot0);
+    } else {
+      const uint16_t* src = ap.v_new + row0 * a.v_stride + (long long)h * Dv;
+      float* scale = fp8 ? d.v_scale + ph : nullptr;
+      uint8_t* dst = vc + ph * P * Dv * es;
+      if (nrows == 16 && P == 16 && Dv == 128)
+        v_page_16x128(src, a.v_stride, fp8, scale, dst);
+      else
+        tile_warp_generic(src, a.v_stride, nrows, Dv, fp8, fresh, scale, dst, true, P, slot0,
+                          nullptr, requant);
+    }
   }
 }
 
@@ -278,45 +373,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
     }
   if (bad_axis) set_error(d.ctl, KV_ERR_INVALID_ARG);
   __syncthreads();
-  // ---- queries
-  const int S = gridDim.y, part = blockIdx.y, H = d.num_kv_heads;
+  const int S = gridDim.y, part = blockIdx.y;
   if (a.q != nullptr)
     queries<kD, IL>(a, cs, row0, nrows, rot16, (int)((long long)a.Hq * part / S),
                     (int)((long long)a.Hq * (part + 1) / S));
-  // ---- keys and values
-  const int pg = ap.page_table[(long long)r * ap.max_pages + jp];
-  if (pg < 0 || pg >= d.num_pages) {
-    if (threadIdx.x == 0) set_error(d.ctl, KV_ERR_BAD_PAGE_ID);
-    return;
-  }
-  const bool fresh = jp * P >= L0;  // popped by this call
-  // a partly filled page that this call's pops handed to a later request is
-  // not written through the stale mapping
-  if (!fresh && d.tags[pg] != ap.exp_tags[(long long)r * ap.max_pages + jp]) return;
-  const bool fp8 = d.dtype == KV_DTYPE_E4M3;
-  const bool requant = fp8 && d.scale_mode == KV_SCALE_REQUANTIZE;
-  const int es = fp8 ? 1 : 2, Dk = kD ? kD : d.head_dim_k, Dv = d.head_dim_v;
-  const int h0 = (int)((long long)H * part / S), nh = (int)((long long)H * (part + 1) / S) - h0;
-  uint8_t* kc = static_cast<uint8_t*>(d.k_cache);
-  uint8_t* vc = static_cast<uint8_t*>(d.v_cache);
-  for (int t = warp; t < 2 * nh; t += kWarps) {
-    const int h = h0 + (t < nh ? t : t - nh);
-    const long long ph = (long long)pg * H + h;
-    if (t < nh) {
-      key_tile<kD, IL>(ap.k_new + row0 * a.k_stride + (long long)h * Dk, a.k_stride, nrows, Dk,
-                       rot16, cs, fp8, fresh, requant, fp8 ? d.k_scale + ph : nullptr,
-                       kc + ph * P * Dk * es, slot0);
-    } else {
-      const uint16_t* src = ap.v_new + row0 * a.v_stride + (long long)h * Dv;
-      float* scale = fp8 ? d.v_scale + ph : nullptr;
-      uint8_t* dst = vc + ph * P * Dv * es;
-      if (nrows == 16 && P == 16 && Dv == 128)
-        v_page_16x128(src, a.v_stride, fp8, scale, dst);
-      else
-        tile_warp_generic(src, a.v_stride, nrows, Dv, fp8, fresh, scale, dst, true, P, slot0,
-                          nullptr, requant);
-    }
-  }
+  keys_values<kD, IL>(a, cs, r, jp, L0, row0, nrows, slot0, rot16);
 }
 
 }  // namespace
