@@ -419,10 +419,11 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
  *   q_out          bf16 [total_new][num_q_heads][head_dim_k] (device); may be
  *                  q itself when q_stride is a row's width.
  * Pair (x, y) becomes (x cos a - y sin a, y cos a + x sin a) with a =
- * positions[axis][t] * inv_freq[i] (64-bit product).  Keys stay in fp32
- * between the rotation and their one rounding: e4m3 pages take their scale
- * from the rotated fp32 rows, bf16 pools round them to bf16.  Everything else
- * (page pops, tags, stops, partly filled pages, both scale modes, new_indptr,
+ * positions[axis][t] * inv_freq[i], taken as a fraction of a turn in 64 bits
+ * (positions may be negative; a frequency that is not finite gives NaN).  Keys
+ * stay in fp32 between the rotation and their one rounding: e4m3 pages take
+ * their scale from the rotated fp32 rows, bf16 pools round them to bf16.  q_out
+ * must not overlap k_new, v_new or another row's q.  Everything else (page pops, tags, stops, partly filled pages, both scale modes, new_indptr,
  * max_new_per_req, page_table, exp_tags, seq_lens) is as for
  * kv_append_quantize; a request that is not served gets no q_out rows.
  * GQA pools with page_size * head_dim <= 2048 for K and V; others return
@@ -489,12 +490,18 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  *               256-byte aligned; contents need not be initialised.
  * Query i of the n of request r (L = seq_lens[r]) attends to positions
  * 0 .. L - n + i; a query with no visible position gets zeros.  A request
- * with a negative length or count, one beyond its page table, or rows beyond
- * total_q sets KV_ERR_INVALID_ARG and is not written; one whose needed pages
- * include an id outside [0, num_pages) sets KV_ERR_BAD_PAGE_ID, and the rows
- * that would read it are not written.  GQA pools with head_dim 128 and
- * page_size 16, e4m3 and bf16, any num_q_heads / num_kv_heads; others return
- * KV_ERR_UNSUPPORTED.
+ * with a negative length or count, one beyond its page table or longer than
+ * 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is not written;
+ * one whose needed pages include an id outside [0, num_pages) sets
+ * KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of the
+ * request may or may not be.  Other requests are not affected.  GQA pools with
+ * head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
+ * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31; others return
+ * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or bf16 for the
+ * product with V, sums and maxima in fp32.  Results do not depend on which
+ * requests are run together beyond rounding, and are the same from run to run.
+ * Calls that may run at the same time need a workspace each.  Three kernel
+ * launches.
  */
 kv_status paged_prefill_attn(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
                              int32_t total_q, const void* q, const int32_t* q_indptr,

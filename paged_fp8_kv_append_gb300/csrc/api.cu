@@ -664,8 +664,8 @@ kv_status paged_prefill_attn(kv_pool* pool, void* stream, int32_t B, int32_t num
   if (st != KV_OK) return st;
   if (B == 0 || total_q == 0) return KV_OK;
   if (!q || !q_indptr || !page_table || max_pages_per_req <= 0 || !seq_lens || !out ||
-      !aligned16(q) || !aligned16(out) || !isfinite(sm_scale) || !workspace ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      !aligned16(q) || !aligned16(out) || !isfinite(sm_scale * 1.4426950408889634f) ||
+      !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return KV_ERR_INVALID_ARG;
   const size_t need = prefill_ws_bytes(pool->d, B, num_q_heads, total_q);
   if (need == 0) return KV_ERR_CUDA;

@@ -33,12 +33,12 @@ class Filled:
             def fill(shape):
                 x = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)
                 return torch.where((x & 0x7F) == 0x7F, x - 1, x)  # no NaN code
-            junk, as_codes = 0x7F, lambda x: x
+            junk = 0x7F
         else:
             def fill(shape):
                 return torch.randn(shape, generator=g).to(torch.bfloat16)
-            junk, as_codes = math.nan, lambda x: x
-        k, v = as_codes(fill(kshape)), None if latent else as_codes(fill(vshape))
+            junk = math.nan
+        k, v = fill(kshape), None if latent else fill(vshape)
         heads = (pages,) if latent else (pages, hkv)
         self.ks = torch.rand(heads, generator=g) * 0.01 + 1e-3 if fp8 else None
         self.vs = torch.rand(heads, generator=g) * 0.01 + 1e-3 if fp8 and not latent else None
