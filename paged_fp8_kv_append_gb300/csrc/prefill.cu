@@ -432,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (threadIdx.x == 64) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_ready[i], kConvWarps);
+      mbar_init(&bar.k_ready[i], kConvWarps / 2);
       mbar_init(&bar.k_free[i], 2);  // (both tiles')
-      mbar_init(&bar.v_ready[i], kConvWarps);
+      mbar_init(&bar.v_ready[i], kConvWarps / 2);
       mbar_init(&bar.v_free[i], 2);
       mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.o_full[i], 1);
@@ -483,12 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
 
   if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ============================ converters ============================
-    const int cw = warp - kSoftWarps, ct = threadIdx.x - kSoftWarps * 32;
+    // Two warps have the keys, two the values: each goes at its own pace.
+    const int cw = warp - kSoftWarps, ct = threadIdx.x & 63;
+    const bool keys = cw < kConvWarps / 2;
     constexpr int kEs = FP8 ? 1 : 2;
-    constexpr int kParts = FP8 ? 1 : 2;        // 16 KB source parts of a block's K or V
+    constexpr int kBatches = 2 * kEs;  // of 8 pieces of 16 bytes a thread, in a block's K or V
     constexpr long long kPageBytes = (long long)kP * kD * kEs;
-    const uint8_t* kc = static_cast<const uint8_t*>(p.d.k_cache);
-    const uint8_t* vc = static_cast<const uint8_t*>(p.d.v_cache);
+    const uint8_t* cache = static_cast<const uint8_t*>(keys ? p.d.k_cache : p.d.v_cache);
+    uint8_t* tiles = smem + (keys ? OFF_K : OFF_V);
+    uint64_t *ready = keys ? bar.k_ready : bar.v_ready, *room = keys ? bar.k_free : bar.v_free;
     const uint32_t page_step = (uint32_t)(H * kPageBytes);
     // this thread's places in a swizzled tile (the row's low bits are the same in every piece)
     const int vr = FP8 ? ct >> 2 : ct >> 3;
@@ -517,40 +520,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       // A page that is not there (behind the length, or an id out of range) is read as
       // page 0: its scores are masked or its item is not written, and its V is
       // zeroed with what lies behind the length.
-      const uint8_t *kh = kc + s.h * kPageBytes, *vh = vc + s.h * kPageBytes;
-      auto page_at = [&](const uint8_t* base, int pgl, int l) {  // lane l's page
-        const uint32_t pg = (uint32_t)__shfl_sync(0xffffffffu, pgl, l);
+      const uint8_t* base = cache + s.h * kPageBytes;
+      auto page_at = [&](int pgl, int l) {  // lane l's page
+        const uint32_t pg = (uint32_t)__shfl_sync(0xffffffffu, max(pgl, 0), l);
         return base + (uint64_t)pg * page_step;
       };
-      // Piece i (16 bytes) of this thread goes to tile row 32 (i / 2) + ct / 4 (a token of K, a
-      // dim of V), half i % 2, as two chunks (bf16: row 16 i + ct / 8 of half `part`, one
-      // chunk): 8 lanes store 2 rows of 4 chunk pairs, which no bank group meets twice.
-      // e4m3: K token 32 (i / 2) + ct / 4, dims 64 (i % 2) + 16 (ct % 4) ..
-      //       V dim 32 (i / 2) + ct / 4, tokens of page 4 (i % 2) + ct % 4
-      // bf16: K token 16 i + ct / 8 (page i), dims 64 part + 8 (ct % 8) ..
-      //       V dim 16 i + ct / 8, tokens 64 part + 8 (ct % 8) ..
-      auto load_k = [&](int pgl, int part, uint4 (&x)[8]) {
-        pgl = max(pgl, 0);
-        const uint8_t* src = nullptr;
+      // Piece i of batch j, e4m3 (16 bytes, two chunks of a tile row: 8 lanes store 2 rows of 4
+      // chunk pairs, which no bank group meets twice):
+      //   K token 64 j + 16 (i / 2) + ct / 4, dims 64 (i % 2) + 16 (ct % 4) ..
+      //   V dim 64 j + 16 (i / 2) + ct / 4, tokens of page 4 (i % 2) + ct % 4
+      // bf16 (one chunk of a row in half j / 2):
+      //   K token 64 (j % 2) + 8 i + ct / 8, dims 64 (j / 2) + 8 (ct % 8) ..
+      //   V dim 64 (j % 2) + 8 i + ct / 8, tokens 64 (j / 2) + 8 (ct % 8) ..
+      auto load = [&](int pgl, int j, uint4 (&x)[8]) {
+        const uint8_t* src[2];
+        if (!keys) {
+          if (FP8) {
+            src[0] = page_at(pgl, ct & 3) + j * 1024 + (ct >> 2) * 16;
+            src[1] = page_at(pgl, 4 + (ct & 3)) + j * 1024 + (ct >> 2) * 16;
+          } else {
+            src[0] = page_at(pgl, 4 * (j >> 1) + ((ct & 7) >> 1)) + (j & 1) * 2048 + (ct >> 3) * 32 +
+                     (ct & 1) * 16;
+          }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!FP8 || (i & 1) == 0)
-            src = page_at(kh, pgl, FP8 ? i + (ct >> 6) : i) +
-                  (FP8 ? ((ct >> 2) & 15) * 128 + (ct & 3) * 16 : (ct >> 3) * 256 + (ct & 7) * 16);
-          x[i] = __ldg(reinterpret_cast<const uint4*>(src + (FP8 ? (i & 1) * 64 : part * 128)));
+          for (int i = 0; i < 8; ++i)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(FP8 ? src[i & 1] + 256 * (i >> 1) : src[0] + 256 * i));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if ((i & 1) == 0)
+              src[0] = page_at(pgl, 4 * (FP8 ? j : j & 1) + (i >> 1)) +
+                       (FP8 ? (ct >> 2) * 128 + (ct & 3) * 16 : (ct >> 3) * 256 + (ct & 7) * 16 + (j >> 1) * 128);
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src[0] + (i & 1) * (FP8 ? 64 : 2048)));
+          }
         }
       };
-      auto load_v = [&](int pgl, int part, uint4 (&x)[8]) {
-        pgl = max(pgl, 0);
-        const uint8_t* s0 = page_at(vh, pgl, FP8 ? ct & 3 : 4 * part + ((ct & 7) >> 1)) +
-                            (FP8 ? (ct >> 2) * 16 : (ct >> 3) * 32 + (ct & 1) * 16);
-        const uint8_t* s1 = FP8 ? page_at(vh, pgl, 4 + (ct & 3)) + (ct >> 2) * 16 : s0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(FP8 ? ((i & 1) ? s1 : s0) + 512 * (i >> 1)
-                                                          : s0 + 512 * i));
-      };
-      auto store = [&](uint8_t* dst, int part, const uint4 (&x)[8]) {
+      auto store = [&](uint8_t* dst, int j, const uint4 (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
@@ -559,11 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             e4m3x4_to_f16(x[i].y, lo.z, lo.w);
             e4m3x4_to_f16(x[i].z, hi.x, hi.y);
             e4m3x4_to_f16(x[i].w, hi.z, hi.w);
-            uint8_t* h = dst + (i & 1) * kHalf + (i >> 1) * 4096;
+            uint8_t* h = dst + (i & 1) * kHalf + j * 8192 + (i >> 1) * 2048;
             *reinterpret_cast<uint4*>(h + off0) = lo;
             *reinterpret_cast<uint4*>(h + off1) = hi;
           } else {
-            *reinterpret_cast<uint4*>(dst + off0 + part * kHalf + 2048 * i) = x[i];
+            *reinterpret_cast<uint4*>(dst + off0 + (j >> 1) * kHalf + (j & 1) * 8192 + 1024 * i) = x[i];
           }
         }
       };
@@ -572,83 +577,70 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       auto clean_v = [&](uint8_t* dst, int b) {
         if ((b + 1) * kBlk <= s.L) return;
 #pragma unroll 1
-        for (int i = 0; i < 16; ++i) {  // the thread's 16-byte chunks of 8 tokens
-          const uint32_t at = FP8 ? ((i >> 1) & 1) * kHalf + (i >> 2) * 4096 + ((i & 1) ? off1 : off0)
-                                  : (i & 1) * kHalf + (i >> 1) * 2048 + off0;
-          const int tok = FP8 ? (4 * ((i >> 1) & 1) + (ct & 3)) * kP + 8 * (i & 1)
-                              : 64 * (i & 1) + 8 * (ct & 7);
+        for (int i = 0; i < 32; ++i) {  // the thread's 16-byte chunks of 8 tokens
+          const int half = FP8 ? (i >> 1) & 1 : i >> 4;
+          const uint32_t at = half * kHalf + (FP8 ? (i >> 2) * 2048 + ((i & 1) ? off1 : off0)
+                                                  : (i & 15) * 1024 + off0);
+          const int tok = FP8 ? (4 * half + (ct & 3)) * kP + 8 * (i & 1) : 64 * half + 8 * (ct & 7);
           const int nv = s.L - b * kBlk - tok;  // valid tokens of the chunk
           if (nv >= 8) continue;
           uint16_t* h = reinterpret_cast<uint16_t*>(dst + at);
           for (int k = max(nv, 0); k < 8; ++k) h[k] = 0;
         }
       };
-      // pages two blocks ahead are pulled into L2 (lanes 0-7 K, 8-15 V, of one warp)
+      // pages two blocks ahead are pulled into L2, 128 bytes a thread at a time (a bulk
+      // prefetch's lanes are issued one after the other: 1,000 cycles for a block's pages)
       auto prefetch = [&](int pgl) {
-        if (cw != 3) return;
-        const int pg = __shfl_sync(0xffffffffu, pgl, lane & 7);
-        if (lane < 16 && pg >= 0)
-          prefetch_l2((lane < 8 ? kc : vc) + ((long long)pg * H + s.h) * kPageBytes,
-                      (uint32_t)kPageBytes);
+#pragma unroll
+        for (int i = 0; i < kBatches; ++i) {
+          const int line = ct + 64 * i, pg = __shfl_sync(0xffffffffu, pgl, line / (16 * kEs));
+          if (pg >= 0)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (uint64_t)(uint32_t)pg * page_step +
+                                                          line % (16 * kEs) * 128));
+        }
       };
       const int raw0 = page_raw(s.b_lo), raw1 = page_raw(s.b_lo + 1);
       int raw2 = page_raw(s.b_lo + 2);
       int pg0 = page_of(raw0, s.b_lo), pg1 = page_of(raw1, s.b_lo + 1);
-      prefetch(pg0);
+      uint4 x[2][8];
+      load(pg0, 0, x[0]);
+      load(pg0, 1, x[1]);
       prefetch(pg1);
-      float2 sc0 = scales_of(pg0);
-      uint4 x0[8], x1[8];
-      load_k(pg0, 0, x0);
+      float2 sc0 = scales_of(pg0), sc1 = scales_of(pg1);
+#pragma unroll 1
       for (int b = s.b_lo; b < s.b_hi; ++b, ++u) {
-        const uint32_t st = u & 1, ms = u & (kMeta - 1), free_phase = (u >> 1) - 1;
+        const uint32_t st = u & 1;
         const int pg2 = page_of(raw2, b + 2);
         prefetch(pg2);
         raw2 = page_raw(b + 3);
-        const float2 sc1 = scales_of(pg1);
-        // K
-        if (u >= 2 && !wait(&bar.k_free[st], free_phase, 3)) break;
-        uint8_t* kd = smem + OFF_K + st * kTileBytes;
-        if (kParts == 2) {
-          load_k(pg0, 1, x1);
-          store(kd, 0, x0);
-          load_v(pg0, 0, x0);
-          store(kd, 1, x1);
-        } else {
-          load_v(pg0, 0, x1);
-          store(kd, 0, x0);
+        const float2 sc2 = scales_of(pg2);
+        if (u >= 2 && !wait(&room[st], (u >> 1) - 1, keys ? 3 : 4)) break;
+        uint8_t* dst = tiles + st * kTileBytes;
+#pragma unroll
+        for (int j = 0; j < kBatches; ++j) {
+          store(dst, j, x[j & 1]);
+          // (behind the last block: page 0, not used)
+          if (j + 2 < kBatches) load(pg0, j + 2, x[j & 1]);
+          else load(pg1, j + 2 - kBatches, x[j & 1]);
         }
+        if (!keys) clean_v(dst, b);
         if (cw == 0) {
           const float bias = __log2f(sc0.y);
           const uint32_t flags =
               (__any_sync(0xffffffffu, pg0 == -2) ? kBadPage : 0u) |
               (__any_sync(0xffffffffu, lane < kBlkPages && fabsf(bias) > 48.0f) ? kWide : 0u);
           if (lane < kBlkPages)
-            meta[ms * kBlkPages + lane] =
+            meta[(u & (kMeta - 1)) * kBlkPages + lane] =
                 make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias), __uint_as_float(flags));
           if (lane == 0 && (flags & kBadPage)) set_error(ctl, KV_ERR_BAD_PAGE_ID);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_ready[st]);
-        // V
-        if (u >= 2 && !wait(&bar.v_free[st], free_phase, 4)) break;
-        uint8_t* vd = smem + OFF_V + st * kTileBytes;
-        if (kParts == 2) {
-          load_v(pg0, 1, x1);
-          store(vd, 0, x0);
-          if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          store(vd, 1, x1);
-        } else {
-          if (b + 1 < s.b_hi) load_k(pg1, 0, x0);
-          store(vd, 0, x1);
-        }
-        clean_v(vd, b);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_ready[st]);
+        if (lane == 0) mbar_arrive(&ready[st]);
         pg0 = pg1;
         pg1 = pg2;
         sc0 = sc1;
+        sc1 = sc2;
       }
     }
   } else if (warp >= kMmaWarp) {
