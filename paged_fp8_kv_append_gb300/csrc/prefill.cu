@@ -12,9 +12,8 @@
 // (token, head of the group); 256 of them are an item's two tiles of 128 rows
 // (A and B).  A block is 128 tokens (8 pages), a unit half of one.  An item with at
 // most 128 rows has one tile, and then A and B are the same rows over the two halves of
-// each block, merged when the item ends.  Items are laid out request-major, a block costing 2 (two
-// tiles) or 1, and the whole batch is cut into equal ranges, one per persistent
-// CTA: every CTA works equally long whatever the lengths.  A CTA writes an item
+// each block, merged when the item ends.  Items are laid out request-major on an axis of
+// costs, and the whole batch is cut into equal ranges, one per persistent CTA: every CTA works equally long whatever the lengths.  A CTA writes an item
 // that lies wholly in its range; an item cut by a range's end leaves fp32
 // partials (o, running max, sum) for the combine kernel, at most two a CTA.
 //
@@ -52,9 +51,12 @@ constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;  // the scheduler is behind it
 constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 3) * 32;
-// what an item costs beside its blocks (queries in, output out), in halves of a two-tile
-// block (about 1 us each)
-__host__ __device__ inline long long item_lead(int nrows) { return nrows > 128 ? 8 : 6; }
+// Costs, about 0.65 us each: a block of an item with two tiles, one of an item with a
+// single tile (1.95 and 1.4 us: the keys and values are as many, the rows half), and what an
+// item costs beside its blocks (queries in, output out).  At 2 : 1 for the blocks four ragged
+// prompts took 973 us, at 3 : 2 856; leads of 10 and 8 cost one prompt of 8k tokens 9%.
+constexpr int kCostTwo = 3, kCostOne = 2;
+__host__ __device__ inline long long item_lead(int nrows) { return nrows > 128 ? 12 : 9; }
 constexpr int kMeta = 4;  // block records in flight
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
           it.z = (int)min((long long)kItemRows, n * p.G - row0);
           const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
           it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = item_lead(it.z) + (long long)it.w * (it.z > kTile ? 2 : 1);
+          cost = item_lead(it.z) + (long long)it.w * (it.z > kTile ? kCostTwo : kCostOne);
         }
       }
       a.ws.items[v] = it;
@@ -199,7 +201,7 @@ struct Piece {
   int b_lo, b_hi, nb, L;
   int n, q0, valid, pad;
   __device__ __forceinline__ bool both() const { return nrows > kTile; }
-  __device__ __forceinline__ int w() const { return both() ? 2 : 1; }
+  __device__ __forceinline__ int w() const { return both() ? kCostTwo : kCostOne; }
   __device__ __forceinline__ int count() const { return b_hi - b_lo; }
 };
 static_assert(sizeof(Piece) == 48, "ring slots");
@@ -217,8 +219,10 @@ struct Walk {
 };
 
 __device__ __forceinline__ int block_at(long long x, const Walk& c) {  // first block at or behind x
-  const long long d = x - c.blocks0(), w = c.s.w();
-  return d <= 0 ? 0 : (int)min((long long)c.s.nb, (d + w - 1) >> (w - 1));
+  const long long d = x - c.blocks0();
+  if (d <= 0) return 0;
+  return (int)min((long long)c.s.nb,
+                  c.s.both() ? (d + kCostTwo - 1) / kCostTwo : (d + kCostOne - 1) / kCostOne);
 }
 
 __device__ __forceinline__ void walk_item(Walk& c, const Args& a) {
@@ -419,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = p.d.num_kv_heads;
   const long long total = a.ws.pfx[a.V] * H;
-  // at least 2, so that every range holds a block's start
-  const long long per = max(2LL, (total + a.grid - 1) / a.grid);
+  // at least a block's cost, so that every range holds a block's start
+  const long long per = max((long long)kCostTwo, (total + a.grid - 1) / a.grid);
   const long long x_begin = (long long)blockIdx.x * per, x_end = min(total, x_begin + per);
   if (threadIdx.x == 0) a.ws.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (x_begin >= x_end) return;
