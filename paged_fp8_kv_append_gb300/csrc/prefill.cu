@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       for (int b = s.b_lo; b < s.b_hi; ++b, ++u) {
         const uint32_t st = u & 1;
         const int pg2 = page_of(raw2, b + 2);
-        prefetch(pg2);
         raw2 = page_raw(b + 3);
         const float2 sc2 = scales_of(pg2);
         if (u >= 2 && !wait(&room[st], (u >> 1) - 1, keys ? 3 : 4)) break;
@@ -641,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ready[st]);
+        prefetch(pg2);
         pg0 = pg1;
         pg1 = pg2;
         sc0 = sc1;
