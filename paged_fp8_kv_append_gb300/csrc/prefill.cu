@@ -6,33 +6,56 @@
 // values as it reads them; bf16 is the baseline format.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j), j <= L - n + i,
-// in one pass over the keys with the running maximum and sum of each row.
+// in one pass over the keys with a running reference and sum of each row.
 //
 // Work decomposition.  A request's query rows of one kv head are row = t * G + g
 // (token, head of the group); 256 of them are an item's two tiles of 128 rows
 // (A and B).  A block is 128 tokens (8 pages), a unit half of one.  An item with at
 // most 128 rows has one tile, and then A and B are the same rows over the two halves of
 // each block, merged when the item ends.  Items are laid out request-major on an axis of
-// costs, and the whole batch is cut into equal ranges, one per persistent CTA: every CTA works equally long whatever the lengths.  A CTA writes an item
-// that lies wholly in its range; an item cut by a range's end leaves fp32
-// partials (o, running max, sum) for the combine kernel, at most two a CTA.
+// costs, and the whole batch is cut into equal ranges, one per persistent CTA: every CTA
+// works equally long whatever the lengths.  A CTA writes an item that lies wholly in its
+// range; an item cut by a range's end leaves fp32 partials (o, reference, sum) for the
+// combine kernel, at most two a CTA.
 //
-// Per CTA (one per SM):
+// Per CTA (one per SM, 15 warps of 128 registers):
 //   softmax A (0-3), B (4-7)  a thread per row: a unit's 64 scores from tensor memory
-//                   into registers, maximum, exp2, P back to tensor memory as the A
-//                   operand of PV; the output accumulator is rescaled only when a row's
-//                   maximum grows by more than 2^8, by the same warp; between two items
-//                   the next item's query rows (f16 by an exact power of two a row,
-//                   or bf16) into shared memory, then the output
-//   converters (8-11)  global pages -> registers -> 128B-swizzled K-major tiles
-//                   in shared memory: K [token][dim] and V [dim][token] (pages
-//                   hold V dim-major: no transpose).  e4m3 codes become f16
-//                   exactly, bf16 is copied
+//                   into registers, exp2 against the row's reference M as it stands, P back
+//                   to tensor memory as the A operand of PV.  The unit's maximum is taken
+//                   only in a first unit, for a row that has seen nothing yet, or when the
+//                   P of a row sum to 2^15 or more (f16 P stay finite below that); M then
+//                   grows if it must and the output accumulator is rescaled by the same
+//                   warp.  Between two items the next item's query rows (f16 by an exact
+//                   power of two a row, or bf16) go into shared memory, then the output
+//   converters (8-11)  two warps for the keys, two for the values: global pages ->
+//                   registers -> 128B-swizzled K-major tiles in shared memory, K
+//                   [token][dim] and V [dim][token] (pages hold V dim-major: no
+//                   transpose).  e4m3 codes become f16 exactly, bf16 is copied
 //   MMA A (12), B (13)  S = Q K^T (M 128, N 64) a unit ahead of O += P V (M = N = 128),
 //                   so that a tile's softmax finds its next scores when it has stored P
 //   scheduler (14)  the CTA's pieces, one after the other into a ring that the other
 //                   warps read, their query rows pulled into L2
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
+//
+// What bounds it, and what was measured (64 query and 8 kv heads, e4m3, TFLOP/s of 4 Hq D
+// a visible pair, of 1,943 that cuBLAS reaches in bf16):
+//   2 x 2048 tokens behind 30k cached   3.27 ms, 1.31e15/s (67%): the tensor pipe is 65%
+//     busy.  S of 64 columns reads its 32 KB of queries from shared memory again for each
+//     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
+//     time cost less there but leave no room in tensor memory to be a step ahead, and
+//     were slower by 10%.
+//   one prompt of 8192    0.97 ms, 1.13e15 (58%): the same, and about 8 us an item (6 of
+//     them queries in) that the other items of the CTA hide in part.
+//   16 tokens of 32 requests, 4k-32k cached   0.29 ms, 0.9e15, 3.6 TB/s of cache: 128 rows
+//     make half the products of a block whose keys and values are the same 32 KB.  Bound
+//     by the converters, a block in 2,600 cycles.
+// Two converter warps for each of K and V against four for both in turn: drafts 378 -> 292
+// us, four ragged bf16 prompts 1,139 -> 965: a block's waits, page ids, fence and arrival
+// are paid once for it, and keys do not wait for values.  Eight converter warps leave 96
+// registers a thread, and the softmax then spills: chunk 3.3 -> 4.0 ms.  Pages by bulk copies
+// or cp.async through 32 KB of shared memory were slower than the loads (a bulk copy is about
+// 66 cycles of its warp, 16 a block).  All of the loops together have to stay small: the code
+// is 70 KB, and variants that unrolled more ran slower by what the instruction cache misses.
 #include <climits>
 
 #include "common.cuh"
@@ -497,10 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     uint8_t* tiles = smem + (keys ? OFF_K : OFF_V);
     uint64_t *ready = keys ? bar.k_ready : bar.v_ready, *room = keys ? bar.k_free : bar.v_free;
     const uint32_t page_step = (uint32_t)(H * kPageBytes);
-    // this thread's places in a swizzled tile (the row's low bits are the same in every piece)
-    const int vr = FP8 ? ct >> 2 : ct >> 3;
-    const uint32_t off0 = swz(vr, FP8 ? 2 * (ct & 3) : ct & 7);
-    const uint32_t off1 = swz(vr, 2 * (ct & 3) + 1);  // e4m3
+    // This thread's places in a swizzled tile (the row's low bits are the same in every piece).
+    // 8 lanes read a whole K row, 4 of each half: those of the second half store their chunk
+    // pair in the other order, so that no bank group is met twice.
+    const bool swap = FP8 && keys && (ct & 4) != 0;
+    const int vr = FP8 && !keys ? ct >> 2 : ct >> 3;
+    const uint32_t row_half = FP8 && keys ? ((ct >> 2) & 1) * kHalf : 0;
+    const uint32_t off0 = row_half + swz(vr, FP8 ? 2 * (ct & 3) + swap : ct & 7);
+    const uint32_t off1 = row_half + swz(vr, 2 * (ct & 3) + !swap);  // e4m3
     uint32_t u = 0;
     for (uint32_t piece = 0; next_piece(piece); ++piece) {
       // ---- the key blocks
@@ -529,13 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         const uint32_t pg = (uint32_t)__shfl_sync(0xffffffffu, max(pgl, 0), l);
         return base + (uint64_t)pg * page_step;
       };
-      // Piece i of batch j, e4m3 (16 bytes, two chunks of a tile row: 8 lanes store 2 rows of 4
-      // chunk pairs, which no bank group meets twice):
-      //   K token 64 j + 16 (i / 2) + ct / 4, dims 64 (i % 2) + 16 (ct % 4) ..
+      // Piece i of batch j, e4m3 (16 bytes, two chunks of a tile row):
+      //   K token 64 j + 8 i + ct / 8, dims 16 (ct % 8) ..
       //   V dim 64 j + 16 (i / 2) + ct / 4, tokens of page 4 (i % 2) + ct % 4
       // bf16 (one chunk of a row in half j / 2):
       //   K token 64 (j % 2) + 8 i + ct / 8, dims 64 (j / 2) + 8 (ct % 8) ..
       //   V dim 64 (j % 2) + 8 i + ct / 8, tokens 64 (j / 2) + 8 (ct % 8) ..
+      // A batch's registers are loaded with the next block's as soon as they are stored: as a
+      // block is some 2,600 cycles, that is what it takes to have 32 KB in flight here.
       auto load = [&](int pgl, int j, uint4 (&x)[8]) {
         const uint8_t* src[2];
         if (!keys) {
@@ -554,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           for (int i = 0; i < 8; ++i) {
             if ((i & 1) == 0)
               src[0] = page_at(pgl, 4 * (FP8 ? j : j & 1) + (i >> 1)) +
-                       (FP8 ? (ct >> 2) * 128 + (ct & 3) * 16 : (ct >> 3) * 256 + (ct & 7) * 16 + (j >> 1) * 128);
-            x[i] = __ldg(reinterpret_cast<const uint4*>(src[0] + (i & 1) * (FP8 ? 64 : 2048)));
+                       (FP8 ? (ct >> 3) * 128 + (ct & 7) * 16 : (ct >> 3) * 256 + (ct & 7) * 16 + (j >> 1) * 128);
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src[0] + (i & 1) * (FP8 ? 1024 : 2048)));
           }
         }
       };
@@ -564,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
             uint4 lo, hi;
-            e4m3x4_to_f16(x[i].x, lo.x, lo.y);
-            e4m3x4_to_f16(x[i].y, lo.z, lo.w);
-            e4m3x4_to_f16(x[i].z, hi.x, hi.y);
-            e4m3x4_to_f16(x[i].w, hi.z, hi.w);
-            uint8_t* h = dst + (i & 1) * kHalf + j * 8192 + (i >> 1) * 2048;
+            e4m3x4_to_f16(swap ? x[i].z : x[i].x, lo.x, lo.y);
+            e4m3x4_to_f16(swap ? x[i].w : x[i].y, lo.z, lo.w);
+            e4m3x4_to_f16(swap ? x[i].x : x[i].z, hi.x, hi.y);
+            e4m3x4_to_f16(swap ? x[i].y : x[i].w, hi.z, hi.w);
+            uint8_t* h = dst + j * 8192 + (keys ? i * 1024 : (i & 1) * kHalf + (i >> 1) * 2048);
             *reinterpret_cast<uint4*>(h + off0) = lo;
             *reinterpret_cast<uint4*>(h + off1) = hi;
           } else {
@@ -777,8 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   } else {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
-    // exponent and the reference maximum M follows max(score + bias), so that P <= 2^8
-    // whatever the scales; the row sum takes the bias back out.
+    // exponent, and M is the largest score + bias of a unit at which it was last taken, so
+    // that P stay below 2^15 whatever the scales; the row sum takes the bias back out.
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t to = tmem + tmem_o(x) + lanes;
