@@ -587,6 +587,8 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
     if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < qw ||
                             q_stride % 8 != 0))
       return KV_ERR_INVALID_ARG;
+    // in place only row for row: at another stride a row's output is a later row's input
+    if (num_q_heads > 0 && q_out == q && q_stride != qw && total_new > 1) return KV_ERR_INVALID_ARG;
   }
   RotaryArgs a = {};
   a.app.d = d;

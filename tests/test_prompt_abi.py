@@ -31,7 +31,7 @@ LATENT = dict(layout=1, num_kv_heads=1, head_dim_k=576, head_dim_v=512, page_siz
               v_cache=None, v_scale=None)
 
 ROTARY = dict(B=2, hq=8, total=10, q=F, qs=1024, k=F, ks=256, v=F, vs=256, ind=F, max_new=5, pos=F,
-              axes=3, axis=F, freq=F, rot=128, il=0, q_out=F, table=F, tags=F, width=4, lens=F)
+              axes=3, axis=F, freq=F, rot=128, il=0, q_out=F + 4096, table=F, tags=F, width=4, lens=F)
 
 
 @pytest.mark.parametrize("over", [
@@ -40,7 +40,7 @@ ROTARY = dict(B=2, hq=8, total=10, q=F, qs=1024, k=F, ks=256, v=F, vs=256, ind=F
     dict(v=None), dict(ind=None), dict(pos=None), dict(axis=None), dict(freq=None), dict(table=None),
     dict(tags=None), dict(lens=None), dict(q=None), dict(q_out=None), dict(q=F + 8),
     dict(k=F + 2), dict(v=F + 4), dict(q_out=F + 8), dict(qs=1016), dict(qs=1028), dict(ks=248),
-    dict(vs=260)])
+    dict(vs=260), dict(q_out=F, q=F, qs=1032)])
 def test_rotary_refusals(kv, over):
     h = _pool(kv)
     try:

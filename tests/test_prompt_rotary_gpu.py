@@ -159,6 +159,40 @@ def test_far_positions(kv):
     _check(f, new, host, _call(f, new, 4, dev, False), False)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_negative_positions_and_frequencies(kv, interleaved):
+    """Turns of either sign and of more than a whole turn a position (4000 positions of 40 radians
+    in 64 bits: the fraction of a turn is off by 2^-38)."""
+    f = Filled(kv, [0, 9], hkv=2, seed=43, spare=20, extra_width=8)
+    new = [20, 30]
+    host, dev = _inputs(f, new, 6, 96, 2, 44)
+    for i, t in ((3, "pos"), (5, "freq")):
+        if t == "pos":
+            host[i][:, ::2] *= -1
+        else:
+            host[i][::3] *= -40.0
+        dev[i].copy_(host[i])
+    _check(f, new, host, _call(f, new, 6, dev, interleaved), interleaved)
+
+
+def test_frequency_that_is_not_finite(kv):
+    """Its pairs become NaN, in queries and bf16 keys; every other dim is right."""
+    f = Filled(kv, [0], hkv=1, fp8=False, seed=45, spare=4, extra_width=3)
+    host, dev = _inputs(f, [18], 2, 128, 1, 46)
+    dev[5][3], dev[5][60] = float("nan"), float("inf")
+    out = _call(f, [18], 2, dev, False).cpu().double()
+    bad = [3, 67, 60, 124]
+    rest = [i for i in range(128) if i not in bad]
+    ref = rotate(host[0], host[3], host[4], host[5], False)
+    bound = 2.0 ** -19 * _pair_len(host[0], 128, False) + 2.0 ** -8 * ref.abs() + 1e-38
+    assert bool(torch.isnan(out[..., bad]).all())
+    assert bool(((out - ref).abs() <= bound)[..., rest].all())
+    k = f.pool.k_cache.cpu()[f.table_d[0, 0].item(), 0].double()  # the first page's 16 rows
+    kr, kl = rotate(host[1], host[3], host[4], host[5], False)[:16, 0], _pair_len(host[1], 128, False)[:16, 0]
+    assert bool(torch.isnan(k[:, bad]).all())
+    assert bool(((k - kr).abs() <= 2.0 ** -19 * kl + 2.0 ** -8 * kr.abs() + 1e-38)[:, rest].all())
+
+
 def test_decode_rows_and_no_queries(kv):
     f = Filled(kv, list(range(30, 94)), hkv=2, seed=17, spare=70, extra_width=3)
     new = [1] * 64
