@@ -520,14 +520,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     uint8_t* tiles = smem + (keys ? OFF_K : OFF_V);
     uint64_t *ready = keys ? bar.k_ready : bar.v_ready, *room = keys ? bar.k_free : bar.v_free;
     const uint32_t page_step = (uint32_t)(H * kPageBytes);
-    // This thread's places in a swizzled tile (the row's low bits are the same in every piece).
-    // 8 lanes read a whole K row, 4 of each half: those of the second half store their chunk
-    // pair in the other order, so that no bank group is met twice.
+    // This thread's places in a swizzled tile.  e4m3: of its piece 2 q (16 codes, two chunks:
+    // the other at ^ 16), piece 2 q + 1 `odd` bytes behind, a batch `turn`.  8 lanes hold a K
+    // row, 4 of each half (those of the second store their chunks in the other order), or
+    // 8 rows of V: no bank group is met twice.
     const bool swap = FP8 && keys && (ct & 4) != 0;
-    const int vr = FP8 && !keys ? ct >> 2 : ct >> 3;
-    const uint32_t row_half = FP8 && keys ? ((ct >> 2) & 1) * kHalf : 0;
-    const uint32_t off0 = row_half + swz(vr, FP8 ? 2 * (ct & 3) + swap : ct & 7);
-    const uint32_t off1 = row_half + swz(vr, 2 * (ct & 3) + !swap);  // e4m3
+    const uint32_t odd = keys ? 1024 : 8192, turn = keys ? 8192 : kHalf;
+    uint32_t off[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      off[q] = !FP8   ? swz(ct >> 3, ct & 7)
+               : keys ? ((ct >> 2) & 1) * kHalf + swz(ct >> 3, 2 * (ct & 3) + swap) + q * 2048
+                      : swz(ct, 2 * q);
     uint32_t u = 0;
     for (uint32_t piece = 0; next_piece(piece); ++piece) {
       // ---- the key blocks
@@ -556,35 +560,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         const uint32_t pg = (uint32_t)__shfl_sync(0xffffffffu, max(pgl, 0), l);
         return base + (uint64_t)pg * page_step;
       };
-      // Piece i of batch j, e4m3 (16 bytes, two chunks of a tile row):
-      //   K token 64 j + 8 i + ct / 8, dims 16 (ct % 8) ..
-      //   V dim 64 j + 16 (i / 2) + ct / 4, tokens of page 4 (i % 2) + ct % 4
+      // Piece i of batch j, e4m3: the 16 bytes ct + 64 (i % 2) of page 4 j + i / 2:
+      //   K token 8 (i % 2) + ct / 8 of the page, dims 16 (ct % 8) ..; V dim 64 (i % 2) + ct
       // bf16 (one chunk of a row in half j / 2):
       //   K token 64 (j % 2) + 8 i + ct / 8, dims 64 (j / 2) + 8 (ct % 8) ..
       //   V dim 64 (j % 2) + 8 i + ct / 8, tokens 64 (j / 2) + 8 (ct % 8) ..
       // A batch's registers are loaded with the next block's as soon as they are stored: as a
       // block is some 2,600 cycles, that is what it takes to have 32 KB in flight here.
       auto load = [&](int pgl, int j, uint4 (&x)[8]) {
-        const uint8_t* src[2];
-        if (!keys) {
-          if (FP8) {
-            src[0] = page_at(pgl, ct & 3) + j * 1024 + (ct >> 2) * 16;
-            src[1] = page_at(pgl, 4 + (ct & 3)) + j * 1024 + (ct >> 2) * 16;
-          } else {
-            src[0] = page_at(pgl, 4 * (j >> 1) + ((ct & 7) >> 1)) + (j & 1) * 2048 + (ct >> 3) * 32 +
-                     (ct & 1) * 16;
-          }
+        const uint8_t* src = nullptr;
+        if (FP8) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(FP8 ? src[i & 1] + 256 * (i >> 1) : src[0] + 256 * i));
-        } else {
+          for (int i = 0; i < 8; ++i) {
+            if ((i & 1) == 0) src = page_at(pgl, 4 * j + (i >> 1)) + ct * 16;
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (i & 1) * 1024));
+          }
+        } else if (keys) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if ((i & 1) == 0)
-              src[0] = page_at(pgl, 4 * (FP8 ? j : j & 1) + (i >> 1)) +
-                       (FP8 ? (ct >> 3) * 128 + (ct & 7) * 16 : (ct >> 3) * 256 + (ct & 7) * 16 + (j >> 1) * 128);
-            x[i] = __ldg(reinterpret_cast<const uint4*>(src[0] + (i & 1) * (FP8 ? 1024 : 2048)));
+              src = page_at(pgl, 4 * (j & 1) + (i >> 1)) + (ct >> 3) * 256 + (ct & 7) * 16 +
+                    (j >> 1) * 128;
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (i & 1) * 2048));
           }
+        } else {
+          src = page_at(pgl, 4 * (j >> 1) + ((ct & 7) >> 1)) + (j & 1) * 2048 + (ct >> 3) * 32 +
+                (ct & 1) * 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src + 256 * i));
         }
       };
       auto store = [&](uint8_t* dst, int j, const uint4 (&x)[8]) {
@@ -596,11 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             e4m3x4_to_f16(swap ? x[i].w : x[i].y, lo.z, lo.w);
             e4m3x4_to_f16(swap ? x[i].x : x[i].z, hi.x, hi.y);
             e4m3x4_to_f16(swap ? x[i].y : x[i].w, hi.z, hi.w);
-            uint8_t* h = dst + j * 8192 + (keys ? i * 1024 : (i & 1) * kHalf + (i >> 1) * 2048);
-            *reinterpret_cast<uint4*>(h + off0) = lo;
-            *reinterpret_cast<uint4*>(h + off1) = hi;
+            const uint32_t at = off[i >> 1] + j * turn + (i & 1) * odd;
+            *reinterpret_cast<uint4*>(dst + at) = lo;
+            *reinterpret_cast<uint4*>(dst + (at ^ 16)) = hi;
           } else {
-            *reinterpret_cast<uint4*>(dst + off0 + (j >> 1) * kHalf + (j & 1) * 8192 + 1024 * i) = x[i];
+            *reinterpret_cast<uint4*>(dst + off[0] + (j >> 1) * kHalf + (j & 1) * 8192 + 1024 * i) = x[i];
           }
         }
       };
@@ -610,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if ((b + 1) * kBlk <= s.L) return;
 #pragma unroll 1
         for (int i = 0; i < 32; ++i) {  // the thread's 16-byte chunks of 8 tokens
-          const int half = FP8 ? (i >> 1) & 1 : i >> 4;
-          const uint32_t at = half * kHalf + (FP8 ? (i >> 2) * 2048 + ((i & 1) ? off1 : off0)
-                                                  : (i & 15) * 1024 + off0);
-          const int tok = FP8 ? (4 * half + (ct & 3)) * kP + 8 * (i & 1) : 64 * half + 8 * (ct & 7);
+          const uint32_t at = FP8 ? (i >> 4) * kHalf + ((i >> 1) & 1) * 8192 +
+                                        (swz(ct, 0) ^ ((((i >> 1) & 6) + (i & 1)) << 4))
+                                  : (i >> 4) * kHalf + (i & 15) * 1024 + off[0];
+          const int tok = FP8 ? (i >> 2) * kP + 8 * (i & 1) : 64 * (i >> 4) + 8 * (ct & 7);
           const int nv = s.L - b * kBlk - tok;  // valid tokens of the chunk
           if (nv >= 8) continue;
           uint16_t* h = reinterpret_cast<uint16_t*>(dst + at);
@@ -631,43 +634,53 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
                                                           line % (16 * kEs) * 128));
         }
       };
-      const int raw0 = page_raw(s.b_lo), raw1 = page_raw(s.b_lo + 1);
-      int raw2 = page_raw(s.b_lo + 2);
-      int pg0 = page_of(raw0, s.b_lo), pg1 = page_of(raw1, s.b_lo + 1);
+      // e4m3: an iteration before the first block loads it (one copy of the loads)
+      const int b0 = s.b_lo - (FP8 ? 1 : 0);
+      int raw2 = page_raw(b0 + 2);
+      int pg0 = FP8 ? -1 : page_of(page_raw(b0), b0), pg1 = page_of(page_raw(b0 + 1), b0 + 1);
       uint4 x[2][8];
-      load(pg0, 0, x[0]);
-      load(pg0, 1, x[1]);
-      prefetch(pg1);
-      float2 sc0 = scales_of(pg0), sc1 = scales_of(pg1);
+      float2 sc0 = make_float2(1.0f, 1.0f), sc1 = scales_of(pg1);
+      if (!FP8) {
+        load(pg0, 0, x[0]);
+        load(pg0, 1, x[1]);
+        prefetch(pg1);
+      }
 #pragma unroll 1
-      for (int b = s.b_lo; b < s.b_hi; ++b, ++u) {
+      for (int b = b0; b < s.b_hi; ++b) {
+        const bool live = !FP8 || b >= s.b_lo;
         const uint32_t st = u & 1;
         const int pg2 = page_of(raw2, b + 2);
         raw2 = page_raw(b + 3);
         const float2 sc2 = scales_of(pg2);
-        if (u >= 2 && !wait(&room[st], (u >> 1) - 1, keys ? 3 : 4)) break;
+        if (live && u >= 2 && !wait(&room[st], (u >> 1) - 1, keys ? 3 : 4)) break;
         uint8_t* dst = tiles + st * kTileBytes;
 #pragma unroll
         for (int j = 0; j < kBatches; ++j) {
-          store(dst, j, x[j & 1]);
+          if (live) store(dst, j, x[j & 1]);
           // (behind the last block: page 0, not used)
-          if (j + 2 < kBatches) load(pg0, j + 2, x[j & 1]);
-          else load(pg1, j + 2 - kBatches, x[j & 1]);
+          if (j + 2 < kBatches) {
+            if (live) load(pg0, j + 2, x[j & 1]);
+          } else {
+            load(pg1, j + 2 - kBatches, x[j & 1]);
+          }
         }
-        if (!keys) clean_v(dst, b);
-        if (cw == 0) {
-          const float bias = __log2f(sc0.y);
-          const uint32_t flags =
-              (__any_sync(0xffffffffu, pg0 == -2) ? kBadPage : 0u) |
-              (__any_sync(0xffffffffu, lane < kBlkPages && fabsf(bias) > 48.0f) ? kWide : 0u);
-          if (lane < kBlkPages)
-            meta[(u & (kMeta - 1)) * kBlkPages + lane] =
-                make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias), __uint_as_float(flags));
-          if (lane == 0 && (flags & kBadPage)) set_error(ctl, KV_ERR_BAD_PAGE_ID);
+        if (live) {
+          if (!keys) clean_v(dst, b);
+          if (cw == 0) {
+            const float bias = __log2f(sc0.y);
+            const uint32_t flags =
+                (__any_sync(0xffffffffu, pg0 == -2) ? kBadPage : 0u) |
+                (__any_sync(0xffffffffu, lane < kBlkPages && fabsf(bias) > 48.0f) ? kWide : 0u);
+            if (lane < kBlkPages)
+              meta[(u & (kMeta - 1)) * kBlkPages + lane] =
+                  make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias), __uint_as_float(flags));
+            if (lane == 0 && (flags & kBadPage)) set_error(ctl, KV_ERR_BAD_PAGE_ID);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ready[st]);
+          ++u;
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[st]);
         prefetch(pg2);
         pg0 = pg1;
         pg1 = pg2;
