@@ -39,14 +39,14 @@
 //
 // What bounds it, and what was measured (64 query and 8 kv heads, e4m3, TFLOP/s of 4 Hq D
 // a visible pair, of 1,943 that cuBLAS reaches in bf16):
-//   2 x 2048 tokens behind 30k cached   3.27 ms, 1.31e15/s (67%): the tensor pipe is 65%
+//   2 x 2048 tokens behind 30k cached   3.20 ms, 1.33e15/s (68%): the tensor pipe is 65%
 //     busy.  S of 64 columns reads its 32 KB of queries from shared memory again for each
 //     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
 //     time cost less there but leave no room in tensor memory to be a step ahead, and
 //     were slower by 10%.
-//   one prompt of 8192    0.97 ms, 1.13e15 (58%): the same, and about 8 us an item (6 of
+//   one prompt of 8192    0.955 ms, 1.15e15 (59%): the same, and about 8 us an item (6 of
 //     them queries in) that the other items of the CTA hide in part.
-//   16 tokens of 32 requests, 4k-32k cached   0.29 ms, 0.9e15, 3.6 TB/s of cache: 128 rows
+//   16 tokens of 32 requests, 4k-32k cached   0.284 ms, 0.91e15, 3.6 TB/s of cache: 128 rows
 //     make half the products of a block whose keys and values are the same 32 KB.  Bound
 //     by the converters, a block in 2,600 cycles.
 // Two converter warps for each of K and V against four for both in turn: drafts 378 -> 292
@@ -55,7 +55,8 @@
 // registers a thread, and the softmax then spills: chunk 3.3 -> 4.0 ms.  Pages by bulk copies
 // or cp.async through 32 KB of shared memory were slower than the loads (a bulk copy is about
 // 66 cycles of its warp, 16 a block).  All of the loops together have to stay small: the code
-// is 70 KB, and variants that unrolled more ran slower by what the instruction cache misses.
+// is 76 KB, and variants that unrolled more (92 KB: drafts 335 us) ran slower by what the
+// instruction cache misses.
 #include <climits>
 
 #include "common.cuh"
