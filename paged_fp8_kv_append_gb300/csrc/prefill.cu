@@ -39,7 +39,7 @@
 //
 // What bounds it, and what was measured (64 query and 8 kv heads, e4m3, TFLOP/s of 4 Hq D
 // a visible pair, of 1,943 that cuBLAS reaches in bf16):
-//   2 x 2048 tokens behind 30k cached   3.20 ms, 1.33e15/s (68%): the tensor pipe is 65%
+//   2 x 2048 tokens behind 30k cached   3.20 ms, 1.33e15/s (68%): the tensor pipe is 68%
 //     busy.  S of 64 columns reads its 32 KB of queries from shared memory again for each
 //     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
 //     time cost less there but leave no room in tensor memory to be a step ahead, and
