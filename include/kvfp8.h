@@ -398,9 +398,9 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
  * as they come, in one pass over them.  The post gives no position encoding;
  * models of the kind it serves rotate q and k before attention.
  *
- *   total_new      rows of q, k_new, v_new and positions; new_indptr[B] must
- *                  not exceed it (a request whose rows do gets
- *                  KV_ERR_INVALID_ARG and none of them is written).
+ *   total_new      rows of q, k_new, v_new and positions; a request with rows
+ *                  outside them stops the append with KV_ERR_INVALID_ARG, as
+ *                  one that does not fit its page table does.
  *   q              bf16 rows of num_q_heads x head_dim_k values, row t at
  *                  q + t * q_stride (device).  num_q_heads 0: no queries (q
  *                  and q_out may be NULL).

@@ -596,6 +596,7 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
   a.app.k_new = static_cast<const uint16_t*>(k_new);
   a.app.v_new = static_cast<const uint16_t*>(v_new);
   a.app.new_indptr = new_indptr;
+  a.app.total_new = total_new;
   a.app.max_new = max_new_per_req < total_new ? max_new_per_req : total_new;
   a.app.page_table = page_table;
   a.app.exp_tags = exp_tags;

@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
       // handoff fills empty requests from rows its source table maps
       if (n < 0 || L < 0 || n > a.max_new || L + n > (long long)a.max_pages * P ||
           L + n > INT_MAX ||
-          (a.from_pool && n > 0 && (L != 0 || n > (long long)a.src_max_pages * P))) {
+          (a.from_pool && n > 0 && (L != 0 || n > (long long)a.src_max_pages * P)) ||
+          (a.total_new != INT_MAX && n > 0 &&
+           (a.new_indptr[r] < 0 || a.new_indptr[r + 1] > a.total_new))) {
         code = KV_ERR_INVALID_ARG;
       } else {
         if (n > 0 && L % P != 0) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -88,6 +89,8 @@ struct AppendArgs {
   const uint16_t* k_new;  // bf16 bits
   const uint16_t* v_new;
   const int32_t* new_indptr;
+  // rows of the inputs: a request with rows outside is refused (INT_MAX: not given)
+  int32_t total_new = INT_MAX;
   int32_t max_new;
   int32_t* page_table;
   uint32_t* exp_tags;

@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2) 
   if (aborted || n == 0) return;
   if (o0 < 0 || n < 0 || o1 > a.total_rows || start < 0 || start + n > L ||
       start + n > (long long)a.max_pages * P) {
-    if (threadIdx.x == 0 && local == 0) set_error(d.ctl, KV_ERR_INVALID_ARG);
+    // (the first block speaks for a first request that begins behind every item)
+    if (threadIdx.x == 0 && (local == 0 || blockIdx.x == 0)) set_error(d.ctl, KV_ERR_INVALID_ARG);
     return;
   }
   const long long j = start / P + local;

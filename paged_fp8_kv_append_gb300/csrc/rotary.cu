@@ -342,12 +342,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
   const int r = ragged_owner(ap.new_indptr, ap.B, P, blockIdx.x);
   if (r >= d.ctl[KV_CTL_APPEND_STOP]) return;  // not served: nothing of it is written
   const long long i0 = ap.new_indptr[r], i1 = ap.new_indptr[r + 1], n = i1 - i0;
-  if (n <= 0) return;
+  if (n <= 0 || i0 < 0 || i1 > a.total_new) return;  // (the plan has refused it)
   const int local = blockIdx.x - ragged_first(i0, P, r);
-  if (i0 < 0 || i1 > a.total_new) {
-    if (threadIdx.x == 0 && local == 0) set_error(d.ctl, KV_ERR_INVALID_ARG);
-    return;
-  }
   const long long Lnew = ap.seq_lens[r], L0 = Lnew - n;
   const long long jp = L0 / P + local;
   const long long lo = max(jp * P, L0), hi = min((jp + 1) * P, Lnew);

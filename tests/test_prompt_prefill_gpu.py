@@ -255,3 +255,20 @@ def test_no_queries(kv):
     out = _run(f, torch.zeros((0, 8, 128), dtype=torch.bfloat16), [0], extra=5)
     assert bool((out == 7.0).all()) and f.pool.error() == 0
     assert math.isfinite(SCALE)
+
+
+@pytest.mark.parametrize("ind", [[0, 40, 81], [-5, 40, 60], [100000, 100040, 100060], [0, 40, 20]])
+def test_rows_outside_the_queries(kv, ind):
+    """Requests whose rows lie outside q are refused, wherever they begin."""
+    f = Filled(kv, [60, 90], hkv=2, seed=67)
+    q = _queries(f, [80], 8, 68)
+    out = torch.full((80, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(f.pool.prefill_workspace_size(2, 8, 80), dtype=torch.uint8, device="cuda")
+    f.pool.prefill_attn(2, 8, q.cuda(), torch.tensor(ind, dtype=torch.int32).cuda(), f.table_d, f.lens_d, None,
+                        SCALE, out, ws)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    if ind[0] == 0:
+        f.B = 1
+        _check(f, q[:40], [40], out)
+    else:
+        assert bool((out[:40] == 7.0).all())

@@ -117,3 +117,17 @@ def test_graph_and_other_stream(kv):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+@pytest.mark.parametrize("ind", [[0, 40, 81], [-5, 40, 60], [100000, 100040, 100060], [0, 40, 20]])
+def test_rows_outside_the_outputs(kv, ind):
+    """Requests whose rows do not fit the outputs are refused, wherever they begin."""
+    f = Filled(kv, [60, 60], hkv=2, seed=91)
+    k = torch.full((80, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    f.pool.read_rows(2, f.table_d, f.lens_d, None, torch.tensor(ind, dtype=torch.int32).cuda(), None, k, v)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    rows = f.rows(0, "k")[:40] if ind[0] == 0 else None
+    assert bool((k[40 if ind[0] == 0 else 0:] == 7.0).all() if ind[0] >= 0 else (k[:40] == 7.0).all())
+    if rows is not None:
+        assert bool(((k[:40].cpu().double() - rows).abs() <= (2.0 ** -8 + 2.0 ** -23) * rows.abs()).all())

@@ -296,6 +296,24 @@ def test_rows_beyond_the_inputs(kv):
     assert torch.equal(before.cpu()[keep], f.pool.k_cache.cpu()[keep])
 
 
+@pytest.mark.parametrize("ind", [[0, 4, 12], [-4, 4, 8], [100000, 100004, 100008], [0, 4, 2]])
+def test_rows_outside_the_inputs_are_not_served(kv, ind):
+    """No page is popped and no length grows for a request with rows outside the inputs, nor for
+    those behind it."""
+    f = Filled(kv, [3, 5], seed=47, spare=8, extra_width=8)
+    host, dev = _inputs(f, [4, 4], 4, 128, 1, 48)
+    before = [x.clone() for x in (f.pool.k_cache, f.pool.v_cache, f.pool.tags, f.table_d)]
+    out = _call(f, [4, 4], 4, dev, False, max_new=8, ind=torch.tensor(ind, dtype=torch.int32, device="cuda"))
+    first = ind[0] == 0  # request 0 is in order
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    assert f.lens_d.tolist() == [7 if first else 3, 5]
+    assert int(f.pool.ctl[0]) == f.free_head
+    assert bool((out[4 if first else 0:] == 7.0).all())
+    for x, y in zip(before, (f.pool.k_cache, f.pool.v_cache, f.pool.tags, f.table_d)):
+        if not (first and x.dim() == 4):
+            assert torch.equal(x, y)
+
+
 def test_axis_out_of_range(kv):
     f = Filled(kv, [0], seed=33, spare=8, extra_width=8)
     host, dev = _inputs(f, [4], 4, 32, 1, 34)
