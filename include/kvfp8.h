@@ -423,7 +423,8 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
  * (positions may be negative; a frequency that is not finite gives NaN).  Keys
  * stay in fp32 between the rotation and their one rounding: e4m3 pages take
  * their scale from the rotated fp32 rows, bf16 pools round them to bf16.  q_out
- * must not overlap k_new, v_new or another row's q.  Everything else (page pops, tags, stops, partly filled pages, both scale modes, new_indptr,
+ * must not overlap k_new, v_new or another row's q.  Everything else (page pops,
+ * tags, stops, partly filled pages, both scale modes, new_indptr,
  * max_new_per_req, page_table, exp_tags, seq_lens) is as for
  * kv_append_quantize; a request that is not served gets no q_out rows.
  * GQA pools with page_size * head_dim <= 2048 for K and V; others return

@@ -42,8 +42,8 @@
 //   2 x 2048 tokens behind 30k cached   3.20 ms, 1.33e15/s (68%): the tensor pipe is 68%
 //     busy.  S of 64 columns reads its 32 KB of queries from shared memory again for each
 //     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
-//     time cost less there but leave no room in tensor memory to be a step ahead, and
-//     were slower by 10%.
+//     time cost less there but leave no room in tensor memory to be a step ahead: 4.25 ms,
+//     the softmax warps wait for their scores.
 //   one prompt of 8192    0.955 ms, 1.15e15 (59%): the same, and about 8 us an item (6 of
 //     them queries in) that the other items of the CTA hide in part.
 //   16 tokens of 32 requests, 4k-32k cached   0.284 ms, 0.91e15, 3.6 TB/s of cache: 128 rows

@@ -139,7 +139,8 @@ enum Shape { kTile16x128, kLatent, kAny };
 // SM read the 16 x 128 tiles back at 6.3 TB/s, 4 (3) at 6.0, 2 at 6.1 (bytes
 // read and written, 32 requests of 4k to 32k rows, 8 heads).
 template <bool FP8, int SHAPE>
-__global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2) read_rows_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2)
+    read_rows_kernel(const ReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const kv_pool_desc& d = a.d;

@@ -10,7 +10,8 @@
 // hold a frequency as turns * 2^64, and the 64-bit integer product drops the
 // whole turns by itself and leaves the fraction, off by no more than position
 // times the table's own rounding (fp64: 2^-55 turns for a frequency of 1), with
-// two integer multiply-adds where fp64 (scarce here) would take six operations.  Sine and cosine of the fraction are fp32.  A rotated key
+// two integer multiply-adds where fp64 (scarce here) would take six operations.
+// Sine and cosine of the fraction are fp32.  A rotated key
 // stays in fp32 until its one rounding: to e4m3 by its page's scale (amax/448
 // of the page's rotated rows, as kv_append_quantize takes it of the rows it is
 // given), or to bf16.
@@ -359,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
       const Freq f = freq[i];
       long long turns = 0;
       if (f.axis >= 0)
-        turns = (long long)((unsigned long long)(long long)a.positions[(long long)f.axis * a.total_new + row0 + t] *
+        turns = (long long)((unsigned long long)(long long)
+                                a.positions[(long long)f.axis * a.total_new + row0 + t] *
                             (unsigned long long)f.turns);
       else
         bad_axis = true;
@@ -391,9 +393,10 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
   split = min(split, a.app.d.num_kv_heads);
   // at most 32 KB: P * Dk <= 2048
   const size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
+  const bool il = a.interleaved != 0;
   const auto kernel = a.app.d.head_dim_k == 128
-                          ? (a.interleaved ? append_rotary_kernel<128, true> : append_rotary_kernel<128, false>)
-                          : (a.interleaved ? append_rotary_kernel<0, true> : append_rotary_kernel<0, false>);
+                          ? (il ? append_rotary_kernel<128, true> : append_rotary_kernel<128, false>)
+                          : (il ? append_rotary_kernel<0, true> : append_rotary_kernel<0, false>);
   e = launch_pdl(kernel, dim3((unsigned)items, split), dim3(kThreads), smem, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
