@@ -44,7 +44,7 @@
 //     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
 //     time cost less there but leave no room in tensor memory to be a step ahead: 4.25 ms,
 //     the softmax warps wait for their scores.
-//   one prompt of 8192    0.955 ms, 1.15e15 (59%): the same, and about 8 us an item (6 of
+//   one prompt of 8192    0.93 ms, 1.18e15 (61%): the same, and about 8 us an item (6 of
 //     them queries in) that the other items of the CTA hide in part.
 //   16 tokens of 32 requests, 4k-32k cached   0.284 ms, 0.91e15, 3.6 TB/s of cache: 128 rows
 //     make half the products of a block whose keys and values are the same 32 KB.  Bound
@@ -75,12 +75,16 @@ constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps;  // the scheduler is behind it
 constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 3) * 32;
-// Costs, about 0.65 us each: a block of an item with two tiles, one of an item with a
+// Costs, about 0.65 us each (e4m3): a block of an item with two tiles, one of an item with a
 // single tile (1.95 and 1.4 us: the keys and values are as many, the rows half), and what an
-// item costs beside its blocks (queries in, output out).  At 2 : 1 for the blocks four ragged
-// prompts took 973 us, at 3 : 2 856; leads of 10 and 8 cost one prompt of 8k tokens 9%.
+// item costs beside its blocks (queries in, output out; fewer of a bf16 pool's blocks, which
+// take longer).  At 2 : 1 for the blocks four ragged prompts took 973 us, at 3 : 2 856; one
+// prompt of 8k tokens takes 994, 954, 929 and 936 us at leads of 11, 12, 13 and 16, the bf16
+// prompts 848, 850, 882 at 11, 12, 13.
 constexpr int kCostTwo = 3, kCostOne = 2;
-__host__ __device__ inline long long item_lead(int nrows) { return nrows > 128 ? 12 : 9; }
+__host__ __device__ inline int item_lead(int nrows, bool fp8) {
+  return nrows > 128 ? (fp8 ? 13 : 11) : 9;
+}
 constexpr int kMeta = 4;  // block records in flight
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
@@ -186,7 +190,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
           it.z = (int)min((long long)kItemRows, n * p.G - row0);
           const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
           it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = item_lead(it.z) + (long long)it.w * (it.z > kTile ? kCostTwo : kCostOne);
+          cost = item_lead(it.z, p.d.dtype == KV_DTYPE_E4M3) +
+                 (long long)it.w * (it.z > kTile ? kCostTwo : kCostOne);
         }
       }
       a.ws.items[v] = it;
@@ -232,13 +237,13 @@ static_assert(sizeof(Piece) == 48, "ring slots");
 
 // The scheduler's place on the cost axis.
 struct Walk {
-  int v, h;
+  int v, h, lead;
   long long x0;  // cost position of (item v, head h)
   Piece s;
   // of its first block, and behind its last
-  __device__ __forceinline__ long long blocks0() const { return x0 + item_lead(s.nrows); }
+  __device__ __forceinline__ long long blocks0() const { return x0 + lead; }
   __device__ __forceinline__ long long cost() const {
-    return item_lead(s.nrows) + (long long)s.nb * s.w();
+    return lead + (long long)s.nb * s.w();
   }
 };
 
@@ -254,6 +259,7 @@ __device__ __forceinline__ void walk_item(Walk& c, const Args& a) {
   c.s.r = it.x;
   c.s.row0 = it.y;
   c.s.nrows = it.z;
+  c.lead = item_lead(it.z, a.p.d.dtype == KV_DTYPE_E4M3);
   c.s.nb = it.w;
   c.s.L = a.p.seq_lens[it.x];
   c.s.q0 = a.p.q_indptr[it.x];
