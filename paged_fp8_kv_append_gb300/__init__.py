@@ -145,9 +145,16 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# (a call of a few microseconds: names found once)
+_Tensor, _I32, _BF16, _U8, _F64 = (torch.Tensor, torch.int32, torch.bfloat16, torch.uint8,
+                                   torch.float64)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # (absent in a build without CUDA)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _device():
     """The current device's number, which a call's tensors must lie on."""
-    return torch._C._cuda_getDevice()
+    return _current_device()
 
 
 def _arg(t, dtype, name, dev, least=0):
@@ -156,8 +163,8 @@ def _arg(t, dtype, name, dev, least=0):
     calls whose device time is a few microseconds."""
     if t is None:
         return None
-    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev
-            or not t.is_contiguous() or t.numel() < least):
+    if (type(t) is not _Tensor or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous() or (least and t.numel() < least)):
         _ptr(t, dtype, name)  # the error by its name
         if t.get_device() != dev:
             raise ValueError(f"{name}: must be on the current device")
@@ -169,9 +176,9 @@ def _arg(t, dtype, name, dev, least=0):
 def _rows(t, rows, heads, dim, name, dev):
     """Device pointer and row stride (elements) of a bf16 [rows][heads][dim]
     tensor whose rows may lie apart (a part of a wider projection)."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: must be a CUDA tensor on the current device")
@@ -185,7 +192,7 @@ def _rows(t, rows, heads, dim, name, dev):
 
 def _stream_on(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _raw_stream(dev)
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError("stream: must be a stream of the current device")
     return _stream(stream)
@@ -350,14 +357,14 @@ def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_ne
     rows any multiple of 8 elements apart; positions int32 [axes][rows]."""
     rows, Hk, Dk = k_new.shape
     B, num_q_heads, axes, pairs = int(B), int(num_q_heads), positions.shape[0], inv_freq.numel()
-    dev, i32 = _device(), torch.int32
+    dev = _device()
     if positions.shape != (axes, rows):
         raise ValueError("positions: expected [axes][rows of k_new]")
     qp = qo = None
     qs = 0
     if num_q_heads > 0:
         qp, qs = _rows(q, rows, num_q_heads, Dk, "q", dev)
-        qo = _arg(q_out, torch.bfloat16, "q_out", dev, rows * num_q_heads * Dk)
+        qo = _arg(q_out, _BF16, "q_out", dev, rows * num_q_heads * Dk)
         if qo == qp and qs != num_q_heads * Dk:
             raise ValueError("q_out may be q only when q is contiguous")
     kp, ks = _rows(k_new, rows, Hk, Dk, "k_new", dev)
@@ -368,13 +375,13 @@ def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_ne
     tags = exp_tags.dtype if exp_tags.dtype in _U32 else _U32
     st = _lib.kv_append_rotary(
         handle, _stream_on(stream, dev), B, num_q_heads, rows, qp, qs, kp, ks, vp, vs,
-        _arg(new_indptr, i32, "new_indptr", dev, B + 1), int(max_new_per_req),
-        _arg(positions, i32, "positions", dev), axes,
-        _arg(pair_axis, torch.uint8, "pair_axis", dev),
-        _arg(inv_freq, torch.float64, "inv_freq", dev), 2 * pairs, int(interleaved), qo,
-        _arg(page_table, i32, "page_table", dev, B * max_pages),
+        _arg(new_indptr, _I32, "new_indptr", dev, B + 1), int(max_new_per_req),
+        _arg(positions, _I32, "positions", dev), axes,
+        _arg(pair_axis, _U8, "pair_axis", dev),
+        _arg(inv_freq, _F64, "inv_freq", dev), 2 * pairs, int(interleaved), qo,
+        _arg(page_table, _I32, "page_table", dev, B * max_pages),
         _arg(exp_tags, tags, "exp_tags", dev, B * max_pages), max_pages,
-        _arg(seq_lens, i32, "seq_lens", dev, B))
+        _arg(seq_lens, _I32, "seq_lens", dev, B))
     if st:
         _check(st, "kv_append_rotary")
 
@@ -384,16 +391,16 @@ def kv_read_rows(handle, B, page_table, seq_lens, row_start, out_indptr, abort_m
     """Cached rows row_start[r] .. of each request as contiguous bf16 rows
     out_indptr[r] .. of k_out / v_out (v_out None for latent pools)."""
     B, max_pages, rows = int(B), page_table.shape[-1], k_out.shape[0]
-    dev, i32 = _device(), torch.int32
+    dev = _device()
     if v_out is not None and v_out.shape[0] != rows:
         raise ValueError("k_out and v_out must have the same rows")
     st = _lib.kv_read_rows(
         handle, _stream_on(stream, dev), B,
-        _arg(page_table, i32, "page_table", dev, B * max_pages), max_pages,
-        _arg(seq_lens, i32, "seq_lens", dev, B), _arg(row_start, i32, "row_start", dev, B),
-        _arg(out_indptr, i32, "out_indptr", dev, B + 1), rows,
-        _arg(abort_mask, torch.uint8, "abort_mask", dev, B),
-        _arg(k_out, torch.bfloat16, "k_out", dev), _arg(v_out, torch.bfloat16, "v_out", dev))
+        _arg(page_table, _I32, "page_table", dev, B * max_pages), max_pages,
+        _arg(seq_lens, _I32, "seq_lens", dev, B), _arg(row_start, _I32, "row_start", dev, B),
+        _arg(out_indptr, _I32, "out_indptr", dev, B + 1), rows,
+        _arg(abort_mask, _U8, "abort_mask", dev, B),
+        _arg(k_out, _BF16, "k_out", dev), _arg(v_out, _BF16, "v_out", dev))
     if st:
         _check(st, "kv_read_rows")
 
@@ -407,17 +414,17 @@ def paged_prefill_attn(handle, B, num_q_heads, q, q_indptr, page_table, seq_lens
     """Causal attention of a ragged batch's new tokens (q [total_q][heads][128],
     request r's at q_indptr[r] ..) over the paged cache (see kvfp8.h)."""
     B, max_pages, total_q = int(B), page_table.shape[-1], q.shape[0]
-    dev, i32 = _device(), torch.int32
+    dev = _device()
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     st = _lib.paged_prefill_attn(
         handle, _stream_on(stream, dev), B, int(num_q_heads), total_q,
-        _arg(q, torch.bfloat16, "q", dev, total_q * int(num_q_heads) * 128),
-        _arg(q_indptr, i32, "q_indptr", dev, B + 1),
-        _arg(page_table, i32, "page_table", dev, B * max_pages), max_pages,
-        _arg(seq_lens, i32, "seq_lens", dev, B),
-        _arg(abort_mask, torch.uint8, "abort_mask", dev, B), float(sm_scale),
-        _arg(out, torch.bfloat16, "out", dev), _arg(workspace, torch.uint8, "workspace", dev),
+        _arg(q, _BF16, "q", dev, total_q * int(num_q_heads) * 128),
+        _arg(q_indptr, _I32, "q_indptr", dev, B + 1),
+        _arg(page_table, _I32, "page_table", dev, B * max_pages), max_pages,
+        _arg(seq_lens, _I32, "seq_lens", dev, B),
+        _arg(abort_mask, _U8, "abort_mask", dev, B), float(sm_scale),
+        _arg(out, _BF16, "out", dev), _arg(workspace, _U8, "workspace", dev),
         workspace.numel())
     if st:
         _check(st, "paged_prefill_attn")
