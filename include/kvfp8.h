@@ -498,7 +498,7 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * request may or may not be.  Other requests are not affected.  GQA pools with
  * head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
  * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31; others return
- * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or bf16 for the
+ * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts for the
  * product with V, sums and maxima in fp32.  Results do not depend on which
  * requests are run together beyond rounding, and are the same from run to run.
  * Calls that may run at the same time need a workspace each.  Three kernel

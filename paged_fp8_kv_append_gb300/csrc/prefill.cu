@@ -21,7 +21,10 @@
 // Per CTA (one per SM, 15 warps of 128 registers):
 //   softmax A (0-3), B (4-7)  a thread per row: a unit's 64 scores from tensor memory
 //                   into registers, exp2 against the row's reference M as it stands, P back
-//                   to tensor memory as the A operand of PV.  The unit's maximum is taken
+//                   to tensor memory as the A operand of PV (e4m3 pools: f16; bf16 pools: two
+//                   bf16 parts, which keep 16 bits of a weight as the decode attention does, for
+//                   a second PV: one part took 854 us for four ragged prompts, two take 1,038, and
+//                   a weight of 8 bits is off by 2^-9).  The unit's maximum is taken
 //                   only in a first unit, for a row that has seen nothing yet, or when the
 //                   P of a row sum to 2^15 or more (f16 P stay finite below that); M then
 //                   grows if it must and the output accumulator is rescaled by the same
@@ -101,7 +104,8 @@ constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
-// tensor memory columns: two S of 64 (P in the first half of each) and O of each tile
+// tensor memory columns: two S of 64 (P in the first half of each; bf16 pools: its second parts
+// in the second) and O of each tile
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_o(int x) { return 256u + 128u * x; }
 
@@ -744,8 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           if (n == 0 && piece > 0 && !wait(&bar.epi_done[x], piece - 1, 7)) break;
           if (!wait(&bar.p_ready[b], (t0 + n) >> 1, 5)) break;
           tc_fence_after();
-          mma_ts4(leader, tm + tmem_o(x), tm + 64 * b,
-                  dv + (uint32_t)((st * kTileBytes + h * kHalf) >> 4), kIdPv, n > 0 ? 1 : 0);
+          const uint64_t vv = dv + (uint32_t)((st * kTileBytes + h * kHalf) >> 4);
+          mma_ts4(leader, tm + tmem_o(x), tm + 64 * b, vv, kIdPv, n > 0 ? 1 : 0);
+          if (!FP8) mma_ts4(leader, tm + tmem_o(x), tm + 64 * b + 32, vv, kIdPv, 1);
           if (leader) {
             mma_commit(&bar.pv_done[x]);
             if (h == 1 || !both) mma_commit(&bar.v_free[st]);
@@ -932,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           // unit, a row that has seen nothing yet, or a sum beyond that takes the unit's
           // maximum, and P again.
           bool take = n == 0 || __any_sync(0xffffffffu, M == -INFINITY);
-          uint32_t pk[32];
+          uint32_t pk[32], pl[FP8 ? 1 : 32];
           uint64_t add_l;
 #pragma unroll 1
           for (;;) {
@@ -984,7 +989,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum = k == 0 ? pack2(e0, e1) : add2(sum, pack2(e0, e1));
-                pk[8 * g + k / 2] = pack_p<FP8>(e0, e1);
+                const uint32_t hi = pack_p<FP8>(e0, e1);
+                pk[8 * g + k / 2] = hi;
+                if (!FP8)
+                  pl[(8 * g + k / 2) % (FP8 ? 1 : 32)] =
+                      pack_p<false>(e0 - bf16_lo(hi), e1 - bf16_hi(hi));
               }
               raw = g == 0 ? sum : add2(raw, sum);
               if (FP8) {
@@ -1018,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
             }
           }
           tmem_st32u(ts, pk);
+          if constexpr (!FP8) tmem_st32u(ts + 32, pl);
           tmem_wait_st();
         }
         tc_fence_before();

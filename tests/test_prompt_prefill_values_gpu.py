@@ -1,0 +1,136 @@
+"""paged_prefill_attn where values are extreme: rows that are no numbers, V scales of zero and
+near fp32's ends, weights far below a row's largest, weights of a bf16 pool that nearly cancel.
+
+Bound of an output o = sum_j p_j v_j / sum_j p_j against the 64-bit form, A = sum_j p_j |v_j| /
+sum_j p_j, S = the row's largest sum over dims of |q k| in log2 units (after scaling), L the
+length:
+  bf16 output       2^-8 |o|, and half the smallest step, 2^-134
+  weights (e4m3)    f16: 2^-11 of each, or half of f16's smallest step (2^-25) where that is more:
+                    the reference is 2^6 or more below a row's largest p * (V scale), so at most
+                    2^-31 of that largest, for every key, times its code
+  weights (bf16)    two bf16 parts: 2^-8 of the second, which is 2^-8 of the weight: 2^-16 A
+  scores            128 products of exact factors (e4m3: f16 holds both; bf16) summed in fp32, and
+                    three roundings of the exponent: 132 * 2^-24 S; ln 2 times that is the
+                    weight's, and the sum's again; exp2 adds 2^-22, twice: 2^-21
+  smallest weights  fp32 has no normal values below 2^-126, and exp2 gives zero there: a weight
+                    below 2^-125 of the sum (which is at least half of its own reference) may be
+                    left out: 2^-125 |v_j| for every key
+  sums              L terms, each at most 2^-23 off its sum (the tensor cores may cut), in o and
+                    in the sum of the weights; 64 more for rescaling and merging: (L + 64) 2^-22
+"""
+import math
+
+import pytest
+import torch
+
+from promptref import Filled, attention, e4m3_values, indptr
+
+pytestmark = pytest.mark.gpu
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(scope="module")
+def kv():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import paged_fp8_kv_append_gb300 as kv
+
+    return kv
+
+
+def _queries(new, hq, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((sum(new), hq, 128), generator=g) * scale).to(torch.bfloat16)
+
+
+def _load(f):
+    """The pool's device copies of what a test has changed."""
+    f.pool.k_cache.copy_(f.k)
+    f.pool.v_cache.copy_(f.v)
+    if f.fp8:
+        f.pool.k_scale.copy_(f.ks)
+        f.pool.v_scale.copy_(f.vs)
+
+
+def _run(f, q, new, copies=1):
+    """The outputs; with `copies`, [copies][rows][heads][dim] of as many requests that share the
+    pages of f's one (so many items that few are cut)."""
+    q = q.repeat(copies, 1, 1)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((f.pool.prefill_workspace_size(f.B * copies, q.shape[1], q.shape[0]),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    f.pool.prefill_attn(f.B * copies, q.shape[1], q.cuda(), indptr(new * copies).cuda(),
+                        f.table_d.repeat(copies, 1), f.lens_d.repeat(copies), None, SCALE, out, ws)
+    got = out.cpu().double()
+    assert f.pool.error() == 0
+    return got if copies == 1 else got.unflatten(0, (copies, -1))
+
+
+def _codes(f, b):
+    """|V| of request b in units of its pages' scales, [L][heads][dim]."""
+    at = torch.arange(f.lens[b])
+    c = f.v[f.table[b].long()[at // 16], :, :, at % 16]
+    return e4m3_values()[c.long()].abs()
+
+
+def _check(f, q, new, got, rows=None):
+    """`rows`: a truth value for each (query row, head) that is looked at."""
+    ind = indptr(new)
+    for b in range(f.B):
+        lo, hi = int(ind[b]), int(ind[b + 1])
+        if lo == hi:
+            continue
+        qb, k, v, L = q[lo:hi].double(), f.rows(b, "k"), f.rows(b, "v"), f.lens[b]
+        old = L - (hi - lo)
+        ref, mag = attention(qb, k, v, SCALE, old), attention(qb, k, v.abs(), SCALE, old)
+        g = q.shape[1] // f.hkv
+        big = torch.einsum("nhd,lhd->hnl", qb.abs(), k.abs().repeat_interleave(g, 1)).amax(-1)
+        S = big.t()[..., None] * SCALE / math.log(2)  # [n][Hq][1]
+        c = (2 * math.log(2) * 132 * 2.0 ** -24 * S + 2.0 ** -21 + (L + 64) * 2.0 ** -22
+             + (2.0 ** -11 if f.fp8 else 2.0 ** -16))
+        bound = 2.0 ** -8 * ref.abs() + c * mag + 2.0 ** -134
+        if f.fp8:
+            s = torch.einsum("nhd,lhd->hnl", qb, k.repeat_interleave(g, 1)) * SCALE
+            see = torch.arange(L)[None] <= old + torch.arange(hi - lo)[:, None]
+            s = s.masked_fill(~see[None], -math.inf)
+            vs = f.vs[f.table[b].long()[torch.arange(L) // 16]].double()
+            p = torch.softmax(s, -1)
+            top = (p * vs.t().repeat_interleave(g, 0)[:, None]).amax(-1).t()[..., None]  # [n][Hq][1]
+            codes = torch.einsum("nl,lhd->nhd", see.double(), _codes(f, b)).repeat_interleave(g, 1)
+            values = torch.einsum("nl,lhd->nhd", see.double(), v.abs()).repeat_interleave(g, 1)
+            bound = bound + 2.0 ** -31 * top * codes + 2.0 ** -125 * values
+        err = (got[..., lo:hi, :, :] - ref).abs() / bound
+        if rows is not None:
+            err = err[rows[lo:hi]]
+        assert bool((err <= 1.0).all()), (b, float(err.max()))
+
+
+# (lengths with the new tokens, new tokens, query heads, kv heads): an item of one tile, of two,
+# and items that are cut over CTAs
+KINDS = {
+    "one tile": ([300], [16], 8, 1),
+    "two tiles": ([290], [64], 8, 2),
+    "two requests": ([200, 70], [3, 40], 8, 2),
+    "single token, cut": ([9000], [1], 8, 1),
+    "cut": ([2600], [130], 16, 2),
+}
+
+
+@pytest.mark.parametrize("new", [1, 16, 60])
+@pytest.mark.parametrize("steps", [-16.8, -2.8, -0.9, 1.8])
+def test_bf16_weights_that_nearly_cancel(kv, new, steps):
+    """Two kinds of keys whose weights lie less than half a bf16 step apart, with values +1 and -1:
+    the output is the difference."""
+    L = 320
+    f = Filled(kv, [L], hkv=1, fp8=False, seed=217)
+    for j in range(L):
+        page = int(f.table[0, j // 16])
+        f.k[page, 0, j % 16] = 0
+        f.v[page, 0, :, j % 16] = 1.0 if j % 2 else -1.0
+        if j % 2:
+            f.k[page, 0, j % 16, 0] = 1.0
+    _load(f)
+    q = torch.zeros((new, 8, 128), dtype=torch.bfloat16)
+    q[..., 0] = math.log1p(steps * 2.0 ** -9) / SCALE
+    _check(f, q, [new], _run(f, q, [new]))
