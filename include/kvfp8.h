@@ -490,7 +490,9 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  *   workspace   device scratch of at least paged_prefill_workspace_size bytes,
  *               256-byte aligned; contents need not be initialised.
  * Query i of the n of request r (L = seq_lens[r]) attends to positions
- * 0 .. L - n + i; a query with no visible position gets zeros.  A request
+ * 0 .. L - n + i; a query with no visible position gets zeros, and one with a
+ * visible score that is not a number (NaN or infinite queries, NaN keys) gets
+ * NaN.  A request
  * with a negative length or count, one beyond its page table or longer than
  * 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is not written;
  * one whose needed pages include an id outside [0, num_pages) sets

@@ -1038,6 +1038,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       if (!go) break;
       if (!stage(piece + 1)) break;
       // ---- the piece's output
+      // (a sum that is no number marks its part so: every part merged with it becomes NaN)
+      if (l != l) M = INFINITY;
       const bool two = !both;  // A and B hold parts of the same rows
       if (!wait(&bar.o_full[x], (ph & kO) != 0, 13)) break;
       ph ^= kO;
@@ -1065,7 +1067,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (warp_live) {
           const bool bad = (flags & kBadPage) != 0, live = tile0 + row < rows;
           const bool whole = pc->b_lo == 0 && pc->b_hi == pc->nb;
-          const float scale = l > 0.0f ? 1.0f / l : 0.0f;
+          // zeros only for a row that sees no position: a sum of 0 or NaN goes into the output
+          const bool none = lim < 0;  // (of a whole item: its first block is block 0)
+          const float scale = 1.0f / l;
           const int slot = 2 * (int)blockIdx.x + (pc->b_lo > 0 ? 0 : 1), tg = pc->row0 + tile0 + row;
           const int t = tg / p.G, g = tg - t * p.G;
           uint16_t* out = p.out + ((long long)(pc->q0 + t) * p.Hq + pc->h * p.G + g) * kD;
@@ -1090,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
                 y.y = pack_p<false>(o[k + 2] * scale, o[k + 3] * scale);
                 y.z = pack_p<false>(o[k + 4] * scale, o[k + 5] * scale);
                 y.w = pack_p<false>(o[k + 6] * scale, o[k + 7] * scale);
-                *reinterpret_cast<uint4*>(out + 16 * c + k) = l > 0.0f ? y : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(out + 16 * c + k) = none ? make_uint4(0, 0, 0, 0) : y;
               }
             } else if (live && !whole) {
 #pragma unroll
@@ -1171,14 +1175,16 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const Args a) {
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  // zeros only for a row that sees no position
+  const int q0 = p.q_indptr[it.x];
+  const bool none = p.seq_lens[it.x] - (p.q_indptr[it.x + 1] - q0) + (it.y + rr) / p.G < 0;
+  const float inv = none ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     tile[lane][warp + 8 * k] = make_uint2(pack_p<false>(acc[k].x * inv, acc[k].y * inv),
                                           pack_p<false>(acc[k].z * inv, acc[k].w * inv));
   if (warp == 0) skip[lane] = !live || bad;
   __syncthreads();
-  const int q0 = p.q_indptr[it.x];
   for (int i = warp; i < 32; i += 8) {
     if (skip[i]) continue;
     const int tg = it.y + blockIdx.y * 32 + i, t = tg / p.G, g = tg - t * p.G;

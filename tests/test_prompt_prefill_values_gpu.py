@@ -117,6 +117,57 @@ KINDS = {
 }
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_queries_that_are_no_numbers(kv, kind, fp8):
+    """A query of NaN or infinities has weights that are no numbers: its row is NaN, whole, and
+    every other is right."""
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, fp8=fp8, seed=201)
+    q = _queries(new, hq, 202)
+    t = q.shape[0]
+    bad = torch.zeros(t, hq, dtype=torch.bool)
+    for i, (row, head, x) in enumerate(((0, 1, math.nan), (t // 2, hq - 1, math.inf), (t - 1, 2, -math.inf))):
+        q[row, head, 5 * i] = x
+        bad[row, head] = True
+    got = _run(f, q, new)
+    assert bool(torch.isnan(got[bad]).all())
+    clean = q.clone()
+    clean[bad] = 0
+    _check(f, clean, new, got, ~bad)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("what", ["key"])
+@pytest.mark.parametrize("at", [0, 70, 130, -3])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_keys_that_are_no_numbers(kv, kind, at, what, fp8):
+    """One key with a NaN, or a page whose K scale is one: the rows that see it are NaN, whole, and
+    the others are right."""
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, fp8=fp8, seed=203)
+    at = at % lens[0]
+    page, head = int(f.table[0, at // 16]), hkv - 1
+    clean = (f.k.clone(), None if f.ks is None else f.ks.clone())
+    if what == "key":
+        f.k[page, head, at % 16, 9] = 0x7F if fp8 else math.nan
+    elif fp8:
+        f.ks[page, head] = math.nan
+        at = at // 16 * 16
+    else:
+        pytest.skip("a bf16 pool has no scales")
+    _load(f)
+    q = _queries(new, hq, 204)
+    got = _run(f, q, new)
+    g = hq // hkv
+    bad = torch.zeros(q.shape[0], hq, dtype=torch.bool)
+    sees = torch.arange(new[0]) + lens[0] - new[0] >= at
+    bad[:new[0], head * g:] = sees[:, None]
+    assert bool(bad.any()) and bool(torch.isnan(got[bad]).all())
+    f.k, f.ks = clean
+    _check(f, q, new, got, ~bad)
+
+
 @pytest.mark.parametrize("new", [1, 16, 60])
 @pytest.mark.parametrize("steps", [-16.8, -2.8, -0.9, 1.8])
 def test_bf16_weights_that_nearly_cancel(kv, new, steps):
