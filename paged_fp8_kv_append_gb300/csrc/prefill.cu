@@ -89,6 +89,10 @@ __host__ __device__ inline int item_lead(int nrows, bool fp8) {
   return nrows > 128 ? (fp8 ? 13 : 11) : 9;
 }
 constexpr int kMeta = 4;  // block records in flight
+// Where a unit's maximum is taken, the reference of a row of an e4m3 pool goes this far (binades)
+// below it: f16 weights lose bits below 2^-14 and end at 2^-25, so what lies far below a row's
+// largest keeps as many more; upwards 2^15 are allowed anyway.
+constexpr float kRoom = 6.0f;
 
 // shared memory: operand tiles of two 64-wide halves, [128 rows][128 B] each
 constexpr int kHalf = 128 * 128, kTileBytes = 2 * kHalf;
@@ -830,8 +834,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   } else {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
-    // exponent, and M is the largest score + bias of a unit at which it was last taken, so
-    // that P stay below 2^15 whatever the scales; the row sum takes the bias back out.
+    // exponent, and M is the largest score + bias of a unit at which it was last taken (kRoom
+    // below it), so that P stay below 2^15 whatever the scales; the row sum takes the bias back
+    // out.
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t to = tmem + tmem_o(x) + lanes;
@@ -962,9 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               }
               float alpha = 1.0f;
               if (mx > M + 8.0f) {
-                alpha = M == -INFINITY ? 0.0f : ex2(M - mx);
+                const float to = FP8 ? mx - kRoom : mx;
+                alpha = M == -INFINITY ? 0.0f : ex2(M - to);
                 l *= alpha;
-                M = mx;
+                M = to;
               }
               if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
                 if (!wait(&bar.pv_done[x], t - 1, 12)) break;  // PV of the unit before

@@ -168,6 +168,44 @@ def test_keys_that_are_no_numbers(kv, kind, at, what, fp8):
     _check(f, q, new, got, ~bad)
 
 
+@pytest.mark.parametrize("nats", [10.0, 18.0])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("at", [0, 2500])
+def test_a_key_far_above_the_rest(kv, at, new, nats):
+    """A key of value zero that leads by 10 or 18 nats: what the others, 2^-26 of it each, add up to
+    is the whole output."""
+    L = 6000
+    f = Filled(kv, [L], hkv=1, seed=213)
+    f.k[f.table[0, :L // 16].long(), :, :, 0] = 0  # no other key has a part of dim 0
+    f.ks.fill_(1e-4)
+    page = int(f.table[0, at // 16])
+    f.k[page] = 0
+    f.k[page, 0, at % 16, 0] = 0x38  # 1.0
+    f.ks[page] = 1.0
+    f.v &= 0x7F  # all other values are positive
+    f.v[f.v == 0x7F] = 0x7E
+    f.v[page, :, :, at % 16] = 0
+    f.vs.fill_(0.01)
+    _load(f)
+    q = _queries([new], 8, 214, 0.01)
+    q[..., 0] = nats / SCALE
+    _check(f, q, [new], _run(f, q, [new], copies=152))
+
+
+@pytest.mark.parametrize("at", [3, 400])
+def test_a_page_of_a_large_scale(kv, at):
+    """A page whose scale one outlier has made 2^12 times the others'."""
+    f = Filled(kv, [6000], hkv=1, seed=215)
+    page = int(f.table[0, at // 16])
+    f.vs.fill_(0.01)
+    f.vs[page] = 0.01 * 2 ** 12
+    f.v[page] = 0x08  # 2^-6: as large as the others' there
+    f.v[page, 0, 7, at % 16] = 0x7E
+    _load(f)
+    q = _queries([50], 8, 216, 2.0)
+    _check(f, q, [50], _run(f, q, [50]))
+
+
 @pytest.mark.parametrize("new", [1, 16, 60])
 @pytest.mark.parametrize("steps", [-16.8, -2.8, -0.9, 1.8])
 def test_bf16_weights_that_nearly_cancel(kv, new, steps):
