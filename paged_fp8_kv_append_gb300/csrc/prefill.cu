@@ -101,12 +101,14 @@ constexpr int OFF_K = OFF_Q + 2 * kTileBytes;     // 2 blocks
 constexpr int OFF_V = OFF_K + 2 * kTileBytes;     // 2 blocks
 constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
 constexpr int OFF_MLB = OFF_META + kMeta * kBlkPages * 16;   // [128] float2
-constexpr int OFF_RING = OFF_MLB + kTile * 8;                // [kRing] Piece
+constexpr int OFF_HB = OFF_MLB + kTile * 8;                  // [128] float
+constexpr int OFF_RING = OFF_HB + kTile * 4;                 // [kRing] Piece
 constexpr int OFF_BAR = OFF_RING + kRing * 48;
 constexpr int kBars = 8 + 2 + 8 + 6 + 3 + 2 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
 constexpr int kSmem = OFF_MISC + 64;
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+// (with the 1 KB that a CTA has besides; one step more leaves 32 KB less of L1: drafts +7%)
+static_assert(kSmem <= (196 - 1) * 1024, "shared memory budget");
 
 // tensor memory columns: two S of 64 (P in the first half of each; bf16 pools: its second parts
 // in the second) and O of each tile
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   float4* meta = reinterpret_cast<float4*>(smem + OFF_META);
   float2* ml_b = reinterpret_cast<float2*>(smem + OFF_MLB);
+  float* h_b = reinterpret_cast<float*>(smem + OFF_HB);
   uint64_t* bp = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   Bars bar;
   bar.k_ready = bp, bar.k_free = bp + 2, bar.v_ready = bp + 4, bar.v_free = bp + 6;
@@ -835,8 +838,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
     // exponent, and M is the largest score + bias of a unit at which it was last taken (kRoom
-    // below it), so that P stay below 2^15 whatever the scales; the row sum takes the bias back
-    // out.
+    // below it), so that P stay below 2^15 whatever the scales.  The row sum l takes the bias back out and
+    // has a reference R of its own: l counts tokens whose V scale is zero or tiny, for whose
+    // scores M says nothing.  R is M as long as scales are near 1 (not kWide), else about the
+    // largest score; it ends at l's own exponent, and O is brought to it.
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t to = tmem + tmem_o(x) + lanes;
@@ -922,7 +927,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       const int lim = seen0 + (pc->row0 + min(tile0 + row, rows - 1)) / p.G;
       const int lim_all = seen0 + (pc->row0 + tile0) / p.G;
       const float qsc = next_qsc;
-      float M = -INFINITY, l = 0.0f;
+      float M = -INFINITY, l = 0.0f, R = -3e38f;
+      // (in two steps: a factor below fp32's range may meet an l above 1)
+      auto raise_R = [&](float to_ref) {
+        const float f = ex2(0.5f * (R - to_ref));
+        l = l * f * f;
+        R = to_ref;
+      };
       uint32_t flags = 0;
       const int units = both ? 2 * cnt : cnt;
 #pragma unroll 1
@@ -969,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               if (mx > M + 8.0f) {
                 const float to = FP8 ? mx - kRoom : mx;
                 alpha = M == -INFINITY ? 0.0f : ex2(M - to);
-                l *= alpha;
+                if (!FP8) l *= alpha;
                 M = to;
               }
               if (n > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
@@ -1016,20 +1027,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           if (!go) break;
           float s0, s1;
           unpack2(add_l, s0, s1);
-          l += s0 + s1;
-          // where V scales lie far apart, P of a page with a small one can fall
-          // below fp32's range while its weight counts: such a block's sum is
-          // taken of the weights themselves (and its pages' factors above are 0)
-          if (FP8 && (fl & kWide)) {
-            const float ref = M == -INFINITY ? 0.0f : M;
+          if (!FP8) l += s0 + s1;
+          // where V scales lie far from 1, or M far above the scores, P can fall below fp32's
+          // range while its weight counts: such a unit's sum is taken of the weights themselves
+          const bool apart = FP8 && ((fl & kWide) || __any_sync(0xffffffffu, M - R > 40.0f && R > -1e38f));
+          if (FP8 && !apart) {
+            if (R < M) raise_R(M);
+            l = __fmaf_rn(s0 + s1, ex2(M - R), l);
+          }
+          if (apart) {
 #pragma unroll 1
-            for (int c = 0; c < kUnitPages; ++c) {
+            for (int c = 0; c < 2 * kUnitPages; ++c) {  // the unit twice: the largest, the sum
+              const int g = c & (kUnitPages - 1);
               float y[16];
-              tmem_ld16(ts + 16 * c, y);
-              const float ks = fmaxf(mt[c].x * qsc, 1e-37f);
+              tmem_ld16(ts + 16 * g, y);
+              const float ks = fmaxf(mt[g].x * qsc, 1e-37f);
+              float mx = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                l += col0 + 16 * c + k <= lim ? ex2(__fmaf_rn(y[k], ks, -ref)) : 0.0f;
+              for (int k = 0; k < 16; ++k) {
+                y[k] = col0 + 16 * g + k <= lim ? y[k] * ks : -INFINITY;
+                mx = fmaxf(mx, y[k]);
+              }
+              if (c < kUnitPages) {
+                if (mx > R + 8.0f) raise_R(mx);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) l += ex2(y[k] - R);
+              }
             }
           }
           tmem_st32u(ts, pk);
@@ -1044,15 +1068,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       if (!go) break;
       if (!stage(piece + 1)) break;
       // ---- the piece's output
+      float h = 1.0f;  // h^2: what brings O to R
+      if (FP8) {
+        if (l > 0.0f && l < INFINITY) {  // l to 1/2 .. 1, so that parts meet with what counts
+          const int e = (int)(__float_as_uint(l) >> 23) - 126;
+          l *= pow2f(-e);
+          R += (float)e;
+        }
+        h = ex2(0.5f * (M - R));
+        M = l == 0.0f ? -INFINITY : R;
+      }
       // (a sum that is no number marks its part so: every part merged with it becomes NaN)
       if (l != l) M = INFINITY;
       const bool two = !both;  // A and B hold parts of the same rows
       if (!wait(&bar.o_full[x], (ph & kO) != 0, 13)) break;
       ph ^= kO;
       tc_fence_after();
-      float wa = 1.0f, wb = 0.0f;
+      float wa = 1.0f, wb = 0.0f, hb = 1.0f;
       if (!both && x == 1) {  // B's part goes to A's warps
         ml_b[row] = make_float2(M, (flags & kBadPage) ? -1.0f : l);
+        h_b[row] = h;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.b_ml);
       } else {
@@ -1063,6 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           tc_fence_after();
           const float2 b = ml_b[row];
           if (b.y < 0.0f) flags |= kBadPage;
+          hb = h_b[row];
           const float Mn = fmaxf(M, b.x);
           wa = M == -INFINITY ? 0.0f : ex2(M - Mn);
           wb = b.x == -INFINITY ? 0.0f : ex2(b.x - Mn);
@@ -1090,7 +1126,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               // (a part that saw nothing holds zeros times whatever: leave it out)
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                o[k] = (wa != 0.0f ? o[k] * wa : 0.0f) + (wb != 0.0f ? ob[k] * wb : 0.0f);
+                o[k] = (wa != 0.0f ? o[k] * h * (h * wa) : 0.0f) +
+                       (wb != 0.0f ? ob[k] * hb * (hb * wb) : 0.0f);
+            } else if (FP8) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = o[k] * h * h;
             }
             if (live && whole && !bad) {
 #pragma unroll

@@ -168,6 +168,49 @@ def test_keys_that_are_no_numbers(kv, kind, at, what, fp8):
     _check(f, q, new, got, ~bad)
 
 
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -130, 1e-38, 1e-20, 1e34])
+@pytest.mark.parametrize("first", [64, 304])
+@pytest.mark.parametrize("lead", [1.0, 30.0])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_scales_of_leading_pages(kv, kind, lead, first, scale):
+    """V scales of zero, below and near fp32's smallest, or near its largest over whole units of
+    pages at a request's begin, whose keys score like the others' or far higher and lower: their
+    weights count in the sum whatever their values are."""
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, seed=205)
+    for b in range(f.B):
+        pages = f.table[b, :min(first, (lens[b] - 1) // 16 * 16) // 16].long()
+        f.vs[pages] = scale
+        f.ks[pages] *= lead
+    _load(f)
+    q = _queries(new, hq, 206)
+    _check(f, q, new, _run(f, q, new))
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -130, 1e-37, 1e-20, 1e34])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_scales_of_every_page(kv, kind, scale):
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, seed=207)
+    f.vs.fill_(scale)
+    _load(f)
+    q = _queries(new, hq, 208)
+    _check(f, q, new, _run(f, q, new))
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_scales_far_apart_anywhere(kv, kind):
+    """Scales of every size from 2^-130 to 2^110, page by page in any order."""
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, seed=209)
+    g = torch.Generator().manual_seed(210)
+    f.vs = torch.exp2(torch.randint(-130, 111, f.vs.shape, generator=g).float())
+    f.ks *= torch.exp2(torch.randint(-3, 5, f.ks.shape, generator=g).float())
+    _load(f)
+    q = _queries(new, hq, 211)
+    _check(f, q, new, _run(f, q, new))
+
+
 @pytest.mark.parametrize("nats", [10.0, 18.0])
 @pytest.mark.parametrize("new", [1, 40])
 @pytest.mark.parametrize("at", [0, 2500])
