@@ -22,15 +22,19 @@ __device__ __forceinline__ long long ragged_first(long long row, int P, int r) {
   return row / P + 2LL * r;
 }
 
-// The request whose item numbers hold `item` (indptr not decreasing), found by
-// a whole warp: 32 entries a step.  Always in [0, B).
-__device__ __forceinline__ int ragged_owner(const int32_t* indptr, int B, int P, long long item) {
+// The request whose item numbers hold `item`, found by a whole warp: 32 entries a step.
+// Always in [0, B).  Only the first `limit` requests are looked at (their rows must not run
+// backwards; what is behind them may), though the loads do not wait for it.
+__device__ __forceinline__ int ragged_owner(const int32_t* indptr, int B, int limit, int P,
+                                            long long item) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;  // the answer is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = lo + lane * step;
-    const bool le = lane * step < n && (lane == 0 || ragged_first(indptr[at], P, at) <= item);
+    const bool in = lane * step < n;
+    const int32_t row = in ? indptr[at] : 0;
+    const bool le = in && (lane == 0 || (at < limit && ragged_first(row, P, at) <= item));
     const int k = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
     n = min(step, n - k * step);
     lo += k * step;

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2)
   pdl_trigger();
   const kv_pool_desc& d = a.d;
   const int P = SHAPE == kTile16x128 ? 16 : d.page_size;
-  const int r = ragged_owner(a.out_indptr, a.B, P, blockIdx.x);
+  const int r = ragged_owner(a.out_indptr, a.B, a.B, P, blockIdx.x);
   const long long o0 = a.out_indptr[r], o1 = a.out_indptr[r + 1], L = a.seq_lens[r];
   const long long start = a.row_start != nullptr ? a.row_start[r] : 0, n = o1 - o0;
   const bool aborted = a.abort_mask != nullptr && a.abort_mask[r] != 0;

@@ -340,8 +340,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
   }
   pdl_wait();
   pdl_trigger();
-  const int r = ragged_owner(ap.new_indptr, ap.B, P, blockIdx.x);
-  if (r >= d.ctl[KV_CTL_APPEND_STOP]) return;  // not served: nothing of it is written
+  // (the served requests' rows are in order; a refused one's may run backwards, and none of
+  // its items may hide a served one's)
+  const int stop = d.ctl[KV_CTL_APPEND_STOP];
+  if (stop <= 0) return;  // nothing is served, and nothing written
+  const int r = ragged_owner(ap.new_indptr, ap.B, stop, P, blockIdx.x);
   const long long i0 = ap.new_indptr[r], i1 = ap.new_indptr[r + 1], n = i1 - i0;
   if (n <= 0 || i0 < 0 || i1 > a.total_new) return;  // (the plan has refused it)
   const int local = blockIdx.x - ragged_first(i0, P, r);
