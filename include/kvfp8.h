@@ -456,9 +456,10 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
  *   v_out       bf16 [total_rows][num_kv_heads][head_dim_v] (device; LATENT:
  *               NULL)
  * e4m3 pools: bf16(code * scale), the product in fp32; bf16 pools: the bits.
- * A request whose rows are not all cached (row_start < 0, a negative count,
- * row_start + rows > seq_lens[r] or beyond its page table) or do not fit the
- * outputs gets KV_ERR_INVALID_ARG and no rows; a page id out of range sets
+ * A request whose rows are not all cached (row_start < 0, row_start + rows >
+ * seq_lens[r] or beyond its page table) or do not fit the outputs gets
+ * KV_ERR_INVALID_ARG and no rows; so do one whose out_indptr runs backwards (a
+ * negative count) and all behind it; a page id out of range sets
  * KV_ERR_BAD_PAGE_ID and that page's rows are not written.  Any pool shape,
  * both layouts.  One kernel launch.
  */

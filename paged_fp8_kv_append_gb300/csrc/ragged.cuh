@@ -42,4 +42,35 @@ __device__ __forceinline__ int ragged_owner(const int32_t* indptr, int B, int li
   return lo;
 }
 
+// The same by reading the offsets in order, 128 a step: -1 where no request's items begin at or
+// before `item`, and only requests before the first whose rows run backwards.  (A search does
+// not see such a place.)
+__device__ __forceinline__ int ragged_owner_in_order(const int32_t* indptr, int B, int P,
+                                                     long long item) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  int owner = -1;
+  bool more = true;
+  for (int base = 0; more && base < B; base += 32 * kAhead) {
+    int32_t i0[kAhead], i1[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = base + 32 * k + lane;
+      i0[k] = r < B ? indptr[r] : 0;
+      i1[k] = r < B ? indptr[r + 1] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = base + 32 * k + lane;
+      const uint32_t back = __ballot_sync(0xffffffffu, i1[k] < i0[k]);
+      const uint32_t le =
+          __ballot_sync(0xffffffffu, r < B && ragged_first(i0[k], P, r) <= item) &
+          (back != 0 ? (back & (0u - back)) - 1u : 0xffffffffu);
+      if (more) owner += __popc(le);
+      more = more && le == 0xffffffffu;
+    }
+  }
+  return owner;
+}
+
 }  // namespace kvfp8

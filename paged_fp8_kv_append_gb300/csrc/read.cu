@@ -133,6 +133,23 @@ __device__ __forceinline__ void read_v_any(const void* src, float s, int slot0, 
   }
 }
 
+// A request's rows, and whether they can be read (one that is aborted or has none: n 0, fits).
+struct Request {
+  long long o0, n, start;
+  bool in_order, fits;
+};
+__device__ __forceinline__ Request request(const ReadArgs& a, int r) {
+  Request q;
+  const long long o1 = a.out_indptr[r + 1], L = a.seq_lens[r];
+  q.o0 = a.out_indptr[r];
+  q.start = a.row_start != nullptr ? a.row_start[r] : 0;
+  q.in_order = q.o0 <= o1;
+  q.n = a.abort_mask != nullptr && a.abort_mask[r] != 0 ? 0 : o1 - q.o0;
+  q.fits = q.n == 0 || (q.n > 0 && q.o0 >= 0 && o1 <= a.total_rows && q.start >= 0 &&
+                        q.start + q.n <= L && q.start + q.n <= (long long)a.max_pages * a.d.page_size);
+  return q;
+}
+
 enum Shape { kTile16x128, kLatent, kAny };
 
 // Registers for the loads in flight matter more than warps: 3 (bf16: 2) CTAs an
@@ -145,18 +162,19 @@ __global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2)
   pdl_trigger();
   const kv_pool_desc& d = a.d;
   const int P = SHAPE == kTile16x128 ? 16 : d.page_size;
-  const int r = ragged_owner(a.out_indptr, a.B, a.B, P, blockIdx.x);
-  const long long o0 = a.out_indptr[r], o1 = a.out_indptr[r + 1], L = a.seq_lens[r];
-  const long long start = a.row_start != nullptr ? a.row_start[r] : 0, n = o1 - o0;
-  const bool aborted = a.abort_mask != nullptr && a.abort_mask[r] != 0;
+  // the last block (its item is seldom one) looks at every request: a refused one's rows may lie
+  // behind every item, or in another's
+  if (blockIdx.x == gridDim.x - 1)
+    for (int r = threadIdx.x; r < a.B; r += kThreads) {
+      const Request q = request(a, r);
+      if (!q.in_order || !q.fits) set_error(d.ctl, KV_ERR_INVALID_ARG);
+    }
+  const int r = ragged_owner_in_order(a.out_indptr, a.B, P, blockIdx.x);
+  if (r < 0) return;
+  const Request q = request(a, r);
+  const long long o0 = q.o0, n = q.n, start = q.start;
+  if (!q.fits || n == 0) return;
   const int local = blockIdx.x - ragged_first(o0, P, r);  // the request's touched page number
-  if (aborted || n == 0) return;
-  if (o0 < 0 || n < 0 || o1 > a.total_rows || start < 0 || start + n > L ||
-      start + n > (long long)a.max_pages * P) {
-    // (the first block speaks for a first request that begins behind every item)
-    if (threadIdx.x == 0 && (local == 0 || blockIdx.x == 0)) set_error(d.ctl, KV_ERR_INVALID_ARG);
-    return;
-  }
   const long long j = start / P + local;
   const long long lo = max(j * P, start), hi = min((j + 1) * P, start + n);
   if (local < 0 || lo >= hi) return;

@@ -6,8 +6,9 @@ Bounds of the values are those of the operators' own tests."""
 import pytest
 import torch
 
+import test_prompt_read_gpu as read
 import test_prompt_rotary_gpu as rotary
-from promptref import Filled
+from promptref import Filled, indptr
 from test_prompt_read_gpu import kv  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,16 @@ def test_rotary(kv, ind, served, fp8):  # noqa: F811
     assert f.lens_d.tolist() == [3 + n for n in new] + [3] * (B - served)
     assert int(f.pool.ctl[kv.KV_CTL_APPEND_STOP]) == served
     rotary._check(f, new + [0] * (B - served), host, out, False, served=served)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("ind,served", BACKWARDS)
+def test_read(kv, ind, served, fp8):  # noqa: F811
+    B = len(ind) - 1
+    f = Filled(kv, [200] * B, hkv=2, fp8=fp8, seed=303)
+    k = torch.full((200, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    f.pool.read_rows(B, f.table_d, f.lens_d, None, _i32(ind), None, k, v)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    f.B = served
+    read._check(f, [0] * served, torch.tensor(ind[:served + 1]) if served else indptr([0]), k, v)
