@@ -482,8 +482,8 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  *   total_q     rows of q and out (device); rows that no request owns are left
  *               untouched.
  *   q           bf16 [total_q][num_q_heads][128]
- *   q_indptr    int32 [B+1] (device), not decreasing: request r's queries are
- *               rows q_indptr[r] .. q_indptr[r+1]-1, its last tokens, in order.
+ *   q_indptr    int32 [B+1] (device): request r's queries are rows
+ *               q_indptr[r] .. q_indptr[r+1]-1, its last tokens, in order.
  *   seq_lens    int32 [B] (device): cached tokens, the new ones included.
  *   abort_mask  uint8 [B] from kv_verify_tags, or NULL: an aborted request's
  *               pages are not read and its output rows are left untouched.
@@ -493,17 +493,18 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * Query i of the n of request r (L = seq_lens[r]) attends to positions
  * 0 .. L - n + i; a query with no visible position gets zeros, and one with a
  * visible score that is not a number (NaN or infinite queries, NaN keys) gets
- * NaN.  A request
- * with a negative length or count, one beyond its page table or longer than
- * 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is not written;
- * one whose needed pages include an id outside [0, num_pages) sets
- * KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of the
- * request may or may not be.  Other requests are not affected.  GQA pools with
- * head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
+ * NaN.  A request with rows and a negative length, one beyond its page table or
+ * longer than 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is
+ * not written; so do one whose q_indptr runs backwards (a negative count) and
+ * all behind it; one whose needed pages include an id outside [0, num_pages)
+ * sets KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of
+ * the request may or may not be.  Other requests are not affected.  GQA pools
+ * with head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
  * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31; others return
- * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts for the
- * product with V, sums and maxima in fp32.  Results do not depend on which
- * requests are run together beyond rounding, and are the same from run to run.
+ * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts
+ * for the product with V, sums and maxima in fp32.  Results do not depend on
+ * which requests are run together beyond rounding, and are the same from run to
+ * run.
  * Calls that may run at the same time need a workspace each.  Three kernel
  * launches.
  */

@@ -169,19 +169,47 @@ struct Args {
 
 constexpr int kPlanThreads = 1024;
 
-// One CTA: every item's request, rows and blocks, and the cost prefix.
+// Whether request r (rows q0 .. q1-1) can be attended: its rows lie in q, and it has a length
+// that its page table holds (positions of a block are ints).
+__device__ __forceinline__ bool request_fits(const PrefillArgs& p, long long q0, long long q1,
+                                             long long L) {
+  return q0 <= q1 && q0 >= 0 && q1 <= p.total_q && L >= 0 && (L + kP - 1) / kP <= p.max_pages &&
+         L <= INT_MAX - 2 * kBlk;
+}
+
+// One CTA: every item's request, rows and blocks, and the cost prefix.  Requests are checked by
+// themselves, as a refused one's rows may lie behind every item or in another's; items are those
+// of the requests before the first whose rows run backwards, so that their search is one of an
+// increasing sequence.
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a) {
   pdl_wait();
   pdl_trigger();
   __shared__ long long sums[32];
   const PrefillArgs& p = a.p;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int first_back = p.B;  // the first of this thread's requests whose rows run backwards
+  for (int r = threadIdx.x; r < p.B; r += kPlanThreads) {
+    const long long q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
+    const bool aborted = p.abort_mask != nullptr && p.abort_mask[r] != 0;
+    if (q1 < q0) first_back = min(first_back, r);
+    if (q1 < q0 || (!aborted && q0 != q1 && !request_fits(p, q0, q1, p.seq_lens[r])))
+      set_error(p.d.ctl, KV_ERR_INVALID_ARG);
+  }
+  int served = p.B;
+  if (__syncthreads_or(first_back < p.B)) {
+    __shared__ int s_served;
+    if (threadIdx.x == 0) s_served = p.B;
+    __syncthreads();
+    atomicMin(&s_served, first_back);
+    __syncthreads();
+    served = s_served;
+  }
   long long carry = 0;
   for (int base = 0; base < a.V; base += kPlanThreads) {
     const int v = base + threadIdx.x;
     long long cost = 0;
     if (v < a.V) {
-      int lo = 0, hi = p.B;  // the last r whose items begin at or before v
+      int lo = 0, hi = served;  // the last r whose items begin at or before v
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (item_first(p.q_indptr[mid], p.G, mid) <= v) lo = mid; else hi = mid;
@@ -191,18 +219,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
       const long long L = p.seq_lens[r], row0 = (v - item_first(q0, p.G, r)) * kItemRows;
       int4 it = make_int4(r, 0, 0, 0);
       const bool aborted = p.abort_mask != nullptr && p.abort_mask[r] != 0;
-      if (!aborted && n != 0) {
-        if (n < 0 || q0 < 0 || q1 > p.total_q || L < 0 || (L + kP - 1) / kP > p.max_pages ||
-            L > INT_MAX - 2 * kBlk) {  // (positions of a block are ints)
-          set_error(p.d.ctl, KV_ERR_INVALID_ARG);
-        } else if (row0 >= 0 && row0 < n * p.G) {
-          it.y = (int)row0;
-          it.z = (int)min((long long)kItemRows, n * p.G - row0);
-          const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
-          it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
-          cost = item_lead(it.z, p.d.dtype == KV_DTYPE_E4M3) +
-                 (long long)it.w * (it.z > kTile ? kCostTwo : kCostOne);
-        }
+      if (r < served && !aborted && request_fits(p, q0, q1, L) && row0 >= 0 && row0 < n * p.G) {
+        it.y = (int)row0;
+        it.z = (int)min((long long)kItemRows, n * p.G - row0);
+        const long long seen = L - n + (row0 + it.z - 1) / p.G + 1;  // by the last row
+        it.w = (int)max(1LL, (seen + kBlk - 1) / kBlk);
+        cost = item_lead(it.z, p.d.dtype == KV_DTYPE_E4M3) +
+               (long long)it.w * (it.z > kTile ? kCostTwo : kCostOne);
       }
       a.ws.items[v] = it;
     }

@@ -6,6 +6,7 @@ Bounds of the values are those of the operators' own tests."""
 import pytest
 import torch
 
+import test_prompt_prefill_gpu as attn
 import test_prompt_read_gpu as read
 import test_prompt_rotary_gpu as rotary
 from promptref import Filled, indptr
@@ -58,3 +59,53 @@ def test_read(kv, ind, served, fp8):  # noqa: F811
     assert f.pool.error() == kv.KV_ERR_INVALID_ARG
     f.B = served
     read._check(f, [0] * served, torch.tensor(ind[:served + 1]) if served else indptr([0]), k, v)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("heads", [(8, 1), (2, 2)])
+@pytest.mark.parametrize("ind,served", BACKWARDS)
+def test_attention(kv, ind, served, heads, fp8):  # noqa: F811
+    B, (hq, hkv) = len(ind) - 1, heads
+    f = Filled(kv, [210] * B, hkv=hkv, fp8=fp8, seed=305)
+    q = attn._queries(f, [200], hq, 306)
+    out = torch.full((200, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(f.pool.prefill_workspace_size(B, hq, 200), dtype=torch.uint8, device="cuda")
+    f.pool.prefill_attn(B, hq, q.cuda(), _i32(ind), f.table_d, f.lens_d, None, attn.SCALE, out, ws)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    f.B = served
+    new = [b - a for a, b in zip(ind, ind[1:])][:served]
+    attn._check(f, q, new, out)
+
+
+@pytest.mark.parametrize("aborted", [[0, 0], [1, 0]])
+@pytest.mark.parametrize("ind", [[0, 100000, 100040], [100000, 100000, 100040], [0, 0, 100040], [0, 80, 10 ** 9]])
+def test_rows_far_behind_the_arrays(kv, ind, aborted):  # noqa: F811
+    """A request whose rows begin or end behind every work item is reported, also behind one that is
+    aborted or has no rows."""
+    ab = torch.tensor(aborted, dtype=torch.uint8, device="cuda")
+    f = Filled(kv, [60, 60], hkv=2, seed=307)
+    k = torch.full((80, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    f.pool.read_rows(2, f.table_d, f.lens_d, None, _i32(ind), ab, k, v)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    assert bool((k == 7.0).all()) and bool((v == 7.0).all())
+    f = Filled(kv, [90, 90], hkv=2, seed=308)
+    q, out = torch.zeros((80, 4, 128), dtype=torch.bfloat16, device="cuda"), k.new_full((80, 4, 128), 7.0)
+    ws = torch.empty(f.pool.prefill_workspace_size(2, 4, 80), dtype=torch.uint8, device="cuda")
+    f.pool.prefill_attn(2, 4, q, _i32(ind), f.table_d, f.lens_d, ab, attn.SCALE, out, ws)
+    assert f.pool.error() == kv.KV_ERR_INVALID_ARG
+    assert bool((out[ind[1] if ind[1] <= 80 and not aborted[0] else 0:] == 7.0).all())
+
+
+def test_aborted_requests_with_bad_rows_are_not_reported(kv):  # noqa: F811
+    ab = torch.tensor([1, 0], dtype=torch.uint8, device="cuda")
+    f = Filled(kv, [60, 60], hkv=2, seed=309)
+    f.lens_d[0] = 10 ** 6
+    k = torch.full((80, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    f.pool.read_rows(2, f.table_d, f.lens_d, None, _i32([0, 40, 80]), ab, k, v)
+    assert f.pool.error() == 0 and bool((k[:40] == 7.0).all()) and not bool((k[40:] == 7.0).all())
+    q, out = torch.zeros((80, 4, 128), dtype=torch.bfloat16, device="cuda"), k.new_full((80, 4, 128), 7.0)
+    ws = torch.empty(f.pool.prefill_workspace_size(2, 4, 80), dtype=torch.uint8, device="cuda")
+    f.pool.prefill_attn(2, 4, q, _i32([0, 40, 80]), f.table_d, f.lens_d, ab, attn.SCALE, out, ws)
+    assert f.pool.error() == 0 and bool((out[:40] == 7.0).all()) and bool((out[40:60] != 7.0).any())
