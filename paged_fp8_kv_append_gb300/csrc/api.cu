@@ -16,16 +16,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+}  // namespace
+
+namespace kvfp8 {
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
   return n;
 }
-
-}  // namespace
-
-namespace kvfp8 {
 
 kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig* cfg) {
   const kv_pool_desc& d = pool->d;

@@ -1276,9 +1276,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches) {
   // instructions, so it takes the compact per-tile kernel below.
   // (a handoff always takes them: the host checked its shape fits)
   const bool bulk = a.from_pool || a.max_new >= 2 * Pl;
-  static int sms = 0;
-  if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess)
-    sms = 0;
+  const int sms = sm_count();
   const size_t pre_bytes = sizeof(int) * ((size_t)a.B + 1);
   // the work-item count is held in an int
   const long long per_page = a.d.layout == KV_LAYOUT_GQA ? 2LL * a.d.num_kv_heads : 1LL;

@@ -82,6 +82,10 @@ struct DecodeArgs {
   DecodeWs ws;
 };
 
+// SMs of the current device (0: there is none).  Asked at each launch: a process may use several
+// devices, and several threads may launch at once.
+int sm_count();
+
 // ---- append -------------------------------------------------------------
 struct AppendArgs {
   kv_pool_desc d;

@@ -1262,13 +1262,6 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const Args a) {
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
-
 }  // namespace
 
 size_t prefill_ws_bytes(const kv_pool_desc& d, int B, int Hq, int total_q) {

@@ -386,9 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
 cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launches) {
   cudaError_t e = launch_append_plan(a.app, s, launches);
   if (e != cudaSuccess || a.total_new == 0) return e;
-  static int sms = 0;
-  if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0) != cudaSuccess)
-    sms = 0;
+  const int sms = sm_count();
   const int P = a.app.d.page_size;
   const long long items = ragged_items(a.total_new, a.app.B, P);
   // few pages: their heads are split, up to one wave of CTAs
