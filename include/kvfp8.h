@@ -427,8 +427,8 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
  * tags, stops, partly filled pages, both scale modes, new_indptr,
  * max_new_per_req, page_table, exp_tags, seq_lens) is as for
  * kv_append_quantize; a request that is not served gets no q_out rows.
- * GQA pools with page_size * head_dim <= 2048 for K and V; others return
- * KV_ERR_UNSUPPORTED.  Two kernel launches.
+ * GQA pools with page_size * head_dim <= 2048 for K and V, and total_new /
+ * page_size + 2 B < 2^31; others return KV_ERR_UNSUPPORTED.  Two kernel launches.
  */
 kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
                            int32_t total_new, const void* q, int64_t q_stride, const void* k_new,
@@ -461,7 +461,8 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
  * KV_ERR_INVALID_ARG and no rows; so do one whose out_indptr runs backwards (a
  * negative count) and all behind it; a page id out of range sets
  * KV_ERR_BAD_PAGE_ID and that page's rows are not written.  Any pool shape,
- * both layouts.  One kernel launch.
+ * both layouts; total_rows / page_size + 2 B >= 2^31 returns KV_ERR_UNSUPPORTED.
+ * One kernel launch.
  */
 kv_status kv_read_rows(kv_pool* pool, void* stream, int32_t B, const int32_t* page_table,
                        int32_t max_pages_per_req, const int32_t* seq_lens,
@@ -500,8 +501,8 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * sets KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of
  * the request may or may not be.  Other requests are not affected.  GQA pools
  * with head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
- * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31; others return
- * KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts
+ * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31 (and B + total_q *
+ * num_q_heads / num_kv_heads / 256); others return KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts
  * for the product with V, sums and maxima in fp32.  Results do not depend on
  * which requests are run together beyond rounding, and are the same from run to
  * run.

@@ -7,6 +7,7 @@
 #include <new>
 
 #include "internal.h"
+#include "ragged.cuh"
 
 using namespace kvfp8;
 
@@ -186,6 +187,8 @@ kv_status prefill_check(const kv_pool_desc& d, int B, int Hq, int total_q) {
   if (d.num_kv_heads > 4096) return KV_ERR_UNSUPPORTED;  // a page of all heads: 32-bit bytes
   // query rows of one kv head are counted in an int
   if ((long long)total_q * Hq > INT32_MAX) return KV_ERR_UNSUPPORTED;
+  // so are items: 256 of those rows each, and one a request more
+  if ((long long)total_q * (Hq / d.num_kv_heads) / 256 + B > INT32_MAX) return KV_ERR_UNSUPPORTED;
   return KV_OK;
 }
 
@@ -587,6 +590,8 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
     if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < qw ||
                             q_stride % 8 != 0))
       return KV_ERR_INVALID_ARG;
+    // a block for each page that may be touched
+    if (ragged_items(total_new, B, d.page_size) > INT32_MAX) return KV_ERR_UNSUPPORTED;
     // in place only row for row: at another stride a row's output is a later row's input
     if (num_q_heads > 0 && q_out == q && q_stride != qw && total_new > 1) return KV_ERR_INVALID_ARG;
   }
@@ -632,6 +637,8 @@ kv_status kv_read_rows(kv_pool* pool, void* stream, int32_t B, const int32_t* pa
   if (!page_table || !seq_lens || !out_indptr || !k_out || !aligned16(k_out))
     return KV_ERR_INVALID_ARG;
   if (pool->d.layout == KV_LAYOUT_GQA && (!v_out || !aligned16(v_out))) return KV_ERR_INVALID_ARG;
+  // a block for each page that may be touched
+  if (ragged_items(total_rows, B, pool->d.page_size) > INT32_MAX) return KV_ERR_UNSUPPORTED;
   ReadArgs a;
   a.d = pool->d;
   a.B = B;
