@@ -68,8 +68,10 @@ __device__ __forceinline__ uint2 quant8(uint4 v, float s) {
 // bits).  Branch-free: a quotient of magnitude >= 1024 (or an infinite / NaN
 // input) stays uncorrected, since the e4m3 conversion saturates it the same
 // way, and the result takes x's sign so that -0 stays -0.  Checked against
-// __fdiv_rn on every bf16 x and every scale amax/448 of a bf16 amax (the
-// inputs this library divides), comparing the e4m3 codes.
+// __fdiv_rn, comparing the e4m3 codes: on every bf16 x and every scale amax/448
+// of a bf16 amax (rows as they are given), and, for fp32 x and scales (turned
+// keys), on every mantissa of a scale with the x around every border between
+// two codes, which is where codes could differ.
 __device__ __forceinline__ bool scale_fast_ok(float s) { return s >= 0x1p-90f; }
 
 __device__ __forceinline__ float div_fast(float x, float s, float rs) {
