@@ -417,6 +417,8 @@ def paged_prefill_attn(handle, B, num_q_heads, q, q_indptr, page_table, seq_lens
     dev = _device()
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
+    if q.numel() != total_q * int(num_q_heads) * 128:
+        raise ValueError("q: expected [rows][num_q_heads][128]")
     st = _lib.paged_prefill_attn(
         handle, _stream_on(stream, dev), B, int(num_q_heads), total_q,
         _arg(q, _BF16, "q", dev, total_q * int(num_q_heads) * 128),
