@@ -122,6 +122,8 @@ constexpr uint32_t idesc(bool bf16, uint32_t n) {
 
 // flags of a key block, kept beside its scales
 constexpr uint32_t kBadPage = 1, kWide = 2;  // an id out of range; V scales far from 1
+// a page whose scales are no numbers (negative, infinite, NaN), and the same of that page alone
+constexpr uint32_t kOdd = 4, kOddPage = 8;
 
 // ------------------------------------------------------------------ plan
 
@@ -708,13 +710,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (live) {
           if (!keys) clean_v(dst, b);
           if (cw == 0) {
+            // (kept out of the arithmetic, where a masked score times NaN would be NaN)
+            const bool odd = FP8 && !(sc0.x >= 0.0f && sc0.y >= 0.0f && sc0.x < INFINITY &&
+                                      sc0.y < INFINITY);
+            if (odd) sc0 = make_float2(1.0f, 1.0f);
             const float bias = __log2f(sc0.y);
             const uint32_t flags =
                 (__any_sync(0xffffffffu, pg0 == -2) ? kBadPage : 0u) |
+                (__any_sync(0xffffffffu, odd) ? kOdd : 0u) |
                 (__any_sync(0xffffffffu, lane < kBlkPages && fabsf(bias) > 48.0f) ? kWide : 0u);
             if (lane < kBlkPages)
               meta[(u & (kMeta - 1)) * kBlkPages + lane] =
-                  make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias), __uint_as_float(flags));
+                  make_float4(sc0.x, bias, flags & kWide ? 0.0f : ex2(-bias),
+                              __uint_as_float(flags | (odd ? kOddPage : 0u)));
             if (lane == 0 && (flags & kBadPage)) set_error(ctl, KV_ERR_BAD_PAGE_ID);
           }
           fence_async_smem();
@@ -1078,6 +1086,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
                 for (int k = 0; k < 16; ++k) l += ex2(y[k] - R);
               }
             }
+          }
+          if (FP8 && (fl & kOdd)) {  // a row that sees such a page becomes NaN
+#pragma unroll 1
+            for (int g = 0; g < kUnitPages; ++g)
+              if ((__float_as_uint(mt[g].w) & kOddPage) && col0 + 16 * g <= lim)
+                l = __int_as_float(0x7FFFFFFF);
           }
           tmem_st32u(ts, pk);
           if constexpr (!FP8) tmem_st32u(ts + 32, pl);

@@ -138,7 +138,7 @@ def test_queries_that_are_no_numbers(kv, kind, fp8):
 
 
 @pytest.mark.parametrize("fp8", [True, False])
-@pytest.mark.parametrize("what", ["key"])
+@pytest.mark.parametrize("what", ["key", "scale"])
 @pytest.mark.parametrize("at", [0, 70, 130, -3])
 @pytest.mark.parametrize("kind", list(KINDS))
 def test_keys_that_are_no_numbers(kv, kind, at, what, fp8):
@@ -266,3 +266,43 @@ def test_bf16_weights_that_nearly_cancel(kv, new, steps):
     q = torch.zeros((new, 8, 128), dtype=torch.bfloat16)
     q[..., 0] = math.log1p(steps * 2.0 ** -9) / SCALE
     _check(f, q, [new], _run(f, q, [new]))
+
+
+@pytest.mark.parametrize("what", ["scale nan", "scale inf"])
+@pytest.mark.parametrize("back", [1, 7, 15])
+@pytest.mark.parametrize("kind", [k for k in KINDS if k != "single token, cut"])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_values_behind_the_mask(kv, fp8, kind, back, what):
+    """A value that is not finite reaches its own dim of the rows that see its position, and nothing
+    of the rows before it; nor does a page's V scale that is not."""
+    if (what == "inf") if fp8 else ("scale" in what):
+        pytest.skip("e4m3 has no infinities, a bf16 pool no scales")
+    lens, new, hq, hkv = KINDS[kind]
+    b = len(lens) - 1
+    f = Filled(kv, lens, hkv=hkv, fp8=fp8, seed=219)
+    at = lens[b] - back
+    if "scale" in what:
+        at = (lens[b] - 1) // 16 * 16  # the last page's first token
+    page, head, g = int(f.table[b, at // 16]), hkv - 1, hq // hkv
+    clean = (f.v.clone(), None if f.vs is None else f.vs.clone())
+    if "scale" in what:
+        f.vs[page, head] = math.nan if "nan" in what else math.inf
+    else:
+        f.v[page, head, 77, at % 16] = 0x7F if fp8 else math.nan if what == "nan" else math.inf
+        f.v[page, head, 3, at % 16] = 0xFF if fp8 else -math.inf
+    _load(f)
+    q = _queries(new, hq, 220)
+    got = _run(f, q, new)
+    f.v, f.vs = clean
+    sees = torch.arange(new[b]) + lens[b] - new[b] >= at
+    rows = torch.zeros(q.shape[0], hq, dtype=torch.bool)
+    rows[-new[b]:, head * g:] = sees[:, None]
+    assert bool(rows.any()) and not bool(rows.all())
+    _check(f, q, new, got, ~rows)
+    if "scale" in what:
+        assert bool(torch.isnan(got[rows]).all())
+        return
+    assert not bool(torch.isfinite(got[rows][:, [3, 77]]).any())
+    got[..., [3, 77]] = 0  # every other dim is right
+    f.v[:, :, [3, 77]] = 0
+    _check(f, q, new, got, rows)
