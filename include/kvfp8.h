@@ -494,7 +494,9 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * Query i of the n of request r (L = seq_lens[r]) attends to positions
  * 0 .. L - n + i; a query with no visible position gets zeros, and one with a
  * visible score that is not a number (NaN or infinite queries, NaN keys, a
- * page's scale that is negative or not finite) gets NaN.  A request with rows and a negative length, one beyond its page table or
+ * page's scale that is negative or not finite) gets NaN.  A cached value that
+ * is not finite makes its dim of the rows that see its position not finite, and
+ * reaches no other.  A request with rows and a negative length, one beyond its page table or
  * longer than 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is
  * not written; so do one whose q_indptr runs backwards (a negative count) and
  * all behind it; one whose needed pages include an id outside [0, num_pages)

@@ -103,10 +103,11 @@ constexpr int OFF_META = OFF_V + 2 * kTileBytes;  // [kMeta][8] float4
 constexpr int OFF_MLB = OFF_META + kMeta * kBlkPages * 16;   // [128] float2
 constexpr int OFF_HB = OFF_MLB + kTile * 8;                  // [128] float
 constexpr int OFF_RING = OFF_HB + kTile * 4;                 // [kRing] Piece
-constexpr int OFF_BAR = OFF_RING + kRing * 48;
-constexpr int kBars = 8 + 2 + 8 + 6 + 3 + 2 * kRing;
+constexpr int OFF_SPOIL = OFF_RING + kRing * 48;             // [kRing][128] uint8_t
+constexpr int OFF_BAR = OFF_SPOIL + kRing * kD;
+constexpr int kBars = 8 + 2 + 8 + 6 + 3 + 3 * kRing;
 constexpr int OFF_MISC = OFF_BAR + kBars * 8;
-constexpr int kSmem = OFF_MISC + 64;
+constexpr int kSmem = OFF_MISC + 8;
 // (with the 1 KB that a CTA has besides; one step more leaves 32 KB less of L1: drafts +7%)
 static_assert(kSmem <= (196 - 1) * 1024, "shared memory budget");
 
@@ -263,7 +264,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Args a
 struct Piece {
   int r, h, row0, nrows;
   int b_lo, b_hi, nb, L;
-  int n, q0, valid, pad;
+  int n, q0, valid, apart;  // (apart: see find_hidden)
+  __device__ __forceinline__ int seen_all(int G) const {  // tokens that every row sees
+    return L - n + row0 / G + 1;
+  }
   __device__ __forceinline__ bool both() const { return nrows > kTile; }
   __device__ __forceinline__ int w() const { return both() ? kCostTwo : kCostOne; }
   __device__ __forceinline__ int count() const { return b_hi - b_lo; }
@@ -454,13 +458,128 @@ __device__ __forceinline__ void mma_ts4(uint32_t leader, uint32_t d, uint32_t a,
       : "memory");
 }
 
+// ---------------------------------------------- values that are not finite
+//
+// A weight of 0 times a value that is not finite is NaN: such a value of a token that not all of
+// an item's rows see would reach those that do not.  The few such tokens of a piece (256 rows / G,
+// and what its last block holds behind them) are looked through by the scheduler; if one has such
+// a value, the piece's values are brought in by a loop of its own that zeroes it, and the output's
+// end makes the dim NaN for the rows that see it.  (Blocks of tokens that every row sees need
+// none of this: their NaN are the rows' own.)
+
+// the request's j-th page, or page 0 where there is none
+__device__ __forceinline__ long long page_or_0(const PrefillArgs& p, const Piece& pc, int j) {
+  const int pg = j * kP < pc.L ? p.page_table[(long long)pc.r * p.max_pages + j] : 0;
+  return pg >= 0 && pg < p.d.num_pages ? pg : 0;
+}
+
+// Whether one of the tokens from seen_all() to the piece's last block's end is not finite; sp[dim]
+// = the first such token of the dim, counted from seen_all() (255: none that a row sees).  One
+// warp.  (Out of line, or with twice as many pages in flight, the code grows and prompts lose 2-5%.)
+template <bool FP8>
+__device__ __forceinline__ bool find_hidden(const PrefillArgs& p, const Piece& pc, uint8_t* sp) {
+  constexpr int kEs = FP8 ? 1 : 2, kQ = kEs, kAhead = 2 / kEs;  // 16-byte pieces of a dim; pages
+  constexpr uint32_t kOnes = FP8 ? 0x7F7F7F7Fu : 0x7F807F80u;   // what a value not finite has
+  constexpr uint32_t kLow = FP8 ? 0x01010101u : 0x00800080u;    // carries it into the sign
+  constexpr uint32_t kSign = FP8 ? 0x80808080u : 0x80008000u;
+  constexpr int kBits = 8 * kEs, kIn = 32 / kBits;
+  const int lane = threadIdx.x & 31;
+  const int t0 = pc.seen_all(p.G), t1 = min(pc.L, pc.b_hi * kBlk);
+  const uint8_t* v = static_cast<const uint8_t*>(p.d.v_cache);
+  int first[4] = {255, 255, 255, 255};
+  bool apart = false;
+  if (t0 < t1) {
+#pragma unroll 1
+    for (int j = max(t0, 0) / kP; j * kP < t1; j += kAhead) {
+      uint4 x[kAhead][4][kQ];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const long long ph = page_or_0(p, pc, j + k) * p.d.num_kv_heads + pc.h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int q = 0; q < kQ; ++q)
+            x[k][e][q] = __ldg(reinterpret_cast<const uint4*>(
+                                   v + (ph * kD + lane + 32 * e) * kP * kEs) + q);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            const uint32_t y[4] = {x[k][e][q].x, x[k][e][q].y, x[k][e][q].z, x[k][e][q].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t odd = ((y[c] & kOnes) + kLow) & kSign;
+#pragma unroll 1
+              for (; odd != 0; odd &= odd - 1) {
+                const int t = (j + k) * kP + (4 * q + c) * kIn + (__ffs(odd) - 1) / kBits;
+                if (t < t0 || t >= t1) continue;
+                apart = true;
+                first[e] = min(first[e], t - t0);
+              }
+            }
+          }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sp[lane + 32 * e] = (uint8_t)first[e];
+  return __any_sync(0xffffffffu, apart);
+}
+
+// The values of a piece that has some: one values warp's part of its blocks, u being the CTA's
+// first.  False once a wait has run out.
+template <bool FP8>
+__device__ __noinline__ bool values_apart(const PrefillArgs& p, const Piece& pc, uint8_t* tiles,
+                                          uint64_t* ready, uint64_t* room, uint32_t u,
+                                          volatile int* abort_flag) {
+  const int ct = threadIdx.x & 63, seen_all = pc.seen_all(p.G);
+  const uint8_t* v = static_cast<const uint8_t*>(p.d.v_cache);
+  for (int b = pc.b_lo; b < pc.b_hi; ++b, ++u) {
+    if (u >= 2 && !wait_phase(&room[u & 1], (u >> 1) - 1, abort_flag, 4)) return false;
+    uint8_t* dst = tiles + (u & 1) * kTileBytes;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      // the thread's chunk i of 8 tokens of a dim, as the converters have it
+      const int tok = b * kBlk + (FP8 ? (i >> 2) * kP + 8 * (i & 1) : 64 * (i >> 4) + 8 * (ct & 7));
+      const uint32_t at = FP8 ? (i >> 4) * kHalf + ((i >> 1) & 1) * 8192 +
+                                    (swz(ct, 0) ^ ((((i >> 1) & 6) + (i & 1)) << 4))
+                              : (i >> 4) * kHalf + (i & 15) * 1024 + swz(ct >> 3, ct & 7);
+      const int dim = FP8 ? ct + 64 * ((i >> 1) & 1) : 8 * (i & 15) + (ct >> 3);
+      const long long ph = page_or_0(p, pc, tok / kP) * p.d.num_kv_heads + pc.h;
+      const uint8_t* src = v + ((ph * kD + dim) * kP + tok % kP) * (FP8 ? 1 : 2);
+      uint4 x;
+      if (FP8) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(src));
+        e4m3x4_to_f16(c.x, x.x, x.y);
+        e4m3x4_to_f16(c.y, x.z, x.w);
+      } else {
+        x = __ldg(reinterpret_cast<const uint4*>(src));
+      }
+      uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t exp = (FP8 ? 0x7C00u : 0x7F80u) << (16 * (k & 1));
+        if (tok + k >= pc.L || (tok + k >= seen_all && (y[k >> 1] & exp) == exp))
+          y[k >> 1] &= 0xFFFFu << (16 * (~k & 1));
+      }
+      *reinterpret_cast<uint4*>(dst + at) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ready[u & 1]);
+  }
+  return true;
+}
+
 struct Bars {
   uint64_t *k_ready, *k_free, *v_ready, *v_free;         // [2]
   uint64_t *q_ready, *q_free;
   uint64_t *s_full, *p_ready;                            // [tile][S buffer]
   uint64_t *pv_done, *o_full, *epi_done;                 // [tile]
   uint64_t *b_ml, *drain;
-  uint64_t *ring_full, *ring_free;                       // [kRing]
+  uint64_t *ring_full, *ring_free, *sp_full;             // [kRing]
 };
 
 // --------------------------------------------------------------- kernel
@@ -473,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   float4* meta = reinterpret_cast<float4*>(smem + OFF_META);
   float2* ml_b = reinterpret_cast<float2*>(smem + OFF_MLB);
   float* h_b = reinterpret_cast<float*>(smem + OFF_HB);
+  uint8_t* spoil = smem + OFF_SPOIL;
   uint64_t* bp = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   Bars bar;
   bar.k_ready = bp, bar.k_free = bp + 2, bar.v_ready = bp + 4, bar.v_free = bp + 6;
@@ -481,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
   bar.o_full = bar.pv_done + 2, bar.epi_done = bar.o_full + 2;
   bar.b_ml = bar.epi_done + 2, bar.drain = bar.b_ml + 1;
   bar.ring_full = bar.drain + 2, bar.ring_free = bar.ring_full + kRing;
+  bar.sp_full = bar.ring_free + kRing;
   Piece* ring = reinterpret_cast<Piece*>(smem + OFF_RING);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -507,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
       mbar_init(&bar.v_ready[i], kConvWarps / 2);
       mbar_init(&bar.v_free[i], 2);
       mbar_init(&bar.pv_done[i], 1);
-      mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.o_full[i], 2);  // the products' end, and the issuing warp itself
       mbar_init(&bar.epi_done[i], 4);
     }
     for (int i = 0; i < 4; ++i) {
@@ -521,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     mbar_init(&bar.drain[1], 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ring_full[i], 1);
+      mbar_init(&bar.sp_full[i], 1);
       mbar_init(&bar.ring_free[i], kMmaWarp + 2);  // every warp that reads it
     }
     *abort_flag = 0;
@@ -578,6 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     uint32_t u = 0;
     for (uint32_t piece = 0; next_piece(piece); ++piece) {
       // ---- the key blocks
+      if (!keys) {
+        if (!wait(&bar.sp_full[piece % kRing], piece / kRing, 16)) break;
+        if (ring[piece % kRing].apart) {
+          if (go) go = values_apart<FP8>(p, s, tiles, ready, room, u, abort_flag);
+          if (!go) break;
+          u += s.count();
+          continue;
+        }
+      }
       const int32_t* prow = p.page_table + (long long)s.r * p.max_pages;
       const int npages = s.L / kP + (s.L % kP != 0);
       // lane l holds page l % 8 of a block: its id, -1 behind the request's
@@ -792,7 +923,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           if (leader) {
             mma_commit(&bar.pv_done[x]);
             if (h == 1 || !both) mma_commit(&bar.v_free[st]);
-            if (n == units - 1) mma_commit(&bar.o_full[x]);
+            if (n == units - 1) {
+              mma_commit(&bar.o_full[x]);
+              mbar_arrive(&bar.o_full[x]);
+            }
           }
           __syncwarp();
         }
@@ -837,6 +971,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
         if (lane == 0) {
           ring[piece % kRing] = c.s;
           mbar_arrive(&bar.ring_full[piece % kRing]);
+        }
+        const bool apart = find_hidden<FP8>(p, c.s, spoil + piece % kRing * kD);
+        if (lane == 0) {
+          ring[piece % kRing].apart = apart;
+          mbar_arrive(&bar.sp_full[piece % kRing]);
         }
         ++piece;
         // its query rows: the heads of a token lie together
@@ -1137,8 +1276,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           if (b.y < 0.0f) flags |= kBadPage;
           hb = h_b[row];
           const float Mn = fmaxf(M, b.x);
-          wa = M == -INFINITY ? 0.0f : ex2(M - Mn);
-          wb = b.x == -INFINITY ? 0.0f : ex2(b.x - Mn);
+          // (-1: a part that saw nothing; its sum is 0)
+          wa = M == -INFINITY ? -1.0f : ex2(M - Mn);
+          wb = b.x == -INFINITY ? -1.0f : ex2(b.x - Mn);
           l = l * wa + b.y * wb;
           M = Mn;
         }
@@ -1151,6 +1291,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           const float scale = 1.0f / l;
           const int slot = 2 * (int)blockIdx.x + (pc->b_lo > 0 ? 0 : 1), tg = pc->row0 + tile0 + row;
           const int t = tg / p.G, g = tg - t * p.G;
+          const uint8_t* sp = spoil + piece % kRing * kD;
+          const bool spoilt =
+              __any_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(sp)[lane] != 0xffffffffu);
+          const int sees = t - pc->row0 / p.G - 1;  // the last of sp's tokens that this row sees
           uint16_t* out = p.out + ((long long)(pc->q0 + t) * p.Hq + pc->h * p.G + g) * kD;
           float4* part = a.ws.o + (long long)slot * 32 * kItemRows + tile0 + row;
 #pragma unroll 1
@@ -1163,11 +1307,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
               // (a part that saw nothing holds zeros times whatever: leave it out)
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                o[k] = (wa != 0.0f ? o[k] * h * (h * wa) : 0.0f) +
-                       (wb != 0.0f ? ob[k] * hb * (hb * wb) : 0.0f);
+                o[k] = (wa != -1.0f ? o[k] * h * (h * wa) : 0.0f) +
+                       (wb != -1.0f ? ob[k] * hb * (hb * wb) : 0.0f);
             } else if (FP8) {
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = o[k] * h * h;
+            }
+            if (spoilt) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if ((int)sp[16 * c + k] <= sees) o[k] = __int_as_float(0x7FFFFFFF);
             }
             if (live && whole && !bad) {
 #pragma unroll
@@ -1245,8 +1394,8 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const Args a) {
   if (live && M != -INFINITY) {
     for (int c = c0; c <= cut.z; ++c) {
       const float2 ml = a.ws.ml[slot_of(c) * kItemRows + rr];
-      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-      if (w == 0.0f) continue;  // (saw nothing, or nothing that counts)
+      if (ml.x == -INFINITY) continue;  // (saw nothing: zeros times whatever)
+      const float w = exp2f(ml.x - M);
       l = __fmaf_rn(ml.y, w, l);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

@@ -268,7 +268,7 @@ def test_bf16_weights_that_nearly_cancel(kv, new, steps):
     _check(f, q, [new], _run(f, q, [new]))
 
 
-@pytest.mark.parametrize("what", ["scale nan", "scale inf"])
+@pytest.mark.parametrize("what", ["nan", "inf", "scale nan", "scale inf"])
 @pytest.mark.parametrize("back", [1, 7, 15])
 @pytest.mark.parametrize("kind", [k for k in KINDS if k != "single token, cut"])
 @pytest.mark.parametrize("fp8", [True, False])
