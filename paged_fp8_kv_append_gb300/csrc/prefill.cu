@@ -80,13 +80,18 @@ constexpr int kRing = 4;  // pieces in flight from the scheduler
 constexpr int kThreads = (kMmaWarp + 3) * 32;
 // Costs, about 0.65 us each (e4m3): a block of an item with two tiles, one of an item with a
 // single tile (1.95 and 1.4 us: the keys and values are as many, the rows half), and what an
-// item costs beside its blocks (queries in, output out; fewer of a bf16 pool's blocks, which
-// take longer).  At 2 : 1 for the blocks four ragged prompts took 973 us, at 3 : 2 856; one
-// prompt of 8k tokens takes 994, 954, 929 and 936 us at leads of 11, 12, 13 and 16, the bf16
-// prompts 848, 850, 882 at 11, 12, 13.
+// item costs beside its blocks (queries in, output out).  At 2 : 1 for the blocks four ragged
+// prompts take 922 us (bf16 1,092), at 3 : 2 871 (1,062), at 4 : 3 882 (1,062).  An item of two tiles, about 8 us, counts fewer of a
+// bf16 pool's blocks, which take longer.  Measured on four shapes for both types (one prompt of
+// 8k tokens and 64 heads, four ragged ones and 96, six and 32, one of 4k and 32; us):
+//   e4m3, lead 10   1090 951 387 185        bf16, lead 10   1211 1056 396 197
+//              11   1036 929 376 177                   11   1211 1056 398 193
+//              12    997 907 371 172                   12   1218 1060 401 193
+//              14    945 871 359 165                   14   1217 1063 405 194
+//              16    951 872 360 163                   16   1219 1084 415 194
 constexpr int kCostTwo = 3, kCostOne = 2;
 __host__ __device__ inline int item_lead(int nrows, bool fp8) {
-  return nrows > 128 ? (fp8 ? 13 : 11) : 9;
+  return nrows > 128 ? (fp8 ? 14 : 11) : 9;
 }
 constexpr int kMeta = 4;  // block records in flight
 // Where a unit's maximum is taken, the reference of a row of an e4m3 pool goes this far (binades)
