@@ -114,6 +114,7 @@ KINDS = {
     "two requests": ([200, 70], [3, 40], 8, 2),
     "single token, cut": ([9000], [1], 8, 1),
     "cut": ([2600], [130], 16, 2),
+    "a query head each": ([400], [300], 2, 2),
 }
 
 
@@ -127,7 +128,7 @@ def test_queries_that_are_no_numbers(kv, kind, fp8):
     q = _queries(new, hq, 202)
     t = q.shape[0]
     bad = torch.zeros(t, hq, dtype=torch.bool)
-    for i, (row, head, x) in enumerate(((0, 1, math.nan), (t // 2, hq - 1, math.inf), (t - 1, 2, -math.inf))):
+    for i, (row, head, x) in enumerate(((0, 1, math.nan), (t // 2, hq - 1, math.inf), (t - 1, hq // 2, -math.inf))):
         q[row, head, 5 * i] = x
         bad[row, head] = True
     got = _run(f, q, new)
@@ -306,3 +307,43 @@ def test_values_behind_the_mask(kv, fp8, kind, back, what):
     got[..., [3, 77]] = 0  # every other dim is right
     f.v[:, :, [3, 77]] = 0
     _check(f, q, new, got, rows)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_values_anywhere_that_are_not_finite(kv, kind, fp8):
+    """Values that are not finite at several positions, one of them seen by (nearly) every row, three
+    dims of a head at each: an output is finite where its row sees none of its dim, and right."""
+    lens, new, hq, hkv = KINDS[kind]
+    f = Filled(kv, lens, hkv=hkv, fp8=fp8, seed=221)
+    g = torch.Generator().manual_seed(222)
+    clean = f.v.clone()
+    first = torch.full((f.B, hkv, 128), 1 << 30)  # the first such position of each dim
+    for b in range(f.B):
+        backs = [k for k in (1, 4, 11, 30, 77, 130, 290) if k == 1 or k <= new[b]]
+        for at in [*(lens[b] - k for k in backs), lens[b] // 3]:
+            h, d = int(torch.randint(0, hkv, (), generator=g)), torch.randint(0, 128, (3,), generator=g)
+            page = int(f.table[b, at // 16])
+            f.v[page, h, d, at % 16] = 0x7F if fp8 else math.nan if at % 2 else -math.inf
+            clean[page, h, d, at % 16] = 0
+            first[b, h, d] = torch.clamp_max(first[b, h, d], at)
+    _load(f)
+    q = _queries(new, hq, 223)
+    got = _run(f, q, new)
+    f.v = clean
+    ind = indptr(new)
+    bad = torch.zeros(got.shape, dtype=torch.bool)
+    for b in range(f.B):
+        last = torch.arange(new[b]) + lens[b] - new[b]  # the last position each row sees
+        bad[ind[b]:ind[b + 1]] = (first[b] <= last[:, None, None]).repeat_interleave(hq // hkv, 1)
+    assert bool(bad.any()) and not bool(bad.all())
+    assert not bool(torch.isfinite(got[bad]).any())
+    assert bool(torch.isfinite(got[~bad]).all())
+    # (where they belong, the reference takes their place)
+    _check(f, q, new, torch.where(bad, _reference(f, q, new), got))
+
+
+def _reference(f, q, new):
+    ind = indptr(new)
+    return torch.cat([attention(q[ind[b]:ind[b + 1]].double(), f.rows(b, "k"), f.rows(b, "v"), SCALE,
+                                f.lens[b] - new[b]) for b in range(f.B)])
