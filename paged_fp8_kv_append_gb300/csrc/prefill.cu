@@ -487,49 +487,44 @@ __device__ __forceinline__ bool find_hidden(const PrefillArgs& p, const Piece& p
   constexpr uint32_t kOnes = FP8 ? 0x7F7F7F7Fu : 0x7F807F80u;   // what a value not finite has
   constexpr uint32_t kLow = FP8 ? 0x01010101u : 0x00800080u;    // carries it into the sign
   constexpr uint32_t kSign = FP8 ? 0x80808080u : 0x80008000u;
-  constexpr int kBits = 8 * kEs, kIn = 32 / kBits;
   const int lane = threadIdx.x & 31;
   const int t0 = pc.seen_all(p.G), t1 = min(pc.L, pc.b_hi * kBlk);
   const uint8_t* v = static_cast<const uint8_t*>(p.d.v_cache);
-  int first[4] = {255, 255, 255, 255};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sp[lane + 32 * e] = 255;
   bool apart = false;
   if (t0 < t1) {
 #pragma unroll 1
     for (int j = max(t0, 0) / kP; j * kP < t1; j += kAhead) {
-      uint4 x[kAhead][4][kQ];
+      const uint8_t* src[kAhead];
+      uint4 x[kAhead][4 * kQ];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const long long ph = page_or_0(p, pc, j + k) * p.d.num_kv_heads + pc.h;
+        src[k] = v + ((page_or_0(p, pc, j + k) * p.d.num_kv_heads + pc.h) * kD + lane) * kP * kEs;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int q = 0; q < kQ; ++q)
-            x[k][e][q] = __ldg(reinterpret_cast<const uint4*>(
-                                   v + (ph * kD + lane + 32 * e) * kP * kEs) + q);
+        for (int e = 0; e < 4 * kQ; ++e)  // dims lane, + 32, ..
+          x[k][e] = __ldg(reinterpret_cast<const uint4*>(src[k] + e / kQ * 32 * kP * kEs) + e % kQ);
       }
+      uint32_t odd = 0;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int q = 0; q < kQ; ++q) {
-            const uint32_t y[4] = {x[k][e][q].x, x[k][e][q].y, x[k][e][q].z, x[k][e][q].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t odd = ((y[c] & kOnes) + kLow) & kSign;
+        for (int e = 0; e < 4 * kQ; ++e)
+          odd |= ((x[k][e].x & kOnes) + kLow) | ((x[k][e].y & kOnes) + kLow) |
+                 ((x[k][e].z & kOnes) + kLow) | ((x[k][e].w & kOnes) + kLow);
+      if ((odd & kSign) == 0) continue;
 #pragma unroll 1
-              for (; odd != 0; odd &= odd - 1) {
-                const int t = (j + k) * kP + (4 * q + c) * kIn + (__ffs(odd) - 1) / kBits;
-                if (t < t0 || t >= t1) continue;
-                apart = true;
-                first[e] = min(first[e], t - t0);
-              }
-            }
-          }
+      for (int i = 0; i < kAhead * kP * 4; ++i) {  // one by one
+        const int e = i & 3, t = j * kP + (i >> 2);
+        if (t < t0 || t >= t1) continue;
+        const uint8_t* at = (i >> 2 < kP ? src[0] : src[kAhead - 1]) + (e * 32 * kP + t % kP) * kEs;
+        const uint32_t c = FP8 ? *at : *reinterpret_cast<const uint16_t*>(at);
+        if ((c & kOnes & (FP8 ? 0xFFu : 0xFFFFu)) != (kOnes & (FP8 ? 0xFFu : 0xFFFFu))) continue;
+        apart = true;
+        if (t - t0 < sp[lane + 32 * e]) sp[lane + 32 * e] = (uint8_t)(t - t0);
+      }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sp[lane + 32 * e] = (uint8_t)first[e];
   return __any_sync(0xffffffffu, apart);
 }
 
