@@ -6,7 +6,9 @@
 // values as it reads them; bf16 is the baseline format.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j), j <= L - n + i,
-// in one pass over the keys with a running reference and sum of each row.
+// in one pass over the keys with a running reference and sum of each row.  What a row does not
+// see does not reach it, whatever it is: scores are masked, pages' scales that are no numbers
+// are kept beside the arithmetic, values that are not finite left out (find_hidden).
 //
 // Work decomposition.  A request's query rows of one kv head are row = t * G + g
 // (token, head of the group); 256 of them are an item's two tiles of 128 rows
@@ -37,7 +39,8 @@
 //   MMA A (12), B (13)  S = Q K^T (M 128, N 64) a unit ahead of O += P V (M = N = 128),
 //                   so that a tile's softmax finds its next scores when it has stored P
 //   scheduler (14)  the CTA's pieces, one after the other into a ring that the other
-//                   warps read, their query rows pulled into L2
+//                   warps read, their query rows pulled into L2, the values that some of
+//                   their rows must not see looked through
 // Every wait is bounded (KV_ERR_TIMEOUT); tensor memory is freed on every path.
 //
 // What bounds it, and what was measured (64 query and 8 kv heads, e4m3, TFLOP/s of 4 Hq D
@@ -47,19 +50,21 @@
 //     unit (48 KB in 384 cycles where its products take 256); scores of 128 columns at a
 //     time cost less there but leave no room in tensor memory to be a step ahead: 4.25 ms,
 //     the softmax warps wait for their scores.
-//   one prompt of 8192    0.93 ms, 1.18e15 (61%): the same, and about 8 us an item (6 of
+//   one prompt of 8192    0.94 ms, 1.16e15 (60%): the same, and about 8 us an item (6 of
 //     them queries in) that the other items of the CTA hide in part.
-//   16 tokens of 32 requests, 4k-32k cached   0.284 ms, 0.91e15, 3.6 TB/s of cache: 128 rows
+//   16 tokens of 32 requests, 4k-32k cached   0.289 ms, 0.89e15, 3.6 TB/s of cache: 128 rows
 //     make half the products of a block whose keys and values are the same 32 KB.  Bound
 //     by the converters, a block in 2,600 cycles.
+//   four ragged bf16 prompts, 96 heads   1.05 ms, 0.84e15 (43%): the tensor pipe is 71% busy,
+//     0.29 of that with the weights' second parts.
 // Two converter warps for each of K and V against four for both in turn: drafts 378 -> 292
 // us, four ragged bf16 prompts 1,139 -> 965: a block's waits, page ids, fence and arrival
-// are paid once for it, and keys do not wait for values.  Eight converter warps leave 96
+// are paid once for it, and keys do not wait for values (weights of one part then).  Eight converter warps leave 96
 // registers a thread, and the softmax then spills: chunk 3.3 -> 4.0 ms.  Pages by bulk copies
 // or cp.async through 32 KB of shared memory were slower than the loads (a bulk copy is about
 // 66 cycles of its warp, 16 a block).  All of the loops together have to stay small: the code
-// is 76 KB, and variants that unrolled more (92 KB: drafts 335 us) ran slower by what the
-// instruction cache misses.
+// is 90 KB (bf16: 84), a fifth of it seldom run, and variants that unrolled more ran slower by
+// what the instruction cache misses (16 KB more in the loops: drafts 284 -> 335 us).
 #include <climits>
 
 #include "common.cuh"

@@ -10,7 +10,9 @@
 // touched page: a page's tiles are contiguous, and a warp's loads and stores
 // are runs of whole sectors (8 values a lane for token-major rows; a dim-major
 // V tile is transposed in registers, a lane holding 4 dims of all 16 tokens).
-// A tile's loads are issued together, K and V of a head by the same warp.
+// A tile's loads are issued together, K and V of a head by the same warp.  Tiles other than 16 x
+// 128 store V element by element: 16 x 256 4.0 TB/s, 16 x 64 3.4, 64 x 128 1.5 (e4m3; 16 x 128
+// 6.1-6.3, bf16 6.0, latent rows 6.3).
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
