@@ -55,7 +55,7 @@
 //   16 tokens of 32 requests, 4k-32k cached   0.289 ms, 0.89e15, 3.6 TB/s of cache: 128 rows
 //     make half the products of a block whose keys and values are the same 32 KB.  Bound
 //     by the converters, a block in 2,600 cycles.
-//   four ragged bf16 prompts, 96 heads   1.05 ms, 0.84e15 (43%): the tensor pipe is 71% busy,
+//   four ragged bf16 prompts, 96 heads   1.05 ms, 0.84e15 (43%): the tensor pipe is 72% busy,
 //     0.29 of that with the weights' second parts.
 // Two converter warps for each of K and V against four for both in turn: drafts 378 -> 292
 // us, four ragged bf16 prompts 1,139 -> 965: a block's waits, page ids, fence and arrival
