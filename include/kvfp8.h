@@ -496,18 +496,18 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * visible score that is not a number (NaN or infinite queries, NaN keys, a
  * page's scale that is negative or not finite) gets NaN.  A cached value that
  * is not finite makes its dim of the rows that see its position not finite, and
- * reaches no other.  A request with rows and a negative length, one beyond its page table or
- * longer than 2^31 - 257, or rows beyond total_q sets KV_ERR_INVALID_ARG and is
- * not written; so do one whose q_indptr runs backwards (a negative count) and
- * all behind it; one whose needed pages include an id outside [0, num_pages)
+ * reaches no other.  A request with rows and a negative length, one beyond its
+ * page table or longer than 2^31 - 257, or rows beyond total_q sets
+ * KV_ERR_INVALID_ARG and is not written; so do one whose q_indptr runs backwards
+ * (a negative count) and all behind it; one whose needed pages include an id outside [0, num_pages)
  * sets KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of
  * the request may or may not be.  Other requests are not affected.  GQA pools
  * with head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
  * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31 (and B + total_q *
- * num_q_heads / num_kv_heads / 256); others return KV_ERR_UNSUPPORTED.  Weights are held in fp16 (e4m3 pools) or two bf16 parts
- * for the product with V, sums and maxima in fp32.  Results do not depend on
- * which requests are run together beyond rounding, and are the same from run to
- * run.
+ * num_q_heads / num_kv_heads / 256); others return KV_ERR_UNSUPPORTED.  Weights
+ * are held in fp16 (e4m3 pools) or two bf16 parts for the product with V, sums
+ * and maxima in fp32.  Results do not depend on which requests are run together
+ * beyond rounding, and are the same from run to run.
  * Calls that may run at the same time need a workspace each.  Three kernel
  * launches.
  */

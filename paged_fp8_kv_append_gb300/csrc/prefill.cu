@@ -59,8 +59,8 @@
 //     0.29 of that with the weights' second parts.
 // Two converter warps for each of K and V against four for both in turn: drafts 378 -> 292
 // us, four ragged bf16 prompts 1,139 -> 965: a block's waits, page ids, fence and arrival
-// are paid once for it, and keys do not wait for values (weights of one part then).  Eight converter warps leave 96
-// registers a thread, and the softmax then spills: chunk 3.3 -> 4.0 ms.  Pages by bulk copies
+// are paid once for it, and keys do not wait for values (weights of one part then).  Eight
+// converter warps leave 96 registers a thread, and the softmax then spills: chunk 3.3 -> 4.0 ms.  Pages by bulk copies
 // or cp.async through 32 KB of shared memory were slower than the loads (a bulk copy is about
 // 66 cycles of its warp, 16 a block).  All of the loops together have to stay small: the code
 // is 90 KB (bf16: 84), a fifth of it seldom run, and variants that unrolled more ran slower by
@@ -86,8 +86,8 @@ constexpr int kThreads = (kMmaWarp + 3) * 32;
 // Costs, about 0.65 us each (e4m3): a block of an item with two tiles, one of an item with a
 // single tile (1.95 and 1.4 us: the keys and values are as many, the rows half), and what an
 // item costs beside its blocks (queries in, output out).  At 2 : 1 for the blocks four ragged
-// prompts take 922 us (bf16 1,092), at 3 : 2 871 (1,062), at 4 : 3 882 (1,062).  An item of two tiles, about 8 us, counts fewer of a
-// bf16 pool's blocks, which take longer.  Measured on four shapes for both types (one prompt of
+// prompts take 922 us (bf16 1,092), at 3 : 2 871 (1,062), at 4 : 3 882 (1,062).  An item of two
+// tiles, about 8 us, counts fewer of a bf16 pool's blocks, which take longer.  Measured on four shapes for both types (one prompt of
 // 8k tokens and 64 heads, four ragged ones and 96, six and 32, one of 4k and 32; us):
 //   e4m3, lead 10   1090 951 387 185        bf16, lead 10   1211 1056 396 197
 //              11   1036 929 376 177                   11   1211 1056 398 193
@@ -485,7 +485,8 @@ __device__ __forceinline__ long long page_or_0(const PrefillArgs& p, const Piece
 
 // Whether one of the tokens from seen_all() to the piece's last block's end is not finite; sp[dim]
 // = the first such token of the dim, counted from seen_all() (255: none that a row sees).  One
-// warp.  (Out of line, or with twice as many pages in flight, the code grows and prompts lose 2-5%.)
+// warp.  (Out of line, or with twice as many pages in flight, the code grows and prompts lose
+// 2-5%.)
 template <bool FP8>
 __device__ __forceinline__ bool find_hidden(const PrefillArgs& p, const Piece& pc, uint8_t* sp) {
   constexpr int kEs = FP8 ? 1 : 2, kQ = kEs, kAhead = 2 / kEs;  // 16-byte pieces of a dim; pages
@@ -1013,8 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
     // ============================== softmax ==============================
     // Scores in log2 units.  A page's V scale enters P as a bias log2(scale) on the
     // exponent, and M is the largest score + bias of a unit at which it was last taken (kRoom
-    // below it), so that P stay below 2^15 whatever the scales.  The row sum l takes the bias back out and
-    // has a reference R of its own: l counts tokens whose V scale is zero or tiny, for whose
+    // below it), so that P stay below 2^15 whatever the scales.  The row sum l takes the bias
+    // back out and has a reference R of its own: l counts tokens whose V scale is zero or tiny, for whose
     // scores M says nothing.  R is M as long as scales are near 1 (not kWide), else about the
     // largest score; it ends at l's own exponent, and O is brought to it.
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;  // tile, row of the tile
@@ -1205,7 +1206,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Args a) {
           if (!FP8) l += s0 + s1;
           // where V scales lie far from 1, or M far above the scores, P can fall below fp32's
           // range while its weight counts: such a unit's sum is taken of the weights themselves
-          const bool apart = FP8 && ((fl & kWide) || __any_sync(0xffffffffu, M - R > 40.0f && R > -1e38f));
+          const bool apart =
+              FP8 && ((fl & kWide) || __any_sync(0xffffffffu, M - R > 40.0f && R > -1e38f));
           if (FP8 && !apart) {
             if (R < M) raise_R(M);
             l = __fmaf_rn(s0 + s1, ex2(M - R), l);
