@@ -59,7 +59,13 @@ typedef enum {
   KV_ERR_TAG_MISMATCH = 8   /* device: append met a partly filled page whose tag changed */
 } kv_status;
 
-typedef enum { KV_DTYPE_E4M3 = 0, KV_DTYPE_BF16 = 1 } kv_dtype;
+typedef enum {
+  KV_DTYPE_E4M3 = 0,
+  KV_DTYPE_BF16 = 1,
+  /* 4 bits a value: e2m1 codes with an e4m3 scale for 16 dims of a token and a
+   * power-of-two scale for each (page, kv head); see kv_pool_desc */
+  KV_DTYPE_E2M1 = 2
+} kv_dtype;
 
 typedef enum {
   /* separate K and V; K rows token-major, V dim-major inside a page;

@@ -30,7 +30,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CUDA = 0, 1, 2, 3
 KV_ERR_OUT_OF_PAGES, KV_ERR_BAD_PAGE_ID, KV_ERR_TIMEOUT, KV_ERR_INTERNAL = 4, 5, 6, 7
 KV_ERR_TAG_MISMATCH = 8
-KV_DTYPE_E4M3, KV_DTYPE_BF16 = 0, 1
+KV_DTYPE_E4M3, KV_DTYPE_BF16, KV_DTYPE_E2M1 = 0, 1, 2
+KV_E2M1_TILE = 1152  # bytes of a (page, kv head) tile of a 4-bit pool
 KV_LAYOUT_GQA, KV_LAYOUT_LATENT = 0, 1
 KV_SCALE_FROZEN, KV_SCALE_REQUANTIZE = 0, 1
 KV_ABORT_TAG, KV_ABORT_UNSERVED, KV_STEP_REMOVE_ABORTED = 1, 2, 1
@@ -440,7 +441,8 @@ class KVPool:
     Allocates the caller-owned buffers the C ABI documents (cache, scales,
     tags, free list, control block) and holds the library handle.  GQA:
     k_cache [pages][Hkv][P][Dk], v_cache [pages][Hkv][Dv][P]; LATENT:
-    k_cache [pages][P][Dk].  e4m3 caches are uint8 tensors.  Buffers that the
+    k_cache [pages][P][Dk].  e4m3 caches are uint8 tensors, and so are 4-bit
+    ones, k_cache and v_cache [pages][Hkv][KV_E2M1_TILE].  Buffers that the
     caller holds already (k_cache, k_scale, v_cache, v_scale, ctl, of those
     shapes and types, contiguous) are taken as they are.
     """
@@ -455,7 +457,7 @@ class KVPool:
         self.num_kv_heads, self.head_dim_k, self.head_dim_v = (
             int(num_kv_heads), int(head_dim_k), int(head_dim_v))
         self.dtype, self.layout = int(dtype), int(layout)
-        edt = torch.uint8 if dtype == KV_DTYPE_E4M3 else torch.bfloat16
+        edt = torch.bfloat16 if dtype == KV_DTYPE_BF16 else torch.uint8
 
         def buf(given, shape, dt, name):
             if given is None:
@@ -466,12 +468,13 @@ class KVPool:
             _ptr(given, dt, name)
             return given
 
-        fp8 = dtype == KV_DTYPE_E4M3
+        fp8 = dtype != KV_DTYPE_BF16  # (or 4 bits: with scales)
         if layout == KV_LAYOUT_GQA:
-            self.k_cache = buf(k_cache, (num_pages, num_kv_heads, page_size, head_dim_k), edt,
-                               "k_cache")
-            self.v_cache = buf(v_cache, (num_pages, num_kv_heads, head_dim_v, page_size), edt,
-                               "v_cache")
+            tile = (KV_E2M1_TILE,) if dtype == KV_DTYPE_E2M1 else None
+            self.k_cache = buf(k_cache, (num_pages, num_kv_heads,
+                                         *(tile or (page_size, head_dim_k))), edt, "k_cache")
+            self.v_cache = buf(v_cache, (num_pages, num_kv_heads,
+                                         *(tile or (head_dim_v, page_size))), edt, "v_cache")
             heads = (num_pages, num_kv_heads)
             self.k_scale = buf(k_scale, heads, torch.float32, "k_scale") if fp8 else None
             self.v_scale = buf(v_scale, heads, torch.float32, "v_scale") if fp8 else None

@@ -39,8 +39,11 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     if (d.head_dim_k != 128 || d.head_dim_v != 128 || d.page_size != 16 || R > 64)
       return KV_ERR_UNSUPPORTED;
     // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16)
-    cfg->kind = d.dtype == KV_DTYPE_E4M3 ? (R > 8 ? 3 : 0) : (R > 8 ? 4 : 1);
-    const bool bf16 = cfg->kind == 1 || cfg->kind == 4, wide = cfg->kind >= 3;
+    // (5, 6: 4-bit)
+    cfg->kind = d.dtype == KV_DTYPE_E2M1 ? (R > 8 ? 6 : 5)
+                : d.dtype == KV_DTYPE_E4M3 ? (R > 8 ? 3 : 0)
+                                           : (R > 8 ? 4 : 1);
+    const bool bf16 = d.dtype == KV_DTYPE_BF16, wide = R > 8;
     // heads per unit: the largest power of two <= 8 (<= 4 for bf16, whose
     // tiles are twice as large) dividing Hkv, with heads x row blocks dividing
     // the consumer warp count; 16-row blocks may be padded with whole unused
@@ -57,7 +60,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     if (hs == 0) return KV_ERR_UNSUPPORTED;  // no split of the consumers fits
     const int rb = wide ? 2 * rbw : rbw;  // row blocks of 8 in the partial layout
     cfg->Hs = hs;
-    const int stage_bytes = 2 * hs * d.page_size * d.head_dim_k * (bf16 ? 2 : 1);
+    const int stage_bytes = 2 * hs * gqa_tile_bytes(cfg->kind);
     cfg->stages = gqa_ring_bytes(cfg->kind) / stage_bytes;
     if (cfg->stages > gqa_max_stages()) cfg->stages = gqa_max_stages();
     // A consumer warp serves every (consumers/Hs)-th unit; the ring depth must
@@ -182,7 +185,7 @@ kv_status decode_prepare(kv_pool* pool, int32_t B, int32_t Hq, int32_t T, const 
 kv_status prefill_check(const kv_pool_desc& d, int B, int Hq, int total_q) {
   if (B < 0 || Hq <= 0 || total_q < 0 || Hq % d.num_kv_heads != 0) return KV_ERR_INVALID_ARG;
   if (d.layout != KV_LAYOUT_GQA || d.head_dim_k != 128 || d.head_dim_v != 128 ||
-      d.page_size != 16)
+      d.page_size != 16 || d.dtype == KV_DTYPE_E2M1)
     return KV_ERR_UNSUPPORTED;
   if (d.num_kv_heads > 4096) return KV_ERR_UNSUPPORTED;  // a page of all heads: 32-bit bytes
   // query rows of one kv head are counted in an int
@@ -204,11 +207,19 @@ kv_status kv_pool_create(const kv_pool_desc* desc, kv_pool** out) {
       d.head_dim_k <= 0 || d.head_dim_v <= 0 || d.head_dim_k % 16 != 0 ||
       d.head_dim_v % 16 != 0 || d.head_dim_k > 1024 || d.head_dim_v > 1024)
     return KV_ERR_INVALID_ARG;
-  if (d.dtype != KV_DTYPE_E4M3 && d.dtype != KV_DTYPE_BF16) return KV_ERR_INVALID_ARG;
+  if (d.dtype != KV_DTYPE_E4M3 && d.dtype != KV_DTYPE_BF16 && d.dtype != KV_DTYPE_E2M1)
+    return KV_ERR_INVALID_ARG;
   if (d.layout != KV_LAYOUT_GQA && d.layout != KV_LAYOUT_LATENT) return KV_ERR_INVALID_ARG;
   if (d.scale_mode != KV_SCALE_FROZEN && d.scale_mode != KV_SCALE_REQUANTIZE)
     return KV_ERR_INVALID_ARG;
   if (!d.k_cache || !d.tags || !d.free_list || !d.ctl) return KV_ERR_INVALID_ARG;
+  if (d.dtype == KV_DTYPE_E2M1) {
+    // a tile's layout is that of the attention's fragments: one shape
+    if (d.layout != KV_LAYOUT_GQA || d.page_size != 16 || d.head_dim_k != 128 ||
+        d.head_dim_v != 128 || d.scale_mode != KV_SCALE_FROZEN || d.num_kv_heads > 4096)
+      return KV_ERR_UNSUPPORTED;
+    if (!d.k_scale || !d.v_scale) return KV_ERR_INVALID_ARG;
+  }
   if (!aligned16(d.k_cache) || !aligned16(d.tags) || !aligned16(d.free_list) ||
       !aligned16(d.ctl))
     return KV_ERR_INVALID_ARG;

@@ -23,6 +23,7 @@
 //     not written through the stale mapping.
 #include <climits>
 
+#include "append_items.cuh"
 #include "append_tile.cuh"
 #include "common.cuh"
 #include "decode_plan.cuh"
@@ -70,13 +71,6 @@ __device__ __forceinline__ int owner_of(const long long* incl, int n, long long 
     if (incl[mid] > g) hi = mid; else lo = mid + 1;
   }
   return lo;
-}
-
-// Rows request r appends in this call (none when the step mask drops it).
-__device__ __forceinline__ long long req_rows(const AppendArgs& a, int r) {
-  if (a.step_mask != nullptr && a.step_mask[r] != 0) return 0;
-  if (a.from_pool) return a.src_lens[r];
-  return (long long)a.new_indptr[r + 1] - a.new_indptr[r];
 }
 
 // With a step mask, every request at or after `stop` is marked unserved.
@@ -499,55 +493,6 @@ __device__ __forceinline__ void v_tile_from_dim_major(const uint16_t* src, int n
     const float x = bf16_bits_to_f32(src[dd * P + i]);
     dst[dd * P + i] = (uint8_t)(e4m3x2(fast ? div_fresh(x, s, rs) : __fdiv_rn(x, s), 0.0f) & 0xFFu);
   }
-}
-
-// Work items of a bulk append: every (request, page this call touches),
-// times per_page (tiles per page for GQA, 1 for latent), in request order.
-// The CTA's threads build the inclusive prefix pre[0..B] in shared memory, so
-// a persistent grid visits only real work however few requests have rows.
-constexpr int kMaxPersistB = 16384;
-
-__device__ int bulk_items_prefix(const AppendArgs& a, int B, int per_page, int* pre, int* wsum) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const long long P = a.d.page_size;
-  int carry = 0;
-  if (threadIdx.x == 0) pre[0] = 0;
-  for (int base = 0; base < B; base += blockDim.x) {
-    const int r = base + threadIdx.x;
-    int v = 0;
-    if (r < B) {
-      const long long n = req_rows(a, r);
-      if (n > 0) {
-        const long long Lnew = a.seq_lens[r], L0 = Lnew - n;
-        v = (int)((Lnew - 1) / P - L0 / P + 1) * per_page;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane == 31) wsum[wid] = v;
-    __syncthreads();
-    int before = carry;
-    for (int k = 0; k < wid; ++k) before += wsum[k];
-    if (r < B) pre[r + 1] = before + v;
-    int chunk = 0;
-    for (int k = 0; k < nw; ++k) chunk += wsum[k];
-    carry += chunk;
-    __syncthreads();
-  }
-  return carry;
-}
-
-// request owning item i: the r with pre[r] <= i < pre[r + 1]
-__device__ __forceinline__ int item_owner(const int* pre, int B, int i) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= i) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // GQA: persistent CTAs; each warp takes (request, page, tile) items in turn.
@@ -1267,6 +1212,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches) {
   const long long P = a.d.page_size;
   long long pieces = a.from_pool ? (long long)a.src_max_pages : (a.max_new + 2 * P - 2) / P;
   if (pieces <= 0 || a.B <= 0) return cudaSuccess;
+  if (a.d.dtype == KV_DTYPE_E2M1) return launch_append_e2m1(a, pieces, s, launches);
   const long long pages_per_req = pieces;
   if (pieces > 65535) pieces = 65535;  // the kernel strides over the rest
   const long long Pl = a.d.page_size;

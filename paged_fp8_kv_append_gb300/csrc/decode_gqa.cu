@@ -38,6 +38,7 @@
 
 #include "common.cuh"
 #include "decode_plan.cuh"
+#include "e2m1.cuh"
 #include "internal.h"
 
 namespace kvfp8 {
@@ -100,6 +101,48 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const int32_t* pfx, int B
 
 // ------------------------------------------------- tensor-core helpers
 
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+// Eight e2m1 codes -> four f16x2 words, one a byte (low half: low nibble).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c,
+                                              uint32_t& d) {
+  asm("{\n .reg .b8 x, y, z, t;\n mov.b32 {x, y, z, t}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, x;\n cvt.rn.f16x2.e2m1x2 %1, y;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, z;\n cvt.rn.f16x2.e2m1x2 %3, t;\n}\n"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(w));
+}
+// The same, bytes 0 and 1 times slo, 2 and 3 times shi (exact: an e2m1 code
+// times an e4m3 scale has six significant bits).
+__device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t slo, uint32_t shi, uint32_t& a,
+                                              uint32_t& b, uint32_t& c, uint32_t& d) {
+  e2m1x8_to_f16(w, a, b, c, d);
+  a = mul_f16x2(a, slo);
+  b = mul_f16x2(b, slo);
+  c = mul_f16x2(c, shi);
+  d = mul_f16x2(d, shi);
+}
+// the low or the high half of w in both halves
+__device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
+  return __byte_perm(w, w, hi ? 0x3232 : 0x1010);
+}
+// Scale bytes of the tokens 2t, 2t + 1, 2t + 8, 2t + 9 that lie below nv (the
+// bytes behind a request's length are stale and may be NaN).
+__device__ __forceinline__ uint32_t e2m1_token_mask(int nv, int t) {
+  const int a = min(max(nv - 2 * t, 0), 2), b = min(max(nv - 8 - 2 * t, 0), 2);
+  return ((1u << (8 * a)) - 1u) | (((1u << (8 * b)) - 1u) << 16);
+}
+// The 8 x 8 f16 matrix that the warp holds two to a lane (lane 4 r + c: row r,
+// columns 2c and 2c + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 // Four e4m3 codes (bytes 0..3 of w) -> two f16x2 words, lo = (b0, b1) and
 // hi = (b2, b3); exact (every e4m3 value is an f16 value).
@@ -215,26 +258,33 @@ __device__ __forceinline__ uint32_t w_of(const uint4& v, int i) {
 #ifndef KV_GQA_BF16_CONSUMERS
 #define KV_GQA_BF16_CONSUMERS 8
 #endif
+#ifndef KV_GQA_E2M1_CONSUMERS
+#define KV_GQA_E2M1_CONSUMERS 12
+#endif
 #ifndef KV_GQA_RING_KB
 #define KV_GQA_RING_KB 160
 #endif
 
 constexpr int kMaxStages = 40;
 
-template <bool FP8>
+// FMT: the pool's kv_dtype
+template <int FMT>
 struct GqaCfg {
+  static constexpr bool FP8 = FMT == KV_DTYPE_E4M3, FP4 = FMT == KV_DTYPE_E2M1;
   static constexpr int P = 16;                      // tokens per page
   static constexpr int D = 128;                     // head dim (K and V)
-  static constexpr int ES = FP8 ? 1 : 2;            // cache element bytes
-  static constexpr int TILE = P * D * ES;           // bytes of one head's K or V tile
+  // bytes of one head's K or V tile
+  static constexpr int TILE = FP4 ? kE2m1Tile : P * D * (FP8 ? 1 : 2);
   static constexpr int RING = KV_GQA_RING_KB * 1024;
   // consumer warps: e4m3 pages carry half the bytes of bf16 ones, so each
   // byte needs twice the consumer work; measured best at 12 (e4m3) and 8 (bf16)
-  static constexpr int CONSUMERS = FP8 ? KV_GQA_FP8_CONSUMERS : KV_GQA_BF16_CONSUMERS;
+  static constexpr int CONSUMERS =
+      FP4 ? KV_GQA_E2M1_CONSUMERS : FP8 ? KV_GQA_FP8_CONSUMERS : KV_GQA_BF16_CONSUMERS;
   static constexpr int THREADS = (CONSUMERS + 1) * 32;
   static constexpr int R8 = 8;                      // query rows per kv head (padded)
   static constexpr int PFX_CACHE = 1024;            // pfx entries cached in smem
-  static constexpr int PBUF = FP8 ? R8 * P * 2 : R8 * P * 4;  // per-warp P transpose
+  // per-warp P transpose (4-bit: by matrix transposes in registers)
+  static constexpr int PBUF = FP4 ? 0 : FP8 ? R8 * P * 2 : R8 * P * 4;
   // shared memory carve-up (byte offsets)
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_MERGE_O = OFF_RING + RING;                         // [W][R8][D] f32
@@ -318,9 +368,11 @@ __device__ __forceinline__ void merge_piece(float* merge_o, float* merge_ml, int
 
 // WIDE: a consumer warp takes 16 query rows of its kv head instead of 8 (see
 // the wide consumer below); the producer and the ring are the same.
-template <bool FP8, bool WIDE>
+template <int FMT, bool WIDE>
 __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
-  using C = GqaCfg<FP8>;
+  using C = GqaCfg<FMT>;
+  constexpr bool FP4 = C::FP4;
+  constexpr bool FP8 = C::FP8 || FP4;  // block scales, and products in f16
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + C::OFF_RING;
   float* merge_o = reinterpret_cast<float*>(smem + C::OFF_MERGE_O);
@@ -351,7 +403,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
                             : (RB <= 4 && (a.R + C::R8 - 1) / C::R8 == RB);
   // (not in the 16-row e4m3 kernel: at its 128-register cap the plan code
   // made it spill)
-  constexpr bool kCanSelfPlan = !(FP8 && WIDE);
+  constexpr bool kCanSelfPlan = !(FMT == KV_DTYPE_E4M3 && WIDE);
   if (Hs < 1 || RB < 1 || !rows_ok || RB * C::R8 != a.R8 ||
       C::CONSUMERS % Hv != 0 || S < 2 || S > kMaxStages || S % (C::CONSUMERS / Hv) != 0 ||
       stage_bytes * S > C::RING ||
@@ -587,11 +639,12 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           const int row = n0 + g + 8 * hr;
           const bool live = row < R;
           const int tq = live ? row / G : 0, hq = live ? h * G + row % G : 0;
-          const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + 32 * t;
+          const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + (FP4 ? 16 : 32) * t;
           uint4 v[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u)  // dims 32t + 8u .. +7: k-steps 2u and 2u+1
-            v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * u) : make_uint4(0, 0, 0, 0);
+            v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * u + (FP4 && u >= 2 ? 48 : 0))
+                        : make_uint4(0, 0, 0, 0);
           float pw = 1.0f;
           if constexpr (FP8) {  // the row's 128 dims are spread over the 4 threads t
             uint32_t mb = max(max(bf16_absbits_max8(v[0]), bf16_absbits_max8(v[1])),
@@ -648,7 +701,26 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           const uint8_t* Vt = ring + (size_t)stage * stage_bytes + (Hs + hw) * C::TILE;
           // ---------------- S = Q K^T: N tile nt, column g = token tok0 + 2 nt
           float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          if constexpr (FP8) {
+          if constexpr (FP4) {
+            // column g of tile nt is token g + 8 nt; k-steps 0 .. 3 are dims 16t + 4j ..,
+            // 4 .. 7 dims 64 + 16t + 4 (j - 4) ..
+            const uint4 k0 = lds128(Kt + 64 * g + 16 * t), k1 = lds128(Kt + 64 * (g + 8) + 16 * t);
+            uint32_t sg, sh;
+            e4m3x4_to_f16(lds32(Kt + kE2m1Scales + 4 * lane), sg, sh);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
+              const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
+              uint32_t x[4], y[4];
+              e2m1x8_scaled(w_of(k0, w), s0, s0, x[0], x[1], x[2], x[3]);
+              e2m1x8_scaled(w_of(k1, w), s1, s1, y[0], y[1], y[2], y[3]);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint4 qa = lds128(qs + ((2 * w + u) * 32 + lane) * 4);
+                mma16816<true>(s[0], qa.x, qa.y, qa.z, qa.w, x[2 * u], x[2 * u + 1]);
+                mma16816<true>(s[1], qa.x, qa.y, qa.z, qa.w, y[2 * u], y[2 * u + 1]);
+              }
+            }
+          } else if constexpr (FP8) {
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) {  // dims 32t + 16 kh .. +15: k-steps 4kh .. 4kh+3
               const uint4 k0 = lds128(Kt + tok0 * 128 + 32 * t + 16 * kh);
@@ -680,7 +752,10 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
               }
             }
           }
-          // s[nt][e]: row g (e < 2) or g+8, token 4t + 2 nt + (e & 1); log2 domain
+          // s[nt][e]: row g (e < 2) or g+8, token tok_of(nt, e); log2 domain
+          auto tok_of = [&](int nt, int e) {
+            return FP4 ? 8 * nt + 2 * t + (e & 1) : 4 * t + 2 * nt + (e & 1);
+          };
           const float ksc = FP8 ? mt.ks[hw] : 1.0f;
           const float scA = ksc * qscA, scB = ksc * qscB;
 #pragma unroll
@@ -695,7 +770,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int tk = 4 * t + 2 * nt + (e & 1);
+                const int tk = tok_of(nt, e);
                 const int lim = e < 2 ? limA : limB;
                 s[nt][e] = (tk < nv && mt.pos0 + tk <= lim) ? s[nt][e] : -INFINITY;
               }
@@ -739,7 +814,22 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           // ---------------- O += P V: P from registers, V tile dim-major;
           // tokens beyond the length are zeroed in V (stale bytes could be NaN)
           const int keep = min(max(nv - 4 * t, 0), 4);
-          if constexpr (FP8) {
+          if constexpr (FP4) {
+            const uint32_t pa0 = f32x2_to_f16x2(p[0][0], p[0][1]);
+            const uint32_t pa1 = f32x2_to_f16x2(p[0][2], p[0][3]);
+            const uint32_t pa2 = f32x2_to_f16x2(p[1][0], p[1][1]);
+            const uint32_t pa3 = f32x2_to_f16x2(p[1][2], p[1][3]);
+            uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+            e4m3x4_to_f16(lds32(Vt + kE2m1Scales + 4 * lane) & e2m1_token_mask(nv, t), slo, shi);
+            const uint4 v0 = lds128(Vt + 16 * lane), v1 = lds128(Vt + 512 + 16 * lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
+              uint32_t b00, b10, b01, b11;
+              e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, b00, b10, b01, b11);
+              mma16816<true>(acc[2 * i], pa0, pa1, pa2, pa3, b00, b01);
+              mma16816<true>(acc[2 * i + 1], pa0, pa1, pa2, pa3, b10, b11);
+            }
+          } else if constexpr (FP8) {
             const uint32_t pa0 = f32x2_to_f16x2(p[0][0], p[0][1]);
             const uint32_t pa1 = f32x2_to_f16x2(p[0][2], p[0][3]);
             const uint32_t pa2 = f32x2_to_f16x2(p[1][0], p[1][1]);
@@ -795,10 +885,20 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         float* mo = merge_o + warp * C::R8 * D + g * D;
+        if constexpr (FP4) {  // column c of tile i is dim 16 c + i
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<float2*>(mo + 8 * i + 2 * t) =
-              half ? make_float2(acc[i][2], acc[i][3]) : make_float2(acc[i][0], acc[i][1]);
+          for (int i = 0; i < 16; i += 2) {
+            *reinterpret_cast<float2*>(mo + 32 * t + i) =
+                half ? make_float2(acc[i][2], acc[i + 1][2]) : make_float2(acc[i][0], acc[i + 1][0]);
+            *reinterpret_cast<float2*>(mo + 32 * t + 16 + i) =
+                half ? make_float2(acc[i][3], acc[i + 1][3]) : make_float2(acc[i][1], acc[i + 1][1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<float2*>(mo + 8 * i + 2 * t) =
+                half ? make_float2(acc[i][2], acc[i][3]) : make_float2(acc[i][0], acc[i][1]);
+        }
         if (t == 0) {
           float* ml = merge_ml + (warp * C::R8 + g) * 2;
           ml[0] = half ? mB : mA;
@@ -926,7 +1026,21 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
         const uint8_t* Vt = ring + (size_t)stage * stage_bytes + (Hs + hw) * C::TILE;
         // ---------------- S^T = K Q^T  (two accumulator chains for ILP)
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (FP8) {
+        if constexpr (FP4) {
+          // row g (and g+8): dims 16t..16t+15 and 64+16t..64+16t+15, as for e4m3
+          const uint4 kg = lds128(Kt + 64 * g + 16 * t), kh = lds128(Kt + 64 * (g + 8) + 16 * t);
+          uint32_t sg, sh;
+          e4m3x4_to_f16(lds32(Kt + kE2m1Scales + 4 * lane), sg, sh);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
+            const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
+            uint32_t x[4], y[4];
+            e2m1x8_scaled(w_of(kg, w), s0, s0, x[0], x[1], x[2], x[3]);
+            e2m1x8_scaled(w_of(kh, w), s1, s1, y[0], y[1], y[2], y[3]);
+            mma16816<true>(sa, x[0], y[0], x[1], y[1], qf[2 * w][0], qf[2 * w][1]);
+            mma16816<true>(sb, x[2], y[2], x[3], y[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+          }
+        } else if constexpr (FP8) {
           // row g (and g+8): dims 16t..16t+15 and 64+16t..64+16t+15
           const uint4 kA = lds128(Kt + g * 128 + 16 * t);
           const uint4 kB = lds128(Kt + g * 128 + 64 + 16 * t);
@@ -1006,7 +1120,20 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
         // ---------------- P^T to the B-fragment layout via shared memory;
         // tokens beyond the request length are zeroed in V (stale cache bytes
         // could be NaN patterns; 0 * NaN would poison the sum)
-        if constexpr (FP8) {
+        if constexpr (FP4) {
+          // row g's weights of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+          const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p0, p1));
+          const uint32_t b1 = transpose8x8(f32x2_to_f16x2(p2, p3));
+          uint32_t slo, shi;  // scales of group g's same tokens
+          e4m3x4_to_f16(lds32(Vt + kE2m1Scales + 4 * lane) & e2m1_token_mask(nv, t), slo, shi);
+          const uint4 v0 = lds128(Vt + 16 * lane), v1 = lds128(Vt + 512 + 16 * lane);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
+            uint32_t a0, a1, a2, a3;
+            e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, a0, a1, a2, a3);
+            mma16816<true>(acc[i], a0, a1, a2, a3, b0, b1);
+          }
+        } else if constexpr (FP8) {
           __half* pb = reinterpret_cast<__half*>(pbuf);  // [8 rows][16 tokens]
           pb[(2 * t) * 16 + g] = __float2half_rn(p0);
           pb[(2 * t + 1) * 16 + g] = __float2half_rn(p1);
@@ -1085,6 +1212,13 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
     float* mo = merge_o + warp * C::R8 * D;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if constexpr (FP4) {
+        *reinterpret_cast<float2*>(mo + (2 * t) * D + 16 * g + 2 * i) =
+            make_float2(acc[i][0], acc[i][2]);
+        *reinterpret_cast<float2*>(mo + (2 * t + 1) * D + 16 * g + 2 * i) =
+            make_float2(acc[i][1], acc[i][3]);
+        continue;
+      }
       mo[(2 * t) * D + 16 * i + g] = acc[i][0];
       mo[(2 * t + 1) * D + 16 * i + g] = acc[i][1];
       mo[(2 * t) * D + 16 * i + g + 8] = acc[i][2];
@@ -1117,20 +1251,16 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
   }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(GqaCfg<FP8>::THREADS, 1)
+template <int FMT>
+__global__ void __launch_bounds__(GqaCfg<FMT>::THREADS, 1)
     gqa_split_kernel(const DecodeArgs a) {
-  gqa_split_body<FP8, false>(a);
+  gqa_split_body<FMT, false>(a);
 }
 
-__global__ void __launch_bounds__(GqaCfg<true>::THREADS, 1)
+template <int FMT>
+__global__ void __launch_bounds__(GqaCfg<FMT>::THREADS, 1)
     gqa_split_wide_kernel(const DecodeArgs a) {
-  gqa_split_body<true, true>(a);
-}
-
-__global__ void __launch_bounds__(GqaCfg<false>::THREADS, 1)
-    gqa_split_wide_bf16_kernel(const DecodeArgs a) {
-  gqa_split_body<false, true>(a);
+  gqa_split_body<FMT, true>(a);
 }
 
 // ------------------------------------------------- combine
@@ -1334,47 +1464,54 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
 // ------------------------------------------------- host side
 
 // kinds: 0 = e4m3 (8-row consumers), 1 = bf16, 3 = e4m3 with 16-row consumers,
-// 4 = bf16 with 16-row consumers
-int gqa_ring_bytes(int kind) {
-  return (kind == 1 || kind == 4) ? GqaCfg<false>::RING : GqaCfg<true>::RING;
+// 4 = bf16 with 16-row consumers, 5 / 6 = 4-bit with 8- / 16-row consumers
+namespace {
+
+struct GqaKind {
+  void (*kernel)(DecodeArgs);
+  int threads, smem, ring, consumers, tile;
+  bool self_plans;
+};
+template <int FMT>
+constexpr GqaKind gqa_kind_of(bool wide, bool self_plans) {
+  using C = GqaCfg<FMT>;
+  return {wide ? gqa_split_wide_kernel<FMT> : gqa_split_kernel<FMT>, C::THREADS, C::SMEM, C::RING,
+          C::CONSUMERS, C::TILE, self_plans};
 }
-int gqa_max_stages() { return kMaxStages; }
-bool gqa_kind_self_plans(int kind) { return kind == 0 || kind == 1 || kind == 4; }
-int gqa_self_plan_max_batch() {
-  static_assert(GqaCfg<true>::PFX_CACHE == GqaCfg<false>::PFX_CACHE, "one prefix cache size");
-  return GqaCfg<true>::PFX_CACHE - 1;
-}
-int gqa_consumer_warps(int kind) {
-  return (kind == 1 || kind == 4) ? GqaCfg<false>::CONSUMERS : GqaCfg<true>::CONSUMERS;
+const GqaKind& gqa_kind(int kind) {
+  static const GqaKind kinds[7] = {gqa_kind_of<KV_DTYPE_E4M3>(false, true),
+                                   gqa_kind_of<KV_DTYPE_BF16>(false, true),
+                                   {},
+                                   gqa_kind_of<KV_DTYPE_E4M3>(true, false),
+                                   gqa_kind_of<KV_DTYPE_BF16>(true, true),
+                                   gqa_kind_of<KV_DTYPE_E2M1>(false, true),
+                                   gqa_kind_of<KV_DTYPE_E2M1>(true, true)};
+  return kinds[kind];
 }
 
+}  // namespace
+
+int gqa_ring_bytes(int kind) { return gqa_kind(kind).ring; }
+int gqa_tile_bytes(int kind) { return gqa_kind(kind).tile; }
+int gqa_max_stages() { return kMaxStages; }
+bool gqa_kind_self_plans(int kind) { return gqa_kind(kind).self_plans; }
+int gqa_self_plan_max_batch() {
+  static_assert(GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE == GqaCfg<KV_DTYPE_BF16>::PFX_CACHE &&
+                    GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE == GqaCfg<KV_DTYPE_E2M1>::PFX_CACHE,
+                "one prefix cache size");
+  return GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE - 1;
+}
+int gqa_consumer_warps(int kind) { return gqa_kind(kind).consumers; }
+
 int gqa_split_ctas_per_sm(int kind) {
-  static int cache[5] = {-1, -1, -1, -1, -1};
-  if (kind < 0 || kind > 4 || kind == 2) return 0;
+  static int cache[7] = {-1, -1, -1, -1, -1, -1, -1};
+  if (kind < 0 || kind > 6 || kind == 2) return 0;
   if (cache[kind] >= 0) return cache[kind];
+  const GqaKind& k = gqa_kind(kind);
   int n = 0;
-  cudaError_t e;
-  if (kind == 4) {
-    cudaFuncSetAttribute(gqa_split_wide_bf16_kernel,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<false>::SMEM);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_bf16_kernel,
-                                                      GqaCfg<false>::THREADS, GqaCfg<false>::SMEM);
-  } else if (kind == 3) {
-    cudaFuncSetAttribute(gqa_split_wide_kernel,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<true>::SMEM);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_kernel,
-                                                      GqaCfg<true>::THREADS, GqaCfg<true>::SMEM);
-  } else if (kind == 0) {
-    cudaFuncSetAttribute(gqa_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         GqaCfg<true>::SMEM);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_kernel<true>,
-                                                      GqaCfg<true>::THREADS, GqaCfg<true>::SMEM);
-  } else {
-    cudaFuncSetAttribute(gqa_split_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         GqaCfg<false>::SMEM);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_kernel<false>,
-                                                      GqaCfg<false>::THREADS, GqaCfg<false>::SMEM);
-  }
+  cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  const cudaError_t e =
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.kernel, k.threads, k.smem);
   if (e != cudaSuccess || n <= 0) return 0;
   cache[kind] = n;
   return n;
@@ -1387,15 +1524,8 @@ cudaError_t launch_decode_plan(const DecodeArgs& a, cudaStream_t s, int* launche
 }
 
 cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
-  const cudaError_t e =
-      kind == 4   ? launch_pdl(gqa_split_wide_bf16_kernel, dim3(a.grid),
-                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a)
-      : kind == 3 ? launch_pdl(gqa_split_wide_kernel, dim3(a.grid),
-                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
-      : kind == 0 ? launch_pdl(gqa_split_kernel<true>, dim3(a.grid),
-                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
-                  : launch_pdl(gqa_split_kernel<false>, dim3(a.grid),
-                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a);
+  const GqaKind& k = gqa_kind(kind);
+  const cudaError_t e = launch_pdl(k.kernel, dim3(a.grid), dim3(k.threads), k.smem, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -122,6 +122,8 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches);
 // the plan kernel alone (pages popped, tags stamped, lengths advanced), for
 // an append whose rows another kernel writes
 cudaError_t launch_append_plan(const AppendArgs& a, cudaStream_t s, int* launches);
+// the rows of an append into a 4-bit pool (behind the plan kernel); at most `pages` pages a request
+cudaError_t launch_append_e2m1(const AppendArgs& a, long long pages, cudaStream_t s, int* launches);
 // whether a (page, kv head, K|V) tile fits one warp's registers
 bool append_tile_fits(const kv_pool_desc& d);
 // whether a pool-to-pool handoff of B requests into a pool of this shape fits
@@ -174,7 +176,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s, int* launches);
 
 // Kernel configuration chosen for a pool (shape checks + grid).
 struct DecodeConfig {
-  int kind;         // 0 = GQA e4m3, 1 = GQA bf16, 2 = latent e4m3, 3 / 4 = GQA e4m3 / bf16 > 8 rows
+  // 0 = GQA e4m3, 1 = GQA bf16, 2 = latent e4m3, 3 / 4 = GQA e4m3 / bf16 > 8 rows, 5 / 6 = GQA
+  // 4-bit up to 8 / > 8 rows
+  int kind;
   int self_plan;    // the split kernel plans the batch itself (no plan launch)
   int grid;         // split-kernel CTAs
   int R8;           // partial rows per (slot, head)
@@ -187,6 +191,7 @@ struct DecodeConfig {
 // Ring bytes and stage limit of the GQA split kernel (for the host-side
 // choice of heads per unit and ring depth).
 int gqa_ring_bytes(int kind);
+int gqa_tile_bytes(int kind);
 int gqa_max_stages();
 int gqa_consumer_warps(int kind);
 int gqa_self_plan_max_batch();

@@ -14,6 +14,7 @@
 // 128 store V element by element: 16 x 256 4.0 TB/s, 16 x 64 3.4, 64 x 128 1.5 (e4m3; 16 x 128
 // 6.1-6.3, bf16 6.0, latent rows 6.3).
 #include "common.cuh"
+#include "e2m1.cuh"
 #include "internal.h"
 #include "quant.cuh"
 #include "ragged.cuh"
@@ -152,18 +153,83 @@ __device__ __forceinline__ Request request(const ReadArgs& a, int r) {
   return q;
 }
 
-enum Shape { kTile16x128, kLatent, kAny };
+// A head's 4-bit tiles of K and V by one warp.  A value has six significant bits (e2m1.cuh), so
+// its bf16 value is exact.
+__device__ __forceinline__ uint32_t values2(uint32_t codes, float s) {  // the two codes of a byte
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes & 0xFFu), __NV_E2M1);
+  const float2 f = __half22float2(__half2(h));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t c) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(c & 0xFFu), __NV_E4M3)));
+}
+__device__ __forceinline__ void read_head_e2m1(const uint8_t* ksrc, const uint8_t* vsrc, float ks,
+                                               float vs, int slot0, int nrows, uint16_t* kdst,
+                                               uint16_t* vdst, long long stride) {
+  const int lane = threadIdx.x & 31;
+  // K: dims 8 (lane % 16) .. + 7 of slots 2 i + lane / 16
+  const int ck = (lane & 15) >> 1, at = 16 * (ck & 3) + 8 * (ck >> 2) + 4 * (lane & 1);
+  uint32_t k[8], kc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int slot = 2 * i + (lane >> 4);
+    k[i] = __ldg(reinterpret_cast<const uint32_t*>(ksrc + 64 * slot + at));
+    kc[i] = __ldg(ksrc + kE2m1Scales + 16 * (slot & 7) + 4 * (ck & 3) + 2 * (slot >> 3) + (ck >> 2));
+  }
+  // V: dims 4 lane .. + 3 of every slot; w[t]: slots 2t, 2t + 1, 2t + 8, 2t + 9
+  const int j = lane & 3, cv = lane >> 2;
+  uint2 w[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    w[t] = __ldg(reinterpret_cast<const uint2*>(vsrc + 512 * (j >> 1) + 64 * cv + 16 * t +
+                                                8 * (j & 1)));
+  const uint4 vc = __ldg(reinterpret_cast<const uint4*>(vsrc + kE2m1Scales + 16 * cv));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 2 * i + (lane >> 4) - slot0;
+    const float s = e4m3_value(kc[i]) * ks;
+    if (r >= 0 && r < nrows)
+      __stcs(reinterpret_cast<uint4*>(kdst + r * stride + 8 * (lane & 15)),
+             make_uint4(values2(k[i], s), values2(k[i] >> 8, s), values2(k[i] >> 16, s),
+                        values2(k[i] >> 24, s)));
+  }
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {  // slots i and i + 1: the halves of a byte
+    const int t = (i & 7) >> 1, b = 2 * (i >> 3), r = i - slot0;  // bytes b, b + 1 of both words
+    const uint32_t cs = (t == 0 ? vc.x : t == 1 ? vc.y : t == 2 ? vc.z : vc.w) >> (8 * b);
+    const float s0 = e4m3_value(cs) * vs, s1 = e4m3_value(cs >> 8) * vs;
+    float2 f[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t c = ((d < 2 ? w[t].x : w[t].y) >> (8 * (b + (d & 1)))) & 0xFFu;
+      f[d] = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)c, __NV_E2M1)));
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float s = u ? s1 : s0;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn((u ? f[0].y : f[0].x) * s, (u ? f[1].y : f[1].x) * s);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn((u ? f[2].y : f[2].x) * s, (u ? f[3].y : f[3].x) * s);
+      if (r + u >= 0 && r + u < nrows)
+        __stcs(reinterpret_cast<uint2*>(vdst + (r + u) * stride + 4 * lane),
+               make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                          *reinterpret_cast<const uint32_t*>(&hi)));
+    }
+  }
+}
+
+enum Shape { kTile16x128, kLatent, kE2m1, kAny };
 
 // Registers for the loads in flight matter more than warps: 3 (bf16: 2) CTAs an
 // SM read the 16 x 128 tiles back at 6.3 TB/s, 4 (3) at 6.0, 2 at 6.1 (bytes
 // read and written, 32 requests of 4k to 32k rows, 8 heads).
 template <bool FP8, int SHAPE>
-__global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, SHAPE == kLatent || SHAPE == kE2m1 ? 2 : FP8 ? 3 : 2)
     read_rows_kernel(const ReadArgs a) {
   pdl_wait();
   pdl_trigger();
   const kv_pool_desc& d = a.d;
-  const int P = SHAPE == kTile16x128 ? 16 : d.page_size;
+  const int P = SHAPE == kTile16x128 || SHAPE == kE2m1 ? 16 : d.page_size;
   // the last block (its item is seldom one) looks at every request: a refused one's rows may lie
   // behind every item, or in another's
   if (blockIdx.x == gridDim.x - 1)
@@ -200,6 +266,12 @@ __global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : FP8 ? 3 : 2)
       read_rows_of<FP8, 576, 6>(src, s, nrows, Dk, dst, Dk, threadIdx.x, kThreads);
     else
       read_rows_of<FP8, 0, 2>(src, s, nrows, Dk, dst, Dk, threadIdx.x, kThreads);
+  } else if (SHAPE == kE2m1) {
+    for (int h = warp; h < H; h += kThreads / 32) {
+      const long long ph = (long long)p * H + h, at = (row * H + h) * 128;
+      read_head_e2m1(kc + ph * kE2m1Tile, vc + ph * kE2m1Tile, d.k_scale[ph], d.v_scale[ph], slot0,
+                     nrows, a.k_out + at, a.v_out + at, H * 128ll);
+    }
   } else if (SHAPE == kTile16x128) {
     for (int h = warp; h < H; h += kThreads / 32) {
       const long long ph = (long long)p * H + h, at = (row * H + h) * 128;
@@ -227,6 +299,8 @@ cudaError_t launch(const ReadArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)ragged_items(a.total_rows, a.B, d.page_size)), block(kThreads);
   if (d.layout == KV_LAYOUT_LATENT)
     return launch_pdl(read_rows_kernel<FP8, kLatent>, grid, block, 0, s, a);
+  if (FP8 && d.dtype == KV_DTYPE_E2M1)
+    return launch_pdl(read_rows_kernel<true, kE2m1>, grid, block, 0, s, a);
   if (d.page_size == 16 && d.head_dim_k == 128 && d.head_dim_v == 128)
     return launch_pdl(read_rows_kernel<FP8, kTile16x128>, grid, block, 0, s, a);
   return launch_pdl(read_rows_kernel<FP8, kAny>, grid, block, 0, s, a);
@@ -235,7 +309,7 @@ cudaError_t launch(const ReadArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_read_rows(const ReadArgs& a, cudaStream_t s, int* launches) {
-  const cudaError_t e = a.d.dtype == KV_DTYPE_E4M3 ? launch<true>(a, s) : launch<false>(a, s);
+  const cudaError_t e = a.d.dtype != KV_DTYPE_BF16 ? launch<true>(a, s) : launch<false>(a, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
