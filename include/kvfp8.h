@@ -446,6 +446,33 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
                            int32_t max_pages_per_req, int32_t* seq_lens);
 
 /*
+ * kv_append_rotary of heads that are normalised first, in the same pass:
+ * every query and key head x becomes x / sqrt(mean(x^2) + norm_eps) * weight
+ * before it is rotated.
+ *
+ *   q_norm, k_norm  bf16 [head_dim_k] (device, 16-byte aligned): the weights of
+ *                   all query heads and of all key heads; NULL: those heads
+ *                   are not normalised.
+ *   norm_eps        finite, >= 0.  (With 0, a head of zeros gives NaN.)
+ * The mean is over all head_dim_k dims, in fp32, whatever rotary_dim is; between
+ * the norm and the rounding after the rotation nothing is rounded to fewer bits.
+ * A sum of squares beyond fp32 (values of about 1e18) gives zeros, a value that
+ * is not finite NaN.  head_dim_k a power of two up to 512 (where there are
+ * weights); others return KV_ERR_UNSUPPORTED.  Everything else is as for
+ * kv_append_rotary.
+ */
+kv_status kv_append_norm_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                                int32_t total_new, const void* q, int64_t q_stride,
+                                const void* k_new, int64_t k_stride, const void* v_new,
+                                int64_t v_stride, const int32_t* new_indptr,
+                                int32_t max_new_per_req, const int32_t* positions,
+                                int32_t num_axes, const uint8_t* pair_axis,
+                                const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                                const void* q_norm, const void* k_norm, float norm_eps,
+                                void* q_out, int32_t* page_table, uint32_t* exp_tags,
+                                int32_t max_pages_per_req, int32_t* seq_lens);
+
+/*
  * Cached rows back as contiguous bf16 rows (SFS "Quantizing the KV cache":
  * prefill works on a BF16 cache, decode on an FP8 one): a prefix that a bf16
  * prefill reuses, a request that moves to another worker.

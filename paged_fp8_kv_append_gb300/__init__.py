@@ -90,6 +90,9 @@ _lib.kv_decode_step.restype = _i32
 _lib.kv_append_rotary.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                   _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp]
 _lib.kv_append_rotary.restype = _i32
+_lib.kv_append_norm_rotary.argtypes = [*_lib.kv_append_rotary.argtypes[:19], _vp, _vp, _f32,
+                                       *_lib.kv_append_rotary.argtypes[19:]]
+_lib.kv_append_norm_rotary.restype = _i32
 _lib.kv_read_rows.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
 _lib.kv_read_rows.restype = _i32
 _lib.paged_prefill_workspace_size.argtypes = [_vp, _i32, _i32, _i32]
@@ -350,12 +353,9 @@ def kv_decode_step(handle, B, num_q_heads, q_tokens, leave_mask, k_new, v_new, n
     _check(st, "kv_decode_step")
 
 
-def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
-                     positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
-                     seq_lens, stream=None):
-    """kv_append_quantize of keys rotated on the way, with the queries rotated
-    into q_out (see kvfp8.h).  q, k_new and v_new are [rows][heads][dim] with
-    rows any multiple of 8 elements apart; positions int32 [axes][rows]."""
+def _append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                   positions, pair_axis, inv_freq, interleaved, norms, q_out, page_table, exp_tags,
+                   seq_lens, stream):
     rows, Hk, Dk = k_new.shape
     B, num_q_heads, axes, pairs = int(B), int(num_q_heads), positions.shape[0], inv_freq.numel()
     dev = _device()
@@ -374,17 +374,45 @@ def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_ne
         raise ValueError("pair_axis and inv_freq must have the same length")
     max_pages = page_table.shape[-1]
     tags = exp_tags.dtype if exp_tags.dtype in _U32 else _U32
-    st = _lib.kv_append_rotary(
-        handle, _stream_on(stream, dev), B, num_q_heads, rows, qp, qs, kp, ks, vp, vs,
-        _arg(new_indptr, _I32, "new_indptr", dev, B + 1), int(max_new_per_req),
-        _arg(positions, _I32, "positions", dev), axes,
-        _arg(pair_axis, _U8, "pair_axis", dev),
-        _arg(inv_freq, _F64, "inv_freq", dev), 2 * pairs, int(interleaved), qo,
-        _arg(page_table, _I32, "page_table", dev, B * max_pages),
-        _arg(exp_tags, tags, "exp_tags", dev, B * max_pages), max_pages,
-        _arg(seq_lens, _I32, "seq_lens", dev, B))
+    head = (handle, _stream_on(stream, dev), B, num_q_heads, rows, qp, qs, kp, ks, vp, vs,
+            _arg(new_indptr, _I32, "new_indptr", dev, B + 1), int(max_new_per_req),
+            _arg(positions, _I32, "positions", dev), axes,
+            _arg(pair_axis, _U8, "pair_axis", dev),
+            _arg(inv_freq, _F64, "inv_freq", dev), 2 * pairs, int(interleaved))
+    tail = (qo, _arg(page_table, _I32, "page_table", dev, B * max_pages),
+            _arg(exp_tags, tags, "exp_tags", dev, B * max_pages), max_pages,
+            _arg(seq_lens, _I32, "seq_lens", dev, B))
+    if norms is None:
+        return _lib.kv_append_rotary(*head, *tail)
+    q_norm, k_norm, eps = norms
+    return _lib.kv_append_norm_rotary(*head, _arg(q_norm, _BF16, "q_norm", dev, Dk),
+                                      _arg(k_norm, _BF16, "k_norm", dev, Dk), float(eps), *tail)
+
+
+def kv_append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                     positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
+                     seq_lens, stream=None):
+    """kv_append_quantize of keys rotated on the way, with the queries rotated
+    into q_out (see kvfp8.h).  q, k_new and v_new are [rows][heads][dim] with
+    rows any multiple of 8 elements apart; positions int32 [axes][rows]."""
+    st = _append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                        positions, pair_axis, inv_freq, interleaved, None, q_out, page_table,
+                        exp_tags, seq_lens, stream)
     if st:
         _check(st, "kv_append_rotary")
+
+
+def kv_append_norm_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                          positions, pair_axis, inv_freq, interleaved, q_norm, k_norm, norm_eps,
+                          q_out, page_table, exp_tags, seq_lens, stream=None):
+    """kv_append_rotary of heads that are normalised first: x / sqrt(mean(x^2)
+    + norm_eps) * weight, with bf16 weights [dim] for the query heads (q_norm)
+    and the key heads (k_norm); None: those are not normalised (see kvfp8.h)."""
+    st = _append_rotary(handle, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                        positions, pair_axis, inv_freq, interleaved, (q_norm, k_norm, norm_eps),
+                        q_out, page_table, exp_tags, seq_lens, stream)
+    if st:
+        _check(st, "kv_append_norm_rotary")
 
 
 def kv_read_rows(handle, B, page_table, seq_lens, row_start, out_indptr, abort_mask, k_out, v_out,
@@ -556,14 +584,26 @@ class KVPool:
                        new_indptr, max_new_per_req, page_table, exp_tags, seq_lens, q, sm_scale,
                        out, abort_mask, flags, workspace, stream)
 
-    def append_rotary(self, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
-                      positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
-                      seq_lens, stream=None):
-        self._same_device()
+    def _head_shapes(self, k_new, v_new):
         if k_new.shape[1:] != (self.num_kv_heads, self.head_dim_k):
             raise ValueError("k_new: expected [rows][num_kv_heads][head_dim_k]")
         if v_new.shape[1:] != (self.num_kv_heads, self.head_dim_v):
             raise ValueError("v_new: expected [rows][num_kv_heads][head_dim_v]")
+
+    def append_norm_rotary(self, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                           positions, pair_axis, inv_freq, interleaved, q_norm, k_norm, norm_eps,
+                           q_out, page_table, exp_tags, seq_lens, stream=None):
+        self._same_device()
+        self._head_shapes(k_new, v_new)
+        kv_append_norm_rotary(self.handle, B, num_q_heads, q, k_new, v_new, new_indptr,
+                              max_new_per_req, positions, pair_axis, inv_freq, interleaved, q_norm,
+                              k_norm, norm_eps, q_out, page_table, exp_tags, seq_lens, stream)
+
+    def append_rotary(self, B, num_q_heads, q, k_new, v_new, new_indptr, max_new_per_req,
+                      positions, pair_axis, inv_freq, interleaved, q_out, page_table, exp_tags,
+                      seq_lens, stream=None):
+        self._same_device()
+        self._head_shapes(k_new, v_new)
         kv_append_rotary(self.handle, B, num_q_heads, q, k_new, v_new, new_indptr,
                          max_new_per_req, positions, pair_axis, inv_freq, interleaved, q_out,
                          page_table, exp_tags, seq_lens, stream)

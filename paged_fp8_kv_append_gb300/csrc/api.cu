@@ -195,6 +195,76 @@ kv_status prefill_check(const kv_pool_desc& d, int B, int Hq, int total_q) {
   return KV_OK;
 }
 
+// kv_append_rotary and kv_append_norm_rotary (norm weights may be NULL)
+kv_status append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                        int32_t total_new, const void* q, int64_t q_stride, const void* k_new,
+                        int64_t k_stride, const void* v_new, int64_t v_stride,
+                        const int32_t* new_indptr, int32_t max_new_per_req,
+                        const int32_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                        const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                        const void* q_norm, const void* k_norm, float norm_eps, void* q_out, int32_t* page_table, uint32_t* exp_tags,
+                        int32_t max_pages_per_req, int32_t* seq_lens) {
+  if (!pool) return KV_ERR_INVALID_ARG;
+  pool->last_launches = 0;
+  const kv_pool_desc& d = pool->d;
+  if (B < 0 || total_new < 0 || max_new_per_req < 0 || max_pages_per_req <= 0 || num_q_heads < 0)
+    return KV_ERR_INVALID_ARG;
+  if (d.layout != KV_LAYOUT_GQA || !append_tile_fits(d)) return KV_ERR_UNSUPPORTED;
+  if (num_axes < 1 || num_axes > 256 || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
+      rotary_dim > d.head_dim_k || (interleaved != 0 && interleaved != 1))
+    return KV_ERR_INVALID_ARG;
+  if (B == 0) return KV_OK;
+  if (!new_indptr || !page_table || !exp_tags || !seq_lens) return KV_ERR_INVALID_ARG;
+  if (total_new > 0) {
+    const int64_t kw = (int64_t)d.num_kv_heads * d.head_dim_k;
+    const int64_t vw = (int64_t)d.num_kv_heads * d.head_dim_v;
+    const int64_t qw = (int64_t)num_q_heads * d.head_dim_k;
+    if (!k_new || !v_new || !positions || !pair_axis || !inv_freq || !aligned16(k_new) ||
+        !aligned16(v_new) || k_stride < kw || v_stride < vw || k_stride % 8 != 0 ||
+        v_stride % 8 != 0)
+      return KV_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < qw ||
+                            q_stride % 8 != 0))
+      return KV_ERR_INVALID_ARG;
+    // a block for each page that may be touched
+    if (ragged_items(total_new, B, d.page_size) > INT32_MAX) return KV_ERR_UNSUPPORTED;
+    // in place only row for row: at another stride a row's output is a later row's input
+    if (num_q_heads > 0 && q_out == q && q_stride != qw && total_new > 1) return KV_ERR_INVALID_ARG;
+  }
+  RotaryArgs a = {};
+  a.app.d = d;
+  a.app.B = B;
+  a.app.k_new = static_cast<const uint16_t*>(k_new);
+  a.app.v_new = static_cast<const uint16_t*>(v_new);
+  a.app.new_indptr = new_indptr;
+  a.app.total_new = total_new;
+  a.app.max_new = max_new_per_req < total_new ? max_new_per_req : total_new;
+  a.app.page_table = page_table;
+  a.app.exp_tags = exp_tags;
+  a.app.max_pages = max_pages_per_req;
+  a.app.seq_lens = seq_lens;
+  a.q = num_q_heads > 0 ? static_cast<const uint16_t*>(q) : nullptr;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.Hq = num_q_heads;
+  a.total_new = total_new;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.inv_freq = inv_freq;
+  a.num_axes = num_axes;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  a.q_norm = num_q_heads > 0 ? static_cast<const uint16_t*>(q_norm) : nullptr;
+  a.k_norm = static_cast<const uint16_t*>(k_norm);
+  a.norm_eps = norm_eps;
+  int n = 0;
+  const cudaError_t e = launch_append_rotary(a, static_cast<cudaStream_t>(stream), &n);
+  pool->last_launches = n;
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -579,62 +649,33 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
                            const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
                            void* q_out, int32_t* page_table, uint32_t* exp_tags,
                            int32_t max_pages_per_req, int32_t* seq_lens) {
+  return append_rotary(pool, stream, B, num_q_heads, total_new, q, q_stride, k_new, k_stride, v_new,
+                       v_stride, new_indptr, max_new_per_req, positions, num_axes, pair_axis,
+                       inv_freq, rotary_dim, interleaved, nullptr, nullptr, 0.0f, q_out, page_table,
+                       exp_tags, max_pages_per_req, seq_lens);
+}
+
+kv_status kv_append_norm_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
+                                int32_t total_new, const void* q, int64_t q_stride,
+                                const void* k_new, int64_t k_stride, const void* v_new,
+                                int64_t v_stride, const int32_t* new_indptr,
+                                int32_t max_new_per_req, const int32_t* positions,
+                                int32_t num_axes, const uint8_t* pair_axis,
+                                const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                                const void* q_norm, const void* k_norm, float norm_eps,
+                                void* q_out, int32_t* page_table, uint32_t* exp_tags,
+                                int32_t max_pages_per_req, int32_t* seq_lens) {
   if (!pool) return KV_ERR_INVALID_ARG;
   pool->last_launches = 0;
-  const kv_pool_desc& d = pool->d;
-  if (B < 0 || total_new < 0 || max_new_per_req < 0 || max_pages_per_req <= 0 || num_q_heads < 0)
+  // a head's sum runs over a power of two of lanes, 16 dims each
+  const int D = pool->d.head_dim_k;
+  if ((q_norm || k_norm) && (D > 512 || (D & (D - 1)) != 0)) return KV_ERR_UNSUPPORTED;
+  if (!(norm_eps >= 0.0f) || !isfinite(norm_eps) || !aligned16(q_norm) || !aligned16(k_norm))
     return KV_ERR_INVALID_ARG;
-  if (d.layout != KV_LAYOUT_GQA || !append_tile_fits(d)) return KV_ERR_UNSUPPORTED;
-  if (num_axes < 1 || num_axes > 256 || rotary_dim <= 0 || rotary_dim % 16 != 0 ||
-      rotary_dim > d.head_dim_k || (interleaved != 0 && interleaved != 1))
-    return KV_ERR_INVALID_ARG;
-  if (B == 0) return KV_OK;
-  if (!new_indptr || !page_table || !exp_tags || !seq_lens) return KV_ERR_INVALID_ARG;
-  if (total_new > 0) {
-    const int64_t kw = (int64_t)d.num_kv_heads * d.head_dim_k;
-    const int64_t vw = (int64_t)d.num_kv_heads * d.head_dim_v;
-    const int64_t qw = (int64_t)num_q_heads * d.head_dim_k;
-    if (!k_new || !v_new || !positions || !pair_axis || !inv_freq || !aligned16(k_new) ||
-        !aligned16(v_new) || k_stride < kw || v_stride < vw || k_stride % 8 != 0 ||
-        v_stride % 8 != 0)
-      return KV_ERR_INVALID_ARG;
-    if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < qw ||
-                            q_stride % 8 != 0))
-      return KV_ERR_INVALID_ARG;
-    // a block for each page that may be touched
-    if (ragged_items(total_new, B, d.page_size) > INT32_MAX) return KV_ERR_UNSUPPORTED;
-    // in place only row for row: at another stride a row's output is a later row's input
-    if (num_q_heads > 0 && q_out == q && q_stride != qw && total_new > 1) return KV_ERR_INVALID_ARG;
-  }
-  RotaryArgs a = {};
-  a.app.d = d;
-  a.app.B = B;
-  a.app.k_new = static_cast<const uint16_t*>(k_new);
-  a.app.v_new = static_cast<const uint16_t*>(v_new);
-  a.app.new_indptr = new_indptr;
-  a.app.total_new = total_new;
-  a.app.max_new = max_new_per_req < total_new ? max_new_per_req : total_new;
-  a.app.page_table = page_table;
-  a.app.exp_tags = exp_tags;
-  a.app.max_pages = max_pages_per_req;
-  a.app.seq_lens = seq_lens;
-  a.q = num_q_heads > 0 ? static_cast<const uint16_t*>(q) : nullptr;
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.Hq = num_q_heads;
-  a.total_new = total_new;
-  a.positions = positions;
-  a.pair_axis = pair_axis;
-  a.inv_freq = inv_freq;
-  a.num_axes = num_axes;
-  a.rotary_dim = rotary_dim;
-  a.interleaved = interleaved;
-  int n = 0;
-  const cudaError_t e = launch_append_rotary(a, static_cast<cudaStream_t>(stream), &n);
-  pool->last_launches = n;
-  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+  return append_rotary(pool, stream, B, num_q_heads, total_new, q, q_stride, k_new, k_stride, v_new,
+                       v_stride, new_indptr, max_new_per_req, positions, num_axes, pair_axis,
+                       inv_freq, rotary_dim, interleaved, q_norm, k_norm, norm_eps, q_out,
+                       page_table, exp_tags, max_pages_per_req, seq_lens);
 }
 
 kv_status kv_read_rows(kv_pool* pool, void* stream, int32_t B, const int32_t* page_table,

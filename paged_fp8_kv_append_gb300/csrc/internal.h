@@ -141,6 +141,9 @@ struct RotaryArgs {
   const uint8_t* pair_axis;   // [rotary_dim / 2]
   const double* inv_freq;     // [rotary_dim / 2]
   int32_t num_axes, rotary_dim, interleaved;
+  const uint16_t* q_norm;     // bf16 bits [Dk]: heads are normalised first (NULL: they are not)
+  const uint16_t* k_norm;
+  float norm_eps;
 };
 cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launches);
 

@@ -35,6 +35,7 @@
 // and whose keys are read twice: pages of 16 x 64 run at 3.4 TB/s, of 8 x 256 at 2.2.
 #include "append_tile.cuh"
 #include "common.cuh"
+#include "e2m1.cuh"
 #include "internal.h"
 #include "quant.cuh"
 #include "ragged.cuh"
@@ -83,15 +84,53 @@ __device__ __forceinline__ void unit_angles(const float2* row, int j, int rot16,
   }
 }
 
-// The unit's values rotated: x[0..7] of chunk c0, x[8..15] of c1.
-template <bool IL>
+// A head's norm: y = x / sqrt(mean(x^2) + eps) * weight, as a thread applies it to its unit.
+// The sum runs over the upr neighbouring lanes of the row (a power of two), in fp32.
+struct UnitNorm {
+  uint4 w0, w1;  // bf16 weights of the chunks c0 and c1
+  float eps, inv_d;
+  uint32_t lanes;  // the row's lanes
+  int upr;
+  bool on;
+};
+template <bool NORM>
+__device__ __forceinline__ UnitNorm unit_norm(const uint16_t* weight, float eps, int D,
+                                              const UnitPlace& p) {
+  UnitNorm n;
+  n.on = NORM && weight != nullptr;
+  if (!n.on) return n;
+  n.w0 = __ldg(reinterpret_cast<const uint4*>(weight) + p.c0);
+  n.w1 = __ldg(reinterpret_cast<const uint4*>(weight) + p.c1);
+  n.eps = eps;
+  n.inv_d = 1.0f / D;  // exact
+  n.upr = D / 16;
+  const int lane = threadIdx.x & 31;
+  n.lanes = (uint32_t)((1ull << n.upr) - 1) << (lane & ~(n.upr - 1));
+  return n;
+}
+
+// The unit's values normalised (NORM) and rotated: x[0..7] of chunk c0, x[8..15] of c1.
+template <bool IL, bool NORM>
 __device__ __forceinline__ void unit_turn(uint4 a, uint4 b, bool turn, const float2 (&c)[8],
-                                          float (&x)[16]) {
+                                          const UnitNorm& n, float (&x)[16]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     x[2 * k] = bf16_lo(w[k]);
     x[2 * k + 1] = bf16_hi(w[k]);
+  }
+  if (NORM && n.on) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
+    for (int o = 1; o < n.upr; o <<= 1) ss += __shfl_xor_sync(n.lanes, ss, o);
+    const float r = rsqrtf(fmaf(ss, n.inv_d, n.eps));
+    const uint32_t g[8] = {n.w0.x, n.w0.y, n.w0.z, n.w0.w, n.w1.x, n.w1.y, n.w1.z, n.w1.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[2 * k] = x[2 * k] * r * bf16_lo(g[k]);
+      x[2 * k + 1] = x[2 * k + 1] * r * bf16_hi(g[k]);
+    }
   }
   if (!turn) return;
 #pragma unroll
@@ -133,9 +172,10 @@ __device__ __forceinline__ uint2 codes8_fresh(const float* x, float s, float rs)
 // One (page, kv head) key tile by one warp: `nrows` rows from slot0 on; any
 // shape, page and scale, a unit at a time (kept out of line: a fresh page's
 // code stays small, and nothing of it lives across this call).
-template <bool IL>
+template <bool IL, bool NORM>
 __device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride, int nrows, int D,
-                                          int rot16, const float2* cs, bool fp8, bool fresh,
+                                          int rot16, const float2* cs, const uint16_t* weight,
+                                          float eps, bool fp8, bool fresh,
                                           bool requant, float* scale_slot, uint8_t* dst,
                                           int slot0) {
   const int lane = threadIdx.x & 31, upr = D / 16, total = nrows * upr;
@@ -160,14 +200,14 @@ __device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride,
     }
     const float rs = __frcp_rn(s);
 #pragma unroll 1
-    for (int u = lane; u < total; u += 32) {
+    for (int u = lane; u < total; u += 32) {  // (whole rows: total is a multiple of upr)
       const int i = u / upr, j = u - i * upr;
       const UnitPlace p = unit_place(j, rot16, upr);
       const uint4* row = reinterpret_cast<const uint4*>(src + i * stride);
       float2 c[8];
       float x[16];
       if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
-      unit_turn<IL>(row[p.c0], row[p.c1], p.turn, c, x);
+      unit_turn<IL, NORM>(row[p.c0], row[p.c1], p.turn, c, unit_norm<NORM>(weight, eps, D, p), x);
       if (pass == 0) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
@@ -189,10 +229,10 @@ __device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride,
 
 // The same for a whole fresh page of 16 x 128 keys: its loads are issued
 // together and its turned values stay in registers.
-template <bool IL>
+template <bool IL, bool NORM>
 __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long stride, int rot16,
-                                                const float2* cs, bool fp8, float* scale_slot,
-                                                uint8_t* dst) {
+                                                const float2* cs, const uint16_t* weight, float eps,
+                                                bool fp8, float* scale_slot, uint8_t* dst) {
   const int lane = threadIdx.x & 31, j = lane & 7, i0 = lane >> 3;  // rows i0 + 4 k
   const UnitPlace p = unit_place(j, rot16, 8);
   uint4 raw[4][2];
@@ -202,13 +242,14 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
     raw[k][0] = __ldcs(row + p.c0);
     raw[k][1] = __ldcs(row + p.c1);
   }
+  const UnitNorm norm = unit_norm<NORM>(weight, eps, 128, p);
   float x[4][16];
   float m = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float2 c[8];
     if (p.turn) unit_angles<IL>(cs + (i0 + 4 * k) * rot16 * 8, j, rot16, c);
-    unit_turn<IL>(raw[k][0], raw[k][1], p.turn, c, x[k]);
+    unit_turn<IL, NORM>(raw[k][0], raw[k][1], p.turn, c, norm, x[k]);
 #pragma unroll
     for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[k][e]));
   }
@@ -223,7 +264,8 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
   }
   const float s = scale_from_amax(warp_max(m)), rs = __frcp_rn(s);
   if (!scale_fast_ok(s)) {
-    key_tile_any<IL>(src, stride, 16, 128, rot16, cs, true, true, false, scale_slot, dst, 0);
+    key_tile_any<IL, NORM>(src, stride, 16, 128, rot16, cs, weight, eps, true, true, false,
+                           scale_slot, dst, 0);
     return;
   }
   if (lane == 0) *scale_slot = s;
@@ -235,9 +277,74 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
   }
 }
 
+// The keys of a 4-bit tile (e2m1.cuh), from their fp32 values: up to 16 rows from slot0 on, lane
+// (i, j) with unit j of rows i, i + 4, ..  A group's 16 dims are two chunks, the other of which
+// may be another lane's.
+template <bool IL, bool NORM>
+__device__ __noinline__ void key_tile_e2m1(const uint16_t* src, long long stride, int nrows,
+                                           int slot0, int rot16, const float2* cs,
+                                           const uint16_t* weight, float eps, bool fresh,
+                                           float* scale_slot, uint8_t* dst) {
+  const int lane = threadIdx.x & 31, j = lane & 7, i0 = lane >> 3;
+  const UnitPlace p = unit_place(j, rot16, 8);
+  const UnitNorm norm = unit_norm<NORM>(weight, eps, 128, p);
+  // the unit of chunk c, and 8 where it is the unit's second chunk
+  auto unit_of = [&](int c) {
+    return c < rot16 ? c : c < 2 * rot16 ? c - rot16 + 8 : c < 8 + rot16 ? c - rot16 : c;
+  };
+  const int other0 = unit_of(p.c0 ^ 1), other1 = unit_of(p.c1 ^ 1);
+  float x[4][16], m[4][2], block = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + 4 * k;
+    const bool ok = i < nrows;
+    const uint4* row = reinterpret_cast<const uint4*>(src + (ok ? i : 0) * stride);
+    float2 c[8];
+    if (p.turn) unit_angles<IL>(cs + (ok ? i : 0) * rot16 * 8, j, rot16, c);
+    unit_turn<IL, NORM>(row[p.c0], row[p.c1], p.turn, c, norm, x[k]);
+    uint32_t b[2] = {0, 0};  // bit patterns: a NaN is the largest
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      b[e >> 3] = max(b[e >> 3], __float_as_uint(x[k][e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = (h ? other1 : other0) & 7, second = (h ? other1 : other0) & 8;
+      const uint32_t b0 = __shfl_sync(0xffffffffu, b[0], (lane & 24) | o);
+      const uint32_t b1 = __shfl_sync(0xffffffffu, b[1], (lane & 24) | o);
+      m[k][h] = __uint_as_float(max(b[h], second ? b1 : b0));
+      if (ok) block = fmaxf(block, finite_or_zero(m[k][h]));
+    }
+  }
+  const float inv_s = pow2_inverse(e2m1_tile_scale(block, fresh, scale_slot));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int slot = slot0 + i0 + 4 * k;
+    if (i0 + 4 * k >= nrows) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int chunk = h ? p.c1 : p.c0, g = chunk >> 1;
+      float f;
+      const uint32_t sc = e2m1_group_scale(m[k][h], inv_s, f);
+      uint32_t c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = e2m1x2(x[k][8 * h + 2 * e] * f, x[k][8 * h + 2 * e + 1] * f);
+      *reinterpret_cast<uint32_t*>(dst + 64 * slot + 16 * (g & 3) + 8 * (g >> 2) +
+                                   4 * (chunk & 1)) =
+          c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+      if ((chunk & 1) == 0)
+        dst[kE2m1Scales + 16 * (slot & 7) + 4 * (g & 3) + 2 * (slot >> 3) + (g >> 2)] = (uint8_t)sc;
+    }
+  }
+}
+__device__ __noinline__ void value_tile_e2m1(const uint16_t* src, long long stride, int nrows,
+                                             int slot0, bool fresh, float* scale_slot,
+                                             uint8_t* dst) {
+  e2m1_v_tile(src, stride, nrows, slot0, fresh, scale_slot, dst);
+}
+
 // Query heads [h0, h1) of the page's tokens.  A thread keeps one unit of one
 // token, so its sines and cosines stay in registers over the heads.
-template <int kD, bool IL>
+template <int kD, bool IL, bool NORM>
 __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, long long row0,
                                         int nrows, int rot16, int h0, int h1) {
   const int D = kD ? kD : a.app.d.head_dim_k, upr = D / 16, groups = kThreads / upr;
@@ -248,6 +355,7 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
   const UnitPlace p = unit_place(j, rot16, upr);
   float2 c[8];
   if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+  const UnitNorm norm = unit_norm<NORM>(a.q_norm, a.norm_eps, D, p);
   const uint16_t* q = a.q + (row0 + i) * a.q_stride;
   uint16_t* out = a.q_out + (row0 + i) * a.Hq * D;
   for (int h = h0 + g - i * hs; h < h1; h += kAhead * hs) {
@@ -263,7 +371,7 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
     for (int k = 0; k < kAhead; ++k)
       if (h + k * hs < h1) {
         float x[16];
-        unit_turn<IL>(r[k][0], r[k][1], p.turn, c, x);
+        unit_turn<IL, NORM>(r[k][0], r[k][1], p.turn, c, norm, x);
         uint4* o = reinterpret_cast<uint4*>(out + (long long)(h + k * hs) * D);
         o[p.c0] = pack8_bf16(x);
         o[p.c1] = pack8_bf16(x + 8);
@@ -272,7 +380,7 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
 }
 
 // The part's kv heads of the page: a warp a tile.
-template <int kD, bool IL>
+template <int kD, bool IL, bool NORM, bool FP4>
 __device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* cs, int r,
                                             long long jp, long long L0, long long row0, int nrows,
                                             int slot0, int rot16) {
@@ -298,15 +406,25 @@ __device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* c
   for (int t = warp; t < 2 * nh; t += kWarps) {
     const int h = h0 + (t < nh ? t : t - nh);
     const long long ph = (long long)pg * H + h;
-    if (t < nh) {
+    if constexpr (FP4) {
+      if (t < nh)
+        key_tile_e2m1<IL, NORM>(ap.k_new + row0 * a.k_stride + (long long)h * 128, a.k_stride,
+                                nrows, slot0, rot16, cs, a.k_norm, a.norm_eps, fresh,
+                                d.k_scale + ph, kc + ph * kE2m1Tile);
+      else
+        value_tile_e2m1(ap.v_new + row0 * a.v_stride + (long long)h * 128, a.v_stride, nrows,
+                        slot0, fresh, d.v_scale + ph, vc + ph * kE2m1Tile);
+      continue;
+    } else if (t < nh) {
       const uint16_t* src = ap.k_new + row0 * a.k_stride + (long long)h * Dk;
       float* scale = fp8 ? d.k_scale + ph : nullptr;
       uint8_t* dst = kc + ph * P * Dk * es;
       if (kD == 128 && nrows == 16 && P == 16)
-        key_page_16x128<IL>(src, a.k_stride, rot16, cs, fp8, scale, dst);
+        key_page_16x128<IL, NORM>(src, a.k_stride, rot16, cs, a.k_norm, a.norm_eps, fp8, scale,
+                                  dst);
       else
-        key_tile_any<IL>(src, a.k_stride, nrows, Dk, rot16, cs, fp8, fresh, requant, scale, dst,
-                         slot0);
+        key_tile_any<IL, NORM>(src, a.k_stride, nrows, Dk, rot16, cs, a.k_norm, a.norm_eps, fp8,
+                               fresh, requant, scale, dst, slot0);
     } else {
       const uint16_t* src = ap.v_new + row0 * a.v_stride + (long long)h * Dv;
       float* scale = fp8 ? d.v_scale + ph : nullptr;
@@ -320,8 +438,9 @@ __device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* c
   }
 }
 
-// kD: head_dim_k when it is known (0: any); IL: neighbouring pairs
-template <int kD, bool IL>
+// kD: head_dim_k when it is known (0: any); IL: neighbouring pairs; NORM: heads are normalised; FP4: a
+// 4-bit pool (kernels of their own: the calls of its tiles cost the others registers)
+template <int kD, bool IL, bool NORM, bool FP4>
 __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const RotaryArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const AppendArgs& ap = a.app;
@@ -378,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
   __syncthreads();
   const int S = gridDim.y, part = blockIdx.y;
   if (a.q != nullptr)
-    queries<kD, IL>(a, cs, row0, nrows, rot16, (int)((long long)a.Hq * part / S),
+    queries<kD, IL, NORM>(a, cs, row0, nrows, rot16, (int)((long long)a.Hq * part / S),
                     (int)((long long)a.Hq * (part + 1) / S));
-  keys_values<kD, IL>(a, cs, r, jp, L0, row0, nrows, slot0, rot16);
+  keys_values<kD, IL, NORM, FP4>(a, cs, r, jp, L0, row0, nrows, slot0, rot16);
 }
 
 }  // namespace
@@ -397,9 +516,17 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
   // at most 32 KB: P * Dk <= 2048
   const size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
   const bool il = a.interleaved != 0;
-  const auto kernel = a.app.d.head_dim_k == 128
-                          ? (il ? append_rotary_kernel<128, true> : append_rotary_kernel<128, false>)
-                          : (il ? append_rotary_kernel<0, true> : append_rotary_kernel<0, false>);
+  const bool norm = a.q_norm != nullptr || a.k_norm != nullptr;
+  const bool fp4 = a.app.d.dtype == KV_DTYPE_E2M1;
+  // [4-bit, head_dim_k 128, any][neighbouring pairs][norm]
+  static constexpr void (*const kKernels[3][2][2])(RotaryArgs) = {
+      {{append_rotary_kernel<128, false, false, true>, append_rotary_kernel<128, false, true, true>},
+       {append_rotary_kernel<128, true, false, true>, append_rotary_kernel<128, true, true, true>}},
+      {{append_rotary_kernel<128, false, false, false>, append_rotary_kernel<128, false, true, false>},
+       {append_rotary_kernel<128, true, false, false>, append_rotary_kernel<128, true, true, false>}},
+      {{append_rotary_kernel<0, false, false, false>, append_rotary_kernel<0, false, true, false>},
+       {append_rotary_kernel<0, true, false, false>, append_rotary_kernel<0, true, true, false>}}};
+  const auto kernel = kKernels[fp4 ? 0 : a.app.d.head_dim_k == 128 ? 1 : 2][il][norm];
   e = launch_pdl(kernel, dim3((unsigned)items, split), dim3(kThreads), smem, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
