@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvfp8.so")
 SOURCES = ["api.cu", "append.cu", "append_e2m1.cu", "verify.cu", "release.cu", "rotary.cu",
-           "read.cu", "prefill.cu", "decode_gqa.cu", "decode_latent.cu", "noalloc.cu"]
+           "read.cu", "prefill.cu", "decode_gqa.cu", "decode_e2m1.cu", "decode_latent.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

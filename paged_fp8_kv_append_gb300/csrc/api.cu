@@ -38,12 +38,10 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     const long long R = (long long)T * G;
     if (d.head_dim_k != 128 || d.head_dim_v != 128 || d.page_size != 16 || R > 64)
       return KV_ERR_UNSUPPORTED;
-    // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16)
-    // (5, 6: 4-bit)
-    cfg->kind = d.dtype == KV_DTYPE_E2M1 ? (R > 8 ? 6 : 5)
-                : d.dtype == KV_DTYPE_E4M3 ? (R > 8 ? 3 : 0)
-                                           : (R > 8 ? 4 : 1);
-    const bool bf16 = d.dtype == KV_DTYPE_BF16, wide = R > 8;
+    // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16, 6: 4-bit)
+    const bool bf16 = d.dtype == KV_DTYPE_BF16, fp4 = d.dtype == KV_DTYPE_E2M1, wide = R > 8;
+    cfg->kind = fp4 ? (wide ? 6 : 5) : bf16 ? (wide ? 4 : 1) : (wide ? 3 : 0);
+    const int warps = fp4 ? e2m1_split_warps() : gqa_consumer_warps(cfg->kind);
     // heads per unit: the largest power of two <= 8 (<= 4 for bf16, whose
     // tiles are twice as large) dividing Hkv, with heads x row blocks dividing
     // the consumer warp count; 16-row blocks may be padded with whole unused
@@ -52,33 +50,38 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     int hs = 0;
     for (; rbw <= (wide ? 4 : 1); ++rbw) {
       hs = bf16 ? 4 : 8;
-      while (hs > 0 &&
-             (d.num_kv_heads % hs != 0 || gqa_consumer_warps(cfg->kind) % (hs * rbw) != 0))
-        hs >>= 1;
+      while (hs > 0 && (d.num_kv_heads % hs != 0 || warps % (hs * rbw) != 0)) hs >>= 1;
       if (hs > 0) break;
     }
     if (hs == 0) return KV_ERR_UNSUPPORTED;  // no split of the consumers fits
     const int rb = wide ? 2 * rbw : rbw;  // row blocks of 8 in the partial layout
     cfg->Hs = hs;
-    const int stage_bytes = 2 * hs * gqa_tile_bytes(cfg->kind);
-    cfg->stages = gqa_ring_bytes(cfg->kind) / stage_bytes;
-    if (cfg->stages > gqa_max_stages()) cfg->stages = gqa_max_stages();
-    // A consumer warp serves every (consumers/Hs)-th unit; the ring depth must
-    // be a multiple of that stride so each warp sees every phase of the stages
-    // it uses (parity waits cannot tell phase n from phase n-2).
-    const int wph = gqa_consumer_warps(cfg->kind) / (hs * rbw);
-    cfg->stages -= cfg->stages % wph;
-    if (cfg->stages < 2 || cfg->stages < wph) return KV_ERR_UNSUPPORTED;
+    cfg->stages = 0;
+    if (!fp4) {  // (a warp of a 4-bit pool's kernel has a ring of its own)
+      const int stage_bytes = 2 * hs * d.page_size * d.head_dim_k * (bf16 ? 2 : 1);
+      cfg->stages = gqa_ring_bytes(cfg->kind) / stage_bytes;
+      if (cfg->stages > gqa_max_stages()) cfg->stages = gqa_max_stages();
+      // A consumer warp serves every (consumers/Hs)-th unit; the ring depth must
+      // be a multiple of that stride so each warp sees every phase of the stages
+      // it uses (parity waits cannot tell phase n from phase n-2).
+      const int wph = warps / (hs * rbw);
+      cfg->stages -= cfg->stages % wph;
+      if (cfg->stages < 2 || cfg->stages < wph) return KV_ERR_UNSUPPORTED;
+    }
     const int sms = sm_count();
-    const int per_sm = sms > 0 ? gqa_split_ctas_per_sm(cfg->kind) : 0;
+    const int per_sm = sms <= 0 ? 0
+                       : fp4    ? e2m1_split_ctas_per_sm(cfg->kind)
+                                : gqa_split_ctas_per_sm(cfg->kind);
     if (sms <= 0 || per_sm <= 0) return KV_ERR_CUDA;
     cfg->grid = sms * per_sm;
     cfg->R8 = 8 * rb;
     cfg->HG = d.num_kv_heads / hs;
-    cfg->unit_tokens = d.page_size;
+    cfg->unit_tokens = fp4 ? 2 * d.page_size : d.page_size;
+    cfg->sub = fp4 ? warps / (hs * rbw) : 1;
     // the split kernel's CTAs plan a batch that fits their shared-memory
     // prefix cache themselves: no separate plan launch
-    cfg->self_plan = (gqa_kind_self_plans(cfg->kind) && B <= gqa_self_plan_max_batch()) ? 1 : 0;
+    cfg->self_plan =
+        ((fp4 || gqa_kind_self_plans(cfg->kind)) && B <= gqa_self_plan_max_batch()) ? 1 : 0;
     return KV_OK;
   }
   // latent layout: query rows (T tokens x Hq heads) in blocks of 64; the
@@ -99,6 +102,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
   cfg->HG = T * Hq / rb;
   cfg->stages = 0;
   cfg->unit_tokens = latent_unit_tokens();
+  cfg->sub = 1;
   return KV_OK;
 }
 
@@ -107,7 +111,8 @@ size_t decode_ws_layout(const kv_pool_desc& d, int B, int Hkv, const DecodeConfi
   // one partial slot per (CTA, segment) piece; segments are (request, head
   // group) or (request, row block); each slot holds Hs heads x R8 rows
   (void)Hkv;
-  const long long slots = (long long)B * cfg.HG + cfg.grid;
+  // (4-bit pools: cfg.sub of them)
+  const long long slots = ((long long)B * cfg.HG + cfg.grid) * cfg.sub;
   size_t off = 0;
   const size_t o_pfx = off;
   off = align256(off + sizeof(int32_t) * (size_t)(B + 1));
@@ -172,6 +177,7 @@ kv_status decode_prepare(kv_pool* pool, int32_t B, int32_t Hq, int32_t T, const 
   x.HG = cfg.HG;
   x.stages = cfg.stages;
   x.unit_tokens = cfg.unit_tokens;
+  x.sub = cfg.sub;
   x.self_plan = cfg.self_plan;
   x.exp_tags = nullptr;
   x.abort_out = nullptr;
@@ -776,6 +782,7 @@ namespace kvfp8 {
 
 cudaError_t launch_decode_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
   if (kind == 2) return launch_latent_split(a, s, launches);
+  if (kind >= 5) return launch_e2m1_split(a, kind, s, launches);
   return launch_gqa_split(a, kind, s, launches);
 }
 

@@ -1,0 +1,804 @@
+// decode_e2m1.cu -- split-K paged decode attention over a 4-bit pool
+// (KV_DTYPE_E2M1): the split kernels; batch plan, partials and combine are those
+// of decode_gqa.cu.
+//
+// "Smaller, faster, safer: running Kimi and GLM at scale", section "Quantizing
+// the KV cache": the kernel converts values as it reads them.
+//
+// A 4-bit page takes 9/16 of the bytes of an e4m3 one and the same arithmetic, so at
+// HBM speed a page of a kv head has 420 cycles of a scheduler, where the e4m3
+// kernels' page has 750.
+//
+// Work: units of two pages of one request for a group of Hs kv heads, cut into equal
+// ranges, one per persistent CTA; a warp serves one (kv head, block of query rows) of
+// every few units.  There is no producer warp, and nothing is shared between warps
+// but the batch plan: each fetches its own head's tiles into a ring of its own (bulk
+// copies of 1152 bytes), keeps its own online softmax and writes its own partial,
+// which the combine kernel merges with the others of the segment.
+//
+// Two pages are taken together: their products are independent chains, and waits,
+// bookkeeping and the softmax's vote are one for 32 tokens.
+//
+// A row's running reference is moved only when a score exceeds it by more than
+// 2^kSlack: weights stay below 2^kSlack (f16 operands; sums in fp32), and most pages
+// need one vote where a maximum over the lanes takes six shuffles.
+//
+// Codes become f16 by cvt.rn.f16x2.e2m1x2 (a byte each, as cheap as a move beside
+// the products); K's and V's group scales multiply them there (exact: six
+// significant bits), block scales go to the scores (K) and as an exponent bias into
+// the weights (V), as an e4m3 page's scales do.
+#include <climits>
+
+#include "common.cuh"
+#include "decode_plan.cuh"
+#include "e2m1.cuh"
+#include "gqa_split.cuh"
+#include "internal.h"
+
+namespace kvfp8 {
+namespace {
+
+#ifndef KV_E2M1_WARPS
+#define KV_E2M1_WARPS 12
+#endif
+#ifndef KV_E2M1_STAGES
+#define KV_E2M1_STAGES 3
+#endif
+#ifndef KV_E2M1_STAGES16
+#define KV_E2M1_STAGES16 3
+#endif
+#ifndef KV_E2M1_PAIR16
+#define KV_E2M1_PAIR16 1
+#endif
+
+constexpr int kWarps = KV_E2M1_WARPS, kThreads = kWarps * 32;
+constexpr int kStage = 4 * kE2m1Tile;  // a unit: K of its two pages, then V
+constexpr int kPfxCache = 1024;        // plan entries cached in shared memory
+
+template <bool WIDE>
+struct E2m1Cfg {
+  static constexpr int ST = WIDE ? KV_E2M1_STAGES16 : KV_E2M1_STAGES;  // units in a warp's ring
+  // shared memory carve-up (byte offsets)
+  static constexpr int OFF_Q = kWarps * ST * kStage;              // WIDE: [W] Q operands of 4 KB
+  static constexpr int OFF_BAR = OFF_Q + (WIDE ? kWarps * 4096 : 0);  // [W][ST] data ready
+  static constexpr int OFF_PFX = OFF_BAR + kWarps * ST * 8;
+  static constexpr int OFF_FLAG = OFF_PFX + kPfxCache * 4;        // abort flag
+  static constexpr int OFF_WSUM = OFF_FLAG + 16;                  // [32] plan scan warp sums
+  static constexpr int SMEM = OFF_WSUM + 32 * 4;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+constexpr float kUnset = -1e38f;  // the reference of a row that has seen no position
+constexpr float kSlack = 8.0f;
+
+struct FalseType {
+  static constexpr bool value = false;
+};
+struct TrueType {
+  static constexpr bool value = true;
+};
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+// Eight e2m1 codes -> four f16x2 words, one a byte (low half: low nibble).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c,
+                                              uint32_t& d) {
+  asm("{\n .reg .b8 x, y, z, t;\n mov.b32 {x, y, z, t}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, x;\n cvt.rn.f16x2.e2m1x2 %1, y;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, z;\n cvt.rn.f16x2.e2m1x2 %3, t;\n}\n"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(w));
+}
+// The same, bytes 0 and 1 times slo, 2 and 3 times shi (exact: an e2m1 code
+// times an e4m3 scale has six significant bits).
+__device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t slo, uint32_t shi, uint32_t& a,
+                                              uint32_t& b, uint32_t& c, uint32_t& d) {
+  e2m1x8_to_f16(w, a, b, c, d);
+  a = mul_f16x2(a, slo);
+  b = mul_f16x2(b, slo);
+  c = mul_f16x2(c, shi);
+  d = mul_f16x2(d, shi);
+}
+// the low or the high half of w in both halves
+__device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
+  return __byte_perm(w, w, hi ? 0x3232 : 0x1010);
+}
+// Scale bytes of the tokens 2t, 2t + 1, 2t + 8, 2t + 9 that lie below nv (the
+// bytes behind a request's length are stale and may be NaN).
+__device__ __forceinline__ uint32_t e2m1_token_mask(int nv, int t) {
+  const int a = min(max(nv - 2 * t, 0), 2), b = min(max(nv - 8 - 2 * t, 0), 2);
+  return ((1u << (8 * a)) - 1u) | (((1u << (8 * b)) - 1u) << 16);
+}
+// The 8 x 8 f16 matrix that the warp holds two to a lane (lane 4 r + c: row r,
+// columns 2c and 2c + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// A page as a warp meets it: its head's tiles, and what is known of them.
+struct E2m1Page {
+  const uint8_t *k, *v;
+  float ks, vs;  // block scales
+  int nv, pos0;  // tokens below the request's length, the first one's position
+};
+
+// Up to 8 query rows of a kv head: S^T = K Q^T (M = 16 tokens, N = 8 rows) and
+// O^T += V^T P^T.  Lane (g, t): tokens g, g + 8 and rows 2t, 2t + 1 of the scores.
+struct E2m1Rows8 {
+  float &m0, &m1, &l0, &l1;
+  float (&acc)[8][4];
+  const uint32_t (&qf)[8][2];
+  const float qsc0, qsc1;  // score scales of rows 2t, 2t + 1
+  const int G, T, seen0;   // query token tq sees positions 0 .. seen0 + tq
+
+  // EDGE: some position may lie behind the length or behind a row's last one
+  template <int NP, bool EDGE>
+  __device__ __forceinline__ void pages(const E2m1Page (&pg)[NP]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint4 va[NP][2];
+    float s[NP][4];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const uint4 kg = lds128(pg[u].k + 64 * g + 16 * t);
+      const uint4 kh = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
+      uint32_t sg, sh;
+      e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg, sh);
+      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
+        const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
+        uint32_t x[4], y[4];
+        e2m1x8_scaled(w_of(kg, w), s0, s0, x[0], x[1], x[2], x[3]);
+        e2m1x8_scaled(w_of(kh, w), s1, s1, y[0], y[1], y[2], y[3]);
+        mma16816<true>(sa, x[0], y[0], x[1], y[1], qf[2 * w][0], qf[2 * w][1]);
+        mma16816<true>(sb, x[2], y[2], x[3], y[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[u][e] = sa[e] + sb[e];
+      va[u][0] = lds128(pg[u].v + 16 * lane);
+      va[u][1] = lds128(pg[u].v + 512 + 16 * lane);
+    }
+    // ---- weights against the rows' references
+    float bias[NP], p[NP][4], big = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      bias[u] = __log2f(pg[u].vs);
+      const float c0 = bias[u] - m0, c1 = bias[u] - m1;
+      const float sc0 = pg[u].ks * qsc0, sc1 = pg[u].ks * qsc1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[u][e] = fmaf(s[u][e], e & 1 ? sc1 : sc0, e & 1 ? c1 : c0);
+    }
+    if constexpr (EDGE) {
+      const int lim0 = seen0 + min(2 * t / G, T - 1), lim1 = seen0 + min((2 * t + 1) / G, T - 1);
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = g + 8 * (e >> 1);
+          if (tok >= pg[u].nv || pg[u].pos0 + tok > (e & 1 ? lim1 : lim0)) p[u][e] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < NP; ++u)
+      big = fmaxf(big, fmaxf(fmaxf(p[u][0], p[u][1]), fmaxf(p[u][2], p[u][3])));
+    if (__any_sync(0xffffffffu, big > kSlack)) {
+      float n0 = kUnset, n1 = kUnset;
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // the biased scores themselves
+          const float y = fmaf(s[u][e], pg[u].ks * (e & 1 ? qsc1 : qsc0), bias[u]);
+          p[u][e] = p[u][e] == -INFINITY ? -INFINITY : y;
+          if (e & 1) n1 = fmaxf(n1, p[u][e]);
+          else n0 = fmaxf(n0, p[u][e]);
+        }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+      }
+      n0 = fmaxf(n0, m0);
+      n1 = fmaxf(n1, m1);
+      const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[i][0] *= a0;
+        acc[i][1] *= a1;
+        acc[i][2] *= a0;
+        acc[i][3] *= a1;
+      }
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[u][e] -= e & 1 ? n1 : n0;
+    }
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[u][e] = fast_exp2(p[u][e]);
+      const float unbias = pow2_inverse(pg[u].vs);
+      l0 = fmaf(p[u][0] + p[u][2], unbias, l0);
+      l1 = fmaf(p[u][1] + p[u][3], unbias, l1);
+    }
+    // ---- O^T += V^T P^T: row g's weights of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p[u][0], p[u][1]));
+      const uint32_t b1 = transpose8x8(f32x2_to_f16x2(p[u][2], p[u][3]));
+      const uint32_t sw = lds32(pg[u].v + kE2m1Scales + 4 * lane);
+      auto add = [&](uint32_t scales, uint32_t c0, uint32_t c1) {
+        uint32_t slo, shi;  // scales of group g's same tokens
+        e4m3x4_to_f16(scales, slo, shi);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
+          uint32_t a0, a1, a2, a3;
+          e2m1x8_scaled(w_of(va[u][i >> 2], i & 3), slo, shi, a0, a1, a2, a3);
+          mma16816<true>(acc[i], a0, a1, a2, a3, c0, c1);
+        }
+      };
+      if constexpr (!EDGE) {
+        add(sw, b0, b1);
+      } else {
+        // A scale of NaN (a value that was not finite; or stale bytes behind the
+        // length) times a weight of zero is NaN: a query token's rows are added
+        // over the tokens that it sees alone.
+        const int mine = min(g / G, T - 1);
+#pragma unroll 1
+        for (int tq = 0; tq < T; ++tq) {
+          const uint32_t on = mine == tq ? 0xFFFFFFFFu : 0u;
+          add(sw & e2m1_token_mask(min(pg[u].nv, seen0 + tq - pg[u].pos0 + 1), t), b0 & on, b1 & on);
+        }
+      }
+    }
+  }
+  // a row that has seen nothing: the merge's -inf
+  __device__ __forceinline__ void finish() {
+    if (m0 == kUnset) m0 = -INFINITY;
+    if (m1 == kUnset) m1 = -INFINITY;
+  }
+};
+
+// 16 query rows of a kv head from n0 on: S = Q K^T (M = 16 rows, N = 8 tokens) and
+// O += P V (N = 8 dims, K = 16 tokens).  Lane (g, t): rows g, g + 8 and tokens 2t,
+// 2t + 1, 2t + 8, 2t + 9, so the weights are the second product's A operand as they are.
+struct E2m1Rows16 {
+  float &mA, &mB, &lA, &lB;
+  float (&acc)[16][4];
+  const uint32_t* qs;  // Q as A operands, [k-step][lane] 16-byte words in shared memory
+  const float qscA, qscB;
+  const int n0, G, T, seen0;
+
+  // EDGE: some position may lie behind the length or behind a row's last one
+  template <int NP, bool EDGE>
+  __device__ __forceinline__ void pages(const E2m1Page (&pg)[NP]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float s[NP][2][4];
+    {
+      uint4 kg[NP], kh[NP];
+      uint32_t sg[NP], sh[NP];
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        kg[u] = lds128(pg[u].k + 64 * g + 16 * t);
+        kh[u] = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
+        e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg[u], sh[u]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][0][e] = s[u][1][e] = 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
+        const uint4 q0 = lds128(qs + (2 * w * 32 + lane) * 4);
+        const uint4 q1 = lds128(qs + ((2 * w + 1) * 32 + lane) * 4);
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+          const uint32_t s0 = half_of(sg[u], w >> 1), s1 = half_of(sh[u], w >> 1);
+          uint32_t x[4], y[4];
+          e2m1x8_scaled(w_of(kg[u], w), s0, s0, x[0], x[1], x[2], x[3]);
+          e2m1x8_scaled(w_of(kh[u], w), s1, s1, y[0], y[1], y[2], y[3]);
+          mma16816<true>(s[u][0], q0.x, q0.y, q0.z, q0.w, x[0], x[1]);
+          mma16816<true>(s[u][1], q0.x, q0.y, q0.z, q0.w, y[0], y[1]);
+          mma16816<true>(s[u][0], q1.x, q1.y, q1.z, q1.w, x[2], x[3]);
+          mma16816<true>(s[u][1], q1.x, q1.y, q1.z, q1.w, y[2], y[3]);
+        }
+      }
+    }
+    // s[u][nt][e]: row g (e < 2) or g + 8, token 8 nt + 2t + (e & 1)
+    float bias[NP], p[NP][2][4], big = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      bias[u] = __log2f(pg[u].vs);
+      const float cA = bias[u] - mA, cB = bias[u] - mB;
+      const float scA = pg[u].ks * qscA, scB = pg[u].ks * qscB;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[u][nt][e] = fmaf(s[u][nt][e], e < 2 ? scA : scB, e < 2 ? cA : cB);
+    }
+    if constexpr (EDGE) {
+      const int limA = seen0 + min((n0 + g) / G, T - 1), limB = seen0 + min((n0 + g + 8) / G, T - 1);
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = 8 * nt + 2 * t + (e & 1);
+            if (tok >= pg[u].nv || pg[u].pos0 + tok > (e < 2 ? limA : limB))
+              p[u][nt][e] = -INFINITY;
+          }
+    }
+#pragma unroll
+    for (int u = 0; u < NP; ++u)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        big = fmaxf(big, fmaxf(fmaxf(p[u][nt][0], p[u][nt][1]), fmaxf(p[u][nt][2], p[u][nt][3])));
+    if (__any_sync(0xffffffffu, big > kSlack)) {
+      float nA = kUnset, nB = kUnset;
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = fmaf(s[u][nt][e], pg[u].ks * (e < 2 ? qscA : qscB), bias[u]);
+            float& x = p[u][nt][e];
+            x = x == -INFINITY ? -INFINITY : y;
+            if (e < 2) nA = fmaxf(nA, x);
+            else nB = fmaxf(nB, x);
+          }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, o));
+        nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, o));
+      }
+      nA = fmaxf(nA, mA);
+      nB = fmaxf(nB, mB);
+      const float aA = fast_exp2(mA - nA), aB = fast_exp2(mB - nB);
+      mA = nA;
+      mB = nB;
+      lA *= aA;
+      lB *= aB;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        acc[i][0] *= aA;
+        acc[i][1] *= aA;
+        acc[i][2] *= aB;
+        acc[i][3] *= aB;
+      }
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[u][nt][e] -= e < 2 ? nA : nB;
+    }
+    uint32_t pa[NP][4];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[u][nt][e] = fast_exp2(p[u][nt][e]);
+      const float unbias = pow2_inverse(pg[u].vs);
+      lA = fmaf((p[u][0][0] + p[u][0][1]) + (p[u][1][0] + p[u][1][1]), unbias, lA);
+      lB = fmaf((p[u][0][2] + p[u][0][3]) + (p[u][1][2] + p[u][1][3]), unbias, lB);
+      pa[u][0] = f32x2_to_f16x2(p[u][0][0], p[u][0][1]);
+      pa[u][1] = f32x2_to_f16x2(p[u][0][2], p[u][0][3]);
+      pa[u][2] = f32x2_to_f16x2(p[u][1][0], p[u][1][1]);
+      pa[u][3] = f32x2_to_f16x2(p[u][1][2], p[u][1][3]);
+    }
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const uint4 v0 = lds128(pg[u].v + 16 * lane), v1 = lds128(pg[u].v + 512 + 16 * lane);
+      const uint32_t sw = lds32(pg[u].v + kE2m1Scales + 4 * lane);
+      auto add = [&](uint32_t scales, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+        e4m3x4_to_f16(scales, slo, shi);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
+          uint32_t b00, b10, b01, b11;
+          e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, b00, b10, b01, b11);
+          mma16816<true>(acc[2 * i], a0, a1, a2, a3, b00, b01);
+          mma16816<true>(acc[2 * i + 1], a0, a1, a2, a3, b10, b11);
+        }
+      };
+      if constexpr (!EDGE) {
+        add(sw, pa[u][0], pa[u][1], pa[u][2], pa[u][3]);
+      } else {  // (as for 8 rows)
+        const int tA = min((n0 + g) / G, T - 1), tB = min((n0 + g + 8) / G, T - 1);
+#pragma unroll 1
+        for (int tq = min(n0 / G, T - 1); tq <= min((n0 + 15) / G, T - 1); ++tq) {
+          const uint32_t onA = tA == tq ? 0xFFFFFFFFu : 0u, onB = tB == tq ? 0xFFFFFFFFu : 0u;
+          add(sw & e2m1_token_mask(min(pg[u].nv, seen0 + tq - pg[u].pos0 + 1), t), pa[u][0] & onA,
+              pa[u][1] & onB, pa[u][2] & onA, pa[u][3] & onB);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void finish() {
+    if (mA == kUnset) mA = -INFINITY;
+    if (mB == kUnset) mB = -INFINITY;
+  }
+};
+
+// What a lane knows of one of the warp's units: its pages' tiles (-1: none, or not
+// to be read) and block scales.
+struct LaneUnit {
+  int tile[2];
+  float ks[2], vs[2];
+  bool bad;  // a page must not be read: its request gets no output
+};
+
+template <bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArgs a) {
+  using C = E2m1Cfg<WIDE>;
+  constexpr int D = 128, ST = C::ST;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  int32_t* pfx_s = reinterpret_cast<int32_t*>(smem + C::OFF_PFX);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
+  int* wsum_s = reinterpret_cast<int*>(smem + C::OFF_WSUM);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int B = a.B, Hkv = a.d.num_kv_heads, Hs = a.Hs, HG = a.HG;
+  // row blocks of a kv head, one a warp (WIDE: of 16 rows)
+  const int RBW = a.R8 / (WIDE ? 16 : 8), Hv = Hs * RBW;
+  if (Hs < 1 || RBW < 1 || (!WIDE && RBW != 1) || RBW * (WIDE ? 16 : 8) != a.R8 || a.R < 1 ||
+      a.R > a.R8 || Hs * HG != Hkv || kWarps % Hv != 0 || a.sub != kWarps / Hv ||
+      a.unit_tokens != 32 || (a.self_plan && B + 1 > kPfxCache)) {
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) set_error(a.d.ctl, KV_ERR_INTERNAL);  // host chose a bad configuration
+    return;
+  }
+  if (threadIdx.x < kWarps * ST) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  fence_mbar_init();
+  pdl_wait();
+  pdl_trigger();  // the combine's CTAs may wait resident in what this kernel leaves free
+  const bool cached = B + 1 <= kPfxCache;
+  if (a.self_plan) {
+    const bool refused = decode_plan_shared(a, pfx_s, wsum_s);
+    if (blockIdx.x == 0) decode_plan_store(a, pfx_s, refused);
+  } else if (cached) {
+    for (int i = threadIdx.x; i <= B; i += kThreads) pfx_s[i] = a.ws.pfx[i];
+  }
+  __syncthreads();  // the plan and the barriers are visible to every warp
+  const int32_t* pfx = cached ? pfx_s : a.ws.pfx;
+  const long long total = (long long)pfx[B] * HG;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long x_begin = (long long)blockIdx.x * per;
+  const int n_units = (int)(min(total, x_begin + per) - x_begin);  // of this CTA
+  if (n_units <= 0) return;
+  const Cursor start = cursor_at(pfx, B, HG, x_begin);
+
+  const int WPH = kWarps / Hv;                // warps per virtual head (kv head, row block)
+  const int vh = warp % Hv, lg = warp / Hv;
+  const int hw = vh / RBW, n0 = (vh - hw * RBW) * 16;  // kv head of the group, first query row
+  uint8_t* ring = smem + warp * (ST * kStage);
+  uint64_t* full = bars + warp * ST;
+  const uint64_t policy = l2_evict_first_policy();
+
+  // ---- this warp's units: i = 0, 1, .. are the CTA's lg + WPH i.  Lane l holds
+  // unit 32 b + l of batch b; page ids are loaded two batches ahead, scales one.
+  const int count = (n_units - lg + WPH - 1) / WPH;  // (<= 0: none)
+  Cursor lc = start;  // per-lane cursor, only moves forward
+  struct Ids {
+    int p[2], hg;  // page ids (-1: behind the length), head group (-1: no unit)
+  };
+  auto locate = [&](int i) {
+    Ids u{{-1, -1}, -1};
+    if (i >= count) return u;
+    const long long x = x_begin + lg + WPH * i;
+    while (x >= lc.seg_start + lc.np) cursor_next(lc, pfx, B, HG);
+    u.hg = lc.h;
+    const int j = 2 * (int)(x - lc.seg_start);
+    const long long at = (long long)lc.r * a.max_pages + j;
+    const int L = a.seq_lens[lc.r];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k == 0 || L > 16 * j + 16) {
+        const int p = a.page_table[at + k];
+        // the fused check: the tag is compared before the page is fetched
+        u.p[k] = p < 0 || p >= a.d.num_pages                                  ? -2
+                 : a.exp_tags == nullptr || a.d.tags[p] == a.exp_tags[at + k] ? p
+                                                                              : -3;
+      }
+    return u;
+  };
+  auto scales = [&](const Ids& id) {
+    LaneUnit u;
+    u.bad = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      u.tile[k] = -1;
+      u.ks[k] = u.vs[k] = 1.0f;
+      if (id.hg < 0) continue;
+      if (id.p[k] == -2) set_error(a.d.ctl, KV_ERR_BAD_PAGE_ID);
+      u.bad = u.bad || id.p[k] < -1;
+      if (id.p[k] < 0) continue;
+      u.tile[k] = id.p[k] * Hkv + id.hg * Hs + hw;  // (a cache of 2^31 tiles is 2 TB)
+      u.ks[k] = a.d.k_scale[u.tile[k]];
+      u.vs[k] = a.d.v_scale[u.tile[k]];
+    }
+    return u;
+  };
+  const Ids id0 = locate(lane), id1 = locate(32 + lane);
+  Ids ids = locate(64 + lane);
+  LaneUnit cur = scales(id0), nxt = scales(id1);
+  uint32_t bad_units = __ballot_sync(0xffffffffu, cur.bad);
+  int batch = 0;  // of cur
+  // Unit i's copies, into stage st: lane k issues K of page k, lane 2 + k V.
+  auto fetch = [&](int i, int st) {
+    if (i >= count) return;
+    const bool c = (i >> 5) == batch;
+    const int t0 = __shfl_sync(0xffffffffu, c ? cur.tile[0] : nxt.tile[0], i & 31);
+    const int t1 = __shfl_sync(0xffffffffu, c ? cur.tile[1] : nxt.tile[1], i & 31);
+    const int tile = lane & 1 ? t1 : t0;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&full[st], ((t0 >= 0) + (t1 >= 0)) * 2 * kE2m1Tile);
+    __syncwarp();
+    if (lane < 4 && tile >= 0)
+      bulk_g2s(ring + st * kStage + lane * kE2m1Tile,
+               static_cast<const uint8_t*>(lane < 2 ? a.d.k_cache : a.d.v_cache) +
+                   (long long)tile * kE2m1Tile,
+               kE2m1Tile, &full[st], policy);
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) fetch(i, i);
+
+  Cursor seg = start;
+  int done = 0;          // units of the CTA before this piece
+  int i = 0, st = 0;     // the warp's next unit and its stage
+  uint32_t phase = 0;
+  bool gone = false;     // a wait gave up: nothing more is waited for, fetched or computed
+  const int G = a.G, T = a.T, R = a.R;
+  const float ssl = a.sm_scale_log2;
+
+  while (done < n_units) {
+    const int u0 = (int)(x_begin + done - seg.seg_start);  // the piece's first unit in its segment
+    const int n_piece = min(seg.np - u0, n_units - done);
+    const int r = seg.r, h = seg.h * Hs + hw, L = a.seq_lens[r];
+    const int rel = done + n_piece - lg;
+    const int i_end = rel > 0 ? (rel + WPH - 1) / WPH : 0;
+    // units whose 32 positions every query token sees: below i_full
+    const int see = max(0, L - T + 1) / 32 + done - u0 - lg;
+    const int i_full = min(i_end, see > 0 ? (see + WPH - 1) / WPH : 0);
+    bool bad = false;
+
+    auto units = [&](auto& rows) {
+      auto unit = [&](auto edge) {
+        if (!gone) {
+          bool ok = mbar_try_wait(&full[st], phase);
+          if (!ok) ok = mbar_wait(&full[st], phase, abort_flag, a.d.ctl, wait_info(warp, 0, st));
+          gone = !__all_sync(0xffffffffu, ok);
+        }
+        E2m1Page pg[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          pg[k].k = ring + st * kStage + k * kE2m1Tile;
+          pg[k].v = pg[k].k + 2 * kE2m1Tile;
+          pg[k].ks = __shfl_sync(0xffffffffu, cur.ks[k], i & 31);
+          pg[k].vs = __shfl_sync(0xffffffffu, cur.vs[k], i & 31);
+          pg[k].pos0 = 32 * (lg + WPH * i - done + u0) + 16 * k;
+          pg[k].nv = min(16, L - pg[k].pos0);
+        }
+        if (!gone) {
+          if constexpr (decltype(edge)::value) {
+            // (a page behind the length was not fetched)
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+              if (k == 0 ? pg[0].nv > 0 : pg[1].nv > 0) {
+                const E2m1Page one[1] = {k == 0 ? pg[0] : pg[1]};
+                rows.template pages<1, true>(one);
+              }
+          } else if constexpr (WIDE && KV_E2M1_PAIR16 == 1) {
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+              const E2m1Page one[1] = {k == 0 ? pg[0] : pg[1]};
+              rows.template pages<1, false>(one);
+            }
+          } else {
+            rows.template pages<2, false>(pg);
+          }
+          __syncwarp();  // every lane has read its part of the stage
+          fetch(i + ST, st);
+        }
+        ++i;
+        if (++st == ST) {
+          st = 0;
+          phase ^= 1u;
+        }
+      };
+      while (i < i_end) {
+        if ((i >> 5) != batch) {
+          cur = nxt;
+          bad_units = __ballot_sync(0xffffffffu, cur.bad);
+          nxt = scales(ids);
+          ++batch;
+          ids = locate(32 * batch + 64 + lane);
+        }
+        // (a unit that must not be read may be computed on all the same: the
+        // request gets no output)
+        const int stop = min(i_end, 32 * batch + 32);
+        bad = bad || (bad_units >> (i & 31)) << (31 - (stop - 1 - i)) != 0;
+        const int full_stop = min(stop, i_full);
+        while (i < full_stop) unit(FalseType{});
+        while (i < stop) unit(TrueType{});
+      }
+    };
+
+    // this warp's partial of the piece
+    const long long prow =
+        ((((long long)r * HG + seg.h + blockIdx.x) * a.sub + lg) * Hs + hw) * a.R8 + n0;
+    float* ml = a.ws.ml_part + prow * 2;
+    float* op = a.ws.o_part + prow * D;
+    if constexpr (WIDE) {
+      // ---- Q as A operands {a0, a1, a2, a3} of k-step j = rows g, g + 8 x dims
+      // d(j) + 0, 1 and d(j) + 2, 3 with d(j) = 16t + 4j (j < 4), 64 + 16t + 4 (j - 4)
+      uint32_t* qs = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + warp * 4096);
+      float qsc[2];  // score scales of rows g and g + 8, with the row's 2^-e
+      {
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const int row = n0 + g + 8 * hr;
+          const bool live = row < R;
+          const int tq = live ? row / G : 0, hq = live ? h * G + row % G : 0;
+          const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + 16 * t;
+          uint4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * (u & 1) + 64 * (u >> 1))
+                        : make_uint4(0, 0, 0, 0);
+          uint32_t mb = max(max(bf16_absbits_max8(v[0]), bf16_absbits_max8(v[1])),
+                            max(bf16_absbits_max8(v[2]), bf16_absbits_max8(v[3])));
+          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+          const int e = q_row_exp(mb);
+          const float pw = pow2f(e);
+          qsc[hr] = ssl * pow2f(-e);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            qa[2 * u][hr] = bf16x2_to_f16x2_scaled(v[u].x, pw);
+            qa[2 * u][2 + hr] = bf16x2_to_f16x2_scaled(v[u].y, pw);
+            qa[2 * u + 1][hr] = bf16x2_to_f16x2_scaled(v[u].z, pw);
+            qa[2 * u + 1][2 + hr] = bf16x2_to_f16x2_scaled(v[u].w, pw);
+          }
+        }
+        __syncwarp();  // the last piece's reads
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(qs + (j * 32 + lane) * 4) =
+              make_uint4(qa[j][0], qa[j][1], qa[j][2], qa[j][3]);
+        __syncwarp();
+      }
+      float mA = kUnset, mB = kUnset, lA = 0.0f, lB = 0.0f;
+      float acc[16][4];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
+      E2m1Rows16 rows{mA, mB, lA, lB, acc, qs, qsc[0], qsc[1], n0, G, T, L - T};
+      units(rows);
+      rows.finish();
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        lA += __shfl_xor_sync(0xffffffffu, lA, o);
+        lB += __shfl_xor_sync(0xffffffffu, lB, o);
+      }
+      if (t == 0) {
+        *reinterpret_cast<float2*>(ml + 2 * g) = make_float2(mA, bad ? -1.0f : lA);
+        *reinterpret_cast<float2*>(ml + 2 * (g + 8)) = make_float2(mB, bad ? -1.0f : lB);
+      }
+      // column c of tile k is dim 16 c + k: a lane's 32 dims of a row are contiguous
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+          *reinterpret_cast<float4*>(op + (g + 8 * (e >> 1)) * D + 32 * t + 16 * (e & 1) + k) =
+              make_float4(acc[k][e], acc[k + 1][e], acc[k + 2][e], acc[k + 3][e]);
+    } else {
+      // ---- query fragments of row g (zero for padding rows): k-step j has dims
+      // 16 (t + 4 (j / 4)) + 4 (j % 4) + 0 .. 3
+      uint32_t qf[8][2];
+      float qsc0, qsc1;  // score scales of rows 2t, 2t + 1, with the row's 2^-e
+      {
+        const bool live = g < R;
+        const int tq = live ? g / G : 0, hq = live ? h * G + g % G : 0;
+        const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + 16 * t;
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * (u & 1) + 64 * (u >> 1))
+                      : make_uint4(0, 0, 0, 0);
+        uint32_t mb = max(max(bf16_absbits_max8(v[0]), bf16_absbits_max8(v[1])),
+                          max(bf16_absbits_max8(v[2]), bf16_absbits_max8(v[3])));
+        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+        const int e = q_row_exp(mb);
+        const float pw = pow2f(e);
+        // rows 2t and 2t + 1 are held by the lanes g = 2t and 2t + 1
+        qsc0 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t));
+        qsc1 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t + 4));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          qf[2 * u][0] = bf16x2_to_f16x2_scaled(v[u].x, pw);
+          qf[2 * u][1] = bf16x2_to_f16x2_scaled(v[u].y, pw);
+          qf[2 * u + 1][0] = bf16x2_to_f16x2_scaled(v[u].z, pw);
+          qf[2 * u + 1][1] = bf16x2_to_f16x2_scaled(v[u].w, pw);
+        }
+      }
+      float m0 = kUnset, m1 = kUnset, l0 = 0.0f, l1 = 0.0f;
+      float acc[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
+      E2m1Rows8 rows{m0, m1, l0, l1, acc, qf, qsc0, qsc1, G, T, L - T};
+      units(rows);
+      rows.finish();
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+      }
+      if (g == 0)
+        *reinterpret_cast<float4*>(ml + 4 * t) =
+            make_float4(m0, bad ? -1.0f : l0, m1, bad ? -1.0f : l1);
+      // rows g, g + 8 of tile k are dims 16g + 2k, + 1: 16 contiguous dims of a row
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < 8; k += 2)
+          *reinterpret_cast<float4*>(op + (2 * t + e) * D + 16 * g + 2 * k) =
+              make_float4(acc[k][e], acc[k][e + 2], acc[k + 1][e], acc[k + 1][e + 2]);
+    }
+    done += n_piece;
+    if (u0 + n_piece == seg.np) cursor_next(seg, pfx, B, HG);
+  }
+  // After a wait gave up, copies already issued may still be landing: wait for
+  // them (bounded) before this CTA's shared memory goes away.
+  if (*abort_flag && lane == 0) {
+    for (int k = 0; k < 2 * ST; ++k) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try_wait(&full[k % ST], k < ST ? 0u : 1u) && global_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int e2m1_split_warps() { return kWarps; }
+
+int e2m1_split_ctas_per_sm(int kind) {
+  static int cache[2] = {-1, -1};
+  const int wide = kind == 6;
+  if (cache[wide] >= 0) return cache[wide];
+  const auto kernel = wide ? e2m1_split_kernel<true> : e2m1_split_kernel<false>;
+  const int smem = wide ? E2m1Cfg<true>::SMEM : E2m1Cfg<false>::SMEM;
+  int n = 0;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem);
+  if (e != cudaSuccess || n <= 0) return 0;
+  cache[wide] = n;
+  return n;
+}
+
+cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
+  const cudaError_t e =
+      kind == 6 ? launch_pdl(e2m1_split_kernel<true>, dim3(a.grid), dim3(kThreads),
+                             E2m1Cfg<true>::SMEM, s, a)
+                : launch_pdl(e2m1_split_kernel<false>, dim3(a.grid), dim3(kThreads),
+                             E2m1Cfg<false>::SMEM, s, a);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace kvfp8

@@ -38,7 +38,7 @@
 
 #include "common.cuh"
 #include "decode_plan.cuh"
-#include "e2m1.cuh"
+#include "gqa_split.cuh"
 #include "internal.h"
 
 namespace kvfp8 {
@@ -52,192 +52,6 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(DecodeArgs a)
   pdl_wait();
   pdl_trigger();
   decode_plan_block(a);
-}
-
-// ------------------------------------------------- segment cursor
-
-// Walks segments (request r, head group h) of the flattened unit sequence;
-// `groups` is the number of head groups per request.  pfx may live in shared
-// or global memory.
-struct Cursor {
-  int r, h, np;
-  long long seg_start;
-};
-
-__device__ __forceinline__ Cursor cursor_at(const int32_t* pfx, int B, int groups, long long x) {
-  // last r with pfx[r] <= x / groups; that request has pages (pfx[r+1] > x/groups)
-  const long long v = x / groups;
-  int lo = 0, hi = B;  // invariant: pfx[lo] <= v < pfx[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pfx[mid] <= v)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  Cursor c;
-  c.r = lo;
-  c.np = pfx[lo + 1] - pfx[lo];
-  c.h = (int)((x - (long long)groups * pfx[lo]) / c.np);
-  c.seg_start = (long long)groups * pfx[lo] + (long long)c.h * c.np;
-  return c;
-}
-
-__device__ __forceinline__ void cursor_next(Cursor& c, const int32_t* pfx, int B, int groups) {
-  if (++c.h == groups) {
-    c.h = 0;
-    do {
-      ++c.r;
-    } while (c.r < B && pfx[c.r + 1] == pfx[c.r]);
-    if (c.r < B) c.np = pfx[c.r + 1] - pfx[c.r];
-  }
-  if (c.r < B) {
-    c.seg_start = (long long)groups * pfx[c.r] + (long long)c.h * c.np;
-  } else {  // past the last request (cannot happen inside a CTA range): end every loop
-    c.seg_start = (long long)groups * pfx[B];
-    c.np = 1;
-  }
-}
-
-// ------------------------------------------------- tensor-core helpers
-
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t c;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-  return c;
-}
-// Eight e2m1 codes -> four f16x2 words, one a byte (low half: low nibble).
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c,
-                                              uint32_t& d) {
-  asm("{\n .reg .b8 x, y, z, t;\n mov.b32 {x, y, z, t}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, x;\n cvt.rn.f16x2.e2m1x2 %1, y;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, z;\n cvt.rn.f16x2.e2m1x2 %3, t;\n}\n"
-      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-      : "r"(w));
-}
-// The same, bytes 0 and 1 times slo, 2 and 3 times shi (exact: an e2m1 code
-// times an e4m3 scale has six significant bits).
-__device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t slo, uint32_t shi, uint32_t& a,
-                                              uint32_t& b, uint32_t& c, uint32_t& d) {
-  e2m1x8_to_f16(w, a, b, c, d);
-  a = mul_f16x2(a, slo);
-  b = mul_f16x2(b, slo);
-  c = mul_f16x2(c, shi);
-  d = mul_f16x2(d, shi);
-}
-// the low or the high half of w in both halves
-__device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
-  return __byte_perm(w, w, hi ? 0x3232 : 0x1010);
-}
-// Scale bytes of the tokens 2t, 2t + 1, 2t + 8, 2t + 9 that lie below nv (the
-// bytes behind a request's length are stale and may be NaN).
-__device__ __forceinline__ uint32_t e2m1_token_mask(int nv, int t) {
-  const int a = min(max(nv - 2 * t, 0), 2), b = min(max(nv - 8 - 2 * t, 0), 2);
-  return ((1u << (8 * a)) - 1u) | (((1u << (8 * b)) - 1u) << 16);
-}
-// The 8 x 8 f16 matrix that the warp holds two to a lane (lane 4 r + c: row r,
-// columns 2c and 2c + 1), transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// Four e4m3 codes (bytes 0..3 of w) -> two f16x2 words, lo = (b0, b1) and
-// hi = (b2, b3); exact (every e4m3 value is an f16 value).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n"
-      " cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-// 2^x on the special-function unit (flushes denormal results to zero, which
-// only drops softmax weights below 2^-126).
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The e4m3 paths multiply the bf16 query in f16.  Each query row is first
-// scaled by an exact power of two 2^e that puts its largest magnitude in
-// [2^15, 2^16): inside f16's range (below 65504) with all of its bits, and
-// small elements stay clear of f16's subnormals.  The row's scores are then
-// 2^e times the true ones and its score scale takes 2^-e.  For a row whose
-// elements are all normal f16 values either way, scores are bit-identical to
-// the unscaled ones (a power-of-two factor commutes with rounding).
-// Largest magnitude of 8 bf16 values as a bit pattern with the sign cleared
-// (bit-pattern order is magnitude order for finite values).
-__device__ __forceinline__ uint32_t bf16_absbits_max8(const uint4& v) {
-  const uint32_t a = max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu);
-  const uint32_t b = max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu);
-  const uint32_t c = max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu);
-  const uint32_t d = max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu);
-  return max(max(a, b), max(c, d));
-}
-// e for a row whose largest magnitude has bf16 bits mb: 15 - floor(log2),
-// within [-112, 112] so that 2^e and 2^-e times the score scale stay normal
-// fp32 numbers (all-zero or subnormal rows take 112).
-__device__ __forceinline__ int q_row_exp(uint32_t mb) {
-  const int E = (int)(mb >> 7);
-  return E == 0 ? 112 : min(112, max(-112, 142 - E));
-}
-__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t w, float pw) {
-  const float lo = __uint_as_float(w << 16) * pw, hi = __uint_as_float(w & 0xFFFF0000u) * pw;
-  return f32x2_to_f16x2(lo, hi);
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (F16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  }
-}
-
-__device__ __forceinline__ uint4 lds128(const void* p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(smem_u32(p)));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(const void* p) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_u32(p)));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(const void* p) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t w_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // ------------------------------------------------- split kernel
@@ -258,33 +72,26 @@ __device__ __forceinline__ uint32_t w_of(const uint4& v, int i) {
 #ifndef KV_GQA_BF16_CONSUMERS
 #define KV_GQA_BF16_CONSUMERS 8
 #endif
-#ifndef KV_GQA_E2M1_CONSUMERS
-#define KV_GQA_E2M1_CONSUMERS 12
-#endif
 #ifndef KV_GQA_RING_KB
 #define KV_GQA_RING_KB 160
 #endif
 
 constexpr int kMaxStages = 40;
 
-// FMT: the pool's kv_dtype
-template <int FMT>
+template <bool FP8>
 struct GqaCfg {
-  static constexpr bool FP8 = FMT == KV_DTYPE_E4M3, FP4 = FMT == KV_DTYPE_E2M1;
   static constexpr int P = 16;                      // tokens per page
   static constexpr int D = 128;                     // head dim (K and V)
-  // bytes of one head's K or V tile
-  static constexpr int TILE = FP4 ? kE2m1Tile : P * D * (FP8 ? 1 : 2);
+  static constexpr int ES = FP8 ? 1 : 2;            // cache element bytes
+  static constexpr int TILE = P * D * ES;           // bytes of one head's K or V tile
   static constexpr int RING = KV_GQA_RING_KB * 1024;
   // consumer warps: e4m3 pages carry half the bytes of bf16 ones, so each
   // byte needs twice the consumer work; measured best at 12 (e4m3) and 8 (bf16)
-  static constexpr int CONSUMERS =
-      FP4 ? KV_GQA_E2M1_CONSUMERS : FP8 ? KV_GQA_FP8_CONSUMERS : KV_GQA_BF16_CONSUMERS;
+  static constexpr int CONSUMERS = FP8 ? KV_GQA_FP8_CONSUMERS : KV_GQA_BF16_CONSUMERS;
   static constexpr int THREADS = (CONSUMERS + 1) * 32;
   static constexpr int R8 = 8;                      // query rows per kv head (padded)
   static constexpr int PFX_CACHE = 1024;            // pfx entries cached in smem
-  // per-warp P transpose (4-bit: by matrix transposes in registers)
-  static constexpr int PBUF = FP4 ? 0 : FP8 ? R8 * P * 2 : R8 * P * 4;
+  static constexpr int PBUF = FP8 ? R8 * P * 2 : R8 * P * 4;  // per-warp P transpose
   // shared memory carve-up (byte offsets)
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_MERGE_O = OFF_RING + RING;                         // [W][R8][D] f32
@@ -314,65 +121,11 @@ struct StageMeta {
 };
 static_assert(sizeof(StageMeta) == 80, "StageMeta layout");
 
-// End of a piece: merges the online-softmax states of the WPH warps that
-// share each of the Hv virtual heads (8 rows each) into the piece's partial.
-// merge_ml[(w * 8 + nw) * 2 + {0, 1}] holds warp w's running max and sum of
-// row nw, merge_o[(w * 8 + nw) * 128 + dd] its unnormalised output.  Pass 1,
-// one thread per row: the row's max M over the warps, each warp's weight
-// 2^(m_w - M) (written over m_w) and the weighted sum, stored with M (a
-// piece that met a page it must not read stores the sum -1 instead).  Pass
-// 2, every consumer thread: the weighted outputs, four dims at a time.
-// row_of(v, nw) is the partial row of virtual head v's row nw.  Starts and
-// ends with the consumer warps synchronised.
-template <class C, class RowOf>
-__device__ __forceinline__ void merge_piece(float* merge_o, float* merge_ml, int Hv, int WPH,
-                                            const DecodeArgs& a, RowOf row_of,
-                                            volatile int* piece_bad, bool reset_bad) {
-  constexpr int R8 = C::R8, D = C::D, NT = C::CONSUMERS * 32;
-  static_assert(R8 == 8 && D == 128, "index shifts");
-  const int tid = threadIdx.x;
-  named_bar_sync(1, NT);  // every warp's state is in the merge buffers
-  if (tid < Hv * R8) {
-    const int v = tid >> 3, nw = tid & 7;
-    float M = -INFINITY;
-    for (int q = 0; q < WPH; ++q) M = fmaxf(M, merge_ml[((q * Hv + v) * R8 + nw) * 2]);
-    float lsum = 0.0f;
-    for (int q = 0; q < WPH; ++q) {
-      float* ml = merge_ml + ((q * Hv + v) * R8 + nw) * 2;
-      const float w = (ml[0] == -INFINITY) ? 0.0f : exp2f(ml[0] - M);
-      lsum += ml[1] * w;
-      ml[0] = w;
-    }
-    const long long row = row_of(v, nw);
-    a.ws.ml_part[row * 2 + 0] = M;
-    a.ws.ml_part[row * 2 + 1] = *piece_bad ? -1.0f : lsum;
-  }
-  named_bar_sync(1, NT);
-  if (reset_bad && tid == 0) *piece_bad = 0;
-  for (int e = tid; e < Hv * R8 * (D / 4); e += NT) {
-    const int d4 = e & 31, rr = e >> 5, v = rr >> 3, nw = rr & 7;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int q = 0; q < WPH; ++q) {
-      const int w = (q * Hv + v) * R8 + nw;
-      const float wt = merge_ml[w * 2];
-      const float4 x = *reinterpret_cast<const float4*>(merge_o + w * D + 4 * d4);
-      o.x = fmaf(wt, x.x, o.x);
-      o.y = fmaf(wt, x.y, o.y);
-      o.z = fmaf(wt, x.z, o.z);
-      o.w = fmaf(wt, x.w, o.w);
-    }
-    *reinterpret_cast<float4*>(a.ws.o_part + row_of(v, nw) * D + 4 * d4) = o;
-  }
-  named_bar_sync(1, NT);
-}
-
 // WIDE: a consumer warp takes 16 query rows of its kv head instead of 8 (see
 // the wide consumer below); the producer and the ring are the same.
-template <int FMT, bool WIDE>
+template <bool FP8, bool WIDE>
 __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
-  using C = GqaCfg<FMT>;
-  constexpr bool FP4 = C::FP4;
-  constexpr bool FP8 = C::FP8 || FP4;  // block scales, and products in f16
+  using C = GqaCfg<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + C::OFF_RING;
   float* merge_o = reinterpret_cast<float*>(smem + C::OFF_MERGE_O);
@@ -403,7 +156,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
                             : (RB <= 4 && (a.R + C::R8 - 1) / C::R8 == RB);
   // (not in the 16-row e4m3 kernel: at its 128-register cap the plan code
   // made it spill)
-  constexpr bool kCanSelfPlan = !(FMT == KV_DTYPE_E4M3 && WIDE);
+  constexpr bool kCanSelfPlan = !(FP8 && WIDE);
   if (Hs < 1 || RB < 1 || !rows_ok || RB * C::R8 != a.R8 ||
       C::CONSUMERS % Hv != 0 || S < 2 || S > kMaxStages || S % (C::CONSUMERS / Hv) != 0 ||
       stage_bytes * S > C::RING ||
@@ -639,12 +392,11 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           const int row = n0 + g + 8 * hr;
           const bool live = row < R;
           const int tq = live ? row / G : 0, hq = live ? h * G + row % G : 0;
-          const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + (FP4 ? 16 : 32) * t;
+          const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + 32 * t;
           uint4 v[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u)  // dims 32t + 8u .. +7: k-steps 2u and 2u+1
-            v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * u + (FP4 && u >= 2 ? 48 : 0))
-                        : make_uint4(0, 0, 0, 0);
+            v[u] = live ? *reinterpret_cast<const uint4*>(qrow + 8 * u) : make_uint4(0, 0, 0, 0);
           float pw = 1.0f;
           if constexpr (FP8) {  // the row's 128 dims are spread over the 4 threads t
             uint32_t mb = max(max(bf16_absbits_max8(v[0]), bf16_absbits_max8(v[1])),
@@ -701,26 +453,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           const uint8_t* Vt = ring + (size_t)stage * stage_bytes + (Hs + hw) * C::TILE;
           // ---------------- S = Q K^T: N tile nt, column g = token tok0 + 2 nt
           float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          if constexpr (FP4) {
-            // column g of tile nt is token g + 8 nt; k-steps 0 .. 3 are dims 16t + 4j ..,
-            // 4 .. 7 dims 64 + 16t + 4 (j - 4) ..
-            const uint4 k0 = lds128(Kt + 64 * g + 16 * t), k1 = lds128(Kt + 64 * (g + 8) + 16 * t);
-            uint32_t sg, sh;
-            e4m3x4_to_f16(lds32(Kt + kE2m1Scales + 4 * lane), sg, sh);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-              const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
-              uint32_t x[4], y[4];
-              e2m1x8_scaled(w_of(k0, w), s0, s0, x[0], x[1], x[2], x[3]);
-              e2m1x8_scaled(w_of(k1, w), s1, s1, y[0], y[1], y[2], y[3]);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint4 qa = lds128(qs + ((2 * w + u) * 32 + lane) * 4);
-                mma16816<true>(s[0], qa.x, qa.y, qa.z, qa.w, x[2 * u], x[2 * u + 1]);
-                mma16816<true>(s[1], qa.x, qa.y, qa.z, qa.w, y[2 * u], y[2 * u + 1]);
-              }
-            }
-          } else if constexpr (FP8) {
+          if constexpr (FP8) {
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) {  // dims 32t + 16 kh .. +15: k-steps 4kh .. 4kh+3
               const uint4 k0 = lds128(Kt + tok0 * 128 + 32 * t + 16 * kh);
@@ -752,10 +485,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
               }
             }
           }
-          // s[nt][e]: row g (e < 2) or g+8, token tok_of(nt, e); log2 domain
-          auto tok_of = [&](int nt, int e) {
-            return FP4 ? 8 * nt + 2 * t + (e & 1) : 4 * t + 2 * nt + (e & 1);
-          };
+          // s[nt][e]: row g (e < 2) or g+8, token 4t + 2 nt + (e & 1); log2 domain
           const float ksc = FP8 ? mt.ks[hw] : 1.0f;
           const float scA = ksc * qscA, scB = ksc * qscB;
 #pragma unroll
@@ -770,7 +500,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int tk = tok_of(nt, e);
+                const int tk = 4 * t + 2 * nt + (e & 1);
                 const int lim = e < 2 ? limA : limB;
                 s[nt][e] = (tk < nv && mt.pos0 + tk <= lim) ? s[nt][e] : -INFINITY;
               }
@@ -814,22 +544,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
           // ---------------- O += P V: P from registers, V tile dim-major;
           // tokens beyond the length are zeroed in V (stale bytes could be NaN)
           const int keep = min(max(nv - 4 * t, 0), 4);
-          if constexpr (FP4) {
-            const uint32_t pa0 = f32x2_to_f16x2(p[0][0], p[0][1]);
-            const uint32_t pa1 = f32x2_to_f16x2(p[0][2], p[0][3]);
-            const uint32_t pa2 = f32x2_to_f16x2(p[1][0], p[1][1]);
-            const uint32_t pa3 = f32x2_to_f16x2(p[1][2], p[1][3]);
-            uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-            e4m3x4_to_f16(lds32(Vt + kE2m1Scales + 4 * lane) & e2m1_token_mask(nv, t), slo, shi);
-            const uint4 v0 = lds128(Vt + 16 * lane), v1 = lds128(Vt + 512 + 16 * lane);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
-              uint32_t b00, b10, b01, b11;
-              e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, b00, b10, b01, b11);
-              mma16816<true>(acc[2 * i], pa0, pa1, pa2, pa3, b00, b01);
-              mma16816<true>(acc[2 * i + 1], pa0, pa1, pa2, pa3, b10, b11);
-            }
-          } else if constexpr (FP8) {
+          if constexpr (FP8) {
             const uint32_t pa0 = f32x2_to_f16x2(p[0][0], p[0][1]);
             const uint32_t pa1 = f32x2_to_f16x2(p[0][2], p[0][3]);
             const uint32_t pa2 = f32x2_to_f16x2(p[1][0], p[1][1]);
@@ -885,20 +600,10 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         float* mo = merge_o + warp * C::R8 * D + g * D;
-        if constexpr (FP4) {  // column c of tile i is dim 16 c + i
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            *reinterpret_cast<float2*>(mo + 32 * t + i) =
-                half ? make_float2(acc[i][2], acc[i + 1][2]) : make_float2(acc[i][0], acc[i + 1][0]);
-            *reinterpret_cast<float2*>(mo + 32 * t + 16 + i) =
-                half ? make_float2(acc[i][3], acc[i + 1][3]) : make_float2(acc[i][1], acc[i + 1][1]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<float2*>(mo + 8 * i + 2 * t) =
-                half ? make_float2(acc[i][2], acc[i][3]) : make_float2(acc[i][0], acc[i][1]);
-        }
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float2*>(mo + 8 * i + 2 * t) =
+              half ? make_float2(acc[i][2], acc[i][3]) : make_float2(acc[i][0], acc[i][1]);
         if (t == 0) {
           float* ml = merge_ml + (warp * C::R8 + g) * 2;
           ml[0] = half ? mB : mA;
@@ -1026,21 +731,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
         const uint8_t* Vt = ring + (size_t)stage * stage_bytes + (Hs + hw) * C::TILE;
         // ---------------- S^T = K Q^T  (two accumulator chains for ILP)
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (FP4) {
-          // row g (and g+8): dims 16t..16t+15 and 64+16t..64+16t+15, as for e4m3
-          const uint4 kg = lds128(Kt + 64 * g + 16 * t), kh = lds128(Kt + 64 * (g + 8) + 16 * t);
-          uint32_t sg, sh;
-          e4m3x4_to_f16(lds32(Kt + kE2m1Scales + 4 * lane), sg, sh);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-            const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
-            uint32_t x[4], y[4];
-            e2m1x8_scaled(w_of(kg, w), s0, s0, x[0], x[1], x[2], x[3]);
-            e2m1x8_scaled(w_of(kh, w), s1, s1, y[0], y[1], y[2], y[3]);
-            mma16816<true>(sa, x[0], y[0], x[1], y[1], qf[2 * w][0], qf[2 * w][1]);
-            mma16816<true>(sb, x[2], y[2], x[3], y[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
-          }
-        } else if constexpr (FP8) {
+        if constexpr (FP8) {
           // row g (and g+8): dims 16t..16t+15 and 64+16t..64+16t+15
           const uint4 kA = lds128(Kt + g * 128 + 16 * t);
           const uint4 kB = lds128(Kt + g * 128 + 64 + 16 * t);
@@ -1120,20 +811,7 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
         // ---------------- P^T to the B-fragment layout via shared memory;
         // tokens beyond the request length are zeroed in V (stale cache bytes
         // could be NaN patterns; 0 * NaN would poison the sum)
-        if constexpr (FP4) {
-          // row g's weights of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-          const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p0, p1));
-          const uint32_t b1 = transpose8x8(f32x2_to_f16x2(p2, p3));
-          uint32_t slo, shi;  // scales of group g's same tokens
-          e4m3x4_to_f16(lds32(Vt + kE2m1Scales + 4 * lane) & e2m1_token_mask(nv, t), slo, shi);
-          const uint4 v0 = lds128(Vt + 16 * lane), v1 = lds128(Vt + 512 + 16 * lane);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
-            uint32_t a0, a1, a2, a3;
-            e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, a0, a1, a2, a3);
-            mma16816<true>(acc[i], a0, a1, a2, a3, b0, b1);
-          }
-        } else if constexpr (FP8) {
+        if constexpr (FP8) {
           __half* pb = reinterpret_cast<__half*>(pbuf);  // [8 rows][16 tokens]
           pb[(2 * t) * 16 + g] = __float2half_rn(p0);
           pb[(2 * t + 1) * 16 + g] = __float2half_rn(p1);
@@ -1212,13 +890,6 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
     float* mo = merge_o + warp * C::R8 * D;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (FP4) {
-        *reinterpret_cast<float2*>(mo + (2 * t) * D + 16 * g + 2 * i) =
-            make_float2(acc[i][0], acc[i][2]);
-        *reinterpret_cast<float2*>(mo + (2 * t + 1) * D + 16 * g + 2 * i) =
-            make_float2(acc[i][1], acc[i][3]);
-        continue;
-      }
       mo[(2 * t) * D + 16 * i + g] = acc[i][0];
       mo[(2 * t + 1) * D + 16 * i + g] = acc[i][1];
       mo[(2 * t) * D + 16 * i + g + 8] = acc[i][2];
@@ -1251,16 +922,20 @@ __device__ __forceinline__ void gqa_split_body(const DecodeArgs& a) {
   }
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(GqaCfg<FMT>::THREADS, 1)
+template <bool FP8>
+__global__ void __launch_bounds__(GqaCfg<FP8>::THREADS, 1)
     gqa_split_kernel(const DecodeArgs a) {
-  gqa_split_body<FMT, false>(a);
+  gqa_split_body<FP8, false>(a);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(GqaCfg<FMT>::THREADS, 1)
+__global__ void __launch_bounds__(GqaCfg<true>::THREADS, 1)
     gqa_split_wide_kernel(const DecodeArgs a) {
-  gqa_split_body<FMT, true>(a);
+  gqa_split_body<true, true>(a);
+}
+
+__global__ void __launch_bounds__(GqaCfg<false>::THREADS, 1)
+    gqa_split_wide_bf16_kernel(const DecodeArgs a) {
+  gqa_split_body<false, true>(a);
 }
 
 // ------------------------------------------------- combine
@@ -1325,9 +1000,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
       const long long per = (total + a.grid - 1) / a.grid;
       const long long start = (long long)HG * pfx_r + (long long)hg * np;
       const int c0 = (int)(start / per), c1 = (int)((start + np - 1) / per);
-      const long long slot0 = seg + c0;
+      const long long slot0 = (seg + c0) * a.sub;
       const int R8 = a.R8;
-      // partial row of this warp's piece jj (pieces c = sub + S jj)
+      // partial row of this warp's partial jj (partials sub + S jj of the segment)
       auto row_of = [&](int jj) -> long long {
         return ((slot0 + sub + (long long)S * jj) * Hs + hw) * R8 + nl;
       };
@@ -1354,7 +1029,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
       // already loading; the chunk's max and weights come from warp
       // reductions, then the weighted outputs are summed with independent
       // loads (no chain through a running max)
-      const int cnt = (c1 - c0 + 1 - sub + S - 1) / S;
+      const int cnt = ((c1 - c0 + 1) * a.sub - sub + S - 1) / S;
       for (int j0 = 0; j0 < cnt; j0 += 32) {
         const int nj = min(32, cnt - j0);
         float4 o[kU][NG];
@@ -1464,54 +1139,47 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
 // ------------------------------------------------- host side
 
 // kinds: 0 = e4m3 (8-row consumers), 1 = bf16, 3 = e4m3 with 16-row consumers,
-// 4 = bf16 with 16-row consumers, 5 / 6 = 4-bit with 8- / 16-row consumers
-namespace {
-
-struct GqaKind {
-  void (*kernel)(DecodeArgs);
-  int threads, smem, ring, consumers, tile;
-  bool self_plans;
-};
-template <int FMT>
-constexpr GqaKind gqa_kind_of(bool wide, bool self_plans) {
-  using C = GqaCfg<FMT>;
-  return {wide ? gqa_split_wide_kernel<FMT> : gqa_split_kernel<FMT>, C::THREADS, C::SMEM, C::RING,
-          C::CONSUMERS, C::TILE, self_plans};
+// 4 = bf16 with 16-row consumers
+int gqa_ring_bytes(int kind) {
+  return (kind == 1 || kind == 4) ? GqaCfg<false>::RING : GqaCfg<true>::RING;
 }
-const GqaKind& gqa_kind(int kind) {
-  static const GqaKind kinds[7] = {gqa_kind_of<KV_DTYPE_E4M3>(false, true),
-                                   gqa_kind_of<KV_DTYPE_BF16>(false, true),
-                                   {},
-                                   gqa_kind_of<KV_DTYPE_E4M3>(true, false),
-                                   gqa_kind_of<KV_DTYPE_BF16>(true, true),
-                                   gqa_kind_of<KV_DTYPE_E2M1>(false, true),
-                                   gqa_kind_of<KV_DTYPE_E2M1>(true, true)};
-  return kinds[kind];
-}
-
-}  // namespace
-
-int gqa_ring_bytes(int kind) { return gqa_kind(kind).ring; }
-int gqa_tile_bytes(int kind) { return gqa_kind(kind).tile; }
 int gqa_max_stages() { return kMaxStages; }
-bool gqa_kind_self_plans(int kind) { return gqa_kind(kind).self_plans; }
+bool gqa_kind_self_plans(int kind) { return kind == 0 || kind == 1 || kind == 4; }
 int gqa_self_plan_max_batch() {
-  static_assert(GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE == GqaCfg<KV_DTYPE_BF16>::PFX_CACHE &&
-                    GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE == GqaCfg<KV_DTYPE_E2M1>::PFX_CACHE,
-                "one prefix cache size");
-  return GqaCfg<KV_DTYPE_E4M3>::PFX_CACHE - 1;
+  static_assert(GqaCfg<true>::PFX_CACHE == GqaCfg<false>::PFX_CACHE, "one prefix cache size");
+  return GqaCfg<true>::PFX_CACHE - 1;
 }
-int gqa_consumer_warps(int kind) { return gqa_kind(kind).consumers; }
+int gqa_consumer_warps(int kind) {
+  return (kind == 1 || kind == 4) ? GqaCfg<false>::CONSUMERS : GqaCfg<true>::CONSUMERS;
+}
 
 int gqa_split_ctas_per_sm(int kind) {
-  static int cache[7] = {-1, -1, -1, -1, -1, -1, -1};
-  if (kind < 0 || kind > 6 || kind == 2) return 0;
+  static int cache[5] = {-1, -1, -1, -1, -1};
+  if (kind < 0 || kind > 4 || kind == 2) return 0;
   if (cache[kind] >= 0) return cache[kind];
-  const GqaKind& k = gqa_kind(kind);
   int n = 0;
-  cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-  const cudaError_t e =
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k.kernel, k.threads, k.smem);
+  cudaError_t e;
+  if (kind == 4) {
+    cudaFuncSetAttribute(gqa_split_wide_bf16_kernel,
+                         cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<false>::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_bf16_kernel,
+                                                      GqaCfg<false>::THREADS, GqaCfg<false>::SMEM);
+  } else if (kind == 3) {
+    cudaFuncSetAttribute(gqa_split_wide_kernel,
+                         cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<true>::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_kernel,
+                                                      GqaCfg<true>::THREADS, GqaCfg<true>::SMEM);
+  } else if (kind == 0) {
+    cudaFuncSetAttribute(gqa_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         GqaCfg<true>::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_kernel<true>,
+                                                      GqaCfg<true>::THREADS, GqaCfg<true>::SMEM);
+  } else {
+    cudaFuncSetAttribute(gqa_split_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         GqaCfg<false>::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_kernel<false>,
+                                                      GqaCfg<false>::THREADS, GqaCfg<false>::SMEM);
+  }
   if (e != cudaSuccess || n <= 0) return 0;
   cache[kind] = n;
   return n;
@@ -1524,8 +1192,15 @@ cudaError_t launch_decode_plan(const DecodeArgs& a, cudaStream_t s, int* launche
 }
 
 cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
-  const GqaKind& k = gqa_kind(kind);
-  const cudaError_t e = launch_pdl(k.kernel, dim3(a.grid), dim3(k.threads), k.smem, s, a);
+  const cudaError_t e =
+      kind == 4   ? launch_pdl(gqa_split_wide_bf16_kernel, dim3(a.grid),
+                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a)
+      : kind == 3 ? launch_pdl(gqa_split_wide_kernel, dim3(a.grid),
+                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
+      : kind == 0 ? launch_pdl(gqa_split_kernel<true>, dim3(a.grid),
+                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
+                  : launch_pdl(gqa_split_kernel<false>, dim3(a.grid),
+                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -1535,7 +1210,7 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* laun
   if (items <= 0) return cudaSuccess;
   // partials of one segment: about 1 + grid / segments; give each merging
   // warp at least two of them
-  const double pieces = 1.0 + (double)a.grid / ((double)a.B * a.HG);
+  const double pieces = (1.0 + (double)a.grid / ((double)a.B * a.HG)) * a.sub;
   int S = 1;
   while (S < kCombineWarps && 4.0 * S <= pieces) S *= 2;
   const long long per_cta = kCombineWarps / S;

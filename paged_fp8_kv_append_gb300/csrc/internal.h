@@ -69,7 +69,8 @@ struct DecodeArgs {
   int32_t Hs;           // kv heads per unit of work (a head group)
   int32_t HG;           // segments per request: head groups (GQA) or 64-row blocks (latent)
   int32_t stages;       // ring stages of the split kernel
-  int32_t unit_tokens;  // tokens per unit of work (a page)
+  int32_t unit_tokens;  // tokens per unit of work (a page; 4-bit pools: two)
+  int32_t sub;          // partials a (CTA, segment) piece leaves (4-bit pools: one a warp of a head)
   // the split kernel builds the batch plan itself (B + 1 <= its shared-memory
   // prefix cache) instead of reading the plan kernel's; its CTA 0 writes the
   // plan to the workspace for the combine
@@ -189,12 +190,12 @@ struct DecodeConfig {
   int HG;           // segments per request
   int stages;       // ring stages
   int unit_tokens;  // tokens per unit of work
+  int sub;          // partials per piece
 };
 
 // Ring bytes and stage limit of the GQA split kernel (for the host-side
 // choice of heads per unit and ring depth).
 int gqa_ring_bytes(int kind);
-int gqa_tile_bytes(int kind);
 int gqa_max_stages();
 int gqa_consumer_warps(int kind);
 int gqa_self_plan_max_batch();
@@ -207,11 +208,14 @@ size_t decode_ws_layout(const kv_pool_desc& d, int B, int Hkv, const DecodeConfi
 cudaError_t launch_decode_plan(const DecodeArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_decode_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
 cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
+cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
 cudaError_t launch_latent_split(const DecodeArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* launches);
 
 // Occupancy-derived CTAs per SM for the split kernels (cached per device).
 int gqa_split_ctas_per_sm(int kind);
+int e2m1_split_ctas_per_sm(int kind);
+int e2m1_split_warps();
 int latent_split_ctas_per_sm();
 int latent_unit_tokens();
 int latent_row_block();
