@@ -41,7 +41,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16, 6: 4-bit)
     const bool bf16 = d.dtype == KV_DTYPE_BF16, fp4 = d.dtype == KV_DTYPE_E2M1, wide = R > 8;
     cfg->kind = fp4 ? (wide ? 6 : 5) : bf16 ? (wide ? 4 : 1) : (wide ? 3 : 0);
-    const int warps = fp4 ? e2m1_split_warps() : gqa_consumer_warps(cfg->kind);
+    const int warps = fp4 ? e2m1_split_warps(cfg->kind) : gqa_consumer_warps(cfg->kind);
     // heads per unit: the largest power of two <= 8 (<= 4 for bf16, whose
     // tiles are twice as large) dividing Hkv, with heads x row blocks dividing
     // the consumer warp count; 16-row blocks may be padded with whole unused

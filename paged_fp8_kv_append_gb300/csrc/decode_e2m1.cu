@@ -39,29 +39,42 @@ namespace kvfp8 {
 namespace {
 
 #ifndef KV_E2M1_WARPS
-#define KV_E2M1_WARPS 12
+#define KV_E2M1_WARPS 16
+#endif
+#ifndef KV_E2M1_WARPS16
+#define KV_E2M1_WARPS16 12
 #endif
 #ifndef KV_E2M1_STAGES
-#define KV_E2M1_STAGES 3
+#define KV_E2M1_STAGES 2
 #endif
 #ifndef KV_E2M1_STAGES16
-#define KV_E2M1_STAGES16 3
+#define KV_E2M1_STAGES16 2
 #endif
 #ifndef KV_E2M1_PAIR16
-#define KV_E2M1_PAIR16 1
+#define KV_E2M1_PAIR16 2
 #endif
 
-constexpr int kWarps = KV_E2M1_WARPS, kThreads = kWarps * 32;
 constexpr int kStage = 4 * kE2m1Tile;  // a unit: K of its two pages, then V
 constexpr int kPfxCache = 1024;        // plan entries cached in shared memory
 
+// What a warp knows of its units, 16 of one batch and 16 of the next: for each of a
+// unit's two pages its tile (-1: none, or not to be read) and block scales.
+struct UnitTable {
+  float2 ks[32], vs[32];
+  int2 tile[32];
+};
+
 template <bool WIDE>
 struct E2m1Cfg {
+  static constexpr int WARPS = WIDE ? KV_E2M1_WARPS16 : KV_E2M1_WARPS;
+  static constexpr int THREADS = WARPS * 32;
   static constexpr int ST = WIDE ? KV_E2M1_STAGES16 : KV_E2M1_STAGES;  // units in a warp's ring
+  static constexpr int QBYTES = WIDE ? 4096 : 2048;
   // shared memory carve-up (byte offsets)
-  static constexpr int OFF_Q = kWarps * ST * kStage;              // WIDE: [W] Q operands of 4 KB
-  static constexpr int OFF_BAR = OFF_Q + (WIDE ? kWarps * 4096 : 0);  // [W][ST] data ready
-  static constexpr int OFF_PFX = OFF_BAR + kWarps * ST * 8;
+  static constexpr int OFF_Q = WARPS * ST * kStage;          // [W] Q operands
+  static constexpr int OFF_UNIT = OFF_Q + WARPS * QBYTES;    // [W] UnitTable
+  static constexpr int OFF_BAR = OFF_UNIT + WARPS * (int)sizeof(UnitTable);  // [W][ST] data ready
+  static constexpr int OFF_PFX = OFF_BAR + WARPS * ST * 8;
   static constexpr int OFF_FLAG = OFF_PFX + kPfxCache * 4;        // abort flag
   static constexpr int OFF_WSUM = OFF_FLAG + 16;                  // [32] plan scan warp sums
   static constexpr int SMEM = OFF_WSUM + 32 * 4;
@@ -132,7 +145,7 @@ struct E2m1Page {
 struct E2m1Rows8 {
   float &m0, &m1, &l0, &l1;
   float (&acc)[8][4];
-  const uint32_t (&qf)[8][2];
+  const uint32_t* qs;      // Q as B operands, [k-steps 2w, 2w + 1][lane] 16-byte words
   const float qsc0, qsc1;  // score scales of rows 2t, 2t + 1
   const int G, T, seen0;   // query token tq sees positions 0 .. seen0 + tq
 
@@ -140,28 +153,36 @@ struct E2m1Rows8 {
   template <int NP, bool EDGE>
   __device__ __forceinline__ void pages(const E2m1Page (&pg)[NP]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint4 va[NP][2];
     float s[NP][4];
+    {
+      uint4 kg[NP], kh[NP];
+      uint32_t sg[NP], sh[NP];
+      float sb[NP][4];
 #pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const uint4 kg = lds128(pg[u].k + 64 * g + 16 * t);
-      const uint4 kh = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
-      uint32_t sg, sh;
-      e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg, sh);
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < NP; ++u) {
+        kg[u] = lds128(pg[u].k + 64 * g + 16 * t);
+        kh[u] = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
+        e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg[u], sh[u]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-        const uint32_t s0 = half_of(sg, w >> 1), s1 = half_of(sh, w >> 1);
-        uint32_t x[4], y[4];
-        e2m1x8_scaled(w_of(kg, w), s0, s0, x[0], x[1], x[2], x[3]);
-        e2m1x8_scaled(w_of(kh, w), s1, s1, y[0], y[1], y[2], y[3]);
-        mma16816<true>(sa, x[0], y[0], x[1], y[1], qf[2 * w][0], qf[2 * w][1]);
-        mma16816<true>(sb, x[2], y[2], x[3], y[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+        for (int e = 0; e < 4; ++e) s[u][e] = sb[u][e] = 0.0f;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[u][e] = sa[e] + sb[e];
-      va[u][0] = lds128(pg[u].v + 16 * lane);
-      va[u][1] = lds128(pg[u].v + 512 + 16 * lane);
+      for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
+        const uint4 q = lds128(qs + (w * 32 + lane) * 4);
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+          const uint32_t s0 = half_of(sg[u], w >> 1), s1 = half_of(sh[u], w >> 1);
+          uint32_t x[4], y[4];
+          e2m1x8_scaled(w_of(kg[u], w), s0, s0, x[0], x[1], x[2], x[3]);
+          e2m1x8_scaled(w_of(kh[u], w), s1, s1, y[0], y[1], y[2], y[3]);
+          mma16816<true>(s[u], x[0], y[0], x[1], y[1], q.x, q.y);
+          mma16816<true>(sb[u], x[2], y[2], x[3], y[3], q.z, q.w);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < NP; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[u][e] += sb[u][e];
     }
     // ---- weights against the rows' references
     float bias[NP], p[NP][4], big = -INFINITY;
@@ -234,6 +255,7 @@ struct E2m1Rows8 {
     for (int u = 0; u < NP; ++u) {
       const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p[u][0], p[u][1]));
       const uint32_t b1 = transpose8x8(f32x2_to_f16x2(p[u][2], p[u][3]));
+      const uint4 v0 = lds128(pg[u].v + 16 * lane), v1 = lds128(pg[u].v + 512 + 16 * lane);
       const uint32_t sw = lds32(pg[u].v + kE2m1Scales + 4 * lane);
       auto add = [&](uint32_t scales, uint32_t c0, uint32_t c1) {
         uint32_t slo, shi;  // scales of group g's same tokens
@@ -241,7 +263,7 @@ struct E2m1Rows8 {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
           uint32_t a0, a1, a2, a3;
-          e2m1x8_scaled(w_of(va[u][i >> 2], i & 3), slo, shi, a0, a1, a2, a3);
+          e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, a0, a1, a2, a3);
           mma16816<true>(acc[i], a0, a1, a2, a3, c0, c1);
         }
       };
@@ -429,16 +451,8 @@ struct E2m1Rows16 {
   }
 };
 
-// What a lane knows of one of the warp's units: its pages' tiles (-1: none, or not
-// to be read) and block scales.
-struct LaneUnit {
-  int tile[2];
-  float ks[2], vs[2];
-  bool bad;  // a page must not be read: its request gets no output
-};
-
 template <bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(const DecodeArgs a) {
   using C = E2m1Cfg<WIDE>;
   constexpr int D = 128, ST = C::ST;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -453,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
   // row blocks of a kv head, one a warp (WIDE: of 16 rows)
   const int RBW = a.R8 / (WIDE ? 16 : 8), Hv = Hs * RBW;
   if (Hs < 1 || RBW < 1 || (!WIDE && RBW != 1) || RBW * (WIDE ? 16 : 8) != a.R8 || a.R < 1 ||
-      a.R > a.R8 || Hs * HG != Hkv || kWarps % Hv != 0 || a.sub != kWarps / Hv ||
+      a.R > a.R8 || Hs * HG != Hkv || C::WARPS % Hv != 0 || a.sub != C::WARPS / Hv ||
       a.unit_tokens != 32 || (a.self_plan && B + 1 > kPfxCache)) {
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x == 0) set_error(a.d.ctl, KV_ERR_INTERNAL);  // host chose a bad configuration
     return;
   }
-  if (threadIdx.x < kWarps * ST) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x < C::WARPS * ST) mbar_init(&bars[threadIdx.x], 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   fence_mbar_init();
   pdl_wait();
@@ -470,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
     const bool refused = decode_plan_shared(a, pfx_s, wsum_s);
     if (blockIdx.x == 0) decode_plan_store(a, pfx_s, refused);
   } else if (cached) {
-    for (int i = threadIdx.x; i <= B; i += kThreads) pfx_s[i] = a.ws.pfx[i];
+    for (int i = threadIdx.x; i <= B; i += C::THREADS) pfx_s[i] = a.ws.pfx[i];
   }
   __syncthreads();  // the plan and the barriers are visible to every warp
   const int32_t* pfx = cached ? pfx_s : a.ws.pfx;
@@ -481,79 +495,80 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
   if (n_units <= 0) return;
   const Cursor start = cursor_at(pfx, B, HG, x_begin);
 
-  const int WPH = kWarps / Hv;                // warps per virtual head (kv head, row block)
+  const int WPH = C::WARPS / Hv;                // warps per virtual head (kv head, row block)
   const int vh = warp % Hv, lg = warp / Hv;
   const int hw = vh / RBW, n0 = (vh - hw * RBW) * 16;  // kv head of the group, first query row
   uint8_t* ring = smem + warp * (ST * kStage);
   uint64_t* full = bars + warp * ST;
   const uint64_t policy = l2_evict_first_policy();
 
-  // ---- this warp's units: i = 0, 1, .. are the CTA's lg + WPH i.  Lane l holds
-  // unit 32 b + l of batch b; page ids are loaded two batches ahead, scales one.
+  UnitTable* table = reinterpret_cast<UnitTable*>(smem + C::OFF_UNIT) + warp;
+
+  // ---- this warp's units: i = 0, 1, .. are the CTA's lg + WPH i, in batches of 16.
+  // Lane l looks after page l % 2 of unit 16 b + l / 2: page ids are loaded two
+  // batches ahead, scales one.
   const int count = (n_units - lg + WPH - 1) / WPH;  // (<= 0: none)
-  Cursor lc = start;  // per-lane cursor, only moves forward
-  struct Ids {
-    int p[2], hg;  // page ids (-1: behind the length), head group (-1: no unit)
+  struct Id {
+    int p, hg;  // page id (-1: none; -2: out of range; -3: a stale tag), head group
   };
-  auto locate = [&](int i) {
-    Ids u{{-1, -1}, -1};
-    if (i >= count) return u;
+  auto locate = [&](int b) {
+    const int i = 16 * b + (lane >> 1);
+    Id id{-1, 0};
+    if (i >= count) return id;
     const long long x = x_begin + lg + WPH * i;
-    while (x >= lc.seg_start + lc.np) cursor_next(lc, pfx, B, HG);
-    u.hg = lc.h;
-    const int j = 2 * (int)(x - lc.seg_start);
-    const long long at = (long long)lc.r * a.max_pages + j;
-    const int L = a.seq_lens[lc.r];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (k == 0 || L > 16 * j + 16) {
-        const int p = a.page_table[at + k];
-        // the fused check: the tag is compared before the page is fetched
-        u.p[k] = p < 0 || p >= a.d.num_pages                                  ? -2
-                 : a.exp_tags == nullptr || a.d.tags[p] == a.exp_tags[at + k] ? p
-                                                                              : -3;
-      }
-    return u;
+    const Cursor c = cursor_at(pfx, B, HG, x);
+    id.hg = c.h;
+    const int j = 2 * (int)(x - c.seg_start) + (lane & 1);
+    if (a.seq_lens[c.r] <= 16 * j) return id;  // (the unit's second page)
+    const long long at = (long long)c.r * a.max_pages + j;
+    const int p = a.page_table[at];
+    // the fused check: the tag is compared before the page is fetched
+    id.p = p < 0 || p >= a.d.num_pages                                ? -2
+           : a.exp_tags == nullptr || a.d.tags[p] == a.exp_tags[at] ? p
+                                                                    : -3;
+    return id;
   };
-  auto scales = [&](const Ids& id) {
-    LaneUnit u;
-    u.bad = false;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      u.tile[k] = -1;
-      u.ks[k] = u.vs[k] = 1.0f;
-      if (id.hg < 0) continue;
-      if (id.p[k] == -2) set_error(a.d.ctl, KV_ERR_BAD_PAGE_ID);
-      u.bad = u.bad || id.p[k] < -1;
-      if (id.p[k] < 0) continue;
-      u.tile[k] = id.p[k] * Hkv + id.hg * Hs + hw;  // (a cache of 2^31 tiles is 2 TB)
-      u.ks[k] = a.d.k_scale[u.tile[k]];
-      u.vs[k] = a.d.v_scale[u.tile[k]];
+  // batch b into the table; which of its pages must not be read
+  auto fill = [&](int b, const Id& id) {
+    int tile = -1;
+    float ks = 1.0f, vs = 1.0f;
+    if (id.p == -2) set_error(a.d.ctl, KV_ERR_BAD_PAGE_ID);
+    if (id.p >= 0) {
+      tile = id.p * Hkv + id.hg * Hs + hw;  // (a cache of 2^31 tiles is 2 TB)
+      ks = a.d.k_scale[tile];
+      vs = a.d.v_scale[tile];
     }
-    return u;
+    const int at = 32 * (b & 1) + lane;
+    reinterpret_cast<float*>(table->ks)[at] = ks;
+    reinterpret_cast<float*>(table->vs)[at] = vs;
+    reinterpret_cast<int*>(table->tile)[at] = tile;
+    return __ballot_sync(0xffffffffu, id.p < -1);
   };
-  const Ids id0 = locate(lane), id1 = locate(32 + lane);
-  Ids ids = locate(64 + lane);
-  LaneUnit cur = scales(id0), nxt = scales(id1);
-  uint32_t bad_units = __ballot_sync(0xffffffffu, cur.bad);
-  int batch = 0;  // of cur
+  uint32_t bad_pages, bad_next;
+  Id ids;
+  {
+    const Id id0 = locate(0), id1 = locate(1);
+    ids = locate(2);
+    bad_pages = fill(0, id0);
+    bad_next = fill(1, id1);
+    __syncwarp();
+  }
+  int batch = 0;
   // Unit i's copies, into stage st: lane k issues K of page k, lane 2 + k V.
   auto fetch = [&](int i, int st) {
     if (i >= count) return;
-    const bool c = (i >> 5) == batch;
-    const int t0 = __shfl_sync(0xffffffffu, c ? cur.tile[0] : nxt.tile[0], i & 31);
-    const int t1 = __shfl_sync(0xffffffffu, c ? cur.tile[1] : nxt.tile[1], i & 31);
-    const int tile = lane & 1 ? t1 : t0;
+    const int2 tl = table->tile[i & 31];
     if (lane == 0)
-      mbar_arrive_expect_tx(&full[st], ((t0 >= 0) + (t1 >= 0)) * 2 * kE2m1Tile);
+      mbar_arrive_expect_tx(&full[st], ((tl.x >= 0) + (tl.y >= 0)) * 2 * kE2m1Tile);
     __syncwarp();
+    const int tile = lane & 1 ? tl.y : tl.x;
     if (lane < 4 && tile >= 0)
       bulk_g2s(ring + st * kStage + lane * kE2m1Tile,
                static_cast<const uint8_t*>(lane < 2 ? a.d.k_cache : a.d.v_cache) +
                    (long long)tile * kE2m1Tile,
                kE2m1Tile, &full[st], policy);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < ST; ++i) fetch(i, i);
 
   Cursor seg = start;
@@ -573,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
     // units whose 32 positions every query token sees: below i_full
     const int see = max(0, L - T + 1) / 32 + done - u0 - lg;
     const int i_full = min(i_end, see > 0 ? (see + WPH - 1) / WPH : 0);
+    int pos = 32 * (lg + WPH * i - done + u0);  // of unit i
     bool bad = false;
 
     auto units = [&](auto& rows) {
@@ -582,16 +598,18 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
           if (!ok) ok = mbar_wait(&full[st], phase, abort_flag, a.d.ctl, wait_info(warp, 0, st));
           gone = !__all_sync(0xffffffffu, ok);
         }
+        const float2 ks = table->ks[i & 31], vs = table->vs[i & 31];
         E2m1Page pg[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           pg[k].k = ring + st * kStage + k * kE2m1Tile;
           pg[k].v = pg[k].k + 2 * kE2m1Tile;
-          pg[k].ks = __shfl_sync(0xffffffffu, cur.ks[k], i & 31);
-          pg[k].vs = __shfl_sync(0xffffffffu, cur.vs[k], i & 31);
-          pg[k].pos0 = 32 * (lg + WPH * i - done + u0) + 16 * k;
+          pg[k].ks = k ? ks.y : ks.x;
+          pg[k].vs = k ? vs.y : vs.x;
+          pg[k].pos0 = pos + 16 * k;
           pg[k].nv = min(16, L - pg[k].pos0);
         }
+        pos += 32 * WPH;
         if (!gone) {
           if constexpr (decltype(edge)::value) {
             // (a page behind the length was not fetched)
@@ -620,17 +638,17 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
         }
       };
       while (i < i_end) {
-        if ((i >> 5) != batch) {
-          cur = nxt;
-          bad_units = __ballot_sync(0xffffffffu, cur.bad);
-          nxt = scales(ids);
+        if ((i >> 4) != batch) {
           ++batch;
-          ids = locate(32 * batch + 64 + lane);
+          bad_pages = bad_next;
+          bad_next = fill(batch + 1, ids);
+          __syncwarp();
+          ids = locate(batch + 2);
         }
         // (a unit that must not be read may be computed on all the same: the
         // request gets no output)
-        const int stop = min(i_end, 32 * batch + 32);
-        bad = bad || (bad_units >> (i & 31)) << (31 - (stop - 1 - i)) != 0;
+        const int stop = min(i_end, 16 * batch + 16);
+        bad = bad || (bad_pages >> (2 * (i & 15))) << (32 - 2 * (stop - i)) != 0;
         const int full_stop = min(stop, i_full);
         while (i < full_stop) unit(FalseType{});
         while (i < stop) unit(TrueType{});
@@ -645,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
     if constexpr (WIDE) {
       // ---- Q as A operands {a0, a1, a2, a3} of k-step j = rows g, g + 8 x dims
       // d(j) + 0, 1 and d(j) + 2, 3 with d(j) = 16t + 4j (j < 4), 64 + 16t + 4 (j - 4)
-      uint32_t* qs = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + warp * 4096);
+      uint32_t* qs = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + warp * C::QBYTES);
       float qsc[2];  // score scales of rows g and g + 8, with the row's 2^-e
       {
         uint32_t qa[8][4];
@@ -706,9 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
           *reinterpret_cast<float4*>(op + (g + 8 * (e >> 1)) * D + 32 * t + 16 * (e & 1) + k) =
               make_float4(acc[k][e], acc[k + 1][e], acc[k + 2][e], acc[k + 3][e]);
     } else {
-      // ---- query fragments of row g (zero for padding rows): k-step j has dims
-      // 16 (t + 4 (j / 4)) + 4 (j % 4) + 0 .. 3
-      uint32_t qf[8][2];
+      // ---- query fragments of row g (zero for padding rows) in shared memory, those of
+      // k-steps 2w and 2w + 1 a 16-byte word: k-step j has dims 16 (t + 4 (j / 4)) + 4 (j % 4) ..
+      uint32_t* qs = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + warp * C::QBYTES);
       float qsc0, qsc1;  // score scales of rows 2t, 2t + 1, with the row's 2^-e
       {
         const bool live = g < R;
@@ -728,19 +746,19 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
         // rows 2t and 2t + 1 are held by the lanes g = 2t and 2t + 1
         qsc0 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t));
         qsc1 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t + 4));
+        __syncwarp();  // the last piece's reads
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          qf[2 * u][0] = bf16x2_to_f16x2_scaled(v[u].x, pw);
-          qf[2 * u][1] = bf16x2_to_f16x2_scaled(v[u].y, pw);
-          qf[2 * u + 1][0] = bf16x2_to_f16x2_scaled(v[u].z, pw);
-          qf[2 * u + 1][1] = bf16x2_to_f16x2_scaled(v[u].w, pw);
-        }
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4*>(qs + (u * 32 + lane) * 4) =
+              make_uint4(bf16x2_to_f16x2_scaled(v[u].x, pw), bf16x2_to_f16x2_scaled(v[u].y, pw),
+                         bf16x2_to_f16x2_scaled(v[u].z, pw), bf16x2_to_f16x2_scaled(v[u].w, pw));
+        __syncwarp();
       }
       float m0 = kUnset, m1 = kUnset, l0 = 0.0f, l1 = 0.0f;
       float acc[8][4];
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-      E2m1Rows8 rows{m0, m1, l0, l1, acc, qf, qsc0, qsc1, G, T, L - T};
+      E2m1Rows8 rows{m0, m1, l0, l1, acc, qs, qsc0, qsc1, G, T, L - T};
       units(rows);
       rows.finish();
 #pragma unroll
@@ -773,9 +791,135 @@ __global__ void __launch_bounds__(kThreads, 1) e2m1_split_kernel(const DecodeArg
   }
 }
 
+// ------------------------------------------------- combine
+
+// O = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over a segment's partials c: S
+// warps an output row, S about a fourth to an eighth of the partials of a row, so that a
+// warp's loads are in flight together and the kernel is a few round trips; lane l has
+// dims 4l .. 4l + 3.  W: warps a block.
+template <int W>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
+    e2m1_combine_kernel(const DecodeArgs a, int S) {
+  constexpr int D = 128, kU = 8;  // partials loaded together
+  __shared__ float4 st_o[W][32];
+  __shared__ float2 st_ml[W];
+  __shared__ int st_bad[W];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (S - 1);
+  const int Hkv = a.d.num_kv_heads, R = a.R;
+  const long long item = (long long)blockIdx.x * (W / S) + warp / S;
+  const bool live = item < (long long)a.B * Hkv * R;
+  // every warp reaches the block's barrier: no early return
+  int r = 0, h = 0, n = 0, parts = 0;
+  long long row0 = 0;
+  bool skip = true;
+  if (live) {
+    const int rh = (int)(item / R);
+    n = (int)(item - (long long)rh * R);
+    r = rh / Hkv;
+    h = rh - r * Hkv;
+    const int first = a.ws.pfx[r], np = a.ws.pfx[r + 1] - first, all = a.ws.pfx[a.B];
+    skip = a.ws.rq_skip[r];  // aborted or invalid length: output left untouched
+    if (!skip && np > 0) {
+      const int hg = h / a.Hs, hw = h - hg * a.Hs;
+      const long long total = (long long)all * a.HG;
+      const long long start = (long long)first * a.HG + (long long)hg * np, last = start + np - 1;
+      int c0, c1;  // the CTAs whose ranges meet the segment
+      if (total < (1ll << 31)) {
+        const uint32_t per = ((uint32_t)total + a.grid - 1) / a.grid;
+        c0 = (uint32_t)start / per;
+        c1 = (uint32_t)last / per;
+      } else {
+        const long long per = (total + a.grid - 1) / a.grid;
+        c0 = (int)(start / per);
+        c1 = (int)(last / per);
+      }
+      parts = (c1 - c0 + 1) * a.sub;
+      row0 = ((((long long)r * a.HG + hg + c0) * a.sub) * a.Hs + hw) * a.R8 + n;
+    }
+  }
+  const int stride = a.Hs * a.R8;  // rows from a partial to the next
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float M = -INFINITY, L = 0.0f;
+  bool bad = false;
+  const int cnt = (parts - sub + S - 1) / S;  // this warp's: sub, sub + S, ..
+  for (int j0 = 0; j0 < cnt; j0 += 32) {
+    const int nj = min(32, cnt - j0);
+    auto row_of = [&](int j) { return row0 + (long long)(sub + S * (j0 + j)) * stride; };
+    auto load = [&](int j) {
+      return j < nj ? *reinterpret_cast<const float4*>(a.ws.o_part + row_of(j) * D + 4 * lane)
+                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    float4 o[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) o[u] = load(u);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < nj) ml = *reinterpret_cast<const float2*>(a.ws.ml_part + row_of(lane) * 2);
+    bad = bad || __any_sync(0xffffffffu, ml.y < 0.0f);
+    const float Mc = warp_max(ml.x);
+    if (Mc == -INFINITY) continue;  // nothing visible
+    const float Mn = fmaxf(M, Mc), keep = exp2f(M - Mn);
+    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - Mn);
+    L = L * keep + warp_sum(ml.y * w);
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+    for (int k = 0; k < nj; k += kU) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (k + u) & 31);
+        // (a partial that saw nothing has weight 0 and adds nothing)
+        if (k + u < nj && wu != 0.0f) {
+          acc.x = fmaf(o[u].x, wu, acc.x);
+          acc.y = fmaf(o[u].y, wu, acc.y);
+          acc.z = fmaf(o[u].z, wu, acc.z);
+          acc.w = fmaf(o[u].w, wu, acc.w);
+        }
+      }
+      if (k + kU < nj)
+#pragma unroll
+        for (int u = 0; u < kU; ++u) o[u] = load(k + kU + u);
+    }
+    M = Mn;
+  }
+  if (S > 1) {
+    st_o[warp][lane] = acc;
+    if (lane == 0) {
+      st_ml[warp] = make_float2(M, L);
+      st_bad[warp] = bad;
+    }
+    __syncthreads();
+    if (sub == 0) {
+      for (int k = 1; k < S; ++k) {
+        bad = bad || st_bad[warp + k] != 0;
+        const float2 ml = st_ml[warp + k];
+        if (ml.x == -INFINITY) continue;
+        const float Mn = fmaxf(M, ml.x), x = exp2f(M - Mn), y = exp2f(ml.x - Mn);
+        const float4 v = st_o[warp + k][lane];
+        L = L * x + ml.y * y;
+        acc.x = acc.x * x + v.x * y;
+        acc.y = acc.y * x + v.y * y;
+        acc.z = acc.z * x + v.z * y;
+        acc.w = acc.w * x + v.w * y;
+        M = Mn;
+      }
+    }
+  }
+  if (!live || sub != 0) return;
+  // fused tag check: the warp of the request's first row writes its abort bit
+  // (every segment and row of a request meets the same pages)
+  if (a.abort_out != nullptr && h == 0 && n == 0) a.abort_out[r] = (skip || bad) ? 1 : 0;
+  if (skip || bad) return;
+  const float inv = M == -INFINITY ? 0.0f : 1.0f / L;  // nothing visible: zeros
+  uint2 w;
+  w.x = f32x2_to_bf16x2(acc.x * inv, acc.y * inv);
+  w.y = f32x2_to_bf16x2(acc.z * inv, acc.w * inv);
+  const int tq = n / a.G, hq = h * a.G + n - tq * a.G;
+  *reinterpret_cast<uint2*>(a.out + (((long long)r * a.T + tq) * a.Hq + hq) * D + 4 * lane) = w;
+}
+
 }  // namespace
 
-int e2m1_split_warps() { return kWarps; }
+int e2m1_split_warps(int kind) { return kind == 6 ? E2m1Cfg<true>::WARPS : E2m1Cfg<false>::WARPS; }
 
 int e2m1_split_ctas_per_sm(int kind) {
   static int cache[2] = {-1, -1};
@@ -785,7 +929,8 @@ int e2m1_split_ctas_per_sm(int kind) {
   const int smem = wide ? E2m1Cfg<true>::SMEM : E2m1Cfg<false>::SMEM;
   int n = 0;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem);
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      &n, kernel, 32 * e2m1_split_warps(kind), smem);
   if (e != cudaSuccess || n <= 0) return 0;
   cache[wide] = n;
   return n;
@@ -793,10 +938,27 @@ int e2m1_split_ctas_per_sm(int kind) {
 
 cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
   const cudaError_t e =
-      kind == 6 ? launch_pdl(e2m1_split_kernel<true>, dim3(a.grid), dim3(kThreads),
+      kind == 6 ? launch_pdl(e2m1_split_kernel<true>, dim3(a.grid), dim3(E2m1Cfg<true>::THREADS),
                              E2m1Cfg<true>::SMEM, s, a)
-                : launch_pdl(e2m1_split_kernel<false>, dim3(a.grid), dim3(kThreads),
+                : launch_pdl(e2m1_split_kernel<false>, dim3(a.grid), dim3(E2m1Cfg<false>::THREADS),
                              E2m1Cfg<false>::SMEM, s, a);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_e2m1_combine(const DecodeArgs& a, cudaStream_t s, int* launches) {
+  const long long rows = (long long)a.B * a.d.num_kv_heads * a.R;
+  if (rows <= 0) return cudaSuccess;
+  const double parts = a.sub * (1.0 + (double)a.grid / ((double)a.B * a.HG));  // a row, about
+  int S = 1;
+  while (S < 8 && 8.0 * S < parts) S *= 2;
+  if (parts > 128.0) S = 32;
+  const int W = S == 32 ? 32 : 8;
+  const long long blocks = (rows + W / S - 1) / (W / S);
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const cudaError_t e =
+      launch_pdl(S == 32 ? e2m1_combine_kernel<32> : e2m1_combine_kernel<8>,
+                 dim3((unsigned)blocks), dim3(W * 32), 0, s, a, S);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -1000,9 +1000,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
       const long long per = (total + a.grid - 1) / a.grid;
       const long long start = (long long)HG * pfx_r + (long long)hg * np;
       const int c0 = (int)(start / per), c1 = (int)((start + np - 1) / per);
-      const long long slot0 = (seg + c0) * a.sub;
+      const long long slot0 = seg + c0;
       const int R8 = a.R8;
-      // partial row of this warp's partial jj (partials sub + S jj of the segment)
+      // partial row of this warp's piece jj (pieces c = sub + S jj)
       auto row_of = [&](int jj) -> long long {
         return ((slot0 + sub + (long long)S * jj) * Hs + hw) * R8 + nl;
       };
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
       // already loading; the chunk's max and weights come from warp
       // reductions, then the weighted outputs are summed with independent
       // loads (no chain through a running max)
-      const int cnt = ((c1 - c0 + 1) * a.sub - sub + S - 1) / S;
+      const int cnt = (c1 - c0 + 1 - sub + S - 1) / S;
       for (int j0 = 0; j0 < cnt; j0 += 32) {
         const int nj = min(32, cnt - j0);
         float4 o[kU][NG];
@@ -1206,11 +1206,12 @@ cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int*
 }
 
 cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* launches) {
+  if (a.d.dtype == KV_DTYPE_E2M1) return launch_e2m1_combine(a, s, launches);
   const long long items = (long long)a.B * a.d.num_kv_heads * a.R;
   if (items <= 0) return cudaSuccess;
   // partials of one segment: about 1 + grid / segments; give each merging
   // warp at least two of them
-  const double pieces = (1.0 + (double)a.grid / ((double)a.B * a.HG)) * a.sub;
+  const double pieces = 1.0 + (double)a.grid / ((double)a.B * a.HG);
   int S = 1;
   while (S < kCombineWarps && 4.0 * S <= pieces) S *= 2;
   const long long per_cta = kCombineWarps / S;

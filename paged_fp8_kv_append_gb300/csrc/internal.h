@@ -208,6 +208,7 @@ size_t decode_ws_layout(const kv_pool_desc& d, int B, int Hkv, const DecodeConfi
 cudaError_t launch_decode_plan(const DecodeArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_decode_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
 cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
+cudaError_t launch_e2m1_combine(const DecodeArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches);
 cudaError_t launch_latent_split(const DecodeArgs& a, cudaStream_t s, int* launches);
 cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* launches);
@@ -215,7 +216,7 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* laun
 // Occupancy-derived CTAs per SM for the split kernels (cached per device).
 int gqa_split_ctas_per_sm(int kind);
 int e2m1_split_ctas_per_sm(int kind);
-int e2m1_split_warps();
+int e2m1_split_warps(int kind);
 int latent_split_ctas_per_sm();
 int latent_unit_tokens();
 int latent_row_block();
