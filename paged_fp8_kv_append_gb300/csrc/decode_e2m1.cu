@@ -50,9 +50,6 @@ namespace {
 #ifndef KV_E2M1_STAGES16
 #define KV_E2M1_STAGES16 2
 #endif
-#ifndef KV_E2M1_PAIR16
-#define KV_E2M1_PAIR16 2
-#endif
 
 constexpr int kStage = 4 * kE2m1Tile;  // a unit: K of its two pages, then V
 constexpr int kPfxCache = 1024;        // plan entries cached in shared memory
@@ -73,10 +70,8 @@ struct E2m1Cfg {
   // shared memory carve-up (byte offsets)
   static constexpr int OFF_Q = WARPS * ST * kStage;          // [W] Q operands
   static constexpr int OFF_UNIT = OFF_Q + WARPS * QBYTES;    // [W] UnitTable
-  static constexpr int OFF_BAR = OFF_UNIT + WARPS * (int)sizeof(UnitTable);  // [W][ST] data ready
-  static constexpr int OFF_PFX = OFF_BAR + WARPS * ST * 8;
-  static constexpr int OFF_FLAG = OFF_PFX + kPfxCache * 4;        // abort flag
-  static constexpr int OFF_WSUM = OFF_FLAG + 16;                  // [32] plan scan warp sums
+  static constexpr int OFF_PFX = OFF_UNIT + WARPS * (int)sizeof(UnitTable);
+  static constexpr int OFF_WSUM = OFF_PFX + kPfxCache * 4;  // [32] plan scan warp sums
   static constexpr int SMEM = OFF_WSUM + 32 * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -133,9 +128,32 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+template <int OFFSET>
+__device__ __forceinline__ uint4 lds128_at(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at), "n"(OFFSET));
+  return v;
+}
+template <int OFFSET>
+__device__ __forceinline__ uint32_t lds32_at(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(OFFSET));
+  return v;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst_smem, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst_smem),
+               "l"(src), "l"(policy)
+               : "memory");
+}
+
 // A page as a warp meets it: its head's tiles, and what is known of them.
+// (shared-memory addresses are 32-bit, with the lane's offset in them: 16 bytes of
+// codes a lane at k16 and k16 + 512, 4 of scales at k4, and V's behind K's of the unit)
 struct E2m1Page {
-  const uint8_t *k, *v;
+  uint32_t k16, k4;
   float ks, vs;  // block scales
   int nv, pos0;  // tokens below the request's length, the first one's position
 };
@@ -145,7 +163,7 @@ struct E2m1Page {
 struct E2m1Rows8 {
   float &m0, &m1, &l0, &l1;
   float (&acc)[8][4];
-  const uint32_t* qs;      // Q as B operands, [k-steps 2w, 2w + 1][lane] 16-byte words
+  const uint32_t q16;      // Q as B operands, [k-steps 2w, 2w + 1][lane] 16-byte words (at this lane's)
   const float qsc0, qsc1;  // score scales of rows 2t, 2t + 1
   const int G, T, seen0;   // query token tq sees positions 0 .. seen0 + tq
 
@@ -160,15 +178,18 @@ struct E2m1Rows8 {
       float sb[NP][4];
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        kg[u] = lds128(pg[u].k + 64 * g + 16 * t);
-        kh[u] = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
-        e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg[u], sh[u]);
+        kg[u] = lds128_at<0>(pg[u].k16);
+        kh[u] = lds128_at<512>(pg[u].k16);
+        e4m3x4_to_f16(lds32_at<0>(pg[u].k4), sg[u], sh[u]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[u][e] = sb[u][e] = 0.0f;
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-        const uint4 q = lds128(qs + (w * 32 + lane) * 4);
+        const uint4 q = w == 0   ? lds128_at<0>(q16)
+                        : w == 1 ? lds128_at<512>(q16)
+                        : w == 2 ? lds128_at<1024>(q16)
+                                 : lds128_at<1536>(q16);
 #pragma unroll
         for (int u = 0; u < NP; ++u) {
           const uint32_t s0 = half_of(sg[u], w >> 1), s1 = half_of(sh[u], w >> 1);
@@ -255,8 +276,9 @@ struct E2m1Rows8 {
     for (int u = 0; u < NP; ++u) {
       const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p[u][0], p[u][1]));
       const uint32_t b1 = transpose8x8(f32x2_to_f16x2(p[u][2], p[u][3]));
-      const uint4 v0 = lds128(pg[u].v + 16 * lane), v1 = lds128(pg[u].v + 512 + 16 * lane);
-      const uint32_t sw = lds32(pg[u].v + kE2m1Scales + 4 * lane);
+      const uint4 v0 = lds128_at<2 * kE2m1Tile>(pg[u].k16);
+      const uint4 v1 = lds128_at<2 * kE2m1Tile + 512>(pg[u].k16);
+      const uint32_t sw = lds32_at<2 * kE2m1Tile>(pg[u].k4);
       auto add = [&](uint32_t scales, uint32_t c0, uint32_t c1) {
         uint32_t slo, shi;  // scales of group g's same tokens
         e4m3x4_to_f16(scales, slo, shi);
@@ -295,7 +317,7 @@ struct E2m1Rows8 {
 struct E2m1Rows16 {
   float &mA, &mB, &lA, &lB;
   float (&acc)[16][4];
-  const uint32_t* qs;  // Q as A operands, [k-step][lane] 16-byte words in shared memory
+  const uint32_t q16;  // Q as A operands, [k-step][lane] 16-byte words (at this lane's)
   const float qscA, qscB;
   const int n0, G, T, seen0;
 
@@ -309,16 +331,15 @@ struct E2m1Rows16 {
       uint32_t sg[NP], sh[NP];
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        kg[u] = lds128(pg[u].k + 64 * g + 16 * t);
-        kh[u] = lds128(pg[u].k + 64 * (g + 8) + 16 * t);
-        e4m3x4_to_f16(lds32(pg[u].k + kE2m1Scales + 4 * lane), sg[u], sh[u]);
+        kg[u] = lds128_at<0>(pg[u].k16);
+        kh[u] = lds128_at<512>(pg[u].k16);
+        e4m3x4_to_f16(lds32_at<0>(pg[u].k4), sg[u], sh[u]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[u][0][e] = s[u][1][e] = 0.0f;
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-        const uint4 q0 = lds128(qs + (2 * w * 32 + lane) * 4);
-        const uint4 q1 = lds128(qs + ((2 * w + 1) * 32 + lane) * 4);
+        const uint4 q0 = lds128_at<0>(q16 + 1024 * w), q1 = lds128_at<512>(q16 + 1024 * w);
 #pragma unroll
         for (int u = 0; u < NP; ++u) {
           const uint32_t s0 = half_of(sg[u], w >> 1), s1 = half_of(sh[u], w >> 1);
@@ -419,8 +440,9 @@ struct E2m1Rows16 {
     }
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const uint4 v0 = lds128(pg[u].v + 16 * lane), v1 = lds128(pg[u].v + 512 + 16 * lane);
-      const uint32_t sw = lds32(pg[u].v + kE2m1Scales + 4 * lane);
+      const uint4 v0 = lds128_at<2 * kE2m1Tile>(pg[u].k16);
+      const uint4 v1 = lds128_at<2 * kE2m1Tile + 512>(pg[u].k16);
+      const uint32_t sw = lds32_at<2 * kE2m1Tile>(pg[u].k4);
       auto add = [&](uint32_t scales, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
         uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
         e4m3x4_to_f16(scales, slo, shi);
@@ -456,9 +478,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   using C = E2m1Cfg<WIDE>;
   constexpr int D = 128, ST = C::ST;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   int32_t* pfx_s = reinterpret_cast<int32_t*>(smem + C::OFF_PFX);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
   int* wsum_s = reinterpret_cast<int*>(smem + C::OFF_WSUM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -474,9 +494,6 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     if (threadIdx.x == 0) set_error(a.d.ctl, KV_ERR_INTERNAL);  // host chose a bad configuration
     return;
   }
-  if (threadIdx.x < C::WARPS * ST) mbar_init(&bars[threadIdx.x], 1);
-  if (threadIdx.x == 0) *abort_flag = 0;
-  fence_mbar_init();
   pdl_wait();
   pdl_trigger();  // the combine's CTAs may wait resident in what this kernel leaves free
   const bool cached = B + 1 <= kPfxCache;
@@ -486,7 +503,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   } else if (cached) {
     for (int i = threadIdx.x; i <= B; i += C::THREADS) pfx_s[i] = a.ws.pfx[i];
   }
-  __syncthreads();  // the plan and the barriers are visible to every warp
+  __syncthreads();  // the plan is visible to every warp
   const int32_t* pfx = cached ? pfx_s : a.ws.pfx;
   const long long total = (long long)pfx[B] * HG;
   const long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -498,10 +515,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   const int WPH = C::WARPS / Hv;                // warps per virtual head (kv head, row block)
   const int vh = warp % Hv, lg = warp / Hv;
   const int hw = vh / RBW, n0 = (vh - hw * RBW) * 16;  // kv head of the group, first query row
-  uint8_t* ring = smem + warp * (ST * kStage);
-  uint64_t* full = bars + warp * ST;
-  const uint64_t policy = l2_evict_first_policy();
-
+  const uint32_t ring = smem_u32(smem) + warp * (ST * kStage);
   UnitTable* table = reinterpret_cast<UnitTable*>(smem + C::OFF_UNIT) + warp;
 
   // ---- this warp's units: i = 0, 1, .. are the CTA's lg + WPH i, in batches of 16.
@@ -519,63 +533,67 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     const Cursor c = cursor_at(pfx, B, HG, x);
     id.hg = c.h;
     const int j = 2 * (int)(x - c.seg_start) + (lane & 1);
-    if (a.seq_lens[c.r] <= 16 * j) return id;  // (the unit's second page)
     const long long at = (long long)c.r * a.max_pages + j;
-    const int p = a.page_table[at];
+    // (a unit's second page may lie behind the length; both loads at once)
+    const int L = a.seq_lens[c.r], p = j < a.max_pages ? a.page_table[at] : -1;
+    if (L <= 16 * j) return id;
     // the fused check: the tag is compared before the page is fetched
     id.p = p < 0 || p >= a.d.num_pages                                ? -2
            : a.exp_tags == nullptr || a.d.tags[p] == a.exp_tags[at] ? p
                                                                     : -3;
     return id;
   };
-  // batch b into the table; which of its pages must not be read
-  auto fill = [&](int b, const Id& id) {
-    int tile = -1;
-    float ks = 1.0f, vs = 1.0f;
+  // batch b into the table, its tiles and then their scales
+  auto fill_tiles = [&](int b, const Id& id) {
     if (id.p == -2) set_error(a.d.ctl, KV_ERR_BAD_PAGE_ID);
-    if (id.p >= 0) {
-      tile = id.p * Hkv + id.hg * Hs + hw;  // (a cache of 2^31 tiles is 2 TB)
-      ks = a.d.k_scale[tile];
-      vs = a.d.v_scale[tile];
+    const int tile = id.p < 0 ? -1 : id.p * Hkv + id.hg * Hs + hw;  // (2^31 tiles are 2 TB)
+    reinterpret_cast<int*>(table->tile)[32 * (b & 1) + lane] = tile;
+    return tile;
+  };
+  auto fill_scales = [&](int b, int tile) {
+    const float ks = tile < 0 ? 1.0f : a.d.k_scale[tile], vs = tile < 0 ? 1.0f : a.d.v_scale[tile];
+    reinterpret_cast<float*>(table->ks)[32 * (b & 1) + lane] = ks;
+    reinterpret_cast<float*>(table->vs)[32 * (b & 1) + lane] = vs;
+  };
+  // Unit i's copies into stage st: 16 bytes a lane each, a group a unit.
+  const uint64_t policy = l2_evict_first_policy();
+  auto fetch = [&](int i, int st) {
+    if (i < count) {
+      const int2 tl = table->tile[i & 31];
+      const uint32_t dst = ring + st * kStage + 16 * lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int tile = k & 1 ? tl.y : tl.x;
+        if (tile < 0) continue;
+        const uint8_t* src = static_cast<const uint8_t*>(k < 2 ? a.d.k_cache : a.d.v_cache) +
+                             (long long)tile * kE2m1Tile + 16 * lane;
+        copy16(dst + k * kE2m1Tile, src, policy);
+        copy16(dst + k * kE2m1Tile + 512, src + 512, policy);
+        if (lane < 8) copy16(dst + k * kE2m1Tile + 1024, src + 1024, policy);
+      }
     }
-    const int at = 32 * (b & 1) + lane;
-    reinterpret_cast<float*>(table->ks)[at] = ks;
-    reinterpret_cast<float*>(table->vs)[at] = vs;
-    reinterpret_cast<int*>(table->tile)[at] = tile;
-    return __ballot_sync(0xffffffffu, id.p < -1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   uint32_t bad_pages, bad_next;
   Id ids;
   {
     const Id id0 = locate(0), id1 = locate(1);
     ids = locate(2);
-    bad_pages = fill(0, id0);
-    bad_next = fill(1, id1);
+    const int t0 = fill_tiles(0, id0), t1 = fill_tiles(1, id1);
+    bad_pages = __ballot_sync(0xffffffffu, id0.p < -1);
+    bad_next = __ballot_sync(0xffffffffu, id1.p < -1);
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < ST; ++i) fetch(i, i);
+    fill_scales(0, t0);
+    fill_scales(1, t1);
     __syncwarp();
   }
   int batch = 0;
-  // Unit i's copies, into stage st: lane k issues K of page k, lane 2 + k V.
-  auto fetch = [&](int i, int st) {
-    if (i >= count) return;
-    const int2 tl = table->tile[i & 31];
-    if (lane == 0)
-      mbar_arrive_expect_tx(&full[st], ((tl.x >= 0) + (tl.y >= 0)) * 2 * kE2m1Tile);
-    __syncwarp();
-    const int tile = lane & 1 ? tl.y : tl.x;
-    if (lane < 4 && tile >= 0)
-      bulk_g2s(ring + st * kStage + lane * kE2m1Tile,
-               static_cast<const uint8_t*>(lane < 2 ? a.d.k_cache : a.d.v_cache) +
-                   (long long)tile * kE2m1Tile,
-               kE2m1Tile, &full[st], policy);
-  };
-#pragma unroll 1
-  for (int i = 0; i < ST; ++i) fetch(i, i);
 
   Cursor seg = start;
   int done = 0;          // units of the CTA before this piece
-  int i = 0, st = 0;     // the warp's next unit and its stage
-  uint32_t phase = 0;
-  bool gone = false;     // a wait gave up: nothing more is waited for, fetched or computed
+  int i = 0, st = 0;  // the warp's next unit and its stage
   const int G = a.G, T = a.T, R = a.R;
   const float ssl = a.sm_scale_log2;
 
@@ -593,55 +611,43 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
 
     auto units = [&](auto& rows) {
       auto unit = [&](auto edge) {
-        if (!gone) {
-          bool ok = mbar_try_wait(&full[st], phase);
-          if (!ok) ok = mbar_wait(&full[st], phase, abort_flag, a.d.ctl, wait_info(warp, 0, st));
-          gone = !__all_sync(0xffffffffu, ok);
-        }
+        // every lane's copies of the unit have landed
+        asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+        __syncwarp();
         const float2 ks = table->ks[i & 31], vs = table->vs[i & 31];
         E2m1Page pg[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          pg[k].k = ring + st * kStage + k * kE2m1Tile;
-          pg[k].v = pg[k].k + 2 * kE2m1Tile;
+          pg[k].k16 = ring + st * kStage + k * kE2m1Tile + 16 * lane;
+          pg[k].k4 = ring + st * kStage + k * kE2m1Tile + kE2m1Scales + 4 * lane;
           pg[k].ks = k ? ks.y : ks.x;
           pg[k].vs = k ? vs.y : vs.x;
           pg[k].pos0 = pos + 16 * k;
           pg[k].nv = min(16, L - pg[k].pos0);
         }
         pos += 32 * WPH;
-        if (!gone) {
-          if constexpr (decltype(edge)::value) {
-            // (a page behind the length was not fetched)
+        if constexpr (decltype(edge)::value) {
+          // (a page behind the length was not fetched)
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k)
-              if (k == 0 ? pg[0].nv > 0 : pg[1].nv > 0) {
-                const E2m1Page one[1] = {k == 0 ? pg[0] : pg[1]};
-                rows.template pages<1, true>(one);
-              }
-          } else if constexpr (WIDE && KV_E2M1_PAIR16 == 1) {
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 2; ++k)
+            if (k == 0 ? pg[0].nv > 0 : pg[1].nv > 0) {
               const E2m1Page one[1] = {k == 0 ? pg[0] : pg[1]};
-              rows.template pages<1, false>(one);
+              rows.template pages<1, true>(one);
             }
-          } else {
-            rows.template pages<2, false>(pg);
-          }
-          __syncwarp();  // every lane has read its part of the stage
-          fetch(i + ST, st);
+        } else {
+          rows.template pages<2, false>(pg);
         }
+        __syncwarp();  // every lane has read its part of the stage
+        fetch(i + ST, st);
         ++i;
-        if (++st == ST) {
-          st = 0;
-          phase ^= 1u;
-        }
+        if (++st == ST) st = 0;
       };
       while (i < i_end) {
         if ((i >> 4) != batch) {
           ++batch;
           bad_pages = bad_next;
-          bad_next = fill(batch + 1, ids);
+          fill_scales(batch + 1, fill_tiles(batch + 1, ids));
+          bad_next = __ballot_sync(0xffffffffu, ids.p < -1);
           __syncwarp();
           ids = locate(batch + 2);
         }
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
       float acc[16][4];
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-      E2m1Rows16 rows{mA, mB, lA, lB, acc, qs, qsc[0], qsc[1], n0, G, T, L - T};
+      E2m1Rows16 rows{mA, mB, lA, lB, acc, smem_u32(qs) + 16 * lane, qsc[0], qsc[1], n0, G, T, L - T};
       units(rows);
       rows.finish();
 #pragma unroll
@@ -758,7 +764,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
       float acc[8][4];
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-      E2m1Rows8 rows{m0, m1, l0, l1, acc, qs, qsc0, qsc1, G, T, L - T};
+      E2m1Rows8 rows{m0, m1, l0, l1, acc, smem_u32(qs) + 16 * lane, qsc0, qsc1, G, T, L - T};
       units(rows);
       rows.finish();
 #pragma unroll
@@ -779,15 +785,6 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     }
     done += n_piece;
     if (u0 + n_piece == seg.np) cursor_next(seg, pfx, B, HG);
-  }
-  // After a wait gave up, copies already issued may still be landing: wait for
-  // them (bounded) before this CTA's shared memory goes away.
-  if (*abort_flag && lane == 0) {
-    for (int k = 0; k < 2 * ST; ++k) {
-      const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(&full[k % ST], k < ST ? 0u : 1u) && global_ns() - t0 < 100000000ull) {
-      }
-    }
   }
 }
 
