@@ -128,6 +128,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// c += a b (m16n8k16, f16 operands)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 template <int OFFSET>
 __device__ __forceinline__ uint4 lds128_at(uint32_t at) {
   uint4 v;
@@ -196,8 +205,8 @@ struct E2m1Rows8 {
           uint32_t x[4], y[4];
           e2m1x8_scaled(w_of(kg[u], w), s0, s0, x[0], x[1], x[2], x[3]);
           e2m1x8_scaled(w_of(kh[u], w), s1, s1, y[0], y[1], y[2], y[3]);
-          mma16816<true>(s[u], x[0], y[0], x[1], y[1], q.x, q.y);
-          mma16816<true>(sb[u], x[2], y[2], x[3], y[3], q.z, q.w);
+          mma_f16(s[u], x[0], y[0], x[1], y[1], q.x, q.y);
+          mma_f16(sb[u], x[2], y[2], x[3], y[3], q.z, q.w);
         }
       }
 #pragma unroll
@@ -286,7 +295,7 @@ struct E2m1Rows8 {
         for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
           uint32_t a0, a1, a2, a3;
           e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, a0, a1, a2, a3);
-          mma16816<true>(acc[i], a0, a1, a2, a3, c0, c1);
+          mma_f16(acc[i], a0, a1, a2, a3, c0, c1);
         }
       };
       if constexpr (!EDGE) {
@@ -346,10 +355,10 @@ struct E2m1Rows16 {
           uint32_t x[4], y[4];
           e2m1x8_scaled(w_of(kg[u], w), s0, s0, x[0], x[1], x[2], x[3]);
           e2m1x8_scaled(w_of(kh[u], w), s1, s1, y[0], y[1], y[2], y[3]);
-          mma16816<true>(s[u][0], q0.x, q0.y, q0.z, q0.w, x[0], x[1]);
-          mma16816<true>(s[u][1], q0.x, q0.y, q0.z, q0.w, y[0], y[1]);
-          mma16816<true>(s[u][0], q1.x, q1.y, q1.z, q1.w, x[2], x[3]);
-          mma16816<true>(s[u][1], q1.x, q1.y, q1.z, q1.w, y[2], y[3]);
+          mma_f16(s[u][0], q0.x, q0.y, q0.z, q0.w, x[0], x[1]);
+          mma_f16(s[u][1], q0.x, q0.y, q0.z, q0.w, y[0], y[1]);
+          mma_f16(s[u][0], q1.x, q1.y, q1.z, q1.w, x[2], x[3]);
+          mma_f16(s[u][1], q1.x, q1.y, q1.z, q1.w, y[2], y[3]);
         }
       }
     }
@@ -450,8 +459,8 @@ struct E2m1Rows16 {
         for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
           uint32_t b00, b10, b01, b11;
           e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, b00, b10, b01, b11);
-          mma16816<true>(acc[2 * i], a0, a1, a2, a3, b00, b01);
-          mma16816<true>(acc[2 * i + 1], a0, a1, a2, a3, b10, b11);
+          mma_f16(acc[2 * i], a0, a1, a2, a3, b00, b01);
+          mma_f16(acc[2 * i + 1], a0, a1, a2, a3, b10, b11);
         }
       };
       if constexpr (!EDGE) {
@@ -525,22 +534,33 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   struct Id {
     int p, hg;  // page id (-1: none; -2: out of range; -3: a stale tag), head group
   };
+  struct Raw {
+    int L, p, j, r, hg;  // length, page id as loaded, page number, request (-1: no unit)
+  };
   auto locate = [&](int b) {
     const int i = 16 * b + (lane >> 1);
-    Id id{-1, 0};
-    if (i >= count) return id;
-    const long long x = x_begin + lg + WPH * i;
-    const Cursor c = cursor_at(pfx, B, HG, x);
-    id.hg = c.h;
-    const int j = 2 * (int)(x - c.seg_start) + (lane & 1);
-    const long long at = (long long)c.r * a.max_pages + j;
-    // (a unit's second page may lie behind the length; both loads at once)
-    const int L = a.seq_lens[c.r], p = j < a.max_pages ? a.page_table[at] : -1;
-    if (L <= 16 * j) return id;
+    Raw w{0, -1, 0, -1, 0};
+    if (i < count) {
+      const long long x = x_begin + lg + WPH * i;
+      const Cursor c = cursor_at(pfx, B, HG, x);
+      w.r = c.r;
+      w.hg = c.h;
+      w.j = 2 * (int)(x - c.seg_start) + (lane & 1);
+      // (a unit's second page may lie behind the length; both loads at once)
+      w.L = a.seq_lens[c.r];
+      if (w.j < a.max_pages) w.p = a.page_table[(long long)c.r * a.max_pages + w.j];
+    }
+    return w;
+  };
+  auto check = [&](const Raw& w) {
+    Id id{-1, w.hg};
+    if (w.r < 0 || w.L <= 16 * w.j) return id;
     // the fused check: the tag is compared before the page is fetched
-    id.p = p < 0 || p >= a.d.num_pages                                ? -2
-           : a.exp_tags == nullptr || a.d.tags[p] == a.exp_tags[at] ? p
-                                                                    : -3;
+    id.p = w.p < 0 || w.p >= a.d.num_pages ? -2
+           : a.exp_tags == nullptr ||
+                   a.d.tags[w.p] == a.exp_tags[(long long)w.r * a.max_pages + w.j]
+               ? w.p
+               : -3;
     return id;
   };
   // batch b into the table, its tiles and then their scales
@@ -550,10 +570,12 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     reinterpret_cast<int*>(table->tile)[32 * (b & 1) + lane] = tile;
     return tile;
   };
-  auto fill_scales = [&](int b, int tile) {
-    const float ks = tile < 0 ? 1.0f : a.d.k_scale[tile], vs = tile < 0 ? 1.0f : a.d.v_scale[tile];
-    reinterpret_cast<float*>(table->ks)[32 * (b & 1) + lane] = ks;
-    reinterpret_cast<float*>(table->vs)[32 * (b & 1) + lane] = vs;
+  auto load_scales = [&](int tile) {
+    return tile < 0 ? make_float2(1.0f, 1.0f) : make_float2(a.d.k_scale[tile], a.d.v_scale[tile]);
+  };
+  auto fill_scales = [&](int b, float2 sc) {
+    reinterpret_cast<float*>(table->ks)[32 * (b & 1) + lane] = sc.x;
+    reinterpret_cast<float*>(table->vs)[32 * (b & 1) + lane] = sc.y;
   };
   // Unit i's copies into stage st: 16 bytes a lane each, a group a unit.
   const uint64_t policy = l2_evict_first_policy();
@@ -574,19 +596,23 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // (the first units' pages are on their way before anything else is looked up)
   uint32_t bad_pages, bad_next;
-  Id ids;
+  Raw ids;
   {
-    const Id id0 = locate(0), id1 = locate(1);
-    ids = locate(2);
-    const int t0 = fill_tiles(0, id0), t1 = fill_tiles(1, id1);
-    bad_pages = __ballot_sync(0xffffffffu, id0.p < -1);
-    bad_next = __ballot_sync(0xffffffffu, id1.p < -1);
+    const Id id0 = check(locate(0));
+    const int t0 = fill_tiles(0, id0);
     __syncwarp();
 #pragma unroll 1
     for (int i = 0; i < ST; ++i) fetch(i, i);
-    fill_scales(0, t0);
-    fill_scales(1, t1);
+    const float2 s0 = load_scales(t0);
+    const Raw w1 = locate(1);
+    ids = locate(2);
+    fill_scales(0, s0);
+    const Id id1 = check(w1);
+    fill_scales(1, load_scales(fill_tiles(1, id1)));
+    bad_pages = __ballot_sync(0xffffffffu, id0.p < -1);
+    bad_next = __ballot_sync(0xffffffffu, id1.p < -1);
     __syncwarp();
   }
   int batch = 0;
@@ -646,8 +672,9 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
         if ((i >> 4) != batch) {
           ++batch;
           bad_pages = bad_next;
-          fill_scales(batch + 1, fill_tiles(batch + 1, ids));
-          bad_next = __ballot_sync(0xffffffffu, ids.p < -1);
+          const Id id = check(ids);
+          fill_scales(batch + 1, load_scales(fill_tiles(batch + 1, id)));
+          bad_next = __ballot_sync(0xffffffffu, id.p < -1);
           __syncwarp();
           ids = locate(batch + 2);
         }
