@@ -316,30 +316,35 @@ __device__ __noinline__ void key_tile_e2m1(const uint16_t* src, long long stride
     }
   }
   const float inv_s = pow2_inverse(e2m1_tile_scale(block, fresh, scale_slot));
+  const int chunk[2] = {p.c0, p.c1};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int slot = slot0 + i0 + 4 * k;
     if (i0 + 4 * k >= nrows) continue;
+    float f[2];
+    const uint32_t sc = e2m1_group_scales(m[k][0], m[k][1], inv_s * kE2m1Sixth, inv_s, f[0], f[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int chunk = h ? p.c1 : p.c0, g = chunk >> 1;
-      float f;
-      const uint32_t sc = e2m1_group_scale(m[k][h], inv_s, f);
-      uint32_t c[4];
+      const int g = chunk[h] >> 1;
+      const uint64_t ff = pack2(f[h], f[h]);
+      uint64_t v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = e2m1x2(x[k][8 * h + 2 * e] * f, x[k][8 * h + 2 * e + 1] * f);
+      for (int e = 0; e < 4; ++e) v[e] = mul2(pack2(x[k][8 * h + 2 * e], x[k][8 * h + 2 * e + 1]), ff);
       *reinterpret_cast<uint32_t*>(dst + 64 * slot + 16 * (g & 3) + 8 * (g >> 2) +
-                                   4 * (chunk & 1)) =
-          c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-      if ((chunk & 1) == 0)
-        dst[kE2m1Scales + 16 * (slot & 7) + 4 * (g & 3) + 2 * (slot >> 3) + (g >> 2)] = (uint8_t)sc;
+                                   4 * (chunk[h] & 1)) = e2m1x8(v[0], v[1], v[2], v[3]);
+      if ((chunk[h] & 1) == 0)
+        dst[kE2m1Scales + 16 * (slot & 7) + 4 * (g & 3) + 2 * (slot >> 3) + (g >> 2)] =
+            (uint8_t)(sc >> (8 * h));
     }
   }
 }
 __device__ __noinline__ void value_tile_e2m1(const uint16_t* src, long long stride, int nrows,
                                              int slot0, bool fresh, float* scale_slot,
                                              uint8_t* dst) {
-  e2m1_v_tile(src, stride, nrows, slot0, fresh, scale_slot, dst);
+  if (nrows == 16)
+    e2m1_v_tile<true>(GlobalRows{src, stride}, 16, 0, true, scale_slot, dst);
+  else
+    e2m1_v_tile<false>(GlobalRows{src, stride}, nrows, slot0, fresh, scale_slot, dst);
 }
 
 // Query heads [h0, h1) of the page's tokens.  A thread keeps one unit of one
