@@ -137,6 +137,8 @@ def _ptr(t, dtype=None, name="tensor"):
     """Device pointer of a contiguous CUDA tensor (None -> NULL)."""
     if t is None:
         return None
+    if type(t) is _Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()  # (a call of a few microseconds: the common case first)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     allowed = dtype if isinstance(dtype, tuple) else (dtype,)
@@ -204,7 +206,7 @@ def _stream_on(stream, dev):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

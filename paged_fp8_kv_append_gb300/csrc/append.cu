@@ -83,6 +83,8 @@ __device__ void mark_unserved(const AppendArgs& a, int stop) {
 // request, so at most half full).
 constexpr int kPartialSlots = 2 * kPlanThreads;
 
+constexpr int kPopAhead = 4;  // free-list entries a thread has in flight
+
 __device__ __forceinline__ int partial_slot(int p) {
   return (int)(((uint32_t)p * 2654435761u) >> 21) & (kPartialSlots - 1);
 }
@@ -178,16 +180,29 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
     // every entry the chunk would pop, all threads at once: the first one
     // that is not a page id marks its request; one that is the partly filled
     // page of a later request fails that request's tag check
-    for (long long g = threadIdx.x; g < chunk_total && pool0 + g < d.num_pages; g += kPlanThreads) {
-      const int p = d.free_list[pool0 + g];
-      if (p < 0 || p >= d.num_pages) {
-        atomicMin(reinterpret_cast<unsigned long long*>(&s_badg), (unsigned long long)g);
-        continue;
+    // (kPopAhead entries a thread in flight: a handoff pops thousands of pages)
+    const long long listed = min(chunk_total, d.num_pages - pool0);
+    for (long long g0 = threadIdx.x; g0 < listed; g0 += kPopAhead * kPlanThreads) {
+      int pop[kPopAhead];
+#pragma unroll
+      for (int u = 0; u < kPopAhead; ++u) {
+        const long long g = g0 + u * kPlanThreads;
+        pop[u] = g < listed ? d.free_list[pool0 + g] : 0;
       }
-      for (int h = partial_slot(p); s_pkey[h] != -1; h = (h + 1) & (kPartialSlots - 1)) {
-        if (s_pkey[h] == p) {
-          const int rr = s_preq[h];
-          if (owner_of(s_incl, nreq, g) < rr) s_tagfail[rr] = 1;
+#pragma unroll
+      for (int u = 0; u < kPopAhead; ++u) {
+        const long long g = g0 + u * kPlanThreads;
+        const int p = pop[u];
+        if (g >= listed) break;
+        if (p < 0 || p >= d.num_pages) {
+          atomicMin(reinterpret_cast<unsigned long long*>(&s_badg), (unsigned long long)g);
+          continue;
+        }
+        for (int h = partial_slot(p); s_pkey[h] != -1; h = (h + 1) & (kPartialSlots - 1)) {
+          if (s_pkey[h] == p) {
+            const int rr = s_preq[h];
+            if (owner_of(s_incl, nreq, g) < rr) s_tagfail[rr] = 1;
+          }
         }
       }
     }
@@ -206,14 +221,28 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
     const int si = chunk_stop - base;
     const long long served =
         chunk_stop < a.B ? (si > 0 ? s_incl[si - 1] : 0) : chunk_total;
-    for (long long g = threadIdx.x; g < served; g += kPlanThreads) {
-      const int i = owner_of(s_incl, nreq, g);
-      const long long j = s_first[i] + g - (i > 0 ? s_incl[i - 1] : 0);
-      const int p = d.free_list[pool0 + g];
-      const uint32_t t = d.tags[p] + 1u;  // wraps mod 2^32
-      d.tags[p] = t;
-      a.page_table[(long long)(base + i) * a.max_pages + j] = p;
-      a.exp_tags[(long long)(base + i) * a.max_pages + j] = t;
+    // (a handoff into a 4-bit pool: its data kernel takes them, on all SMs)
+    for (long long g0 = a.defer_pops ? served : threadIdx.x; g0 < served;
+         g0 += kPopAhead * kPlanThreads) {
+      int pop[kPopAhead];
+      uint32_t tag[kPopAhead];
+#pragma unroll
+      for (int u = 0; u < kPopAhead; ++u) {
+        const long long g = g0 + u * kPlanThreads;
+        pop[u] = g < served ? d.free_list[pool0 + g] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kPopAhead; ++u) tag[u] = pop[u] >= 0 ? d.tags[pop[u]] + 1u : 0u;  // wraps mod 2^32
+#pragma unroll
+      for (int u = 0; u < kPopAhead; ++u) {
+        const long long g = g0 + u * kPlanThreads;
+        if (g >= served) break;
+        const int i = owner_of(s_incl, nreq, g);
+        const long long j = s_first[i] + g - (i > 0 ? s_incl[i - 1] : 0);
+        d.tags[pop[u]] = tag[u];
+        a.page_table[(long long)(base + i) * a.max_pages + j] = pop[u];
+        a.exp_tags[(long long)(base + i) * a.max_pages + j] = tag[u];
+      }
     }
     if (r < a.B && r < chunk_stop) a.seq_lens[r] = (int32_t)(L + n);
     consumed += served;
@@ -1205,7 +1234,9 @@ cudaError_t launch_append_plan(const AppendArgs& a, cudaStream_t s, int* launche
 
 bool append_tile_fits(const kv_pool_desc& d) { return gqa_tile_fits(d); }
 
-cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches) {
+cudaError_t launch_append(const AppendArgs& given, cudaStream_t s, int* launches) {
+  AppendArgs a = given;
+  a.defer_pops = a.from_pool && a.d.dtype == KV_DTYPE_E2M1;
   cudaError_t e = launch_append_plan(a, s, launches);
   if (e != cudaSuccess) return e;
   // pages a request can touch in one call: ceil((max_new + P - 1) / P)

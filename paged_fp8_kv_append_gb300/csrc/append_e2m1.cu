@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_e2m1_bulk_kernel(const
   const int B = min(a.B, (int)d.ctl[KV_CTL_APPEND_STOP]);
   const int pages = B > 0 ? bulk_items_prefix(a, B, 1, pre, wsum) : 0;
   __syncthreads();
+  const long long head0 = (long long)d.ctl[KV_CTL_FREE_HEAD] - pages;  // of a handoff's pops
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kTileBytes);
   const int H = d.num_kv_heads;
   const long long tiles = 2LL * H * pages, step = (long long)gridDim.x * kWarps;
@@ -138,7 +139,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_e2m1_bulk_kernel(const
       const long long lo = max(jp * 16, L0), hi = min((jp + 1) * 16, Lnew);
       const long long row0 = FROM_POOL ? 0 : a.new_indptr[r] + (lo - L0);
       const long long at = (long long)r * a.max_pages + jp;
-      const int p = a.page_table[at];
+      // a handoff's pages are popped here (a.defer_pops): every request was empty, so the
+      // touched pages, in order, are the popped ones
+      const int p = FROM_POOL ? d.free_list[head0 + page] : a.page_table[at];
       const int sp = FROM_POOL ? a.src_page_table[(long long)r * a.src_max_pages + jp] : 0;
       m.fresh = jp * 16 >= L0;  // popped by this call
       m.is_v = t & 1;
@@ -149,6 +152,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_e2m1_bulk_kernel(const
                 ((long long)sp * H + h) * 2048;
       else
         m.src = (m.is_v ? a.v_new : a.k_new) + (row0 * H + h) * 128;
+      if (FROM_POOL && t == 0 && p >= 0 && p < d.num_pages) {  // (each page once)
+        const uint32_t tag = d.tags[p] + 1u;  // wraps mod 2^32
+        d.tags[p] = tag;
+        a.page_table[at] = p;
+        a.exp_tags[at] = tag;
+      }
       if (p < 0 || p >= d.num_pages || (FROM_POOL && (sp < 0 || sp >= a.src.num_pages)))
         set_error(d.ctl, KV_ERR_BAD_PAGE_ID);
       // a partly filled page that this call's pops handed to a later request is

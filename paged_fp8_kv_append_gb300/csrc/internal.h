@@ -118,6 +118,9 @@ struct AppendArgs {
   const int32_t* src_page_table;
   int32_t src_max_pages;
   const int32_t* src_lens;
+  // the plan moves the free head and the lengths only; popped pages are tagged and
+  // mapped by the data kernel (a handoff, where no page is partly filled)
+  bool defer_pops = false;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s, int* launches);
 // the plan kernel alone (pages popped, tags stamped, lengths advanced), for

@@ -154,66 +154,68 @@ __device__ __forceinline__ Request request(const ReadArgs& a, int r) {
 }
 
 // A head's 4-bit tiles of K and V by one warp.  A value has six significant bits (e2m1.cuh), so
-// its bf16 value is exact.
-__device__ __forceinline__ uint32_t values2(uint32_t codes, float s) {  // the two codes of a byte
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes & 0xFFu), __NV_E2M1);
-  const float2 f = __half22float2(__half2(h));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-  return *reinterpret_cast<const uint32_t*>(&b);
+// its bf16 value is exact.  The tiles are staged in shared memory: the loops then hold few
+// registers, and many pages are in flight on an SM.
+__device__ __forceinline__ float2 e2m1_pair(uint32_t codes) {  // the two codes of a byte
+  return __half22float2(
+      __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes & 0xFFu), __NV_E2M1)));
 }
 __device__ __forceinline__ float e4m3_value(uint32_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(c & 0xFFu), __NV_E4M3)));
 }
-__device__ __forceinline__ void read_head_e2m1(const uint8_t* ksrc, const uint8_t* vsrc, float ks,
-                                               float vs, int slot0, int nrows, uint16_t* kdst,
-                                               uint16_t* vdst, long long stride) {
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ void read_head_e2m1(uint8_t* stage, const uint8_t* ksrc,
+                                               const uint8_t* vsrc, const float* ks_at,
+                                               const float* vs_at, int slot0, int nrows,
+                                               uint16_t* kdst, uint16_t* vdst, long long stride) {
   const int lane = threadIdx.x & 31;
-  // K: dims 8 (lane % 16) .. + 7 of slots 2 i + lane / 16
+  constexpr int kChunks = kE2m1Tile / 16;
+  __syncwarp();  // the last head's reads
+  for (int c = lane; c < 2 * kChunks; c += 32)
+    reinterpret_cast<uint4*>(stage)[c] =
+        __ldcs(reinterpret_cast<const uint4*>(c < kChunks ? ksrc : vsrc - kE2m1Tile) + c);
+  const float ks = *ks_at, vs = *vs_at;
+  __syncwarp();
+  // K: dims 8 (lane % 16) .. + 7 of two slots at a time
   const int ck = (lane & 15) >> 1, at = 16 * (ck & 3) + 8 * (ck >> 2) + 4 * (lane & 1);
-  uint32_t k[8], kc[8];
+#pragma unroll 2
+  for (int i = lane >> 4; i < nrows; i += 2) {
+    const int slot = slot0 + i;
+    const uint32_t k = *reinterpret_cast<const uint32_t*>(stage + 64 * slot + at);
+    const float s = e4m3_value(stage[kE2m1Scales + 16 * (slot & 7) + 4 * (ck & 3) + 2 * (slot >> 3) +
+                                     (ck >> 2)]) * ks;
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int slot = 2 * i + (lane >> 4);
-    k[i] = __ldg(reinterpret_cast<const uint32_t*>(ksrc + 64 * slot + at));
-    kc[i] = __ldg(ksrc + kE2m1Scales + 16 * (slot & 7) + 4 * (ck & 3) + 2 * (slot >> 3) + (ck >> 2));
-  }
-  // V: dims 4 lane .. + 3 of every slot; w[t]: slots 2t, 2t + 1, 2t + 8, 2t + 9
-  const int j = lane & 3, cv = lane >> 2;
-  uint2 w[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    w[t] = __ldg(reinterpret_cast<const uint2*>(vsrc + 512 * (j >> 1) + 64 * cv + 16 * t +
-                                                8 * (j & 1)));
-  const uint4 vc = __ldg(reinterpret_cast<const uint4*>(vsrc + kE2m1Scales + 16 * cv));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 2 * i + (lane >> 4) - slot0;
-    const float s = e4m3_value(kc[i]) * ks;
-    if (r >= 0 && r < nrows)
-      __stcs(reinterpret_cast<uint4*>(kdst + r * stride + 8 * (lane & 15)),
-             make_uint4(values2(k[i], s), values2(k[i] >> 8, s), values2(k[i] >> 16, s),
-                        values2(k[i] >> 24, s)));
-  }
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {  // slots i and i + 1: the halves of a byte
-    const int t = (i & 7) >> 1, b = 2 * (i >> 3), r = i - slot0;  // bytes b, b + 1 of both words
-    const uint32_t cs = (t == 0 ? vc.x : t == 1 ? vc.y : t == 2 ? vc.z : vc.w) >> (8 * b);
-    const float s0 = e4m3_value(cs) * vs, s1 = e4m3_value(cs >> 8) * vs;
-    float2 f[4];
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const uint32_t c = ((d < 2 ? w[t].x : w[t].y) >> (8 * (b + (d & 1)))) & 0xFFu;
-      f[d] = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)c, __NV_E2M1)));
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = e2m1_pair(k >> (8 * e));
+      w[e] = bf16_pair(f.x * s, f.y * s);
     }
+    __stcs(reinterpret_cast<uint4*>(kdst + i * stride + 8 * (lane & 15)),
+           make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  // V: dims 4 lane .. + 3; a word pair holds slots 2t, 2t + 1, 2t + 8, 2t + 9
+  const int j = lane & 3, cv = lane >> 2;
+  const uint8_t* v = stage + kE2m1Tile;
+#pragma unroll 1
+  for (int t = 0; t < 4; ++t) {
+    const uint2 w = *reinterpret_cast<const uint2*>(v + 512 * (j >> 1) + 64 * cv + 16 * t + 8 * (j & 1));
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(v + kE2m1Scales + 16 * cv + 4 * t);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float s = u ? s1 : s0;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn((u ? f[0].y : f[0].x) * s, (u ? f[1].y : f[1].x) * s);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn((u ? f[2].y : f[2].x) * s, (u ? f[3].y : f[3].x) * s);
-      if (r + u >= 0 && r + u < nrows)
-        __stcs(reinterpret_cast<uint2*>(vdst + (r + u) * stride + 4 * lane),
-               make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                          *reinterpret_cast<const uint32_t*>(&hi)));
+    for (int hi = 0; hi < 2; ++hi) {
+      const uint32_t a = w.x >> (16 * hi), b = w.y >> (16 * hi);  // dims 0, 1 and 2, 3
+      const float2 f0 = e2m1_pair(a), f1 = e2m1_pair(a >> 8), f2 = e2m1_pair(b), f3 = e2m1_pair(b >> 8);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float s = e4m3_value(sc >> (16 * hi + 8 * u)) * vs;
+        const int i = 2 * t + 8 * hi + u - slot0;
+        if (i >= 0 && i < nrows)
+          __stcs(reinterpret_cast<uint2*>(vdst + i * stride + 4 * lane),
+                 u ? make_uint2(bf16_pair(f0.y * s, f1.y * s), bf16_pair(f2.y * s, f3.y * s))
+                   : make_uint2(bf16_pair(f0.x * s, f1.x * s), bf16_pair(f2.x * s, f3.x * s)));
+      }
     }
   }
 }
@@ -224,7 +226,7 @@ enum Shape { kTile16x128, kLatent, kE2m1, kAny };
 // SM read the 16 x 128 tiles back at 6.3 TB/s, 4 (3) at 6.0, 2 at 6.1 (bytes
 // read and written, 32 requests of 4k to 32k rows, 8 heads).
 template <bool FP8, int SHAPE>
-__global__ void __launch_bounds__(kThreads, SHAPE == kLatent || SHAPE == kE2m1 ? 2 : FP8 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, SHAPE == kLatent ? 2 : SHAPE == kE2m1 ? 7 : FP8 ? 3 : 2)
     read_rows_kernel(const ReadArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -267,10 +269,12 @@ __global__ void __launch_bounds__(kThreads, SHAPE == kLatent || SHAPE == kE2m1 ?
     else
       read_rows_of<FP8, 0, 2>(src, s, nrows, Dk, dst, Dk, threadIdx.x, kThreads);
   } else if (SHAPE == kE2m1) {
+    __shared__ __align__(16) uint8_t stages[SHAPE == kE2m1 ? kThreads / 32 : 1][2 * kE2m1Tile];
     for (int h = warp; h < H; h += kThreads / 32) {
       const long long ph = (long long)p * H + h, at = (row * H + h) * 128;
-      read_head_e2m1(kc + ph * kE2m1Tile, vc + ph * kE2m1Tile, d.k_scale[ph], d.v_scale[ph], slot0,
-                     nrows, a.k_out + at, a.v_out + at, H * 128ll);
+      read_head_e2m1(stages[warp % (sizeof(stages) / sizeof(stages[0]))], kc + ph * kE2m1Tile,
+                     vc + ph * kE2m1Tile, d.k_scale + ph, d.v_scale + ph, slot0, nrows,
+                     a.k_out + at, a.v_out + at, H * 128ll);
     }
   } else if (SHAPE == kTile16x128) {
     for (int h = warp; h < H; h += kThreads / 32) {
