@@ -77,7 +77,10 @@ struct E2m1Cfg {
 };
 
 constexpr float kUnset = -1e38f;  // the reference of a row that has seen no position
-constexpr float kSlack = 8.0f;
+// A reference is set 2^kBelow below the row's largest weight, and moved when a weight exceeds it
+// by more than 2^kSlack: f16 then keeps its 11 bits for weights down to 2^-20 of the largest
+// (2^-14 without the distance), and none passes its 65504.
+constexpr float kBelow = 6.0f, kSlack = 15.0f;
 
 struct FalseType {
   static constexpr bool value = false;
@@ -119,6 +122,19 @@ __device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
 __device__ __forceinline__ uint32_t e2m1_token_mask(int nv, int t) {
   const int a = min(max(nv - 2 * t, 0), 2), b = min(max(nv - 8 - 2 * t, 0), 2);
   return ((1u << (8 * a)) - 1u) | (((1u << (8 * b)) - 1u) << 16);
+}
+// The first slot whose scale byte (of the lane's group, tokens as above) is NaN, over the group's
+// four lanes; 16: none.  NaN bytes become 0.
+__device__ __forceinline__ int e2m1_first_nan(uint32_t& scales, int t) {
+  int first = 16;
+#pragma unroll
+  for (int k = 3; k >= 0; --k)
+    if ((scales >> (8 * k) & 0x7Fu) == 0x7Fu) {
+      first = min(first, 2 * t + (k & 1) + 8 * (k >> 1));
+      scales &= ~(0xFFu << (8 * k));
+    }
+  first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+  return min(first, __shfl_xor_sync(0xffffffffu, first, 2));
 }
 // The 8 x 8 f16 matrix that the warp holds two to a lane (lane 4 r + c: row r,
 // columns 2c and 2c + 1), transposed.
@@ -253,8 +269,8 @@ struct E2m1Rows8 {
         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
         n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
       }
-      n0 = fmaxf(n0, m0);
-      n1 = fmaxf(n1, m1);
+      n0 = fmaxf(n0 - kBelow, m0);
+      n1 = fmaxf(n1 - kBelow, m1);
       const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
       m0 = n0;
       m1 = n1;
@@ -301,14 +317,19 @@ struct E2m1Rows8 {
       if constexpr (!EDGE) {
         add(sw, b0, b1);
       } else {
-        // A scale of NaN (a value that was not finite; or stale bytes behind the
-        // length) times a weight of zero is NaN: a query token's rows are added
-        // over the tokens that it sees alone.
-        const int mine = min(g / G, T - 1);
-#pragma unroll 1
-        for (int tq = 0; tq < T; ++tq) {
-          const uint32_t on = mine == tq ? 0xFFFFFFFFu : 0u;
-          add(sw & e2m1_token_mask(min(pg[u].nv, seen0 + tq - pg[u].pos0 + 1), t), b0 & on, b1 & on);
+        // A scale of NaN (a value that was not finite) times a weight of zero is NaN: it
+        // is left out of the product, and reaches the rows that see its token.
+        uint32_t clean = sw & e2m1_token_mask(pg[u].nv, t);
+        const int first = e2m1_first_nan(clean, t);
+        add(clean, b0, b1);
+        if (__any_sync(0xffffffffu, first < 16)) {
+          const bool x0 = first < 16 && pg[u].pos0 + first <= seen0 + min(2 * t / G, T - 1);
+          const bool x1 = first < 16 && pg[u].pos0 + first <= seen0 + min((2 * t + 1) / G, T - 1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (x0) acc[i][0] = acc[i][2] = __int_as_float(0x7FFFFFFF);
+            if (x1) acc[i][1] = acc[i][3] = __int_as_float(0x7FFFFFFF);
+          }
         }
       }
     }
@@ -411,8 +432,8 @@ struct E2m1Rows16 {
         nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, o));
         nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, o));
       }
-      nA = fmaxf(nA, mA);
-      nB = fmaxf(nB, mB);
+      nA = fmaxf(nA - kBelow, mA);
+      nB = fmaxf(nB - kBelow, mB);
       const float aA = fast_exp2(mA - nA), aB = fast_exp2(mB - nB);
       mA = nA;
       mB = nB;
@@ -466,12 +487,22 @@ struct E2m1Rows16 {
       if constexpr (!EDGE) {
         add(sw, pa[u][0], pa[u][1], pa[u][2], pa[u][3]);
       } else {  // (as for 8 rows)
-        const int tA = min((n0 + g) / G, T - 1), tB = min((n0 + g + 8) / G, T - 1);
-#pragma unroll 1
-        for (int tq = min(n0 / G, T - 1); tq <= min((n0 + 15) / G, T - 1); ++tq) {
-          const uint32_t onA = tA == tq ? 0xFFFFFFFFu : 0u, onB = tB == tq ? 0xFFFFFFFFu : 0u;
-          add(sw & e2m1_token_mask(min(pg[u].nv, seen0 + tq - pg[u].pos0 + 1), t), pa[u][0] & onA,
-              pa[u][1] & onB, pa[u][2] & onA, pa[u][3] & onB);
+        uint32_t clean = sw & e2m1_token_mask(pg[u].nv, t);
+        const int first = e2m1_first_nan(clean, t);  // of group g
+        add(clean, pa[u][0], pa[u][1], pa[u][2], pa[u][3]);
+        if (__any_sync(0xffffffffu, first < 16)) {
+          // columns 2t, 2t + 1 of every tile: groups 2t and 2t + 1
+          const int f0 = __shfl_sync(0xffffffffu, first, 8 * t);
+          const int f1 = __shfl_sync(0xffffffffu, first, 8 * t + 4);
+          const int limA = seen0 + min((n0 + g) / G, T - 1) - pg[u].pos0;
+          const int limB = seen0 + min((n0 + g + 8) / G, T - 1) - pg[u].pos0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (f0 < 16 && f0 <= limA) acc[i][0] = __int_as_float(0x7FFFFFFF);
+            if (f1 < 16 && f1 <= limA) acc[i][1] = __int_as_float(0x7FFFFFFF);
+            if (f0 < 16 && f0 <= limB) acc[i][2] = __int_as_float(0x7FFFFFFF);
+            if (f1 < 16 && f1 <= limB) acc[i][3] = __int_as_float(0x7FFFFFFF);
+          }
         }
       }
     }

@@ -45,6 +45,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kAhead = 4;   // query units a thread has in flight
+constexpr int kDepth = 6;  // the same where they come through shared memory
 
 // A frequency as the table holds it: turns per position in units of 2^-64,
 // whole turns dropped.
@@ -71,14 +72,23 @@ __device__ __forceinline__ UnitPlace unit_place(int j, int rot16, int upr) {
   return u;
 }
 
+// Where 16 bytes (two pairs' sines and cosines) of a token's row lie in it.  Neighbouring units
+// read 64 bytes each, and in order eight of them meet in two groups of banks: where every head's
+// unit reads them anew (NORM) they are spread; elsewhere the addresses would cost registers.
+template <bool NORM>
+__device__ __forceinline__ int angle_chunk(int k) {
+  return NORM ? (k & ~3) | ((k ^ (k >> 3)) & 3) : k;
+}
+
 // (cos, sin) of a unit's 8 pairs from its token's row of them
-template <bool IL>
+template <bool IL, bool NORM>
 __device__ __forceinline__ void unit_angles(const float2* row, int j, int rot16, float2 (&c)[8]) {
-  const float4* a = reinterpret_cast<const float4*>(row + (IL ? 4 : 8) * j);
-  const float4* b = IL ? reinterpret_cast<const float4*>(row + 4 * (j + rot16)) : a + 2;
+  const float4* a = reinterpret_cast<const float4*>(row + (NORM ? 0 : (IL ? 4 : 8) * j));
+  const float4* b = NORM ? a : IL ? reinterpret_cast<const float4*>(row + 4 * (j + rot16)) : a + 2;
+  const int k0 = NORM ? (IL ? 2 : 4) * j : 0, k1 = NORM ? (IL ? 2 * (j + rot16) : k0 + 2) : 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float4 t = k < 2 ? a[k] : b[k - 2];
+    const float4 t = k < 2 ? a[angle_chunk<NORM>(k0 + k)] : b[angle_chunk<NORM>(k1 + k - 2)];
     c[2 * k] = make_float2(t.x, t.y);
     c[2 * k + 1] = make_float2(t.z, t.w);
   }
@@ -87,7 +97,8 @@ __device__ __forceinline__ void unit_angles(const float2* row, int j, int rot16,
 // A head's norm: y = x / sqrt(mean(x^2) + eps) * weight, as a thread applies it to its unit.
 // The sum runs over the upr neighbouring lanes of the row (a power of two), in fp32.
 struct UnitNorm {
-  uint4 w0, w1;  // bf16 weights of the chunks c0 and c1
+  const uint4 *w0, *w1;  // bf16 weights of the chunks c0 and c1 (read at each use: they stay in
+                         // the L1, and registers are what a key page lacks)
   float eps, inv_d;
   uint32_t lanes;  // the row's lanes
   int upr;
@@ -99,8 +110,8 @@ __device__ __forceinline__ UnitNorm unit_norm(const uint16_t* weight, float eps,
   UnitNorm n;
   n.on = NORM && weight != nullptr;
   if (!n.on) return n;
-  n.w0 = __ldg(reinterpret_cast<const uint4*>(weight) + p.c0);
-  n.w1 = __ldg(reinterpret_cast<const uint4*>(weight) + p.c1);
+  n.w0 = reinterpret_cast<const uint4*>(weight) + p.c0;
+  n.w1 = reinterpret_cast<const uint4*>(weight) + p.c1;
   n.eps = eps;
   n.inv_d = 1.0f / D;  // exact
   n.upr = D / 16;
@@ -125,7 +136,8 @@ __device__ __forceinline__ void unit_turn(uint4 a, uint4 b, bool turn, const flo
     for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
     for (int o = 1; o < n.upr; o <<= 1) ss += __shfl_xor_sync(n.lanes, ss, o);
     const float r = rsqrtf(fmaf(ss, n.inv_d, n.eps));
-    const uint32_t g[8] = {n.w0.x, n.w0.y, n.w0.z, n.w0.w, n.w1.x, n.w1.y, n.w1.z, n.w1.w};
+    const uint4 w0 = __ldg(n.w0), w1 = __ldg(n.w1);
+    const uint32_t g[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       x[2 * k] = x[2 * k] * r * bf16_lo(g[k]);
@@ -169,6 +181,21 @@ __device__ __forceinline__ uint2 codes8_fresh(const float* x, float s, float rs)
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// A thread's slots in shared memory for normalised heads of 128: 32 bytes each, 16 of a unit's
+// first chunk and 16 of its second.
+constexpr uint32_t kHalfSlot = 16 * kThreads, kSlot = 2 * kHalfSlot;
+__device__ __forceinline__ void copy16(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 take16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // One (page, kv head) key tile by one warp: `nrows` rows from slot0 on; any
 // shape, page and scale, a unit at a time (kept out of line: a fresh page's
 // code stays small, and nothing of it lives across this call).
@@ -206,7 +233,7 @@ __device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride,
       const uint4* row = reinterpret_cast<const uint4*>(src + i * stride);
       float2 c[8];
       float x[16];
-      if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+      if (p.turn) unit_angles<IL, NORM>(cs + i * rot16 * 8, j, rot16, c);
       unit_turn<IL, NORM>(row[p.c0], row[p.c1], p.turn, c, unit_norm<NORM>(weight, eps, D, p), x);
       if (pass == 0) {
 #pragma unroll
@@ -229,10 +256,10 @@ __device__ __noinline__ void key_tile_any(const uint16_t* src, long long stride,
 
 // The same for a whole fresh page of 16 x 128 keys: its loads are issued
 // together and its turned values stay in registers.
-template <bool IL, bool NORM>
+template <bool IL>
 __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long stride, int rot16,
-                                                const float2* cs, const uint16_t* weight, float eps,
-                                                bool fp8, float* scale_slot, uint8_t* dst) {
+                                                const float2* cs, bool fp8, float* scale_slot,
+                                                uint8_t* dst) {
   const int lane = threadIdx.x & 31, j = lane & 7, i0 = lane >> 3;  // rows i0 + 4 k
   const UnitPlace p = unit_place(j, rot16, 8);
   uint4 raw[4][2];
@@ -242,14 +269,14 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
     raw[k][0] = __ldcs(row + p.c0);
     raw[k][1] = __ldcs(row + p.c1);
   }
-  const UnitNorm norm = unit_norm<NORM>(weight, eps, 128, p);
+  const UnitNorm none = unit_norm<false>(nullptr, 0.0f, 128, p);
   float x[4][16];
   float m = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float2 c[8];
-    if (p.turn) unit_angles<IL>(cs + (i0 + 4 * k) * rot16 * 8, j, rot16, c);
-    unit_turn<IL, NORM>(raw[k][0], raw[k][1], p.turn, c, norm, x[k]);
+    if (p.turn) unit_angles<IL, false>(cs + (i0 + 4 * k) * rot16 * 8, j, rot16, c);
+    unit_turn<IL, false>(raw[k][0], raw[k][1], p.turn, c, none, x[k]);
 #pragma unroll
     for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[k][e]));
   }
@@ -264,8 +291,8 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
   }
   const float s = scale_from_amax(warp_max(m)), rs = __frcp_rn(s);
   if (!scale_fast_ok(s)) {
-    key_tile_any<IL, NORM>(src, stride, 16, 128, rot16, cs, weight, eps, true, true, false,
-                           scale_slot, dst, 0);
+    key_tile_any<IL, false>(src, stride, 16, 128, rot16, cs, nullptr, 0.0f, true, true, false,
+                            scale_slot, dst, 0);
     return;
   }
   if (lane == 0) *scale_slot = s;
@@ -274,6 +301,62 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
     uint2* o = reinterpret_cast<uint2*>(dst + (i0 + 4 * k) * 128);
     o[p.c0] = codes8_fresh(x[k], s, rs);
     o[p.c1] = codes8_fresh(x[k] + 8, s, rs);
+  }
+}
+
+// The same of keys that are normalised too: with the weights their values do not fit the
+// registers, and what spills finds little of the L1 beside the queries' slots (180 us for 8
+// prompts became 205 with more of either).  So the rows wait in the thread's slots, and are
+// normalised and turned once for the scale and once for the codes.
+template <bool IL>
+__device__ __noinline__ void key_page_norm_16x128(const uint16_t* src, long long stride, int rot16,
+                                                  const float2* cs, uint32_t slots,
+                                                  const uint16_t* weight, float eps, bool fp8,
+                                                  float* scale_slot, uint8_t* dst) {
+  const int lane = threadIdx.x & 31, j = lane & 7, i0 = lane >> 3;  // rows i0 + 4 k
+  const UnitPlace p = unit_place(j, rot16, 8);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4* row = reinterpret_cast<const uint4*>(src + (i0 + 4 * k) * stride);
+    copy16(slots + k * kSlot, row + p.c0);
+    copy16(slots + k * kSlot + kHalfSlot, row + p.c1);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  const UnitNorm norm = unit_norm<true>(weight, eps, 128, p);
+  auto turned = [&](int k, float (&y)[16]) {
+    float2 c[8];
+    if (p.turn) unit_angles<IL, true>(cs + (i0 + 4 * k) * rot16 * 8, j, rot16, c);
+    unit_turn<IL, true>(take16(slots + k * kSlot), take16(slots + k * kSlot + kHalfSlot), p.turn, c,
+                        norm, y);
+  };
+  float m = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    float y[16];
+    turned(k, y);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(y[e]));
+    if (!fp8) {
+      uint4* o = reinterpret_cast<uint4*>(dst + (i0 + 4 * k) * 256);
+      o[p.c0] = pack8_bf16(y);
+      o[p.c1] = pack8_bf16(y + 8);
+    }
+  }
+  if (!fp8) return;
+  const float s = scale_from_amax(warp_max(m)), rs = __frcp_rn(s);
+  if (lane == 0) *scale_slot = s;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    float y[16];
+    turned(k, y);
+    uint2* o = reinterpret_cast<uint2*>(dst + (i0 + 4 * k) * 128);
+    if (scale_fast_ok(s)) {
+      o[p.c0] = codes8_fresh(y, s, rs);
+      o[p.c1] = codes8_fresh(y + 8, s, rs);
+    } else {
+      o[p.c0] = codes8(y, s, rs);
+      o[p.c1] = codes8(y + 8, s, rs);
+    }
   }
 }
 
@@ -300,7 +383,7 @@ __device__ __noinline__ void key_tile_e2m1(const uint16_t* src, long long stride
     const bool ok = i < nrows;
     const uint4* row = reinterpret_cast<const uint4*>(src + (ok ? i : 0) * stride);
     float2 c[8];
-    if (p.turn) unit_angles<IL>(cs + (ok ? i : 0) * rot16 * 8, j, rot16, c);
+    if (p.turn) unit_angles<IL, NORM>(cs + (ok ? i : 0) * rot16 * 8, j, rot16, c);
     unit_turn<IL, NORM>(row[p.c0], row[p.c1], p.turn, c, norm, x[k]);
     uint32_t b[2] = {0, 0};  // bit patterns: a NaN is the largest
 #pragma unroll
@@ -359,21 +442,22 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
   if (g >= groups || i >= nrows) return;
   const UnitPlace p = unit_place(j, rot16, upr);
   float2 c[8];
-  if (p.turn) unit_angles<IL>(cs + i * rot16 * 8, j, rot16, c);
+  if (p.turn) unit_angles<IL, NORM>(cs + i * rot16 * 8, j, rot16, c);
   const UnitNorm norm = unit_norm<NORM>(a.q_norm, a.norm_eps, D, p);
   const uint16_t* q = a.q + (row0 + i) * a.q_stride;
   uint16_t* out = a.q_out + (row0 + i) * a.Hq * D;
-  for (int h = h0 + g - i * hs; h < h1; h += kAhead * hs) {
-    uint4 r[kAhead][2];
+  constexpr int kQ = kAhead;
+  for (int h = h0 + g - i * hs; h < h1; h += kQ * hs) {
+    uint4 r[kQ][2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kQ; ++k)
       if (h + k * hs < h1) {
         const uint4* src = reinterpret_cast<const uint4*>(q + (long long)(h + k * hs) * D);
         r[k][0] = __ldcs(src + p.c0);
         r[k][1] = __ldcs(src + p.c1);
       }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kQ; ++k)
       if (h + k * hs < h1) {
         float x[16];
         unit_turn<IL, NORM>(r[k][0], r[k][1], p.turn, c, norm, x);
@@ -384,9 +468,63 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
   }
 }
 
+// The same for heads of 128 that are normalised: the weights and the sums take the registers
+// that the loads in flight would, so a thread's come asynchronously through 32 bytes of shared
+// memory each of its own.  The CTA's 32 groups of 8 threads sweep the tokens' heads in order, so
+// that what is in flight on an SM lies together (a group a token, as above: 178 us for 8 prompts
+// of 1k-4k tokens, and more CTAs an SM only worse).
+template <bool IL>
+__device__ __forceinline__ void queries_norm_128(const RotaryArgs& a, const float2* cs,
+                                                 uint32_t at, long long row0, int nrows,
+                                                 int rot16, int h0, int h1) {
+  constexpr int kGroups = kThreads / 8;
+  const int g = threadIdx.x >> 3, j = threadIdx.x & 7, nh = h1 - h0, items = nrows * nh;
+  const UnitPlace p = unit_place(j, rot16, 8);
+  const UnitNorm norm = unit_norm<true>(a.q_norm, a.norm_eps, 128, p);
+  // (token, head) of an item, kGroups further at each step
+  const int dt = kGroups / nh, dh = kGroups - dt * nh;
+  auto next = [&](int& i, int& h) {
+    i += dt;
+    h += dh;
+    if (h >= nh) {
+      h -= nh;
+      ++i;
+    }
+  };
+  int fi = g / nh, fh = g - fi * nh;  // the next item to fetch
+  auto fetch = [&](uint32_t slot) {
+    if (fi < nrows) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (row0 + fi) * a.q_stride + (h0 + fh) * 128);
+      copy16(at + slot, src + p.c0);
+      copy16(at + slot + kHalfSlot, src + p.c1);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next(fi, fh);
+  };
+  int i = fi, h = fh;
+#pragma unroll 1
+  for (int k = 0; k < kDepth; ++k) fetch(k * kSlot);
+  uint32_t slot = 0;
+  for (int m = g; m < items; m += kGroups) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    const uint4 r0 = take16(at + slot), r1 = take16(at + slot + kHalfSlot);
+    fetch(slot);  // (this thread alone reads and fills its slots)
+    float2 c[8];
+    if (p.turn) unit_angles<IL, true>(cs + i * rot16 * 8, j, rot16, c);
+    float x[16];
+    unit_turn<IL, true>(r0, r1, p.turn, c, norm, x);
+    uint4* o = reinterpret_cast<uint4*>(a.q_out + ((row0 + i) * a.Hq + h0 + h) * 128);
+    o[p.c0] = pack8_bf16(x);
+    o[p.c1] = pack8_bf16(x + 8);
+    next(i, h);
+    slot = slot + kSlot == kDepth * kSlot ? 0 : slot + kSlot;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // The part's kv heads of the page: a warp a tile.
 template <int kD, bool IL, bool NORM, bool FP4>
-__device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* cs, int r,
+__device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* cs, uint32_t slots, int r,
                                             long long jp, long long L0, long long row0, int nrows,
                                             int slot0, int rot16) {
   const AppendArgs& ap = a.app;
@@ -424,9 +562,11 @@ __device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* c
       const uint16_t* src = ap.k_new + row0 * a.k_stride + (long long)h * Dk;
       float* scale = fp8 ? d.k_scale + ph : nullptr;
       uint8_t* dst = kc + ph * P * Dk * es;
-      if (kD == 128 && nrows == 16 && P == 16)
-        key_page_16x128<IL, NORM>(src, a.k_stride, rot16, cs, a.k_norm, a.norm_eps, fp8, scale,
-                                  dst);
+      if (kD == 128 && nrows == 16 && P == 16 && !NORM)
+        key_page_16x128<IL>(src, a.k_stride, rot16, cs, fp8, scale, dst);
+      else if (kD == 128 && NORM && nrows == 16 && P == 16 && a.k_norm != nullptr)
+        key_page_norm_16x128<IL>(src, a.k_stride, rot16, cs, slots, a.k_norm, a.norm_eps, fp8,
+                                 scale, dst);
       else
         key_tile_any<IL, NORM>(src, a.k_stride, nrows, Dk, rot16, cs, a.k_norm, a.norm_eps, fp8,
                                fresh, requant, scale, dst, slot0);
@@ -441,6 +581,11 @@ __device__ __forceinline__ void keys_values(const RotaryArgs& a, const float2* c
                           nullptr, requant);
     }
   }
+}
+
+// the tables before the queries' slots, in bytes
+__host__ __device__ constexpr int norm_ring_offset(int P, int half) {
+  return (int)(sizeof(Freq) + sizeof(float2) * P) * half;
 }
 
 // kD: head_dim_k when it is known (0: any); IL: neighbouring pairs; NORM: heads are normalised; FP4: a
@@ -496,15 +641,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
         bad_axis = true;
       float2 v;
       sincospif(__ll2float_rn(turns) * 0x1p-63f + f.skew, &v.y, &v.x);
-      cs[t * half + i] = v;
+      cs[t * half + 2 * angle_chunk<NORM>(i >> 1) + (i & 1)] = v;
     }
   if (bad_axis) set_error(d.ctl, KV_ERR_INVALID_ARG);
   __syncthreads();
   const int S = gridDim.y, part = blockIdx.y;
-  if (a.q != nullptr)
-    queries<kD, IL, NORM>(a, cs, row0, nrows, rot16, (int)((long long)a.Hq * part / S),
-                    (int)((long long)a.Hq * (part + 1) / S));
-  keys_values<kD, IL, NORM, FP4>(a, cs, r, jp, L0, row0, nrows, slot0, rot16);
+  // (NORM, heads of 128: this thread's slots)
+  const uint32_t slots = smem_u32(smem) + norm_ring_offset(P, half) + 16 * threadIdx.x;
+  if (a.q != nullptr) {
+    const int h0 = (int)((long long)a.Hq * part / S), h1 = (int)((long long)a.Hq * (part + 1) / S);
+    if constexpr (NORM && kD == 128)
+      queries_norm_128<IL>(a, cs, slots, row0, nrows, rot16, h0, h1);
+    else
+      queries<kD, IL, NORM>(a, cs, row0, nrows, rot16, h0, h1);
+  }
+  keys_values<kD, IL, NORM, FP4>(a, cs, slots, r, jp, L0, row0, nrows, slot0, rot16);
 }
 
 }  // namespace
@@ -519,7 +670,7 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
   int split = (int)min(8LL, max(1LL, 2LL * sms / items));
   split = min(split, a.app.d.num_kv_heads);
   // at most 32 KB: P * Dk <= 2048
-  const size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
+  size_t smem = (sizeof(Freq) + sizeof(float2) * (size_t)P) * (a.rotary_dim / 2);
   const bool il = a.interleaved != 0;
   const bool norm = a.q_norm != nullptr || a.k_norm != nullptr;
   const bool fp4 = a.app.d.dtype == KV_DTYPE_E2M1;
@@ -532,6 +683,11 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
       {{append_rotary_kernel<0, false, false, false>, append_rotary_kernel<0, false, true, false>},
        {append_rotary_kernel<0, true, false, false>, append_rotary_kernel<0, true, true, false>}}};
   const auto kernel = kKernels[fp4 ? 0 : a.app.d.head_dim_k == 128 ? 1 : 2][il][norm];
+  if (norm && a.app.d.head_dim_k == 128) {
+    smem = norm_ring_offset(P, a.rotary_dim / 2) + kDepth * 32 * kThreads;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(kernel, dim3((unsigned)items, split), dim3(kThreads), smem, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
