@@ -77,6 +77,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     cfg->R8 = 8 * rb;
     cfg->HG = d.num_kv_heads / hs;
     cfg->unit_tokens = fp4 ? 2 * d.page_size : d.page_size;
+    cfg->unit_extra = fp4 ? e2m1_unit_extra(cfg->kind) : 0;
     cfg->sub = fp4 ? warps / (hs * rbw) : 1;
     // the split kernel's CTAs plan a batch that fits their shared-memory
     // prefix cache themselves: no separate plan launch
@@ -102,6 +103,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
   cfg->HG = T * Hq / rb;
   cfg->stages = 0;
   cfg->unit_tokens = latent_unit_tokens();
+  cfg->unit_extra = 0;
   cfg->sub = 1;
   return KV_OK;
 }
@@ -177,6 +179,7 @@ kv_status decode_prepare(kv_pool* pool, int32_t B, int32_t Hq, int32_t T, const 
   x.HG = cfg.HG;
   x.stages = cfg.stages;
   x.unit_tokens = cfg.unit_tokens;
+  x.unit_extra = cfg.unit_extra;
   x.sub = cfg.sub;
   x.self_plan = cfg.self_plan;
   x.exp_tags = nullptr;

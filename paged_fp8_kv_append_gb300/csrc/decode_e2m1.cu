@@ -610,16 +610,20 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   };
   // Unit i's copies into stage st: 16 bytes a lane each, a group a unit.
   const uint64_t policy = l2_evict_first_policy();
+  // (WIDE, which is bound by its warps' instructions: where one of its pages is not there, or
+  // must not be read, page 0's tile is copied: it is never counted, or its request gets no
+  // output.  Without a branch the copies' addresses are worked out between what surrounds them.
+  // Up to 8 rows, bound by HBM, it is 1 us in 128 the other way.)
   auto fetch = [&](int i, int st) {
-    if (i < count) {
-      const int2 tl = table->tile[i & 31];
+    const int2 tl = table->tile[i & 31];
+    if (i < count && (tl.x & tl.y) >= 0) {
       const uint32_t dst = ring + st * kStage + 16 * lane;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int tile = k & 1 ? tl.y : tl.x;
-        if (tile < 0) continue;
+        if (!WIDE && tile < 0) continue;
         const uint8_t* src = static_cast<const uint8_t*>(k < 2 ? a.d.k_cache : a.d.v_cache) +
-                             (long long)tile * kE2m1Tile + 16 * lane;
+                             (long long)max(tile, 0) * kE2m1Tile + 16 * lane;
         copy16(dst + k * kE2m1Tile, src, policy);
         copy16(dst + k * kE2m1Tile + 512, src + 512, policy);
         if (lane < 8) copy16(dst + k * kE2m1Tile + 1024, src + 1024, policy);
@@ -627,6 +631,16 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // a piece's queries into the L2: 256 bytes a row, two lanes
+  auto prefetch_queries = [&](const Cursor& c) {
+    const int row = n0 + (lane >> 1);
+    if (row < a.R && (WIDE || lane < 16)) {
+      const int tq = row / a.G, hq = (c.h * Hs + hw) * a.G + row - tq * a.G;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + (((long long)c.r * a.T + tq) * a.Hq + hq) * D +
+                                                     64 * (lane & 1)));
+    }
+  };
+  prefetch_queries(start);
   // (the first units' pages are on their way before anything else is looked up)
   uint32_t bad_pages, bad_next;
   Raw ids;
@@ -719,6 +733,11 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
       }
     };
 
+    if (done + n_piece < n_units) {
+      Cursor next = seg;
+      cursor_next(next, pfx, B, HG);
+      prefetch_queries(next);
+    }
     // this warp's partial of the piece
     const long long prow =
         ((((long long)r * HG + seg.h + blockIdx.x) * a.sub + lg) * Hs + hw) * a.R8 + n0;
@@ -944,18 +963,24 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     }
     __syncthreads();
     if (sub == 0) {
-      for (int k = 1; k < S; ++k) {
-        bad = bad || st_bad[warp + k] != 0;
-        const float2 ml = st_ml[warp + k];
-        if (ml.x == -INFINITY) continue;
-        const float Mn = fmaxf(M, ml.x), x = exp2f(M - Mn), y = exp2f(ml.x - Mn);
-        const float4 v = st_o[warp + k][lane];
-        L = L * x + ml.y * y;
-        acc.x = acc.x * x + v.x * y;
-        acc.y = acc.y * x + v.y * y;
-        acc.z = acc.z * x + v.z * y;
-        acc.w = acc.w * x + v.w * y;
-        M = Mn;
+      // lane k: the state of the row's warp k (S <= 32); then the weighted outputs, independent
+      const int k = warp + min(lane, S - 1);
+      const float2 ml = lane < S ? st_ml[k] : make_float2(-INFINITY, 0.0f);
+      bad = __any_sync(0xffffffffu, lane < S && st_bad[k] != 0);
+      M = warp_max(ml.x);
+      const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+      L = warp_sum(ml.y * w);
+      acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int j = 0; j < S; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const float4 v = st_o[warp + j][lane];
+        if (wj != 0.0f) {
+          acc.x = fmaf(v.x, wj, acc.x);
+          acc.y = fmaf(v.y, wj, acc.y);
+          acc.z = fmaf(v.z, wj, acc.z);
+          acc.w = fmaf(v.w, wj, acc.w);
+        }
       }
     }
   }
@@ -975,6 +1000,14 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 }  // namespace
 
 int e2m1_split_warps(int kind) { return kind == 6 ? E2m1Cfg<true>::WARPS : E2m1Cfg<false>::WARPS; }
+
+#ifndef KV_E2M1_EXTRA
+#define KV_E2M1_EXTRA 4
+#endif
+#ifndef KV_E2M1_EXTRA16
+#define KV_E2M1_EXTRA16 12
+#endif
+int e2m1_unit_extra(int kind) { return kind == 6 ? KV_E2M1_EXTRA16 : KV_E2M1_EXTRA; }
 
 int e2m1_split_ctas_per_sm(int kind) {
   static int cache[2] = {-1, -1};

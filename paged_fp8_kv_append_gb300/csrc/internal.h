@@ -70,6 +70,9 @@ struct DecodeArgs {
   int32_t HG;           // segments per request: head groups (GQA) or 64-row blocks (latent)
   int32_t stages;       // ring stages of the split kernel
   int32_t unit_tokens;  // tokens per unit of work (a page; 4-bit pools: two)
+  // units that a request's length is taken for more: what a segment costs beside its units,
+  // for equal ranges (4-bit pools; these units hold no token)
+  int32_t unit_extra;
   int32_t sub;          // partials a (CTA, segment) piece leaves (4-bit pools: one a warp of a head)
   // the split kernel builds the batch plan itself (B + 1 <= its shared-memory
   // prefix cache) instead of reading the plan kernel's; its CTA 0 writes the
@@ -193,6 +196,7 @@ struct DecodeConfig {
   int HG;           // segments per request
   int stages;       // ring stages
   int unit_tokens;  // tokens per unit of work
+  int unit_extra;   // units added to a request's
   int sub;          // partials per piece
 };
 
@@ -220,6 +224,7 @@ cudaError_t launch_decode_combine(const DecodeArgs& a, cudaStream_t s, int* laun
 int gqa_split_ctas_per_sm(int kind);
 int e2m1_split_ctas_per_sm(int kind);
 int e2m1_split_warps(int kind);
+int e2m1_unit_extra(int kind);
 int latent_split_ctas_per_sm();
 int latent_unit_tokens();
 int latent_row_block();
