@@ -115,7 +115,30 @@ enum {
  * GQA layout (element = 1 byte for e4m3, 2 bytes for bf16):
  *   k_cache  [num_pages][num_kv_heads][page_size][head_dim_k]   token-major
  *   v_cache  [num_pages][num_kv_heads][head_dim_v][page_size]   dim-major
- *   k_scale, v_scale [num_pages][num_kv_heads] fp32 (e4m3 only; NULL for bf16)
+ *   k_scale, v_scale [num_pages][num_kv_heads] fp32 (e4m3 and 4 bits; NULL for
+ *   bf16)
+ * 4 bits (KV_DTYPE_E2M1; GQA layout, page_size 16, head_dim_k = head_dim_v = 128,
+ * KV_SCALE_FROZEN, up to 4096 kv heads; others: KV_ERR_UNSUPPORTED):
+ *   k_cache, v_cache [num_pages][num_kv_heads][1152 bytes]
+ *   A value is code * s * S: an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6, signed),
+ *   the e4m3 scale s of its group (16 dims of one token) and the block scale S
+ *   of its (page, kv head) in k_scale / v_scale, a power of two.  S comes from
+ *   the finite values that an append writes into a fresh page, of largest magnitude m: 2^(floor(log2
+ *   m) - 6), its exponent in -100 .. 121, 1 when m is 0; it stays as its first
+ *   write set it.  s = e4m3(m_g / S * fp32(1/6)) with m_g the group's largest
+ *   magnitude, to nearest even, saturating: a row may exceed its page's first rows
+ *   21 times before its scale saturates.  code = e2m1(fp32(x * (fp32(1/s) / S)))
+ *   to nearest even, saturating; 0 where s is.  A group with a value that is not
+ *   finite gets s = NaN (and codes of no meaning).
+ *   With c = d / 16, in bytes of the 1152 (a code's low half is the first of the
+ *   two it shares a byte with):
+ *     K code  64 slot + 16 (c % 4) + 8 (c / 4) + (d % 16) / 2, low half d even
+ *     K s     1024 + 16 (slot % 8) + 4 (c % 4) + 2 (slot / 8) + c / 4
+ *     V code  512 (d % 16 / 8) + 64 c + 16 (slot % 8 / 2) + 4 (d % 8 / 2)
+ *             + 2 (slot / 8) + d % 2, low half slot even
+ *     V s     1024 + 16 c + 4 (slot % 8 / 2) + 2 (slot / 8) + slot % 2
+ *   Such a pool takes every call but paged_prefill_attn (prompts are attended
+ *   in a bf16 pool and handed off with kv_append_from_pool).
  * LATENT layout (e4m3 only, num_kv_heads == 1):
  *   k_cache  [num_pages][page_size][head_dim_k]; v_cache NULL (V = first
  *   head_dim_v dims of each row); k_scale [num_pages]; v_scale NULL.
@@ -142,7 +165,7 @@ typedef struct {
   uint32_t* tags;
   int32_t* free_list;
   int32_t* ctl;
-  int32_t scale_mode;  /* kv_scale_mode (e4m3 pools; ignored for bf16) */
+  int32_t scale_mode;  /* kv_scale_mode (e4m3 pools; ignored for bf16; 4 bits: KV_SCALE_FROZEN) */
 } kv_pool_desc;
 
 typedef struct kv_pool kv_pool; /* opaque host handle */
@@ -180,7 +203,7 @@ kv_status kv_pool_destroy(kv_pool* pool);
  * scale = amax/448 (IEEE fp32; 1.0 if that is 0) from the rows this call
  * writes into it, separately for K and V; a partly filled page keeps its
  * scale; each element becomes e4m3_rne_satfinite(x / scale).  bf16: the bits
- * are copied.  Before rows go into a request's partly filled last page (n > 0
+ * are copied.  4 bits: as kv_pool_desc says.  Before rows go into a request's partly filled last page (n > 0
  * and L not a multiple of P) that mapping is checked like a read: the page
  * id must be in range and its tag must still be the expected one, so a page
  * reallocated since is never written.  The first request that cannot be
@@ -205,7 +228,7 @@ kv_status kv_append_quantize(kv_pool* pool, void* stream, int32_t B,
  * [B][src_max_pages_per_req], device) -- are appended to request r of
  * `pool` exactly as kv_append_quantize would append the same rows given as
  * k_new / v_new (page pops, tag stamps, per-(page, kv head) scales, codes;
- * bf16 destinations copy the bits).
+ * bf16 destinations copy the bits; 4-bit ones quantise as kv_pool_desc says).
  *   src          a pool with dtype KV_DTYPE_BF16 and the same layout, kv heads,
  *                head dims and page size as `pool` (else KV_ERR_INVALID_ARG);
  *                read only.
@@ -312,8 +335,12 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  * [2^15, 2^16) before it is narrowed to f16, and the row's scores take the
  * inverse factor, so any finite bf16 query is accepted; bf16 pools keep the
  * query in bf16.
+ * 4-bit pools multiply in f16 too (a code times its group's scale is exact),
+ * and weights are held in f16, relative to a reference at most 2^6 below the
+ * row's largest.  There a group that is NaN reaches, as V, the group's dims of
+ * the rows that see its position and no other, as K all of those rows.
  * Supported: GQA with head_dim 128, page_size 16 and up to 64 query rows per
- * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3 and bf16); LATENT
+ * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3, bf16 and 4 bits); LATENT
  * with head_dim_k 576, head_dim_v 512, page_size 64, e4m3.  Other shapes
  * return KV_ERR_UNSUPPORTED.
  */
@@ -435,6 +462,7 @@ kv_status paged_decode_attn_noalloc(kv_pool* pool, void* stream, int32_t B,
  * kv_append_quantize; a request that is not served gets no q_out rows.
  * GQA pools with page_size * head_dim <= 2048 for K and V, and total_new /
  * page_size + 2 B < 2^31; others return KV_ERR_UNSUPPORTED.  Two kernel launches.
+ * (4-bit pools quantise the turned fp32 keys as kv_pool_desc says.)
  */
 kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_heads,
                            int32_t total_new, const void* q, int64_t q_stride, const void* k_new,
@@ -488,7 +516,8 @@ kv_status kv_append_norm_rotary(kv_pool* pool, void* stream, int32_t B, int32_t 
  *               [total_rows][head_dim_k])
  *   v_out       bf16 [total_rows][num_kv_heads][head_dim_v] (device; LATENT:
  *               NULL)
- * e4m3 pools: bf16(code * scale), the product in fp32; bf16 pools: the bits.
+ * e4m3 pools: bf16(code * scale), the product in fp32; bf16 pools: the bits;
+ * 4-bit pools: the values as they are (six significant bits).
  * A request whose rows are not all cached (row_start < 0, row_start + rows >
  * seq_lens[r] or beyond its page table) or do not fit the outputs gets
  * KV_ERR_INVALID_ARG and no rows; so do one whose out_indptr runs backwards (a
@@ -535,7 +564,7 @@ size_t paged_prefill_workspace_size(const kv_pool* pool, int32_t B, int32_t num_
  * (a negative count) and all behind it; one whose needed pages include an id outside [0, num_pages)
  * sets KV_ERR_BAD_PAGE_ID: rows that would read it are not written, others of
  * the request may or may not be.  Other requests are not affected.  GQA pools
- * with head_dim 128 and page_size 16, e4m3 and bf16, up to 4096 kv heads, any
+ * with head_dim 128 and page_size 16, e4m3 and bf16 (not 4 bits), up to 4096 kv heads, any
  * num_q_heads / num_kv_heads, total_q * num_q_heads < 2^31 (and B + total_q *
  * num_q_heads / num_kv_heads / 256); others return KV_ERR_UNSUPPORTED.  Weights
  * are held in fp16 (e4m3 pools) or two bf16 parts for the product with V, sums

@@ -1,32 +1,42 @@
 // decode_e2m1.cu -- split-K paged decode attention over a 4-bit pool
-// (KV_DTYPE_E2M1): the split kernels; batch plan, partials and combine are those
-// of decode_gqa.cu.
+// (KV_DTYPE_E2M1): its split kernels and its combine; the batch plan is that of
+// the other formats (decode_plan.cuh).
 //
 // "Smaller, faster, safer: running Kimi and GLM at scale", section "Quantizing
 // the KV cache": the kernel converts values as it reads them.
 //
 // A 4-bit page takes 9/16 of the bytes of an e4m3 one and the same arithmetic, so at
-// HBM speed a page of a kv head has 420 cycles of a scheduler, where the e4m3
-// kernels' page has 750.
+// HBM speed a page of a kv head leaves 420 cycles of a scheduler, where the e4m3
+// kernels' page leaves 750.
 //
 // Work: units of two pages of one request for a group of Hs kv heads, cut into equal
 // ranges, one per persistent CTA; a warp serves one (kv head, block of query rows) of
 // every few units.  There is no producer warp, and nothing is shared between warps
-// but the batch plan: each fetches its own head's tiles into a ring of its own (bulk
-// copies of 1152 bytes), keeps its own online softmax and writes its own partial,
-// which the combine kernel merges with the others of the segment.
+// but the batch plan: each copies its own head's tiles into a ring of its own (16
+// bytes a lane, cp.async), keeps its own online softmax and writes its own partial,
+// which the combine merges with the others of the segment.  (With a producer's bulk
+// copies and partials merged in the CTA: 166 us for the batch below; with bulk copies
+// of each warp's own, 1152 bytes: 134.)
 //
 // Two pages are taken together: their products are independent chains, and waits,
 // bookkeeping and the softmax's vote are one for 32 tokens.
 //
 // A row's running reference is moved only when a score exceeds it by more than
-// 2^kSlack: weights stay below 2^kSlack (f16 operands; sums in fp32), and most pages
-// need one vote where a maximum over the lanes takes six shuffles.
+// 2^kSlack, so most pages need one vote where a maximum over the lanes takes six
+// shuffles.
 //
 // Codes become f16 by cvt.rn.f16x2.e2m1x2 (a byte each, as cheap as a move beside
 // the products); K's and V's group scales multiply them there (exact: six
 // significant bits), block scales go to the scores (K) and as an exponent bias into
 // the weights (V), as an e4m3 page's scales do.
+//
+// Up to 8 query rows a kv head bound by HBM: 32 requests of 4k-32k tokens, 64 and 8
+// heads, 128 us in all, 5.7 TB/s of the 6.8 of a plain copy (the split's loop alone at
+// the copy's rate; its first loads, a chain of three misses, take 6 us, the combine
+// 5).  16 warps of 128 registers: with 12 of 168 it is 151 us.  Above 8 rows bound by
+// the warps' instructions: 12 query heads a kv head, 48 requests of up to 8k: 70 us, 3.4
+// TB/s, the tensor pipe busy 38%, issue 45%; there 64 accumulators a lane want 168
+// registers (16 warps of 128: 96 us, what spills finds no L1 beside the ring).
 #include <climits>
 
 #include "common.cuh"
@@ -37,19 +47,6 @@
 
 namespace kvfp8 {
 namespace {
-
-#ifndef KV_E2M1_WARPS
-#define KV_E2M1_WARPS 16
-#endif
-#ifndef KV_E2M1_WARPS16
-#define KV_E2M1_WARPS16 12
-#endif
-#ifndef KV_E2M1_STAGES
-#define KV_E2M1_STAGES 2
-#endif
-#ifndef KV_E2M1_STAGES16
-#define KV_E2M1_STAGES16 2
-#endif
 
 constexpr int kStage = 4 * kE2m1Tile;  // a unit: K of its two pages, then V
 constexpr int kPfxCache = 1024;        // plan entries cached in shared memory
@@ -63,9 +60,9 @@ struct UnitTable {
 
 template <bool WIDE>
 struct E2m1Cfg {
-  static constexpr int WARPS = WIDE ? KV_E2M1_WARPS16 : KV_E2M1_WARPS;
+  static constexpr int WARPS = WIDE ? 12 : 16;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int ST = WIDE ? KV_E2M1_STAGES16 : KV_E2M1_STAGES;  // units in a warp's ring
+  static constexpr int ST = 2;  // units in a warp's ring (3 and 4 were no faster)
   static constexpr int QBYTES = WIDE ? 4096 : 2048;
   // shared memory carve-up (byte offsets)
   static constexpr int OFF_Q = WARPS * ST * kStage;          // [W] Q operands
@@ -1001,13 +998,11 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 
 int e2m1_split_warps(int kind) { return kind == 6 ? E2m1Cfg<true>::WARPS : E2m1Cfg<false>::WARPS; }
 
-#ifndef KV_E2M1_EXTRA
-#define KV_E2M1_EXTRA 4
-#endif
-#ifndef KV_E2M1_EXTRA16
-#define KV_E2M1_EXTRA16 12
-#endif
-int e2m1_unit_extra(int kind) { return kind == 6 ? KV_E2M1_EXTRA16 : KV_E2M1_EXTRA; }
+// What a piece costs beside its units (its queries, its first and last pages, its partial) in
+// units, by which a request is counted longer.  Above 8 rows 12: 94 us against 105 without for 24
+// requests of 4 drafts, 70 against 79 for the ragged batch above (6: 103 and 73, 20: 95 and 72).
+// Up to 8 rows 4: 1 us in 128, where 16 takes it back.
+int e2m1_unit_extra(int kind) { return kind == 6 ? 12 : 4; }
 
 int e2m1_split_ctas_per_sm(int kind) {
   static int cache[2] = {-1, -1};

@@ -33,6 +33,11 @@
 // 64) is bounded by latency: about 13 us for the two kernels in a graph, a chain of dependent
 // loads each.  Other shapes take the slower tiles, whose values are stored element by element
 // and whose keys are read twice: pages of 16 x 64 run at 3.4 TB/s, of 8 x 256 at 2.2.
+//
+// kv_append_norm_rotary normalises the heads in the same pass.  A row's sum of squares runs over
+// the eight lanes that hold it (heads of 128).  The same prompts: 164 us (the bytes are the same:
+// 122 at a plain copy's rate), of which the plan 9; the first query loads wait behind the page's
+// angles no more (169 us if they do), the keys' and values' still do behind the queries.
 #include "append_tile.cuh"
 #include "common.cuh"
 #include "e2m1.cuh"
@@ -88,7 +93,8 @@ __device__ __forceinline__ void unit_angles(const float2* row, int j, int rot16,
   const int k0 = NORM ? (IL ? 2 : 4) * j : 0, k1 = NORM ? (IL ? 2 * (j + rot16) : k0 + 2) : 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float4 t = k < 2 ? a[angle_chunk<NORM>(k0 + k)] : b[angle_chunk<NORM>(k1 + k - 2)];
+    float4 t = k < 2 ? a[angle_chunk<NORM>(k0 + k)] : b[angle_chunk<NORM>(k1 + k - 2)];
+    if (NORM) t = make_float4(t.x, t.z, t.y, t.w);  // (as they lie there: two cosines, two sines)
     c[2 * k] = make_float2(t.x, t.y);
     c[2 * k + 1] = make_float2(t.z, t.w);
   }
@@ -307,7 +313,7 @@ __device__ __forceinline__ void key_page_16x128(const uint16_t* src, long long s
 // The same of keys that are normalised too: with the weights their values do not fit the
 // registers, and what spills finds little of the L1 beside the queries' slots (180 us for 8
 // prompts became 205 with more of either).  So the rows wait in the thread's slots, and are
-// normalised and turned once for the scale and once for the codes.
+// normalised and turned once for the scale and once for the codes (172 us).
 template <bool IL>
 __device__ __noinline__ void key_page_norm_16x128(const uint16_t* src, long long stride, int rot16,
                                                   const float2* cs, uint32_t slots,
@@ -468,19 +474,52 @@ __device__ __forceinline__ void queries(const RotaryArgs& a, const float2* cs, l
   }
 }
 
+// Two fp32 products or sums at a time
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+
+// A unit's values of a head of 128 as packed pairs: x[j], x[4 + j] hold both values of the pairs
+// 2j and 2j + 1 (first values in x[j], second in x[4 + j]).
+template <bool IL>
+__device__ __forceinline__ void unit_pairs(uint4 a, uint4 b, uint64_t (&x)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = IL ? w[2 * j] : w[j], v = IL ? w[2 * j + 1] : w[4 + j];
+    x[j] = IL ? pack2(bf16_lo(u), bf16_lo(v)) : pack2(bf16_lo(u), bf16_hi(u));
+    x[4 + j] = IL ? pack2(bf16_hi(u), bf16_hi(v)) : pack2(bf16_lo(v), bf16_hi(v));
+  }
+}
+
 // The same for heads of 128 that are normalised: the weights and the sums take the registers
 // that the loads in flight would, so a thread's come asynchronously through 32 bytes of shared
-// memory each of its own.  The CTA's 32 groups of 8 threads sweep the tokens' heads in order, so
-// that what is in flight on an SM lies together (a group a token, as above: 178 us for 8 prompts
-// of 1k-4k tokens, and more CTAs an SM only worse).
-template <bool IL>
+// memory each of its own.  The CTA's 32 groups of 8 threads sweep the tokens' heads in order.
+// The fp32 arithmetic is packed, two values each.  (8 prompts of 1k-4k tokens: loads into registers
+// 185 us, slots with a group a token 178, this with single products 172, packed 169; three CTAs an
+// SM 179, queries and keys in kernels of their own 194, two CTAs a page 184.)
+// angles(): works out the page's angles into cs, for the whole CTA; the first loads are on their
+// way before it.
+template <bool IL, class Angles>
 __device__ __forceinline__ void queries_norm_128(const RotaryArgs& a, const float2* cs,
                                                  uint32_t at, long long row0, int nrows,
-                                                 int rot16, int h0, int h1) {
+                                                 int rot16, int h0, int h1, const Angles& angles) {
   constexpr int kGroups = kThreads / 8;
   const int g = threadIdx.x >> 3, j = threadIdx.x & 7, nh = h1 - h0, items = nrows * nh;
   const UnitPlace p = unit_place(j, rot16, 8);
-  const UnitNorm norm = unit_norm<true>(a.q_norm, a.norm_eps, 128, p);
+  const bool normed = a.q_norm != nullptr;
+  uint64_t weight[8];
+  if (normed)
+    unit_pairs<IL>(reinterpret_cast<const uint4*>(a.q_norm)[p.c0],
+                   reinterpret_cast<const uint4*>(a.q_norm)[p.c1], weight);
+  const uint64_t minus = pack2(-1.0f, -1.0f);
   // (token, head) of an item, kGroups further at each step
   const int dt = kGroups / nh, dh = kGroups - dt * nh;
   auto next = [&](int& i, int& h) {
@@ -504,18 +543,52 @@ __device__ __forceinline__ void queries_norm_128(const RotaryArgs& a, const floa
   int i = fi, h = fh;
 #pragma unroll 1
   for (int k = 0; k < kDepth; ++k) fetch(k * kSlot);
+  angles();
   uint32_t slot = 0;
   for (int m = g; m < items; m += kGroups) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
     const uint4 r0 = take16(at + slot), r1 = take16(at + slot + kHalfSlot);
     fetch(slot);  // (this thread alone reads and fills its slots)
-    float2 c[8];
-    if (p.turn) unit_angles<IL, true>(cs + i * rot16 * 8, j, rot16, c);
-    float x[16];
-    unit_turn<IL, true>(r0, r1, p.turn, c, norm, x);
+    uint64_t x[8];
+    unit_pairs<IL>(r0, r1, x);
+    if (normed) {
+      uint64_t s0 = mul2(x[0], x[0]), s1 = mul2(x[4], x[4]);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        s0 = fma2(x[k], x[k], s0);
+        s1 = fma2(x[4 + k], x[4 + k], s1);
+      }
+      const float2 u = unpack2(s0), v = unpack2(s1);
+      float ss = (u.x + u.y) + (v.x + v.y);
+      const uint32_t lanes = 0xFFu << (threadIdx.x & 24);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(lanes, ss, o);
+      const float r = rsqrtf(fmaf(ss, 1.0f / 128, a.norm_eps));
+      const uint64_t rr = pack2(r, r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = mul2(mul2(x[k], rr), weight[k]);
+    }
+    if (p.turn) {
+      const float2* row = cs + i * rot16 * 8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = IL ? (k < 2 ? 2 * j + k : 2 * (j + rot16) + k - 2) : 4 * j + k;
+        const ulonglong2 t = reinterpret_cast<const ulonglong2*>(row)[angle_chunk<true>(c)];
+        const uint64_t y = mul2(x[4 + k], mul2(t.y, minus)), z = mul2(x[k], t.y);
+        x[k] = fma2(x[k], t.x, y);
+        x[4 + k] = fma2(x[4 + k], t.x, z);
+      }
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 u = unpack2(x[k]), v = unpack2(x[4 + k]);
+      w[IL ? 2 * k : k] = IL ? pack_bf16(u.x, v.x) : pack_bf16(u.x, u.y);
+      w[IL ? 2 * k + 1 : 4 + k] = IL ? pack_bf16(u.y, v.y) : pack_bf16(v.x, v.y);
+    }
     uint4* o = reinterpret_cast<uint4*>(a.q_out + ((row0 + i) * a.Hq + h0 + h) * 128);
-    o[p.c0] = pack8_bf16(x);
-    o[p.c1] = pack8_bf16(x + 8);
+    o[p.c0] = make_uint4(w[0], w[1], w[2], w[3]);
+    o[p.c1] = make_uint4(w[4], w[5], w[6], w[7]);
     next(i, h);
     slot = slot + kSlot == kDepth * kSlot ? 0 : slot + kSlot;
   }
@@ -628,32 +701,40 @@ __global__ void __launch_bounds__(kThreads, 2) append_rotary_kernel(const Rotary
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   // ---- the angles of the page's tokens
-  bool bad_axis = false;
-  for (int t = warp; t < nrows; t += kWarps)
-    for (int i = lane; i < half; i += 32) {
-      const Freq f = freq[i];
-      long long turns = 0;
-      if (f.axis >= 0)
-        turns = (long long)((unsigned long long)(long long)
-                                a.positions[(long long)f.axis * a.total_new + row0 + t] *
-                            (unsigned long long)f.turns);
-      else
-        bad_axis = true;
-      float2 v;
-      sincospif(__ll2float_rn(turns) * 0x1p-63f + f.skew, &v.y, &v.x);
-      cs[t * half + 2 * angle_chunk<NORM>(i >> 1) + (i & 1)] = v;
-    }
-  if (bad_axis) set_error(d.ctl, KV_ERR_INVALID_ARG);
-  __syncthreads();
+  auto angles = [&]() {
+    bool bad_axis = false;
+    for (int t = warp; t < nrows; t += kWarps)
+      for (int i = lane; i < half; i += 32) {
+        const Freq f = freq[i];
+        long long turns = 0;
+        if (f.axis >= 0)
+          turns = (long long)((unsigned long long)(long long)
+                                  a.positions[(long long)f.axis * a.total_new + row0 + t] *
+                              (unsigned long long)f.turns);
+        else
+          bad_axis = true;
+        float2 v;
+        sincospif(__ll2float_rn(turns) * 0x1p-63f + f.skew, &v.y, &v.x);
+        if (NORM) {  // two pairs' cosines, then their sines: operands of the packed products
+          float* at = reinterpret_cast<float*>(cs + t * half + 2 * angle_chunk<NORM>(i >> 1)) + (i & 1);
+          at[0] = v.x;
+          at[2] = v.y;
+        } else {
+          cs[t * half + i] = v;
+        }
+      }
+    if (bad_axis) set_error(d.ctl, KV_ERR_INVALID_ARG);
+    __syncthreads();
+  };
   const int S = gridDim.y, part = blockIdx.y;
   // (NORM, heads of 128: this thread's slots)
   const uint32_t slots = smem_u32(smem) + norm_ring_offset(P, half) + 16 * threadIdx.x;
-  if (a.q != nullptr) {
-    const int h0 = (int)((long long)a.Hq * part / S), h1 = (int)((long long)a.Hq * (part + 1) / S);
-    if constexpr (NORM && kD == 128)
-      queries_norm_128<IL>(a, cs, slots, row0, nrows, rot16, h0, h1);
-    else
-      queries<kD, IL, NORM>(a, cs, row0, nrows, rot16, h0, h1);
+  const int h0 = (int)((long long)a.Hq * part / S), h1 = (int)((long long)a.Hq * (part + 1) / S);
+  if (NORM && kD == 128 && h1 > h0) {
+    queries_norm_128<IL>(a, cs, slots, row0, nrows, rot16, h0, h1, angles);
+  } else {
+    angles();
+    if (a.q != nullptr) queries<kD, IL, NORM>(a, cs, row0, nrows, rot16, h0, h1);
   }
   keys_values<kD, IL, NORM, FP4>(a, cs, slots, r, jp, L0, row0, nrows, slot0, rot16);
 }
