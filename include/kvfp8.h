@@ -123,9 +123,9 @@ enum {
  *   A value is code * s * S: an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6, signed),
  *   the e4m3 scale s of its group (16 dims of one token) and the block scale S
  *   of its (page, kv head) in k_scale / v_scale, a power of two.  S comes from
- *   the finite values that an append writes into a fresh page, of largest magnitude m: 2^(floor(log2
- *   m) - 6), its exponent in -100 .. 121, 1 when m is 0; it stays as its first
- *   write set it.  s = e4m3(m_g / S * fp32(1/6)) with m_g the group's largest
+ *   the finite values that an append writes into a fresh page, of largest
+ *   magnitude m: 2^(floor(log2 m) - 6), its exponent in -100 .. 121, 1 when m
+ *   is 0; it stays as its first write set it.  s = e4m3(m_g / S * fp32(1/6)) with m_g the group's largest
  *   magnitude, to nearest even, saturating: a row may exceed its page's first rows
  *   21 times before its scale saturates.  code = e2m1(fp32(x * (fp32(1/s) / S)))
  *   to nearest even, saturating; 0 where s is.  A group with a value that is not
@@ -203,7 +203,8 @@ kv_status kv_pool_destroy(kv_pool* pool);
  * scale = amax/448 (IEEE fp32; 1.0 if that is 0) from the rows this call
  * writes into it, separately for K and V; a partly filled page keeps its
  * scale; each element becomes e4m3_rne_satfinite(x / scale).  bf16: the bits
- * are copied.  4 bits: as kv_pool_desc says.  Before rows go into a request's partly filled last page (n > 0
+ * are copied.  4 bits: as kv_pool_desc says.
+ * Before rows go into a request's partly filled last page (n > 0
  * and L not a multiple of P) that mapping is checked like a read: the page
  * id must be in range and its tag must still be the expected one, so a page
  * reallocated since is never written.  The first request that cannot be

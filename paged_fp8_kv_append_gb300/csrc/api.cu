@@ -211,8 +211,9 @@ kv_status append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q_he
                         const int32_t* new_indptr, int32_t max_new_per_req,
                         const int32_t* positions, int32_t num_axes, const uint8_t* pair_axis,
                         const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                        const void* q_norm, const void* k_norm, float norm_eps, void* q_out, int32_t* page_table, uint32_t* exp_tags,
-                        int32_t max_pages_per_req, int32_t* seq_lens) {
+                        const void* q_norm, const void* k_norm, float norm_eps, void* q_out,
+                        int32_t* page_table, uint32_t* exp_tags, int32_t max_pages_per_req,
+                        int32_t* seq_lens) {
   if (!pool) return KV_ERR_INVALID_ARG;
   pool->last_launches = 0;
   const kv_pool_desc& d = pool->d;

@@ -243,10 +243,13 @@ cudaError_t launch_append_e2m1(const AppendArgs& a, long long pages, cudaStream_
   if (a.from_pool && !bulk) return cudaErrorNotSupported;
   cudaError_t e;
   if (bulk) {
-    const auto kernel = a.from_pool ? append_e2m1_bulk_kernel<true> : append_e2m1_bulk_kernel<false>;
-    const size_t smem =
-        kWarps * (kStages * kTileBytes + 64 * sizeof(Item)) + sizeof(int) * ((size_t)a.B + 1);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto kernel =
+        a.from_pool ? append_e2m1_bulk_kernel<true> : append_e2m1_bulk_kernel<false>;
+    constexpr size_t kFixed = kWarps * (kStages * kTileBytes + 64 * sizeof(Item));
+    const size_t smem = kFixed + sizeof(int) * ((size_t)a.B + 1);
+    // (the largest batch's: the same from every thread that may be between this and its launch)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kFixed + sizeof(int) * (kMaxPersistB + 1)));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)sms * kCtas), dim3(kThreads), smem, s, a);
   } else {

@@ -1005,9 +1005,11 @@ int e2m1_split_warps(int kind) { return kind == 6 ? E2m1Cfg<true>::WARPS : E2m1C
 int e2m1_unit_extra(int kind) { return kind == 6 ? 12 : 4; }
 
 int e2m1_split_ctas_per_sm(int kind) {
-  static int cache[2] = {-1, -1};
+  static int cache[64][2];  // by device, as the attribute below is; 0: not asked yet
   const int wide = kind == 6;
-  if (cache[wide] >= 0) return cache[wide];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cache[dev][wide] > 0) return cache[dev][wide];
   const auto kernel = wide ? e2m1_split_kernel<true> : e2m1_split_kernel<false>;
   const int smem = wide ? E2m1Cfg<true>::SMEM : E2m1Cfg<false>::SMEM;
   int n = 0;
@@ -1015,7 +1017,7 @@ int e2m1_split_ctas_per_sm(int kind) {
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
       &n, kernel, 32 * e2m1_split_warps(kind), smem);
   if (e != cudaSuccess || n <= 0) return 0;
-  cache[wide] = n;
+  cache[dev][wide] = n;
   return n;
 }
 

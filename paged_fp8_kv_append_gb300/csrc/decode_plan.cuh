@@ -94,7 +94,9 @@ __device__ __forceinline__ bool decode_plan_shared(const DecodeArgs& a, int32_t*
         const bool aborted = a.abort_mask != nullptr && a.abort_mask[lane] != 0;
         const bool bad_len = L < 0 || (L + P - 1) / P > a.max_pages;
         if (!aborted && bad_len) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
-        np = (aborted || bad_len) ? 0 : (L + a.unit_tokens - 1) / a.unit_tokens + (L > 0 ? a.unit_extra : 0);
+        np = (aborted || bad_len)
+                 ? 0
+                 : (L + a.unit_tokens - 1) / a.unit_tokens + (L > 0 ? a.unit_extra : 0);
       }
       long long v = np;
 #pragma unroll
@@ -125,7 +127,8 @@ __device__ __forceinline__ bool decode_plan_shared(const DecodeArgs& a, int32_t*
       const bool bad_len = L < 0 || (L + P - 1) / P > a.max_pages;
       if (!aborted && bad_len) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
       np = (aborted || bad_len) ? 0
-                                : (int)((L + a.unit_tokens - 1) / a.unit_tokens) + (L > 0 ? a.unit_extra : 0);
+                                : (int)((L + a.unit_tokens - 1) / a.unit_tokens) +
+                                      (L > 0 ? a.unit_extra : 0);
     }
     int v = np;
 #pragma unroll

@@ -766,7 +766,9 @@ cudaError_t launch_append_rotary(const RotaryArgs& a, cudaStream_t s, int* launc
   const auto kernel = kKernels[fp4 ? 0 : a.app.d.head_dim_k == 128 ? 1 : 2][il][norm];
   if (norm && a.app.d.head_dim_k == 128) {
     smem = norm_ring_offset(P, a.rotary_dim / 2) + kDepth * 32 * kThreads;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the largest page's: the same from every thread that may be between this and its launch)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)norm_ring_offset(16, 64) + kDepth * 32 * kThreads);
     if (e != cudaSuccess) return e;
   }
   e = launch_pdl(kernel, dim3((unsigned)items, split), dim3(kThreads), smem, s, a);
