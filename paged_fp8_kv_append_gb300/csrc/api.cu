@@ -38,23 +38,30 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     const long long R = (long long)T * G;
     if (d.head_dim_k != 128 || d.head_dim_v != 128 || d.page_size != 16 || R > 64)
       return KV_ERR_UNSUPPORTED;
-    // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16, 6: 4-bit)
+    // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16, 6: 4-bit), for 4-bit
+    // pools of 32 (kind 7) where the blocks of 16 are pairs and at most two of the eight warps serve
+    // a (kv head, 32 rows) together (measured at the head of decode_e2m1.cu)
     const bool bf16 = d.dtype == KV_DTYPE_BF16, fp4 = d.dtype == KV_DTYPE_E2M1, wide = R > 8;
-    cfg->kind = fp4 ? (wide ? 6 : 5) : bf16 ? (wide ? 4 : 1) : (wide ? 3 : 0);
+    const long long pairs = (R + 15) / 32, heads = d.num_kv_heads & -d.num_kv_heads;
+    const bool wide32 = fp4 && wide && (R + 15) / 16 % 2 == 0 && pairs * heads >= 4;
+    cfg->kind = fp4    ? (wide32 ? 7 : wide ? 6 : 5)
+                : bf16 ? (wide ? 4 : 1)
+                       : (wide ? 3 : 0);
+    const int warp_rows = cfg->kind == 7 ? 32 : wide ? 16 : 8;
     const int warps = fp4 ? e2m1_split_warps(cfg->kind) : gqa_consumer_warps(cfg->kind);
     // heads per unit: the largest power of two <= 8 (<= 4 for bf16, whose
     // tiles are twice as large) dividing Hkv, with heads x row blocks dividing
     // the consumer warp count; 16-row blocks may be padded with whole unused
     // blocks until such a split exists; ring depth from the ring size
-    int rbw = wide ? (int)((R + 15) / 16) : (int)((R + 7) / 8);  // row blocks, one warp each
+    int rbw = (int)((R + warp_rows - 1) / warp_rows);  // row blocks, one warp each
     int hs = 0;
-    for (; rbw <= (wide ? 4 : 1); ++rbw) {
+    for (; rbw <= (wide ? 64 / warp_rows : 1); ++rbw) {
       hs = bf16 ? 4 : 8;
       while (hs > 0 && (d.num_kv_heads % hs != 0 || warps % (hs * rbw) != 0)) hs >>= 1;
       if (hs > 0) break;
     }
     if (hs == 0) return KV_ERR_UNSUPPORTED;  // no split of the consumers fits
-    const int rb = wide ? 2 * rbw : rbw;  // row blocks of 8 in the partial layout
+    const int rb = rbw * warp_rows / 8;  // row blocks of 8 in the partial layout
     cfg->Hs = hs;
     cfg->stages = 0;
     if (!fp4) {  // (a warp of a 4-bit pool's kernel has a ring of its own)

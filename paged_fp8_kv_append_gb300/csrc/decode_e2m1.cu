@@ -37,6 +37,16 @@
 // the warps' instructions: 12 query heads a kv head, 48 requests of up to 8k: 70 us, 3.4
 // TB/s, the tensor pipe busy 38%, issue 45%; there 64 accumulators a lane want 168
 // registers (16 warps of 128: 96 us, what spills finds no L1 beside the ring).
+//
+// Two blocks of 16 rows are served by one warp where that leaves at most two warps for a
+// head's units (decode_config): each page is copied and its codes are converted once for
+// 32 rows.  24 requests of 4 drafts, 32 rows: 88 us against 94; 64 rows: 147 against 169.
+// With more warps a head it is no faster, and slower for short requests (8 of 2k-9k on one
+// kv head: 32 us against 26; each of its warps begins and ends every piece).  An odd number
+// of blocks would pad the last (48 rows 145 against 128).  The products' rate (37 us for the
+// drafts) stays far: a product takes 8 cycles of a scheduler, and what is issued beside it
+// about 0.65 of its own cycles more (2 products 16, 4 conversions with their
+// multiplications 12.5, together 25).
 #include <climits>
 
 #include "common.cuh"
@@ -58,12 +68,14 @@ struct UnitTable {
   int2 tile[32];
 };
 
-template <bool WIDE>
+// NB: blocks of 16 query rows a warp serves; 0: up to 8 rows.
+template <int NB>
 struct E2m1Cfg {
-  static constexpr int WARPS = WIDE ? 12 : 16;
+  static constexpr int ROWS = NB > 0 ? 16 * NB : 8;  // of a warp
+  static constexpr int WARPS = NB == 0 ? 16 : NB == 1 ? 12 : 8;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int ST = 2;  // units in a warp's ring (3 and 4 were no faster)
-  static constexpr int QBYTES = WIDE ? 4096 : 2048;
+  static constexpr int QBYTES = 256 * ROWS;
   // shared memory carve-up (byte offsets)
   static constexpr int OFF_Q = WARPS * ST * kStage;          // [W] Q operands
   static constexpr int OFF_UNIT = OFF_Q + WARPS * QBYTES;    // [W] UnitTable
@@ -338,21 +350,27 @@ struct E2m1Rows8 {
   }
 };
 
-// 16 query rows of a kv head from n0 on: S = Q K^T (M = 16 rows, N = 8 tokens) and
-// O += P V (N = 8 dims, K = 16 tokens).  Lane (g, t): rows g, g + 8 and tokens 2t,
-// 2t + 1, 2t + 8, 2t + 9, so the weights are the second product's A operand as they are.
+// NB blocks of 16 query rows of a kv head, from row n0 on: S = Q K^T (M = 16 rows, N = 8 tokens)
+// and O += P V (N = 8 dims, K = 16 tokens).  Lane (g, t): rows g, g + 8 of a block and tokens 2t,
+// 2t + 1, 2t + 8, 2t + 9, so the weights are the second product's A operand as they are.  The
+// operands made of a page's codes serve all blocks.
+template <int NB>
 struct E2m1Rows16 {
-  float &mA, &mB, &lA, &lB;
-  float (&acc)[16][4];
-  const uint32_t q16;  // Q as A operands, [k-step][lane] 16-byte words (at this lane's)
-  const float qscA, qscB;
+  float (&m)[NB][2], (&l)[NB][2];  // of rows g and g + 8 of each block
+  float (&acc)[NB][16][4];
+  const uint32_t q16;  // Q as A operands, [block][k-step][lane] 16-byte words (at this lane's)
+  const float (&qsc)[NB][2];
   const int n0, G, T, seen0;
 
+  // the last position that row g + 8 hr of block b sees
+  __device__ __forceinline__ int last(int b, int hr) const {
+    return seen0 + min((n0 + 16 * b + (int)((threadIdx.x & 31) >> 2) + 8 * hr) / G, T - 1);
+  }
   // EDGE: some position may lie behind the length or behind a row's last one
   template <int NP, bool EDGE>
   __device__ __forceinline__ void pages(const E2m1Page (&pg)[NP]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float s[NP][2][4];
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    float s[NP][NB][2][4];
     {
       uint4 kg[NP], kh[NP];
       uint32_t sg[NP], sh[NP];
@@ -362,157 +380,187 @@ struct E2m1Rows16 {
         kh[u] = lds128_at<512>(pg[u].k16);
         e4m3x4_to_f16(lds32_at<0>(pg[u].k4), sg[u], sh[u]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[u][0][e] = s[u][1][e] = 0.0f;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[u][b][0][e] = s[u][b][1][e] = 0.0f;
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {  // a code word: k-steps 2w, 2w + 1
-        const uint4 q0 = lds128_at<0>(q16 + 1024 * w), q1 = lds128_at<512>(q16 + 1024 * w);
+        uint4 q0[NB], q1[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          q0[b] = lds128_at<0>(q16 + 4096 * b + 1024 * w);
+          q1[b] = lds128_at<512>(q16 + 4096 * b + 1024 * w);
+        }
 #pragma unroll
         for (int u = 0; u < NP; ++u) {
           const uint32_t s0 = half_of(sg[u], w >> 1), s1 = half_of(sh[u], w >> 1);
           uint32_t x[4], y[4];
           e2m1x8_scaled(w_of(kg[u], w), s0, s0, x[0], x[1], x[2], x[3]);
           e2m1x8_scaled(w_of(kh[u], w), s1, s1, y[0], y[1], y[2], y[3]);
-          mma_f16(s[u][0], q0.x, q0.y, q0.z, q0.w, x[0], x[1]);
-          mma_f16(s[u][1], q0.x, q0.y, q0.z, q0.w, y[0], y[1]);
-          mma_f16(s[u][0], q1.x, q1.y, q1.z, q1.w, x[2], x[3]);
-          mma_f16(s[u][1], q1.x, q1.y, q1.z, q1.w, y[2], y[3]);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma_f16(s[u][b][0], q0[b].x, q0[b].y, q0[b].z, q0[b].w, x[0], x[1]);
+            mma_f16(s[u][b][1], q0[b].x, q0[b].y, q0[b].z, q0[b].w, y[0], y[1]);
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma_f16(s[u][b][0], q1[b].x, q1[b].y, q1[b].z, q1[b].w, x[2], x[3]);
+            mma_f16(s[u][b][1], q1[b].x, q1[b].y, q1[b].z, q1[b].w, y[2], y[3]);
+          }
         }
       }
     }
-    // s[u][nt][e]: row g (e < 2) or g + 8, token 8 nt + 2t + (e & 1)
-    float bias[NP], p[NP][2][4], big = -INFINITY;
+    // s[u][b][nt][e]: row g (e < 2) or g + 8 of block b, token 8 nt + 2t + (e & 1)
+    float bias[NP];
+    uint32_t pa[NP][NB][4];
 #pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      bias[u] = __log2f(pg[u].vs);
-      const float cA = bias[u] - mA, cB = bias[u] - mB;
-      const float scA = pg[u].ks * qscA, scB = pg[u].ks * qscB;
+    for (int u = 0; u < NP; ++u) bias[u] = __log2f(pg[u].vs);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+    for (int b = 0; b < NB; ++b) {
+      float &mA = m[b][0], &mB = m[b][1], p[NP][2][4], big = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[u][nt][e] = fmaf(s[u][nt][e], e < 2 ? scA : scB, e < 2 ? cA : cB);
-    }
-    if constexpr (EDGE) {
-      const int limA = seen0 + min((n0 + g) / G, T - 1), limB = seen0 + min((n0 + g + 8) / G, T - 1);
-#pragma unroll
-      for (int u = 0; u < NP; ++u)
+      for (int u = 0; u < NP; ++u) {
+        const float cA = bias[u] - mA, cB = bias[u] - mB;
+        const float scA = pg[u].ks * qsc[b][0], scB = pg[u].ks * qsc[b][1];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = 8 * nt + 2 * t + (e & 1);
-            if (tok >= pg[u].nv || pg[u].pos0 + tok > (e < 2 ? limA : limB))
-              p[u][nt][e] = -INFINITY;
-          }
-    }
-#pragma unroll
-    for (int u = 0; u < NP; ++u)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        big = fmaxf(big, fmaxf(fmaxf(p[u][nt][0], p[u][nt][1]), fmaxf(p[u][nt][2], p[u][nt][3])));
-    if (__any_sync(0xffffffffu, big > kSlack)) {
-      float nA = kUnset, nB = kUnset;
-#pragma unroll
-      for (int u = 0; u < NP; ++u)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = fmaf(s[u][nt][e], pg[u].ks * (e < 2 ? qscA : qscB), bias[u]);
-            float& x = p[u][nt][e];
-            x = x == -INFINITY ? -INFINITY : y;
-            if (e < 2) nA = fmaxf(nA, x);
-            else nB = fmaxf(nB, x);
-          }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, o));
-        nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, o));
+          for (int e = 0; e < 4; ++e)
+            p[u][nt][e] = fmaf(s[u][b][nt][e], e < 2 ? scA : scB, e < 2 ? cA : cB);
       }
-      nA = fmaxf(nA - kBelow, mA);
-      nB = fmaxf(nB - kBelow, mB);
-      const float aA = fast_exp2(mA - nA), aB = fast_exp2(mB - nB);
-      mA = nA;
-      mB = nB;
-      lA *= aA;
-      lB *= aB;
+      if constexpr (EDGE) {
+        const int limA = last(b, 0), limB = last(b, 1);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        acc[i][0] *= aA;
-        acc[i][1] *= aA;
-        acc[i][2] *= aB;
-        acc[i][3] *= aB;
+        for (int u = 0; u < NP; ++u)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = 8 * nt + 2 * t + (e & 1);
+              if (tok >= pg[u].nv || pg[u].pos0 + tok > (e < 2 ? limA : limB))
+                p[u][nt][e] = -INFINITY;
+            }
       }
 #pragma unroll
       for (int u = 0; u < NP; ++u)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
+          big = fmaxf(big,
+                      fmaxf(fmaxf(p[u][nt][0], p[u][nt][1]), fmaxf(p[u][nt][2], p[u][nt][3])));
+      if (__any_sync(0xffffffffu, big > kSlack)) {
+        float nA = kUnset, nB = kUnset;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[u][nt][e] -= e < 2 ? nA : nB;
-    }
-    uint32_t pa[NP][4];
+        for (int u = 0; u < NP; ++u)
 #pragma unroll
-    for (int u = 0; u < NP; ++u) {
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+            for (int e = 0; e < 4; ++e) {
+              const float y = fmaf(s[u][b][nt][e], pg[u].ks * qsc[b][e >> 1], bias[u]);
+              float& x = p[u][nt][e];
+              x = x == -INFINITY ? -INFINITY : y;
+              if (e < 2) nA = fmaxf(nA, x);
+              else nB = fmaxf(nB, x);
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[u][nt][e] = fast_exp2(p[u][nt][e]);
-      const float unbias = pow2_inverse(pg[u].vs);
-      lA = fmaf((p[u][0][0] + p[u][0][1]) + (p[u][1][0] + p[u][1][1]), unbias, lA);
-      lB = fmaf((p[u][0][2] + p[u][0][3]) + (p[u][1][2] + p[u][1][3]), unbias, lB);
-      pa[u][0] = f32x2_to_f16x2(p[u][0][0], p[u][0][1]);
-      pa[u][1] = f32x2_to_f16x2(p[u][0][2], p[u][0][3]);
-      pa[u][2] = f32x2_to_f16x2(p[u][1][0], p[u][1][1]);
-      pa[u][3] = f32x2_to_f16x2(p[u][1][2], p[u][1][3]);
+        for (int o = 1; o < 4; o <<= 1) {
+          nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, o));
+          nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, o));
+        }
+        nA = fmaxf(nA - kBelow, mA);
+        nB = fmaxf(nB - kBelow, mB);
+        const float aA = fast_exp2(mA - nA), aB = fast_exp2(mB - nB);
+        mA = nA;
+        mB = nB;
+        l[b][0] *= aA;
+        l[b][1] *= aB;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          acc[b][i][0] *= aA;
+          acc[b][i][1] *= aA;
+          acc[b][i][2] *= aB;
+          acc[b][i][3] *= aB;
+        }
+#pragma unroll
+        for (int u = 0; u < NP; ++u)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[u][nt][e] -= e < 2 ? nA : nB;
+      }
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[u][nt][e] = fast_exp2(p[u][nt][e]);
+        const float unbias = pow2_inverse(pg[u].vs);
+        l[b][0] = fmaf((p[u][0][0] + p[u][0][1]) + (p[u][1][0] + p[u][1][1]), unbias, l[b][0]);
+        l[b][1] = fmaf((p[u][0][2] + p[u][0][3]) + (p[u][1][2] + p[u][1][3]), unbias, l[b][1]);
+        pa[u][b][0] = f32x2_to_f16x2(p[u][0][0], p[u][0][1]);
+        pa[u][b][1] = f32x2_to_f16x2(p[u][0][2], p[u][0][3]);
+        pa[u][b][2] = f32x2_to_f16x2(p[u][1][0], p[u][1][1]);
+        pa[u][b][3] = f32x2_to_f16x2(p[u][1][2], p[u][1][3]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const uint4 v0 = lds128_at<2 * kE2m1Tile>(pg[u].k16);
       const uint4 v1 = lds128_at<2 * kE2m1Tile + 512>(pg[u].k16);
       const uint32_t sw = lds32_at<2 * kE2m1Tile>(pg[u].k4);
-      auto add = [&](uint32_t scales, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      auto add = [&](uint32_t scales) {
         uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
         e4m3x4_to_f16(scales, slo, shi);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
           uint32_t b00, b10, b01, b11;
           e2m1x8_scaled(w_of(i < 4 ? v0 : v1, i & 3), slo, shi, b00, b10, b01, b11);
-          mma_f16(acc[2 * i], a0, a1, a2, a3, b00, b01);
-          mma_f16(acc[2 * i + 1], a0, a1, a2, a3, b10, b11);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t(&a)[4] = pa[u][b];
+            mma_f16(acc[b][2 * i], a[0], a[1], a[2], a[3], b00, b01);
+            mma_f16(acc[b][2 * i + 1], a[0], a[1], a[2], a[3], b10, b11);
+          }
         }
       };
       if constexpr (!EDGE) {
-        add(sw, pa[u][0], pa[u][1], pa[u][2], pa[u][3]);
+        add(sw);
       } else {  // (as for 8 rows)
         uint32_t clean = sw & e2m1_token_mask(pg[u].nv, t);
         const int first = e2m1_first_nan(clean, t);  // of group g
-        add(clean, pa[u][0], pa[u][1], pa[u][2], pa[u][3]);
+        add(clean);
         if (__any_sync(0xffffffffu, first < 16)) {
           // columns 2t, 2t + 1 of every tile: groups 2t and 2t + 1
           const int f0 = __shfl_sync(0xffffffffu, first, 8 * t);
           const int f1 = __shfl_sync(0xffffffffu, first, 8 * t + 4);
-          const int limA = seen0 + min((n0 + g) / G, T - 1) - pg[u].pos0;
-          const int limB = seen0 + min((n0 + g + 8) / G, T - 1) - pg[u].pos0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (f0 < 16 && f0 <= limA) acc[i][0] = __int_as_float(0x7FFFFFFF);
-            if (f1 < 16 && f1 <= limA) acc[i][1] = __int_as_float(0x7FFFFFFF);
-            if (f0 < 16 && f0 <= limB) acc[i][2] = __int_as_float(0x7FFFFFFF);
-            if (f1 < 16 && f1 <= limB) acc[i][3] = __int_as_float(0x7FFFFFFF);
+          for (int b = 0; b < NB; ++b) {
+            const int limA = last(b, 0) - pg[u].pos0, limB = last(b, 1) - pg[u].pos0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (f0 < 16 && f0 <= limA) acc[b][i][0] = __int_as_float(0x7FFFFFFF);
+              if (f1 < 16 && f1 <= limA) acc[b][i][1] = __int_as_float(0x7FFFFFFF);
+              if (f0 < 16 && f0 <= limB) acc[b][i][2] = __int_as_float(0x7FFFFFFF);
+              if (f1 < 16 && f1 <= limB) acc[b][i][3] = __int_as_float(0x7FFFFFFF);
+            }
           }
         }
       }
     }
   }
   __device__ __forceinline__ void finish() {
-    if (mA == kUnset) mA = -INFINITY;
-    if (mB == kUnset) mB = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr)
+        if (m[b][hr] == kUnset) m[b][hr] = -INFINITY;
   }
 };
 
-template <bool WIDE>
-__global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(const DecodeArgs a) {
-  using C = E2m1Cfg<WIDE>;
+template <int NB>
+__global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(const DecodeArgs a) {
+  using C = E2m1Cfg<NB>;
+  constexpr bool WIDE = NB > 0;
   constexpr int D = 128, ST = C::ST;
   extern __shared__ __align__(1024) uint8_t smem[];
   int32_t* pfx_s = reinterpret_cast<int32_t*>(smem + C::OFF_PFX);
@@ -521,9 +569,9 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int B = a.B, Hkv = a.d.num_kv_heads, Hs = a.Hs, HG = a.HG;
-  // row blocks of a kv head, one a warp (WIDE: of 16 rows)
-  const int RBW = a.R8 / (WIDE ? 16 : 8), Hv = Hs * RBW;
-  if (Hs < 1 || RBW < 1 || (!WIDE && RBW != 1) || RBW * (WIDE ? 16 : 8) != a.R8 || a.R < 1 ||
+  // row blocks of a kv head, one a warp
+  const int RBW = a.R8 / C::ROWS, Hv = Hs * RBW;
+  if (Hs < 1 || RBW < 1 || (!WIDE && RBW != 1) || RBW * C::ROWS != a.R8 || a.R < 1 ||
       a.R > a.R8 || Hs * HG != Hkv || C::WARPS % Hv != 0 || a.sub != C::WARPS / Hv ||
       a.unit_tokens != 32 || (a.self_plan && B + 1 > kPfxCache)) {
     pdl_wait();
@@ -551,7 +599,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
 
   const int WPH = C::WARPS / Hv;                // warps per virtual head (kv head, row block)
   const int vh = warp % Hv, lg = warp / Hv;
-  const int hw = vh / RBW, n0 = (vh - hw * RBW) * 16;  // kv head of the group, first query row
+  const int hw = vh / RBW, n0 = (vh - hw * RBW) * C::ROWS;  // kv head of the group, first query row
   const uint32_t ring = smem_u32(smem) + warp * (ST * kStage);
   UnitTable* table = reinterpret_cast<UnitTable*>(smem + C::OFF_UNIT) + warp;
 
@@ -630,11 +678,14 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
   };
   // a piece's queries into the L2: 256 bytes a row, two lanes
   auto prefetch_queries = [&](const Cursor& c) {
-    const int row = n0 + (lane >> 1);
-    if (row < a.R && (WIDE || lane < 16)) {
-      const int tq = row / a.G, hq = (c.h * Hs + hw) * a.G + row - tq * a.G;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + (((long long)c.r * a.T + tq) * a.Hq + hq) * D +
-                                                     64 * (lane & 1)));
+#pragma unroll
+    for (int k = 0; k < (NB > 1 ? NB : 1); ++k) {
+      const int row = n0 + 16 * k + (lane >> 1);
+      if (row < a.R && (WIDE || lane < 16)) {
+        const int tq = row / a.G, hq = (c.h * Hs + hw) * a.G + row - tq * a.G;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            a.q + (((long long)c.r * a.T + tq) * a.Hq + hq) * D + 64 * (lane & 1)));
+      }
     }
   };
   prefetch_queries(start);
@@ -744,12 +795,14 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
       // ---- Q as A operands {a0, a1, a2, a3} of k-step j = rows g, g + 8 x dims
       // d(j) + 0, 1 and d(j) + 2, 3 with d(j) = 16t + 4j (j < 4), 64 + 16t + 4 (j - 4)
       uint32_t* qs = reinterpret_cast<uint32_t*>(smem + C::OFF_Q + warp * C::QBYTES);
-      float qsc[2];  // score scales of rows g and g + 8, with the row's 2^-e
-      {
+      float qsc[NB][2];  // score scales of rows g and g + 8 of a block, with the row's 2^-e
+      __syncwarp();      // the last piece's reads
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
         uint32_t qa[8][4];
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          const int row = n0 + g + 8 * hr;
+          const int row = n0 + 16 * b + g + 8 * hr;
           const bool live = row < R;
           const int tq = live ? row / G : 0, hq = live ? h * G + row % G : 0;
           const uint16_t* qrow = a.q + (((long long)r * T + tq) * a.Hq + hq) * D + 16 * t;
@@ -764,7 +817,7 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
           mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
           const int e = q_row_exp(mb);
           const float pw = pow2f(e);
-          qsc[hr] = ssl * pow2f(-e);
+          qsc[b][hr] = ssl * pow2f(-e);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             qa[2 * u][hr] = bf16x2_to_f16x2_scaled(v[u].x, pw);
@@ -773,36 +826,44 @@ __global__ void __launch_bounds__(E2m1Cfg<WIDE>::THREADS, 1) e2m1_split_kernel(c
             qa[2 * u + 1][2 + hr] = bf16x2_to_f16x2_scaled(v[u].w, pw);
           }
         }
-        __syncwarp();  // the last piece's reads
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(qs + (j * 32 + lane) * 4) =
+          *reinterpret_cast<uint4*>(qs + ((8 * b + j) * 32 + lane) * 4) =
               make_uint4(qa[j][0], qa[j][1], qa[j][2], qa[j][3]);
-        __syncwarp();
       }
-      float mA = kUnset, mB = kUnset, lA = 0.0f, lB = 0.0f;
-      float acc[16][4];
+      __syncwarp();
+      float m[NB][2], l[NB][2], acc[NB][16][4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-      E2m1Rows16 rows{mA, mB, lA, lB, acc, smem_u32(qs) + 16 * lane, qsc[0], qsc[1], n0, G, T, L - T};
+      for (int b = 0; b < NB; ++b) {
+        m[b][0] = m[b][1] = kUnset;
+        l[b][0] = l[b][1] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          acc[b][k][0] = acc[b][k][1] = acc[b][k][2] = acc[b][k][3] = 0.0f;
+      }
+      E2m1Rows16<NB> rows{m, l, acc, smem_u32(qs) + 16 * lane, qsc, n0, G, T, L - T};
       units(rows);
       rows.finish();
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        lA += __shfl_xor_sync(0xffffffffu, lA, o);
-        lB += __shfl_xor_sync(0xffffffffu, lB, o);
-      }
-      if (t == 0) {
-        *reinterpret_cast<float2*>(ml + 2 * g) = make_float2(mA, bad ? -1.0f : lA);
-        *reinterpret_cast<float2*>(ml + 2 * (g + 8)) = make_float2(mB, bad ? -1.0f : lB);
-      }
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) l[b][hr] += __shfl_xor_sync(0xffffffffu, l[b][hr], o);
+          if (t == 0)
+            *reinterpret_cast<float2*>(ml + 2 * (16 * b + g + 8 * hr)) =
+                make_float2(m[b][hr], bad ? -1.0f : l[b][hr]);
+        }
       // column c of tile k is dim 16 c + k: a lane's 32 dims of a row are contiguous
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int k = 0; k < 16; k += 4)
-          *reinterpret_cast<float4*>(op + (g + 8 * (e >> 1)) * D + 32 * t + 16 * (e & 1) + k) =
-              make_float4(acc[k][e], acc[k + 1][e], acc[k + 2][e], acc[k + 3][e]);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4*>(op + (16 * b + g + 8 * (e >> 1)) * D + 32 * t +
+                                       16 * (e & 1) + k) =
+                make_float4(acc[b][k][e], acc[b][k + 1][e], acc[b][k + 2][e], acc[b][k + 3][e]);
     } else {
       // ---- query fragments of row g (zero for padding rows) in shared memory, those of
       // k-steps 2w and 2w + 1 a 16-byte word: k-step j has dims 16 (t + 4 (j / 4)) + 4 (j % 4) ..
@@ -996,37 +1057,49 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 
 }  // namespace
 
-int e2m1_split_warps(int kind) { return kind == 6 ? E2m1Cfg<true>::WARPS : E2m1Cfg<false>::WARPS; }
+int e2m1_split_warps(int kind) {
+  return kind == 7 ? E2m1Cfg<2>::WARPS : kind == 6 ? E2m1Cfg<1>::WARPS : E2m1Cfg<0>::WARPS;
+}
 
 // What a piece costs beside its units (its queries, its first and last pages, its partial) in
-// units, by which a request is counted longer.  Above 8 rows 12: 94 us against 105 without for 24
-// requests of 4 drafts, 70 against 79 for the ragged batch above (6: 103 and 73, 20: 95 and 72).
+// units, by which a request is counted longer.  Above 8 rows 12: 88 us against 100 without for 24
+// requests of 4 drafts, 70 against 79 for the ragged batch above (6: 93 and 73, 20: 90 and 72).
 // Up to 8 rows 4: 1 us in 128, where 16 takes it back.
-int e2m1_unit_extra(int kind) { return kind == 6 ? 12 : 4; }
+int e2m1_unit_extra(int kind) { return kind >= 6 ? 12 : 4; }
 
 int e2m1_split_ctas_per_sm(int kind) {
-  static int cache[64][2];  // by device, as the attribute below is; 0: not asked yet
-  const int wide = kind == 6;
+  static int cache[64][3];  // by device, as the attribute below is; 0: not asked yet
+  const int nb = kind - 5;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (cache[dev][wide] > 0) return cache[dev][wide];
-  const auto kernel = wide ? e2m1_split_kernel<true> : e2m1_split_kernel<false>;
-  const int smem = wide ? E2m1Cfg<true>::SMEM : E2m1Cfg<false>::SMEM;
+  if (cache[dev][nb] > 0) return cache[dev][nb];
+  const auto kernel = nb == 2   ? e2m1_split_kernel<2>
+                      : nb == 1 ? e2m1_split_kernel<1>
+                                : e2m1_split_kernel<0>;
+  const int smem = nb == 2 ? E2m1Cfg<2>::SMEM : nb == 1 ? E2m1Cfg<1>::SMEM : E2m1Cfg<0>::SMEM;
   int n = 0;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
       &n, kernel, 32 * e2m1_split_warps(kind), smem);
   if (e != cudaSuccess || n <= 0) return 0;
-  cache[dev][wide] = n;
+  cache[dev][nb] = n;
   return n;
 }
 
+namespace {
+
+template <int NB>
+cudaError_t launch_split(const DecodeArgs& a, cudaStream_t s) {
+  return launch_pdl(e2m1_split_kernel<NB>, dim3(a.grid), dim3(E2m1Cfg<NB>::THREADS),
+                    E2m1Cfg<NB>::SMEM, s, a);
+}
+
+}  // namespace
+
 cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
-  const cudaError_t e =
-      kind == 6 ? launch_pdl(e2m1_split_kernel<true>, dim3(a.grid), dim3(E2m1Cfg<true>::THREADS),
-                             E2m1Cfg<true>::SMEM, s, a)
-                : launch_pdl(e2m1_split_kernel<false>, dim3(a.grid), dim3(E2m1Cfg<false>::THREADS),
-                             E2m1Cfg<false>::SMEM, s, a);
+  const cudaError_t e = kind == 7   ? launch_split<2>(a, s)
+                        : kind == 6 ? launch_split<1>(a, s)
+                                    : launch_split<0>(a, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -1037,7 +1110,9 @@ cudaError_t launch_e2m1_combine(const DecodeArgs& a, cudaStream_t s, int* launch
   const double parts = a.sub * (1.0 + (double)a.grid / ((double)a.B * a.HG));  // a row, about
   int S = 1;
   while (S < 8 && 8.0 * S < parts) S *= 2;
-  if (parts > 128.0) S = 32;
+  // (32 where the rows' blocks are one wave: 64 rows of 300 partials 40 us against 44 in all; 256
+  // rows of 160, two waves, 36 against 32)
+  if (parts > 128.0 && rows <= a.grid) S = 32;
   const int W = S == 32 ? 32 : 8;
   const long long blocks = (rows + W / S - 1) / (W / S);
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;

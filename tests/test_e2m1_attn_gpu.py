@@ -279,3 +279,101 @@ def test_one_call_step(kv, hq):
     assert bool((got[1] == 7.0).all())
     for b in (0, 2, 3):
         assert torch.equal(got[b], want[b])
+
+
+PAIRS = [  # 17 to 32 and 49 to 64 query rows a kv head, of 4 or 8 kv heads
+    (80, 4, 1), (128, 4, 1), (24, 4, 3), (192, 8, 1), (48, 4, 2), (64, 4, 4), (52, 4, 4), (98, 2, 1), (512, 8, 1),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,T", PAIRS)
+@pytest.mark.parametrize("lens", [[0, 1, 2, 15, 16, 17], [31, 32, 33, 63, 64, 65], [700, 5, 0, 1033]])
+def test_warps_of_32_rows(kv, hq, hkv, T, lens):
+    f = Filled4(kv, lens, hkv=hkv, seed=hq + T)
+    q = _queries(len(lens), T, hq, 31, 0.5)
+    got = _run(f, q, 0.09)
+    assert f.pool.error() == 0
+    for b in range(len(lens)):
+        _bounded(f, b, got[b], q[b], 0.09)
+
+
+@pytest.mark.parametrize("where", [0, 40, 600, 950])
+@pytest.mark.parametrize("row", [3, 12, 17, 30])
+def test_one_key_far_above_the_rest_for_one_row_of_32(kv, where, row):
+    """One row's query lies along one key, which is several times longer than the others: its score
+    is 40 and theirs below 20, so the row is that key's value; the block's other rows, and the other
+    block's, keep their references.  (A row's terms sum to at most 40 / 0.09 < 2^9.)"""
+    f = Filled4(kv, [1000], hkv=4, seed=33, spread=0)
+    p, slot = int(f.table[0, where // 16]), where % 16
+    f.cache["k"][p, 0, PLACES["k"][2][slot]] = 0x50  # 8: the others are below 2
+    f.to_device()
+    q = _queries(1, 1, 128, 34, 0.02)
+    keys = f.rows(0, "k")[:, 0]
+    k = keys[where]
+    q[0, 0, row] = (k * (40.0 / float(k @ k) / 0.09)).to(torch.bfloat16)
+    score = keys @ q[0, 0, row].double() * 0.09
+    score[where] = -40.0
+    assert float(score.max()) < 20
+    got = _run(f, q, 0.09)[0]
+    # The file's bound with its last part by itself: the other keys' weights, below 2^-20 of the
+    # largest, are off by up to 2^-31 of it each, which is no part of A in a dim where that key's
+    # value is 0: 999 * 2^-31 of the largest value for the row.
+    v = f.rows(0, "v")
+    ref, mag = (attention(q[0].double(), f.rows(0, "k"), x, 0.09, 999) for x in (v, v.abs()))
+    bound = 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag
+    bound[0, row] += 999 * 2.0 ** -31 * v[:, 0].abs().max()
+    assert bool(((got.double() - ref).abs() <= bound).all())
+    assert float((got[0, row].double() - v[where, 0]).abs().max()) <= 2.0 ** -7 * float(v[where, 0].abs().max())
+
+
+def test_values_that_are_not_finite_in_warps_of_32_rows(kv):
+    T, n = 4, 40
+    f = Filled4(kv, [n], hkv=4, seed=35)
+    q = _queries(1, T, 32, 36, 0.5)
+    clean = _run(f, q, 0.09)
+    pos = n - 2
+    p, slot = int(f.table[0, pos // 16]), pos % 16
+    f.cache["v"][p, 0, PLACES["v"][2][slot, 3]] = 0x7F
+    f.to_device()
+    got = _run(f, q, 0.09)
+    nan = torch.isnan(got[0])
+    keep = torch.ones_like(nan)
+    keep[2:, :8, 48:64] = False
+    assert bool(nan[~keep].all()) and not nan[keep].any()
+    assert torch.equal(got[0][keep], clean[0][keep])
+    f.cache["v"][p, 0, PLACES["v"][2][slot, 3]] = 0x38
+    f.cache["k"][p, 0, PLACES["k"][2][slot, 5]] = 0x7F
+    f.to_device()
+    nan = torch.isnan(_run(f, q, 0.09)[0])
+    assert bool(nan[2:, :8].all()) and not nan[:2].any() and not nan[:, 8:].any()
+
+
+@pytest.mark.parametrize("hq,B", [(128, 5), (256, 1200)])
+def test_checked_and_captured_in_warps_of_32_rows(kv, hq, B):
+    """32 and 64 rows: stale tags, and the same bits from a replayed graph and in the fixed scratch."""
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 60, B).tolist()
+    lens[1], lens[3] = 50, 33
+    f = Filled4(kv, lens, hkv=4, seed=37)
+    tags = torch.zeros((B, f.table.shape[1]), dtype=torch.int32, device="cuda")
+    tags[1, 2] = 5
+    q = _queries(B, 1, hq, 38, 0.5)
+    qd, out = q.cuda(), torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    mask = torch.full((B,), 9, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(f.pool.workspace_size(B, hq, 1), dtype=torch.uint8, device="cuda")
+
+    def run():
+        kv.paged_decode_attn_checked(f.pool.handle, B, hq, 1, qd, f.table_d, tags, f.lens_d, 0.09, out, mask, ws)
+
+    run()
+    first = out.cpu()
+    assert mask.nonzero().flatten().tolist() == [1] and f.pool.error() == 0
+    assert bool((first[1] == 7.0).all())
+    for b in [0, 2, 3, 4, B - 1]:
+        _bounded(f, b, first[b], q[b], 0.09)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    out.fill_(7.0)
+    graph.replay()
+    assert torch.equal(out.cpu(), first)
