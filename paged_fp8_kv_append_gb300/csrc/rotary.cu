@@ -35,9 +35,9 @@
 // and whose keys are read twice: pages of 16 x 64 run at 3.4 TB/s, of 8 x 256 at 2.2.
 //
 // kv_append_norm_rotary normalises the heads in the same pass.  A row's sum of squares runs over
-// the eight lanes that hold it (heads of 128).  The same prompts: 164 us (the bytes are the same:
+// the eight lanes that hold it (heads of 128).  The same prompts: 162 us (the bytes are the same:
 // 122 at a plain copy's rate), of which the plan 9; the first query loads wait behind the page's
-// angles no more (169 us if they do), the keys' and values' still do behind the queries.
+// angles no more (164 us against 169 in one run), the keys' and values' still do behind the queries.
 #include "append_tile.cuh"
 #include "common.cuh"
 #include "e2m1.cuh"
