@@ -320,7 +320,8 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  *               Aborted requests read no page and their output rows are
  *               left untouched (SFS: an aborted request returns no data).
  *   sm_scale    softmax scale applied to q.k (fp32).
- *   out         bf16 [B][q_tokens][num_q_heads][head_dim_v] (device)
+ *   out         bf16 [B][q_tokens][num_q_heads][head_dim_v] (device; 8-byte
+ *               aligned, as q is 16-byte aligned, else KV_ERR_INVALID_ARG)
  *   workspace   device scratch of at least paged_decode_workspace_size bytes,
  *               256-byte aligned; contents need not be initialised.
  *

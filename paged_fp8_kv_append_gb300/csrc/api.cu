@@ -158,7 +158,9 @@ kv_status decode_prepare(kv_pool* pool, int32_t B, int32_t Hq, int32_t T, const 
     if (need_inputs && (!q || !page_table || !seq_lens || max_pages <= 0 || !aligned16(q) ||
                         !isfinite(sm_scale)))
       return KV_ERR_INVALID_ARG;
-    if (need_out && !out) return KV_ERR_INVALID_ARG;
+    // (every combine stores 8 bytes a lane)
+    if (need_out && (!out || (reinterpret_cast<uintptr_t>(out) & 7u) != 0))
+      return KV_ERR_INVALID_ARG;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
       return KV_ERR_INVALID_ARG;
   }
