@@ -340,7 +340,8 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  * 4-bit pools multiply in f16 too (a code times its group's scale is exact),
  * and weights are held in f16, relative to a reference at most 2^6 below the
  * row's largest.  There a group that is NaN reaches, as V, the group's dims of
- * the rows that see its position and no other, as K all of those rows.
+ * the rows that see its position and no other, as K all of those rows; a query
+ * that is not finite makes its row NaN (where it sees a position).
  * Supported: GQA with head_dim 128, page_size 16 and up to 64 query rows per
  * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3, bf16 and 4 bits); LATENT
  * with head_dim_k 576, head_dim_v 512, page_size 64, e4m3.  Other shapes

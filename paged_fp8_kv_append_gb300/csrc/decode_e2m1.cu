@@ -91,6 +91,18 @@ constexpr float kUnset = -1e38f;  // the reference of a row that has seen no pos
 // (2^-14 without the distance), and none passes its 65504.
 constexpr float kBelow = 6.0f, kSlack = 15.0f;
 
+// A row's reference at the end of a warp's part, with its sum: -inf where the part holds no
+// position for the merge.  Scores that are NaN pass no vote and leave the reference unset, but
+// not the sum, which has to reach the merge.
+__device__ __forceinline__ float final_reference(float m, float sum) {
+  return m != kUnset ? m : sum != sum ? 0.0f : -INFINITY;
+}
+// A row's score scale, with the 2^-e of its queries; mb: their largest magnitude's bits.  A query
+// that is not finite makes NaN of every score (an infinite one could otherwise pass for a mask).
+__device__ __forceinline__ float row_score_scale(float scale, int e, uint32_t mb) {
+  return mb >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : scale * pow2f(-e);
+}
+
 struct FalseType {
   static constexpr bool value = false;
 };
@@ -343,10 +355,15 @@ struct E2m1Rows8 {
       }
     }
   }
-  // a row that has seen nothing: the merge's -inf
+  // the sums over the lanes, and the references as the merge wants them
   __device__ __forceinline__ void finish() {
-    if (m0 == kUnset) m0 = -INFINITY;
-    if (m1 == kUnset) m1 = -INFINITY;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    m0 = final_reference(m0, l0);
+    m1 = final_reference(m1, l1);
   }
 };
 
@@ -552,8 +569,11 @@ struct E2m1Rows16 {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr)
-        if (m[b][hr] == kUnset) m[b][hr] = -INFINITY;
+      for (int hr = 0; hr < 2; ++hr) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) l[b][hr] += __shfl_xor_sync(0xffffffffu, l[b][hr], o);
+        m[b][hr] = final_reference(m[b][hr], l[b][hr]);
+      }
   }
 };
 
@@ -817,7 +837,7 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
           mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
           const int e = q_row_exp(mb);
           const float pw = pow2f(e);
-          qsc[b][hr] = ssl * pow2f(-e);
+          qsc[b][hr] = row_score_scale(ssl, e, mb);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             qa[2 * u][hr] = bf16x2_to_f16x2_scaled(v[u].x, pw);
@@ -847,13 +867,10 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) l[b][hr] += __shfl_xor_sync(0xffffffffu, l[b][hr], o);
+        for (int hr = 0; hr < 2; ++hr)
           if (t == 0)
             *reinterpret_cast<float2*>(ml + 2 * (16 * b + g + 8 * hr)) =
                 make_float2(m[b][hr], bad ? -1.0f : l[b][hr]);
-        }
       // column c of tile k is dim 16 c + k: a lane's 32 dims of a row are contiguous
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -885,8 +902,9 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
         const int e = q_row_exp(mb);
         const float pw = pow2f(e);
         // rows 2t and 2t + 1 are held by the lanes g = 2t and 2t + 1
-        qsc0 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t));
-        qsc1 = ssl * pow2f(-__shfl_sync(0xffffffffu, e, 8 * t + 4));
+        const float sc = row_score_scale(ssl, e, mb);
+        qsc0 = __shfl_sync(0xffffffffu, sc, 8 * t);
+        qsc1 = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
         __syncwarp();  // the last piece's reads
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -902,11 +920,6 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
       E2m1Rows8 rows{m0, m1, l0, l1, acc, smem_u32(qs) + 16 * lane, qsc0, qsc1, G, T, L - T};
       units(rows);
       rows.finish();
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-      }
       if (g == 0)
         *reinterpret_cast<float4*>(ml + 4 * t) =
             make_float4(m0, bad ? -1.0f : l0, m1, bad ? -1.0f : l1);

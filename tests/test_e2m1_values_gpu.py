@@ -1,0 +1,92 @@
+"""Decode attention over 4-bit pools where keys, values or queries are no numbers: what reaches a
+row, whatever part of its positions a warp has.  Rows that nothing reaches keep the bound of
+test_e2m1_attn_gpu."""
+import pytest
+import torch
+
+from e2m1ref import PLACES, Filled4
+from promptref import attention
+from test_e2m1_attn_gpu import _queries, _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kv():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import paged_fp8_kv_append_gb300 as kv
+
+    return kv
+
+
+# query heads, kv heads: 8 rows a warp; 16 (of one, two and three blocks); 32 (of one and two)
+SHAPES = [(8, 1), (8, 2), (64, 8), (16, 1), (24, 2), (64, 2), (48, 1), (128, 4), (128, 2)]
+
+
+def _bounded_rows(f, b, got, q, scale, rows):
+    """The bound over the (token, head) pairs of the mask `rows`."""
+    n, T = f.lens[b], q.shape[0]
+    k, v = f.rows(b, "k"), f.rows(b, "v")
+    ref, mag = (attention(torch.where(rows[..., None], q.double(), 0.0), k, x, scale, n - T)
+                for x in (v, v.abs()))
+    bad = (got.double() - ref).abs() > 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag + 1e-30
+    assert not bool((bad | torch.isnan(got))[rows].any())
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("n", [1, 17, 33, 65, 700])
+def test_a_newest_key_that_is_no_number(kv, hq, hkv, n):
+    """The newest token's key has a NaN: it may be the only position of a warp's part, or of the
+    request.  The kv head's rows are NaN; other heads', and the other request's, are not."""
+    f = Filled4(kv, [n, 40], hkv=hkv, seed=41)
+    q = _queries(2, 1, hq, 42, 0.5)
+    p, slot = int(f.table[0, (n - 1) // 16]), (n - 1) % 16
+    f.cache["k"][p, hkv - 1, PLACES["k"][2][slot, 5]] = 0x7F
+    f.to_device()
+    got = _run(f, q, 0.09)
+    assert f.pool.error() == 0
+    G = hq // hkv
+    assert bool(torch.isnan(got[0, :, -G:]).all())
+    f.cache["k"][p, hkv - 1, PLACES["k"][2][slot, 5]] = 0x30
+    rows = torch.ones((1, hq), dtype=torch.bool)
+    _bounded_rows(f, 1, got[1], q[1], 0.09, rows)
+    rows[:, -G:] = False
+    _bounded_rows(f, 0, got[0], q[0], 0.09, rows)
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("n", [1, 33, 700])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_no_number(kv, hq, hkv, n, value):
+    """Every score of such a row is NaN or infinite: the row is NaN, and no other."""
+    f = Filled4(kv, [n, 40], hkv=hkv, seed=43)
+    q = _queries(2, 1, hq, 44, 0.5)
+    q[0, 0, hq // 2, 77] = value
+    got = _run(f, q, 0.09)
+    rows = torch.ones((1, hq), dtype=torch.bool)
+    _bounded_rows(f, 1, got[1], q[1], 0.09, rows)
+    assert bool(torch.isnan(got[0, 0, hq // 2]).all())
+    rows[0, hq // 2] = False
+    _bounded_rows(f, 0, got[0], q[0], 0.09, rows)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (24, 2), (64, 4)])
+def test_drafts_before_the_bad_key_and_rows_that_see_nothing(kv, hq, hkv):
+    """Four tokens over three positions: the first sees none (zeros), the second and third do not
+    see the newest key, which has a NaN; the last does."""
+    f = Filled4(kv, [3], hkv=hkv, seed=45)
+    q = _queries(1, 4, hq, 46, 0.5)
+    q[0, 0, 0, 0] = float("nan")  # (a row that sees nothing is zero whatever its query is)
+    p = int(f.table[0, 0])
+    for h in range(hkv):
+        f.cache["k"][p, h, PLACES["k"][2][2, 0]] = 0x7F
+    f.to_device()
+    got = _run(f, q, 0.09)[0]
+    assert not got[0].any() and bool(torch.isnan(got[3]).all())
+    for h in range(hkv):
+        f.cache["k"][p, h, PLACES["k"][2][2, 0]] = 0x30
+    rows = torch.zeros((4, hq), dtype=torch.bool)
+    rows[1:3] = True
+    _bounded_rows(f, 0, got, q[0], 0.09, rows)
