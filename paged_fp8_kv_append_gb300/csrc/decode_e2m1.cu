@@ -1012,8 +1012,8 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const float wu = __shfl_sync(0xffffffffu, w, (k + u) & 31);
-        // (a partial that saw nothing has weight 0 and adds nothing)
-        if (k + u < nj && wu != 0.0f) {
+        // (a partial that saw nothing is zeros; one whose weight is 0 may hold a V that is NaN)
+        if (k + u < nj) {
           acc.x = fmaf(o[u].x, wu, acc.x);
           acc.y = fmaf(o[u].y, wu, acc.y);
           acc.z = fmaf(o[u].z, wu, acc.z);
@@ -1046,12 +1046,10 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
       for (int j = 0; j < S; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, j);
         const float4 v = st_o[warp + j][lane];
-        if (wj != 0.0f) {
-          acc.x = fmaf(v.x, wj, acc.x);
-          acc.y = fmaf(v.y, wj, acc.y);
-          acc.z = fmaf(v.z, wj, acc.z);
-          acc.w = fmaf(v.w, wj, acc.w);
-        }
+        acc.x = fmaf(v.x, wj, acc.x);
+        acc.y = fmaf(v.y, wj, acc.y);
+        acc.z = fmaf(v.z, wj, acc.z);
+        acc.w = fmaf(v.w, wj, acc.w);
       }
     }
   }
