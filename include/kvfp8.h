@@ -338,10 +338,13 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  * inverse factor, so any finite bf16 query is accepted; bf16 pools keep the
  * query in bf16.
  * 4-bit pools multiply in f16 too (a code times its group's scale is exact),
- * and weights are held in f16, relative to a reference at most 2^6 below the
- * row's largest.  There a group that is NaN reaches, as V, the group's dims of
- * the rows that see its position and no other, as K all of those rows; a query
- * that is not finite makes its row NaN (where it sees a position).
+ * and weights are held in f16, relative to a reference 2^6 to 2^15 below the
+ * row's largest of a warp's part, whatever V is: V block scales within 2^60 of
+ * the largest of a request's cost no bits, and values further below it are off
+ * by less than 2^-56 of the largest value.  There a group that is NaN reaches,
+ * as V, the group's dims of the rows that see its position and no other, as K
+ * all of those rows; a query that is not finite makes its row NaN (where it
+ * sees a position).
  * Supported: GQA with head_dim 128, page_size 16 and up to 64 query rows per
  * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3, bf16 and 4 bits); LATENT
  * with head_dim_k 576, head_dim_v 512, page_size 64, e4m3.  Other shapes

@@ -27,8 +27,13 @@
 //
 // Codes become f16 by cvt.rn.f16x2.e2m1x2 (a byte each, as cheap as a move beside
 // the products); K's and V's group scales multiply them there (exact: six
-// significant bits), block scales go to the scores (K) and as an exponent bias into
-// the weights (V), as an e4m3 page's scales do.
+// significant bits).  K's block scales go to the scores.  V's say nothing about a
+// token's weight, so they stay out of the weights and their reference: a warp's
+// outputs are in units of a power of two near its pages' V block scales, what a page
+// differs by goes into its group scales (exact too, within 2^+-4), and where it
+// differs by more the outputs move to its unit first, pages one at a time.  (With the
+// block scale as an exponent bias of the weights the batch below took 0.7 us less, the
+// ragged one 1.5, and a page of V 2^20 below another lost its weights' bits.)
 //
 // Up to 8 query rows a kv head bound by HBM: 32 requests of 4k-32k tokens, 64 and 8
 // heads, 128 us in all, 5.7 TB/s of the 6.8 of a plain copy (the split's loop alone at
@@ -90,6 +95,19 @@ constexpr float kUnset = -1e38f;  // the reference of a row that has seen no pos
 // by more than 2^kSlack: f16 then keeps its 11 bits for weights down to 2^-20 of the largest
 // (2^-14 without the distance), and none passes its 65504.
 constexpr float kBelow = 6.0f, kSlack = 15.0f;
+// The unit of a warp's outputs, as a float's exponent field.  Within kNear of it a page's group
+// scales take the difference: 448 * 6 * 2^4 and 0.5 * 2^-9 * 2^-4 are normal f16 values.  The
+// unit does not follow a page more than kFar below the largest page's: outputs in a unit (at most
+// 2^31 weights of 2^15 times values of 2^12) then stay below fp32's largest, and what such a page
+// loses is below 2^-56 of the largest values.
+constexpr int kNear = 4, kFar = 64;
+
+struct FalseType {
+  static constexpr bool value = false;
+};
+struct TrueType {
+  static constexpr bool value = true;
+};
 
 // A row's reference at the end of a warp's part, with its sum: -inf where the part holds no
 // position for the merge.  Scores that are NaN pass no vote and leave the reference unset, but
@@ -102,13 +120,6 @@ __device__ __forceinline__ float final_reference(float m, float sum) {
 __device__ __forceinline__ float row_score_scale(float scale, int e, uint32_t mb) {
   return mb >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : scale * pow2f(-e);
 }
-
-struct FalseType {
-  static constexpr bool value = false;
-};
-struct TrueType {
-  static constexpr bool value = true;
-};
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t c;
@@ -133,6 +144,29 @@ __device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t slo, uint32_t
   b = mul_f16x2(b, slo);
   c = mul_f16x2(c, shi);
   d = mul_f16x2(d, shi);
+}
+__device__ __forceinline__ int exponent_field(float s) {  // of a positive value
+  return (int)(__float_as_uint(s) >> 23);
+}
+// 2^x in both halves, x <= 15; FAR: 0 below f16's normal range
+template <bool FAR>
+__device__ __forceinline__ uint32_t pow2_f16x2(int x) {
+  return FAR && x < -14 ? 0u : (uint32_t)(x + 15) * 0x04000400u;
+}
+// 2^x as a factor of sums, x <= 127; 0 below fp32's normal range
+__device__ __forceinline__ float pow2_or_zero(int x) { return x < -126 ? 0.0f : pow2f(x); }
+// A partial is 2^m (o, sum): with o in units of 2^x it is 2^(m + x) (o, 2^-x sum), which is how it
+// is left for units up to 2^+-kPlain.  Beyond, the merge's factors would flush what is small:
+// there outputs are multiplied out, but for a shift that keeps them below 2^115 (unit and sum give
+// their size; 0 but for values above 2^90, or a sum that is NaN).
+constexpr int kPlain = 24;
+__device__ __forceinline__ int partial_shift(int x, float sum) {
+  return min(126, max(0, x + exponent_field(fabsf(sum)) - 127 - 102));
+}
+// The unit for a page of V block scale `page` (exponent fields; `largest` so far)
+__device__ __forceinline__ int unit_for(int page, int& largest) {
+  largest = max(largest, page);
+  return max(page, largest - kFar);
 }
 // the low or the high half of w in both halves
 __device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
@@ -212,6 +246,7 @@ struct E2m1Rows8 {
   const uint32_t q16;      // Q as B operands, [k-steps 2w, 2w + 1][lane] 16-byte words (at this lane's)
   const float qsc0, qsc1;  // score scales of rows 2t, 2t + 1
   const int G, T, seen0;   // query token tq sees positions 0 .. seen0 + tq
+  int unit = -1, largest = -1;  // of acc, and of the pages' V block scales (-1: no page yet)
 
   // EDGE: some position may lie behind the length or behind a row's last one
   template <int NP, bool EDGE>
@@ -252,14 +287,12 @@ struct E2m1Rows8 {
         for (int e = 0; e < 4; ++e) s[u][e] += sb[u][e];
     }
     // ---- weights against the rows' references
-    float bias[NP], p[NP][4], big = -INFINITY;
+    float p[NP][4], big = -INFINITY;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      bias[u] = __log2f(pg[u].vs);
-      const float c0 = bias[u] - m0, c1 = bias[u] - m1;
       const float sc0 = pg[u].ks * qsc0, sc1 = pg[u].ks * qsc1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[u][e] = fmaf(s[u][e], e & 1 ? sc1 : sc0, e & 1 ? c1 : c0);
+      for (int e = 0; e < 4; ++e) p[u][e] = fmaf(s[u][e], e & 1 ? sc1 : sc0, e & 1 ? -m1 : -m0);
     }
     if constexpr (EDGE) {
       const int lim0 = seen0 + min(2 * t / G, T - 1), lim1 = seen0 + min((2 * t + 1) / G, T - 1);
@@ -279,8 +312,8 @@ struct E2m1Rows8 {
 #pragma unroll
       for (int u = 0; u < NP; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the biased scores themselves
-          const float y = fmaf(s[u][e], pg[u].ks * (e & 1 ? qsc1 : qsc0), bias[u]);
+        for (int e = 0; e < 4; ++e) {  // the scores themselves
+          const float y = s[u][e] * (pg[u].ks * (e & 1 ? qsc1 : qsc0));
           p[u][e] = p[u][e] == -INFINITY ? -INFINITY : y;
           if (e & 1) n1 = fmaxf(n1, p[u][e]);
           else n0 = fmaxf(n0, p[u][e]);
@@ -313,11 +346,22 @@ struct E2m1Rows8 {
     for (int u = 0; u < NP; ++u) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[u][e] = fast_exp2(p[u][e]);
-      const float unbias = pow2_inverse(pg[u].vs);
-      l0 = fmaf(p[u][0] + p[u][2], unbias, l0);
-      l1 = fmaf(p[u][1] + p[u][3], unbias, l1);
+      l0 += p[u][0] + p[u][2];
+      l1 += p[u][1] + p[u][3];
     }
     // ---- O^T += V^T P^T: row g's weights of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+    if constexpr (EDGE) {  // (others are near: the caller looks)
+      const int page = exponent_field(pg[0].vs);
+      if (abs(page - unit) > kNear) {
+        const int to = unit_for(page, largest);
+        const float f = pow2_or_zero(unit - to);
+        unit = to;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const uint32_t b0 = transpose8x8(f32x2_to_f16x2(p[u][0], p[u][1]));
@@ -328,6 +372,9 @@ struct E2m1Rows8 {
       auto add = [&](uint32_t scales, uint32_t c0, uint32_t c1) {
         uint32_t slo, shi;  // scales of group g's same tokens
         e4m3x4_to_f16(scales, slo, shi);
+        const uint32_t f = pow2_f16x2<EDGE>(exponent_field(pg[u].vs) - unit);
+        slo = mul_f16x2(slo, f);
+        shi = mul_f16x2(shi, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // rows g, g + 8 of tile i: dims 16g + 2i, + 1
           uint32_t a0, a1, a2, a3;
@@ -378,6 +425,7 @@ struct E2m1Rows16 {
   const uint32_t q16;  // Q as A operands, [block][k-step][lane] 16-byte words (at this lane's)
   const float (&qsc)[NB][2];
   const int n0, G, T, seen0;
+  int unit = -1, largest = -1;
 
   // the last position that row g + 8 hr of block b sees
   __device__ __forceinline__ int last(int b, int hr) const {
@@ -429,22 +477,18 @@ struct E2m1Rows16 {
       }
     }
     // s[u][b][nt][e]: row g (e < 2) or g + 8 of block b, token 8 nt + 2t + (e & 1)
-    float bias[NP];
     uint32_t pa[NP][NB][4];
-#pragma unroll
-    for (int u = 0; u < NP; ++u) bias[u] = __log2f(pg[u].vs);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float &mA = m[b][0], &mB = m[b][1], p[NP][2][4], big = -INFINITY;
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        const float cA = bias[u] - mA, cB = bias[u] - mB;
         const float scA = pg[u].ks * qsc[b][0], scB = pg[u].ks * qsc[b][1];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            p[u][nt][e] = fmaf(s[u][b][nt][e], e < 2 ? scA : scB, e < 2 ? cA : cB);
+            p[u][nt][e] = fmaf(s[u][b][nt][e], e < 2 ? scA : scB, e < 2 ? -mA : -mB);
       }
       if constexpr (EDGE) {
         const int limA = last(b, 0), limB = last(b, 1);
@@ -473,7 +517,7 @@ struct E2m1Rows16 {
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float y = fmaf(s[u][b][nt][e], pg[u].ks * qsc[b][e >> 1], bias[u]);
+              const float y = s[u][b][nt][e] * (pg[u].ks * qsc[b][e >> 1]);
               float& x = p[u][nt][e];
               x = x == -INFINITY ? -INFINITY : y;
               if (e < 2) nA = fmaxf(nA, x);
@@ -511,13 +555,26 @@ struct E2m1Rows16 {
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) p[u][nt][e] = fast_exp2(p[u][nt][e]);
-        const float unbias = pow2_inverse(pg[u].vs);
-        l[b][0] = fmaf((p[u][0][0] + p[u][0][1]) + (p[u][1][0] + p[u][1][1]), unbias, l[b][0]);
-        l[b][1] = fmaf((p[u][0][2] + p[u][0][3]) + (p[u][1][2] + p[u][1][3]), unbias, l[b][1]);
+        l[b][0] += (p[u][0][0] + p[u][0][1]) + (p[u][1][0] + p[u][1][1]);
+        l[b][1] += (p[u][0][2] + p[u][0][3]) + (p[u][1][2] + p[u][1][3]);
         pa[u][b][0] = f32x2_to_f16x2(p[u][0][0], p[u][0][1]);
         pa[u][b][1] = f32x2_to_f16x2(p[u][0][2], p[u][0][3]);
         pa[u][b][2] = f32x2_to_f16x2(p[u][1][0], p[u][1][1]);
         pa[u][b][3] = f32x2_to_f16x2(p[u][1][2], p[u][1][3]);
+      }
+    }
+    if constexpr (EDGE) {  // (as for 8 rows)
+      const int page = exponent_field(pg[0].vs);
+      if (abs(page - unit) > kNear) {
+        const int to = unit_for(page, largest);
+        const float f = pow2_or_zero(unit - to);
+        unit = to;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[b][i][e] *= f;
       }
     }
 #pragma unroll
@@ -528,6 +585,9 @@ struct E2m1Rows16 {
       auto add = [&](uint32_t scales) {
         uint32_t slo, shi;  // scales of group g's tokens 2t, 2t + 1 and 2t + 8, 2t + 9
         e4m3x4_to_f16(scales, slo, shi);
+        const uint32_t f = pow2_f16x2<EDGE>(exponent_field(pg[u].vs) - unit);
+        slo = mul_f16x2(slo, f);
+        shi = mul_f16x2(shi, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // column g of tiles 2i, 2i + 1: dims 16g + 2i, + 1
           uint32_t b00, b10, b01, b11;
@@ -749,7 +809,7 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
     bool bad = false;
 
     auto units = [&](auto& rows) {
-      auto unit = [&](auto edge) {
+      auto unit = [&](auto whole) {
         // every lane's copies of the unit have landed
         asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
         __syncwarp();
@@ -765,7 +825,9 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
           pg[k].nv = min(16, L - pg[k].pos0);
         }
         pos += 32 * WPH;
-        if constexpr (decltype(edge)::value) {
+        if constexpr (decltype(whole)::value) {
+          rows.template pages<2, false>(pg);
+        } else {
           // (a page behind the length was not fetched)
 #pragma unroll 1
           for (int k = 0; k < 2; ++k)
@@ -773,8 +835,6 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
               const E2m1Page one[1] = {k == 0 ? pg[0] : pg[1]};
               rows.template pages<1, true>(one);
             }
-        } else {
-          rows.template pages<2, false>(pg);
         }
         __syncwarp();  // every lane has read its part of the stage
         fetch(i + ST, st);
@@ -796,8 +856,16 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
         const int stop = min(i_end, 16 * batch + 16);
         bad = bad || (bad_pages >> (2 * (i & 15))) << (32 - 2 * (stop - i)) != 0;
         const int full_stop = min(stop, i_full);
-        while (i < full_stop) unit(FalseType{});
-        while (i < stop) unit(TrueType{});
+        // Whether the units' whole pages can be taken in the unit of the outputs, two at a time
+        // (their first page's where there is none yet)
+        if (rows.unit < 0) rows.unit = rows.largest = exponent_field(table->vs[i & 31].x);
+        const int mine = (lane >> 1) + 16 * batch;
+        const int v = mine >= i && mine < full_stop
+                          ? exponent_field(reinterpret_cast<const float*>(table->vs)[32 * (batch & 1) + lane])
+                          : rows.unit;
+        const int fast = __any_sync(0xffffffffu, abs(v - rows.unit) > kNear) ? i : full_stop;
+        while (i < fast) unit(TrueType{});
+        while (i < stop) unit(FalseType{});
       }
     };
 
@@ -864,13 +932,22 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
       E2m1Rows16<NB> rows{m, l, acc, smem_u32(qs) + 16 * lane, qsc, n0, G, T, L - T};
       units(rows);
       rows.finish();
+      const int x = rows.unit < 0 ? 0 : rows.unit - 127;
+      const bool plain = abs(x) <= kPlain;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr)
+        for (int hr = 0; hr < 2; ++hr) {
+          const int down = plain ? x : partial_shift(x, l[b][hr]);
           if (t == 0)
             *reinterpret_cast<float2*>(ml + 2 * (16 * b + g + 8 * hr)) =
-                make_float2(m[b][hr], bad ? -1.0f : l[b][hr]);
+                make_float2(m[b][hr] + down, bad ? -1.0f : l[b][hr] * pow2f(-down));
+          if (!plain) {
+            const float f = pow2f(x - down);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[b][k][2 * hr] *= f, acc[b][k][2 * hr + 1] *= f;
+          }
+        }
       // column c of tile k is dim 16 c + k: a lane's 32 dims of a row are contiguous
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -920,9 +997,23 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
       E2m1Rows8 rows{m0, m1, l0, l1, acc, smem_u32(qs) + 16 * lane, qsc0, qsc1, G, T, L - T};
       units(rows);
       rows.finish();
+      const int x = rows.unit < 0 ? 0 : rows.unit - 127;
+      const bool plain = abs(x) <= kPlain;
+      const int down0 = plain ? x : partial_shift(x, l0), down1 = plain ? x : partial_shift(x, l1);
+      if (!plain) {
+        const float f0 = pow2f(x - down0), f1 = pow2f(x - down1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[k][0] *= f0;
+          acc[k][1] *= f1;
+          acc[k][2] *= f0;
+          acc[k][3] *= f1;
+        }
+      }
       if (g == 0)
         *reinterpret_cast<float4*>(ml + 4 * t) =
-            make_float4(m0, bad ? -1.0f : l0, m1, bad ? -1.0f : l1);
+            make_float4(m0 + down0, bad ? -1.0f : l0 * pow2f(-down0), m1 + down1,
+                        bad ? -1.0f : l1 * pow2f(-down1));
       // rows g, g + 8 of tile k are dims 16g + 2k, + 1: 16 contiguous dims of a row
 #pragma unroll
       for (int e = 0; e < 2; ++e)
