@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
           pg[k].pos0 = pos + 16 * k;
           pg[k].nv = min(16, L - pg[k].pos0);
         }
-        pos += 32 * WPH;
+        pos = (int)((uint32_t)pos + 32u * WPH);  // (may pass 2^31 behind the last unit)
         if constexpr (decltype(whole)::value) {
           rows.template pages<2, false>(pg);
         } else {

@@ -14,6 +14,14 @@ namespace kvfp8 {
 
 constexpr int kDecodePlanThreads = 1024;
 
+// Units of a request of L tokens (0 <= L < 2^31): what its tokens make and unit_extra more, as
+// long as every unit's first token is an int.
+__device__ __forceinline__ int plan_units(const DecodeArgs& a, long long L) {
+  const int np = (int)((L + a.unit_tokens - 1) / a.unit_tokens);
+  if (a.unit_extra == 0 || L == 0) return np;
+  return min(np + a.unit_extra, (int)((1u << 31) / (uint32_t)a.unit_tokens));
+}
+
 // pfx[r] = exclusive prefix of units of work (pages) over requests that get
 // output, and rq_skip.  A request is skipped (no pages, no output) when
 // aborted or when its length is negative or needs more pages than its page
@@ -38,7 +46,7 @@ __device__ __forceinline__ void decode_plan_block(const DecodeArgs& a) {
       if (!aborted && bad_len) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
       const bool skip = aborted || bad_len;
       // at most ceil(2^31 / P) units: an int
-      np = skip ? 0 : (int)((L + a.unit_tokens - 1) / a.unit_tokens) + (L > 0 ? a.unit_extra : 0);
+      np = skip ? 0 : plan_units(a, L);
       a.ws.rq_skip[r] = skip ? 1 : 0;
     }
     int v = np;
@@ -94,9 +102,7 @@ __device__ __forceinline__ bool decode_plan_shared(const DecodeArgs& a, int32_t*
         const bool aborted = a.abort_mask != nullptr && a.abort_mask[lane] != 0;
         const bool bad_len = L < 0 || (L + P - 1) / P > a.max_pages;
         if (!aborted && bad_len) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
-        np = (aborted || bad_len)
-                 ? 0
-                 : (L + a.unit_tokens - 1) / a.unit_tokens + (L > 0 ? a.unit_extra : 0);
+        np = (aborted || bad_len) ? 0 : plan_units(a, L);
       }
       long long v = np;
 #pragma unroll
@@ -126,9 +132,7 @@ __device__ __forceinline__ bool decode_plan_shared(const DecodeArgs& a, int32_t*
       const bool aborted = a.abort_mask != nullptr && a.abort_mask[r] != 0;
       const bool bad_len = L < 0 || (L + P - 1) / P > a.max_pages;
       if (!aborted && bad_len) set_error(a.d.ctl, KV_ERR_INVALID_ARG);
-      np = (aborted || bad_len) ? 0
-                                : (int)((L + a.unit_tokens - 1) / a.unit_tokens) +
-                                      (L > 0 ? a.unit_extra : 0);
+      np = (aborted || bad_len) ? 0 : plan_units(a, L);
     }
     int v = np;
 #pragma unroll
