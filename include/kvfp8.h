@@ -123,13 +123,16 @@ enum {
  *   A value is code * s * S: an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6, signed),
  *   the e4m3 scale s of its group (16 dims of one token) and the block scale S
  *   of its (page, kv head) in k_scale / v_scale, a power of two.  S comes from
- *   the finite values that an append writes into a fresh page, of largest
- *   magnitude m: 2^(floor(log2 m) - 6), its exponent in -100 .. 121, 1 when m
- *   is 0; it stays as its first write set it.  s = e4m3(m_g / S * fp32(1/6)) with m_g the group's largest
- *   magnitude, to nearest even, saturating: a row may exceed its page's first rows
- *   21 times before its scale saturates.  code = e2m1(fp32(x * (fp32(1/s) / S)))
- *   to nearest even, saturating; 0 where s is.  A group with a value that is not
- *   finite gets s = NaN (and codes of no meaning).
+ *   the groups of all-finite values that an append writes into a fresh page, of
+ *   largest magnitude m: 2^(floor(log2 m) - 6), its exponent in -100 .. 121, 1
+ *   when m is 0; it stays as its first write set it.  s = e4m3(m_g / S *
+ *   fp32(1/6)) with m_g the group's largest magnitude, to nearest even,
+ *   saturating: a row may exceed its page's first rows 21 times before its scale
+ *   saturates.  code = e2m1(fp32(x * (fp32(1/s) / S))) to nearest even,
+ *   saturating; 0 where s is.  A group with a value that is not finite gets
+ *   s = NaN (and codes of no meaning), and no part in S.  (Groups of magnitudes
+ *   from 3.35e38 on, within 2% of the type's largest, may come back infinite:
+ *   their scale rounds up.)
  *   With c = d / 16, in bytes of the 1152 (a code's low half is the first of the
  *   two it shares a byte with):
  *     K code  64 slot + 16 (c % 4) + 8 (c / 4) + (d % 16) / 2, low half d even
