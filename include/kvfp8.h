@@ -415,6 +415,9 @@ kv_status paged_decode_attn_combine(kv_pool* pool, void* stream, int32_t B,
  *     library (held by every GPU that loads the library until the process
  *     exits).  A batch whose workspace (paged_decode_workspace_size) exceeds
  *     32 MiB is rejected with KV_ERR_UNSUPPORTED before anything is enqueued.
+ *     (4-bit pools leave a partial for every warp and need more of it than the
+ *     others with few kv heads: about 350 requests of up to 8 query rows a kv
+ *     head and 1, 2, 4 or 8 kv heads fit, 180 of 64 rows and one.)
  *   - Calls no cudaMalloc, cudaFree or other allocating routine.
  *   - A call made outside stream capture looks up the array's device
  *     address (cudaGetSymbolAddress) with the current device, so the address

@@ -24,8 +24,12 @@
 namespace {
 
 // Capacity of the static scratch.  Every GPU that loads the library keeps
-// this much device memory until the process exits.  Enough for GQA batches of
-// up to a few thousand (request, kv head) pairs at head dim 128.
+// this much device memory until the process exits.  Every request leaves a
+// partial of 520 bytes a query row for each kv head, and so does every CTA:
+// enough for GQA batches of up to a few thousand (request, kv head) pairs of 8
+// rows at head dim 128.  4-bit pools leave a partial a warp (DecodeArgs::sub),
+// up to 16 with few kv heads: on 152 SMs 352 requests of up to 8 rows and 1, 2, 4
+// or 8 kv heads, 184 of 64 rows and one, 100 of 32 rows and 4 or 8.
 constexpr size_t kStaticScratchBytes = size_t(32) << 20;  // 32 MiB
 
 __device__ __align__(256) uint8_t g_decode_scratch[kStaticScratchBytes];
