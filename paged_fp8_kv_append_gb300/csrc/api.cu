@@ -38,16 +38,15 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
     const long long R = (long long)T * G;
     if (d.head_dim_k != 128 || d.head_dim_v != 128 || d.page_size != 16 || R > 64)
       return KV_ERR_UNSUPPORTED;
-    // more than 8 rows: consumer warps of 16 rows (kinds 3: e4m3, 4: bf16, 6: 4-bit), for 4-bit
-    // pools of 32 (kind 7) where the blocks of 16 are pairs and at most two of the eight warps serve
+    // more than 8 rows: consumer warps of 16 rows, for 4-bit pools of 32 where the blocks of 16 are pairs and at most two of the eight warps serve
     // a (kv head, 32 rows) together (measured at the head of decode_e2m1.cu)
     const bool bf16 = d.dtype == KV_DTYPE_BF16, fp4 = d.dtype == KV_DTYPE_E2M1, wide = R > 8;
     const long long pairs = (R + 15) / 32, heads = d.num_kv_heads & -d.num_kv_heads;
     const bool wide32 = fp4 && wide && (R + 15) / 16 % 2 == 0 && pairs * heads >= 4;
-    cfg->kind = fp4    ? (wide32 ? 7 : wide ? 6 : 5)
-                : bf16 ? (wide ? 4 : 1)
-                       : (wide ? 3 : 0);
-    const int warp_rows = cfg->kind == 7 ? 32 : wide ? 16 : 8;
+    cfg->kind = fp4    ? (wide32 ? kGqaE2m1Rows32 : wide ? kGqaE2m1Rows16 : kGqaE2m1)
+                : bf16 ? (wide ? kGqaBf16Wide : kGqaBf16)
+                       : (wide ? kGqaE4m3Wide : kGqaE4m3);
+    const int warp_rows = wide32 ? 32 : wide ? 16 : 8;
     const int warps = fp4 ? e2m1_split_warps(cfg->kind) : gqa_consumer_warps(cfg->kind);
     // heads per unit: the largest power of two <= 8 (<= 4 for bf16, whose
     // tiles are twice as large) dividing Hkv, with heads x row blocks dividing
@@ -102,7 +101,7 @@ kv_status decode_config(const kv_pool* pool, int B, int Hq, int T, DecodeConfig*
   const int sms = sm_count();
   const int per_sm = sms > 0 ? latent_split_ctas_per_sm() : 0;
   if (sms <= 0 || per_sm <= 0) return KV_ERR_CUDA;
-  cfg->kind = 2;
+  cfg->kind = kLatentE4m3;
   cfg->self_plan = 0;
   cfg->grid = sms * per_sm;
   cfg->R8 = rb;
@@ -794,8 +793,8 @@ int32_t kv_last_launch_count(const kv_pool* pool) { return pool ? pool->last_lau
 namespace kvfp8 {
 
 cudaError_t launch_decode_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
-  if (kind == 2) return launch_latent_split(a, s, launches);
-  if (kind >= 5) return launch_e2m1_split(a, kind, s, launches);
+  if (kind == kLatentE4m3) return launch_latent_split(a, s, launches);
+  if (kind >= kGqaE2m1) return launch_e2m1_split(a, kind, s, launches);
   return launch_gqa_split(a, kind, s, launches);
 }
 

@@ -1160,18 +1160,20 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 }  // namespace
 
 int e2m1_split_warps(int kind) {
-  return kind == 7 ? E2m1Cfg<2>::WARPS : kind == 6 ? E2m1Cfg<1>::WARPS : E2m1Cfg<0>::WARPS;
+  return kind == kGqaE2m1Rows32   ? E2m1Cfg<2>::WARPS
+         : kind == kGqaE2m1Rows16 ? E2m1Cfg<1>::WARPS
+                                  : E2m1Cfg<0>::WARPS;
 }
 
 // What a piece costs beside its units (its queries, its first and last pages, its partial) in
 // units, by which a request is counted longer.  Above 8 rows 12: 88 us against 100 without for 24
 // requests of 4 drafts, 70 against 79 for the ragged batch above (6: 93 and 73, 20: 90 and 72).
 // Up to 8 rows 4: 1 us in 128, where 16 takes it back.
-int e2m1_unit_extra(int kind) { return kind >= 6 ? 12 : 4; }
+int e2m1_unit_extra(int kind) { return kind == kGqaE2m1 ? 4 : 12; }
 
 int e2m1_split_ctas_per_sm(int kind) {
   static int cache[64][3];  // by device, as the attribute below is; 0: not asked yet
-  const int nb = kind - 5;
+  const int nb = kind - kGqaE2m1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (cache[dev][nb] > 0) return cache[dev][nb];
@@ -1199,9 +1201,9 @@ cudaError_t launch_split(const DecodeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_e2m1_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
-  const cudaError_t e = kind == 7   ? launch_split<2>(a, s)
-                        : kind == 6 ? launch_split<1>(a, s)
-                                    : launch_split<0>(a, s);
+  const cudaError_t e = kind == kGqaE2m1Rows32   ? launch_split<2>(a, s)
+                        : kind == kGqaE2m1Rows16 ? launch_split<1>(a, s)
+                                                 : launch_split<0>(a, s);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -54,6 +54,96 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(DecodeArgs a)
   decode_plan_block(a);
 }
 
+// ------------------------------------------------- products, loads, the end of a piece
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(const void* p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p)));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(const void* p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_u32(p)));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)));
+  return v;
+}
+
+// End of a piece: merges the online-softmax states of the WPH warps that
+// share each of the Hv virtual heads (8 rows each) into the piece's partial.
+// merge_ml[(w * 8 + nw) * 2 + {0, 1}] holds warp w's running max and sum of
+// row nw, merge_o[(w * 8 + nw) * 128 + dd] its unnormalised output.  Pass 1,
+// one thread per row: the row's max M over the warps, each warp's weight
+// 2^(m_w - M) (written over m_w) and the weighted sum, stored with M (a
+// piece that met a page it must not read stores the sum -1 instead).  Pass
+// 2, every consumer thread: the weighted outputs, four dims at a time.
+// row_of(v, nw) is the partial row of virtual head v's row nw.  Starts and
+// ends with the consumer warps synchronised.
+template <class C, class RowOf>
+__device__ __forceinline__ void merge_piece(float* merge_o, float* merge_ml, int Hv, int WPH,
+                                            const DecodeArgs& a, RowOf row_of,
+                                            volatile int* piece_bad, bool reset_bad) {
+  constexpr int R8 = C::R8, D = C::D, NT = C::CONSUMERS * 32;
+  static_assert(R8 == 8 && D == 128, "index shifts");
+  const int tid = threadIdx.x;
+  named_bar_sync(1, NT);  // every warp's state is in the merge buffers
+  if (tid < Hv * R8) {
+    const int v = tid >> 3, nw = tid & 7;
+    float M = -INFINITY;
+    for (int q = 0; q < WPH; ++q) M = fmaxf(M, merge_ml[((q * Hv + v) * R8 + nw) * 2]);
+    float lsum = 0.0f;
+    for (int q = 0; q < WPH; ++q) {
+      float* ml = merge_ml + ((q * Hv + v) * R8 + nw) * 2;
+      const float w = (ml[0] == -INFINITY) ? 0.0f : exp2f(ml[0] - M);
+      lsum += ml[1] * w;
+      ml[0] = w;
+    }
+    const long long row = row_of(v, nw);
+    a.ws.ml_part[row * 2 + 0] = M;
+    a.ws.ml_part[row * 2 + 1] = *piece_bad ? -1.0f : lsum;
+  }
+  named_bar_sync(1, NT);
+  if (reset_bad && tid == 0) *piece_bad = 0;
+  for (int e = tid; e < Hv * R8 * (D / 4); e += NT) {
+    const int d4 = e & 31, rr = e >> 5, v = rr >> 3, nw = rr & 7;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int q = 0; q < WPH; ++q) {
+      const int w = (q * Hv + v) * R8 + nw;
+      const float wt = merge_ml[w * 2];
+      const float4 x = *reinterpret_cast<const float4*>(merge_o + w * D + 4 * d4);
+      o.x = fmaf(wt, x.x, o.x);
+      o.y = fmaf(wt, x.y, o.y);
+      o.z = fmaf(wt, x.z, o.z);
+      o.w = fmaf(wt, x.w, o.w);
+    }
+    *reinterpret_cast<float4*>(a.ws.o_part + row_of(v, nw) * D + 4 * d4) = o;
+  }
+  named_bar_sync(1, NT);
+}
+
 // ------------------------------------------------- split kernel
 
 // A unit of work is one page of one request for Hs kv heads (a "head
@@ -1138,38 +1228,38 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
 
 // ------------------------------------------------- host side
 
-// kinds: 0 = e4m3 (8-row consumers), 1 = bf16, 3 = e4m3 with 16-row consumers,
-// 4 = bf16 with 16-row consumers
 int gqa_ring_bytes(int kind) {
-  return (kind == 1 || kind == 4) ? GqaCfg<false>::RING : GqaCfg<true>::RING;
+  return (kind == kGqaBf16 || kind == kGqaBf16Wide) ? GqaCfg<false>::RING : GqaCfg<true>::RING;
 }
 int gqa_max_stages() { return kMaxStages; }
-bool gqa_kind_self_plans(int kind) { return kind == 0 || kind == 1 || kind == 4; }
+bool gqa_kind_self_plans(int kind) {
+  return kind == kGqaE4m3 || kind == kGqaBf16 || kind == kGqaBf16Wide;
+}
 int gqa_self_plan_max_batch() {
   static_assert(GqaCfg<true>::PFX_CACHE == GqaCfg<false>::PFX_CACHE, "one prefix cache size");
   return GqaCfg<true>::PFX_CACHE - 1;
 }
 int gqa_consumer_warps(int kind) {
-  return (kind == 1 || kind == 4) ? GqaCfg<false>::CONSUMERS : GqaCfg<true>::CONSUMERS;
+  return (kind == kGqaBf16 || kind == kGqaBf16Wide) ? GqaCfg<false>::CONSUMERS : GqaCfg<true>::CONSUMERS;
 }
 
 int gqa_split_ctas_per_sm(int kind) {
   static int cache[5] = {-1, -1, -1, -1, -1};
-  if (kind < 0 || kind > 4 || kind == 2) return 0;
+  if (kind < 0 || kind > kGqaBf16Wide || kind == kLatentE4m3) return 0;
   if (cache[kind] >= 0) return cache[kind];
   int n = 0;
   cudaError_t e;
-  if (kind == 4) {
+  if (kind == kGqaBf16Wide) {
     cudaFuncSetAttribute(gqa_split_wide_bf16_kernel,
                          cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<false>::SMEM);
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_bf16_kernel,
                                                       GqaCfg<false>::THREADS, GqaCfg<false>::SMEM);
-  } else if (kind == 3) {
+  } else if (kind == kGqaE4m3Wide) {
     cudaFuncSetAttribute(gqa_split_wide_kernel,
                          cudaFuncAttributeMaxDynamicSharedMemorySize, GqaCfg<true>::SMEM);
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_wide_kernel,
                                                       GqaCfg<true>::THREADS, GqaCfg<true>::SMEM);
-  } else if (kind == 0) {
+  } else if (kind == kGqaE4m3) {
     cudaFuncSetAttribute(gqa_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          GqaCfg<true>::SMEM);
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, gqa_split_kernel<true>,
@@ -1193,14 +1283,14 @@ cudaError_t launch_decode_plan(const DecodeArgs& a, cudaStream_t s, int* launche
 
 cudaError_t launch_gqa_split(const DecodeArgs& a, int kind, cudaStream_t s, int* launches) {
   const cudaError_t e =
-      kind == 4   ? launch_pdl(gqa_split_wide_bf16_kernel, dim3(a.grid),
-                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a)
-      : kind == 3 ? launch_pdl(gqa_split_wide_kernel, dim3(a.grid),
-                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
-      : kind == 0 ? launch_pdl(gqa_split_kernel<true>, dim3(a.grid),
-                               dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
-                  : launch_pdl(gqa_split_kernel<false>, dim3(a.grid),
-                               dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a);
+      kind == kGqaBf16Wide   ? launch_pdl(gqa_split_wide_bf16_kernel, dim3(a.grid),
+                                          dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a)
+      : kind == kGqaE4m3Wide ? launch_pdl(gqa_split_wide_kernel, dim3(a.grid),
+                                          dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
+      : kind == kGqaE4m3     ? launch_pdl(gqa_split_kernel<true>, dim3(a.grid),
+                                          dim3(GqaCfg<true>::THREADS), GqaCfg<true>::SMEM, s, a)
+                             : launch_pdl(gqa_split_kernel<false>, dim3(a.grid),
+                                          dim3(GqaCfg<false>::THREADS), GqaCfg<false>::SMEM, s, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

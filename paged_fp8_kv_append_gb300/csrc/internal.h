@@ -184,11 +184,21 @@ struct PrefillArgs {
 size_t prefill_ws_bytes(const kv_pool_desc& d, int B, int Hq, int total_q);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s, int* launches);
 
+// Split kernels: GQA pools by type, with up to 8 query rows a kv head or warps of 16 (32) rows.
+enum DecodeKind {
+  kGqaE4m3 = 0,
+  kGqaBf16 = 1,
+  kLatentE4m3 = 2,
+  kGqaE4m3Wide = 3,
+  kGqaBf16Wide = 4,
+  kGqaE2m1 = 5,        // kGqaE2m1 + n: n blocks of 16 rows a warp (0: 8 rows)
+  kGqaE2m1Rows16 = 6,
+  kGqaE2m1Rows32 = 7
+};
+
 // Kernel configuration chosen for a pool (shape checks + grid).
 struct DecodeConfig {
-  // 0 = GQA e4m3, 1 = GQA bf16, 2 = latent e4m3, 3 / 4 = GQA e4m3 / bf16 > 8 rows, 5 / 6 = GQA
-  // 4-bit up to 8 / > 8 rows
-  int kind;
+  int kind;         // DecodeKind
   int self_plan;    // the split kernel plans the batch itself (no plan launch)
   int grid;         // split-kernel CTAs
   int R8;           // partial rows per (slot, head)
