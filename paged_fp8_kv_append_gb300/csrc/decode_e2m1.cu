@@ -30,8 +30,8 @@
 // significant bits).  K's block scales go to the scores.  V's say nothing about a
 // token's weight, so they stay out of the weights and their reference: a warp's
 // outputs are in units of a power of two near its pages' V block scales, what a page
-// differs by goes into its group scales (exact too, within 2^+-4), and where it
-// differs by more the outputs move to its unit first, pages one at a time.  (With the
+// differs by goes into its group scales (exact too, 2^14 below to 2^4 above), and where
+// it differs by more the outputs move to another unit first, pages one at a time.  (With the
 // block scale as an exponent bias of the weights the batch below took 0.7 us less, the
 // ragged one 1.5, and a page of V 2^20 below another lost its weights' bits.)
 //
@@ -95,12 +95,16 @@ constexpr float kUnset = -1e38f;  // the reference of a row that has seen no pos
 // by more than 2^kSlack: f16 then keeps its 11 bits for weights down to 2^-20 of the largest
 // (2^-14 without the distance), and none passes its 65504.
 constexpr float kBelow = 6.0f, kSlack = 15.0f;
-// The unit of a warp's outputs, as a float's exponent field.  Within kNear of it a page's group
-// scales take the difference: 448 * 6 * 2^4 and 0.5 * 2^-9 * 2^-4 are normal f16 values.  The
-// unit does not follow a page more than kFar below the largest page's: outputs in a unit (at most
-// 2^31 weights of 2^15 times values of 2^12) then stay below fp32's largest, and what such a page
+// The unit of a warp's outputs, as a float's exponent field.  A page's group scales take the
+// difference from kUnder below it to kOver above: 448 * 6 * 2^4 is below f16's largest and
+// 0.5 * 2^-9 * 2^-14 its smallest, so every value is exact.  A part begins with a unit for its
+// first pages, and a page that does not fit moves it so that it lies 2 inside: pages within 2^16
+// of each other move it no more, and are taken two at a time.  (32 requests of 4k-32k with a page
+// in 8 2^12 below the others: 125 us, as without; moved by each of them in turn, 180.)  The unit
+// does not follow a page more than kFar below the largest page's: outputs in a unit (at most 2^31
+// weights of 2^15 times values of 2^15.4) then stay below fp32's largest, and what such a page
 // loses is below 2^-56 of the largest values.
-constexpr int kNear = 4, kFar = 64;
+constexpr int kUnder = 14, kOver = 4, kFar = 64;
 
 struct FalseType {
   static constexpr bool value = false;
@@ -163,10 +167,15 @@ constexpr int kPlain = 24;
 __device__ __forceinline__ int partial_shift(int x, float sum) {
   return min(126, max(0, x + exponent_field(fabsf(sum)) - 127 - 102));
 }
-// The unit for a page of V block scale `page` (exponent fields; `largest` so far)
-__device__ __forceinline__ int unit_for(int page, int& largest) {
+// Whether a page of V block scale `page` lies where its group scales take the difference
+// (exponent fields)
+__device__ __forceinline__ bool unit_fits(int page, int unit) {
+  return (uint32_t)(page - unit + kUnder) <= kUnder + kOver;
+}
+// The unit for a page that does not (`largest` so far)
+__device__ __forceinline__ int unit_for(int page, int unit, int& largest) {
   largest = max(largest, page);
-  return max(page, largest - kFar);
+  return max(page > unit ? page - (kOver - 2) : page + (kUnder - 2), largest - kFar);
 }
 // the low or the high half of w in both halves
 __device__ __forceinline__ uint32_t half_of(uint32_t w, int hi) {
@@ -350,10 +359,10 @@ struct E2m1Rows8 {
       l1 += p[u][1] + p[u][3];
     }
     // ---- O^T += V^T P^T: row g's weights of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-    if constexpr (EDGE) {  // (others are near: the caller looks)
+    if constexpr (EDGE) {  // (others fit: the caller looks)
       const int page = exponent_field(pg[0].vs);
-      if (abs(page - unit) > kNear) {
-        const int to = unit_for(page, largest);
+      if (!unit_fits(page, unit)) {
+        const int to = unit_for(page, unit, largest);
         const float f = pow2_or_zero(unit - to);
         unit = to;
 #pragma unroll
@@ -565,8 +574,8 @@ struct E2m1Rows16 {
     }
     if constexpr (EDGE) {  // (as for 8 rows)
       const int page = exponent_field(pg[0].vs);
-      if (abs(page - unit) > kNear) {
-        const int to = unit_for(page, largest);
+      if (!unit_fits(page, unit)) {
+        const int to = unit_for(page, unit, largest);
         const float f = pow2_or_zero(unit - to);
         unit = to;
 #pragma unroll
@@ -856,14 +865,18 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
         const int stop = min(i_end, 16 * batch + 16);
         bad = bad || (bad_pages >> (2 * (i & 15))) << (32 - 2 * (stop - i)) != 0;
         const int full_stop = min(stop, i_full);
-        // Whether the units' whole pages can be taken in the unit of the outputs, two at a time
-        // (their first page's where there is none yet)
-        if (rows.unit < 0) rows.unit = rows.largest = exponent_field(table->vs[i & 31].x);
+        // Whether the whole units' pages fit the unit of the outputs, two at a time; the first unit
+        // is one that most of them fit
         const int mine = (lane >> 1) + 16 * batch;
-        const int v = mine >= i && mine < full_stop
-                          ? exponent_field(reinterpret_cast<const float*>(table->vs)[32 * (batch & 1) + lane])
-                          : rows.unit;
-        const int fast = __any_sync(0xffffffffu, abs(v - rows.unit) > kNear) ? i : full_stop;
+        const bool whole = mine >= i && mine < full_stop;
+        const int page = exponent_field(reinterpret_cast<const float*>(table->vs)[32 * (batch & 1) + lane]);
+        if (rows.unit < 0) {
+          rows.largest = (int)__reduce_max_sync(0xffffffffu, whole ? page : 0);
+          if (rows.largest == 0) rows.largest = exponent_field(table->vs[i & 31].x);
+          rows.unit = rows.largest - (kOver - 2);
+        }
+        const int fast =
+            __any_sync(0xffffffffu, whole && !unit_fits(page, rows.unit)) ? i : full_stop;
         while (i < fast) unit(TrueType{});
         while (i < stop) unit(FalseType{});
       }

@@ -120,3 +120,20 @@ def test_far_scales_and_a_value_that_is_no_number(kv, hq, hkv):
     want = torch.zeros((hq, 128), dtype=torch.bool)
     want[:hq // hkv, 96:112] = True
     assert torch.equal(torch.isnan(got), want)
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("exp", [-10, -12, -13, -14, -15, -16, -17])
+def test_the_smallest_values_of_pages_below_others(kv, hq, hkv, exp):
+    """Pages 2^exp below the others with the smallest group scales, subnormal ones among them: the
+    others are zero there, so every bit of those values counts."""
+    rng = np.random.default_rng(74)
+    f = Filled4(kv, [1600], hkv=hkv, seed=75)
+    _spread_pages(f, np.arange(100) % 3 // 2 * 2, (0, 0, exp))  # every third
+    scale = PLACES["v"][2]
+    for j in range(2, 100, 3):
+        p = f.table[0, j]
+        f.cache["v"][p][:, scale[:, 1:]] = rng.integers(0, 16, (hkv, 16, 7))
+    f.to_device()
+    q = _queries(1, 1, hq, 76, 0.5)
+    _check(f, q, _run(f, q, 0.09))
