@@ -347,7 +347,8 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  * by less than 2^-56 of the largest value.  There a group that is NaN reaches,
  * as V, the group's dims of the rows that see its position and no other, as K
  * all of those rows; a query that is not finite makes its row NaN (where it
- * sees a position).
+ * sees a position).  e4m3 and bf16 pools promise none of this: there a row
+ * whose scores are NaN may come out as if it had not seen their positions.
  * Supported: GQA with head_dim 128, page_size 16 and up to 64 query rows per
  * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3, bf16 and 4 bits); LATENT
  * with head_dim_k 576, head_dim_v 512, page_size 64, e4m3.  Other shapes
@@ -493,7 +494,9 @@ kv_status kv_append_rotary(kv_pool* pool, void* stream, int32_t B, int32_t num_q
  *   q_norm, k_norm  bf16 [head_dim_k] (device, 16-byte aligned): the weights of
  *                   all query heads and of all key heads; NULL: those heads
  *                   are not normalised.
- *   norm_eps        finite, >= 0.  (With 0, a head of zeros gives NaN.)
+ *   norm_eps        finite, >= 0.  (With 0, a head of zeros gives NaN; squares
+ *                   are fp32, so heads of values below about 1e-20 lose bits and
+ *                   those of about 1e-23 become infinite.)
  * The mean is over all head_dim_k dims, in fp32, whatever rotary_dim is; between
  * the norm and the rounding after the rotation nothing is rounded to fewer bits.
  * A sum of squares beyond fp32 (values of about 1e18) gives zeros, a value that

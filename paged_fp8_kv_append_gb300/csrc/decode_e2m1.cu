@@ -40,7 +40,7 @@
 // the copy's rate; its first loads, a chain of three misses, take 6 us, the combine
 // 5).  16 warps of 128 registers: with 12 of 168 it is 151 us.  Above 8 rows bound by
 // the warps' instructions: 12 query heads a kv head, 48 requests of up to 8k: 70 us, 3.4
-// TB/s, the tensor pipe busy 38%, issue 45%; there 64 accumulators a lane want 168
+// TB/s, the tensor pipe busy 37%, issue 46%; there 64 accumulators a lane want 168
 // registers (16 warps of 128: 96 us, what spills finds no L1 beside the ring).
 //
 // Two blocks of 16 rows are served by one warp where that leaves at most two warps for a
