@@ -160,11 +160,14 @@ __device__ __forceinline__ uint32_t pow2_f16x2(int x) {
 // 2^x as a factor of sums, x <= 127; 0 below fp32's normal range
 __device__ __forceinline__ float pow2_or_zero(int x) { return x < -126 ? 0.0f : pow2f(x); }
 // A partial is 2^m (o, sum): with o in units of 2^x it is 2^(m + x) (o, 2^-x sum), which is how it
-// is left for units up to 2^+-kPlain.  Beyond, the merge's factors would flush what is small:
-// there outputs are multiplied out, but for a shift that keeps them below 2^115 (unit and sum give
-// their size; 0 but for values above 2^90, or a sum that is NaN).
+// is left for units up to 2^+-kPlain and references that take x exactly.  Beyond, the merge's
+// factors would flush what is small, or the sum would lose x: there outputs are multiplied out, but
+// for a shift that keeps them below 2^115 (unit and sum give their size; 0 but for values above
+// 2^90, or a sum that is NaN).
 constexpr int kPlain = 24;
-__device__ __forceinline__ int partial_shift(int x, float sum) {
+constexpr float kPlainReference = 1048576.0f;
+__device__ __forceinline__ int partial_shift(int x, float m, float sum) {
+  if (abs(x) <= kPlain && (fabsf(m) < kPlainReference || m == -INFINITY)) return x;
   return min(126, max(0, x + exponent_field(fabsf(sum)) - 127 - 102));
 }
 // Whether a page of V block scale `page` lies where its group scales take the difference
@@ -946,16 +949,15 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
       units(rows);
       rows.finish();
       const int x = rows.unit < 0 ? 0 : rows.unit - 127;
-      const bool plain = abs(x) <= kPlain;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          const int down = plain ? x : partial_shift(x, l[b][hr]);
+          const int down = partial_shift(x, m[b][hr], l[b][hr]);
           if (t == 0)
             *reinterpret_cast<float2*>(ml + 2 * (16 * b + g + 8 * hr)) =
                 make_float2(m[b][hr] + down, bad ? -1.0f : l[b][hr] * pow2f(-down));
-          if (!plain) {
+          if (down != x) {
             const float f = pow2f(x - down);
 #pragma unroll
             for (int k = 0; k < 16; ++k) acc[b][k][2 * hr] *= f, acc[b][k][2 * hr + 1] *= f;
@@ -1011,9 +1013,8 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
       units(rows);
       rows.finish();
       const int x = rows.unit < 0 ? 0 : rows.unit - 127;
-      const bool plain = abs(x) <= kPlain;
-      const int down0 = plain ? x : partial_shift(x, l0), down1 = plain ? x : partial_shift(x, l1);
-      if (!plain) {
+      const int down0 = partial_shift(x, m0, l0), down1 = partial_shift(x, m1, l1);
+      if (down0 != x || down1 != x) {
         const float f0 = pow2f(x - down0), f1 = pow2f(x - down1);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

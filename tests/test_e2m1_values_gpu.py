@@ -90,3 +90,25 @@ def test_drafts_before_the_bad_key_and_rows_that_see_nothing(kv, hq, hkv):
     rows = torch.zeros((4, hq), dtype=torch.bool)
     rows[1:3] = True
     _bounded_rows(f, 0, got, q[0], 0.09, rows)
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("exp", [40, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_equal_keys_of_far_scores(kv, hq, hkv, exp, sign):
+    """All keys are alike and every score is 1.5 * 2^exp (as a power of 2's exponent), to which no page's
+    V block scale can be added in fp32: each position has the same weight, whatever part it is in."""
+    n = 1600
+    f = Filled4(kv, [n], hkv=hkv, seed=48)
+    for j, p in enumerate(f.table[0, :n // 16]):
+        f.cache["k"][p][:, :1024] = 0x22  # 1
+        f.cache["k"][p][:, 1024:] = 0x38  # times 1
+        f.scale["k"][p] = 1.0
+        f.scale["v"][p] = 2.0 ** (-20 if j < 40 else 0 if j < 70 else 15)
+    f.to_device()
+    q = torch.full((1, 1, hq, 128), sign * 2.0 ** 20, dtype=torch.bfloat16)
+    got = _run(f, q, 1.5 * 2.0 ** (exp - 20 - 7) * 0.6931471805599453)
+    G = hq // hkv
+    v = f.rows(0, "v")
+    ref, mag = (x.mean(0).repeat_interleave(G, 0) for x in (v, v.abs()))
+    assert bool(((got[0, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag).all())
