@@ -90,7 +90,8 @@ struct E2m1Cfg {
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
-constexpr float kUnset = -1e38f;  // the reference of a row that has seen no position
+// the reference of a row that has seen no position: fp32's lowest, so that any finite score passes it
+constexpr float kUnset = -3.402823466e38f;
 // A reference is set 2^kBelow below the row's largest weight, and moved when a weight exceeds it
 // by more than 2^kSlack: f16 then keeps its 11 bits for weights down to 2^-20 of the largest
 // (2^-14 without the distance), and none passes its 65504.

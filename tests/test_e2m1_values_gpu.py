@@ -112,3 +112,22 @@ def test_equal_keys_of_far_scores(kv, hq, hkv, exp, sign):
     v = f.rows(0, "v")
     ref, mag = (x.mean(0).repeat_interleave(G, 0) for x in (v, v.abs()))
     assert bool(((got[0, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag).all())
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_scores_next_to_the_lowest(kv, hq, hkv, n):
+    """All keys are alike and every score is -1.5 * 2^127 (as a power of 2's exponent; fp32's lowest is
+    -2 * 2^127): each position has the same weight."""
+    f = Filled4(kv, [n], hkv=hkv, seed=47)
+    for p in f.table[0, :-(-n // 16)]:
+        f.cache["k"][p][:, :1024] = 0x22  # 1
+        f.cache["k"][p][:, 1024:] = 0x38  # times 1
+        f.scale["k"][p] = 2.0 ** 13
+    f.to_device()
+    q = torch.full((1, 1, hq, 128), -2.0 ** 100, dtype=torch.bfloat16)
+    got = _run(f, q, 1.5 * 2.0 ** (127 - 100 - 13 - 7) * 0.6931471805599453)
+    G = hq // hkv
+    v = f.rows(0, "v")
+    ref, mag = (x.mean(0).repeat_interleave(G, 0) for x in (v, v.abs()))
+    assert bool(((got[0, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag).all())
