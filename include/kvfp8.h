@@ -347,7 +347,8 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int32_t B,
  * by less than 2^-56 of the largest value.  There a group that is NaN reaches,
  * as V, the group's dims of the rows that see its position and no other, as K
  * all of those rows; a query that is not finite makes its row NaN (where it
- * sees a position).  e4m3 and bf16 pools promise none of this: there a row
+ * sees a position), and so does a block scale that is NaN, and a V block scale
+ * that is negative or infinite, of the rows that see its page.  e4m3 and bf16 pools promise none of this: there a row
  * whose scores are NaN may come out as if it had not seen their positions.
  * Supported: GQA with head_dim 128, page_size 16 and up to 64 query rows per
  * kv head, q_tokens * (Hq/Hkv) <= 64 (e4m3, bf16 and 4 bits); LATENT

@@ -740,7 +740,12 @@ __global__ void __launch_bounds__(E2m1Cfg<NB>::THREADS, 1) e2m1_split_kernel(con
     return tile;
   };
   auto load_scales = [&](int tile) {
-    return tile < 0 ? make_float2(1.0f, 1.0f) : make_float2(a.d.k_scale[tile], a.d.v_scale[tile]);
+    float2 sc = make_float2(1.0f, 1.0f);
+    if (tile >= 0) sc = make_float2(a.d.k_scale[tile], a.d.v_scale[tile]);
+    // (V's is taken by its exponent alone: one that no append leaves, negative or not finite, makes
+    // NaN of the page's scores instead)
+    if (__float_as_uint(sc.y) >= 0x7F800000u) sc = make_float2(__int_as_float(0x7FFFFFFF), 1.0f);
+    return sc;
   };
   auto fill_scales = [&](int b, float2 sc) {
     reinterpret_cast<float*>(table->ks)[32 * (b & 1) + lane] = sc.x;

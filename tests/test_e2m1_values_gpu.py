@@ -131,3 +131,23 @@ def test_scores_next_to_the_lowest(kv, hq, hkv, n):
     v = f.rows(0, "v")
     ref, mag = (x.mean(0).repeat_interleave(G, 0) for x in (v, v.abs()))
     assert bool(((got[0, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag).all())
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("which,value", [("k", float("nan")), ("v", float("nan")), ("v", float("inf")), ("v", -1.0)])
+@pytest.mark.parametrize("page", [0, 20, 43])
+def test_a_block_scale_that_is_no_number(kv, hq, hkv, which, value, page):
+    """The kv head's rows, which all see the page, are NaN, and no others."""
+    f = Filled4(kv, [700, 40], hkv=hkv, seed=49)
+    q = _queries(2, 1, hq, 50, 0.5)
+    p, G = int(f.table[0, page]), hq // hkv
+    was = f.scale[which][p, 0]
+    f.scale[which][p, 0] = value
+    f.to_device()
+    got = _run(f, q, 0.09)
+    f.scale[which][p, 0] = was
+    assert bool(torch.isnan(got[0, 0, :G]).all())
+    rows = torch.ones((1, hq), dtype=torch.bool)
+    _bounded_rows(f, 1, got[1], q[1], 0.09, rows)
+    rows[0, :G] = False
+    _bounded_rows(f, 0, got[0], q[0], 0.09, rows)
